@@ -56,6 +56,20 @@ class kvq_kernel_stat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
 
+class kvq_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+        ("scaling", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+        ("original_ctx", ctypes.c_int), ("low", ctypes.c_double), ("high", ctypes.c_double),
+        ("magnitude", ctypes.c_double),
+    ]
+
+
+class kvq_rope_plan(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("step", ctypes.c_uint64 * 128)]
+
+
 CERT_DTYPE = np.dtype([("e_key", "<f4"), ("e_val", "<f4"), ("rank_ok", "<i4"), ("level", "<i4"),
                        ("k_star", "<i4"), ("n_val_promoted", "<i4"), ("promoted_bytes", "<i8")])
 assert CERT_DTYPE.itemsize == 32
@@ -71,7 +85,7 @@ def load_library() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libkvq.so not built at {LIB_PATH}; run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i32, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    vp, i32, f32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_int64
     sigs = {
         "kvq_cache_create": [ctypes.POINTER(kvq_config), ctypes.POINTER(vp)],
         "kvq_cache_destroy": [vp],
@@ -89,6 +103,15 @@ def load_library() -> ctypes.CDLL:
         "kvq_debug_fill_tier2": [vp, i32, ctypes.c_uint16],
         "kvq_residency_stats": [vp, i32, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
                                 ctypes.POINTER(i32), i32],
+        "kvq_rope_plan_init": [ctypes.POINTER(kvq_rope_config), ctypes.POINTER(kvq_rope_plan)],
+        "kvq_rope": [vp, i32, vp, i64, i64, vp, i32, i32, vp, i64, i64, vp],
+        "kvq_paged_page_bytes": [i32, ctypes.POINTER(ctypes.c_size_t)],
+        "kvq_paged_append": [vp, i32, vp, i64, i64, vp, i64, i64, vp, vp, i32, i32, i32, vp, i32,
+                             vp, i64, i64, i32, vp, i64, i64, vp],
+        "kvq_paged_gather": [vp, i32, vp, i32, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp],
+        "kvq_paged_attention_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "kvq_paged_attention": [i32, vp, i64, i64, vp, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, f32,
+                                vp, vp, vp, ctypes.c_size_t, vp],
     }
     for name, argt in sigs.items():
         fn = getattr(lib, name)
@@ -336,6 +359,236 @@ def dense_attention(q, k, v, out, workspace=None, stream=None):
         _need(workspace, "workspace", torch.uint8, nbytes=need)
         _check(load_library().kvq_dense_attention(_ptr(q), _ptr(k), _ptr(v), B, Hq, Hkv, N, _ptr(out),
                                                   _ptr(workspace), workspace.numel(), _stream(stream)))
+    return workspace
+
+
+# ---- rotary positions and the paged 4-bit cache ----
+
+PAGE = 64   # tokens per page
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
+
+
+class RopePlan:
+    """Rotary frequencies of a model, for `rope` and `paged_append` (kvq_rope_plan_init).
+
+    layout: "half" pairs elements (i, i + rotary_dim / 2), "interleaved" (2i, 2i + 1).
+    scaling: "none", "linear", "ntk", "parts" (frequencies blended by their turns within
+    original_ctx, between low and high) or "yarn" (blended over the pair index, cos and sin
+    times 0.1 ln(factor) + 1 unless `magnitude` is given); see include/kvq.h.
+    """
+
+    def __init__(self, head_dim, rotary_dim=None, layout="half", base=10000.0, scaling="none", factor=1.0,
+                 original_ctx=0, low=1.0, high=32.0, magnitude=0.0):
+        if layout not in ("half", "interleaved"):
+            raise ValueError('layout must be "half" or "interleaved"')
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        cfg = kvq_rope_config(head_dim, head_dim if rotary_dim is None else rotary_dim, int(layout == "interleaved"),
+                              ROPE_SCALINGS[scaling], base, factor, original_ctx, low, high, magnitude)
+        self.plan = kvq_rope_plan()
+        _check(load_library().kvq_rope_plan_init(ctypes.byref(cfg), ctypes.byref(self.plan)))
+        self.address = ctypes.addressof(self.plan)
+        self.head_dim = head_dim
+
+
+def _float_code(t, name) -> int:
+    import torch
+    if t.dtype == torch.float16:
+        return 0
+    if t.dtype == torch.bfloat16:
+        return 1
+    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+
+
+def _rows(t, name, dtype, shape):
+    """Address and (token, head) strides of a [tokens, heads, head_dim] operand whose rows
+    are contiguous."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 and shape[2] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # a dimension of one row has no stride to speak of
+    return t.data_ptr(), st[0] if shape[0] > 1 else 8, st[1] if shape[1] > 1 else 8
+
+
+def _ints(t, name, shape):
+    import torch
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _one_device(*named):
+    """The CUDA device that all given tensors are on."""
+    dev = named[0][1].device
+    if dev.type != "cuda":
+        raise ValueError(f"{named[0][0]} must be a CUDA tensor")
+    for name, t in named[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, like {named[0][0]}")
+    return dev
+
+
+def _call(dev, fn, *args, stream=None):
+    """Run a library call on `dev` and `stream` (that device's current one when None)."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, _stream(stream)))
+
+
+def rope(x, positions, plan, out=None, stream=None):
+    """Rotary positions (kvq_rope): x [T, H, head_dim] fp16 or bf16 with contiguous rows (any
+    token and head strides, e.g. a slice of a fused projection), positions [T] int32.
+    out=None allocates the result; out=x works in place.  Returns out."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [n_tokens, n_heads, head_dim]")
+    if out is None:
+        if stream is not None:
+            raise ValueError("out must be given with a stream")
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dev = _one_device(("x", x), ("positions", positions), ("out", out))
+    shape, code = x.shape, _float_code(x, "x")
+    if shape[2] != plan.head_dim:
+        raise ValueError(f"x must have head_dim {plan.head_dim}, got {shape[2]}")
+    _call(dev, load_library().kvq_rope, plan.address, code, *_rows(x, "x", x.dtype, shape),
+          _ints(positions, "positions", shape[:1]), shape[0], shape[1], *_rows(out, "out", x.dtype, shape),
+          stream=stream)
+    return out
+
+
+def paged_page_bytes(head_dim: int = HEAD_DIM) -> int:
+    """Bytes of one page of one KV head: a pool of pages is a contiguous CUDA uint8 tensor
+    [n_pages, n_kv_heads, paged_page_bytes(head_dim)] (its initial contents do not matter)."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().kvq_paged_page_bytes(head_dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+_PAGE_BYTES = {64: 5120, 128: 10240}
+
+
+def _pool(pages, n_kv_heads, head_dim):
+    """Address and page count of a pool of pages."""
+    import torch
+    if head_dim not in _PAGE_BYTES:
+        raise ValueError("head_dim must be 64 or 128")
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.shape[1] != n_kv_heads \
+            or pages.shape[2] != _PAGE_BYTES[head_dim] or not pages.is_contiguous():
+        raise ValueError(f"pages must be a contiguous uint8 tensor [n_pages, {n_kv_heads}, {_PAGE_BYTES[head_dim]}]")
+    return pages.data_ptr(), pages.shape[0]
+
+
+def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=None, stream=None):
+    """Write tokens into a pool of pages in 4 bits (kvq_paged_append).
+
+    k, v: [T, n_kv_heads, head_dim] fp16 or bf16 with contiguous rows; slots: int32 [T] (page *
+    64 + offset; outside the pool, e.g. -1: skipped; all distinct).  With a RopePlan and
+    positions (int32 [T]) keys are rotated on the way, and q [T, n_q_heads, head_dim], when
+    given, into q_out (which may be q)."""
+    if k.dim() != 3:
+        raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
+    dev = _one_device(("k", k), ("v", v), ("slots", slots), ("pages", pages), ("positions", positions), ("q", q),
+                      ("q_out", q_out))
+    shape, code = k.shape, _float_code(k, "k")
+    T, hkv, hd = shape
+    pool, n_pages = _pool(pages, hkv, hd)
+    if (plan is None) != (positions is None):
+        raise ValueError("plan and positions go together")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    hq, qa, oa = 0, (None, 0, 0), (None, 0, 0)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [n_tokens, n_q_heads, head_dim]")
+        hq = q.shape[1]
+        qa, oa = _rows(q, "q", k.dtype, (T, hq, hd)), _rows(q_out, "q_out", k.dtype, (T, hq, hd))
+    _call(dev, load_library().kvq_paged_append, None if plan is None else plan.address, code,
+          *_rows(k, "k", k.dtype, shape), *_rows(v, "v", k.dtype, shape), _ints(slots, "slots", shape[:1]),
+          None if positions is None else _ints(positions, "positions", shape[:1]), T, hkv, hd, pool, n_pages,
+          *qa, hq, *oa, stream=stream)
+
+
+def paged_gather(pages, slots, k, v, stream=None):
+    """Read tokens back from a pool of pages (kvq_paged_gather): k, v [T, n_kv_heads, head_dim]
+    fp16 or bf16 receive what the slots hold (rows of slots outside the pool become 0)."""
+    if k.dim() != 3:
+        raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
+    dev = _one_device(("pages", pages), ("slots", slots), ("k", k), ("v", v))
+    shape, code = k.shape, _float_code(k, "k")
+    _call(dev, load_library().kvq_paged_gather, *_pool(pages, shape[1], shape[2]), _ints(slots, "slots", shape[:1]),
+          *shape, code, *_rows(k, "k", k.dtype, shape), *_rows(v, "v", k.dtype, shape), stream=stream)
+
+
+def paged_attention_workspace(batch: int, n_q_tokens: int, n_q_heads: int, n_kv_heads: int,
+                              head_dim: int = HEAD_DIM) -> int:
+    """Workspace bytes kvq_paged_attention needs for this shape on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().kvq_paged_attention_workspace(batch, n_q_tokens, n_q_heads, n_kv_heads, head_dim,
+                                                        ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, window=0, workspace=None, stream=None):
+    """Decode attention over a pool of 4-bit pages (kvq_paged_attention).
+
+    q: [B, Hq, head_dim] or [B, n_q_tokens, Hq, head_dim] fp16 or bf16, the last tokens of each
+    sequence; page_table: int32 [B, max_pages]; seq_lens: int32 [B], those tokens included (0:
+    a padding sequence, whose out is 0); out: like q, contiguous; lse: float32 like q without
+    its last dimension, or None.  `workspace` is a device uint8 tensor of at least
+    paged_attention_workspace(...) bytes (allocated here when omitted).  Returns
+    `workspace` so a caller can reuse it."""
+    import torch
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [batch, n_q_heads, head_dim] or [batch, n_q_tokens, n_q_heads, head_dim]")
+    dev = _one_device(("q", q), ("pages", pages), ("page_table", page_table), ("seq_lens", seq_lens), ("out", out),
+                      ("lse", lse), ("workspace", workspace))
+    code, shape, st = _float_code(q, "q"), q.shape, q.stride()
+    B, hq, hd = shape[0], shape[-2], shape[-1]
+    Q = shape[1] if len(shape) == 4 else 1
+    if st[-1] != 1:
+        raise ValueError("q: the last dimension must be contiguous")
+    qt = st[1] if Q > 1 else st[0] if B > 1 else 8
+    if Q > 1 and B > 1 and st[0] != Q * st[1]:
+        raise ValueError("q: the query tokens must be evenly spaced in memory")
+    if pages.dim() != 3:
+        raise ValueError("pages must be [n_pages, n_kv_heads, page bytes]")
+    hkv = pages.shape[1]
+    pool, n_pages = _pool(pages, hkv, hd)
+    if out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1] or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32, of q's shape without the last dimension")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be int32 [{B}, max_pages]")
+    ts, max_pages = page_table.stride(), page_table.shape[1]
+    if ts[1] != 1 and max_pages > 1:
+        raise ValueError("page_table: the last dimension must be contiguous")
+    lens = _ints(seq_lens, "seq_lens", shape[:1])
+    lib = load_library()
+    if workspace is None:
+        with torch.cuda.device(dev):
+            workspace = torch.empty(max(paged_attention_workspace(B, Q, hq, hkv, hd), 16), dtype=torch.uint8,
+                                    device=dev)
+        if stream is not None:   # keep its memory until that stream is done with it
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream), device=dev))
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _call(dev, lib.kvq_paged_attention, code, q.data_ptr(), qt, st[-2] if hq > 1 else 8, pool, n_pages,
+          page_table.data_ptr(), ts[0] if B > 1 else max_pages, max_pages, lens, B, Q, hq, hkv, hd, window,
+          0.0 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
+          workspace.data_ptr(), workspace.numel(), stream=stream)
     return workspace
 
 

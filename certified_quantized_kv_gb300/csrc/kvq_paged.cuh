@@ -1,0 +1,99 @@
+// kvq_paged.cuh -- layout of the paged 4-bit cache, rotary phases and the element types
+// of the calls that use them.
+//
+// A page holds 64 consecutive tokens of one KV head in one contiguous piece, so that one
+// bulk copy moves it (10240 bytes at head_dim 128, 5120 at 64).  With NG = head_dim / 32
+// groups:
+//   key codes      64 rows (tokens) of head_dim / 2 bytes; channel c = 32g + 8a + j sits in
+//                  byte a * 4NG + 4g + (j >> 1), low nibble for even j.  Lane (gid, tig) of
+//                  an mma.m16n8k16 reads the piece a = tig of row gid in one load: one 32-bit
+//                  word (eight channels) per group.
+//   value codes    64 rows of head_dim / 2 bytes; channel c = 32g + 4a + j sits in byte
+//                  a * 2NG + 2g + (j >> 1): lane gid reads piece a = gid of the four tokens
+//                  of its k columns.  Token t sits in row t ^ ((t >> 1) & 1), bytes XOR
+//                  32 ((t >> 2) & 1), at head_dim 128 and in row t ^ ((t >> 2) & 1) at 64, so
+//                  that the lanes of one load (two tokens apart) hit distinct banks.
+//   key scales     binary16 [64][NG], then key offsets, the same
+//   value scales   binary16 [NG][64], token t at 16((t >> 1) & 3) + 4(t >> 4) + 2((t >> 3) & 1)
+//                  + (t & 1): the token pairs that lane tig multiplies are contiguous; then
+//                  value offsets, the same
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvq.h"
+#include "kvq_common.cuh"
+
+namespace kvq {
+
+constexpr int PG = 64;   // tokens per page
+
+template <int HD>
+struct Page {
+  static constexpr int G = HD / 32;              // 32-channel groups
+  static constexpr int ROW = HD / 2;             // code bytes per token
+  static constexpr int CODES = PG * ROW;         // code bytes of the keys (and of the values)
+  static constexpr int SCALES = PG * G * 2;      // bytes of one scale or offset array
+  static constexpr int VC = CODES, KS = 2 * CODES, KO = KS + SCALES, VS = KO + SCALES, VO = VS + SCALES;
+  static constexpr int BYTES = VO + SCALES;
+};
+
+__host__ __device__ constexpr int page_bytes(int head_dim) { return head_dim == 128 ? Page<128>::BYTES : Page<64>::BYTES; }
+
+// element of token t within one group's 64 value scales (or offsets)
+__host__ __device__ __forceinline__ constexpr int vscale_at(int t) {
+  return ((t >> 1) & 3) * 16 + (t >> 4) * 4 + ((t >> 3) & 1) * 2 + (t & 1);
+}
+// byte of (token t, piece byte x) within the value codes
+template <int HD>
+__host__ __device__ __forceinline__ constexpr int vcode_at(int t, int x) {
+  return HD == 128 ? (t ^ ((t >> 1) & 1)) * Page<HD>::ROW + (x ^ (32 * ((t >> 2) & 1)))
+                   : (t ^ ((t >> 2) & 1)) * Page<HD>::ROW + x;
+}
+
+// ---- element types of q, k, v and outputs (kvq_dtype) ----
+__device__ __forceinline__ float2 pair_to_f2(uint32_t u, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  return __half22float2(u32_as_h2(u));
+}
+__device__ __forceinline__ uint32_t f2_to_pair(float x, float y, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return h2_as_u32(__floats2half2_rn(x, y));
+}
+__device__ __forceinline__ float elem_to_f(const void* p, size_t i, bool bf16) {
+  const unsigned short u = static_cast<const unsigned short*>(p)[i];
+  return bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+}
+__device__ __forceinline__ void f_to_elem(void* p, size_t i, float x, bool bf16) {
+  static_cast<unsigned short*>(p)[i] =
+      bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+}
+
+// ---- rotary phases ----
+// The angle of position p and pair i is p * step_i in units of 2^-64 turn, an exact
+// integer product modulo one turn whatever the position's size and sign; its top 32 bits
+// give the angle to 2^-33 turn and cos and sin to fp32 accuracy.
+__device__ __forceinline__ float2 rope_cos_sin(int pos, uint64_t step, float magnitude) {
+  const uint64_t ph = (uint64_t)(int64_t)pos * step + 0x80000000ull;
+  float s, c;
+  sincospif((float)(int32_t)(uint32_t)(ph >> 32) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
+  return make_float2(c * magnitude, s * magnitude);
+}
+
+// ---- checks shared by the calls of this file's users (kvq_rope.cu) ----
+// Each returns KVQ_OK or reports `fn`'s failure through kvq_last_error().
+kvq_status paged_fail(kvq_status s, const char* fn, const char* what);
+kvq_status paged_cuda_fail(cudaError_t e, const char* fn, const char* what);
+// device memory of `dev`, aligned to `align` bytes
+kvq_status check_buffer(const void* p, int dev, size_t align, const char* fn, const char* name);
+// rows of a strided [tokens, heads, head_dim] operand: non-negative strides, multiples of 8
+kvq_status check_strides(int64_t token, int64_t head, const char* fn, const char* name);
+kvq_status check_plan(const kvq_rope_plan* plan, int head_dim, const char* fn);
+
+}  // namespace kvq

@@ -1,0 +1,180 @@
+// kvq_rope.cu -- rotary positions, and the argument checks of the paged-cache calls.
+//
+// Pair i of a head at position p is turned by p w_i: (a, b) -> (a cos - b sin, b cos + a sin).
+// The plan holds w_i / (2 pi) as a 64-bit fraction of a turn, so p w_i modulo one turn is an
+// integer product without rounding (rope_cos_sin): a position of 2 million costs no
+// accuracy, which an fp32 product of position and frequency would.
+#include <cmath>
+#include <string>
+
+#include "kvq.h"
+#include "kvq_launch.h"
+#include "kvq_paged.cuh"
+
+namespace kvq {
+
+void set_last_error(const std::string& msg);
+
+kvq_status paged_fail(kvq_status s, const char* fn, const char* what) {
+  set_last_error(std::string(fn) + ": " + what);
+  return s;
+}
+
+kvq_status paged_cuda_fail(cudaError_t e, const char* fn, const char* what) {
+  set_last_error(std::string(fn) + ": " + what + ": " + cudaGetErrorString(e));
+  return KVQ_ERR_CUDA;
+}
+
+kvq_status check_buffer(const void* p, int dev, size_t align, const char* fn, const char* name) {
+  const std::string n(name);
+  if (!p) return paged_fail(KVQ_ERR_INVALID, fn, (n + " is NULL").c_str());
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
+    at.type = cudaMemoryTypeUnregistered;
+  }
+  const bool ok = at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+  if (!ok) return paged_fail(KVQ_ERR_INVALID, fn, (n + " must be device memory of the current device").c_str());
+  if (reinterpret_cast<uintptr_t>(p) % align != 0)
+    return paged_fail(KVQ_ERR_INVALID, fn, (n + " must be " + std::to_string(align) + "-byte aligned").c_str());
+  return KVQ_OK;
+}
+
+kvq_status check_strides(int64_t token, int64_t head, const char* fn, const char* name) {
+  if (token < 0 || head < 0 || token % 8 != 0 || head % 8 != 0)
+    return paged_fail(KVQ_ERR_INVALID, fn,
+                      (std::string(name) + ": strides must be non-negative multiples of 8 elements").c_str());
+  return KVQ_OK;
+}
+
+kvq_status check_plan(const kvq_rope_plan* plan, int head_dim, const char* fn) {
+  if (plan->head_dim != head_dim) return paged_fail(KVQ_ERR_INVALID, fn, "the plan is for another head_dim");
+  if (plan->rotary_dim < 2 || plan->rotary_dim > plan->head_dim || plan->rotary_dim % 2 != 0 || plan->head_dim > 256)
+    return paged_fail(KVQ_ERR_INVALID, fn, "the plan was not initialised by kvq_rope_plan_init");
+  return KVQ_OK;
+}
+
+namespace {
+
+struct RopeArgs {
+  const void* x;
+  void* out;
+  const int32_t* pos;
+  long long xt, xh, ot, oh;   // strides in elements
+  int T, H;
+  bool bf16;
+};
+
+// One thread per element pair (or copied element) of one row.
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ kvq_rope_plan P, RopeArgs a) {
+  const int half = P.rotary_dim / 2, units = half + (P.head_dim - P.rotary_dim);
+  const long long n = (long long)a.T * a.H * units;
+  for (long long u = blockIdx.x * 256ll + threadIdx.x; u < n; u += gridDim.x * 256ll) {
+    const long long row = u / units;
+    const int i = (int)(u - row * units);
+    const long long t = row / a.H, h = row - t * a.H;
+    const size_t xo = (size_t)(t * a.xt + h * a.xh), oo = (size_t)(t * a.ot + h * a.oh);
+    if (i >= half) {
+      const int c = P.rotary_dim + (i - half);
+      f_to_elem(a.out, oo + c, elem_to_f(a.x, xo + c, a.bf16), a.bf16);
+      continue;
+    }
+    const int c0 = P.interleaved ? 2 * i : i, c1 = P.interleaved ? 2 * i + 1 : i + half;
+    const float2 cs = rope_cos_sin(a.pos[t], P.step[i], P.magnitude);
+    const float x0 = elem_to_f(a.x, xo + c0, a.bf16), x1 = elem_to_f(a.x, xo + c1, a.bf16);
+    f_to_elem(a.out, oo + c0, fmaf(x0, cs.x, -x1 * cs.y), a.bf16);
+    f_to_elem(a.out, oo + c1, fmaf(x1, cs.x, x0 * cs.y), a.bf16);
+  }
+}
+
+kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_t xt, int64_t xh,
+                     const int32_t* positions, int T, int H, void* out, int64_t ot, int64_t oh, void* stream) {
+  const char* fn = "kvq_rope";
+  if (!plan) return paged_fail(KVQ_ERR_INVALID, fn, "plan is NULL");
+  if (kvq_status s = check_plan(plan, plan->head_dim, fn)) return s;
+  if (plan->head_dim % 8 != 0) return paged_fail(KVQ_ERR_INVALID, fn, "head_dim must be a multiple of 8");
+  if (dtype != KVQ_F16 && dtype != KVQ_BF16) return paged_fail(KVQ_ERR_INVALID, fn, "dtype must be KVQ_F16 or KVQ_BF16");
+  if (T < 0 || H < 0) return paged_fail(KVQ_ERR_INVALID, fn, "n_tokens and n_heads must be >= 0");
+  if (T == 0 || H == 0) return KVQ_OK;
+  if (kvq_status s = check_strides(xt, xh, fn, "x")) return s;
+  if (kvq_status s = check_strides(ot, oh, fn, "out")) return s;
+  if ((T > 1 && ot == 0) || (H > 1 && oh == 0)) return paged_fail(KVQ_ERR_INVALID, fn, "out: rows must not overlap");
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");
+  if (kvq_status s = check_buffer(x, dev, 16, fn, "x")) return s;
+  if (kvq_status s = check_buffer(out, dev, 16, fn, "out")) return s;
+  if (kvq_status s = check_buffer(positions, dev, 4, fn, "positions")) return s;
+  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, dtype == KVQ_BF16};
+  const long long n = (long long)T * H * (plan->head_dim - plan->rotary_dim / 2);
+  const int grid = (int)((n + 255) / 256 < 152 * 64 ? (n + 255) / 256 : 152 * 64);
+  rope_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(*plan, a);
+  if (cudaError_t e = cudaGetLastError()) return paged_cuda_fail(e, fn, "launch");
+  return KVQ_OK;
+}
+
+kvq_status plan_impl(const kvq_rope_config* c, kvq_rope_plan* p) {
+  const char* fn = "kvq_rope_plan_init";
+  auto bad = [&](const char* what) { return paged_fail(KVQ_ERR_INVALID, fn, what); };
+  if (!c || !p) return bad("NULL argument");
+  if (c->head_dim < 2 || c->head_dim > 256 || c->head_dim % 2) return bad("head_dim must be even and in 2..256");
+  if (c->rotary_dim < 2 || c->rotary_dim > c->head_dim || c->rotary_dim % 2)
+    return bad("rotary_dim must be even and in 2..head_dim");
+  if (c->interleaved != 0 && c->interleaved != 1) return bad("interleaved must be 0 or 1");
+  if (c->scaling < KVQ_ROPE_NONE || c->scaling > KVQ_ROPE_YARN) return bad("unknown scaling");
+  if (!(c->base > 1.0) || !std::isfinite(c->base)) return bad("base must be finite and > 1");
+  const bool scaled = c->scaling != KVQ_ROPE_NONE;
+  const bool blend = c->scaling == KVQ_ROPE_PARTS || c->scaling == KVQ_ROPE_YARN;
+  if (scaled && (!(c->factor >= 1.0) || !std::isfinite(c->factor))) return bad("factor must be finite and >= 1");
+  if (blend && c->original_ctx < 1) return bad("original_ctx must be >= 1");
+  if (blend && !(c->low > 0.0 && c->low < c->high && std::isfinite(c->high))) return bad("0 < low < high is needed");
+  if (!(c->magnitude >= 0.0) || !std::isfinite(c->magnitude)) return bad("magnitude must be finite and >= 0");
+  const int rd = c->rotary_dim;
+  double base = c->base;
+  if (c->scaling == KVQ_ROPE_NTK) {
+    if (rd < 4) return bad("NTK scaling needs rotary_dim >= 4");
+    base *= std::pow(c->factor, (double)rd / (rd - 2));
+    if (!std::isfinite(base)) return bad("base * factor^(rotary_dim / (rotary_dim - 2)) overflows");
+  }
+  const double two_pi = 6.283185307179586476925286766559;
+  double d_lo = 0, d_hi = 1;   // YARN: pair indices where the blend falls from 1 to 0
+  if (c->scaling == KVQ_ROPE_YARN) {
+    auto d = [&](double turns) { return rd * std::log(c->original_ctx / (two_pi * turns)) / (2.0 * std::log(base)); };
+    d_lo = std::fmax(std::floor(d(c->high)), 0.0);
+    d_hi = std::fmin(std::ceil(d(c->low)), rd - 1.0);
+  }
+  p->head_dim = c->head_dim;
+  p->rotary_dim = rd;
+  p->interleaved = c->interleaved;
+  p->magnitude = (float)(c->magnitude > 0 ? c->magnitude
+                                          : c->scaling == KVQ_ROPE_YARN ? 0.1 * std::log(c->factor) + 1.0 : 1.0);
+  for (int i = 0; i < 128; ++i) {
+    p->step[i] = 0;
+    if (i >= rd / 2) continue;
+    double w = std::pow(base, -2.0 * i / rd), k = 1.0;
+    if (c->scaling == KVQ_ROPE_LINEAR) k = 0.0;
+    if (c->scaling == KVQ_ROPE_PARTS) k = (c->original_ctx * w / two_pi - c->low) / (c->high - c->low);
+    if (c->scaling == KVQ_ROPE_YARN) k = 1.0 - (i - d_lo) / std::fmax(d_hi - d_lo, 1e-3);
+    k = std::fmin(std::fmax(k, 0.0), 1.0);
+    if (scaled) w = c->scaling == KVQ_ROPE_NTK ? w : w * k + w / c->factor * (1.0 - k);
+    p->step[i] = (uint64_t)std::llrint(std::ldexp(w / two_pi, 62)) << 2;   // w <= 1: below a sixth of a turn
+  }
+  return KVQ_OK;
+}
+
+}  // namespace
+}  // namespace kvq
+
+extern "C" kvq_status kvq_rope_plan_init(const kvq_rope_config* cfg, kvq_rope_plan* plan) try {
+  return kvq::plan_impl(cfg, plan);
+} catch (...) {   // no exception leaves the C ABI (only a failing string allocation can throw)
+  return KVQ_ERR_HOST_OOM;
+}
+
+extern "C" kvq_status kvq_rope(const kvq_rope_plan* plan, int dtype, const void* x, int64_t x_token_stride,
+                               int64_t x_head_stride, const int32_t* positions, int n_tokens, int n_heads, void* out,
+                               int64_t out_token_stride, int64_t out_head_stride, void* stream) try {
+  return kvq::rope_impl(plan, dtype, x, x_token_stride, x_head_stride, positions, n_tokens, n_heads, out,
+                        out_token_stride, out_head_stride, stream);
+} catch (...) {
+  return KVQ_ERR_HOST_OOM;
+}

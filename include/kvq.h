@@ -301,6 +301,152 @@ kvq_status kvq_dense_decode_noalloc(const void* q, const void* k, const void* v,
                                     int n_q_heads, int n_kv_heads, int n_tokens, void* out,
                                     void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Paged 4-bit cache and rotary positions (not part of the paper: operators of this
+ * library for serving loops that keep a whole cache in device memory).
+ *
+ * A page holds 64 consecutive tokens of every KV head; a pool of pages is one caller-owned
+ * device buffer [n_pages][Hkv][kvq_paged_page_bytes(D)], 16-byte aligned, whose initial
+ * contents do not matter.  Keys and values are held in 4 bits per element with a binary16
+ * scale s and offset o per (token, 32-channel group), x^ = o + s * code, code in 0..15:
+ * s = fp16 rounded up of (max - min) / 15, o = fp16 of the group's minimum and code =
+ * rint((x - o) / s), ties to even, clamped.  Values of odd slots count down from the
+ * maximum instead (o = fp16 of the maximum, s negative), so that sums of codes over tokens
+ * change sign from one token to the next and do not lose precision to a common offset.
+ * Elements beyond the binary16 range are held as +-65504.  Slot p * 64 + i is token i of
+ * page p.
+ *
+ * Element types of q, k, v and outputs: kvq_dtype.  Strided operands [tokens, heads, D]
+ * are given by a base pointer (16-byte aligned) and the strides of tokens and heads in
+ * elements (multiples of 8); the D elements of a row are contiguous.  Every buffer is
+ * device memory of the current device.  All calls are stream-ordered, allocate nothing
+ * and may be captured into a CUDA graph.
+ * ---------------------------------------------------------------------------------- */
+typedef enum kvq_dtype { KVQ_F16 = 0, KVQ_BF16 = 1 } kvq_dtype;
+
+/* How rotary frequencies are scaled for contexts beyond the trained one (factor f,
+ * trained context n).  w_i = base^(-2i / rotary_dim) is pair i's angle per position and
+ * u_i = n w_i / (2 pi) its turns within the trained context. */
+typedef enum kvq_rope_scaling {
+  KVQ_ROPE_NONE = 0,
+  KVQ_ROPE_LINEAR = 1, /* w_i / f */
+  KVQ_ROPE_NTK = 2,    /* base * f^(rotary_dim / (rotary_dim - 2)) in place of base */
+  KVQ_ROPE_PARTS = 3,  /* k w_i + (1 - k) w_i / f, k = (u_i - low) / (high - low) clamped to
+                          [0, 1] */
+  KVQ_ROPE_YARN = 4    /* the same blend with k falling from 1 to 0 over the pair index,
+                          between floor(d(high)) and ceil(d(low)), d(u) = rotary_dim
+                          ln(n / (2 pi u)) / (2 ln base) (clamped to 0 and rotary_dim - 1);
+                          cos and sin times `magnitude` */
+} kvq_rope_scaling;
+
+typedef struct kvq_rope_config {
+  int head_dim;      /* even, 2..256 */
+  int rotary_dim;    /* even, 2..head_dim: elements 0..rotary_dim-1 of a head are rotated */
+  int interleaved;   /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
+  int scaling;       /* kvq_rope_scaling */
+  double base;       /* > 1 */
+  double factor;     /* >= 1; used by every scaling but NONE */
+  int original_ctx;  /* n >= 1; used by PARTS and YARN */
+  double low, high;  /* 0 < low < high, turns; used by PARTS and YARN */
+  double magnitude;  /* factor on cos and sin; 0: 1, and 0.1 ln(f) + 1 with YARN */
+} kvq_rope_config;
+
+/* What the kernels take: plain data, initialised on the host by kvq_rope_plan_init and
+ * copied by value into every launch (no device memory, nothing to destroy). */
+typedef struct kvq_rope_plan {
+  int32_t head_dim, rotary_dim, interleaved;
+  float magnitude;
+  uint64_t step[128];   /* angle per position of each pair, in 2^-64 turns */
+} kvq_rope_plan;
+
+/* kvq_rope_plan_init -- fill `plan` from `cfg` (host only; no CUDA call).
+ * Errors: KVQ_ERR_INVALID (NULL, or a field outside the ranges above). */
+kvq_status kvq_rope_plan_init(const kvq_rope_config* cfg, kvq_rope_plan* plan);
+
+/* kvq_rope -- rotary positions: out[t, h] = x[t, h] with pair i turned by positions[t] w_i
+ * (times the plan's magnitude); elements from rotary_dim on are copied.
+ *   x, out     [n_tokens, n_heads, plan->head_dim] strided; out may be x with the same
+ *              strides (in place), and must not overlap it otherwise
+ *   positions  [n_tokens] int32, device; any value.  A negative position turns back: with
+ *              -p the call is the transpose of the call with p (its gradient), and undoes
+ *              it where the magnitude is 1.
+ * head_dim must be a multiple of 8.  Angles are exact to 2^-33 turn plus the rounding of
+ * the frequencies to double, for positions of any size.  Arithmetic in fp32, one rounding
+ * to the element type.  n_tokens or n_heads = 0 is a no-op.
+ * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_rope(const kvq_rope_plan* plan, int dtype, const void* x, int64_t x_token_stride,
+                    int64_t x_head_stride, const int32_t* positions, int n_tokens, int n_heads, void* out,
+                    int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* kvq_paged_page_bytes -- bytes of one page of one KV head (head_dim 64 or 128).
+ * Errors: KVQ_ERR_INVALID. */
+kvq_status kvq_paged_page_bytes(int head_dim, size_t* bytes);
+
+/* kvq_paged_append -- write tokens into pages: keys are turned by their positions in fp32
+ * (plan != NULL), keys and values quantised from fp32 and stored in their slots.
+ *   plan       NULL: keys are stored as they are (positions and q are then NULL)
+ *   k, v       [n_tokens, n_kv_heads, head_dim] strided
+ *   slots      [n_tokens] int32, device: where each token goes.  Slots outside the pool
+ *              (negative ones: padding) are skipped.  The slots of one call must be
+ *              distinct: a slot given twice ends up holding a mixture of its tokens.
+ *   positions  [n_tokens] int32, device
+ *   pages      the pool; only the bytes of the given slots change
+ *   q, q_out   optional (NULL): [n_tokens, n_q_heads, head_dim] strided, turned by the same
+ *              positions in the same launch (as kvq_rope), for every token, skipped or not
+ * head_dim 64 or 128.  One kernel.  n_tokens = 0 is a no-op.
+ * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_paged_append(const kvq_rope_plan* plan, int dtype, const void* k, int64_t k_token_stride,
+                            int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                            const int32_t* slots, const int32_t* positions, int n_tokens, int n_kv_heads,
+                            int head_dim, void* pages, int n_pages, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, int n_q_heads, void* q_out, int64_t q_out_token_stride,
+                            int64_t q_out_head_stride, void* stream);
+
+/* kvq_paged_gather -- read tokens back from pages: k, v [n_tokens, n_kv_heads, head_dim]
+ * strided receive o + s * code of the slots (keys as turned by the append), computed in
+ * fp32 and rounded to the element type; rows of slots outside the pool become 0.
+ * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_paged_gather(const void* pages, int n_pages, const int32_t* slots, int n_tokens, int n_kv_heads,
+                            int head_dim, int dtype, void* k, int64_t k_token_stride, int64_t k_head_stride, void* v,
+                            int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/* kvq_paged_attention_workspace -- device workspace bytes that kvq_paged_attention needs
+ * for this shape on the current device, whatever the lengths.
+ * Errors: KVQ_ERR_INVALID (NULL bytes, bad shape), KVQ_ERR_CUDA. */
+kvq_status kvq_paged_attention_workspace(int batch, int n_q_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                                         size_t* bytes);
+
+/* kvq_paged_attention -- decode attention over the paged 4-bit cache:
+ * out = softmax(scale q k^T) v over the tokens each query sees.
+ *   q           [batch * n_q_tokens, Hq, head_dim] strided: the last n_q_tokens tokens of
+ *               each sequence (1 for plain decoding, more when drafted tokens are verified)
+ *   page_table  [batch, max_pages] int32, device, row stride table_stride elements: page j
+ *               of a sequence holds its tokens 64j..64j+63.  Entries past the sequence's
+ *               length are never read; tokens of an entry outside the pool are not seen.
+ *   seq_lens    [batch] int32, device: tokens of each sequence in the cache, the
+ *               n_q_tokens new ones included; clamped to 0..64 max_pages.  0: a padding
+ *               sequence.
+ *   window      0: query i of a sequence of n tokens sees tokens 0..n - n_q_tokens + i;
+ *               w > 0: only the last w of them
+ *   scale       0: 1 / sqrt(head_dim)
+ *   out         [batch, n_q_tokens, Hq, head_dim], contiguous, of q's type
+ *   lse         optional (NULL): [batch, n_q_tokens, Hq] float, natural log of the sum of
+ *               exp(scale q k), for merging with attention over other keys
+ * A query that sees no token gets out = 0 and lse = -inf.  What pages hold behind a
+ * sequence's length (NaN included) does not matter.
+ *   workspace   at least kvq_paged_attention_workspace(...) bytes, 16-byte aligned; needs no
+ *               initialisation.  Calls that share it must not overlap on the GPU.
+ * Hq / Hkv an integer in 1..64, n_q_tokens 1..64, batch <= 4096, head_dim 64 or 128,
+ * batch * max_pages < 2^31.  Scores and sums in fp32.  batch = 0 is a no-op.  Every
+ * device-side wait is bounded (2 s); one that runs out, which does not happen in correct
+ * operation, makes the affected outputs NaN.
+ * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_paged_attention(int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               const void* pages, int n_pages, const int32_t* page_table, int64_t table_stride,
+                               int max_pages, const int32_t* seq_lens, int batch, int n_q_tokens, int n_q_heads,
+                               int n_kv_heads, int head_dim, int window, float scale, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
