@@ -1,8 +1,30 @@
 // kvq_paged_attn.cu -- decode attention over the paged 4-bit cache.
 //
-// With k^ = o + s code per group g of 32 channels,
-//   score_t = sum_g s_tg (q_g . code_tg) + o_tg sum(q_g),   out = sum_t p_t (o_tg + s_tg code_tc) / sum_t p_t
-// over the tokens that a query sees, p_t = exp(score_t - m).
+// With k^ = o + s code per group g of 32 channels (and v^ likewise),
+//   score_t = scale (sum_g s_tg (q_g . code_tg) + sum_g o_tg sum(q_g))
+//   out_c   = (sum_t (p_t s_tg) code_tc + sum_t p_t o_tg) / sum_t p_t,   p_t = exp(score_t - m)
+// over the tokens that a query sees.  A token of one KV head is 160 bytes at head_dim 128 and
+// is read once, so HBM is the floor; the work per byte is what the design is about.
+//
+//  - Nibbles are never converted: masked out of their words they are binary16 subnormals
+//    n 2^-24 (low nibble of a byte) or 16 n 2^-24 (high nibble), exact MMA operands.
+//    Scales and offsets enter outside the code products: the key scales multiply the group's
+//    fp32 sums, the value scales the softmax weights, the offsets are MMAs of their own
+//    (4 of the 72 per page each).  Channels that sit in high nibbles carry 1/16 in q.
+//  - Scores: tokens are MMA rows, the (up to 8 per tile) query rows are columns: one
+//    m16n8k16 covers 16 tokens x 16 channels.  A score fragment turned by movmatrix is the B
+//    fragment (k = tokens) of the value product, whose rows are channels.
+//  - Weights go into the value product as binary16 halves hi + lo of p s (together 2^-21),
+//    formed by exact products.  With at most four query rows they fill one tile's eight
+//    columns (four hi, four lo); with more, hi and lo are two MMAs into the same sums.
+//  - Weights are p 2^k with k = 14 unless a value scale of 2 or more appears (then smaller,
+//    so that p s stays finite in binary16): small weights of long caches stay normal numbers.
+//  - The (sequence, KV head, row tile, page) units are numbered in that order and cut into
+//    equal contiguous ranges, one per warp, whatever the lengths; every warp works alone on
+//    whole pages, fed by bulk copies into its own shared-memory ring.  A group (sequence, KV
+//    head, row tile) that lies within one warp's range is written out directly; the pieces
+//    of one that is cut are merged within the CTA and then by a second kernel in a fixed
+//    order.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -15,77 +37,678 @@ namespace kvq {
 
 namespace {
 
+constexpr int PA_WARPS = 8;
+constexpr int PA_STAGES = 2;
+constexpr int PA_THREADS = 32 * PA_WARPS;
+constexpr int PA_K = 14;                                    // weights are p 2^14 at most
+constexpr unsigned long long PA_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
+
+// What the second kernel needs to know about a warp's range: the group that is open at its
+// end and started in it (or none), and the warp that ends that group.
+struct PaRec {
+  int b, gr, last_warp, started;
+};
+
 struct PaArgs {
   const void* q;
   const unsigned char* pages;
   const int32_t *table, *lens;
   void* out;
   float* lse;
+  float* part;   // [warps][2][R (HD + 2)]: 0: the end of a group begun in an earlier warp, 1: an open group
+  PaRec* recs;   // [warps]
   long long qt, qh, table_stride;
-  int n_pages, max_pages, B, Q, Hq, Hkv, n_rep, window;
-  float scale;
+  int n_pages, max_pages, B, Q, Hq, Hkv, n_rep, rows, RT, window, grid;
+  float scale_log2;   // scale * log2(e)
   bool bf16;
 };
 
-// One warp per (sequence, query token, query head): lanes split the tokens of a page for
-// the scores and the channels for the sums.
-template <int HD>
-__global__ void __launch_bounds__(128) paged_attention_kernel(PaArgs a) {
+// Tokens, first page and page count of a sequence.
+__device__ __forceinline__ int pa_len(const PaArgs& a, int b) { return min(max(a.lens[b], 0), a.max_pages * PG); }
+__device__ __forceinline__ int pa_first(const PaArgs& a, int len) {
+  return a.window ? max(0, len - a.Q + 1 - a.window) / PG : 0;
+}
+
+// Contiguous ranges of the T units: `ge` CTAs in use, none empty; within a CTA the first
+// min(PA_WARPS, units) warps, none empty.
+struct PaSplit {
+  long long T;
+  int ge;
+  __device__ __forceinline__ long long cta0(int c) const { return c * T / ge; }
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * ge - 1) / T); }
+  // global index of the warp that holds unit x
+  __device__ __forceinline__ int warp_of(long long x) const {
+    const int c = cta_of(x);
+    const long long c0 = cta0(c);
+    const int n = (int)(cta0(c + 1) - c0), na = min(PA_WARPS, n);
+    return c * PA_WARPS + (int)(((x - c0 + 1) * na - 1) / n);
+  }
+};
+
+__device__ __forceinline__ unsigned long long pa_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool pa_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool pa_wait_slow(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = pa_ns();
+  while (!pa_try(bar, parity))
+    if (pa_ns() - t0 > PA_WAIT_NS) return false;
+  return true;
+}
+__device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity) {
+  return pa_try(bar, parity) || pa_wait_slow(bar, parity);
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// N 32-bit words of shared memory in one load
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const unsigned char* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// R query rows per tile: PACK 4 (hi and lo weights share one column tile), else 8 NT.
+template <int HD, int NT, bool PACK>
+__global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a) {
   using L = Page<HD>;
-  __shared__ float qs[4][HD], ps[4][PG];
+  constexpr int G = L::G, MT = HD / 16, R = PACK ? 4 : 8 * NT, PART = R * (HD + 2);
+  constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ __align__(8) unsigned long long bars[PA_WARPS][PA_STAGES];
+  __shared__ long long open_key[PA_WARPS];
+  __shared__ int wsum[PA_WARPS];
+  int* pre = reinterpret_cast<int*>(sm + PA_WARPS * PA_STAGES * L::BYTES);   // [B + 1] pages before each sequence
+  int* slen = pre + a.B + 1;                                                 // [B]
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long n = (long long)a.B * a.Q * a.Hq;
-  for (long long u = blockIdx.x * 4ll + warp; u < n; u += gridDim.x * 4ll) {
-    const int h = (int)(u % a.Hq);
-    const long long tok = u / a.Hq;
-    const int b = (int)(tok / a.Q), i = (int)(tok % a.Q), g = h / a.n_rep;
-    const int len = min(max(a.lens[b], 0), a.max_pages * PG);
-    const int end = max(0, len - a.Q + 1 + i), begin = a.window ? max(0, end - a.window) : 0;
-    __syncwarp();
-    for (int c = lane; c < HD; c += 32) qs[warp][c] = elem_to_f(a.q, (size_t)(tok * a.qt + h * a.qh) + c, a.bf16);
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, acc[L::G];
-    for (int j = 0; j < L::G; ++j) acc[j] = 0.f;
-    for (int pg = begin / PG; pg * PG < end; ++pg) {
-      const int id = a.table[b * a.table_stride + pg];
-      if (id < 0 || id >= a.n_pages) continue;
-      const unsigned char* page = a.pages + ((size_t)id * a.Hkv + g) * L::BYTES;
-      auto h16 = [&](int off, int e) { return __half2float(reinterpret_cast<const __half*>(page + off)[e]); };
-      float s[2];
-      for (int r = 0; r < 2; ++r) {
-        const int t = lane + 32 * r;
-        s[r] = -INFINITY;
-        if (pg * PG + t < begin || pg * PG + t >= end) continue;
-        float x = 0.f;
-        for (int c = 0; c < HD; ++c) {
-          const int j = c % 32, kb = page[t * L::ROW + (j >> 3) * 4 * L::G + 4 * (c / 32) + ((j & 7) >> 1)];
-          x = fmaf(qs[warp][c], fmaf((float)((kb >> (4 * (c & 1))) & 15), h16(L::KS, t * L::G + c / 32), h16(L::KO, t * L::G + c / 32)), x);
-        }
-        s[r] = x * a.scale;
+  const int gid = lane >> 2, tig = lane & 3;
+  unsigned char* ring = sm + warp * PA_STAGES * L::BYTES;
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t bar_s = (uint32_t)__cvta_generic_to_shared(&bars[warp][0]);
+  pdl_trigger();
+  if (lane == 0) {
+    for (int s = 0; s < PA_STAGES; ++s) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(bar_s + 8 * s) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    open_key[warp] = -1;
+  }
+
+  // pages of every sequence, summed up; rows of empty sequences are written here
+  if (threadIdx.x == 0) pre[0] = 0;
+  for (int base = 0, run = 0; base < a.B; base += PA_THREADS) {
+    const int b = base + threadIdx.x;
+    const int len = b < a.B ? pa_len(a, b) : 0;
+    const int np = len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0;
+    int inc = np;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int before = run, all = run;
+    for (int w = 0; w < PA_WARPS; ++w) {
+      before += w < warp ? wsum[w] : 0;
+      all += wsum[w];
+    }
+    if (b < a.B) {
+      pre[b + 1] = before + inc;
+      slen[b] = len;
+    }
+    run = all;
+    __syncthreads();
+  }
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (slen[b] > 0) continue;
+    const size_t row0 = (size_t)b * a.Q * a.Hq;
+    for (size_t i = threadIdx.x; i < (size_t)a.Q * a.Hq * (HD / 8); i += PA_THREADS)
+      reinterpret_cast<uint4*>(a.out)[row0 * (HD / 8) + i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = threadIdx.x; i < a.Q * a.Hq; i += PA_THREADS) a.lse[row0 + i] = -INFINITY;
+  }
+
+  const int U = a.Hkv * a.RT;
+  PaSplit sp;
+  sp.T = (long long)pre[a.B] * U;
+  sp.ge = (int)min((long long)a.grid, sp.T);
+  const int gw = blockIdx.x * PA_WARPS + warp;
+  long long x0 = 0, x1 = 0;
+  if ((int)blockIdx.x < sp.ge) {
+    const long long c0 = sp.cta0(blockIdx.x);
+    const int n = (int)(sp.cta0(blockIdx.x + 1) - c0), na = min(PA_WARPS, n);
+    if (warp < na) {
+      x0 = c0 + (long long)warp * n / na;
+      x1 = c0 + (long long)(warp + 1) * n / na;
+    }
+  }
+
+  // a walk through the units: sequence b, group gr = KV head * RT + row tile, page p of np
+  struct Walk {
+    int b, gr, p, np, first;
+  };
+  auto enter = [&](Walk& w) {   // a sequence's page range
+    while (pre[w.b + 1] == pre[w.b]) ++w.b;
+    w.np = pre[w.b + 1] - pre[w.b];
+    w.first = pa_first(a, slen[w.b]);
+  };
+  auto advance = [&](Walk& w, bool more) {
+    if (++w.p < w.np) return;
+    w.p = 0;
+    if (++w.gr < U) return;
+    w.gr = 0;
+    ++w.b;
+    if (more) enter(w);
+  };
+  Walk cw = {0, 0, 0, 0, 0};
+  if (x0 < x1) {
+    const int pg = (int)(x0 / U);
+    int lo = 0, hi = a.B - 1;   // the last sequence with pre[b] <= pg
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= pg) lo = mid;
+      else hi = mid - 1;
+    }
+    cw.b = lo;
+    enter(cw);
+    const long long rem = x0 - (long long)pre[cw.b] * U;
+    cw.gr = (int)(rem / cw.np);
+    cw.p = (int)(rem - (long long)cw.gr * cw.np);
+  }
+  Walk pw = cw;             // the copies run PA_STAGES units ahead of the computation, the
+  long long px = x0;        // page numbers one further
+  int next_id = x0 < x1 ? a.table[pw.b * a.table_stride + pw.first + pw.p] : 0;
+  uint32_t valid = 0;       // bit s: stage s holds a page
+  const unsigned long long pol = evict_first_policy();
+  auto issue = [&](int s) {
+    const bool ok = next_id >= 0 && next_id < a.n_pages;
+    valid = (valid & ~(1u << s)) | ((uint32_t)ok << s);
+    if (lane == 0) {
+      const uint32_t bar = bar_s + 8 * s;
+      if (ok) {
+        const unsigned char* src = a.pages + ((size_t)next_id * a.Hkv + pw.gr / a.RT) * L::BYTES;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(L::BYTES) : "memory");
+        if (a.RT == 1)   // read once
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+              :: "r"(ring_s + s * L::BYTES), "l"(src), "r"(L::BYTES), "r"(bar), "l"(pol) : "memory");
+        else
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                       :: "r"(ring_s + s * L::BYTES), "l"(src), "r"(L::BYTES), "r"(bar) : "memory");
+      } else {
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
       }
-      const float mn = fmaxf(m, warp_max(fmaxf(s[0], s[1])));
-      if (mn == -INFINITY) continue;
-      const float alpha = expf(m - mn), p0 = expf(s[0] - mn), p1 = expf(s[1] - mn);
-      m = mn;
-      l = l * alpha + warp_sum(p0 + p1);
-      __syncwarp();
-      ps[warp][lane] = p0;
-      ps[warp][lane + 32] = p1;
-      __syncwarp();
-      for (int j = 0; j < L::G; ++j) {
-        float x = 0.f;
-        for (int t = 0; t < PG; ++t) {
-          if (pg * PG + t < begin || pg * PG + t >= end) continue;
-          const int e = j * PG + vscale_at(t);
-          const int vb = page[L::VC + vcode_at<HD>(t, (lane >> 2) * 2 * L::G + 2 * j + ((lane & 3) >> 1))];
-          x = fmaf(ps[warp][t], fmaf((float)((vb >> (4 * (lane & 1))) & 15), h16(L::VS, e), h16(L::VO, e)), x);
+    }
+    ++px;
+    advance(pw, px < x1);
+    if (px < x1) next_id = a.table[pw.b * a.table_stride + pw.first + pw.p];
+  };
+  __syncwarp();
+#pragma unroll
+  for (int s = 0; s < PA_STAGES; ++s)
+    if (px < x1) issue(s);
+
+  // ---- state of the group at hand ----
+  uint32_t qb[NT][G][2][2];   // B fragments of q: group, low and high nibbles
+  uint32_t qo[NT];            // B fragment of the group sums of q (hi and lo halves), for the offsets
+  float cs[NT][2];            // score factor of this lane's two columns
+  int c_lo[NT][2], c_hi[NT][2];   // tokens its columns see
+  int t_lo = 0, t_hi = 0, t_all = 0, t_end = 0;   // seen by every row: [t_lo, t_hi); by any: [t_all, t_end)
+  float m[NT][2], l[NT][2], acc[NT][MT][4], off[NT][4];
+  uint32_t smax = 0;          // largest value scale of the group so far when 2 or more (binary16 bits)
+  bool started = false, failed = false;
+
+  auto load_group = [&](const Walk& w) {
+    const int len = slen[w.b], g = w.gr / a.RT, r0 = (w.gr - g * a.RT) * R;
+    const int rn = min(R, a.rows - r0);
+    const int i0 = r0 / a.n_rep, i1 = (r0 + rn - 1) / a.n_rep;   // first and last query token of the tile
+    auto hi_of = [&](int i) { return max(0, len - a.Q + 1 + i); };
+    auto lo_of = [&](int i) { return a.window ? max(0, hi_of(i) - a.window) : 0; };
+    t_hi = hi_of(i0), t_lo = lo_of(i1), t_all = lo_of(i0), t_end = len;
+#pragma unroll
+    for (int ct = 0; ct < NT; ++ct) {
+      const int r = ct * 8 + (PACK ? gid & 3 : gid);   // this lane's row of q
+      const bool live = r < rn;
+      const int rr = r0 + (live ? r : 0), i = rr / a.n_rep, h = g * a.n_rep + rr - i * a.n_rep;
+      const unsigned short* src = static_cast<const unsigned short*>(a.q) +
+                                  (size_t)(((long long)w.b * a.Q + i) * a.qt + h * a.qh) + 8 * tig;
+      float f[G][8], mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 32 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = pair_to_f2(word_of(v, j), a.bf16);
+          f[k][2 * j] = p.x, f[k][2 * j + 1] = p.y;
+          mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
         }
-        acc[j] = acc[j] * alpha + x;
       }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // the row times 2^e with a largest element in [2^9, 2^10): binary16 keeps all of a
+      // binary16 or bfloat16 element down to 2^-24 of 2^10 (elements below lose bits that
+      // are 2^-34 of the row's largest), and the sums of 32 stay finite
+      int e = 0;
+      if (mx > 0.f) frexpf(mx, &e);
+      e = max(-100, min(100, 10 - e));
+      const float up = ldexpf(1.f, e), upl = up * 0.0625f;
+      float gs[G];
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t += f[k][j];
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        gs[k] = t * up;
+        qb[ct][k][0][0] = h2_as_u32(__floats2half2_rn(f[k][0] * up, f[k][4] * up));
+        qb[ct][k][0][1] = h2_as_u32(__floats2half2_rn(f[k][2] * up, f[k][6] * up));
+        qb[ct][k][1][0] = h2_as_u32(__floats2half2_rn(f[k][1] * upl, f[k][5] * upl));
+        qb[ct][k][1][1] = h2_as_u32(__floats2half2_rn(f[k][3] * upl, f[k][7] * upl));
+      }
+      // k columns 2tig, 2tig+1: the sums of two groups, hi halves first, then lo halves
+      const int pr = tig % (G / 2), piece = tig / (G / 2);
+      const float u = pr ? gs[G - 2] : gs[0], v = pr ? gs[G - 1] : gs[1];
+      const __half2 h2 = __floats2half2_rn(u, v);
+      const float2 hf = __half22float2(h2);
+      qo[ct] = piece == 0 ? h2_as_u32(h2) : piece == 1 ? h2_as_u32(__floats2half2_rn(u - hf.x, v - hf.y)) : 0u;
+      const float mine = ldexpf(a.scale_log2, -e);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        cs[ct][j] = __shfl_sync(0xffffffffu, mine, (2 * tig + j) * 4);
+        const int c = ct * 8 + (PACK ? (2 * tig + j) & 3 : 2 * tig + j);
+        const int ci = (r0 + min(c, rn - 1)) / a.n_rep;
+        c_lo[ct][j] = lo_of(ci), c_hi[ct][j] = hi_of(ci);
+        m[ct][j] = -INFINITY, l[ct][j] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[ct][mt][j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) off[ct][j] = 0.f;
+    }
+    smax = 0;
+  };
+
+  const int pr_k = tig % (G / 2);
+  // byte of this lane's value pieces of tokens 2tig and 2tig + 1
+  const int vrow0 = (HD == 128 ? (2 * tig + (tig & 1)) : (2 * tig + (tig >> 1))) * L::ROW;
+  const int vrow1 = (HD == 128 ? (2 * tig + 1 - (tig & 1)) : (2 * tig + 1 - (tig >> 1))) * L::ROW;
+  const int vx = HD == 128 ? (gid * 8) ^ (32 * (tig >> 1)) : gid * 4;
+
+  auto page = [&](unsigned char* pg, int tok0) {
+    const bool edge = tok0 < t_lo || tok0 + PG > t_hi;
+    if (edge) {
+      if (tok0 + PG <= t_all || tok0 >= t_end) return;
+      // what lies outside of every row's tokens may be anything, NaN included: the value
+      // scales and offsets there become 0 (the scores are masked below)
+      for (int i = lane; i < G * PG; i += 32) {
+        const int t = i % PG, at = (i / PG) * PG + vscale_at(t);
+        if (tok0 + t < t_all || tok0 + t >= t_end) {
+          reinterpret_cast<__half*>(pg + L::VS)[at] = __ushort_as_half(0);
+          reinterpret_cast<__half*>(pg + L::VO)[at] = __ushort_as_half(0);
+        }
+      }
+      // ordered before the bulk copy that will overwrite the stage
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     }
-    for (int j = 0; j < L::G; ++j) f_to_elem(a.out, (size_t)u * HD + 32 * j + lane, l > 0.f ? acc[j] / l : 0.f, a.bf16);
-    if (a.lse && lane == 0) a.lse[u] = l > 0.f ? m + logf(l) : -INFINITY;
+    // value scales of 2 or more (exponent field above 15) lower the weights' power of two
+    const float k_old = (float)(PA_K - max(0, (int)(smax >> 10) - 15));
+    {
+      uint32_t w[G];
+      lds(w, pg + L::VS + lane * 4 * G);
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < G; ++i) any |= w[i];
+      if (__any_sync(0xffffffffu, (any & 0x40004000u) != 0u)) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < G; ++i) mx = max(mx, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        smax = max(smax, __reduce_max_sync(0xffffffffu, mx));
+      }
+    }
+    const float k_new = (float)(PA_K - max(0, (int)(smax >> 10) - 15));
+
+    // ---- scores (base 2) ----
+    float S[NT][4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ta = 16 * i + gid, tb = ta + 8;
+      uint32_t wa[G], wb[G], sa[G / 2], sb[G / 2];
+      lds(wa, pg + ta * L::ROW + tig * 4 * G);
+      lds(wb, pg + tb * L::ROW + tig * 4 * G);
+      lds(sa, pg + L::KS + ta * 2 * G);
+      lds(sb, pg + L::KS + tb * 2 * G);
+      const uint32_t oa = *reinterpret_cast<const uint32_t*>(pg + L::KO + ta * 2 * G + 4 * pr_k);
+      const uint32_t ob = *reinterpret_cast<const uint32_t*>(pg + L::KO + tb * 2 * G + 4 * pr_k);
+      float2 ra[NT], rb[NT];
+#pragma unroll
+      for (int ct = 0; ct < NT; ++ct) ra[ct] = rb[ct] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t xa = wa[g] >> 8, xb = wb[g] >> 8;
+        const float2 s2a = __half22float2(u32_as_h2(sa[g >> 1])), s2b = __half22float2(u32_as_h2(sb[g >> 1]));
+        const float fa = (g & 1) ? s2a.y : s2a.x, fb = (g & 1) ? s2b.y : s2b.x;
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct) {
+          float X[4] = {0.f, 0.f, 0.f, 0.f};
+          mma(X, wa[g] & LO, wb[g] & LO, xa & LO, xb & LO, qb[ct][g][0][0], qb[ct][g][0][1]);
+          mma(X, wa[g] & HI, wb[g] & HI, xa & HI, xb & HI, qb[ct][g][1][0], qb[ct][g][1][1]);
+          ra[ct] = fma2(make_float2(X[0], X[1]), make_float2(fa, fa), ra[ct]);
+          rb[ct] = fma2(make_float2(X[2], X[3]), make_float2(fb, fb), rb[ct]);
+        }
+      }
+#pragma unroll
+      for (int ct = 0; ct < NT; ++ct) {
+        float O[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(O, oa, ob, 0u, 0u, qo[ct], 0u);
+        const float2 c = make_float2(cs[ct][0], cs[ct][1]);
+        const float2 ua = mul2(fma2(ra[ct], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[0], O[1])), c);
+        const float2 ub = mul2(fma2(rb[ct], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[2], O[3])), c);
+        S[ct][i][0] = ua.x, S[ct][i][1] = ua.y, S[ct][i][2] = ub.x, S[ct][i][3] = ub.y;
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = tok0 + (j < 2 ? ta : tb);
+            if (t < c_lo[ct][j & 1] || t >= c_hi[ct][j & 1]) S[ct][i][j] = -INFINITY;
+          }
+        }
+      }
+    }
+
+    // ---- softmax weights p 2^k ----
+#pragma unroll
+    for (int ct = 0; ct < NT; ++ct) {
+      float al[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float bm = fmaxf(S[ct][0][j], S[ct][0][j + 2]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) bm = fmaxf(bm, fmaxf(S[ct][i][j], S[ct][i][j + 2]));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+        const float mn = fmaxf(m[ct][j], bm), ref = mn == -INFINITY ? 0.f : mn;
+        al[j] = exp2_approx(m[ct][j] - ref + (k_new - k_old));
+        m[ct][j] = mn;
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          S[ct][i][j] = exp2_approx(S[ct][i][j] - ref + k_new);
+          S[ct][i][j + 2] = exp2_approx(S[ct][i][j + 2] - ref + k_new);
+          t += S[ct][i][j] + S[ct][i][j + 2];
+        }
+        l[ct][j] = fmaf(l[ct][j], al[j], t);
+      }
+      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          acc[ct][mt][0] *= al[0], acc[ct][mt][1] *= al[1];
+          acc[ct][mt][2] *= al[0], acc[ct][mt][3] *= al[1];
+        }
+        off[ct][0] *= al[0], off[ct][1] *= al[1];
+      }
+    }
+
+    // ---- values ----
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // B fragments of the weights (k = tokens 16i + 2tig, +1 and 8 more), hi and lo halves
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 p = make_float2(S[ct][i][2 * h], S[ct][i][2 * h + 1]);
+          const __half2 hi = __floats2half2_rn(p.x, p.y);
+          const float2 r = sub2(p, __half22float2(hi));
+          ph[ct][h] = movmatrix_t(h2_as_u32(hi));
+          pl[ct][h] = movmatrix_t(h2_as_u32(__floats2half2_rn(r.x, r.y)));
+        }
+      // offsets: rows = groups
+      {
+        uint32_t o[2] = {0u, 0u};
+        if (gid < G) lds(o, pg + L::VO + gid * 2 * PG + tig * 32 + i * 8);
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct) {
+          if (PACK) {
+            mma(off[ct], o[0], 0u, o[1], 0u, gid >= 4 ? pl[ct][0] : ph[ct][0], gid >= 4 ? pl[ct][1] : ph[ct][1]);
+          } else {
+            mma(off[ct], o[0], 0u, o[1], 0u, ph[ct][0], ph[ct][1]);
+            mma(off[ct], o[0], 0u, o[1], 0u, pl[ct][0], pl[ct][1]);
+          }
+        }
+      }
+      // codes of token pairs: word g of x[h] holds four channels of group g of two tokens
+      uint32_t x[2][G];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t t0[G / 2], t1[G / 2];
+        lds(t0, pg + L::VC + (16 * i + 8 * h) * L::ROW + vrow0 + vx);
+        lds(t1, pg + L::VC + (16 * i + 8 * h) * L::ROW + vrow1 + vx);
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[h][g] = __byte_perm(t0[g >> 1], t1[g >> 1], (g & 1) ? 0x7632 : 0x5410);
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        uint32_t s[2];
+        lds(s, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
+        const uint32_t y0 = x[0][g] >> 8, y1 = x[1][g] >> 8;
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct) {
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const __half2 sv = u32_as_h2(s[h]), p = u32_as_h2(ph[ct][h]);
+            const __half2 w = __hmul2_rn(p, sv);
+            const __half2 r = __hfma2(p, sv, __hneg2(w));   // exact remainder
+            hi[h] = h2_as_u32(w);
+            lo[h] = h2_as_u32(__hfma2(u32_as_h2(pl[ct][h]), sv, r));
+          }
+          if (PACK) {
+            const uint32_t b0 = gid >= 4 ? lo[0] : hi[0], b1 = gid >= 4 ? lo[1] : hi[1];
+            mma(acc[ct][2 * g], x[0][g] & LO, x[0][g] & HI, x[1][g] & LO, x[1][g] & HI, b0, b1);
+            mma(acc[ct][2 * g + 1], y0 & LO, y0 & HI, y1 & LO, y1 & HI, b0, b1);
+          } else {
+            mma(acc[ct][2 * g], x[0][g] & LO, x[0][g] & HI, x[1][g] & LO, x[1][g] & HI, hi[0], hi[1]);
+            mma(acc[ct][2 * g + 1], y0 & LO, y0 & HI, y1 & LO, y1 & HI, hi[0], hi[1]);
+            mma(acc[ct][2 * g], x[0][g] & LO, x[0][g] & HI, x[1][g] & LO, x[1][g] & HI, lo[0], lo[1]);
+            mma(acc[ct][2 * g + 1], y0 & LO, y0 & HI, y1 & LO, y1 & HI, lo[0], lo[1]);
+          }
+        }
+      }
+    }
+  };
+
+  // Writes the group's rows: the finished output (dst == nullptr) or sums, reference and
+  // weight sum into dst: [R][HD] floats, then [R][2].
+  auto emit = [&](const Walk& w, float* dst) {
+    const int g = w.gr / a.RT, r0 = (w.gr - g * a.RT) * R, rn = min(R, a.rows - r0);
+    const float k = (float)(PA_K - max(0, (int)(smax >> 10) - 15));
+#pragma unroll
+    for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float lt = l[ct][j];
+        lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+        lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+        lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+        if (failed) lt = __int_as_float(0x7fc00000);
+        const float ref = m[ct][j] == -INFINITY ? -INFINITY : m[ct][j] - k;
+        const int c = ct * 8 + 2 * tig + j;
+        const bool live = c < rn;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const int rr = r0 + (live ? c : 0), qi = rr / a.n_rep;
+        const size_t orow = ((size_t)w.b * a.Q + qi) * a.Hq + g * a.n_rep + (rr - qi * a.n_rep);
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) {
+          const float o = __shfl_sync(0xffffffffu, off[ct][j], 4 * gg + tig);
+          float4 v = make_float4(fmaf(acc[ct][2 * gg][j], NIB_ROW_SCALE_LO, o), fmaf(acc[ct][2 * gg][j + 2], NIB_ROW_SCALE_HI, o),
+                                 fmaf(acc[ct][2 * gg + 1][j], NIB_ROW_SCALE_LO, o),
+                                 fmaf(acc[ct][2 * gg + 1][j + 2], NIB_ROW_SCALE_HI, o));
+          if (PACK) {   // columns 4..7 hold the lo halves' sums
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, 2);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, 2);
+            v.z += __shfl_xor_sync(0xffffffffu, v.z, 2);
+            v.w += __shfl_xor_sync(0xffffffffu, v.w, 2);
+          }
+          if (PACK && tig >= 2) continue;
+          if (dst) {
+            *reinterpret_cast<float4*>(dst + c * HD + 32 * gg + 4 * gid) = v;
+          } else if (live) {
+            *reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.out) + orow * HD + 32 * gg + 4 * gid) =
+                make_uint2(f2_to_pair(v.x * inv, v.y * inv, a.bf16), f2_to_pair(v.z * inv, v.w * inv, a.bf16));
+          }
+        }
+        if (gid == 0 && !(PACK && tig >= 2)) {
+          if (dst) *reinterpret_cast<float2*>(dst + R * HD + 2 * c) = make_float2(ref, lt);
+          else if (live && a.lse) a.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+        }
+      }
+  };
+
+  bool open = false;
+  int it = 0;
+  for (long long x = x0; x < x1; ++x, ++it) {
+    if (!open) {
+      load_group(cw);
+      open = true;
+      started = cw.p == 0;
+    }
+    const int s = it % PA_STAGES;
+    if (!failed && !pa_wait(bar_s + 8 * s, (uint32_t)(it / PA_STAGES) & 1u)) failed = true;
+    failed = __any_sync(0xffffffffu, failed);
+    if (!failed && ((valid >> s) & 1u)) page(ring + s * L::BYTES, (cw.first + cw.p) * PG);
+    __syncwarp();
+    if (!failed && px < x1) issue(s);
+    if (cw.p + 1 == cw.np) {
+      emit(cw, started ? nullptr : a.part + ((size_t)gw * 2) * PART);
+      open = false;
+    }
+    if (x + 1 < x1) advance(cw, true);
+  }
+  if (failed)   // the copies still in flight write into this CTA's memory: wait for them, within limits
+    for (int k = 0; k < PA_STAGES && it - 1 - k >= 0; ++k) pa_wait(bar_s + 8 * ((it - 1 - k) % PA_STAGES), (uint32_t)((it - 1 - k) / PA_STAGES) & 1u);
+  // an open group's piece goes to this warp's ring, which no copy uses any more
+  if (open) emit(cw, reinterpret_cast<float*>(ring));
+  if (lane == 0) {
+    open_key[warp] = open ? (long long)cw.b * U + cw.gr : -1;
+    PaRec r = {cw.b, cw.gr, 0, open && started};
+    if (r.started) r.last_warp = sp.warp_of((long long)pre[cw.b] * U + (long long)(cw.gr + 1) * cw.np - 1);
+    a.recs[gw] = r;
+  }
+  __syncthreads();
+  // the first warp of each run of warps with the same open group: one piece per run
+  for (int w0 = 0; w0 < PA_WARPS; ++w0) {
+    if (open_key[w0] < 0 || (w0 > 0 && open_key[w0 - 1] == open_key[w0])) continue;
+    int w1 = w0 + 1;
+    while (w1 < PA_WARPS && open_key[w1] == open_key[w0]) ++w1;
+    float* dst = a.part + ((size_t)(blockIdx.x * PA_WARPS + w0) * 2 + 1) * PART;
+    for (int e = threadIdx.x; e < R * HD / 4; e += PA_THREADS) {
+      const int c = e / (HD / 4);
+      auto piece = [&](int w) { return reinterpret_cast<const float*>(sm + w * PA_STAGES * L::BYTES); };
+      float M = -INFINITY, Ls = 0.f;
+      for (int w = w0; w < w1; ++w) M = fmaxf(M, piece(w)[R * HD + 2 * c]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = w0; w < w1; ++w) {
+        const float mw = piece(w)[R * HD + 2 * c], f = mw == -INFINITY ? 0.f : exp2_approx(mw - M);
+        const float4 v = reinterpret_cast<const float4*>(piece(w))[e];
+        Ls = fmaf(piece(w)[R * HD + 2 * c + 1], f, Ls);
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+      }
+      reinterpret_cast<float4*>(dst)[e] = o;
+      if (e % (HD / 4) == 0) *reinterpret_cast<float2*>(dst + R * HD + 2 * c) = make_float2(M, Ls);
+    }
+  }
+}
+
+// Adds up the pieces of the groups that were cut: CTA c takes the groups that started in
+// CTA c of the first kernel and were still open at the end of one of its warps.  Pieces in
+// order: the run of warps that started it, one per following CTA, and the ending warp's.
+constexpr int PC_THREADS = 512;
+template <int HD, int R>
+__global__ void __launch_bounds__(PC_THREADS) paged_combine_kernel(PaArgs a) {
+  constexpr int PART = R * (HD + 2), VEC = R * HD / 4, KS = PC_THREADS / VEC;   // KS threads share a sum
+  static_assert(VEC * KS == PC_THREADS, "the rows of a tile fill the block");
+  __shared__ float4 red[PC_THREADS];
+  __shared__ float redl[PC_THREADS];
+  pdl_wait();
+  const int ks = threadIdx.x / VEC, e = threadIdx.x % VEC, c = e / (HD / 4);
+  for (int w = 0; w < PA_WARPS; ++w) {
+    const int gw = blockIdx.x * PA_WARPS + w;
+    const PaRec r = a.recs[gw];
+    if (!r.started) continue;
+    const int last_cta = r.last_warp / PA_WARPS, first = blockIdx.x;
+    // whole or partial CTAs after the first whose warp 0 leaves the group open
+    const int nl = last_cta - first - ((last_cta > first && r.last_warp % PA_WARPS == 0) ? 1 : 0);
+    const int n = nl + 2;
+    auto piece = [&](int k) {
+      const size_t slot = k == 0 ? (size_t)gw * 2 + 1
+                          : k <= nl ? (size_t)(first + k) * PA_WARPS * 2 + 1 : (size_t)r.last_warp * 2;
+      return a.part + slot * PART;
+    };
+    float M = -INFINITY;
+    for (int k = 0; k < n; ++k) M = fmaxf(M, piece(k)[R * HD + 2 * c]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float Ls = 0.f;
+#pragma unroll 4
+    for (int k = ks; k < n; k += KS) {
+      const float* p = piece(k);
+      const float2 ml = *reinterpret_cast<const float2*>(p + R * HD + 2 * c);
+      const float4 v = reinterpret_cast<const float4*>(p)[e];
+      const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
+      Ls = fmaf(ml.y, f, Ls);
+      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    }
+    if (KS > 1) {
+      __syncthreads();
+      red[threadIdx.x] = o;
+      redl[threadIdx.x] = Ls;
+      __syncthreads();
+      if (ks == 0)
+        for (int k = 1; k < KS; ++k) {
+          const float4 v = red[k * VEC + e];
+          o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+          Ls += redl[k * VEC + e];
+        }
+    }
+    const int g = r.gr / a.RT, rr = (r.gr - g * a.RT) * R + c;
+    if (ks == 0 && rr < a.rows) {
+      const int qi = rr / a.n_rep;
+      const size_t orow = ((size_t)r.b * a.Q + qi) * a.Hq + g * a.n_rep + (rr - qi * a.n_rep);
+      const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+      reinterpret_cast<uint2*>(a.out)[orow * (HD / 4) + e % (HD / 4)] =
+          make_uint2(f2_to_pair(o.x * inv, o.y * inv, a.bf16), f2_to_pair(o.z * inv, o.w * inv, a.bf16));
+      if (a.lse && e % (HD / 4) == 0) a.lse[orow] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
+    }
   }
 }
 
@@ -97,7 +720,31 @@ const char* shape_error(int B, int Q, int Hq, int Hkv, int hd) {
   return nullptr;
 }
 
-size_t workspace_bytes_of(int, int, int, int, int) { return 16; }
+// Query rows per tile: the smallest that holds a KV head's rows, 16 at most.
+int tile_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+// partials (two per warp), then the records
+size_t part_bytes(int sms, int R, int hd) { return (size_t)sms * PA_WARPS * 2 * R * (hd + 2) * sizeof(float); }
+size_t ws_bytes(int sms, int Q, int Hq, int Hkv, int hd) {
+  return part_bytes(sms, tile_rows(Q * (Hq / Hkv)), hd) + (size_t)sms * PA_WARPS * sizeof(PaRec);
+}
+
+template <int HD, int NT, bool PACK>
+cudaError_t launch(const PaArgs& a, cudaStream_t st) {
+  constexpr int R = PACK ? 4 : 8 * NT;
+  const size_t smem = (size_t)PA_WARPS * PA_STAGES * Page<HD>::BYTES + (2 * (size_t)a.B + 1) * sizeof(int);
+  auto* k = paged_attention_kernel<HD, NT, PACK>;
+  if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+  k<<<a.grid, PA_THREADS, smem, st>>>(a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  return launch_dependent(paged_combine_kernel<HD, R>, dim3(a.grid), dim3(PC_THREADS), 0, st, a);
+}
 
 kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, const void* pages, int n_pages,
                           const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens, int B, int Q,
@@ -107,15 +754,16 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   if (dtype != KVQ_F16 && dtype != KVQ_BF16) return paged_fail(KVQ_ERR_INVALID, fn, "dtype must be KVQ_F16 or KVQ_BF16");
   if (const char* msg = shape_error(B, Q, Hq, Hkv, hd)) return paged_fail(KVQ_ERR_INVALID, fn, msg);
   if (n_pages < 1 || n_pages > (1 << 25)) return paged_fail(KVQ_ERR_INVALID, fn, "n_pages must be in 1..33554432");
-  if (max_pages < 1 || max_pages > (1 << 25) || (long long)B * max_pages >= (1ll << 31))
-    return paged_fail(KVQ_ERR_INVALID, fn, "max_pages must be in 1..33554432 and batch * max_pages below 2^31");
+  if (max_pages < 1 || max_pages > (1 << 24) || (long long)B * max_pages >= (1ll << 31))
+    return paged_fail(KVQ_ERR_INVALID, fn, "max_pages must be in 1..16777216 and batch * max_pages below 2^31");
   if (table_stride < 0) return paged_fail(KVQ_ERR_INVALID, fn, "table_stride must be >= 0");
   if (window < 0) return paged_fail(KVQ_ERR_INVALID, fn, "window must be >= 0");
   if (!std::isfinite(scale)) return paged_fail(KVQ_ERR_INVALID, fn, "scale must be finite");
   if (B == 0) return KVQ_OK;
   if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
-  int dev = 0;
+  int dev = 0, sms = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");
+  if (cudaError_t e = sm_count(&sms)) return paged_cuda_fail(e, fn, "device attributes");
   if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
   if (kvq_status s = check_buffer(pages, dev, 16, fn, "pages")) return s;
   if (kvq_status s = check_buffer(table, dev, 4, fn, "page_table")) return s;
@@ -124,16 +772,26 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   if (lse)
     if (kvq_status s = check_buffer(lse, dev, 4, fn, "lse")) return s;
   if (kvq_status s = check_buffer(workspace, dev, 16, fn, "workspace")) return s;
-  if (workspace_bytes < workspace_bytes_of(B, Q, Hq, Hkv, hd))
+  if (workspace_bytes < ws_bytes(sms, Q, Hq, Hkv, hd))
     return paged_fail(KVQ_ERR_INVALID, fn, "workspace smaller than kvq_paged_attention_workspace reports");
-  PaArgs a{q, static_cast<const unsigned char*>(pages), table, lens, out, lse, qt, qh, table_stride, n_pages, max_pages,
-           B, Q, Hq, Hkv, Hq / Hkv, window, scale != 0.f ? scale : 1.f / std::sqrt((float)hd), dtype == KVQ_BF16};
-  const long long blocks = ((long long)B * Q * Hq + 3) / 4;
-  const int grid = (int)std::min<long long>(blocks, 152 * 64);
+  PaArgs a = {};
+  a.q = q, a.pages = static_cast<const unsigned char*>(pages), a.table = table, a.lens = lens, a.out = out, a.lse = lse;
+  a.qt = qt, a.qh = qh, a.table_stride = table_stride, a.n_pages = n_pages, a.max_pages = max_pages;
+  a.B = B, a.Q = Q, a.Hq = Hq, a.Hkv = Hkv, a.n_rep = Hq / Hkv, a.rows = Q * a.n_rep;
+  a.window = std::min(window, 1 << 30);   // lengths stay below 2^30
+  a.scale_log2 = (scale != 0.f ? scale : 1.f / std::sqrt((float)hd)) * LOG2E_F;
+  a.bf16 = dtype == KVQ_BF16;
+  const int R = tile_rows(a.rows);
+  a.RT = (a.rows + R - 1) / R;
+  // one CTA per SM, fewer when the table cannot hold that many units
+  a.grid = (int)std::min<long long>(sms, (long long)B * max_pages * Hkv * a.RT);
+  a.part = static_cast<float*>(workspace);
+  a.recs = reinterpret_cast<PaRec*>(static_cast<char*>(workspace) + part_bytes(sms, R, hd));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (hd == 128) paged_attention_kernel<128><<<grid, 128, 0, st>>>(a);
-  else paged_attention_kernel<64><<<grid, 128, 0, st>>>(a);
-  if (cudaError_t e = cudaGetLastError()) return paged_cuda_fail(e, fn, "launch");
+  cudaError_t e = cudaSuccess;
+  if (hd == 128) e = R == 4 ? launch<128, 1, true>(a, st) : R == 8 ? launch<128, 1, false>(a, st) : launch<128, 2, false>(a, st);
+  else e = R == 4 ? launch<64, 1, true>(a, st) : R == 8 ? launch<64, 1, false>(a, st) : launch<64, 2, false>(a, st);
+  if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
 
@@ -146,7 +804,12 @@ extern "C" kvq_status kvq_paged_attention_workspace(int batch, int n_q_tokens, i
   if (!bytes) return kvq::paged_fail(KVQ_ERR_INVALID, fn, "NULL output");
   if (const char* msg = kvq::shape_error(batch, n_q_tokens, n_q_heads, n_kv_heads, head_dim))
     return kvq::paged_fail(KVQ_ERR_INVALID, fn, msg);
-  *bytes = kvq::workspace_bytes_of(batch, n_q_tokens, n_q_heads, n_kv_heads, head_dim);
+  int sms = 0;
+  if (cudaError_t e = kvq::sm_count(&sms)) {
+    cudaGetLastError();
+    return kvq::paged_cuda_fail(e, fn, "no current CUDA device");
+  }
+  *bytes = kvq::ws_bytes(sms, n_q_tokens, n_q_heads, n_kv_heads, head_dim);
   return KVQ_OK;
 } catch (...) {
   return KVQ_ERR_HOST_OOM;
