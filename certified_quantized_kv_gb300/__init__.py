@@ -546,8 +546,8 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     sequence; page_table: int32 [B, max_pages]; seq_lens: int32 [B], those tokens included (0:
     a padding sequence, whose out is 0); out: like q, contiguous; lse: float32 like q without
     its last dimension, or None.  `workspace` is a device uint8 tensor of at least
-    paged_attention_workspace(...) bytes (allocated here when omitted).  Returns
-    `workspace` so a caller can reuse it."""
+    paged_attention_workspace(...) bytes, zeroed once before its first use (allocated here
+    when omitted).  Returns `workspace` so a caller can reuse it."""
     import torch
     if q.dim() not in (3, 4):
         raise ValueError("q must be [batch, n_q_heads, head_dim] or [batch, n_q_tokens, n_q_heads, head_dim]")
@@ -578,8 +578,7 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     lib = load_library()
     if workspace is None:
         with torch.cuda.device(dev):
-            workspace = torch.empty(max(paged_attention_workspace(B, Q, hq, hkv, hd), 16), dtype=torch.uint8,
-                                    device=dev)
+            workspace = torch.zeros(paged_attention_workspace(B, Q, hq, hkv, hd), dtype=torch.uint8, device=dev)
         if stream is not None:   # keep its memory until that stream is done with it
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                     else torch.cuda.ExternalStream(int(stream), device=dev))

@@ -22,9 +22,9 @@
 //  - The (sequence, KV head, row tile, page) units are numbered in that order and cut into
 //    equal contiguous ranges, one per warp, whatever the lengths; every warp works alone on
 //    whole pages, fed by bulk copies into its own shared-memory ring.  A group (sequence, KV
-//    head, row tile) that lies within one warp's range is written out directly; the pieces
-//    of one that is cut are merged within the CTA and then by a second kernel in a fixed
-//    order.
+//    head, row tile) that lies within one warp's range is written out directly.  The pieces
+//    of one that is cut are merged within the CTA, and across CTAs by the last of them to
+//    arrive, each time in a fixed order, so the result does not depend on timing.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -37,17 +37,23 @@ namespace kvq {
 
 namespace {
 
-constexpr int PA_WARPS = 8;
+#ifndef PAW
+#define PAW 8
+#endif
+#ifndef PATT
+#define PATT 4
+#endif
+constexpr int PA_WARPS = PAW;
 constexpr int PA_STAGES = 2;
 constexpr int PA_THREADS = 32 * PA_WARPS;
-constexpr int PA_K = 14;                                    // weights are p 2^14 at most
+constexpr int PA_STEP = PATT;                               // 16-token tiles per step
+#ifndef PALEAD
+#define PALEAD 2
+#endif
+constexpr int PA_LEAD = PALEAD;
+constexpr float PA_TOP = 14.f;                              // weights are 2^14 at most,
+constexpr float PA_SLACK = 4.f;                             // 2^10 when their reference is set
 constexpr unsigned long long PA_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
-
-// What the second kernel needs to know about a warp's range: the group that is open at its
-// end and started in it (or none), and the warp that ends that group.
-struct PaRec {
-  int b, gr, last_warp, started;
-};
 
 struct PaArgs {
   const void* q;
@@ -55,8 +61,10 @@ struct PaArgs {
   const int32_t *table, *lens;
   void* out;
   float* lse;
-  float* part;   // [warps][2][R (HD + 2)]: 0: the end of a group begun in an earlier warp, 1: an open group
-  PaRec* recs;   // [warps]
+  int* arrived;  // [CTAs] arrivals at the group that starts in a CTA and leaves it; 0 between calls
+  float* part;   // pieces of R (HD + 2) floats: [warps][2] (0: the end of a group begun in an
+                 // earlier warp, 1: an open group), then [CTAs][2] (0: of a group begun in an
+                 // earlier CTA, 1: of one that leaves the CTA)
   long long qt, qh, table_stride;
   int n_pages, max_pages, B, Q, Hq, Hkv, n_rep, rows, RT, window, grid;
   float scale_log2;   // scale * log2(e)
@@ -69,20 +77,14 @@ __device__ __forceinline__ int pa_first(const PaArgs& a, int len) {
   return a.window ? max(0, len - a.Q + 1 - a.window) / PG : 0;
 }
 
-// Contiguous ranges of the T units: `ge` CTAs in use, none empty; within a CTA the first
-// min(PA_WARPS, units) warps, none empty.
+// Equal contiguous ranges of T unit positions for `ge` CTAs, none empty.  A group takes PA_LEAD
+// positions besides one per page when the ranges are long enough, for what starting and
+// finishing it costs.
 struct PaSplit {
   long long T;
   int ge;
   __device__ __forceinline__ long long cta0(int c) const { return c * T / ge; }
   __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * ge - 1) / T); }
-  // global index of the warp that holds unit x
-  __device__ __forceinline__ int warp_of(long long x) const {
-    const int c = cta_of(x);
-    const long long c0 = cta0(c);
-    const int n = (int)(cta0(c + 1) - c0), na = min(PA_WARPS, n);
-    return c * PA_WARPS + (int)(((x - c0 + 1) * na - 1) / n);
-  }
 };
 
 __device__ __forceinline__ unsigned long long pa_ns() {
@@ -114,6 +116,13 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// ... with a zero C
+__device__ __forceinline__ void mma_z(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -139,12 +148,18 @@ template <int HD, int NT, bool PACK>
 __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a) {
   using L = Page<HD>;
   constexpr int G = L::G, MT = HD / 16, R = PACK ? 4 : 8 * NT, PART = R * (HD + 2);
-  constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
+  constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTE = 0x00FF00FFu;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ __align__(8) unsigned long long bars[PA_WARPS][PA_STAGES];
-  __shared__ long long open_key[PA_WARPS];
-  __shared__ int wsum[PA_WARPS];
-  int* pre = reinterpret_cast<int*>(sm + PA_WARPS * PA_STAGES * L::BYTES);   // [B + 1] pages before each sequence
+  // groups of each warp that are cut (sequence, group; -1: none): the one it ends, and the
+  // one it leaves open (started in this warp or before)
+  __shared__ int2 ended[PA_WARPS], open_at[PA_WARPS];
+  __shared__ bool open_new[PA_WARPS];
+  __shared__ int wsum[PA_WARPS], wcnt[PA_WARPS];
+  __shared__ int final_n[2];
+  __shared__ float4 red[PA_THREADS];
+  __shared__ float2 redm[PA_THREADS];
+  int* pre = reinterpret_cast<int*>(sm + PA_WARPS * PA_STAGES * L::BYTES);   // [B + 1] positions before each sequence
   int* slen = pre + a.B + 1;                                                 // [B]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -152,40 +167,53 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   unsigned char* ring = sm + warp * PA_STAGES * L::BYTES;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   const uint32_t bar_s = (uint32_t)__cvta_generic_to_shared(&bars[warp][0]);
-  pdl_trigger();
   if (lane == 0) {
     for (int s = 0; s < PA_STAGES; ++s) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(bar_s + 8 * s) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    open_key[warp] = -1;
+    ended[warp].x = open_at[warp].x = -1;
   }
 
-  // pages of every sequence, summed up; rows of empty sequences are written here
+  // pages of every sequence and their sum, then the positions before each sequence
+  auto pages_of = [&](int len) { return len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0; };
+  int pages = 0, full = 0;
+  for (int b = threadIdx.x; b < a.B; b += PA_THREADS) {
+    const int len = pa_len(a, b);
+    slen[b] = len;
+    pages += pages_of(len);
+    full += len > 0;
+  }
+  pages = __reduce_add_sync(0xffffffffu, pages);
+  full = __reduce_add_sync(0xffffffffu, full);
+  if (lane == 0) wsum[warp] = pages, wcnt[warp] = full;
+  __syncthreads();
+  pages = full = 0;
+#pragma unroll
+  for (int w = 0; w < PA_WARPS; ++w) pages += wsum[w], full += wcnt[w];
+  const int U = a.Hkv * a.RT;
+  const int lead = ((long long)pages + (long long)full * PA_LEAD) * U >= (long long)a.grid * PA_WARPS * (PA_LEAD + 2) ? PA_LEAD : 0;
   if (threadIdx.x == 0) pre[0] = 0;
   for (int base = 0, run = 0; base < a.B; base += PA_THREADS) {
     const int b = base + threadIdx.x;
-    const int len = b < a.B ? pa_len(a, b) : 0;
-    const int np = len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0;
-    int inc = np;
+    const int np = b < a.B ? pages_of(slen[b]) : 0;
+    int inc = np ? np + lead : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
+    __syncthreads();
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    int before = run, all = run;
+    int before = run;
+#pragma unroll
     for (int w = 0; w < PA_WARPS; ++w) {
       before += w < warp ? wsum[w] : 0;
-      all += wsum[w];
+      run += wsum[w];
     }
-    if (b < a.B) {
-      pre[b + 1] = before + inc;
-      slen[b] = len;
-    }
-    run = all;
-    __syncthreads();
+    if (b < a.B) pre[b + 1] = before + inc;
   }
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+  __syncthreads();
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {   // rows of empty sequences
     if (slen[b] > 0) continue;
     const size_t row0 = (size_t)b * a.Q * a.Hq;
     for (size_t i = threadIdx.x; i < (size_t)a.Q * a.Hq * (HD / 8); i += PA_THREADS)
@@ -194,56 +222,62 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       for (int i = threadIdx.x; i < a.Q * a.Hq; i += PA_THREADS) a.lse[row0 + i] = -INFINITY;
   }
 
-  const int U = a.Hkv * a.RT;
   PaSplit sp;
   sp.T = (long long)pre[a.B] * U;
   sp.ge = (int)min((long long)a.grid, sp.T);
+  if ((int)blockIdx.x >= sp.ge) return;
   const int gw = blockIdx.x * PA_WARPS + warp;
-  long long x0 = 0, x1 = 0;
-  if ((int)blockIdx.x < sp.ge) {
+  long long x0 = 0;
+  int n_pos = 0;   // positions of this warp
+  {
     const long long c0 = sp.cta0(blockIdx.x);
     const int n = (int)(sp.cta0(blockIdx.x + 1) - c0), na = min(PA_WARPS, n);
     if (warp < na) {
-      x0 = c0 + (long long)warp * n / na;
-      x1 = c0 + (long long)(warp + 1) * n / na;
+      const int w0 = (int)((long long)warp * n / na);
+      x0 = c0 + w0;
+      n_pos = (int)((long long)(warp + 1) * n / na) - w0;
     }
   }
 
-  // a walk through the units: sequence b, group gr = KV head * RT + row tile, page p of np
+  // a walk through the units: sequence b, group gr = KV head * RT + row tile, page p of np, at
+  // position x of the warp's n_pos
   struct Walk {
-    int b, gr, p, np, first;
+    int b, gr, p, np, first, x;
   };
   auto enter = [&](Walk& w) {   // a sequence's page range
     while (pre[w.b + 1] == pre[w.b]) ++w.b;
-    w.np = pre[w.b + 1] - pre[w.b];
+    w.np = pre[w.b + 1] - pre[w.b] - lead;
     w.first = pa_first(a, slen[w.b]);
   };
-  auto advance = [&](Walk& w, bool more) {
+  auto advance = [&](Walk& w) {   // to the next page of the range, if there is one
+    ++w.x;
     if (++w.p < w.np) return;
+    w.x += lead;
     w.p = 0;
     if (++w.gr < U) return;
     w.gr = 0;
     ++w.b;
-    if (more) enter(w);
+    if (w.x < n_pos) enter(w);
   };
-  Walk cw = {0, 0, 0, 0, 0};
-  if (x0 < x1) {
-    const int pg = (int)(x0 / U);
-    int lo = 0, hi = a.B - 1;   // the last sequence with pre[b] <= pg
+  Walk cw = {0, 0, 0, 0, 0, 0};
+  if (n_pos) {
+    const int at = (int)(x0 / U);
+    int lo = 0, hi = a.B - 1;   // the last sequence with pre[b] <= at
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= pg) lo = mid;
+      if (pre[mid] <= at) lo = mid;
       else hi = mid - 1;
     }
     cw.b = lo;
     enter(cw);
     const long long rem = x0 - (long long)pre[cw.b] * U;
-    cw.gr = (int)(rem / cw.np);
-    cw.p = (int)(rem - (long long)cw.gr * cw.np);
+    cw.gr = (int)(rem / (cw.np + lead));
+    cw.p = (int)(rem - (long long)cw.gr * (cw.np + lead)) - lead;
+    if (cw.p < 0) cw.x = -cw.p, cw.p = 0;
   }
   Walk pw = cw;             // the copies run PA_STAGES units ahead of the computation, the
-  long long px = x0;        // page numbers one further
-  int next_id = x0 < x1 ? a.table[pw.b * a.table_stride + pw.first + pw.p] : 0;
+                            // page numbers one further
+  int next_id = pw.x < n_pos ? a.table[pw.b * a.table_stride + pw.first + pw.p] : 0;
   uint32_t valid = 0;       // bit s: stage s holds a page
   const unsigned long long pol = evict_first_policy();
   auto issue = [&](int s) {
@@ -265,14 +299,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
       }
     }
-    ++px;
-    advance(pw, px < x1);
-    if (px < x1) next_id = a.table[pw.b * a.table_stride + pw.first + pw.p];
+    advance(pw);
+    if (pw.x < n_pos) next_id = a.table[pw.b * a.table_stride + pw.first + pw.p];
   };
-  __syncwarp();
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < PA_STAGES; ++s)
-    if (px < x1) issue(s);
+    if (pw.x < n_pos) issue(s);
 
   // ---- state of the group at hand ----
   uint32_t qb[NT][G][2][2];   // B fragments of q: group, low and high nibbles
@@ -280,8 +312,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   float cs[NT][2];            // score factor of this lane's two columns
   int c_lo[NT][2], c_hi[NT][2];   // tokens its columns see
   int t_lo = 0, t_hi = 0, t_all = 0, t_end = 0;   // seen by every row: [t_lo, t_hi); by any: [t_all, t_end)
-  float m[NT][2], l[NT][2], acc[NT][MT][4], off[NT][4];
-  uint32_t smax = 0;          // largest value scale of the group so far when 2 or more (binary16 bits)
+  // softmax reference (base 2) and weight sum; sums over the codes: rows gid the low nibble's
+  // channel, rows gid + 8 the byte's (16 times the high nibble's plus the low one's)
+  float ref[NT][2], l[NT][2], acc[NT][MT][4], off[NT][4];
+  float top = PA_TOP;         // weights stay below 2^top
   bool started = false, failed = false;
 
   auto load_group = [&](const Walk& w) {
@@ -345,7 +379,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         const int c = ct * 8 + (PACK ? (2 * tig + j) & 3 : 2 * tig + j);
         const int ci = (r0 + min(c, rn - 1)) / a.n_rep;
         c_lo[ct][j] = lo_of(ci), c_hi[ct][j] = hi_of(ci);
-        m[ct][j] = -INFINITY, l[ct][j] = 0.f;
+        ref[ct][j] = -3.402823466e38f, l[ct][j] = 0.f;
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -354,10 +388,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll
       for (int j = 0; j < 4; ++j) off[ct][j] = 0.f;
     }
-    smax = 0;
+    top = PA_TOP;
   };
 
   const int pr_k = tig % (G / 2);
+  const bool lo_col = gid >= 4;
   // byte of this lane's value pieces of tokens 2tig and 2tig + 1
   const int vrow0 = (HD == 128 ? (2 * tig + (tig & 1)) : (2 * tig + (tig >> 1))) * L::ROW;
   const int vrow1 = (HD == 128 ? (2 * tig + 1 - (tig & 1)) : (2 * tig + 1 - (tig >> 1))) * L::ROW;
@@ -380,8 +415,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     }
-    // value scales of 2 or more (exponent field above 15) lower the weights' power of two
-    const float k_old = (float)(PA_K - max(0, (int)(smax >> 10) - 15));
+    // value scales of 2 or more (exponent field above 15) lower the weights' limit
     {
       uint32_t w[G];
       lds(w, pg + L::VS + lane * 4 * G);
@@ -392,156 +426,177 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < G; ++i) mx = max(mx, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        smax = max(smax, __reduce_max_sync(0xffffffffu, mx));
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        top = fminf(top, PA_TOP - (float)((int)(mx >> 10) - 15));
       }
     }
-    const float k_new = (float)(PA_K - max(0, (int)(smax >> 10) - 15));
 
-    // ---- scores (base 2) ----
-    float S[NT][4][4];
+#pragma unroll 1
+    for (int i0 = 0; i0 < 4; i0 += PA_STEP) {
+      // ---- scores (base 2) ----
+      float S[NT][PA_STEP][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ta = 16 * i + gid, tb = ta + 8;
-      uint32_t wa[G], wb[G], sa[G / 2], sb[G / 2];
-      lds(wa, pg + ta * L::ROW + tig * 4 * G);
-      lds(wb, pg + tb * L::ROW + tig * 4 * G);
-      lds(sa, pg + L::KS + ta * 2 * G);
-      lds(sb, pg + L::KS + tb * 2 * G);
-      const uint32_t oa = *reinterpret_cast<const uint32_t*>(pg + L::KO + ta * 2 * G + 4 * pr_k);
-      const uint32_t ob = *reinterpret_cast<const uint32_t*>(pg + L::KO + tb * 2 * G + 4 * pr_k);
-      float2 ra[NT], rb[NT];
+      for (int ii = 0; ii < PA_STEP; ++ii) {
+        const int ta = 16 * (i0 + ii) + gid, tb = ta + 8;
+        uint32_t wa[G], wb[G], sa[G / 2], sb[G / 2];
+        lds(wa, pg + ta * L::ROW + tig * 4 * G);
+        lds(wb, pg + tb * L::ROW + tig * 4 * G);
+        lds(sa, pg + L::KS + ta * 2 * G);
+        lds(sb, pg + L::KS + tb * 2 * G);
+        const uint32_t oa = *reinterpret_cast<const uint32_t*>(pg + L::KO + ta * 2 * G + 4 * pr_k);
+        const uint32_t ob = *reinterpret_cast<const uint32_t*>(pg + L::KO + tb * 2 * G + 4 * pr_k);
+        float r[NT][4];
 #pragma unroll
-      for (int ct = 0; ct < NT; ++ct) ra[ct] = rb[ct] = make_float2(0.f, 0.f);
+        for (int g = 0; g < G; ++g) {
+          const uint32_t xa = wa[g] >> 8, xb = wb[g] >> 8;
+          const float2 s2a = __half22float2(u32_as_h2(sa[g >> 1])), s2b = __half22float2(u32_as_h2(sb[g >> 1]));
+          const float fa = (g & 1) ? s2a.y : s2a.x, fb = (g & 1) ? s2b.y : s2b.x;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint32_t xa = wa[g] >> 8, xb = wb[g] >> 8;
-        const float2 s2a = __half22float2(u32_as_h2(sa[g >> 1])), s2b = __half22float2(u32_as_h2(sb[g >> 1]));
-        const float fa = (g & 1) ? s2a.y : s2a.x, fb = (g & 1) ? s2b.y : s2b.x;
+          for (int ct = 0; ct < NT; ++ct) {
+            float X[4];
+            mma_z(X, wa[g] & LO, wb[g] & LO, xa & LO, xb & LO, qb[ct][g][0][0], qb[ct][g][0][1]);
+            mma(X, wa[g] & HI, wb[g] & HI, xa & HI, xb & HI, qb[ct][g][1][0], qb[ct][g][1][1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float f = j < 2 ? fa : fb;
+              r[ct][j] = g == 0 ? X[j] * f : fmaf(X[j], f, r[ct][j]);
+            }
+          }
+        }
 #pragma unroll
         for (int ct = 0; ct < NT; ++ct) {
-          float X[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(X, wa[g] & LO, wb[g] & LO, xa & LO, xb & LO, qb[ct][g][0][0], qb[ct][g][0][1]);
-          mma(X, wa[g] & HI, wb[g] & HI, xa & HI, xb & HI, qb[ct][g][1][0], qb[ct][g][1][1]);
-          ra[ct] = fma2(make_float2(X[0], X[1]), make_float2(fa, fa), ra[ct]);
-          rb[ct] = fma2(make_float2(X[2], X[3]), make_float2(fb, fb), rb[ct]);
-        }
-      }
+          float O[4];
+          mma_z(O, oa, ob, 0u, 0u, qo[ct], 0u);
 #pragma unroll
-      for (int ct = 0; ct < NT; ++ct) {
-        float O[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(O, oa, ob, 0u, 0u, qo[ct], 0u);
-        const float2 c = make_float2(cs[ct][0], cs[ct][1]);
-        const float2 ua = mul2(fma2(ra[ct], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[0], O[1])), c);
-        const float2 ub = mul2(fma2(rb[ct], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[2], O[3])), c);
-        S[ct][i][0] = ua.x, S[ct][i][1] = ua.y, S[ct][i][2] = ub.x, S[ct][i][3] = ub.y;
-        if (edge) {
+          for (int j = 0; j < 4; ++j) S[ct][ii][j] = fmaf(r[ct][j], NIB_ROW_SCALE_LO, O[j]) * cs[ct][j & 1];
+          if (edge) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = tok0 + (j < 2 ? ta : tb);
-            if (t < c_lo[ct][j & 1] || t >= c_hi[ct][j & 1]) S[ct][i][j] = -INFINITY;
+            for (int j = 0; j < 4; ++j) {
+              const int t = tok0 + (j < 2 ? ta : tb);
+              if (t < c_lo[ct][j & 1] || t >= c_hi[ct][j & 1]) S[ct][ii][j] = -INFINITY;
+            }
           }
         }
       }
-    }
 
-    // ---- softmax weights p 2^k ----
-#pragma unroll
-    for (int ct = 0; ct < NT; ++ct) {
-      float al[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float bm = fmaxf(S[ct][0][j], S[ct][0][j + 2]);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) bm = fmaxf(bm, fmaxf(S[ct][i][j], S[ct][i][j + 2]));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-        const float mn = fmaxf(m[ct][j], bm), ref = mn == -INFINITY ? 0.f : mn;
-        al[j] = exp2_approx(m[ct][j] - ref + (k_new - k_old));
-        m[ct][j] = mn;
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          S[ct][i][j] = exp2_approx(S[ct][i][j] - ref + k_new);
-          S[ct][i][j + 2] = exp2_approx(S[ct][i][j + 2] - ref + k_new);
-          t += S[ct][i][j] + S[ct][i][j + 2];
-        }
-        l[ct][j] = fmaf(l[ct][j], al[j], t);
-      }
-      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          acc[ct][mt][0] *= al[0], acc[ct][mt][1] *= al[1];
-          acc[ct][mt][2] *= al[0], acc[ct][mt][3] *= al[1];
-        }
-        off[ct][0] *= al[0], off[ct][1] *= al[1];
-      }
-    }
-
-    // ---- values ----
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // B fragments of the weights (k = tokens 16i + 2tig, +1 and 8 more), hi and lo halves
-      uint32_t ph[NT][2], pl[NT][2];
+      // ---- softmax weights 2^(S - ref): the reference moves only when one would pass 2^top ----
+      float mx[NT][2];
+      bool over = false;
 #pragma unroll
       for (int ct = 0; ct < NT; ++ct)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2 p = make_float2(S[ct][i][2 * h], S[ct][i][2 * h + 1]);
-          const __half2 hi = __floats2half2_rn(p.x, p.y);
-          const float2 r = sub2(p, __half22float2(hi));
-          ph[ct][h] = movmatrix_t(h2_as_u32(hi));
-          pl[ct][h] = movmatrix_t(h2_as_u32(__floats2half2_rn(r.x, r.y)));
+        for (int j = 0; j < 2; ++j) {
+          float t = fmaxf(S[ct][0][j], S[ct][0][j + 2]);
+#pragma unroll
+          for (int ii = 1; ii < PA_STEP; ++ii) t = fmaxf(t, fmaxf(S[ct][ii][j], S[ct][ii][j + 2]));
+          mx[ct][j] = t;
+          over = over || t > ref[ct][j] + top;
         }
-      // offsets: rows = groups
-      {
-        uint32_t o[2] = {0u, 0u};
-        if (gid < G) lds(o, pg + L::VO + gid * 2 * PG + tig * 32 + i * 8);
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int ct = 0; ct < NT; ++ct) {
-          if (PACK) {
-            mma(off[ct], o[0], 0u, o[1], 0u, gid >= 4 ? pl[ct][0] : ph[ct][0], gid >= 4 ? pl[ct][1] : ph[ct][1]);
-          } else {
+          float al[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float t = mx[ct][j];
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            const float now = t > ref[ct][j] + top ? t - (top - PA_SLACK) : ref[ct][j];
+            al[j] = exp2_approx(ref[ct][j] - now);
+            ref[ct][j] = now;
+            l[ct][j] *= al[j];
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            acc[ct][mt][0] *= al[0], acc[ct][mt][1] *= al[1];
+            acc[ct][mt][2] *= al[0], acc[ct][mt][3] *= al[1];
+          }
+          off[ct][0] *= al[0], off[ct][1] *= al[1];
+        }
+      }
+
+      // ---- values ----
+#pragma unroll
+      for (int ii = 0; ii < PA_STEP; ++ii) {
+        const int i = i0 + ii;
+        // B fragments of the weights (k = tokens 16i + 2tig, +1 and 8 more), hi and lo halves
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 p = make_float2(exp2_approx(S[ct][ii][2 * h] - ref[ct][0]), exp2_approx(S[ct][ii][2 * h + 1] - ref[ct][1]));
+            l[ct][0] += p.x, l[ct][1] += p.y;
+            const __half2 hi = __floats2half2_rn(p.x, p.y);
+            const float2 hf = __half22float2(hi);
+            ph[ct][h] = movmatrix_t(h2_as_u32(hi));
+            pl[ct][h] = movmatrix_t(h2_as_u32(__floats2half2_rn(p.x - hf.x, p.y - hf.y)));
+          }
+        // codes of token pairs: word g of x[h] holds four channels of group g of two tokens
+        uint32_t x[2][G];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t t0[G / 2], t1[G / 2];
+          lds(t0, pg + L::VC + (16 * i + 8 * h) * L::ROW + vrow0 + vx);
+          lds(t1, pg + L::VC + (16 * i + 8 * h) * L::ROW + vrow1 + vx);
+#pragma unroll
+          for (int g = 0; g < G; ++g) x[h][g] = __byte_perm(t0[g >> 1], t1[g >> 1], (g & 1) ? 0x7632 : 0x5410);
+        }
+        uint32_t o[2] = {0u, 0u};   // offsets: rows = groups
+        if (gid < G) lds(o, pg + L::VO + gid * 2 * PG + tig * 32 + i * 8);
+        if (PACK) {
+          // columns 4..7 take the lo halves: there the product p_hi s is formed twice and
+          // only its remainder kept
+          uint32_t pz[2], pw[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            pw[h] = lo_col ? pl[0][h] : 0u;
+            pz[h] = lo_col ? ph[0][h] : 0u;
+          }
+          mma(off[0], o[0], 0u, o[1], 0u, lo_col ? pw[0] : ph[0][0], lo_col ? pw[1] : ph[0][1]);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            uint32_t s[2], b[2];
+            lds(s, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const __half2 sv = u32_as_h2(s[h]);
+              const __half2 t = __hmul2_rn(u32_as_h2(pz[h]), sv);
+              b[h] = h2_as_u32(__hfma2(u32_as_h2(pw[h]), sv, __hfma2(u32_as_h2(ph[0][h]), sv, __hneg2(t))));
+            }
+            const uint32_t y0 = __byte_perm(x[0][g], 0u, 0x4341), y1 = __byte_perm(x[1][g], 0u, 0x4341);
+            mma(acc[0][2 * g], x[0][g] & LO, x[0][g] & BYTE, x[1][g] & LO, x[1][g] & BYTE, b[0], b[1]);
+            mma(acc[0][2 * g + 1], y0 & LO, y0, y1 & LO, y1, b[0], b[1]);
+          }
+        } else {
+#pragma unroll
+          for (int ct = 0; ct < NT; ++ct) {
             mma(off[ct], o[0], 0u, o[1], 0u, ph[ct][0], ph[ct][1]);
             mma(off[ct], o[0], 0u, o[1], 0u, pl[ct][0], pl[ct][1]);
           }
-        }
-      }
-      // codes of token pairs: word g of x[h] holds four channels of group g of two tokens
-      uint32_t x[2][G];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t t0[G / 2], t1[G / 2];
-        lds(t0, pg + L::VC + (16 * i + 8 * h) * L::ROW + vrow0 + vx);
-        lds(t1, pg + L::VC + (16 * i + 8 * h) * L::ROW + vrow1 + vx);
+          for (int g = 0; g < G; ++g) {
+            uint32_t s[2];
+            lds(s, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
+            const uint32_t y0 = __byte_perm(x[0][g], 0u, 0x4341), y1 = __byte_perm(x[1][g], 0u, 0x4341);
+            const uint32_t x0l = x[0][g] & LO, x0b = x[0][g] & BYTE, x1l = x[1][g] & LO, x1b = x[1][g] & BYTE;
+            const uint32_t y0l = y0 & LO, y1l = y1 & LO;
 #pragma unroll
-        for (int g = 0; g < G; ++g) x[h][g] = __byte_perm(t0[g >> 1], t1[g >> 1], (g & 1) ? 0x7632 : 0x5410);
-      }
+            for (int ct = 0; ct < NT; ++ct) {
+              uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        uint32_t s[2];
-        lds(s, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
-        const uint32_t y0 = x[0][g] >> 8, y1 = x[1][g] >> 8;
-#pragma unroll
-        for (int ct = 0; ct < NT; ++ct) {
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __half2 sv = u32_as_h2(s[h]), p = u32_as_h2(ph[ct][h]);
-            const __half2 w = __hmul2_rn(p, sv);
-            const __half2 r = __hfma2(p, sv, __hneg2(w));   // exact remainder
-            hi[h] = h2_as_u32(w);
-            lo[h] = h2_as_u32(__hfma2(u32_as_h2(pl[ct][h]), sv, r));
-          }
-          if (PACK) {
-            const uint32_t b0 = gid >= 4 ? lo[0] : hi[0], b1 = gid >= 4 ? lo[1] : hi[1];
-            mma(acc[ct][2 * g], x[0][g] & LO, x[0][g] & HI, x[1][g] & LO, x[1][g] & HI, b0, b1);
-            mma(acc[ct][2 * g + 1], y0 & LO, y0 & HI, y1 & LO, y1 & HI, b0, b1);
-          } else {
-            mma(acc[ct][2 * g], x[0][g] & LO, x[0][g] & HI, x[1][g] & LO, x[1][g] & HI, hi[0], hi[1]);
-            mma(acc[ct][2 * g + 1], y0 & LO, y0 & HI, y1 & LO, y1 & HI, hi[0], hi[1]);
-            mma(acc[ct][2 * g], x[0][g] & LO, x[0][g] & HI, x[1][g] & LO, x[1][g] & HI, lo[0], lo[1]);
-            mma(acc[ct][2 * g + 1], y0 & LO, y0 & HI, y1 & LO, y1 & HI, lo[0], lo[1]);
+              for (int h = 0; h < 2; ++h) {
+                const __half2 sv = u32_as_h2(s[h]), p = u32_as_h2(ph[ct][h]);
+                const __half2 w = __hmul2_rn(p, sv);
+                hi[h] = h2_as_u32(w);
+                lo[h] = h2_as_u32(__hfma2(u32_as_h2(pl[ct][h]), sv, __hfma2(p, sv, __hneg2(w))));   // the remainder is exact
+              }
+              mma(acc[ct][2 * g], x0l, x0b, x1l, x1b, hi[0], hi[1]);
+              mma(acc[ct][2 * g + 1], y0l, y0, y1l, y1, hi[0], hi[1]);
+              mma(acc[ct][2 * g], x0l, x0b, x1l, x1b, lo[0], lo[1]);
+              mma(acc[ct][2 * g + 1], y0l, y0, y1l, y1, lo[0], lo[1]);
+            }
           }
         }
       }
@@ -552,7 +607,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   // weight sum into dst: [R][HD] floats, then [R][2].
   auto emit = [&](const Walk& w, float* dst) {
     const int g = w.gr / a.RT, r0 = (w.gr - g * a.RT) * R, rn = min(R, a.rows - r0);
-    const float k = (float)(PA_K - max(0, (int)(smax >> 10) - 15));
 #pragma unroll
     for (int ct = 0; ct < NT; ++ct)
 #pragma unroll
@@ -562,7 +616,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         lt += __shfl_xor_sync(0xffffffffu, lt, 8);
         lt += __shfl_xor_sync(0xffffffffu, lt, 16);
         if (failed) lt = __int_as_float(0x7fc00000);
-        const float ref = m[ct][j] == -INFINITY ? -INFINITY : m[ct][j] - k;
+        const float rf = lt == 0.f ? -INFINITY : ref[ct][j];
         const int c = ct * 8 + 2 * tig + j;
         const bool live = c < rn;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
@@ -571,9 +625,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           const float o = __shfl_sync(0xffffffffu, off[ct][j], 4 * gg + tig);
-          float4 v = make_float4(fmaf(acc[ct][2 * gg][j], NIB_ROW_SCALE_LO, o), fmaf(acc[ct][2 * gg][j + 2], NIB_ROW_SCALE_HI, o),
-                                 fmaf(acc[ct][2 * gg + 1][j], NIB_ROW_SCALE_LO, o),
-                                 fmaf(acc[ct][2 * gg + 1][j + 2], NIB_ROW_SCALE_HI, o));
+          const float e0 = acc[ct][2 * gg][j], e1 = acc[ct][2 * gg][j + 2], e2 = acc[ct][2 * gg + 1][j], e3 = acc[ct][2 * gg + 1][j + 2];
+          float4 v = make_float4(fmaf(e0, NIB_ROW_SCALE_LO, o), fmaf(e1 - e0, NIB_ROW_SCALE_HI, o),
+                                 fmaf(e2, NIB_ROW_SCALE_LO, o), fmaf(e3 - e2, NIB_ROW_SCALE_HI, o));
           if (PACK) {   // columns 4..7 hold the lo halves' sums
             v.x += __shfl_xor_sync(0xffffffffu, v.x, 2);
             v.y += __shfl_xor_sync(0xffffffffu, v.y, 2);
@@ -589,15 +643,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
           }
         }
         if (gid == 0 && !(PACK && tig >= 2)) {
-          if (dst) *reinterpret_cast<float2*>(dst + R * HD + 2 * c) = make_float2(ref, lt);
-          else if (live && a.lse) a.lse[orow] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+          if (dst) *reinterpret_cast<float2*>(dst + R * HD + 2 * c) = make_float2(rf, lt);
+          else if (live && a.lse) a.lse[orow] = lt == 0.f ? -INFINITY : (rf + log2f(lt)) * 0.69314718055994531f;
         }
       }
   };
 
   bool open = false;
   int it = 0;
-  for (long long x = x0; x < x1; ++x, ++it) {
+  while (cw.x < n_pos) {
     if (!open) {
       load_group(cw);
       open = true;
@@ -608,107 +662,148 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     failed = __any_sync(0xffffffffu, failed);
     if (!failed && ((valid >> s) & 1u)) page(ring + s * L::BYTES, (cw.first + cw.p) * PG);
     __syncwarp();
-    if (!failed && px < x1) issue(s);
-    if (cw.p + 1 == cw.np) {
-      emit(cw, started ? nullptr : a.part + ((size_t)gw * 2) * PART);
+    if (!failed && pw.x < n_pos) issue(s);
+    ++it;
+    const Walk at = cw;
+    advance(cw);
+    const bool end = at.p + 1 == at.np;
+    if (end || cw.x >= n_pos) {
+      emit(at, end && started ? nullptr : a.part + ((size_t)gw * 2 + !end) * PART);
+      if (lane == 0) {
+        if (end) {
+          if (!started) ended[warp] = make_int2(at.b, at.gr);
+        } else {
+          open_at[warp] = make_int2(at.b, at.gr);
+          open_new[warp] = started;
+        }
+      }
       open = false;
     }
-    if (x + 1 < x1) advance(cw, true);
   }
   if (failed)   // the copies still in flight write into this CTA's memory: wait for them, within limits
     for (int k = 0; k < PA_STAGES && it - 1 - k >= 0; ++k) pa_wait(bar_s + 8 * ((it - 1 - k) % PA_STAGES), (uint32_t)((it - 1 - k) / PA_STAGES) & 1u);
-  // an open group's piece goes to this warp's ring, which no copy uses any more
-  if (open) emit(cw, reinterpret_cast<float*>(ring));
-  if (lane == 0) {
-    open_key[warp] = open ? (long long)cw.b * U + cw.gr : -1;
-    PaRec r = {cw.b, cw.gr, 0, open && started};
-    if (r.started) r.last_warp = sp.warp_of((long long)pre[cw.b] * U + (long long)(cw.gr + 1) * cw.np - 1);
-    a.recs[gw] = r;
-  }
   __syncthreads();
-  // the first warp of each run of warps with the same open group: one piece per run
-  for (int w0 = 0; w0 < PA_WARPS; ++w0) {
-    if (open_key[w0] < 0 || (w0 > 0 && open_key[w0 - 1] == open_key[w0])) continue;
-    int w1 = w0 + 1;
-    while (w1 < PA_WARPS && open_key[w1] == open_key[w0]) ++w1;
-    float* dst = a.part + ((size_t)(blockIdx.x * PA_WARPS + w0) * 2 + 1) * PART;
-    for (int e = threadIdx.x; e < R * HD / 4; e += PA_THREADS) {
-      const int c = e / (HD / 4);
-      auto piece = [&](int w) { return reinterpret_cast<const float*>(sm + w * PA_STAGES * L::BYTES); };
-      float M = -INFINITY, Ls = 0.f;
-      for (int w = w0; w < w1; ++w) M = fmaxf(M, piece(w)[R * HD + 2 * c]);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = w0; w < w1; ++w) {
-        const float mw = piece(w)[R * HD + 2 * c], f = mw == -INFINITY ? 0.f : exp2_approx(mw - M);
-        const float4 v = reinterpret_cast<const float4*>(piece(w))[e];
-        Ls = fmaf(piece(w)[R * HD + 2 * c + 1], f, Ls);
-        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-      }
-      reinterpret_cast<float4*>(dst)[e] = o;
-      if (e % (HD / 4) == 0) *reinterpret_cast<float2*>(dst + R * HD + 2 * c) = make_float2(M, Ls);
-    }
-  }
-}
 
-// Adds up the pieces of the groups that were cut: CTA c takes the groups that started in
-// CTA c of the first kernel and were still open at the end of one of its warps.  Pieces in
-// order: the run of warps that started it, one per following CTA, and the ending warp's.
-constexpr int PC_THREADS = 512;
-template <int HD, int R>
-__global__ void __launch_bounds__(PC_THREADS) paged_combine_kernel(PaArgs a) {
-  constexpr int PART = R * (HD + 2), VEC = R * HD / 4, KS = PC_THREADS / VEC;   // KS threads share a sum
-  static_assert(VEC * KS == PC_THREADS, "the rows of a tile fill the block");
-  __shared__ float4 red[PC_THREADS];
-  __shared__ float redl[PC_THREADS];
-  pdl_wait();
-  const int ks = threadIdx.x / VEC, e = threadIdx.x % VEC, c = e / (HD / 4);
-  for (int w = 0; w < PA_WARPS; ++w) {
-    const int gw = blockIdx.x * PA_WARPS + w;
-    const PaRec r = a.recs[gw];
-    if (!r.started) continue;
-    const int last_cta = r.last_warp / PA_WARPS, first = blockIdx.x;
-    // whole or partial CTAs after the first whose warp 0 leaves the group open
-    const int nl = last_cta - first - ((last_cta > first && r.last_warp % PA_WARPS == 0) ? 1 : 0);
-    const int n = nl + 2;
-    auto piece = [&](int k) {
-      const size_t slot = k == 0 ? (size_t)gw * 2 + 1
-                          : k <= nl ? (size_t)(first + k) * PA_WARPS * 2 + 1 : (size_t)r.last_warp * 2;
-      return a.part + slot * PART;
-    };
-    float M = -INFINITY;
-    for (int k = 0; k < n; ++k) M = fmaxf(M, piece(k)[R * HD + 2 * c]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float Ls = 0.f;
-#pragma unroll 4
-    for (int k = ks; k < n; k += KS) {
-      const float* p = piece(k);
-      const float2 ml = *reinterpret_cast<const float2*>(p + R * HD + 2 * c);
-      const float4 v = reinterpret_cast<const float4*>(p)[e];
-      const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
-      Ls = fmaf(ml.y, f, Ls);
-      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-    }
-    if (KS > 1) {
-      __syncthreads();
-      red[threadIdx.x] = o;
-      redl[threadIdx.x] = Ls;
-      __syncthreads();
-      if (ks == 0)
-        for (int k = 1; k < KS; ++k) {
-          const float4 v = red[k * VEC + e];
-          o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-          Ls += redl[k * VEC + e];
+  // ---- groups that were cut ----
+  // The sum of n pieces in order, for float4 e of the tile's rows; KS threads share a sum.
+  constexpr int VEC = R * HD / 4, KS = PA_THREADS / VEC > 1 ? PA_THREADS / VEC : 1;
+  auto merge = [&](int n, auto piece, auto store) {
+    for (int e0 = 0; e0 < VEC; e0 += PA_THREADS) {
+      const int e = (e0 + threadIdx.x) % VEC, ks = threadIdx.x / VEC, c = e / (HD / 4);
+      float M = -INFINITY, Ls = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](float2 ml, float4 v) {
+        const float to = fmaxf(M, ml.x), f = M == to ? 1.f : exp2_approx(M - to);
+        const float g = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - to);
+        M = to;
+        Ls = fmaf(Ls, f, ml.y * g);
+        o.x = fmaf(o.x, f, v.x * g), o.y = fmaf(o.y, f, v.y * g), o.z = fmaf(o.z, f, v.z * g), o.w = fmaf(o.w, f, v.w * g);
+      };
+      if (KS == 1 || ks < KS)
+        for (int k0 = ks; k0 < n; k0 += 4 * KS) {
+          float2 ml[4];
+          float4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k0 + k * KS < n) {
+              const float* src = piece(k0 + k * KS);
+              v[k] = __ldcg(reinterpret_cast<const float4*>(src) + e);
+              ml[k] = __ldcg(reinterpret_cast<const float2*>(src + R * HD) + c);
+            }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k0 + k * KS < n) add(ml[k], v[k]);
         }
+      if (KS > 1) {
+        red[threadIdx.x] = o;
+        redm[threadIdx.x] = make_float2(M, Ls);
+        __syncthreads();
+        if (ks == 0)
+          for (int k = 1; k < KS; ++k) add(redm[k * VEC + e], red[k * VEC + e]);
+        __syncthreads();
+      }
+      if (ks == 0) store(e, c, o, M, Ls);
     }
-    const int g = r.gr / a.RT, rr = (r.gr - g * a.RT) * R + c;
-    if (ks == 0 && rr < a.rows) {
+  };
+  auto store_piece = [&](float* dst) {
+    return [=](int e, int c, float4 o, float M, float Ls) {
+      reinterpret_cast<float4*>(dst)[e] = o;
+      if (e % (HD / 4) == 0) reinterpret_cast<float2*>(dst + R * HD)[c] = make_float2(M, Ls);
+    };
+  };
+  auto store_rows = [&](int2 grp) {
+    const int g = grp.y / a.RT, r0 = (grp.y - g * a.RT) * R;
+    return [=, &a](int e, int c, float4 o, float M, float Ls) {
+      const int rr = r0 + c;
+      if (rr >= a.rows) return;
       const int qi = rr / a.n_rep;
-      const size_t orow = ((size_t)r.b * a.Q + qi) * a.Hq + g * a.n_rep + (rr - qi * a.n_rep);
+      const size_t orow = ((size_t)grp.x * a.Q + qi) * a.Hq + g * a.n_rep + (rr - qi * a.n_rep);
       const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
       reinterpret_cast<uint2*>(a.out)[orow * (HD / 4) + e % (HD / 4)] =
           make_uint2(f2_to_pair(o.x * inv, o.y * inv, a.bf16), f2_to_pair(o.z * inv, o.w * inv, a.bf16));
       if (a.lse && e % (HD / 4) == 0) a.lse[orow] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
+    };
+  };
+  float* wpart = a.part + (size_t)blockIdx.x * PA_WARPS * 2 * PART;
+  float* cpart = a.part + (size_t)a.grid * PA_WARPS * 2 * PART;
+  // runs of pieces of one group within this CTA: that of a group begun in an earlier CTA (w =
+  // -1), then those of the groups that each warp starts and leaves open
+  int2 away[2] = {make_int2(-1, 0), make_int2(-1, 0)};   // groups with pieces in other CTAs
+  for (int w = -1; w < PA_WARPS; ++w) {
+    int2 grp;
+    bool closed = false;
+    int first = w, n = 0, last = w;   // pieces: the open ones of warps first..last - 1 or last, then an ending one
+    if (w < 0) {
+      first = 0;
+      grp = ended[0].x >= 0 ? ended[0] : (open_at[0].x >= 0 && !open_new[0]) ? open_at[0] : make_int2(-1, 0);
+      if (grp.x < 0) continue;
+      closed = ended[0].x >= 0;
+      n = 1, last = 0;
+    } else {
+      grp = open_at[w];
+      if (grp.x < 0 || !open_new[w]) continue;
+      n = 1;
     }
+    while (!closed && last + 1 < PA_WARPS) {
+      const int2 en = ended[last + 1], op = open_at[last + 1];
+      if (en.x == grp.x && en.y == grp.y) closed = true;
+      else if (!(op.x == grp.x && op.y == grp.y)) break;
+      ++n, ++last;
+    }
+    auto piece = [&](int k) { return wpart + ((first + k) * 2 + !(closed && k == n - 1)) * PART; };
+    if (closed && w >= 0) {
+      merge(n, piece, store_rows(grp));
+    } else {
+      const int slot = w >= 0;
+      away[slot] = grp;
+      merge(n, piece, store_piece(cpart + ((size_t)blockIdx.x * 2 + slot) * PART));
+    }
+  }
+  if (away[0].x < 0 && away[1].x < 0) return;
+  __syncthreads();
+  int first_cta[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (away[k].x < 0) continue;
+    const long long size = pre[away[k].x + 1] - pre[away[k].x];
+    const long long at = (long long)pre[away[k].x] * U + away[k].y * size;
+    // the CTAs that hold its first page and its last one
+    first_cta[k] = k ? (int)blockIdx.x : sp.cta_of(at + lead);
+    if (threadIdx.x == 32 * k) {
+      const int n = sp.cta_of(at + size - 1) - first_cta[k] + 1;
+      __threadfence();
+      const int before = atomicAdd(&a.arrived[first_cta[k]], 1);
+      final_n[k] = before == n - 1 ? n : 0;
+      if (before == n - 1) a.arrived[first_cta[k]] = 0;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (away[k].x < 0 || final_n[k] == 0) continue;
+    const int c0 = first_cta[k];
+    merge(final_n[k], [&](int i) { return cpart + ((size_t)(c0 + i) * 2 + (i == 0)) * PART; }, store_rows(away[k]));
   }
 }
 
@@ -729,21 +824,19 @@ cudaError_t sm_count(int* sms) {
   return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
-// partials (two per warp), then the records
-size_t part_bytes(int sms, int R, int hd) { return (size_t)sms * PA_WARPS * 2 * R * (hd + 2) * sizeof(float); }
+// arrival counters, then pieces: two per warp and two per CTA
+constexpr size_t PA_COUNTERS = 4096;
 size_t ws_bytes(int sms, int Q, int Hq, int Hkv, int hd) {
-  return part_bytes(sms, tile_rows(Q * (Hq / Hkv)), hd) + (size_t)sms * PA_WARPS * sizeof(PaRec);
+  return PA_COUNTERS + (size_t)sms * (PA_WARPS + 1) * 2 * tile_rows(Q * (Hq / Hkv)) * (hd + 2) * sizeof(float);
 }
 
 template <int HD, int NT, bool PACK>
 cudaError_t launch(const PaArgs& a, cudaStream_t st) {
-  constexpr int R = PACK ? 4 : 8 * NT;
   const size_t smem = (size_t)PA_WARPS * PA_STAGES * Page<HD>::BYTES + (2 * (size_t)a.B + 1) * sizeof(int);
   auto* k = paged_attention_kernel<HD, NT, PACK>;
   if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
   k<<<a.grid, PA_THREADS, smem, st>>>(a);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  return launch_dependent(paged_combine_kernel<HD, R>, dim3(a.grid), dim3(PC_THREADS), 0, st, a);
+  return cudaGetLastError();
 }
 
 kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, const void* pages, int n_pages,
@@ -754,8 +847,8 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   if (dtype != KVQ_F16 && dtype != KVQ_BF16) return paged_fail(KVQ_ERR_INVALID, fn, "dtype must be KVQ_F16 or KVQ_BF16");
   if (const char* msg = shape_error(B, Q, Hq, Hkv, hd)) return paged_fail(KVQ_ERR_INVALID, fn, msg);
   if (n_pages < 1 || n_pages > (1 << 25)) return paged_fail(KVQ_ERR_INVALID, fn, "n_pages must be in 1..33554432");
-  if (max_pages < 1 || max_pages > (1 << 24) || (long long)B * max_pages >= (1ll << 31))
-    return paged_fail(KVQ_ERR_INVALID, fn, "max_pages must be in 1..16777216 and batch * max_pages below 2^31");
+  if (max_pages < 1 || max_pages > (1 << 24) || (long long)B * max_pages >= (1ll << 30))
+    return paged_fail(KVQ_ERR_INVALID, fn, "max_pages must be in 1..16777216 and batch * max_pages below 2^30");
   if (table_stride < 0) return paged_fail(KVQ_ERR_INVALID, fn, "table_stride must be >= 0");
   if (window < 0) return paged_fail(KVQ_ERR_INVALID, fn, "window must be >= 0");
   if (!std::isfinite(scale)) return paged_fail(KVQ_ERR_INVALID, fn, "scale must be finite");
@@ -783,10 +876,10 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   a.bf16 = dtype == KVQ_BF16;
   const int R = tile_rows(a.rows);
   a.RT = (a.rows + R - 1) / R;
-  // one CTA per SM, fewer when the table cannot hold that many units
-  a.grid = (int)std::min<long long>(sms, (long long)B * max_pages * Hkv * a.RT);
-  a.part = static_cast<float*>(workspace);
-  a.recs = reinterpret_cast<PaRec*>(static_cast<char*>(workspace) + part_bytes(sms, R, hd));
+  // one CTA per SM (the counters hold 1024), fewer when the table cannot hold that many units
+  a.grid = (int)std::min<long long>(std::min(sms, 1024), (long long)B * max_pages * Hkv * a.RT);
+  a.arrived = static_cast<int*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + PA_COUNTERS);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (hd == 128) e = R == 4 ? launch<128, 1, true>(a, st) : R == 8 ? launch<128, 1, false>(a, st) : launch<128, 2, false>(a, st);

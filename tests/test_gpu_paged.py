@@ -651,7 +651,7 @@ def test_serving_loop_against_64_bits():
     table = order[:B * 10].reshape(B, 10).astype(np.int32)
     pages = torch.zeros(40, Hkv, 10240, dtype=torch.uint8, device="cuda")
     tab = torch.from_numpy(table).cuda()
-    ws = torch.empty(kvq.paged_attention_workspace(B, 1, Hq, Hkv), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(kvq.paged_attention_workspace(B, 1, Hq, Hkv), dtype=torch.uint8, device="cuda")
     # prompts, one flat batch with padding at its end
     seq = np.concatenate([np.full(n, b) for b, n in enumerate(lens)])
     pos = np.concatenate([np.arange(n) for n in lens])
@@ -698,7 +698,7 @@ def test_captured_and_replayed_step():
     start = torch.zeros(int(table.max()) + 1, Hkv, 10240, dtype=torch.uint8, device="cuda")
     fused = torch.zeros(B, Hq + 2 * Hkv, D, dtype=torch.float16, device="cuda")
     slots, pos, lens = _ints([-1] * B), _ints([0] * B), _ints([0] * B)
-    ws = torch.empty(kvq.paged_attention_workspace(B, 1, Hq, Hkv), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(kvq.paged_attention_workspace(B, 1, Hq, Hkv), dtype=torch.uint8, device="cuda")
     pages = [start.clone(), start.clone()]
     outs = [torch.zeros(B, Hq, D, dtype=torch.float16, device="cuda") for _ in range(2)]
     _step(plan, fused.clone(), pages[0], tab, slots, pos, lens, outs[0], ws, Hq, Hkv)    # loads the kernels
