@@ -391,14 +391,9 @@ class RopePlan:
         self.head_dim = head_dim
 
 
-def _float_code(t, name) -> int:
-    import torch
-    if t.dtype == torch.float16:
-        return 0
-    if t.dtype == torch.bfloat16:
-        return 1
-    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
-
+# The calls below are made once per layer and token, where their host time counts (a decoding
+# step of a few microseconds on the device): operands are checked with as few attribute reads
+# as that takes.
 
 def _rows(t, name, dtype, shape):
     """Address and (token, head) strides of a [tokens, heads, head_dim] operand whose rows
@@ -407,63 +402,77 @@ def _rows(t, name, dtype, shape):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[2] != 1 and shape[2] != 1:
+    a, b, c = t.stride()
+    if c != 1 and shape[2] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # a dimension of one row has no stride to speak of
-    return t.data_ptr(), st[0] if shape[0] > 1 else 8, st[1] if shape[1] > 1 else 8
+    return t.data_ptr(), a if shape[0] > 1 else 8, b if shape[1] > 1 else 8
 
 
-def _ints(t, name, shape):
+def _ints(t, name, n):
     import torch
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous torch.int32 tensor of {n} elements")
     return t.data_ptr()
 
 
-def _one_device(*named):
-    """The CUDA device that all given tensors are on."""
-    dev = named[0][1].device
-    if dev.type != "cuda":
-        raise ValueError(f"{named[0][0]} must be a CUDA tensor")
-    for name, t in named[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, like {named[0][0]}")
+def _float_code(t, name) -> int:
+    import torch
+    dt = t.dtype
+    if dt == torch.float16:
+        return 0
+    if dt == torch.bfloat16:
+        return 1
+    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {dt}")
+
+
+def _device_of(names, first, *others) -> int:
+    """Index of the CUDA device that all given tensors (None: absent) are on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"{names.split()[0]} must be a CUDA tensor")
+    for k, t in enumerate(others):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{names.split()[k + 1]} must be on {first.device}, like {names.split()[0]}")
     return dev
 
 
-def _call(dev, fn, *args, stream=None):
-    """Run a library call on `dev` and `stream` (that device's current one when None)."""
+def _call(dev, stream, fn, *args):
+    """Run a library call on device `dev` and `stream` (the device's current one when None)."""
     import torch
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _check(fn(*args, _stream(stream)))
+    if stream is None:   # the address alone: building a Stream object costs 2.7 us
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, stream or None)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream or None)
+    if status != KVQ_OK:
+        _check(status)
 
 
 def rope(x, positions, plan, out=None, stream=None):
     """Rotary positions (kvq_rope): x [T, H, head_dim] fp16 or bf16 with contiguous rows (any
     token and head strides, e.g. a slice of a fused projection), positions [T] int32.
     out=None allocates the result; out=x works in place.  Returns out."""
-    import torch
     if x.dim() != 3:
         raise ValueError("x must be [n_tokens, n_heads, head_dim]")
     if out is None:
+        import torch
         if stream is not None:
             raise ValueError("out must be given with a stream")
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dev = _one_device(("x", x), ("positions", positions), ("out", out))
-    shape, code = x.shape, _float_code(x, "x")
-    if shape[2] != plan.head_dim:
-        raise ValueError(f"x must have head_dim {plan.head_dim}, got {shape[2]}")
-    _call(dev, load_library().kvq_rope, plan.address, code, *_rows(x, "x", x.dtype, shape),
-          _ints(positions, "positions", shape[:1]), shape[0], shape[1], *_rows(out, "out", x.dtype, shape),
-          stream=stream)
+    dev = _device_of("x positions out", x, positions, out)
+    code, shape, dt = _float_code(x, "x"), x.shape, x.dtype
+    T, H, hd = shape
+    if hd != plan.head_dim:
+        raise ValueError(f"x must have head_dim {plan.head_dim}, got {hd}")
+    a = _rows(x, "x", dt, shape)
+    b = a if out is x else _rows(out, "out", dt, shape)
+    _call(dev, stream, load_library().kvq_rope, plan.address, code, *a, _ints(positions, "positions", T), T, H, *b)
     return out
 
 
@@ -481,11 +490,12 @@ _PAGE_BYTES = {64: 5120, 128: 10240}
 def _pool(pages, n_kv_heads, head_dim):
     """Address and page count of a pool of pages."""
     import torch
-    if head_dim not in _PAGE_BYTES:
+    nbytes = _PAGE_BYTES.get(head_dim)
+    if nbytes is None:
         raise ValueError("head_dim must be 64 or 128")
-    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.shape[1] != n_kv_heads \
-            or pages.shape[2] != _PAGE_BYTES[head_dim] or not pages.is_contiguous():
-        raise ValueError(f"pages must be a contiguous uint8 tensor [n_pages, {n_kv_heads}, {_PAGE_BYTES[head_dim]}]")
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.shape[1:] != (n_kv_heads, nbytes) \
+            or not pages.is_contiguous():
+        raise ValueError(f"pages must be a contiguous uint8 tensor [n_pages, {n_kv_heads}, {nbytes}]")
     return pages.data_ptr(), pages.shape[0]
 
 
@@ -498,11 +508,9 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
     given, into q_out (which may be q)."""
     if k.dim() != 3:
         raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
-    dev = _one_device(("k", k), ("v", v), ("slots", slots), ("pages", pages), ("positions", positions), ("q", q),
-                      ("q_out", q_out))
-    shape, code = k.shape, _float_code(k, "k")
+    dev = _device_of("k v slots pages positions q q_out", k, v, slots, pages, positions, q, q_out)
+    code, shape, dt = _float_code(k, "k"), k.shape, k.dtype
     T, hkv, hd = shape
-    pool, n_pages = _pool(pages, hkv, hd)
     if (plan is None) != (positions is None):
         raise ValueError("plan and positions go together")
     if (q is None) != (q_out is None):
@@ -512,11 +520,12 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
         if q.dim() != 3:
             raise ValueError("q must be [n_tokens, n_q_heads, head_dim]")
         hq = q.shape[1]
-        qa, oa = _rows(q, "q", k.dtype, (T, hq, hd)), _rows(q_out, "q_out", k.dtype, (T, hq, hd))
-    _call(dev, load_library().kvq_paged_append, None if plan is None else plan.address, code,
-          *_rows(k, "k", k.dtype, shape), *_rows(v, "v", k.dtype, shape), _ints(slots, "slots", shape[:1]),
-          None if positions is None else _ints(positions, "positions", shape[:1]), T, hkv, hd, pool, n_pages,
-          *qa, hq, *oa, stream=stream)
+        qa = _rows(q, "q", dt, (T, hq, hd))
+        oa = qa if q_out is q else _rows(q_out, "q_out", dt, (T, hq, hd))
+    _call(dev, stream, load_library().kvq_paged_append, None if plan is None else plan.address, code,
+          *_rows(k, "k", dt, shape), *_rows(v, "v", dt, shape), _ints(slots, "slots", T),
+          None if positions is None else _ints(positions, "positions", T), T, hkv, hd, *_pool(pages, hkv, hd),
+          *qa, hq, *oa)
 
 
 def paged_gather(pages, slots, k, v, stream=None):
@@ -524,10 +533,11 @@ def paged_gather(pages, slots, k, v, stream=None):
     fp16 or bf16 receive what the slots hold (rows of slots outside the pool become 0)."""
     if k.dim() != 3:
         raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
-    dev = _one_device(("pages", pages), ("slots", slots), ("k", k), ("v", v))
-    shape, code = k.shape, _float_code(k, "k")
-    _call(dev, load_library().kvq_paged_gather, *_pool(pages, shape[1], shape[2]), _ints(slots, "slots", shape[:1]),
-          *shape, code, *_rows(k, "k", k.dtype, shape), *_rows(v, "v", k.dtype, shape), stream=stream)
+    dev = _device_of("pages slots k v", pages, slots, k, v)
+    code, shape, dt = _float_code(k, "k"), k.shape, k.dtype
+    T, hkv, hd = shape
+    _call(dev, stream, load_library().kvq_paged_gather, *_pool(pages, hkv, hd), _ints(slots, "slots", T), T, hkv, hd,
+          code, *_rows(k, "k", dt, shape), *_rows(v, "v", dt, shape))
 
 
 def paged_attention_workspace(batch: int, n_q_tokens: int, n_q_heads: int, n_kv_heads: int,
@@ -551,9 +561,9 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     import torch
     if q.dim() not in (3, 4):
         raise ValueError("q must be [batch, n_q_heads, head_dim] or [batch, n_q_tokens, n_q_heads, head_dim]")
-    dev = _one_device(("q", q), ("pages", pages), ("page_table", page_table), ("seq_lens", seq_lens), ("out", out),
-                      ("lse", lse), ("workspace", workspace))
-    code, shape, st = _float_code(q, "q"), q.shape, q.stride()
+    dev = _device_of("q pages page_table seq_lens out lse workspace", q, pages, page_table, seq_lens, out, lse,
+                     workspace)
+    code, shape, st, dt = _float_code(q, "q"), q.shape, q.stride(), q.dtype
     B, hq, hd = shape[0], shape[-2], shape[-1]
     Q = shape[1] if len(shape) == 4 else 1
     if st[-1] != 1:
@@ -564,30 +574,33 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     if pages.dim() != 3:
         raise ValueError("pages must be [n_pages, n_kv_heads, page bytes]")
     hkv = pages.shape[1]
-    pool, n_pages = _pool(pages, hkv, hd)
-    if out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
+    pool = _pool(pages, hkv, hd)
+    if out.dtype != dt or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and type")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1] or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32, of q's shape without the last dimension")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B:
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
         raise ValueError(f"page_table must be int32 [{B}, max_pages]")
-    ts, max_pages = page_table.stride(), page_table.shape[1]
+    (rows, max_pages), ts = page_table.shape, page_table.stride()
+    if rows != B:
+        raise ValueError(f"page_table must be int32 [{B}, max_pages]")
     if ts[1] != 1 and max_pages > 1:
         raise ValueError("page_table: the last dimension must be contiguous")
-    lens = _ints(seq_lens, "seq_lens", shape[:1])
-    lib = load_library()
+    lens = _ints(seq_lens, "seq_lens", B)
     if workspace is None:
         with torch.cuda.device(dev):
-            workspace = torch.zeros(paged_attention_workspace(B, Q, hq, hkv, hd), dtype=torch.uint8, device=dev)
-        if stream is not None:   # keep its memory until that stream is done with it
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream), device=dev))
+            workspace = torch.zeros(paged_attention_workspace(B, Q, hq, hkv, hd), dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                # zeroed on the current stream and used on the other one
+                other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+                other.wait_stream(torch.cuda.current_stream())
+                workspace.record_stream(other)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    _call(dev, lib.kvq_paged_attention, code, q.data_ptr(), qt, st[-2] if hq > 1 else 8, pool, n_pages,
+    _call(dev, stream, load_library().kvq_paged_attention, code, q.data_ptr(), qt, st[-2] if hq > 1 else 8, *pool,
           page_table.data_ptr(), ts[0] if B > 1 else max_pages, max_pages, lens, B, Q, hq, hkv, hd, window,
           0.0 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
-          workspace.data_ptr(), workspace.numel(), stream=stream)
+          workspace.data_ptr(), workspace.numel())
     return workspace
 
 

@@ -37,16 +37,18 @@ namespace kvq {
 
 namespace {
 
-#ifndef PAW
-#define PAW 8
+#ifndef PABATCH
+#define PABATCH 4
 #endif
-#ifndef PATT
-#define PATT 4
+#ifndef PASTEP1
+#define PASTEP1 4
 #endif
-constexpr int PA_WARPS = PAW;
+#ifndef PASTEP2
+#define PASTEP2 2
+#endif
+constexpr int PA_WARPS = 8;
 constexpr int PA_STAGES = 2;
 constexpr int PA_THREADS = 32 * PA_WARPS;
-constexpr int PA_STEP = PATT;                               // 16-token tiles per step
 #ifndef PALEAD
 #define PALEAD 2
 #endif
@@ -80,11 +82,15 @@ __device__ __forceinline__ int pa_first(const PaArgs& a, int len) {
 // Equal contiguous ranges of T unit positions for `ge` CTAs, none empty.  A group takes PA_LEAD
 // positions besides one per page when the ranges are long enough, for what starting and
 // finishing it costs.
+// a / b for 64-bit a and positive b: the 32-bit division (a quarter of the time) where it serves
+__device__ __forceinline__ long long pa_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 struct PaSplit {
   long long T;
   int ge;
-  __device__ __forceinline__ long long cta0(int c) const { return c * T / ge; }
-  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * ge - 1) / T); }
+  __device__ __forceinline__ long long cta0(int c) const { return pa_div(c * T, ge); }
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)pa_div((x + 1) * ge - 1, T); }
 };
 
 __device__ __forceinline__ unsigned long long pa_ns() {
@@ -147,7 +153,7 @@ __device__ __forceinline__ void lds(uint32_t (&w)[N], const unsigned char* p) {
 template <int HD, int NT, bool PACK>
 __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a) {
   using L = Page<HD>;
-  constexpr int G = L::G, MT = HD / 16, R = PACK ? 4 : 8 * NT, PART = R * (HD + 2);
+  constexpr int G = L::G, MT = HD / 16, R = PACK ? 4 : 8 * NT, PART = R * (HD + 2), STEP = NT == 1 ? PASTEP1 : PASTEP2;
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTE = 0x00FF00FFu;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ __align__(8) unsigned long long bars[PA_WARPS][PA_STAGES];
@@ -172,6 +178,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ended[warp].x = open_at[warp].x = -1;
   }
+
+  pdl_trigger();
+  pdl_wait();   // the launch and what lies above overlap the end of the previous kernel
 
   // pages of every sequence and their sum, then the positions before each sequence
   auto pages_of = [&](int len) { return len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0; };
@@ -233,9 +242,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     const long long c0 = sp.cta0(blockIdx.x);
     const int n = (int)(sp.cta0(blockIdx.x + 1) - c0), na = min(PA_WARPS, n);
     if (warp < na) {
-      const int w0 = (int)((long long)warp * n / na);
+      const int w0 = (int)pa_div((long long)warp * n, na);
       x0 = c0 + w0;
-      n_pos = (int)((long long)(warp + 1) * n / na) - w0;
+      n_pos = (int)pa_div((long long)(warp + 1) * n, na) - w0;
     }
   }
 
@@ -244,6 +253,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   struct Walk {
     int b, gr, p, np, first, x;
   };
+  const long long page_step = (long long)a.Hkv * L::BYTES;
   auto enter = [&](Walk& w) {   // a sequence's page range
     while (pre[w.b + 1] == pre[w.b]) ++w.b;
     w.np = pre[w.b + 1] - pre[w.b] - lead;
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   };
   Walk cw = {0, 0, 0, 0, 0, 0};
   if (n_pos) {
-    const int at = (int)(x0 / U);
+    const int at = (int)pa_div(x0, U);
     int lo = 0, hi = a.B - 1;   // the last sequence with pre[b] <= at
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -271,7 +281,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     cw.b = lo;
     enter(cw);
     const long long rem = x0 - (long long)pre[cw.b] * U;
-    cw.gr = (int)(rem / (cw.np + lead));
+    cw.gr = (int)pa_div(rem, cw.np + lead);
     cw.p = (int)(rem - (long long)cw.gr * (cw.np + lead)) - lead;
     if (cw.p < 0) cw.x = -cw.p, cw.p = 0;
   }
@@ -279,27 +289,27 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
                             // page numbers one further
   int next_id = pw.x < n_pos ? a.table[pw.b * a.table_stride + pw.first + pw.p] : 0;
   uint32_t valid = 0;       // bit s: stage s holds a page
-  const unsigned long long pol = evict_first_policy();
+  const unsigned char* head = a.pages + (pw.gr / a.RT) * L::BYTES;   // the KV head's part of page 0
+  // pages are read once, unless several row tiles take them
+  unsigned long long pol = evict_first_policy();
+  if (a.RT > 1) asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
   auto issue = [&](int s) {
     const bool ok = next_id >= 0 && next_id < a.n_pages;
     valid = (valid & ~(1u << s)) | ((uint32_t)ok << s);
     if (lane == 0) {
       const uint32_t bar = bar_s + 8 * s;
       if (ok) {
-        const unsigned char* src = a.pages + ((size_t)next_id * a.Hkv + pw.gr / a.RT) * L::BYTES;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(L::BYTES) : "memory");
-        if (a.RT == 1)   // read once
-          asm volatile(
-              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-              :: "r"(ring_s + s * L::BYTES), "l"(src), "r"(L::BYTES), "r"(bar), "l"(pol) : "memory");
-        else
-          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                       :: "r"(ring_s + s * L::BYTES), "l"(src), "r"(L::BYTES), "r"(bar) : "memory");
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+            :: "r"(ring_s + s * L::BYTES), "l"(head + next_id * page_step), "r"(L::BYTES), "r"(bar), "l"(pol) : "memory");
       } else {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
       }
     }
+    const int gr = pw.gr;
     advance(pw);
+    if (pw.gr != gr) head = a.pages + (pw.gr / a.RT) * L::BYTES;
     if (pw.x < n_pos) next_id = a.table[pw.b * a.table_stride + pw.first + pw.p];
   };
 #pragma unroll 1
@@ -312,9 +322,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   float cs[NT][2];            // score factor of this lane's two columns
   int c_lo[NT][2], c_hi[NT][2];   // tokens its columns see
   int t_lo = 0, t_hi = 0, t_all = 0, t_end = 0;   // seen by every row: [t_lo, t_hi); by any: [t_all, t_end)
-  // softmax reference (base 2) and weight sum; sums over the codes: rows gid the low nibble's
+  // softmax reference (base 2), the largest score / cs that needs no new one; sums over the codes: rows gid the low nibble's
   // channel, rows gid + 8 the byte's (16 times the high nibble's plus the low one's)
-  float ref[NT][2], l[NT][2], acc[NT][MT][4], off[NT][4];
+  // and the sums of weights times offsets, rows = groups, then the weights' own (row G)
+  float ref[NT][2], lim[NT][2], acc[NT][MT][4], off[NT][4];
   float top = PA_TOP;         // weights stay below 2^top
   bool started = false, failed = false;
 
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       int e = 0;
       if (mx > 0.f) frexpf(mx, &e);
       e = max(-100, min(100, 10 - e));
-      const float up = ldexpf(1.f, e), upl = up * 0.0625f;
+      const float up = a.scale_log2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e), upl = up * 0.0625f;
       float gs[G];
 #pragma unroll
       for (int k = 0; k < G; ++k) {
@@ -372,14 +383,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       const __half2 h2 = __floats2half2_rn(u, v);
       const float2 hf = __half22float2(h2);
       qo[ct] = piece == 0 ? h2_as_u32(h2) : piece == 1 ? h2_as_u32(__floats2half2_rn(u - hf.x, v - hf.y)) : 0u;
-      const float mine = ldexpf(a.scale_log2, -e);
+      // never 0, so that -inf stays -inf; the scale's sign is in q
+      const float mine = fmaxf(ldexpf(fabsf(a.scale_log2), -e), 1.17549435e-38f);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         cs[ct][j] = __shfl_sync(0xffffffffu, mine, (2 * tig + j) * 4);
         const int c = ct * 8 + (PACK ? (2 * tig + j) & 3 : 2 * tig + j);
         const int ci = (r0 + min(c, rn - 1)) / a.n_rep;
         c_lo[ct][j] = lo_of(ci), c_hi[ct][j] = hi_of(ci);
-        ref[ct][j] = -3.402823466e38f, l[ct][j] = 0.f;
+        ref[ct][j] = -3.402823466e38f, lim[ct][j] = -INFINITY;
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -393,6 +405,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 
   const int pr_k = tig % (G / 2);
   const bool lo_col = gid >= 4;
+  // A rows of the offset product: groups, then a row of ones, then nothing
+  const uint32_t o_mask = gid < G ? 0xffffffffu : 0u, o_one = gid == G ? 0x3C003C00u : 0u;
+  const int o_at = L::VO + (gid % G) * 2 * PG + tig * 32;
   // byte of this lane's value pieces of tokens 2tig and 2tig + 1
   const int vrow0 = (HD == 128 ? (2 * tig + (tig & 1)) : (2 * tig + (tig >> 1))) * L::ROW;
   const int vrow1 = (HD == 128 ? (2 * tig + 1 - (tig & 1)) : (2 * tig + 1 - (tig >> 1))) * L::ROW;
@@ -427,16 +442,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll
         for (int i = 0; i < G; ++i) mx = max(mx, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
         mx = __reduce_max_sync(0xffffffffu, mx);
-        top = fminf(top, PA_TOP - (float)((int)(mx >> 10) - 15));
+        const float now = fminf(top, PA_TOP - (float)((int)(mx >> 10) - 15));
+        if (now != top) {
+          top = now;
+#pragma unroll
+          for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) lim[ct][j] = ref[ct][j] < -3e38f ? -INFINITY : (ref[ct][j] + top) / cs[ct][j];
+        }
       }
     }
 
 #pragma unroll 1
-    for (int i0 = 0; i0 < 4; i0 += PA_STEP) {
-      // ---- scores (base 2) ----
-      float S[NT][PA_STEP][4];
+    for (int i0 = 0; i0 < 4; i0 += STEP) {
+      // ---- scores: S cs is the score in base 2 ----
+      float S[NT][STEP][4];
 #pragma unroll
-      for (int ii = 0; ii < PA_STEP; ++ii) {
+      for (int ii = 0; ii < STEP; ++ii) {
         const int ta = 16 * (i0 + ii) + gid, tb = ta + 8;
         uint32_t wa[G], wb[G], sa[G / 2], sb[G / 2];
         lds(wa, pg + ta * L::ROW + tig * 4 * G);
@@ -468,18 +490,22 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
           float O[4];
           mma_z(O, oa, ob, 0u, 0u, qo[ct], 0u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) S[ct][ii][j] = fmaf(r[ct][j], NIB_ROW_SCALE_LO, O[j]) * cs[ct][j & 1];
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int t = tok0 + (j < 2 ? ta : tb);
-              if (t < c_lo[ct][j & 1] || t >= c_hi[ct][j & 1]) S[ct][ii][j] = -INFINITY;
-            }
-          }
+          for (int j = 0; j < 4; ++j) S[ct][ii][j] = fmaf(r[ct][j], NIB_ROW_SCALE_LO, O[j]);
         }
       }
+      if (edge) {
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+          for (int ii = 0; ii < STEP; ++ii)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int t = tok0 + 16 * (i0 + ii) + gid + (j < 2 ? 0 : 8);
+              if (t < c_lo[ct][j & 1] || t >= c_hi[ct][j & 1]) S[ct][ii][j] = -INFINITY;
+            }
+      }
 
-      // ---- softmax weights 2^(S - ref): the reference moves only when one would pass 2^top ----
+      // ---- softmax weights 2^(S cs - ref): the reference moves only when one would pass 2^top ----
       float mx[NT][2];
       bool over = false;
 #pragma unroll
@@ -488,9 +514,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         for (int j = 0; j < 2; ++j) {
           float t = fmaxf(S[ct][0][j], S[ct][0][j + 2]);
 #pragma unroll
-          for (int ii = 1; ii < PA_STEP; ++ii) t = fmaxf(t, fmaxf(S[ct][ii][j], S[ct][ii][j + 2]));
+          for (int ii = 1; ii < STEP; ++ii) t = fmaxf(t, fmaxf(S[ct][ii][j], S[ct][ii][j + 2]));
           mx[ct][j] = t;
-          over = over || t > ref[ct][j] + top;
+          over = over || t > lim[ct][j];
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -502,10 +528,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            const float now = t > ref[ct][j] + top ? t - (top - PA_SLACK) : ref[ct][j];
+            const float now = t > lim[ct][j] ? t * cs[ct][j] - (top - PA_SLACK) : ref[ct][j];
             al[j] = exp2_approx(ref[ct][j] - now);
+            if (t > lim[ct][j]) lim[ct][j] = (now + top) / cs[ct][j];
             ref[ct][j] = now;
-            l[ct][j] *= al[j];
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -518,7 +544,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 
       // ---- values ----
 #pragma unroll
-      for (int ii = 0; ii < PA_STEP; ++ii) {
+      for (int ii = 0; ii < STEP; ++ii) {
         const int i = i0 + ii;
         // B fragments of the weights (k = tokens 16i + 2tig, +1 and 8 more), hi and lo halves
         uint32_t ph[NT][2], pl[NT][2];
@@ -526,12 +552,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         for (int ct = 0; ct < NT; ++ct)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float2 p = make_float2(exp2_approx(S[ct][ii][2 * h] - ref[ct][0]), exp2_approx(S[ct][ii][2 * h + 1] - ref[ct][1]));
-            l[ct][0] += p.x, l[ct][1] += p.y;
-            const __half2 hi = __floats2half2_rn(p.x, p.y);
+            const float p0 = exp2_approx(fmaf(S[ct][ii][2 * h], cs[ct][0], -ref[ct][0]));
+            const float p1 = exp2_approx(fmaf(S[ct][ii][2 * h + 1], cs[ct][1], -ref[ct][1]));
+            const __half2 hi = __floats2half2_rn(p0, p1);
             const float2 hf = __half22float2(hi);
             ph[ct][h] = movmatrix_t(h2_as_u32(hi));
-            pl[ct][h] = movmatrix_t(h2_as_u32(__floats2half2_rn(p.x - hf.x, p.y - hf.y)));
+            pl[ct][h] = movmatrix_t(h2_as_u32(__floats2half2_rn(p0 - hf.x, p1 - hf.y)));
           }
         // codes of token pairs: word g of x[h] holds four channels of group g of two tokens
         uint32_t x[2][G];
@@ -543,27 +569,26 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll
           for (int g = 0; g < G; ++g) x[h][g] = __byte_perm(t0[g >> 1], t1[g >> 1], (g & 1) ? 0x7632 : 0x5410);
         }
-        uint32_t o[2] = {0u, 0u};   // offsets: rows = groups
-        if (gid < G) lds(o, pg + L::VO + gid * 2 * PG + tig * 32 + i * 8);
+        uint32_t o[2];
+        lds(o, pg + o_at + i * 8);
+        o[0] = (o[0] & o_mask) | o_one, o[1] = (o[1] & o_mask) | o_one;
         if (PACK) {
-          // columns 4..7 take the lo halves: there the product p_hi s is formed twice and
-          // only its remainder kept
-          uint32_t pz[2], pw[2];
+          // columns 4..7 take the lo halves: there p_hi s is formed again for its remainder
+          uint32_t pm[2], pz[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            pw[h] = lo_col ? pl[0][h] : 0u;
+            pm[h] = lo_col ? pl[0][h] : ph[0][h];
             pz[h] = lo_col ? ph[0][h] : 0u;
           }
-          mma(off[0], o[0], 0u, o[1], 0u, lo_col ? pw[0] : ph[0][0], lo_col ? pw[1] : ph[0][1]);
+          mma(off[0], o[0], 0u, o[1], 0u, pm[0], pm[1]);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            uint32_t s[2], b[2];
-            lds(s, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
+            uint32_t sc[2], b[2];
+            lds(sc, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const __half2 sv = u32_as_h2(s[h]);
-              const __half2 t = __hmul2_rn(u32_as_h2(pz[h]), sv);
-              b[h] = h2_as_u32(__hfma2(u32_as_h2(pw[h]), sv, __hfma2(u32_as_h2(ph[0][h]), sv, __hneg2(t))));
+              const __half2 sv = u32_as_h2(sc[h]), z = u32_as_h2(pz[h]);
+              b[h] = h2_as_u32(__hfma2(u32_as_h2(pm[h]), sv, __hfma2(z, sv, __hneg2(__hmul2_rn(z, sv)))));
             }
             const uint32_t y0 = __byte_perm(x[0][g], 0u, 0x4341), y1 = __byte_perm(x[1][g], 0u, 0x4341);
             mma(acc[0][2 * g], x[0][g] & LO, x[0][g] & BYTE, x[1][g] & LO, x[1][g] & BYTE, b[0], b[1]);
@@ -577,8 +602,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
           }
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            uint32_t s[2];
-            lds(s, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
+            uint32_t sc[2];
+            lds(sc, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
             const uint32_t y0 = __byte_perm(x[0][g], 0u, 0x4341), y1 = __byte_perm(x[1][g], 0u, 0x4341);
             const uint32_t x0l = x[0][g] & LO, x0b = x[0][g] & BYTE, x1l = x[1][g] & LO, x1b = x[1][g] & BYTE;
             const uint32_t y0l = y0 & LO, y1l = y1 & LO;
@@ -587,7 +612,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
               uint32_t hi[2], lo[2];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const __half2 sv = u32_as_h2(s[h]), p = u32_as_h2(ph[ct][h]);
+                const __half2 sv = u32_as_h2(sc[h]), p = u32_as_h2(ph[ct][h]);
                 const __half2 w = __hmul2_rn(p, sv);
                 hi[h] = h2_as_u32(w);
                 lo[h] = h2_as_u32(__hfma2(u32_as_h2(pl[ct][h]), sv, __hfma2(p, sv, __hneg2(w))));   // the remainder is exact
@@ -611,10 +636,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     for (int ct = 0; ct < NT; ++ct)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float lt = l[ct][j];
-        lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-        lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-        lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+        float lt = __shfl_sync(0xffffffffu, off[ct][j], 4 * G + tig);
+        if (PACK) lt += __shfl_xor_sync(0xffffffffu, lt, 2);
         if (failed) lt = __int_as_float(0x7fc00000);
         const float rf = lt == 0.f ? -INFINITY : ref[ct][j];
         const int c = ct * 8 + 2 * tig + j;
@@ -700,18 +723,18 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         o.x = fmaf(o.x, f, v.x * g), o.y = fmaf(o.y, f, v.y * g), o.z = fmaf(o.z, f, v.z * g), o.w = fmaf(o.w, f, v.w * g);
       };
       if (KS == 1 || ks < KS)
-        for (int k0 = ks; k0 < n; k0 += 4 * KS) {
-          float2 ml[4];
-          float4 v[4];
+        for (int k0 = ks; k0 < n; k0 += PABATCH * KS) {
+          float2 ml[PABATCH];
+          float4 v[PABATCH];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < PABATCH; ++k)
             if (k0 + k * KS < n) {
               const float* src = piece(k0 + k * KS);
               v[k] = __ldcg(reinterpret_cast<const float4*>(src) + e);
               ml[k] = __ldcg(reinterpret_cast<const float2*>(src + R * HD) + c);
             }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < PABATCH; ++k)
             if (k0 + k * KS < n) add(ml[k], v[k]);
         }
       if (KS > 1) {
@@ -835,8 +858,7 @@ cudaError_t launch(const PaArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)PA_WARPS * PA_STAGES * Page<HD>::BYTES + (2 * (size_t)a.B + 1) * sizeof(int);
   auto* k = paged_attention_kernel<HD, NT, PACK>;
   if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-  k<<<a.grid, PA_THREADS, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(k, dim3(a.grid), dim3(PA_THREADS), smem, st, a);
 }
 
 kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, const void* pages, int n_pages,
