@@ -37,9 +37,6 @@ namespace kvq {
 
 namespace {
 
-#ifndef PABATCH
-#define PABATCH 4
-#endif
 #ifndef PASTEP1
 #define PASTEP1 4
 #endif
@@ -64,9 +61,9 @@ struct PaArgs {
   void* out;
   float* lse;
   int* arrived;  // [CTAs] arrivals at the group that starts in a CTA and leaves it; 0 between calls
-  float* part;   // pieces of R (HD + 2) floats: [warps][2] (0: the end of a group begun in an
-                 // earlier warp, 1: an open group), then [CTAs][2] (0: of a group begun in an
-                 // earlier CTA, 1: of one that leaves the CTA)
+  float* part;   // pieces of R (HD + 2) floats: [warps] the end of a group begun in an earlier
+                 // warp, then [CTAs][2] (0: of a group begun in an earlier CTA, 1: of one that
+                 // leaves the CTA)
   long long qt, qh, table_stride;
   int n_pages, max_pages, B, Q, Hq, Hkv, n_rep, rows, RT, window, grid;
   float scale_log2;   // scale * log2(e)
@@ -129,6 +126,12 @@ __device__ __forceinline__ void mma_z(float (&c)[4], uint32_t a0, uint32_t a1, u
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// ... of half the depth, with a zero C
+__device__ __forceinline__ void mma_k8_z(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -149,6 +152,82 @@ __device__ __forceinline__ void lds(uint32_t (&w)[N], const unsigned char* p) {
   }
 }
 
+template <int HD>
+struct PaStage {
+  static constexpr int FLOATS = 8 * (HD + 4) + 8 * (HD / 32) + 16;   // a multiple of 4
+};
+
+// Four channels of one row of the output: v / lt, and the row's lse.
+template <int HD>
+__device__ __forceinline__ void pa_store_row(const PaArgs& a, int b, int g, int r, int x, float4 v, float ref, float lt) {
+  const int qi = r / a.n_rep;
+  const size_t row = ((size_t)b * a.Q + qi) * a.Hq + g * a.n_rep + (r - qi * a.n_rep);
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  reinterpret_cast<uint2*>(a.out)[row * (HD / 4) + x] =
+      make_uint2(f2_to_pair(v.x * inv, v.y * inv, a.bf16), f2_to_pair(v.z * inv, v.w * inv, a.bf16));
+  if (x == 0 && a.lse) a.lse[row] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+}
+
+// The sum of n pieces of group grp in order, by the whole CTA (KS threads share a sum): into
+// dst, or as output rows.  The pieces are those of the CTAs from `across` on (the first one
+// in its second slot, the others in their first), or, when that is null, of the warps from
+// *at on (the last one an ended piece when `closed`).  Not inlined: its registers and its
+// schedule stay out of the page loop's, and the second use finds its instructions cached.
+template <int HD, int R>
+__device__ __noinline__ void pa_merge(const PaArgs& a, const float* const* at, const float* across, int n, bool closed,
+                                      int2 grp, float* dst) {
+  constexpr int PART = R * (HD + 2), VEC = R * HD / 4, KS = PA_THREADS / VEC > 1 ? PA_THREADS / VEC : 1;
+#ifndef PABATCH
+#define PABATCH 10
+#endif
+  constexpr int BATCH = PABATCH;   // pieces on their way at once
+  __shared__ float4 red[KS > 1 ? PA_THREADS : 1];
+  __shared__ float2 redm[KS > 1 ? PA_THREADS : 1];
+  for (int e0 = 0; e0 < VEC; e0 += PA_THREADS) {
+    const int e = (e0 + threadIdx.x) % VEC, ks = threadIdx.x / VEC, c = e / (HD / 4);
+    float M = -INFINITY, Ls = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 ml, float4 v) {
+      const float to = fmaxf(M, ml.x), f = M == to ? 1.f : exp2_approx(M - to);
+      const float g = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - to);
+      M = to;
+      Ls = fmaf(Ls, f, ml.y * g);
+      o.x = fmaf(o.x, f, v.x * g), o.y = fmaf(o.y, f, v.y * g), o.z = fmaf(o.z, f, v.z * g), o.w = fmaf(o.w, f, v.w * g);
+    };
+    for (int k0 = KS > 1 ? ks : 0; k0 < n; k0 += BATCH * KS) {
+      float2 ml[BATCH];
+      float4 v[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int k = k0 + i * KS;
+        if (k >= n) continue;
+        const float* src = across ? across + (size_t)(2 * k + (k == 0)) * PART : at[2 * k + !(closed && k == n - 1)];
+        v[i] = reinterpret_cast<const float4*>(src)[e];
+        ml[i] = reinterpret_cast<const float2*>(src + R * HD)[c];
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (k0 + i * KS < n) add(ml[i], v[i]);
+    }
+    if (KS > 1) {
+      red[threadIdx.x] = o;
+      redm[threadIdx.x] = make_float2(M, Ls);
+      __syncthreads();
+      if (ks == 0)
+        for (int k = 1; k < KS; ++k) add(redm[k * VEC + e], red[k * VEC + e]);
+      __syncthreads();
+      if (ks != 0) continue;
+    }
+    if (dst) {
+      reinterpret_cast<float4*>(dst)[e] = o;
+      if (e % (HD / 4) == 0) reinterpret_cast<float2*>(dst + R * HD)[c] = make_float2(M, Ls);
+    } else {
+      const int g = grp.y / a.RT, r = (grp.y - g * a.RT) * R + c;
+      if (r < a.rows) pa_store_row<HD>(a, grp.x, g, r, e % (HD / 4), o, M, Ls);
+    }
+  }
+}
+
 // R query rows per tile: PACK 4 (hi and lo weights share one column tile), else 8 NT.
 template <int HD, int NT, bool PACK>
 __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a) {
@@ -163,14 +242,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   __shared__ bool open_new[PA_WARPS];
   __shared__ int wsum[PA_WARPS], wcnt[PA_WARPS];
   __shared__ int final_n[2];
-  __shared__ float4 red[PA_THREADS];
-  __shared__ float2 redm[PA_THREADS];
-  int* pre = reinterpret_cast<int*>(sm + PA_WARPS * PA_STAGES * L::BYTES);   // [B + 1] positions before each sequence
+  __shared__ const float* piece_at[PA_WARPS][2];   // where a warp's ended and open pieces lie
+  int* pre = reinterpret_cast<int*>(sm + PA_WARPS * (PA_STAGES * L::BYTES + PaStage<HD>::FLOATS * 4));   // [B + 1] positions before each sequence
   int* slen = pre + a.B + 1;                                                 // [B]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // broadcast, so that the compiler knows it (and all that follows from it) as warp-uniform
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   unsigned char* ring = sm + warp * PA_STAGES * L::BYTES;
+  // per warp: eight columns of a finished tile (rows padded to distinct banks), then their
+  // offsets per group, weight sums and references
+  constexpr int SROW = HD + 4;
+  float* stage = reinterpret_cast<float*>(sm + PA_WARPS * PA_STAGES * L::BYTES) + warp * PaStage<HD>::FLOATS;
+  float* stage_o = stage + 8 * SROW;   // [8][G]
+  float* stage_l = stage_o + 8 * G;    // [8]
+  float* stage_r = stage_l + 8;        // [8]
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   const uint32_t bar_s = (uint32_t)__cvta_generic_to_shared(&bars[warp][0]);
   if (lane == 0) {
@@ -488,7 +574,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll
         for (int ct = 0; ct < NT; ++ct) {
           float O[4];
-          mma_z(O, oa, ob, 0u, 0u, qo[ct], 0u);
+          mma_k8_z(O, oa, ob, qo[ct]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) S[ct][ii][j] = fmaf(r[ct][j], NIB_ROW_SCALE_LO, O[j]);
         }
@@ -628,48 +714,52 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     }
   };
 
-  // Writes the group's rows: the finished output (dst == nullptr) or sums, reference and
-  // weight sum into dst: [R][HD] floats, then [R][2].
+  // Writes the group's rows through the warp's stage: the finished output (dst == nullptr) or
+  // a piece: sums [R][HD], then reference and weight sum [R][2].
   auto emit = [&](const Walk& w, float* dst) {
     const int g = w.gr / a.RT, r0 = (w.gr - g * a.RT) * R, rn = min(R, a.rows - r0);
 #pragma unroll
-    for (int ct = 0; ct < NT; ++ct)
+    for (int ct = 0; ct < NT; ++ct) {
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float lt = __shfl_sync(0xffffffffu, off[ct][j], 4 * G + tig);
-        if (PACK) lt += __shfl_xor_sync(0xffffffffu, lt, 2);
-        if (failed) lt = __int_as_float(0x7fc00000);
-        const float rf = lt == 0.f ? -INFINITY : ref[ct][j];
-        const int c = ct * 8 + 2 * tig + j;
-        const bool live = c < rn;
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        const int rr = r0 + (live ? c : 0), qi = rr / a.n_rep;
-        const size_t orow = ((size_t)w.b * a.Q + qi) * a.Hq + g * a.n_rep + (rr - qi * a.n_rep);
+        float* row = stage + (2 * tig + j) * SROW + 4 * gid;
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
-          const float o = __shfl_sync(0xffffffffu, off[ct][j], 4 * gg + tig);
           const float e0 = acc[ct][2 * gg][j], e1 = acc[ct][2 * gg][j + 2], e2 = acc[ct][2 * gg + 1][j], e3 = acc[ct][2 * gg + 1][j + 2];
-          float4 v = make_float4(fmaf(e0, NIB_ROW_SCALE_LO, o), fmaf(e1 - e0, NIB_ROW_SCALE_HI, o),
-                                 fmaf(e2, NIB_ROW_SCALE_LO, o), fmaf(e3 - e2, NIB_ROW_SCALE_HI, o));
-          if (PACK) {   // columns 4..7 hold the lo halves' sums
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, 2);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, 2);
-            v.z += __shfl_xor_sync(0xffffffffu, v.z, 2);
-            v.w += __shfl_xor_sync(0xffffffffu, v.w, 2);
-          }
-          if (PACK && tig >= 2) continue;
-          if (dst) {
-            *reinterpret_cast<float4*>(dst + c * HD + 32 * gg + 4 * gid) = v;
-          } else if (live) {
-            *reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.out) + orow * HD + 32 * gg + 4 * gid) =
-                make_uint2(f2_to_pair(v.x * inv, v.y * inv, a.bf16), f2_to_pair(v.z * inv, v.w * inv, a.bf16));
-          }
+          *reinterpret_cast<float4*>(row + 32 * gg) =
+              make_float4(e0 * NIB_ROW_SCALE_LO, (e1 - e0) * NIB_ROW_SCALE_HI, e2 * NIB_ROW_SCALE_LO, (e3 - e2) * NIB_ROW_SCALE_HI);
         }
-        if (gid == 0 && !(PACK && tig >= 2)) {
-          if (dst) *reinterpret_cast<float2*>(dst + R * HD + 2 * c) = make_float2(rf, lt);
-          else if (live && a.lse) a.lse[orow] = lt == 0.f ? -INFINITY : (rf + log2f(lt)) * 0.69314718055994531f;
+        if (gid < G) stage_o[(2 * tig + j) * G + gid] = off[ct][j];
+        if (gid == G) stage_l[2 * tig + j] = failed ? __int_as_float(0x7fc00000) : off[ct][j];
+        if (gid == 0) stage_r[2 * tig + j] = ref[ct][j];
+      }
+      __syncwarp();
+      constexpr int TR = PACK ? 4 : 8, F4 = HD / 4;   // rows of the tile, float4s of a row
+#pragma unroll
+      for (int k = 0; k < TR * F4 / 32; ++k) {
+        const int e = lane + 32 * k, c = e / F4, x = e % F4;
+        auto at = [&](int col) {
+          const float4 v = *reinterpret_cast<const float4*>(stage + col * SROW + 4 * x);
+          const float o = stage_o[col * G + x / 8];
+          return make_float4(v.x + o, v.y + o, v.z + o, v.w + o);
+        };
+        float4 v = at(c);
+        float lt = stage_l[c];
+        if (PACK) {   // columns 4..7 hold the lo halves' sums
+          const float4 u = at(c + 4);
+          v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+          lt += stage_l[c + 4];
+        }
+        const int rt = 8 * ct + c;   // row of the tile
+        if (dst) {
+          reinterpret_cast<float4*>(dst)[rt * F4 + x] = v;
+          if (x == 0) reinterpret_cast<float2*>(dst + R * HD)[rt] = make_float2(lt == 0.f ? -INFINITY : stage_r[c], lt);
+        } else if (rt < rn) {
+          pa_store_row<HD>(a, w.b, g, r0 + rt, x, v, stage_r[c], lt);
         }
       }
+    }
   };
 
   bool open = false;
@@ -691,8 +781,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     advance(cw);
     const bool end = at.p + 1 == at.np;
     if (end || cw.x >= n_pos) {
-      emit(at, end && started ? nullptr : a.part + ((size_t)gw * 2 + !end) * PART);
+      // an open group's piece goes to the ring, which no copy uses any more
+      float* dst = !end ? reinterpret_cast<float*>(ring) : started ? nullptr : a.part + (size_t)gw * PART;
+      emit(at, dst);
       if (lane == 0) {
+        if (dst) piece_at[warp][!end] = dst;
         if (end) {
           if (!started) ended[warp] = make_int2(at.b, at.gr);
         } else {
@@ -708,67 +801,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   __syncthreads();
 
   // ---- groups that were cut ----
-  // The sum of n pieces in order, for float4 e of the tile's rows; KS threads share a sum.
-  constexpr int VEC = R * HD / 4, KS = PA_THREADS / VEC > 1 ? PA_THREADS / VEC : 1;
-  auto merge = [&](int n, auto piece, auto store) {
-    for (int e0 = 0; e0 < VEC; e0 += PA_THREADS) {
-      const int e = (e0 + threadIdx.x) % VEC, ks = threadIdx.x / VEC, c = e / (HD / 4);
-      float M = -INFINITY, Ls = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](float2 ml, float4 v) {
-        const float to = fmaxf(M, ml.x), f = M == to ? 1.f : exp2_approx(M - to);
-        const float g = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - to);
-        M = to;
-        Ls = fmaf(Ls, f, ml.y * g);
-        o.x = fmaf(o.x, f, v.x * g), o.y = fmaf(o.y, f, v.y * g), o.z = fmaf(o.z, f, v.z * g), o.w = fmaf(o.w, f, v.w * g);
-      };
-      if (KS == 1 || ks < KS)
-        for (int k0 = ks; k0 < n; k0 += PABATCH * KS) {
-          float2 ml[PABATCH];
-          float4 v[PABATCH];
-#pragma unroll
-          for (int k = 0; k < PABATCH; ++k)
-            if (k0 + k * KS < n) {
-              const float* src = piece(k0 + k * KS);
-              v[k] = __ldcg(reinterpret_cast<const float4*>(src) + e);
-              ml[k] = __ldcg(reinterpret_cast<const float2*>(src + R * HD) + c);
-            }
-#pragma unroll
-          for (int k = 0; k < PABATCH; ++k)
-            if (k0 + k * KS < n) add(ml[k], v[k]);
-        }
-      if (KS > 1) {
-        red[threadIdx.x] = o;
-        redm[threadIdx.x] = make_float2(M, Ls);
-        __syncthreads();
-        if (ks == 0)
-          for (int k = 1; k < KS; ++k) add(redm[k * VEC + e], red[k * VEC + e]);
-        __syncthreads();
-      }
-      if (ks == 0) store(e, c, o, M, Ls);
-    }
-  };
-  auto store_piece = [&](float* dst) {
-    return [=](int e, int c, float4 o, float M, float Ls) {
-      reinterpret_cast<float4*>(dst)[e] = o;
-      if (e % (HD / 4) == 0) reinterpret_cast<float2*>(dst + R * HD)[c] = make_float2(M, Ls);
-    };
-  };
-  auto store_rows = [&](int2 grp) {
-    const int g = grp.y / a.RT, r0 = (grp.y - g * a.RT) * R;
-    return [=, &a](int e, int c, float4 o, float M, float Ls) {
-      const int rr = r0 + c;
-      if (rr >= a.rows) return;
-      const int qi = rr / a.n_rep;
-      const size_t orow = ((size_t)grp.x * a.Q + qi) * a.Hq + g * a.n_rep + (rr - qi * a.n_rep);
-      const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
-      reinterpret_cast<uint2*>(a.out)[orow * (HD / 4) + e % (HD / 4)] =
-          make_uint2(f2_to_pair(o.x * inv, o.y * inv, a.bf16), f2_to_pair(o.z * inv, o.w * inv, a.bf16));
-      if (a.lse && e % (HD / 4) == 0) a.lse[orow] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
-    };
-  };
-  float* wpart = a.part + (size_t)blockIdx.x * PA_WARPS * 2 * PART;
-  float* cpart = a.part + (size_t)a.grid * PA_WARPS * 2 * PART;
+  float* cpart = a.part + (size_t)a.grid * PA_WARPS * PART;
   // runs of pieces of one group within this CTA: that of a group begun in an earlier CTA (w =
   // -1), then those of the groups that each warp starts and leaves open
   int2 away[2] = {make_int2(-1, 0), make_int2(-1, 0)};   // groups with pieces in other CTAs
@@ -793,14 +826,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       else if (!(op.x == grp.x && op.y == grp.y)) break;
       ++n, ++last;
     }
-    auto piece = [&](int k) { return wpart + ((first + k) * 2 + !(closed && k == n - 1)) * PART; };
-    if (closed && w >= 0) {
-      merge(n, piece, store_rows(grp));
-    } else {
-      const int slot = w >= 0;
-      away[slot] = grp;
-      merge(n, piece, store_piece(cpart + ((size_t)blockIdx.x * 2 + slot) * PART));
-    }
+    const int slot = w >= 0;
+    const bool all = closed && w >= 0;
+    if (!all) away[slot] = grp;
+    pa_merge<HD, R>(a, &piece_at[first][0], nullptr, n, closed, grp, all ? nullptr : cpart + ((size_t)blockIdx.x * 2 + slot) * PART);
   }
   if (away[0].x < 0 && away[1].x < 0) return;
   __syncthreads();
@@ -825,13 +854,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     if (away[k].x < 0 || final_n[k] == 0) continue;
-    const int c0 = first_cta[k];
-    merge(final_n[k], [&](int i) { return cpart + ((size_t)(c0 + i) * 2 + (i == 0)) * PART; }, store_rows(away[k]));
+    pa_merge<HD, R>(a, nullptr, cpart + (size_t)first_cta[k] * 2 * PART, final_n[k], false, away[k], nullptr);
   }
 }
 
 const char* shape_error(int B, int Q, int Hq, int Hkv, int hd) {
-  if (B < 0 || B > 4096) return "batch must be in 0..4096";
+  if (B < 0 || B > 2048) return "batch must be in 0..2048";
   if (Q < 1 || Q > 64) return "n_q_tokens must be in 1..64";
   if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 64) return "n_q_heads / n_kv_heads must be an integer in 1..64";
   if (hd != 64 && hd != 128) return "head_dim must be 64 or 128";
@@ -847,15 +875,16 @@ cudaError_t sm_count(int* sms) {
   return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
-// arrival counters, then pieces: two per warp and two per CTA
+// arrival counters, then pieces: one per warp and two per CTA
 constexpr size_t PA_COUNTERS = 4096;
 size_t ws_bytes(int sms, int Q, int Hq, int Hkv, int hd) {
-  return PA_COUNTERS + (size_t)sms * (PA_WARPS + 1) * 2 * tile_rows(Q * (Hq / Hkv)) * (hd + 2) * sizeof(float);
+  return PA_COUNTERS + (size_t)sms * (PA_WARPS + 2) * tile_rows(Q * (Hq / Hkv)) * (hd + 2) * sizeof(float);
 }
 
 template <int HD, int NT, bool PACK>
 cudaError_t launch(const PaArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)PA_WARPS * PA_STAGES * Page<HD>::BYTES + (2 * (size_t)a.B + 1) * sizeof(int);
+  const size_t smem = (size_t)PA_WARPS * (PA_STAGES * Page<HD>::BYTES + PaStage<HD>::FLOATS * sizeof(float)) +
+                      (2 * (size_t)a.B + 1) * sizeof(int);
   auto* k = paged_attention_kernel<HD, NT, PACK>;
   if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
   return launch_dependent(k, dim3(a.grid), dim3(PA_THREADS), smem, st, a);

@@ -438,7 +438,7 @@ kvq_status kvq_paged_attention_workspace(int batch, int n_q_tokens, int n_q_head
  *               first 4096 bytes set to zero once, before the first call that uses it: every
  *               call leaves them zero (they count the arrivals of a row's pieces), whatever
  *               its shape.  Calls that share it must not overlap on the GPU.
- * One kernel.  Hq / Hkv an integer in 1..64, n_q_tokens 1..64, batch <= 4096, head_dim 64 or
+ * One kernel.  Hq / Hkv an integer in 1..64, n_q_tokens 1..64, batch <= 2048, head_dim 64 or
  * 128, batch * max_pages < 2^30.  Scores and sums in fp32.  batch = 0 is a no-op.  Every
  * device-side wait is bounded (2 s); one that runs out, which does not happen in correct
  * operation, makes the affected outputs NaN.

@@ -164,7 +164,7 @@ def _attend(**kw):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(dtype=3), dict(B=-1), dict(B=4097), dict(Q=0), dict(Q=65), dict(Hq=7), dict(Hkv=0), dict(Hq=0),
+    dict(dtype=3), dict(B=-1), dict(B=2049), dict(Q=0), dict(Q=65), dict(Hq=7), dict(Hkv=0), dict(Hq=0),
     dict(Hq=130, Hkv=2), dict(hd=256), dict(n_pages=0), dict(max_pages=0), dict(max_pages=(1 << 24) + 1), dict(max_pages=1 << 24, B=64), dict(ts=-1),
     dict(window=-1), dict(scale=float("nan")), dict(scale=float("inf")), dict(qt=-8), dict(qh=3),
 ])
