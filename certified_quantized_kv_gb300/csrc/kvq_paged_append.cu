@@ -6,86 +6,244 @@
 // and for the values of odd slots, counted down from the maximum,
 //   s = -(fp16 rounded up of (max - min) / 15), o = fp16(max), code = clamp(rint((o - x) / |s|), 0, 15)
 // so x^ = o + s code in both.  The scale is rounded up so that 15 steps span the group.
+#include <algorithm>
 #include <string>
 
 #include "kvq.h"
 #include "kvq_launch.h"
 #include "kvq_paged.cuh"
+#include "kvq_rope.cuh"
 
 namespace kvq {
 
 namespace {
 
 struct AppendPagedArgs {
-  const void *k, *v, *q;
-  void* q_out;
+  const void *k, *v;
   const int32_t *slots, *pos;
   unsigned char* pages;
-  long long kt, kh, vt, vh, qt, qh, ot, oh;   // strides in elements
-  int T, Hkv, Hq, n_pages;
-  bool bf16, rotate;
+  long long kt, kh, vt, vh;   // strides in elements
+  int T, Hkv, n_pages, per;   // per: KV heads of one item
+  int kv_blocks;              // the blocks behind these turn q
+  RopeArgs q;
 };
 
-// rotated element c of the row at element offset `row`
-__device__ float rotated(const kvq_rope_plan& P, const void* x, size_t row, int c, int pos, bool bf16) {
-  const float own = elem_to_f(x, row + c, bf16);
-  if (c >= P.rotary_dim) return own;
-  const int half = P.rotary_dim / 2;
-  const int i = P.interleaved ? c >> 1 : (c < half ? c : c - half);
-  const bool first = P.interleaved ? (c & 1) == 0 : c < half;
-  const int other = P.interleaved ? c ^ 1 : (first ? c + half : c - half);
-  const float2 cs = rope_cos_sin(pos, P.step[i], P.magnitude);
-  const float o = elem_to_f(x, row + other, bf16);
-  return first ? fmaf(own, cs.x, -o * cs.y) : fmaf(own, cs.x, o * cs.y);
+// A row of HD elements over a warp: lane holds E = HD / 32 neighbouring ones.  In fp32 pairs.
+template <int HD>
+struct Row {
+  static constexpr int E = HD / 32, W = E / 2;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const void* base, long long at, int lane) {
+    const unsigned short* p = static_cast<const unsigned short*>(base) + at + E * lane;
+    if constexpr (W == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void store(void* base, long long at, int lane) const {
+    unsigned short* p = static_cast<unsigned short*>(base) + at + E * lane;
+    if constexpr (W == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+};
+
+// Rotation of such rows at one token's position.  The other element of a pair is in the
+// same lane (INTERLEAVED), or a whole number of lanes away (LANES), or, when half of rotary_dim
+// is no multiple of E, anywhere (ELEMENTS).
+enum class Turn { NONE, INTERLEAVED, LANES, ELEMENTS };
+template <int HD, Turn TURN, bool BF16>
+struct Rotation {
+  static constexpr int E = HD / 32, W = E / 2;
+  int from[E], el[E];
+  float c[E], s[E];  // y = x c + other s (s carries the sign; elements not rotated: 1, 0)
+  __device__ __forceinline__ void set(const kvq_rope_plan& P, const int32_t* pos, int lane) {
+    if (TURN == Turn::NONE) return;
+    const int half = P.rotary_dim / 2, at = *pos;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int ch = E * lane + e;
+      const bool in = ch < P.rotary_dim, second = TURN == Turn::INTERLEAVED ? (e & 1) : ch >= half;
+      const int i = TURN == Turn::INTERLEAVED ? ch >> 1 : second ? ch - half : ch;
+      const int other = !in ? ch : second ? ch - half : ch + half;
+      from[e] = other / E, el[e] = other % E;
+      float2 cs = make_float2(1.f, 0.f);
+      if (TURN == Turn::INTERLEAVED && (e & 1)) cs = make_float2(c[e ^ 1], -s[e ^ 1]);
+      else if (in) cs = rope_cos_sin(at, P.step[i], P.magnitude);
+      c[e] = cs.x;
+      s[e] = second ? cs.y : -cs.y;
+    }
+  }
+  __device__ __forceinline__ void apply(const Row<HD>& r, float (&y)[E]) const {
+    float x[E], o[E];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float2 p = pair_to_f2(r.w[k], BF16);
+      x[2 * k] = p.x, x[2 * k + 1] = p.y;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = TURN == Turn::INTERLEAVED ? x[e ^ 1] : 0.f;
+    if (TURN == Turn::LANES) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float2 p = pair_to_f2(__shfl_sync(0xffffffffu, r.w[k], from[0]), BF16);
+        o[2 * k] = p.x, o[2 * k + 1] = p.y;
+      }
+    }
+    if (TURN == Turn::ELEMENTS) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          const float v = __shfl_sync(0xffffffffu, x[k], from[e]);
+          if (el[e] == k) o[e] = v;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = TURN == Turn::NONE ? x[e] : fmaf(x[e], c[e], o[e] * s[e]);
+  }
+};
+
+// Scale, offset and packed codes (4 bits each, from bit 0) of this lane's E elements; LANES =
+// 32 / E lanes share a group.  Codes are rint(d / |s|) for the IEEE quotient: they come from a
+// product with the reciprocal, and where the remainder d - code s shows that another code is as
+// near or nearer (a quotient at or next to a half), from the division itself.
+template <int HD>
+__device__ __forceinline__ uint32_t quantize(const float (&x)[HD / 32], float lo, float hi, bool down, __half& sh, __half& oh) {
+  constexpr int E = HD / 32;
+  constexpr float RND = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, ties to even
+  // elements beyond the binary16 range saturate to the first or the last code
+  lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+  oh = __float2half_rn(down ? hi : lo);
+  const float of = __half2float(oh);
+  sh = __float2half_ru(__fdiv_rn(fmaxf(down ? of - lo : hi - of, 0.f), 15.f));
+  const float sa = __half2float(sh), s = down ? -sa : sa;
+  const float inv = sa > 0.f ? __fdividef(1.f, 15.f * s) : 0.f;   // 15 |s| lies in [2^-21, 2^17]
+  float t[E];
+  bool check = false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float d = x[e] - of;
+    t[e] = fmaf(__saturatef(d * inv), 15.f, RND);   // bits: RND's plus the code
+    check = check || fabsf(fmaf(-(t[e] - RND), s, d)) >= 0.5f * sa;
+  }
+  if (check && sa > 0.f) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) t[e] = fminf(fmaxf(rintf(__fdiv_rn(x[e] - of, s)), 0.f), 15.f) + RND;
+  }
+  if (down) sh = __hneg(sh);
+  uint32_t code = __float_as_uint(t[0]);   // RND's bits lie above the codes' 16
+#pragma unroll
+  for (int e = 1; e < E; ++e) code += __float_as_uint(t[e]) << (4 * e);
+  return code;
 }
 
-// One warp per (token, head): KV heads first, then query heads; lane = channel of a group.
-template <int HD>
-__global__ void __launch_bounds__(128) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
+// One warp per item: a token's KV heads [h, h + a.per), with cos and sin formed once per item and the
+// rows of two heads on their way at once.  The blocks behind a.kv_blocks turn q, a thread per
+// V pairs.  HBM bound with q (32K tokens of 32 + 8 heads: 712 MB); without q the quantisation's
+// arithmetic, about 200 instructions per token and KV head, weighs as much as its bytes.
+constexpr int APPEND_THREADS = 128;
+template <int HD, Turn TURN, int V, bool BF16>
+__global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
   using L = Page<HD>;
-  const int lane = threadIdx.x & 31;
-  const long long n = (long long)a.T * (a.Hkv + a.Hq);
-  for (long long u = blockIdx.x * 4ll + (threadIdx.x >> 5); u < n; u += gridDim.x * 4ll) {
-    const long long t = u / (a.Hkv + a.Hq);
-    const int h = (int)(u - t * (a.Hkv + a.Hq));
-    const int pos = a.rotate ? a.pos[t] : 0;
-    if (h >= a.Hkv) {
-      const size_t in = (size_t)(t * a.qt + (h - a.Hkv) * a.qh), out = (size_t)(t * a.ot + (h - a.Hkv) * a.oh);
-      float y[L::G];
-      for (int g = 0; g < L::G; ++g) y[g] = rotated(P, a.q, in, 32 * g + lane, pos, a.bf16);
-      __syncwarp();   // q_out may be q: every lane has read before any writes
-      for (int g = 0; g < L::G; ++g) f_to_elem(a.q_out, out + 32 * g + lane, y[g], a.bf16);
-      continue;
-    }
+  constexpr int E = HD / 32, LANES = 32 / E, KU = 2;
+  pdl_trigger();
+  pdl_wait();
+  if (V > 0 && (int)blockIdx.x >= a.kv_blocks) {
+    rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16>(P, a.q, (long long)(blockIdx.x - a.kv_blocks) * APPEND_THREADS + threadIdx.x,
+                                                          (long long)(gridDim.x - a.kv_blocks) * APPEND_THREADS);
+    return;
+  }
+  const int lane = threadIdx.x & 31, g = lane / LANES, j = lane % LANES;
+  const int items = (a.Hkv + a.per - 1) / a.per;
+  const long long n = (long long)a.T * items;
+  for (long long u = blockIdx.x * (APPEND_THREADS / 32ll) + (threadIdx.x >> 5); u < n; u += a.kv_blocks * (APPEND_THREADS / 32ll)) {
+    const long long t = u / items;
     const int slot = a.slots[t];
     if (slot < 0 || slot / PG >= a.n_pages) continue;
-    unsigned char* page = a.pages + ((size_t)(slot / PG) * a.Hkv + h) * L::BYTES;
-    const int at = slot % PG;
-    for (int kv = 0; kv < 2; ++kv)
-      for (int g = 0; g < L::G; ++g) {
-        const int c = 32 * g + lane;
-        const size_t row = kv ? (size_t)(t * a.vt + h * a.vh) : (size_t)(t * a.kt + h * a.kh);
-        float x = kv || !a.rotate ? elem_to_f(kv ? a.v : a.k, row + c, a.bf16) : rotated(P, a.k, row, c, pos, a.bf16);
-        x = fminf(fmaxf(x, -65504.f), 65504.f);
-        const float hi = warp_max(x), lo = -warp_max(-x);
-        const bool down = kv && (at & 1);
-        const __half o = __float2half_rn(down ? hi : lo);
-        const float of = __half2float(o);
-        const __half s = __float2half_ru(__fdiv_rn(fmaxf(down ? of - lo : hi - of, 0.f), 15.f));
-        const float sf = __half2float(s), d = down ? of - x : x - of;
-        const int code = sf > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(d, sf)), 0.f), 15.f) : 0;
-        const int next = __shfl_down_sync(0xffffffffu, code, 1);
-        if ((lane & 1) == 0) {
-          if (kv) page[L::VC + vcode_at<HD>(at, (lane >> 2) * 2 * L::G + 2 * g + ((lane & 3) >> 1))] = code | (next << 4);
-          else page[at * L::ROW + (lane >> 3) * 4 * L::G + 4 * g + ((lane & 7) >> 1)] = code | (next << 4);
+    const int at = slot % PG, h0 = (int)(u - t * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
+    unsigned char* pg = a.pages + ((size_t)(slot / PG) * a.Hkv + h0) * L::BYTES;
+    // this lane's bytes of the codes, and its group's scale and offset (lane j = 0 writes)
+    const int kc = at * L::ROW + (E * j / 8) * 4 * L::G + 4 * g + (E * j % 8) / 2;
+    const int vc = L::VC + vcode_at<HD>(at, (E * j / 4) * 2 * L::G + 2 * g + (E * j % 4) / 2);
+    const int ks = L::KS + 2 * (at * L::G + g), vs = L::VS + 2 * (g * PG + vscale_at(at));
+    const bool down = at & 1;
+    long long ka = t * a.kt + h0 * a.kh, va = t * a.vt + h0 * a.vh;
+    Row<HD> rk[KU], rv[KU];
+    auto fetch = [&](int h) {
+#pragma unroll
+      for (int k = 0; k < KU; ++k) {
+        if (h + k < h1) {
+          rk[k].load(a.k, ka, lane);
+          rv[k].load(a.v, va, lane);
         }
-        if (lane == 0) {
-          const int e = kv ? g * PG + vscale_at(at) : at * L::G + g;
-          reinterpret_cast<__half*>(page + (kv ? L::VS : L::KS))[e] = down ? __hneg(s) : s;
-          reinterpret_cast<__half*>(page + (kv ? L::VO : L::KO))[e] = o;
-        }
+        ka += a.kh, va += a.vh;
       }
+    };
+    fetch(h0);
+    Rotation<HD, TURN, BF16> rot;
+    rot.set(P, a.pos + t, lane);
+    for (int h = h0; h < h1; h += KU) {
+      Row<HD> ck[KU], cv[KU];
+#pragma unroll
+      for (int k = 0; k < KU; ++k) ck[k] = rk[k], cv[k] = rv[k];
+      if (h + KU < h1) fetch(h + KU);
+#pragma unroll
+      for (int k = 0; k < KU; ++k) {
+        if (h + k >= h1) continue;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          float x[E];
+          if (kv) {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+              const float2 p = pair_to_f2(cv[k].w[i], BF16);
+              x[2 * i] = p.x, x[2 * i + 1] = p.y;
+            }
+          } else {
+            rot.apply(ck[k], x);
+          }
+          float lo = x[0], hi = x[0];
+#pragma unroll
+          for (int e = 1; e < E; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
+#pragma unroll
+          for (int o = 1; o < LANES; o <<= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+          }
+          __half s, o;
+          const uint32_t code = quantize<HD>(x, lo, hi, kv && down, s, o);
+          unsigned char* dst = pg + (kv ? vc : kc);
+          if (E == 4) *reinterpret_cast<unsigned short*>(dst) = (unsigned short)code;
+          else *dst = (unsigned char)code;
+          if (j == 0) {
+            *reinterpret_cast<__half*>(pg + (kv ? vs : ks)) = s;
+            *reinterpret_cast<__half*>(pg + (kv ? vs : ks) + L::SCALES) = o;
+          }
+        }
+        pg += L::BYTES;
+      }
+    }
   }
+}
+
+template <int HD, bool BF16>
+auto append_kernel_of(const kvq_rope_plan* plan, bool q) {
+  using K = void (*)(kvq_rope_plan, AppendPagedArgs);
+  if (!plan) return (K)paged_append_kernel<HD, Turn::NONE, 0, BF16>;
+  const bool wide = q && rope_pairs(*plan) == 8;
+  if (plan->interleaved)
+    return wide ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 1, BF16>;
+  if (plan->rotary_dim / 2 % (HD / 32) == 0)
+    return wide ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16> : (K)paged_append_kernel<HD, Turn::LANES, HD / 32, BF16>;
+  return (K)paged_append_kernel<HD, Turn::ELEMENTS, 1, BF16>;
+}
+
+// Pairs per thread with which that kernel turns q.
+int append_pairs(const kvq_rope_plan& plan) {
+  if (rope_pairs(plan) == 8) return 8;
+  return plan.interleaved || plan.rotary_dim / 2 % (plan.head_dim / 32) != 0 ? 1 : plan.head_dim / 32;
 }
 
 struct GatherArgs {
@@ -93,38 +251,65 @@ struct GatherArgs {
   const int32_t* slots;
   void *k, *v;
   long long kt, kh, vt, vh;
-  int T, Hkv, n_pages;
-  bool bf16;
+  int T, Hkv, n_pages, per;   // per: heads of one item
 };
 
-// One thread per element.
-template <int HD>
-__global__ void __launch_bounds__(256) paged_gather_kernel(GatherArgs a) {
+// One warp per item of a token's heads [h, h + a.per): half of the lanes read keys, half values, eight
+// channels each (one 16-byte store); at head_dim 64 a warp takes two heads at once.  HBM bound.
+constexpr int GATHER_THREADS = 128;
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs a) {
   using L = Page<HD>;
-  const long long n = (long long)a.T * a.Hkv * HD;
-  for (long long u = blockIdx.x * 256ll + threadIdx.x; u < n; u += gridDim.x * 256ll) {
-    const int c = (int)(u % HD), g = c / 32, j = c % 32;
-    const long long row = u / HD, t = row / a.Hkv, h = row - t * a.Hkv;
+  constexpr int LANES = HD / 8, HEADS = 32 / (2 * LANES), U = 4;   // lanes of a row, heads at once, steps on their way
+  const int lane = threadIdx.x & 31, sub = lane % LANES, kv = (lane / LANES) & 1, hh = lane / (2 * LANES);
+  const int g = sub / 4, piece = sub % 4;   // channels 32g + 8 piece
+  const int items = (a.Hkv + a.per - 1) / a.per;
+  const long long n = (long long)a.T * items;
+  pdl_trigger();
+  pdl_wait();
+  for (long long u = blockIdx.x * (GATHER_THREADS / 32ll) + (threadIdx.x >> 5); u < n; u += gridDim.x * (GATHER_THREADS / 32ll)) {
+    const long long t = u / items;
+    const int h0 = (int)(u - t * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
     const int slot = a.slots[t];
-    float k = 0.f, v = 0.f;
-    if (slot >= 0 && slot / PG < a.n_pages) {
-      const unsigned char* page = a.pages + ((size_t)(slot / PG) * a.Hkv + h) * L::BYTES;
-      const int at = slot % PG;
-      const int kb = page[at * L::ROW + (j >> 3) * 4 * L::G + 4 * g + ((j & 7) >> 1)];
-      const int vb = page[L::VC + vcode_at<HD>(at, (j >> 2) * 2 * L::G + 2 * g + ((j & 3) >> 1))];
-      const int ke = at * L::G + g, ve = g * PG + vscale_at(at), sh = 4 * (c & 1);
-      auto h16 = [&](int off, int e) { return __half2float(reinterpret_cast<const __half*>(page + off)[e]); };
-      k = fmaf((float)((kb >> sh) & 15), h16(L::KS, ke), h16(L::KO, ke));
-      v = fmaf((float)((vb >> sh) & 15), h16(L::VS, ve), h16(L::VO, ve));
+    const bool held = slot >= 0 && slot / PG < a.n_pages;
+    const int at = held ? slot % PG : 0;
+    const unsigned char* page = a.pages + (held ? (size_t)(slot / PG) * a.Hkv * L::BYTES : 0);
+    const int c0 = kv ? L::VC + vcode_at<HD>(at, 2 * piece * 2 * L::G + 2 * g) : at * L::ROW + piece * 4 * L::G + 4 * g;
+    const int c1 = kv ? L::VC + vcode_at<HD>(at, (2 * piece + 1) * 2 * L::G + 2 * g) : c0 + 2;
+    const int sc = kv ? L::VS + 2 * (g * PG + vscale_at(at)) : L::KS + 2 * (at * L::G + g);
+    unsigned short* out = static_cast<unsigned short*>(kv ? a.v : a.k) + t * (kv ? a.vt : a.kt) + 8 * sub;
+    const long long oh = kv ? a.vh : a.kh;
+    for (int h = h0 + hh; h < h1; h += U * HEADS) {
+      uint32_t code[U];
+      __half s[U], o[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        code[k] = 0u, s[k] = o[k] = __ushort_as_half(0);
+        if (held && h + k * HEADS < h1) {
+          const unsigned char* pg = page + (size_t)(h + k * HEADS) * L::BYTES;
+          code[k] = *reinterpret_cast<const unsigned short*>(pg + c0) | ((uint32_t)*reinterpret_cast<const unsigned short*>(pg + c1) << 16);
+          s[k] = *reinterpret_cast<const __half*>(pg + sc);
+          o[k] = *reinterpret_cast<const __half*>(pg + sc + L::SCALES);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (h + k * HEADS >= h1) continue;
+        const float sf = __half2float(s[k]), of = __half2float(o[k]);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = f2_to_pair(fmaf((float)((code[k] >> (8 * i)) & 15u), sf, of), fmaf((float)((code[k] >> (8 * i + 4)) & 15u), sf, of), BF16);
+        *reinterpret_cast<uint4*>(out + (h + k * HEADS) * oh) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    f_to_elem(a.k, (size_t)(t * a.kt + h * a.kh) + c, k, a.bf16);
-    f_to_elem(a.v, (size_t)(t * a.vt + h * a.vh) + c, v, a.bf16);
   }
 }
 
-constexpr int MAX_GRID = 152 * 64;
-
-int grid_of(long long blocks) { return (int)(blocks < MAX_GRID ? blocks : MAX_GRID); }
+// Heads per item: few while the call does not fill the GPU, eight when it does.
+int heads_per_item(long long T, int H) {
+  return (int)std::min<long long>(8, std::max<long long>(1, T * H / (152 * 32)));   // 32 warps per SM
+}
 
 // checks shared by append and gather
 kvq_status check_common(const char* fn, int dtype, int T, int Hkv, int hd, int n_pages) {
@@ -169,15 +354,22 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
     if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
     if (kvq_status s = check_buffer(q_out, dev, 16, fn, "q_out")) return s;
   }
-  AppendPagedArgs a{k,  v,  q,  q_out, slots, positions, static_cast<unsigned char*>(pages),
-                    kt, kh, vt, vh,    qt,    qh,        ot, oh, T, Hkv, q ? Hq : 0, n_pages,
-                    dtype == KVQ_BF16, plan != nullptr};
+  AppendPagedArgs a{k, v, slots, positions, static_cast<unsigned char*>(pages), kt, kh, vt, vh, T, Hkv, n_pages, heads_per_item(T, Hkv), 0, {}};
+  const long long items = (long long)T * ((Hkv + a.per - 1) / a.per);
+  long long blocks = std::min<long long>((items + 3) / 4, 1 << 29);
+  a.kv_blocks = (int)blocks;
+  if (q) {
+    const int chunks = plan->rotary_dim / 2 / append_pairs(*plan);
+    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, rope_lanes(T, Hq, chunks), q != q_out && plan->rotary_dim < hd};
+    blocks += std::min<long long>(((long long)T * a.q.lanes * chunks + APPEND_THREADS - 1) / APPEND_THREADS, 1 << 29);
+  }
+  const bool bf16 = dtype == KVQ_BF16;
+  auto* kern = hd == 128 ? (bf16 ? append_kernel_of<128, true>(plan, q) : append_kernel_of<128, false>(plan, q))
+                         : (bf16 ? append_kernel_of<64, true>(plan, q) : append_kernel_of<64, false>(plan, q));
   kvq_rope_plan none = {};
-  const int grid = grid_of(((long long)T * (Hkv + a.Hq) + 3) / 4);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (hd == 128) paged_append_kernel<128><<<grid, 128, 0, st>>>(plan ? *plan : none, a);
-  else paged_append_kernel<64><<<grid, 128, 0, st>>>(plan ? *plan : none, a);
-  if (cudaError_t e = cudaGetLastError()) return paged_cuda_fail(e, fn, "launch");
+  cudaError_t e = launch_dependent(kern, dim3((unsigned)blocks), dim3(APPEND_THREADS), 0, static_cast<cudaStream_t>(stream),
+                                   plan ? *plan : none, a);
+  if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
 
@@ -196,12 +388,13 @@ kvq_status gather_impl(const void* pages, int n_pages, const int32_t* slots, int
   if (kvq_status s = check_buffer(slots, dev, 4, fn, "slots")) return s;
   if (kvq_status s = check_buffer(k, dev, 16, fn, "k")) return s;
   if (kvq_status s = check_buffer(v, dev, 16, fn, "v")) return s;
-  GatherArgs a{static_cast<const unsigned char*>(pages), slots, k, v, kt, kh, vt, vh, T, Hkv, n_pages, dtype == KVQ_BF16};
-  const int grid = grid_of(((long long)T * Hkv * hd + 255) / 256);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (hd == 128) paged_gather_kernel<128><<<grid, 256, 0, st>>>(a);
-  else paged_gather_kernel<64><<<grid, 256, 0, st>>>(a);
-  if (cudaError_t e = cudaGetLastError()) return paged_cuda_fail(e, fn, "launch");
+  GatherArgs a{static_cast<const unsigned char*>(pages), slots, k, v, kt, kh, vt, vh, T, Hkv, n_pages, heads_per_item(T, Hkv)};
+  const long long items = (long long)T * ((Hkv + a.per - 1) / a.per);
+  const dim3 grid((unsigned)std::min<long long>((items + 3) / 4, 1 << 30));
+  auto* kern = hd == 128 ? (dtype == KVQ_BF16 ? paged_gather_kernel<128, true> : paged_gather_kernel<128, false>)
+                         : (dtype == KVQ_BF16 ? paged_gather_kernel<64, true> : paged_gather_kernel<64, false>);
+  cudaError_t e = launch_dependent(kern, grid, dim3(GATHER_THREADS), 0, static_cast<cudaStream_t>(stream), a);
+  if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
 

@@ -4,12 +4,14 @@
 // The plan holds w_i / (2 pi) as a 64-bit fraction of a turn, so p w_i modulo one turn is an
 // integer product without rounding (rope_cos_sin): a position of 2 million costs no
 // accuracy, which an fp32 product of position and frequency would.
+#include <algorithm>
 #include <cmath>
 #include <string>
 
 #include "kvq.h"
 #include "kvq_launch.h"
 #include "kvq_paged.cuh"
+#include "kvq_rope.cuh"
 
 namespace kvq {
 
@@ -56,35 +58,19 @@ kvq_status check_plan(const kvq_rope_plan* plan, int head_dim, const char* fn) {
 
 namespace {
 
-struct RopeArgs {
-  const void* x;
-  void* out;
-  const int32_t* pos;
-  long long xt, xh, ot, oh;   // strides in elements
-  int T, H;
-  bool bf16;
-};
+constexpr int ROPE_THREADS = 256;
 
-// One thread per element pair (or copied element) of one row.
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ kvq_rope_plan P, RopeArgs a) {
-  const int half = P.rotary_dim / 2, units = half + (P.head_dim - P.rotary_dim);
-  const long long n = (long long)a.T * a.H * units;
-  for (long long u = blockIdx.x * 256ll + threadIdx.x; u < n; u += gridDim.x * 256ll) {
-    const long long row = u / units;
-    const int i = (int)(u - row * units);
-    const long long t = row / a.H, h = row - t * a.H;
-    const size_t xo = (size_t)(t * a.xt + h * a.xh), oo = (size_t)(t * a.ot + h * a.oh);
-    if (i >= half) {
-      const int c = P.rotary_dim + (i - half);
-      f_to_elem(a.out, oo + c, elem_to_f(a.x, xo + c, a.bf16), a.bf16);
-      continue;
-    }
-    const int c0 = P.interleaved ? 2 * i : i, c1 = P.interleaved ? 2 * i + 1 : i + half;
-    const float2 cs = rope_cos_sin(a.pos[t], P.step[i], P.magnitude);
-    const float x0 = elem_to_f(a.x, xo + c0, a.bf16), x1 = elem_to_f(a.x, xo + c1, a.bf16);
-    f_to_elem(a.out, oo + c0, fmaf(x0, cs.x, -x1 * cs.y), a.bf16);
-    f_to_elem(a.out, oo + c1, fmaf(x1, cs.x, x0 * cs.y), a.bf16);
-  }
+template <int V, bool INTERLEAVED, bool BF16>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ kvq_rope_plan P, RopeArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  rope_part<V, INTERLEAVED, BF16>(P, a, blockIdx.x * (long long)ROPE_THREADS + threadIdx.x, (long long)gridDim.x * ROPE_THREADS);
+}
+
+template <bool INTERLEAVED, bool BF16>
+auto rope_kernel_of(int V) {
+  return V == 8 ? rope_kernel<8, INTERLEAVED, BF16> : V == 4 ? rope_kernel<4, INTERLEAVED, BF16>
+         : V == 2 ? rope_kernel<2, INTERLEAVED, BF16> : rope_kernel<1, INTERLEAVED, BF16>;
 }
 
 kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_t xt, int64_t xh,
@@ -104,11 +90,15 @@ kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_
   if (kvq_status s = check_buffer(x, dev, 16, fn, "x")) return s;
   if (kvq_status s = check_buffer(out, dev, 16, fn, "out")) return s;
   if (kvq_status s = check_buffer(positions, dev, 4, fn, "positions")) return s;
-  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, dtype == KVQ_BF16};
-  const long long n = (long long)T * H * (plan->head_dim - plan->rotary_dim / 2);
-  const int grid = (int)((n + 255) / 256 < 152 * 64 ? (n + 255) / 256 : 152 * 64);
-  rope_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(*plan, a);
-  if (cudaError_t e = cudaGetLastError()) return paged_cuda_fail(e, fn, "launch");
+  const int V = rope_pairs(*plan), chunks = plan->rotary_dim / 2 / V;
+  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, rope_lanes(T, H, chunks), x != out && plan->rotary_dim < plan->head_dim};
+  const long long blocks = ((long long)T * a.lanes * chunks + ROPE_THREADS - 1) / ROPE_THREADS;
+  const bool bf16 = dtype == KVQ_BF16;
+  auto* k = plan->interleaved ? (bf16 ? rope_kernel_of<true, true>(V) : rope_kernel_of<true, false>(V))
+                              : (bf16 ? rope_kernel_of<false, true>(V) : rope_kernel_of<false, false>(V));
+  const dim3 grid((unsigned)std::min<long long>(blocks, 1 << 30));
+  const cudaError_t e = launch_dependent(k, grid, dim3(ROPE_THREADS), 0, static_cast<cudaStream_t>(stream), *plan, a);
+  if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
 
