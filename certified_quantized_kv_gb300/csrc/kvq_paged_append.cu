@@ -24,7 +24,7 @@ struct AppendPagedArgs {
   unsigned char* pages;
   long long kt, kh, vt, vh;   // strides in elements
   int T, Hkv, n_pages, per;   // per: KV heads of one item
-  int kv_blocks;              // the blocks behind these turn q
+  int kv_blocks;              // the other blocks turn q
   RopeArgs q;
 };
 
@@ -33,19 +33,13 @@ template <int HD>
 struct Row {
   static constexpr int E = HD / 32, W = E / 2;
   uint32_t w[W];
-  __device__ __forceinline__ void load(const void* base, long long at, int lane) {
-    const unsigned short* p = static_cast<const unsigned short*>(base) + at + E * lane;
+  __device__ __forceinline__ void load(const unsigned short* p) {   // this lane's elements
     if constexpr (W == 2) {
       const uint2 v = *reinterpret_cast<const uint2*>(p);
       w[0] = v.x, w[1] = v.y;
     } else {
       w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
-  }
-  __device__ __forceinline__ void store(void* base, long long at, int lane) const {
-    unsigned short* p = static_cast<unsigned short*>(base) + at + E * lane;
-    if constexpr (W == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(p) = w[0];
   }
 };
 
@@ -105,32 +99,41 @@ struct Rotation {
   }
 };
 
-// Scale, offset and packed codes (4 bits each, from bit 0) of this lane's E elements; LANES =
-// 32 / E lanes share a group.  Codes are rint(d / |s|) for the IEEE quotient: they come from a
-// product with the reciprocal, and where the remainder d - code s shows that another code is as
-// near or nearer (a quotient at or next to a half), from the division itself.
-template <int HD>
+// Scale, offset and packed codes (4 bits each, from bit 0) of this lane's E elements of a group
+// with extremes lo and hi.  The scale is the smallest binary16 h with 15 h >= the span (15 h is
+// exact in fp32), which is the span / 15 rounded up.  Codes are rint(d / |s|) for the exact
+// quotient: they come from a product with the reciprocal, and the remainder d - code s, exact
+// near a half, tells where a neighbour is nearer, or as near and even (values on the binary16
+// grid meet exact halves in about one element of a hundred).
+template <int HD, bool CLAMP>
 __device__ __forceinline__ uint32_t quantize(const float (&x)[HD / 32], float lo, float hi, bool down, __half& sh, __half& oh) {
   constexpr int E = HD / 32;
   constexpr float RND = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, ties to even
   // elements beyond the binary16 range saturate to the first or the last code
-  lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+  if (CLAMP) lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
   oh = __float2half_rn(down ? hi : lo);
-  const float of = __half2float(oh);
-  sh = __float2half_ru(__fdiv_rn(fmaxf(down ? of - lo : hi - of, 0.f), 15.f));
-  const float sa = __half2float(sh), s = down ? -sa : sa;
+  const float of = __half2float(oh), span = fmaxf(down ? of - lo : hi - of, 0.f);
+  const unsigned short h = __half_as_ushort(__float2half_ru(span * 0.06666667f));
+  const float sh1 = __half2float(__ushort_as_half(h)), sh0 = __half2float(__ushort_as_half((unsigned short)(h - 1)));
+  const int step = 15.f * sh0 >= span ? -1 : 15.f * sh1 < span ? 1 : 0;   // (h = 0: sh0 is a NaN)
+  sh = __ushort_as_half((unsigned short)(h + step));
+  const float sa = __half2float(sh), s = down ? -sa : sa, half = 0.5f * sa;
   const float inv = sa > 0.f ? __fdividef(1.f, 15.f * s) : 0.f;   // 15 |s| lies in [2^-21, 2^17]
-  float t[E];
-  bool check = false;
+  float t[E], r[E], worst = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const float d = x[e] - of;
     t[e] = fmaf(__saturatef(d * inv), 15.f, RND);   // bits: RND's plus the code
-    check = check || fabsf(fmaf(-(t[e] - RND), s, d)) >= 0.5f * sa;
+    r[e] = fmaf(-(t[e] - RND), s, d);
+    worst = fmaxf(worst, fabsf(r[e]));
   }
-  if (check && sa > 0.f) {
+  if (worst >= half) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) t[e] = fminf(fmaxf(rintf(__fdiv_rn(x[e] - of, s)), 0.f), 15.f) + RND;
+    for (int e = 0; e < E; ++e) {
+      const bool off = fabsf(r[e]) > half || (fabsf(r[e]) == half && (__float_as_uint(t[e]) & 1u));
+      const float to = t[e] + ((r[e] < 0.f) == down ? 1.f : -1.f);
+      t[e] = off && sa > 0.f ? fminf(fmaxf(to, RND), RND + 15.f) : t[e];
+    }
   }
   if (down) sh = __hneg(sh);
   uint32_t code = __float_as_uint(t[0]);   // RND's bits lie above the codes' 16
@@ -140,55 +143,53 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[HD / 32], float lo
 }
 
 // One warp per item: a token's KV heads [h, h + a.per), with cos and sin formed once per item and the
-// rows of two heads on their way at once.  The blocks behind a.kv_blocks turn q, a thread per
-// V pairs.  HBM bound with q (32K tokens of 32 + 8 heads: 712 MB); without q the quantisation's
-// arithmetic, about 200 instructions per token and KV head, weighs as much as its bytes.
+// rows of two heads on their way at once.  The other blocks turn q, a thread per V pairs; the two
+// kinds are spread over the grid in turn, since the first are bound by their arithmetic (about 280
+// instructions per token and KV head) and the second by HBM: 32K tokens of 32 + 8 heads 140 us so,
+// 172 with one kind behind the other.  Eight blocks per SM (64 registers): 140 us; six without
+// the bound, 161; ten, 170.
 constexpr int APPEND_THREADS = 128;
 template <int HD, Turn TURN, int V, bool BF16>
-__global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
+__global__ void __launch_bounds__(APPEND_THREADS, 8) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
   using L = Page<HD>;
   constexpr int E = HD / 32, LANES = 32 / E, KU = 2;
   pdl_trigger();
   pdl_wait();
-  if (V > 0 && (int)blockIdx.x >= a.kv_blocks) {
-    rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16>(P, a.q, (long long)(blockIdx.x - a.kv_blocks) * APPEND_THREADS + threadIdx.x,
+  // block b is KV block number floor(b kv / all) when that number changes behind it
+  const int k0 = (int)((long long)blockIdx.x * a.kv_blocks / gridDim.x), k1 = (int)((blockIdx.x + 1ll) * a.kv_blocks / gridDim.x);
+  if (V > 0 && k0 == k1) {
+    rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16>(P, a.q, (long long)(blockIdx.x - k0) * APPEND_THREADS + threadIdx.x,
                                                           (long long)(gridDim.x - a.kv_blocks) * APPEND_THREADS);
     return;
   }
   const int lane = threadIdx.x & 31, g = lane / LANES, j = lane % LANES;
   const int items = (a.Hkv + a.per - 1) / a.per;
   const long long n = (long long)a.T * items;
-  for (long long u = blockIdx.x * (APPEND_THREADS / 32ll) + (threadIdx.x >> 5); u < n; u += a.kv_blocks * (APPEND_THREADS / 32ll)) {
+  for (long long u = k0 * (APPEND_THREADS / 32ll) + (threadIdx.x >> 5); u < n; u += a.kv_blocks * (APPEND_THREADS / 32ll)) {
     const long long t = u / items;
     const int slot = a.slots[t];
     if (slot < 0 || slot / PG >= a.n_pages) continue;
     const int at = slot % PG, h0 = (int)(u - t * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
-    unsigned char* pg = a.pages + ((size_t)(slot / PG) * a.Hkv + h0) * L::BYTES;
-    // this lane's bytes of the codes, and its group's scale and offset (lane j = 0 writes)
-    const int kc = at * L::ROW + (E * j / 8) * 4 * L::G + 4 * g + (E * j % 8) / 2;
-    const int vc = L::VC + vcode_at<HD>(at, (E * j / 4) * 2 * L::G + 2 * g + (E * j % 4) / 2);
-    const int ks = L::KS + 2 * (at * L::G + g), vs = L::VS + 2 * (g * PG + vscale_at(at));
     const bool down = at & 1;
-    long long ka = t * a.kt + h0 * a.kh, va = t * a.vt + h0 * a.vh;
-    Row<HD> rk[KU], rv[KU];
-    auto fetch = [&](int h) {
-#pragma unroll
-      for (int k = 0; k < KU; ++k) {
-        if (h + k < h1) {
-          rk[k].load(a.k, ka, lane);
-          rv[k].load(a.v, va, lane);
-        }
-        ka += a.kh, va += a.vh;
-      }
-    };
-    fetch(h0);
+    const unsigned short* kp = static_cast<const unsigned short*>(a.k) + t * a.kt + h0 * a.kh + E * lane;
+    const unsigned short* vp = static_cast<const unsigned short*>(a.v) + t * a.vt + h0 * a.vh + E * lane;
+    // this lane's bytes of the codes, and its group's scale and offset (lane j = 0 writes)
+    unsigned char* pg = a.pages + ((size_t)(slot / PG) * a.Hkv + h0) * L::BYTES;
+    unsigned char* kc = pg + at * L::ROW + (E * j / 8) * 4 * L::G + 4 * g + (E * j % 8) / 2;
+    unsigned char* vc = pg + L::VC + vcode_at<HD>(at, (E * j / 4) * 2 * L::G + 2 * g + (E * j % 4) / 2);
+    __half* ks = reinterpret_cast<__half*>(pg + L::KS) + at * L::G + g;
+    __half* vs = reinterpret_cast<__half*>(pg + L::VS) + g * PG + vscale_at(at);
     Rotation<HD, TURN, BF16> rot;
-    rot.set(P, a.pos + t, lane);
     for (int h = h0; h < h1; h += KU) {
-      Row<HD> ck[KU], cv[KU];
+      Row<HD> rk[KU], rv[KU];
 #pragma unroll
-      for (int k = 0; k < KU; ++k) ck[k] = rk[k], cv[k] = rv[k];
-      if (h + KU < h1) fetch(h + KU);
+      for (int k = 0; k < KU; ++k)
+        if (h + k < h1) {
+          rk[k].load(kp);
+          rv[k].load(vp);
+          kp += a.kh, vp += a.vh;
+        }
+      if (h == h0) rot.set(P, a.pos + t, lane);
 #pragma unroll
       for (int k = 0; k < KU; ++k) {
         if (h + k >= h1) continue;
@@ -198,11 +199,11 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
           if (kv) {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) {
-              const float2 p = pair_to_f2(cv[k].w[i], BF16);
+              const float2 p = pair_to_f2(rv[k].w[i], BF16);
               x[2 * i] = p.x, x[2 * i + 1] = p.y;
             }
           } else {
-            rot.apply(ck[k], x);
+            rot.apply(rk[k], x);
           }
           float lo = x[0], hi = x[0];
 #pragma unroll
@@ -213,17 +214,19 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
           }
           __half s, o;
-          const uint32_t code = quantize<HD>(x, lo, hi, kv && down, s, o);
-          unsigned char* dst = pg + (kv ? vc : kc);
+          const uint32_t code = kv ? quantize<HD, BF16>(x, lo, hi, down, s, o)
+                                   : quantize<HD, BF16 || TURN != Turn::NONE>(x, lo, hi, false, s, o);
+          unsigned char* dst = (kv ? vc : kc) + k * L::BYTES;
           if (E == 4) *reinterpret_cast<unsigned short*>(dst) = (unsigned short)code;
           else *dst = (unsigned char)code;
           if (j == 0) {
-            *reinterpret_cast<__half*>(pg + (kv ? vs : ks)) = s;
-            *reinterpret_cast<__half*>(pg + (kv ? vs : ks) + L::SCALES) = o;
+            __half* so = (kv ? vs : ks) + k * (L::BYTES / 2);
+            so[0] = s;
+            so[L::SCALES / 2] = o;
           }
         }
-        pg += L::BYTES;
       }
+      kc += KU * L::BYTES, vc += KU * L::BYTES, ks += KU * L::BYTES / 2, vs += KU * L::BYTES / 2;
     }
   }
 }
@@ -273,34 +276,42 @@ __global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs
     const int slot = a.slots[t];
     const bool held = slot >= 0 && slot / PG < a.n_pages;
     const int at = held ? slot % PG : 0;
-    const unsigned char* page = a.pages + (held ? (size_t)(slot / PG) * a.Hkv * L::BYTES : 0);
-    const int c0 = kv ? L::VC + vcode_at<HD>(at, 2 * piece * 2 * L::G + 2 * g) : at * L::ROW + piece * 4 * L::G + 4 * g;
-    const int c1 = kv ? L::VC + vcode_at<HD>(at, (2 * piece + 1) * 2 * L::G + 2 * g) : c0 + 2;
-    const int sc = kv ? L::VS + 2 * (g * PG + vscale_at(at)) : L::KS + 2 * (at * L::G + g);
-    unsigned short* out = static_cast<unsigned short*>(kv ? a.v : a.k) + t * (kv ? a.vt : a.kt) + 8 * sub;
-    const long long oh = kv ? a.vh : a.kh;
-    for (int h = h0 + hh; h < h1; h += U * HEADS) {
+    const int h_ = h0 + hh;
+    const unsigned char* pg = a.pages + ((held ? (size_t)(slot / PG) * a.Hkv : 0) + h_) * L::BYTES;
+    const unsigned char* c0 = pg + (kv ? L::VC + vcode_at<HD>(at, 2 * piece * 2 * L::G + 2 * g) : at * L::ROW + piece * 4 * L::G + 4 * g);
+    const unsigned char* c1 = kv ? pg + L::VC + vcode_at<HD>(at, (2 * piece + 1) * 2 * L::G + 2 * g) : c0 + 2;
+    const __half* sc = reinterpret_cast<const __half*>(pg + (kv ? L::VS + 2 * (g * PG + vscale_at(at)) : L::KS + 2 * (at * L::G + g)));
+    const long long step = HEADS * (kv ? a.vh : a.kh);
+    unsigned short* out = static_cast<unsigned short*>(kv ? a.v : a.k) + t * (kv ? a.vt : a.kt) + h_ * (kv ? a.vh : a.kh) + 8 * sub;
+    for (int h = h_; h < h1; h += U * HEADS) {
       uint32_t code[U];
       __half s[U], o[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         code[k] = 0u, s[k] = o[k] = __ushort_as_half(0);
         if (held && h + k * HEADS < h1) {
-          const unsigned char* pg = page + (size_t)(h + k * HEADS) * L::BYTES;
-          code[k] = *reinterpret_cast<const unsigned short*>(pg + c0) | ((uint32_t)*reinterpret_cast<const unsigned short*>(pg + c1) << 16);
-          s[k] = *reinterpret_cast<const __half*>(pg + sc);
-          o[k] = *reinterpret_cast<const __half*>(pg + sc + L::SCALES);
+          constexpr int NEXT = HEADS * L::BYTES;
+          code[k] = __byte_perm(*reinterpret_cast<const unsigned short*>(c0 + k * NEXT),
+                                *reinterpret_cast<const unsigned short*>(c1 + k * NEXT), 0x5410);
+          s[k] = sc[k * (NEXT / 2)];
+          o[k] = sc[k * (NEXT / 2) + L::SCALES / 2];
         }
       }
+      c0 += U * HEADS * L::BYTES, c1 += U * HEADS * L::BYTES, sc += U * HEADS * L::BYTES / 2;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         if (h + k * HEADS >= h1) continue;
         const float sf = __half2float(s[k]), of = __half2float(o[k]);
         uint32_t w[4];
+        // 2^23 + code as a float's bits, less 2^23
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = f2_to_pair(fmaf((float)((code[k] >> (8 * i)) & 15u), sf, of), fmaf((float)((code[k] >> (8 * i + 4)) & 15u), sf, of), BF16);
-        *reinterpret_cast<uint4*>(out + (h + k * HEADS) * oh) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; ++i) {
+          const float n0 = __uint_as_float(((code[k] >> (8 * i)) & 15u) | 0x4B000000u) - 8388608.f;
+          const float n1 = __uint_as_float(((code[k] >> (8 * i + 4)) & 15u) | 0x4B000000u) - 8388608.f;
+          w[i] = f2_to_pair(fmaf(n0, sf, of), fmaf(n1, sf, of), BF16);
+        }
+        *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+        out += step;
       }
     }
   }
