@@ -37,19 +37,10 @@ namespace kvq {
 
 namespace {
 
-#ifndef PASTEP1
-#define PASTEP1 4
-#endif
-#ifndef PASTEP2
-#define PASTEP2 2
-#endif
 constexpr int PA_WARPS = 8;
 constexpr int PA_STAGES = 2;
 constexpr int PA_THREADS = 32 * PA_WARPS;
-#ifndef PALEAD
-#define PALEAD 2
-#endif
-constexpr int PA_LEAD = PALEAD;
+constexpr int PA_LEAD = 2;
 constexpr float PA_TOP = 14.f;                              // weights are 2^14 at most,
 constexpr float PA_SLACK = 4.f;                             // 2^10 when their reference is set
 constexpr unsigned long long PA_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
@@ -157,73 +148,104 @@ struct PaStage {
   static constexpr int FLOATS = 8 * (HD + 4) + 8 * (HD / 32) + 16;   // a multiple of 4
 };
 
-// Four channels of one row of the output: v / lt, and the row's lse.
-template <int HD>
-__device__ __forceinline__ void pa_store_row(const PaArgs& a, int b, int g, int r, int x, float4 v, float ref, float lt) {
-  const int qi = r / a.n_rep;
-  const size_t row = ((size_t)b * a.Q + qi) * a.Hq + g * a.n_rep + (r - qi * a.n_rep);
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  reinterpret_cast<uint2*>(a.out)[row * (HD / 4) + x] =
-      make_uint2(f2_to_pair(v.x * inv, v.y * inv, a.bf16), f2_to_pair(v.z * inv, v.w * inv, a.bf16));
-  if (x == 0 && a.lse) a.lse[row] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
-}
+// Where rows of the output go.
+struct PaOut {
+  void* out;
+  float* lse;
+  int Q, Hq, n_rep;
+  bool bf16;
+  // row of the output of row r of (sequence b, KV head g)
+  __device__ __forceinline__ size_t row(int b, int g, int r) const {
+    const int qi = n_rep == 1 ? r : r / n_rep;
+    return ((size_t)b * Q + qi) * Hq + g * n_rep + (r - qi * n_rep);
+  }
+  // four channels of a row: v / lt, and its lse
+  template <int HD>
+  __device__ __forceinline__ void store(size_t row, int x, float4 v, float ref, float lt) const {
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    reinterpret_cast<uint2*>(out)[row * (HD / 4) + x] = make_uint2(f2_to_pair(v.x * inv, v.y * inv, bf16), f2_to_pair(v.z * inv, v.w * inv, bf16));
+    if (x == 0 && lse) lse[row] = lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994531f;
+  }
+};
+
+// Pieces added up: reference M, weight sum L and four channels' sums o.
+struct PaSum {
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N]) {   // (reference, weight sum), sums
+    float to = M;
+#pragma unroll
+    for (int i = 0; i < N; ++i) to = fmaxf(to, ml[i].x);
+    const float f = M == to ? 1.f : exp2_approx(M - to);   // (both -inf: nothing seen yet)
+    M = to;
+    L *= f;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float w = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - to);
+      L = fmaf(ml[i].y, w, L);
+      o.x = fmaf(v[i].x, w, o.x), o.y = fmaf(v[i].y, w, o.y), o.z = fmaf(v[i].z, w, o.z), o.w = fmaf(v[i].w, w, o.w);
+    }
+  }
+};
 
 // The sum of n pieces of group grp in order, by the whole CTA (KS threads share a sum): into
-// dst, or as output rows.  The pieces are those of the CTAs from `across` on (the first one
-// in its second slot, the others in their first), or, when that is null, of the warps from
-// *at on (the last one an ended piece when `closed`).  Not inlined: its registers and its
-// schedule stay out of the page loop's, and the second use finds its instructions cached.
-template <int HD, int R>
-__device__ __noinline__ void pa_merge(const PaArgs& a, const float* const* at, const float* across, int n, bool closed,
-                                      int2 grp, float* dst) {
+// dst, or as output rows.  ACROSS: the pieces of the CTAs from *at on, the first one's second
+// slot and the others' first; else those of warps, at their pointers from `at` on, the last
+// one an ended piece when `closed`.  Not inlined: its registers and its schedule stay out of
+// the page loop's.  Loads are not predicated (the last piece is read again in place of those
+// behind it), so that a batch of them is on its way at once.
+template <int HD, int R, bool ACROSS>
+__device__ __noinline__ void pa_merge(PaOut po, const float* const* at, int n, bool closed, int b, int g, int r0, int rn, float* dst) {
   constexpr int PART = R * (HD + 2), VEC = R * HD / 4, KS = PA_THREADS / VEC > 1 ? PA_THREADS / VEC : 1;
-#ifndef PABATCH
-#define PABATCH 10
-#endif
-  constexpr int BATCH = PABATCH;   // pieces on their way at once
+  constexpr int BATCH = 5;
   __shared__ float4 red[KS > 1 ? PA_THREADS : 1];
   __shared__ float2 redm[KS > 1 ? PA_THREADS : 1];
+  const float* const base = ACROSS ? *at : nullptr;
   for (int e0 = 0; e0 < VEC; e0 += PA_THREADS) {
     const int e = (e0 + threadIdx.x) % VEC, ks = threadIdx.x / VEC, c = e / (HD / 4);
-    float M = -INFINITY, Ls = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, float4 v) {
-      const float to = fmaxf(M, ml.x), f = M == to ? 1.f : exp2_approx(M - to);
-      const float g = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - to);
-      M = to;
-      Ls = fmaf(Ls, f, ml.y * g);
-      o.x = fmaf(o.x, f, v.x * g), o.y = fmaf(o.y, f, v.y * g), o.z = fmaf(o.z, f, v.z * g), o.w = fmaf(o.w, f, v.w * g);
-    };
+    const size_t row = dst || c >= rn ? 0 : po.row(b, g, r0 + c);   // before the loads, whose time covers it
+    PaSum sum;
     for (int k0 = KS > 1 ? ks : 0; k0 < n; k0 += BATCH * KS) {
       float2 ml[BATCH];
       float4 v[BATCH];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int k = k0 + i * KS;
-        if (k >= n) continue;
-        const float* src = across ? across + (size_t)(2 * k + (k == 0)) * PART : at[2 * k + !(closed && k == n - 1)];
-        v[i] = reinterpret_cast<const float4*>(src)[e];
-        ml[i] = reinterpret_cast<const float2*>(src + R * HD)[c];
+        const int k = min(k0 + i * KS, n - 1);
+        if (ACROSS) {
+          const float* src = base + (size_t)(2 * k + (k == 0)) * PART;
+          v[i] = __ldcg(reinterpret_cast<const float4*>(src) + e);
+          ml[i] = __ldcg(reinterpret_cast<const float2*>(src + R * HD) + c);
+        } else {
+          const float* src = at[2 * k + !(closed && k == n - 1)];
+          v[i] = reinterpret_cast<const float4*>(src)[e];
+          ml[i] = reinterpret_cast<const float2*>(src + R * HD)[c];
+        }
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i)
-        if (k0 + i * KS < n) add(ml[i], v[i]);
+        if (k0 + i * KS >= n) ml[i] = make_float2(-INFINITY, 0.f);
+      sum.add(ml, v);
     }
     if (KS > 1) {
-      red[threadIdx.x] = o;
-      redm[threadIdx.x] = make_float2(M, Ls);
+      red[threadIdx.x] = sum.o;
+      redm[threadIdx.x] = make_float2(sum.M, sum.L);
       __syncthreads();
       if (ks == 0)
-        for (int k = 1; k < KS; ++k) add(redm[k * VEC + e], red[k * VEC + e]);
+        for (int k = 1; k < KS; ++k) {
+          float2 ml[1] = {redm[k * VEC + e]};
+          float4 v[1] = {red[k * VEC + e]};
+          sum.add(ml, v);
+        }
       __syncthreads();
       if (ks != 0) continue;
     }
     if (dst) {
-      reinterpret_cast<float4*>(dst)[e] = o;
-      if (e % (HD / 4) == 0) reinterpret_cast<float2*>(dst + R * HD)[c] = make_float2(M, Ls);
+      reinterpret_cast<float4*>(dst)[e] = sum.o;
+      if (e % (HD / 4) == 0) reinterpret_cast<float2*>(dst + R * HD)[c] = make_float2(sum.M, sum.L);
     } else {
-      const int g = grp.y / a.RT, r = (grp.y - g * a.RT) * R + c;
-      if (r < a.rows) pa_store_row<HD>(a, grp.x, g, r, e % (HD / 4), o, M, Ls);
+      if (c < rn) po.store<HD>(row, e % (HD / 4), sum.o, sum.M, sum.L);
     }
   }
 }
@@ -232,7 +254,7 @@ __device__ __noinline__ void pa_merge(const PaArgs& a, const float* const* at, c
 template <int HD, int NT, bool PACK>
 __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a) {
   using L = Page<HD>;
-  constexpr int G = L::G, MT = HD / 16, R = PACK ? 4 : 8 * NT, PART = R * (HD + 2), STEP = NT == 1 ? PASTEP1 : PASTEP2;
+  constexpr int G = L::G, MT = HD / 16, R = PACK ? 4 : 8 * NT, PART = R * (HD + 2), STEP = NT == 1 ? 4 : 2;
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTE = 0x00FF00FFu;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ __align__(8) unsigned long long bars[PA_WARPS][PA_STAGES];
@@ -317,6 +339,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       for (int i = threadIdx.x; i < a.Q * a.Hq; i += PA_THREADS) a.lse[row0 + i] = -INFINITY;
   }
 
+  const PaOut po = {a.out, a.lse, a.Q, a.Hq, a.n_rep, a.bf16};
   PaSplit sp;
   sp.T = (long long)pre[a.B] * U;
   sp.ge = (int)min((long long)a.grid, sp.T);
@@ -756,7 +779,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
           reinterpret_cast<float4*>(dst)[rt * F4 + x] = v;
           if (x == 0) reinterpret_cast<float2*>(dst + R * HD)[rt] = make_float2(lt == 0.f ? -INFINITY : stage_r[c], lt);
         } else if (rt < rn) {
-          pa_store_row<HD>(a, w.b, g, r0 + rt, x, v, stage_r[c], lt);
+          po.store<HD>(po.row(w.b, g, r0 + rt), x, v, stage_r[c], lt);
         }
       }
     }
@@ -829,7 +852,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     const int slot = w >= 0;
     const bool all = closed && w >= 0;
     if (!all) away[slot] = grp;
-    pa_merge<HD, R>(a, &piece_at[first][0], nullptr, n, closed, grp, all ? nullptr : cpart + ((size_t)blockIdx.x * 2 + slot) * PART);
+    const int g = grp.y / a.RT, r0 = (grp.y - g * a.RT) * R;
+    pa_merge<HD, R, false>(po, &piece_at[first][0], n, closed, grp.x, g, r0, min(R, a.rows - r0),
+                           all ? nullptr : cpart + ((size_t)blockIdx.x * 2 + slot) * PART);
   }
   if (away[0].x < 0 && away[1].x < 0) return;
   __syncthreads();
@@ -854,7 +879,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     if (away[k].x < 0 || final_n[k] == 0) continue;
-    pa_merge<HD, R>(a, nullptr, cpart + (size_t)first_cta[k] * 2 * PART, final_n[k], false, away[k], nullptr);
+    const float* at = cpart + (size_t)first_cta[k] * 2 * PART;
+    const int g = away[k].y / a.RT, r0 = (away[k].y - g * a.RT) * R;
+    pa_merge<HD, R, true>(po, &at, final_n[k], false, away[k].x, g, r0, min(R, a.rows - r0), nullptr);
   }
 }
 
