@@ -28,51 +28,44 @@ struct AppendPagedArgs {
   RopeArgs q;
 };
 
-// A row of HD elements over a warp: lane holds E = HD / 32 neighbouring ones.  In fp32 pairs.
-template <int HD>
-struct Row {
-  static constexpr int E = HD / 32, W = E / 2;
-  uint32_t w[W];
-  __device__ __forceinline__ void load(const unsigned short* p) {   // this lane's elements
-    if constexpr (W == 2) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x, w[1] = v.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
+constexpr int E = 4;   // neighbouring elements of a row that a lane holds
+struct Quad {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const unsigned short* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
   }
 };
 
-// Rotation of such rows at one token's position.  The other element of a pair is in the
-// same lane (INTERLEAVED), or a whole number of lanes away (LANES), or, when half of rotary_dim
-// is no multiple of E, anywhere (ELEMENTS).
+// Rotation of rows spread over HD / 4 lanes at one token's position.  The other element of a
+// pair is in the same lane (INTERLEAVED), or a whole number of lanes away (LANES), or, when half of
+// rotary_dim is no multiple of 4, anywhere (ELEMENTS).
 enum class Turn { NONE, INTERLEAVED, LANES, ELEMENTS };
 template <int HD, Turn TURN, bool BF16>
 struct Rotation {
-  static constexpr int E = HD / 32, W = E / 2;
   int from[E], el[E];
   float c[E], s[E];  // y = x c + other s (s carries the sign; elements not rotated: 1, 0)
-  __device__ __forceinline__ void set(const kvq_rope_plan& P, const int32_t* pos, int lane) {
+  __device__ __forceinline__ void set(const kvq_rope_plan& P, const uint64_t* steps, const int32_t* pos, int lane) {
     if (TURN == Turn::NONE) return;
-    const int half = P.rotary_dim / 2, at = *pos;
+    const int half = P.rotary_dim / 2, at = *pos, sub = lane % (HD / E);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int ch = E * lane + e;
+      const int ch = E * sub + e;
       const bool in = ch < P.rotary_dim, second = TURN == Turn::INTERLEAVED ? (e & 1) : ch >= half;
       const int i = TURN == Turn::INTERLEAVED ? ch >> 1 : second ? ch - half : ch;
       const int other = !in ? ch : second ? ch - half : ch + half;
-      from[e] = other / E, el[e] = other % E;
+      from[e] = lane - sub + other / E, el[e] = other % E;
       float2 cs = make_float2(1.f, 0.f);
       if (TURN == Turn::INTERLEAVED && (e & 1)) cs = make_float2(c[e ^ 1], -s[e ^ 1]);
-      else if (in) cs = rope_cos_sin(at, P.step[i], P.magnitude);
+      else if (in) cs = rope_cos_sin(at, steps[i], P.magnitude);
       c[e] = cs.x;
       s[e] = second ? cs.y : -cs.y;
     }
   }
-  __device__ __forceinline__ void apply(const Row<HD>& r, float (&y)[E]) const {
+  __device__ __forceinline__ void apply(const Quad& r, float (&y)[E]) const {
     float x[E], o[E];
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const float2 p = pair_to_f2(r.w[k], BF16);
       x[2 * k] = p.x, x[2 * k + 1] = p.y;
     }
@@ -80,7 +73,7 @@ struct Rotation {
     for (int e = 0; e < E; ++e) o[e] = TURN == Turn::INTERLEAVED ? x[e ^ 1] : 0.f;
     if (TURN == Turn::LANES) {
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
+      for (int k = 0; k < 2; ++k) {
         const float2 p = pair_to_f2(__shfl_sync(0xffffffffu, r.w[k], from[0]), BF16);
         o[2 * k] = p.x, o[2 * k + 1] = p.y;
       }
@@ -99,134 +92,160 @@ struct Rotation {
   }
 };
 
-// Scale, offset and packed codes (4 bits each, from bit 0) of this lane's E elements of a group
-// with extremes lo and hi.  The scale is the smallest binary16 h with 15 h >= the span (15 h is
-// exact in fp32), which is the span / 15 rounded up.  Codes are rint(d / |s|) for the exact
+// Extremes of a group (eight lanes) of fp32 elements.
+__device__ __forceinline__ float2 extremes(const float (&x)[E]) {
+  float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  return make_float2(lo, hi);
+}
+// ... of 16-bit elements as they are: pairs (maximum, negated minimum), one shuffle a round
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  if (BF16) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  return h2_as_u32(__hmax2(u32_as_h2(a), u32_as_h2(b)));
+}
+template <bool BF16>
+__device__ __forceinline__ float2 extremes(const Quad& r) {
+  const uint32_t n0 = r.w[0] ^ 0x80008000u, n1 = r.w[1] ^ 0x80008000u;
+  const uint32_t hi = max_pair<BF16>(r.w[0], r.w[1]), lo = max_pair<BF16>(n0, n1);
+  uint32_t m = max_pair<BF16>(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = max_pair<BF16>(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float2 p = pair_to_f2(m, BF16);
+  return make_float2(-p.y, p.x);
+}
+
+// Scale, offset and packed codes (4 bits each, from bit 0) of this lane's four elements of a
+// group with extremes lo and hi.  The scale is the smallest binary16 h with 15 h >= the span (15 h
+// is exact in fp32), which is the span / 15 rounded up.  Codes are rint(d / |s|) for the exact
 // quotient: they come from a product with the reciprocal, and the remainder d - code s, exact
 // near a half, tells where a neighbour is nearer, or as near and even (values on the binary16
-// grid meet exact halves in about one element of a hundred).
-template <int HD, bool CLAMP>
-__device__ __forceinline__ uint32_t quantize(const float (&x)[HD / 32], float lo, float hi, bool down, __half& sh, __half& oh) {
-  constexpr int E = HD / 32;
+// grid meet exact halves in about one element of a hundred).  The slow path also clamps the codes,
+// which only elements beyond the rounded offset or the binary16 range need.
+__device__ __forceinline__ uint32_t quantize(const float (&x)[E], float2 ext, bool down, __half& sh, __half& oh) {
   constexpr float RND = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, ties to even
-  // elements beyond the binary16 range saturate to the first or the last code
-  if (CLAMP) lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+  const float lo = fminf(fmaxf(ext.x, -65504.f), 65504.f), hi = fminf(fmaxf(ext.y, -65504.f), 65504.f);
   oh = __float2half_rn(down ? hi : lo);
   const float of = __half2float(oh), span = fmaxf(down ? of - lo : hi - of, 0.f);
+  const float before = down ? ext.y - of : of - ext.x;   // how far the extreme lies before the offset,
+  const float behind = (down ? of - ext.x : ext.y - of) - span;   // and the other one behind the span
   const unsigned short h = __half_as_ushort(__float2half_ru(span * 0.06666667f));
   const float sh1 = __half2float(__ushort_as_half(h)), sh0 = __half2float(__ushort_as_half((unsigned short)(h - 1)));
   const int step = 15.f * sh0 >= span ? -1 : 15.f * sh1 < span ? 1 : 0;   // (h = 0: sh0 is a NaN)
   sh = __ushort_as_half((unsigned short)(h + step));
   const float sa = __half2float(sh), s = down ? -sa : sa, half = 0.5f * sa;
-  const float inv = sa > 0.f ? __fdividef(1.f, 15.f * s) : 0.f;   // 15 |s| lies in [2^-21, 2^17]
-  float t[E], r[E], worst = 0.f;
+  const float inv = sa > 0.f ? __fdividef(1.f, s) : 0.f;   // |s| lies in [2^-24, 2^14]
+  const float2 rnd = make_float2(RND, RND);
+  float2 t[2], r[2];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float d = x[e] - of;
-    t[e] = fmaf(__saturatef(d * inv), 15.f, RND);   // bits: RND's plus the code
-    r[e] = fmaf(-(t[e] - RND), s, d);
-    worst = fmaxf(worst, fabsf(r[e]));
+  for (int k = 0; k < 2; ++k) {
+    const float2 d = sub2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(of, of));
+    t[k] = fma2(d, make_float2(inv, inv), rnd);   // bits: RND's plus the code
+    r[k] = fma2(sub2(rnd, t[k]), make_float2(s, s), d);
   }
-  if (worst >= half) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const bool off = fabsf(r[e]) > half || (fabsf(r[e]) == half && (__float_as_uint(t[e]) & 1u));
-      const float to = t[e] + ((r[e] < 0.f) == down ? 1.f : -1.f);
-      t[e] = off && sa > 0.f ? fminf(fmaxf(to, RND), RND + 15.f) : t[e];
-    }
+  const float worst = fmaxf(fmaxf(fabsf(r[0].x), fabsf(r[0].y)), fmaxf(fabsf(r[1].x), fabsf(r[1].y)));
+  if (fmaxf(fmaxf(worst, before), behind) >= half) {
+    auto fix = [&](float xe, float& te, float re) {
+      const bool off = fabsf(re) > half || (fabsf(re) == half && (__float_as_uint(te) & 1u));
+      const float to = off ? te + ((re < 0.f) == down ? 1.f : -1.f) : te;
+      // beyond what the sum with RND holds as an integer, te is far from every code
+      te = sa > 0.f ? fminf(fmaxf(to, RND), RND + 15.f) : RND;
+    };
+    fix(x[0], t[0].x, r[0].x), fix(x[1], t[0].y, r[0].y), fix(x[2], t[1].x, r[1].x), fix(x[3], t[1].y, r[1].y);
   }
   if (down) sh = __hneg(sh);
-  uint32_t code = __float_as_uint(t[0]);   // RND's bits lie above the codes' 16
-#pragma unroll
-  for (int e = 1; e < E; ++e) code += __float_as_uint(t[e]) << (4 * e);
-  return code;
+  // RND's bits lie above the codes' 16
+  return __float_as_uint(t[0].x) + (__float_as_uint(t[0].y) << 4) + (__float_as_uint(t[1].x) << 8) + (__float_as_uint(t[1].y) << 12);
 }
 
-// One warp per item: a token's KV heads [h, h + a.per), with cos and sin formed once per item and the
-// rows of two heads on their way at once.  The other blocks turn q, a thread per V pairs; the two
-// kinds are spread over the grid in turn, since the first are bound by their arithmetic (about 280
-// instructions per token and KV head) and the second by HBM: 32K tokens of 32 + 8 heads 140 us so,
-// 172 with one kind behind the other.  Eight blocks per SM (64 registers): 140 us; six without
-// the bound, 161; ten, 170.
+// One warp per item: a token's KV heads [h, h + a.per), one at a time at head_dim 128 and two at 64,
+// with cos and sin formed once per item and the rows of two steps on their way at once.  The
+// other blocks turn q, a thread per V pairs; the two kinds are spread over the grid in turn, since
+// the first are bound by their arithmetic and the second by HBM.
 constexpr int APPEND_THREADS = 128;
 template <int HD, Turn TURN, int V, bool BF16>
 __global__ void __launch_bounds__(APPEND_THREADS, 8) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
   using L = Page<HD>;
-  constexpr int E = HD / 32, LANES = 32 / E, KU = 2;
+  constexpr int LANES = HD / E, HEADS = 32 / LANES, KU = 2;   // lanes of a row, heads of a step, steps at once
+  constexpr int WARPS = APPEND_THREADS / 32;
+  __shared__ __align__(16) uint64_t steps[128];
   pdl_trigger();
+  if (TURN != Turn::NONE) load_steps(P, steps);
   pdl_wait();
   // block b is KV block number floor(b kv / all) when that number changes behind it
   const int k0 = (int)((long long)blockIdx.x * a.kv_blocks / gridDim.x), k1 = (int)((blockIdx.x + 1ll) * a.kv_blocks / gridDim.x);
   if (V > 0 && k0 == k1) {
-    rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16>(P, a.q, (long long)(blockIdx.x - k0) * APPEND_THREADS + threadIdx.x,
-                                                          (long long)(gridDim.x - a.kv_blocks) * APPEND_THREADS);
+    rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16, APPEND_THREADS, false>(P, steps, nullptr, a.q, (long long)(blockIdx.x - k0) * APPEND_THREADS,
+                                                                          (long long)(gridDim.x - a.kv_blocks) * APPEND_THREADS);
     return;
   }
-  const int lane = threadIdx.x & 31, g = lane / LANES, j = lane % LANES;
+  const int lane = threadIdx.x & 31, sub = lane % LANES, hh = lane / LANES, g = sub / 8, j = sub % 8;
   const int items = (a.Hkv + a.per - 1) / a.per;
   const long long n = (long long)a.T * items;
-  for (long long u = k0 * (APPEND_THREADS / 32ll) + (threadIdx.x >> 5); u < n; u += a.kv_blocks * (APPEND_THREADS / 32ll)) {
-    const long long t = u / items;
-    const int slot = a.slots[t];
+  for (long long base = (long long)k0 * WARPS; base < n; base += (long long)a.kv_blocks * WARPS) {
+    const long long u = base + (threadIdx.x >> 5), t = u / items;
+    const int slot = u < n ? a.slots[t] : -1;
     if (slot < 0 || slot / PG >= a.n_pages) continue;
     const int at = slot % PG, h0 = (int)(u - t * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
     const bool down = at & 1;
-    const unsigned short* kp = static_cast<const unsigned short*>(a.k) + t * a.kt + h0 * a.kh + E * lane;
-    const unsigned short* vp = static_cast<const unsigned short*>(a.v) + t * a.vt + h0 * a.vh + E * lane;
+    const unsigned short* kp = static_cast<const unsigned short*>(a.k) + t * a.kt + (h0 + hh) * a.kh + E * sub;
+    const unsigned short* vp = static_cast<const unsigned short*>(a.v) + t * a.vt + (h0 + hh) * a.vh + E * sub;
     // this lane's bytes of the codes, and its group's scale and offset (lane j = 0 writes)
-    unsigned char* pg = a.pages + ((size_t)(slot / PG) * a.Hkv + h0) * L::BYTES;
-    unsigned char* kc = pg + at * L::ROW + (E * j / 8) * 4 * L::G + 4 * g + (E * j % 8) / 2;
-    unsigned char* vc = pg + L::VC + vcode_at<HD>(at, (E * j / 4) * 2 * L::G + 2 * g + (E * j % 4) / 2);
+    unsigned char* pg = a.pages + ((size_t)(slot / PG) * a.Hkv + h0 + hh) * L::BYTES;
+    unsigned char* kc = pg + at * L::ROW + (j >> 1) * 4 * L::G + 4 * g + 2 * (j & 1);
+    unsigned char* vc = pg + L::VC + vcode_at<HD>(at, j * 2 * L::G + 2 * g);
     __half* ks = reinterpret_cast<__half*>(pg + L::KS) + at * L::G + g;
     __half* vs = reinterpret_cast<__half*>(pg + L::VS) + g * PG + vscale_at(at);
     Rotation<HD, TURN, BF16> rot;
-    for (int h = h0; h < h1; h += KU) {
-      Row<HD> rk[KU], rv[KU];
-#pragma unroll
-      for (int k = 0; k < KU; ++k)
-        if (h + k < h1) {
-          rk[k].load(kp);
-          rv[k].load(vp);
-          kp += a.kh, vp += a.vh;
-        }
-      if (h == h0) rot.set(P, a.pos + t, lane);
+    for (int h = h0; h < h1; h += KU * HEADS) {   // (the same for the whole warp)
+      Quad rk[KU], rv[KU];
 #pragma unroll
       for (int k = 0; k < KU; ++k) {
-        if (h + k >= h1) continue;
+        rk[k].w[0] = rk[k].w[1] = rv[k].w[0] = rv[k].w[1] = 0u;
+        if (h + k * HEADS + hh < h1) {
+          rk[k].load(kp);
+          rv[k].load(vp);
+          kp += HEADS * a.kh, vp += HEADS * a.vh;
+        }
+      }
+      if (h == h0) rot.set(P, steps, a.pos + t, lane);
+#pragma unroll
+      for (int k = 0; k < KU; ++k) {
+        if (h + k * HEADS >= h1) continue;
+        const bool live = HEADS == 1 || h + k * HEADS + hh < h1;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           float x[E];
-          if (kv) {
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-              const float2 p = pair_to_f2(rv[k].w[i], BF16);
-              x[2 * i] = p.x, x[2 * i + 1] = p.y;
-            }
+          float2 ext;
+          if (kv || TURN == Turn::NONE) {
+            const Quad& r = kv ? rv[k] : rk[k];
+            ext = extremes<BF16>(r);
+            const float2 p = pair_to_f2(r.w[0], BF16), q = pair_to_f2(r.w[1], BF16);
+            x[0] = p.x, x[1] = p.y, x[2] = q.x, x[3] = q.y;
           } else {
             rot.apply(rk[k], x);
-          }
-          float lo = x[0], hi = x[0];
-#pragma unroll
-          for (int e = 1; e < E; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
-#pragma unroll
-          for (int o = 1; o < LANES; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            ext = extremes(x);
           }
           __half s, o;
-          const uint32_t code = kv ? quantize<HD, BF16>(x, lo, hi, down, s, o)
-                                   : quantize<HD, BF16 || TURN != Turn::NONE>(x, lo, hi, false, s, o);
-          unsigned char* dst = (kv ? vc : kc) + k * L::BYTES;
-          if (E == 4) *reinterpret_cast<unsigned short*>(dst) = (unsigned short)code;
-          else *dst = (unsigned char)code;
-          if (j == 0) {
-            __half* so = (kv ? vs : ks) + k * (L::BYTES / 2);
-            so[0] = s;
-            so[L::SCALES / 2] = o;
+          const uint32_t code = quantize(x, ext, kv && down, s, o);
+          if (live) {
+            *reinterpret_cast<unsigned short*>((kv ? vc : kc) + k * HEADS * L::BYTES) = (unsigned short)code;
+            if (j == 0) {
+              __half* so = (kv ? vs : ks) + k * HEADS * (L::BYTES / 2);
+              so[0] = s;
+              so[L::SCALES / 2] = o;
+            }
           }
         }
       }
-      kc += KU * L::BYTES, vc += KU * L::BYTES, ks += KU * L::BYTES / 2, vs += KU * L::BYTES / 2;
+      kc += KU * HEADS * L::BYTES, vc += KU * HEADS * L::BYTES, ks += KU * HEADS * L::BYTES / 2, vs += KU * HEADS * L::BYTES / 2;
     }
   }
 }
@@ -238,15 +257,15 @@ auto append_kernel_of(const kvq_rope_plan* plan, bool q) {
   const bool wide = q && rope_pairs(*plan) == 8;
   if (plan->interleaved)
     return wide ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 1, BF16>;
-  if (plan->rotary_dim / 2 % (HD / 32) == 0)
-    return wide ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16> : (K)paged_append_kernel<HD, Turn::LANES, HD / 32, BF16>;
+  if (plan->rotary_dim / 2 % E == 0)
+    return wide ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16> : (K)paged_append_kernel<HD, Turn::LANES, 4, BF16>;
   return (K)paged_append_kernel<HD, Turn::ELEMENTS, 1, BF16>;
 }
 
 // Pairs per thread with which that kernel turns q.
 int append_pairs(const kvq_rope_plan& plan) {
-  if (rope_pairs(plan) == 8) return 8;
-  return plan.interleaved || plan.rotary_dim / 2 % (plan.head_dim / 32) != 0 ? 1 : plan.head_dim / 32;
+  const int V = rope_pairs(plan);
+  return V == 8 || (V == 4 && !plan.interleaved) ? V : 1;
 }
 
 struct GatherArgs {
@@ -367,12 +386,13 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   }
   AppendPagedArgs a{k, v, slots, positions, static_cast<unsigned char*>(pages), kt, kh, vt, vh, T, Hkv, n_pages, heads_per_item(T, Hkv), 0, {}};
   const long long items = (long long)T * ((Hkv + a.per - 1) / a.per);
-  long long blocks = std::min<long long>((items + 3) / 4, 1 << 29);
+  long long blocks = std::min<long long>((items + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32), 152 * 32);
   a.kv_blocks = (int)blocks;
   if (q) {
-    const int chunks = plan->rotary_dim / 2 / append_pairs(*plan);
-    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, rope_lanes(T, Hq, chunks), q != q_out && plan->rotary_dim < hd};
-    blocks += std::min<long long>(((long long)T * a.q.lanes * chunks + APPEND_THREADS - 1) / APPEND_THREADS, 1 << 29);
+    const bool copy = q != q_out && plan->rotary_dim < hd;
+    const int units = rope_units(*plan, append_pairs(*plan), copy);
+    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, rope_lanes(T, Hq, units), copy};
+    blocks += std::min<long long>(((long long)T * a.q.lanes * units + APPEND_THREADS - 1) / APPEND_THREADS, 152 * 32);
   }
   const bool bf16 = dtype == KVQ_BF16;
   auto* kern = hd == 128 ? (bf16 ? append_kernel_of<128, true>(plan, q) : append_kernel_of<128, false>(plan, q))

@@ -62,9 +62,12 @@ constexpr int ROPE_THREADS = 256;
 
 template <int V, bool INTERLEAVED, bool BF16>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ kvq_rope_plan P, RopeArgs a) {
+  __shared__ __align__(16) uint64_t step[128];
+  __shared__ __align__(16) float2 turns[ROPE_THREADS * V + 256];
   pdl_trigger();
+  load_steps(P, step);
   pdl_wait();
-  rope_part<V, INTERLEAVED, BF16>(P, a, blockIdx.x * (long long)ROPE_THREADS + threadIdx.x, (long long)gridDim.x * ROPE_THREADS);
+  rope_part<V, INTERLEAVED, BF16, ROPE_THREADS, true>(P, step, turns, a, blockIdx.x * (long long)ROPE_THREADS, (long long)gridDim.x * ROPE_THREADS);
 }
 
 template <bool INTERLEAVED, bool BF16>
@@ -90,13 +93,15 @@ kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_
   if (kvq_status s = check_buffer(x, dev, 16, fn, "x")) return s;
   if (kvq_status s = check_buffer(out, dev, 16, fn, "out")) return s;
   if (kvq_status s = check_buffer(positions, dev, 4, fn, "positions")) return s;
-  const int V = rope_pairs(*plan), chunks = plan->rotary_dim / 2 / V;
-  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, rope_lanes(T, H, chunks), x != out && plan->rotary_dim < plan->head_dim};
-  const long long blocks = ((long long)T * a.lanes * chunks + ROPE_THREADS - 1) / ROPE_THREADS;
+  const int V = rope_pairs(*plan);
+  const bool copy = x != out && plan->rotary_dim < plan->head_dim;
+  const int units = rope_units(*plan, V, copy);
+  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, rope_lanes(T, H, units), copy};
+  const long long blocks = ((long long)T * a.lanes * units + ROPE_THREADS - 1) / ROPE_THREADS;
   const bool bf16 = dtype == KVQ_BF16;
   auto* k = plan->interleaved ? (bf16 ? rope_kernel_of<true, true>(V) : rope_kernel_of<true, false>(V))
                               : (bf16 ? rope_kernel_of<false, true>(V) : rope_kernel_of<false, false>(V));
-  const dim3 grid((unsigned)std::min<long long>(blocks, 1 << 30));
+  const dim3 grid((unsigned)std::min<long long>(blocks, 152 * 32));
   const cudaError_t e = launch_dependent(k, grid, dim3(ROPE_THREADS), 0, static_cast<cudaStream_t>(stream), *plan, a);
   if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;

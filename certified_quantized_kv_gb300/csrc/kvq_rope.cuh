@@ -17,12 +17,14 @@ struct RopeArgs {
   bool copy;         // the elements behind the rotated ones as well
 };
 
-// One thread per V pairs of a token, for every `lanes`-th head: cos and sin are formed once and
-// used for H / lanes heads, the loads of up to ROPE_UNROLL heads are on their way at once.
-// HBM bound (4 bytes per element, 32K tokens of 40 heads of 128: 671 MB); at V = 8, which
-// every even layout with rotary_dim a multiple of 16 takes, all accesses are 16 bytes.
-// Smaller V serve the other rotary_dims (pairs that start or end between vectors).
-constexpr int ROPE_UNROLL = 4;
+// One thread per V pairs of a token, for every `lanes`-th head; the loads of several heads are on
+// their way at once.  HBM bound (4 bytes per element, 32K tokens of 40 heads of 128: 671 MB);
+// at V = 8, which every layout with rotary_dim a multiple of 16 takes, all accesses are 16
+// bytes.  Smaller V serve the other rotary_dims (pairs that start or end between vectors).
+// A cosine and sine cost about 60 instructions.  With TABLE a block forms those of its tokens once, in
+// shared memory (64 tokens of 40 heads: 2.44 us, 2.65 without; 4099 tokens of 13: 9.1 and 9.7);
+// without, each thread those of its pairs (in the append, whose blocks live on many warps in
+// different phases, the table's barriers cost more than they save: 179 us against 167).
 
 template <int N>
 struct Words {   // N elements in one or two loads of at most 16 bytes
@@ -60,17 +62,47 @@ struct Words {   // N elements in one or two loads of at most 16 bytes
   }
 };
 
-// The part of thread `first` of `threads`.
-template <int V, bool INTERLEAVED, bool BF16>
-__device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const RopeArgs& a, long long first, long long threads) {
+// The plan's steps in shared memory: lanes read different ones at once, which constant memory
+// would serve one at a time.
+__device__ __forceinline__ void load_steps(const kvq_rope_plan& P, uint64_t (&step)[128]) {
+  for (int i = threadIdx.x; i < P.rotary_dim / 2; i += blockDim.x) step[i] = P.step[i];
+  __syncthreads();
+}
+
+// (cos, sin) of all pairs of tokens t0..t0 + n - 1, by the whole block.  With V = 8 two pairs of each
+// chunk of eight lie side by side, then the next two of each: lanes with a chunk each read
+// neighbouring 16 bytes.
+template <int V>
+__device__ __forceinline__ int turn_at(int i, int half) {
+  return V == 8 ? ((i % 8) / 2 * (half / 8) + i / 8) * 2 + i % 2 : i;
+}
+template <int V>
+__device__ __forceinline__ void fill_turns(const kvq_rope_plan& P, const uint64_t* step, const int32_t* pos, long long t0, int n,
+                                           float2* turns) {
+  const int half = P.rotary_dim / 2;
+  for (int e = threadIdx.x; e < n * half; e += blockDim.x) {
+    const int t = e / half, i = e - t * half;
+    turns[t * half + turn_at<V>(i, half)] = rope_cos_sin(pos[t0 + t], step[i], P.magnitude);
+  }
+}
+
+// The units of a block that starts with unit `base` and takes every `stride`-th run of THREADS units;
+// turns (TABLE): room for THREADS * V + 2 * 128 elements.
+template <int V, bool INTERLEAVED, bool BF16, int THREADS, bool TABLE>
+__device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t* step, float2* turns, const RopeArgs& a, long long base,
+                                          long long stride) {
+  constexpr int ROPE_UNROLL = TABLE ? 4 : 2;    // (two heads fit the append's 64 registers)
   constexpr int N0 = INTERLEAVED ? 2 * V : V;   // elements of one load (and of the other, half a head on)
-  constexpr int NT = 2 * V < 8 ? 2 * V : 8;     // elements of one copied piece behind the rotated ones
   const int half = P.rotary_dim / 2, chunks = half / V;
-  const long long n = (long long)a.T * a.lanes * chunks;
-  for (long long u = first; u < n; u += threads) {
-    const long long r = u / chunks, t = r / a.lanes;
-    const int c = (int)(u - r * chunks), i0 = c * V, h0 = (int)(r - t * a.lanes);
-    const int pos = a.pos[t];
+  const int copies = a.copy ? P.head_dim / 8 - (P.rotary_dim + 7) / 8 : 0;   // vectors behind the rotated elements
+  const int units = chunks + copies;
+  const long long n = (long long)a.T * a.lanes * units;
+  const int per_token = a.lanes * units;
+  for (; base < n; base += stride) {
+    const long long u = base + threadIdx.x, t0 = base / per_token, t1 = min(n - 1, base + THREADS - 1) / per_token;
+    const long long r = u / units, t = r / a.lanes;
+    const int c = (int)(u - r * units), i0 = c * V, h0 = (int)(r - t * a.lanes);
+    const bool live = u < n;
     const int e0 = INTERLEAVED ? 2 * i0 : i0, e1 = i0 + half;
     const unsigned short* x = static_cast<const unsigned short*>(a.x) + t * a.xt;
     unsigned short* out = static_cast<unsigned short*>(a.out) + t * a.ot;
@@ -83,10 +115,37 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const RopeArgs
           if (!INTERLEAVED) B[k].load(x + (h + k * a.lanes) * a.xh + e1);
         }
     };
-    fetch(h0);   // on their way while cos and sin are formed
+    const bool turned = live && c < chunks;
+    if (turned) fetch(h0);   // on their way while cos and sin are formed
+    if (TABLE) {
+      __syncthreads();   // its previous readers are done
+      fill_turns<V>(P, step, a.pos, t0, (int)(t1 - t0) + 1, turns);
+      __syncthreads();
+    }
+    if (!live) continue;
+    if (!turned) {
+      const int e = (P.rotary_dim + 7) / 8 * 8 + 8 * (c - chunks);
+#pragma unroll 4
+      for (int h = h0; h < a.H; h += a.lanes)
+        *reinterpret_cast<uint4*>(out + h * a.oh + e) = *reinterpret_cast<const uint4*>(x + h * a.xh + e);
+      continue;
+    }
     float2 cs[V];
+    const float2* mine = turns + (t - t0) * half;
+    if constexpr (!TABLE) {
+      const int pos = a.pos[t];
 #pragma unroll
-    for (int i = 0; i < V; ++i) cs[i] = rope_cos_sin(pos, P.step[i0 + i], P.magnitude);
+      for (int i = 0; i < V; ++i) cs[i] = rope_cos_sin(pos, step[i0 + i], P.magnitude);
+    } else if constexpr (V == 8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = reinterpret_cast<const float4*>(mine)[k * chunks + c];
+        cs[2 * k] = make_float2(v.x, v.y), cs[2 * k + 1] = make_float2(v.z, v.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) cs[i] = mine[i0 + i];
+    }
     for (int h = h0; h < a.H; h += ROPE_UNROLL * a.lanes) {
       if (h != h0) fetch(h);
 #pragma unroll
@@ -112,13 +171,11 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const RopeArgs
         if (!INTERLEAVED) B[k].store(o + e1);
       }
     }
-    if (a.copy)   // what follows the rotated elements
-      for (int e = P.rotary_dim + NT * c; e < P.head_dim; e += NT * chunks)
-        for (int h = h0; h < a.H; h += a.lanes) {
-          Words<NT> w;
-          w.load(x + h * a.xh + e);
-          w.store(out + h * a.oh + e);
-        }
+    if (a.copy && c == 0) {   // what lies between the rotated elements and the next whole vector
+      const int e1 = min(P.head_dim, (P.rotary_dim + 7) / 8 * 8);
+      for (int h = h0; h < a.H; h += a.lanes)
+        for (int e = P.rotary_dim; e < e1; ++e) out[h * a.oh + e] = x[h * a.xh + e];
+    }
   }
 }
 
@@ -126,6 +183,11 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const RopeArgs
 inline int rope_pairs(const kvq_rope_plan& plan) {
   const int half = plan.rotary_dim / 2;
   return half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
+}
+
+// Pieces of a row: chunks of V pairs, and the vectors that are only copied.
+inline int rope_units(const kvq_rope_plan& plan, int V, bool copy) {
+  return plan.rotary_dim / 2 / V + (copy ? plan.head_dim / 8 - (plan.rotary_dim + 7) / 8 : 0);
 }
 
 // Heads in step (RopeArgs::lanes): a thread takes one head while the call does not fill the GPU (64
