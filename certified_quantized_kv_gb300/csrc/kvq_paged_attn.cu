@@ -250,11 +250,15 @@ __device__ __noinline__ void pa_merge(PaOut po, const float* const* at, int n, b
   }
 }
 
-// R query rows per tile: PACK 4 (hi and lo weights share one column tile), else 8 NT.
-template <int HD, int NT, bool PACK>
+// R query rows per tile: 4 (hi and lo weights share the eight columns), 8 (a row each), or 16, where
+// queries are MMA rows instead of columns (WIDE): a score fragment then is an A fragment of
+// the value product as it stands, and hi and lo weights multiply the same code fragments.
+template <int HD, int R>
 __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a) {
   using L = Page<HD>;
-  constexpr int G = L::G, MT = HD / 16, R = PACK ? 4 : 8 * NT, PART = R * (HD + 2), STEP = NT == 1 ? 4 : 2;
+  constexpr bool PACK = R == 4, WIDE = R == 16;
+  constexpr int G = L::G, MT = WIDE ? HD / 8 : HD / 16, PART = R * (HD + 2);   // MT: accumulator tiles
+  constexpr int STEP = WIDE ? 2 : 4;   // tiles of 16 tokens at once
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTE = 0x00FF00FFu;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ __align__(8) unsigned long long bars[PA_WARPS][PA_STAGES];
@@ -426,15 +430,20 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     if (pw.x < n_pos) issue(s);
 
   // ---- state of the group at hand ----
-  uint32_t qb[NT][G][2][2];   // B fragments of q: group, low and high nibbles
-  uint32_t qo[NT];            // B fragment of the group sums of q (hi and lo halves), for the offsets
-  float cs[NT][2];            // score factor of this lane's two columns
-  int c_lo[NT][2], c_hi[NT][2];   // tokens its columns see
+  // q as MMA operands: group, low and high nibbles, columns (B) or rows gid and gid + 8 (A)
+  uint32_t qf[G][2][WIDE ? 4 : 2];
+  uint32_t qo[WIDE ? 2 : 1];  // the group sums of q (hi and lo halves), for the offsets
+  // of this lane's two rows of the tile (its columns 2tig, 2tig + 1; WIDE: gid, gid + 8):
+  float cs[2];                // score factor
+  int c_lo[2], c_hi[2];       // tokens seen
   int t_lo = 0, t_hi = 0, t_all = 0, t_end = 0;   // seen by every row: [t_lo, t_hi); by any: [t_all, t_end)
-  // softmax reference (base 2), the largest score / cs that needs no new one; sums over the codes: rows gid the low nibble's
-  // channel, rows gid + 8 the byte's (16 times the high nibble's plus the low one's)
-  // and the sums of weights times offsets, rows = groups, then the weights' own (row G)
-  float ref[NT][2], lim[NT][2], acc[NT][MT][4], off[NT][4];
+  // softmax reference (base 2), and the largest score / cs that needs no new one
+  float ref[2], lim[2];
+  // Sums over the codes.  Accumulator rows are channels, gid the low nibble's and gid + 8 the
+  // byte's (16 times the high nibble's plus the low one's), and columns are queries; WIDE: rows
+  // are queries and tiles 4g + n the channels 4 gid + n of group g, odd n the bytes'.  off: the sums
+  // of weights times offsets per group, then (group G) the weights' own.
+  float acc[MT][4], off[4];
   float top = PA_TOP;         // weights stay below 2^top
   bool started = false, failed = false;
 
@@ -446,8 +455,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     auto lo_of = [&](int i) { return a.window ? max(0, hi_of(i) - a.window) : 0; };
     t_hi = hi_of(i0), t_lo = lo_of(i1), t_all = lo_of(i0), t_end = len;
 #pragma unroll
-    for (int ct = 0; ct < NT; ++ct) {
-      const int r = ct * 8 + (PACK ? gid & 3 : gid);   // this lane's row of q
+    for (int rj = 0; rj < (WIDE ? 2 : 1); ++rj) {
+      const int r = WIDE ? gid + 8 * rj : PACK ? gid & 3 : gid;   // this lane's row of q
       const bool live = r < rn;
       const int rr = r0 + (live ? r : 0), i = rr / a.n_rep, h = g * a.n_rep + rr - i * a.n_rep;
       const unsigned short* src = static_cast<const unsigned short*>(a.q) +
@@ -481,34 +490,37 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         t += __shfl_xor_sync(0xffffffffu, t, 1);
         t += __shfl_xor_sync(0xffffffffu, t, 2);
         gs[k] = t * up;
-        qb[ct][k][0][0] = h2_as_u32(__floats2half2_rn(f[k][0] * up, f[k][4] * up));
-        qb[ct][k][0][1] = h2_as_u32(__floats2half2_rn(f[k][2] * up, f[k][6] * up));
-        qb[ct][k][1][0] = h2_as_u32(__floats2half2_rn(f[k][1] * upl, f[k][5] * upl));
-        qb[ct][k][1][1] = h2_as_u32(__floats2half2_rn(f[k][3] * upl, f[k][7] * upl));
+        // A operands: rows gid, gid + 8 in registers 0 and 1, the upper half of k in 2 and 3
+        constexpr int U = WIDE ? 2 : 1;
+        qf[k][0][rj] = h2_as_u32(__floats2half2_rn(f[k][0] * up, f[k][4] * up));
+        qf[k][0][U + rj] = h2_as_u32(__floats2half2_rn(f[k][2] * up, f[k][6] * up));
+        qf[k][1][rj] = h2_as_u32(__floats2half2_rn(f[k][1] * upl, f[k][5] * upl));
+        qf[k][1][U + rj] = h2_as_u32(__floats2half2_rn(f[k][3] * upl, f[k][7] * upl));
       }
-      // k columns 2tig, 2tig+1: the sums of two groups, hi halves first, then lo halves
+      // k 2tig, 2tig+1: the sums of two groups, hi halves first, then lo halves
       const int pr = tig % (G / 2), piece = tig / (G / 2);
       const float u = pr ? gs[G - 2] : gs[0], v = pr ? gs[G - 1] : gs[1];
       const __half2 h2 = __floats2half2_rn(u, v);
       const float2 hf = __half22float2(h2);
-      qo[ct] = piece == 0 ? h2_as_u32(h2) : piece == 1 ? h2_as_u32(__floats2half2_rn(u - hf.x, v - hf.y)) : 0u;
+      qo[rj] = piece == 0 ? h2_as_u32(h2) : piece == 1 ? h2_as_u32(__floats2half2_rn(u - hf.x, v - hf.y)) : 0u;
       // never 0, so that -inf stays -inf; the scale's sign is in q
       const float mine = fmaxf(ldexpf(fabsf(a.scale_log2), -e), 1.17549435e-38f);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        cs[ct][j] = __shfl_sync(0xffffffffu, mine, (2 * tig + j) * 4);
-        const int c = ct * 8 + (PACK ? (2 * tig + j) & 3 : 2 * tig + j);
+        if (WIDE && j != rj) continue;
+        cs[j] = WIDE ? mine : __shfl_sync(0xffffffffu, mine, (2 * tig + j) * 4);
+        const int c = WIDE ? r : PACK ? (2 * tig + j) & 3 : 2 * tig + j;
         const int ci = (r0 + min(c, rn - 1)) / a.n_rep;
-        c_lo[ct][j] = lo_of(ci), c_hi[ct][j] = hi_of(ci);
-        ref[ct][j] = -3.402823466e38f, lim[ct][j] = -INFINITY;
+        c_lo[j] = lo_of(ci), c_hi[j] = hi_of(ci);
+        ref[j] = -3.402823466e38f, lim[j] = -INFINITY;
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[ct][mt][j] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) off[ct][j] = 0.f;
     }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[mt][j] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) off[j] = 0.f;
     top = PA_TOP;
   };
 
@@ -555,9 +567,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         if (now != top) {
           top = now;
 #pragma unroll
-          for (int ct = 0; ct < NT; ++ct)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) lim[ct][j] = ref[ct][j] < -3e38f ? -INFINITY : (ref[ct][j] + top) / cs[ct][j];
+          for (int j = 0; j < 2; ++j) lim[j] = ref[j] < -3e38f ? -INFINITY : (ref[j] + top) / cs[j];
         }
       }
     }
@@ -565,109 +575,119 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll 1
     for (int i0 = 0; i0 < 4; i0 += STEP) {
       // ---- scores: S cs is the score in base 2 ----
-      float S[NT][STEP][4];
+      // S[.][j]: tokens gid, gid + 8 (j / 2) of a tile and column j % 2; WIDE: S[.][h][j], tokens
+      // 8h + 2tig + j % 2 and row j / 2
+      float S[STEP][WIDE ? 8 : 4];
 #pragma unroll
       for (int ii = 0; ii < STEP; ++ii) {
         const int ta = 16 * (i0 + ii) + gid, tb = ta + 8;
-        uint32_t wa[G], wb[G], sa[G / 2], sb[G / 2];
+        uint32_t wa[G], wb[G];
         lds(wa, pg + ta * L::ROW + tig * 4 * G);
         lds(wb, pg + tb * L::ROW + tig * 4 * G);
-        lds(sa, pg + L::KS + ta * 2 * G);
-        lds(sb, pg + L::KS + tb * 2 * G);
         const uint32_t oa = *reinterpret_cast<const uint32_t*>(pg + L::KO + ta * 2 * G + 4 * pr_k);
         const uint32_t ob = *reinterpret_cast<const uint32_t*>(pg + L::KO + tb * 2 * G + 4 * pr_k);
-        float r[NT][4];
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint32_t xa = wa[g] >> 8, xb = wb[g] >> 8;
-          const float2 s2a = __half22float2(u32_as_h2(sa[g >> 1])), s2b = __half22float2(u32_as_h2(sb[g >> 1]));
-          const float fa = (g & 1) ? s2a.y : s2a.x, fb = (g & 1) ? s2b.y : s2b.x;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t sc[G];   // scales of tokens 2tig, 2tig + 1 of the eight: G / 2 words each
+            lds(sc, pg + L::KS + (16 * (i0 + ii) + 8 * h + 2 * tig) * 2 * G);
+            const uint32_t* w = h ? wb : wa;
+            float r[4];
 #pragma unroll
-          for (int ct = 0; ct < NT; ++ct) {
-            float X[4];
-            mma_z(X, wa[g] & LO, wb[g] & LO, xa & LO, xb & LO, qb[ct][g][0][0], qb[ct][g][0][1]);
-            mma(X, wa[g] & HI, wb[g] & HI, xa & HI, xb & HI, qb[ct][g][1][0], qb[ct][g][1][1]);
+            for (int g = 0; g < G; ++g) {
+              const uint32_t x = w[g] >> 8;
+              const float2 s0 = __half22float2(u32_as_h2(sc[g >> 1])), s1 = __half22float2(u32_as_h2(sc[G / 2 + (g >> 1)]));
+              const float f0 = (g & 1) ? s0.y : s0.x, f1 = (g & 1) ? s1.y : s1.x;
+              float X[4];
+              mma_z(X, qf[g][0][0], qf[g][0][1], qf[g][0][2], qf[g][0][3], w[g] & LO, x & LO);
+              mma(X, qf[g][1][0], qf[g][1][1], qf[g][1][2], qf[g][1][3], w[g] & HI, x & HI);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float f = j < 2 ? fa : fb;
-              r[ct][j] = g == 0 ? X[j] * f : fmaf(X[j], f, r[ct][j]);
+              for (int j = 0; j < 4; ++j) r[j] = g == 0 ? X[j] * ((j & 1) ? f1 : f0) : fmaf(X[j], (j & 1) ? f1 : f0, r[j]);
             }
+            float O[4];
+            mma_k8_z(O, qo[0], qo[1], h ? ob : oa);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[ii][4 * h + j] = fmaf(r[j], NIB_ROW_SCALE_LO, O[j]);
           }
-        }
+        } else {
+          uint32_t sa[G / 2], sb[G / 2];
+          lds(sa, pg + L::KS + ta * 2 * G);
+          lds(sb, pg + L::KS + tb * 2 * G);
+          float r[4];
 #pragma unroll
-        for (int ct = 0; ct < NT; ++ct) {
+          for (int g = 0; g < G; ++g) {
+            const uint32_t xa = wa[g] >> 8, xb = wb[g] >> 8;
+            const float2 s2a = __half22float2(u32_as_h2(sa[g >> 1])), s2b = __half22float2(u32_as_h2(sb[g >> 1]));
+            const float fa = (g & 1) ? s2a.y : s2a.x, fb = (g & 1) ? s2b.y : s2b.x;
+            float X[4];
+            mma_z(X, wa[g] & LO, wb[g] & LO, xa & LO, xb & LO, qf[g][0][0], qf[g][0][1]);
+            mma(X, wa[g] & HI, wb[g] & HI, xa & HI, xb & HI, qf[g][1][0], qf[g][1][1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = g == 0 ? X[j] * (j < 2 ? fa : fb) : fmaf(X[j], j < 2 ? fa : fb, r[j]);
+          }
           float O[4];
-          mma_k8_z(O, oa, ob, qo[ct]);
+          mma_k8_z(O, oa, ob, qo[0]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) S[ct][ii][j] = fmaf(r[ct][j], NIB_ROW_SCALE_LO, O[j]);
+          for (int j = 0; j < 4; ++j) S[ii][j] = fmaf(r[j], NIB_ROW_SCALE_LO, O[j]);
         }
       }
+      constexpr int NS = WIDE ? 8 : 4;
+      auto row_of = [](int j) { return WIDE ? (j >> 1) & 1 : j & 1; };   // which of the lane's two rows
       if (edge) {
 #pragma unroll
-        for (int ct = 0; ct < NT; ++ct)
+        for (int ii = 0; ii < STEP; ++ii)
 #pragma unroll
-          for (int ii = 0; ii < STEP; ++ii)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int t = tok0 + 16 * (i0 + ii) + gid + (j < 2 ? 0 : 8);
-              if (t < c_lo[ct][j & 1] || t >= c_hi[ct][j & 1]) S[ct][ii][j] = -INFINITY;
-            }
+          for (int j = 0; j < NS; ++j) {
+            const int t = tok0 + 16 * (i0 + ii) + (WIDE ? 8 * (j >> 2) + 2 * tig + (j & 1) : gid + 8 * (j >> 1));
+            if (t < c_lo[row_of(j)] || t >= c_hi[row_of(j)]) S[ii][j] = -INFINITY;
+          }
       }
 
       // ---- softmax weights 2^(S cs - ref): the reference moves only when one would pass 2^top ----
-      float mx[NT][2];
-      bool over = false;
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int ct = 0; ct < NT; ++ct)
+      for (int ii = 0; ii < STEP; ++ii)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float t = fmaxf(S[ct][0][j], S[ct][0][j + 2]);
+        for (int j = 0; j < NS; ++j) mx[row_of(j)] = fmaxf(mx[row_of(j)], S[ii][j]);
+      if (__any_sync(0xffffffffu, mx[0] > lim[0] || mx[1] > lim[1])) {
+        float al[2];
 #pragma unroll
-          for (int ii = 1; ii < STEP; ++ii) t = fmaxf(t, fmaxf(S[ct][ii][j], S[ct][ii][j + 2]));
-          mx[ct][j] = t;
-          over = over || t > lim[ct][j];
+        for (int j = 0; j < 2; ++j) {   // over the lanes that hold a row's other tokens
+          float t = mx[j];
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, WIDE ? 1 : 4));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, WIDE ? 2 : 8));
+          if (!WIDE) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          const float now = t > lim[j] ? t * cs[j] - (top - PA_SLACK) : ref[j];
+          al[j] = exp2_approx(ref[j] - now);
+          if (t > lim[j]) lim[j] = (now + top) / cs[j];
+          ref[j] = now;
         }
-      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-        for (int ct = 0; ct < NT; ++ct) {
-          float al[2];
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float t = mx[ct][j];
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            const float now = t > lim[ct][j] ? t * cs[ct][j] - (top - PA_SLACK) : ref[ct][j];
-            al[j] = exp2_approx(ref[ct][j] - now);
-            if (t > lim[ct][j]) lim[ct][j] = (now + top) / cs[ct][j];
-            ref[ct][j] = now;
-          }
+          for (int j = 0; j < 4; ++j) acc[mt][j] *= al[row_of(j)];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            acc[ct][mt][0] *= al[0], acc[ct][mt][1] *= al[1];
-            acc[ct][mt][2] *= al[0], acc[ct][mt][3] *= al[1];
-          }
-          off[ct][0] *= al[0], off[ct][1] *= al[1];
-        }
+        for (int j = 0; j < 4; ++j) off[j] *= al[row_of(j)];
       }
 
       // ---- values ----
 #pragma unroll
       for (int ii = 0; ii < STEP; ++ii) {
         const int i = i0 + ii;
-        // B fragments of the weights (k = tokens 16i + 2tig, +1 and 8 more), hi and lo halves
-        uint32_t ph[NT][2], pl[NT][2];
+        // Weights in hi and lo halves, tokens 2tig, +1 and 8 more.  B fragments (k = tokens,
+        // column gid), turned; WIDE: A fragments as they are (rows gid, gid + 8, then 8 tokens on).
+        constexpr int NP = WIDE ? 4 : 2;
+        uint32_t ph[NP], pl[NP];
 #pragma unroll
-        for (int ct = 0; ct < NT; ++ct)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float p0 = exp2_approx(fmaf(S[ct][ii][2 * h], cs[ct][0], -ref[ct][0]));
-            const float p1 = exp2_approx(fmaf(S[ct][ii][2 * h + 1], cs[ct][1], -ref[ct][1]));
-            const __half2 hi = __floats2half2_rn(p0, p1);
-            const float2 hf = __half22float2(hi);
-            ph[ct][h] = movmatrix_t(h2_as_u32(hi));
-            pl[ct][h] = movmatrix_t(h2_as_u32(__floats2half2_rn(p0 - hf.x, p1 - hf.y)));
-          }
+        for (int k = 0; k < NP; ++k) {
+          const float p0 = exp2_approx(fmaf(S[ii][2 * k], cs[row_of(2 * k)], -ref[row_of(2 * k)]));
+          const float p1 = exp2_approx(fmaf(S[ii][2 * k + 1], cs[row_of(2 * k + 1)], -ref[row_of(2 * k + 1)]));
+          const __half2 hi = __floats2half2_rn(p0, p1);
+          const float2 hf = __half22float2(hi);
+          const __half2 lo = __floats2half2_rn(p0 - hf.x, p1 - hf.y);
+          ph[k] = WIDE ? h2_as_u32(hi) : movmatrix_t(h2_as_u32(hi));
+          pl[k] = WIDE ? h2_as_u32(lo) : movmatrix_t(h2_as_u32(lo));
+        }
         // codes of token pairs: word g of x[h] holds four channels of group g of two tokens
         uint32_t x[2][G];
 #pragma unroll
@@ -681,55 +701,61 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         uint32_t o[2];
         lds(o, pg + o_at + i * 8);
         o[0] = (o[0] & o_mask) | o_one, o[1] = (o[1] & o_mask) | o_one;
-        if (PACK) {
+        uint32_t pm[2], pz[2];
+        if constexpr (PACK) {
           // columns 4..7 take the lo halves: there p_hi s is formed again for its remainder
-          uint32_t pm[2], pz[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            pm[h] = lo_col ? pl[0][h] : ph[0][h];
-            pz[h] = lo_col ? ph[0][h] : 0u;
+            pm[h] = lo_col ? pl[h] : ph[h];
+            pz[h] = lo_col ? ph[h] : 0u;
           }
-          mma(off[0], o[0], 0u, o[1], 0u, pm[0], pm[1]);
+          mma(off, o[0], 0u, o[1], 0u, pm[0], pm[1]);
+        } else if constexpr (WIDE) {
+          mma(off, ph[0], ph[1], ph[2], ph[3], o[0], o[1]);
+          mma(off, pl[0], pl[1], pl[2], pl[3], o[0], o[1]);
+        } else {
+          mma(off, o[0], 0u, o[1], 0u, ph[0], ph[1]);
+          mma(off, o[0], 0u, o[1], 0u, pl[0], pl[1]);
+        }
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            uint32_t sc[2], b[2];
-            lds(sc, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
+        for (int g = 0; g < G; ++g) {
+          uint32_t sc[2];
+          lds(sc, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
+          const uint32_t y0 = __byte_perm(x[0][g], 0u, 0x4341), y1 = __byte_perm(x[1][g], 0u, 0x4341);
+          if constexpr (PACK) {
+            uint32_t b[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const __half2 sv = u32_as_h2(sc[h]), z = u32_as_h2(pz[h]);
               b[h] = h2_as_u32(__hfma2(u32_as_h2(pm[h]), sv, __hfma2(z, sv, __hneg2(__hmul2_rn(z, sv)))));
             }
-            const uint32_t y0 = __byte_perm(x[0][g], 0u, 0x4341), y1 = __byte_perm(x[1][g], 0u, 0x4341);
-            mma(acc[0][2 * g], x[0][g] & LO, x[0][g] & BYTE, x[1][g] & LO, x[1][g] & BYTE, b[0], b[1]);
-            mma(acc[0][2 * g + 1], y0 & LO, y0, y1 & LO, y1, b[0], b[1]);
-          }
-        } else {
+            mma(acc[2 * g], x[0][g] & LO, x[0][g] & BYTE, x[1][g] & LO, x[1][g] & BYTE, b[0], b[1]);
+            mma(acc[2 * g + 1], y0 & LO, y0, y1 & LO, y1, b[0], b[1]);
+          } else {
+            uint32_t hi[NP], lo[NP];
 #pragma unroll
-          for (int ct = 0; ct < NT; ++ct) {
-            mma(off[ct], o[0], 0u, o[1], 0u, ph[ct][0], ph[ct][1]);
-            mma(off[ct], o[0], 0u, o[1], 0u, pl[ct][0], pl[ct][1]);
-          }
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            uint32_t sc[2];
-            lds(sc, pg + L::VS + g * 2 * PG + tig * 32 + i * 8);
-            const uint32_t y0 = __byte_perm(x[0][g], 0u, 0x4341), y1 = __byte_perm(x[1][g], 0u, 0x4341);
+            for (int k = 0; k < NP; ++k) {
+              const __half2 sv = u32_as_h2(sc[WIDE ? k >> 1 : k]), p = u32_as_h2(ph[k]);
+              const __half2 w = __hmul2_rn(p, sv);
+              hi[k] = h2_as_u32(w);
+              lo[k] = h2_as_u32(__hfma2(u32_as_h2(pl[k]), sv, __hfma2(p, sv, __hneg2(w))));   // the remainder is exact
+            }
             const uint32_t x0l = x[0][g] & LO, x0b = x[0][g] & BYTE, x1l = x[1][g] & LO, x1b = x[1][g] & BYTE;
             const uint32_t y0l = y0 & LO, y1l = y1 & LO;
-#pragma unroll
-            for (int ct = 0; ct < NT; ++ct) {
-              uint32_t hi[2], lo[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const __half2 sv = u32_as_h2(sc[h]), p = u32_as_h2(ph[ct][h]);
-                const __half2 w = __hmul2_rn(p, sv);
-                hi[h] = h2_as_u32(w);
-                lo[h] = h2_as_u32(__hfma2(u32_as_h2(pl[ct][h]), sv, __hfma2(p, sv, __hneg2(w))));   // the remainder is exact
-              }
-              mma(acc[ct][2 * g], x0l, x0b, x1l, x1b, hi[0], hi[1]);
-              mma(acc[ct][2 * g + 1], y0l, y0, y1l, y1, hi[0], hi[1]);
-              mma(acc[ct][2 * g], x0l, x0b, x1l, x1b, lo[0], lo[1]);
-              mma(acc[ct][2 * g + 1], y0l, y0, y1l, y1, lo[0], lo[1]);
+            if constexpr (WIDE) {
+              mma(acc[4 * g], hi[0], hi[1], hi[2], hi[3], x0l, x1l);
+              mma(acc[4 * g + 1], hi[0], hi[1], hi[2], hi[3], x0b, x1b);
+              mma(acc[4 * g + 2], hi[0], hi[1], hi[2], hi[3], y0l, y1l);
+              mma(acc[4 * g + 3], hi[0], hi[1], hi[2], hi[3], y0, y1);
+              mma(acc[4 * g], lo[0], lo[1], lo[2], lo[3], x0l, x1l);
+              mma(acc[4 * g + 1], lo[0], lo[1], lo[2], lo[3], x0b, x1b);
+              mma(acc[4 * g + 2], lo[0], lo[1], lo[2], lo[3], y0l, y1l);
+              mma(acc[4 * g + 3], lo[0], lo[1], lo[2], lo[3], y0, y1);
+            } else {
+              mma(acc[2 * g], x0l, x0b, x1l, x1b, hi[0], hi[1]);
+              mma(acc[2 * g + 1], y0l, y0, y1l, y1, hi[0], hi[1]);
+              mma(acc[2 * g], x0l, x0b, x1l, x1b, lo[0], lo[1]);
+              mma(acc[2 * g + 1], y0l, y0, y1l, y1, lo[0], lo[1]);
             }
           }
         }
@@ -742,20 +768,35 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   auto emit = [&](const Walk& w, float* dst) {
     const int g = w.gr / a.RT, r0 = (w.gr - g * a.RT) * R, rn = min(R, a.rows - r0);
 #pragma unroll
-    for (int ct = 0; ct < NT; ++ct) {
+    for (int ct = 0; ct < (WIDE ? 2 : 1); ++ct) {   // eight rows (columns) at a time
       __syncwarp();
+      if constexpr (WIDE) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float* row = stage + (2 * tig + j) * SROW + 4 * gid;
+        for (int gg = 0; gg < G; ++gg)
 #pragma unroll
-        for (int gg = 0; gg < G; ++gg) {
-          const float e0 = acc[ct][2 * gg][j], e1 = acc[ct][2 * gg][j + 2], e2 = acc[ct][2 * gg + 1][j], e3 = acc[ct][2 * gg + 1][j + 2];
-          *reinterpret_cast<float4*>(row + 32 * gg) =
-              make_float4(e0 * NIB_ROW_SCALE_LO, (e1 - e0) * NIB_ROW_SCALE_HI, e2 * NIB_ROW_SCALE_LO, (e3 - e2) * NIB_ROW_SCALE_HI);
+          for (int e = 0; e < 2; ++e) {
+            const int k = 2 * ct + e;
+            *reinterpret_cast<float4*>(stage + gid * SROW + 32 * gg + 8 * tig + 4 * e) =
+                make_float4(acc[4 * gg][k] * NIB_ROW_SCALE_LO, (acc[4 * gg + 1][k] - acc[4 * gg][k]) * NIB_ROW_SCALE_HI,
+                            acc[4 * gg + 2][k] * NIB_ROW_SCALE_LO, (acc[4 * gg + 3][k] - acc[4 * gg + 2][k]) * NIB_ROW_SCALE_HI);
+          }
+        if (tig < G / 2) stage_o[gid * G + 2 * tig] = off[2 * ct], stage_o[gid * G + 2 * tig + 1] = off[2 * ct + 1];
+        if (tig == G / 2) stage_l[gid] = failed ? __int_as_float(0x7fc00000) : off[2 * ct];
+        if (tig == 0) stage_r[gid] = ref[ct];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float* row = stage + (2 * tig + j) * SROW + 4 * gid;
+#pragma unroll
+          for (int gg = 0; gg < G; ++gg) {
+            const float e0 = acc[2 * gg][j], e1 = acc[2 * gg][j + 2], e2 = acc[2 * gg + 1][j], e3 = acc[2 * gg + 1][j + 2];
+            *reinterpret_cast<float4*>(row + 32 * gg) =
+                make_float4(e0 * NIB_ROW_SCALE_LO, (e1 - e0) * NIB_ROW_SCALE_HI, e2 * NIB_ROW_SCALE_LO, (e3 - e2) * NIB_ROW_SCALE_HI);
+          }
+          if (gid < G) stage_o[(2 * tig + j) * G + gid] = off[j];
+          if (gid == G) stage_l[2 * tig + j] = failed ? __int_as_float(0x7fc00000) : off[j];
+          if (gid == 0) stage_r[2 * tig + j] = ref[j];
         }
-        if (gid < G) stage_o[(2 * tig + j) * G + gid] = off[ct][j];
-        if (gid == G) stage_l[2 * tig + j] = failed ? __int_as_float(0x7fc00000) : off[ct][j];
-        if (gid == 0) stage_r[2 * tig + j] = ref[ct][j];
       }
       __syncwarp();
       constexpr int TR = PACK ? 4 : 8, F4 = HD / 4;   // rows of the tile, float4s of a row
@@ -908,11 +949,11 @@ size_t ws_bytes(int sms, int Q, int Hq, int Hkv, int hd) {
   return PA_COUNTERS + (size_t)sms * (PA_WARPS + 2) * tile_rows(Q * (Hq / Hkv)) * (hd + 2) * sizeof(float);
 }
 
-template <int HD, int NT, bool PACK>
+template <int HD, int R>
 cudaError_t launch(const PaArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)PA_WARPS * (PA_STAGES * Page<HD>::BYTES + PaStage<HD>::FLOATS * sizeof(float)) +
                       (2 * (size_t)a.B + 1) * sizeof(int);
-  auto* k = paged_attention_kernel<HD, NT, PACK>;
+  auto* k = paged_attention_kernel<HD, R>;
   if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
   return launch_dependent(k, dim3(a.grid), dim3(PA_THREADS), smem, st, a);
 }
@@ -960,8 +1001,8 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + PA_COUNTERS);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (hd == 128) e = R == 4 ? launch<128, 1, true>(a, st) : R == 8 ? launch<128, 1, false>(a, st) : launch<128, 2, false>(a, st);
-  else e = R == 4 ? launch<64, 1, true>(a, st) : R == 8 ? launch<64, 1, false>(a, st) : launch<64, 2, false>(a, st);
+  if (hd == 128) e = R == 4 ? launch<128, 4>(a, st) : R == 8 ? launch<128, 8>(a, st) : launch<128, 16>(a, st);
+  else e = R == 4 ? launch<64, 4>(a, st) : R == 8 ? launch<64, 8>(a, st) : launch<64, 16>(a, st);
   if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
