@@ -199,7 +199,7 @@ struct PaSum {
 template <int HD, int R, bool ACROSS>
 __device__ __noinline__ void pa_merge(PaOut po, const float* const* at, int n, bool closed, int b, int g, int r0, int rn, float* dst) {
   constexpr int PART = R * (HD + 2), VEC = R * HD / 4, KS = PA_THREADS / VEC > 1 ? PA_THREADS / VEC : 1;
-  constexpr int BATCH = 5;
+  constexpr int BATCH = KS > 1 ? 5 : 10;
   __shared__ float4 red[KS > 1 ? PA_THREADS : 1];
   __shared__ float2 redm[KS > 1 ? PA_THREADS : 1];
   const float* const base = ACROSS ? *at : nullptr;
@@ -800,6 +800,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       }
       __syncwarp();
       constexpr int TR = PACK ? 4 : 8, F4 = HD / 4;   // rows of the tile, float4s of a row
+      // lane c prepares row c: where it goes and 1 / its weight sum
+      const int mine = lane % TR, rt0 = 8 * ct;
+      float lt = stage_l[mine];
+      if (PACK) lt += stage_l[mine + 4];   // columns 4..7 hold the lo halves' sums
+      const float rf = stage_r[mine], inv = lt == 0.f ? 0.f : 1.f / lt;
+      const bool live = rt0 + mine < rn;
+      const size_t row = live && !dst ? po.row(w.b, g, r0 + rt0 + mine) : 0;
+      if (lane < TR) {
+        if (dst) reinterpret_cast<float2*>(dst + R * HD)[rt0 + lane] = make_float2(lt == 0.f ? -INFINITY : rf, lt);
+        else if (live && a.lse) a.lse[row] = lt == 0.f ? -INFINITY : (rf + log2f(lt)) * 0.69314718055994531f;
+      }
 #pragma unroll
       for (int k = 0; k < TR * F4 / 32; ++k) {
         const int e = lane + 32 * k, c = e / F4, x = e % F4;
@@ -809,19 +820,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
           return make_float4(v.x + o, v.y + o, v.z + o, v.w + o);
         };
         float4 v = at(c);
-        float lt = stage_l[c];
-        if (PACK) {   // columns 4..7 hold the lo halves' sums
+        if (PACK) {
           const float4 u = at(c + 4);
           v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-          lt += stage_l[c + 4];
         }
-        const int rt = 8 * ct + c;   // row of the tile
-        if (dst) {
-          reinterpret_cast<float4*>(dst)[rt * F4 + x] = v;
-          if (x == 0) reinterpret_cast<float2*>(dst + R * HD)[rt] = make_float2(lt == 0.f ? -INFINITY : stage_r[c], lt);
-        } else if (rt < rn) {
-          po.store<HD>(po.row(w.b, g, r0 + rt), x, v, stage_r[c], lt);
-        }
+        const float f = __shfl_sync(0xffffffffu, inv, c);
+        const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)row, c);
+        if (dst)
+          reinterpret_cast<float4*>(dst)[(rt0 + c) * F4 + x] = v;
+        else if (rt0 + c < rn)
+          reinterpret_cast<uint2*>(a.out)[to * F4 + x] = make_uint2(f2_to_pair(v.x * f, v.y * f, a.bf16), f2_to_pair(v.z * f, v.w * f, a.bf16));
       }
     }
   };
