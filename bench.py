@@ -31,6 +31,7 @@ import numpy as np  # noqa: E402
 
 WORKLOAD = dict(name="c3_llama8b_ctx128k_32l", batch=1, ctx=131072, layers=32, q_heads=32,
                 kv_heads=8, head_dim=128, tau_cov=0.995, eps=0.25, seed=2)
+ROPE = dict(base=500000.0, scaling="parts", factor=8.0, original_ctx=8192, low=1.0, high=4.0)   # Llama-3.1-8B's
 METRIC = "certified decode-attn tokens/s/layer at 128K ctx; HBM GB/s vs peak"
 UNIT = "tokens/s/layer"
 TIER1_BYTES_PER_TOKEN_HEAD = 212        # 128 K codes + 4 K scales + 64 V codes + 16 V scale/offset
@@ -1018,10 +1019,19 @@ def decode_loop(args):
     out = torch.empty(B, Hq, D, dtype=torch.float16, device="cuda")
     cert = torch.empty(B * Hq * 32, dtype=torch.uint8, device="cuda")
 
+    plan = kvq.RopePlan(D, **ROPE) if args.rope else None
+    if plan:
+        pos = torch.arange(n0, n0 + steps, dtype=torch.int32, device="cuda").repeat_interleave(B).reshape(steps, B)
+
     def step(t):
         for layer in range(L):
+            q = qnew[t, layer]
+            if plan:   # new tokens of a model's projections: rotated in place
+                kvq.rope(q, pos[t], plan, out=q)
+                k = knew[t, layer].squeeze(2)
+                kvq.rope(k, pos[t], plan, out=k)
             cache.append(layer, knew[t, layer], vnew[t, layer])
-            cache.decode(layer, qnew[t, layer], tau, eps, out, cert)
+            cache.decode(layer, q, tau, eps, out, cert)
 
     for t in range(Wm):
         step(t)
@@ -1038,12 +1048,72 @@ def decode_loop(args):
     rs = [cache.residency_stats(layer) for layer in range(L)]
     print(json.dumps({"mode": "decode_loop", "metric": "tokens/s/layer (append + certified decode per token)",
                       "value": B / (ms / L / 1e3), "ms_per_step": ms, "steps": T, "warmup": Wm,
-                      "layers": L, "batch": B, "ctx_end": N, "tau_cov": tau, "eps": eps,
+                      "layers": L, "batch": B, "ctx_end": N, "tau_cov": tau, "eps": eps, "rope": bool(args.rope),
                       "resident_fraction": args.resident, "resident_blocks_per_layer": slots,
                       "host_bytes_per_step": sum(x["host_bytes"] for x in rs) / T if slots else None,
                       "resident_bytes_per_step": sum(x["resident_bytes"] for x in rs) / T if slots else None}),
           flush=True)
     cache.close()
+
+
+def paged_loop(args):
+    """The same loop on the paged 4-bit cache: every step turns a layer's new query and key by
+    their position, appends the key and the value to its pages (one call) and attends over
+    them (a second one).  The pool of pages lies in device memory, in shuffled order.  Prints
+    one JSON line."""
+    import torch
+    import certified_quantized_kv_gb300 as kvq
+    import workloads as W
+
+    torch.cuda.set_device(int(os.environ.get("LOCAL_RANK", "0")))
+    wl = dict(WORKLOAD)
+    B, L, N = args.batch or wl["batch"], args.layers or wl["layers"], args.ctx or wl["ctx"]
+    Hq, Hkv, D = wl["q_heads"], wl["kv_heads"], wl["head_dim"]
+    T, Wm = args.steps, args.warmup
+    steps = T + Wm
+    n0, per = N - steps, -(-N // 64)
+    plan = kvq.RopePlan(D, **ROPE)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(wl["seed"] + 77)
+    table = torch.randperm(B * per, generator=gen, device="cuda").to(torch.int32).reshape(B, per)
+    pools = [torch.empty(B * per, Hkv, kvq.paged_page_bytes(D), dtype=torch.uint8, device="cuda") for _ in range(L)]
+    ws = torch.zeros(kvq.paged_attention_workspace(B, 1, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    at = torch.arange(N, device="cuda")
+    slots = (table.long()[:, at // 64] * 64 + at % 64).to(torch.int32)           # [B, N]
+    at = at.to(torch.int32)
+    for layer in range(L):
+        _, K, V = W.c3_layer(layer, device="cuda", seed=wl["seed"], batch=B, ctx=n0, Hq=Hq, Hkv=Hkv)
+        for b in range(B):
+            kvq.paged_append(pools[layer], K[b].transpose(0, 1), V[b].transpose(0, 1), slots[b, :n0].contiguous(),
+                             positions=at[:n0], plan=plan)
+        del K, V
+    new = torch.randn(steps, L, B, Hq + 2 * Hkv, D, generator=gen, device="cuda").half()
+    slot = [slots[:, n0 + t].contiguous() for t in range(steps)]
+    pos = [torch.full((B,), n0 + t, dtype=torch.int32, device="cuda") for t in range(steps)]
+    lens = [torch.full((B,), n0 + t + 1, dtype=torch.int32, device="cuda") for t in range(steps)]
+    out = torch.empty(B, Hq, D, dtype=torch.float16, device="cuda")
+
+    def step(t):
+        for layer in range(L):
+            x = new[t, layer]
+            q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+            kvq.paged_append(pools[layer], k, v, slot[t], positions=pos[t], plan=plan, q=q, q_out=q)
+            kvq.paged_attention(q, pools[layer], table, lens[t], out, workspace=ws)
+
+    for t in range(Wm):
+        step(t)
+    torch.cuda.synchronize()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    for t in range(Wm, steps):
+        step(t)
+    e1.record()
+    torch.cuda.synchronize()
+    ms = e0.elapsed_time(e1) / T
+    read = B * N * Hkv * (D + 8 * (D // 32))
+    print(json.dumps({"mode": "paged_loop", "metric": "tokens/s/layer (append + attention over 4-bit pages per token)",
+                      "value": B / (ms / L / 1e3), "ms_per_step": ms, "steps": T, "warmup": Wm, "layers": L, "batch": B,
+                      "ctx_end": N, "page_bytes_read_per_layer": read, "page_gbs": read / (ms / L * 1e6)}), flush=True)
 
 
 VTOL_SWEEP = (0.0, 0.2, 0.1, 0.05, 0.02)
@@ -1138,6 +1208,10 @@ def main():
                     help="with --loop: fraction of each layer's FP16 blocks kept resident in HBM")
     ap.add_argument("--loop", action="store_true",
                     help="token-by-token decode loop (append + decode per layer and step)")
+    ap.add_argument("--cache", choices=["certified", "paged"], default="certified",
+                    help="with --loop: the certified tiered cache, or the paged 4-bit cache in device memory")
+    ap.add_argument("--rope", action="store_true",
+                    help="with --loop on the certified cache: rotate each step's queries and keys first")
     ap.add_argument("--profile-layer", dest="profile_layer", action="store_true",
                     help="run the fixed launch sequence of profile_layer (for ncu captures) and exit")
     ap.add_argument("--sweep", choices=["c5", "vtol"], default=None,
@@ -1150,7 +1224,7 @@ def main():
         sweep_vtol(args)
         return
     if args.loop:
-        decode_loop(args)
+        (paged_loop if args.cache == "paged" else decode_loop)(args)
         return
     if args.profile_layer:
         profile_layer(args)
