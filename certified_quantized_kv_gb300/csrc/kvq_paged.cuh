@@ -30,6 +30,7 @@
 namespace kvq {
 
 constexpr int PG = 64;   // tokens per page
+constexpr int MAX_KV_HEADS = 4096;
 
 template <int HD>
 struct Page {

@@ -92,13 +92,25 @@ struct Rotation {
   }
 };
 
-// Extremes of a group (eight lanes) of fp32 elements.
+// minimum and maximum that are NaN when an operand is
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Extremes of a group (eight lanes) of fp32 elements, both NaN when an element is.
 __device__ __forceinline__ float2 extremes(const float (&x)[E]) {
-  float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  float lo = min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), hi = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   return make_float2(lo, hi);
 }
@@ -106,10 +118,10 @@ __device__ __forceinline__ float2 extremes(const float (&x)[E]) {
 template <bool BF16>
 __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
   if (BF16) {
-    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&m);
   }
-  return h2_as_u32(__hmax2(u32_as_h2(a), u32_as_h2(b)));
+  return h2_as_u32(__hmax2_nan(u32_as_h2(a), u32_as_h2(b)));
 }
 template <bool BF16>
 __device__ __forceinline__ float2 extremes(const Quad& r) {
@@ -128,10 +140,11 @@ __device__ __forceinline__ float2 extremes(const Quad& r) {
 // quotient: they come from a product with the reciprocal, and the remainder d - code s, exact
 // near a half, tells where a neighbour is nearer, or as near and even (values on the binary16
 // grid meet exact halves in about one element of a hundred).  The slow path also clamps the codes,
-// which only elements beyond the rounded offset or the binary16 range need.
+// which only elements beyond the rounded offset or the binary16 range need.  Extremes that are NaN
+// make the offset NaN and the scale 0: the group then reads as NaN, whatever its codes.
 __device__ __forceinline__ uint32_t quantize(const float (&x)[E], float2 ext, bool down, __half& sh, __half& oh) {
   constexpr float RND = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, ties to even
-  const float lo = fminf(fmaxf(ext.x, -65504.f), 65504.f), hi = fminf(fmaxf(ext.y, -65504.f), 65504.f);
+  const float lo = min_nan(max_nan(ext.x, -65504.f), 65504.f), hi = min_nan(max_nan(ext.y, -65504.f), 65504.f);
   oh = __float2half_rn(down ? hi : lo);
   const float of = __half2float(oh), span = fmaxf(down ? of - lo : hi - of, 0.f);
   const float before = down ? ext.y - of : of - ext.x;   // how far the extreme lies before the offset,
@@ -346,7 +359,7 @@ kvq_status check_common(const char* fn, int dtype, int T, int Hkv, int hd, int n
   if (dtype != KVQ_F16 && dtype != KVQ_BF16) return paged_fail(KVQ_ERR_INVALID, fn, "dtype must be KVQ_F16 or KVQ_BF16");
   if (hd != 64 && hd != 128) return paged_fail(KVQ_ERR_INVALID, fn, "head_dim must be 64 or 128");
   if (T < 0) return paged_fail(KVQ_ERR_INVALID, fn, "n_tokens must be >= 0");
-  if (Hkv < 1) return paged_fail(KVQ_ERR_INVALID, fn, "n_kv_heads must be >= 1");
+  if (Hkv < 1 || Hkv > MAX_KV_HEADS) return paged_fail(KVQ_ERR_INVALID, fn, "n_kv_heads must be in 1..4096");
   if (n_pages < 1 || n_pages > (1 << 25))   // slots are int32
     return paged_fail(KVQ_ERR_INVALID, fn, "n_pages must be in 1..33554432");
   return KVQ_OK;
@@ -381,6 +394,8 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
     if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
     if (kvq_status s = check_strides(ot, oh, fn, "q_out")) return s;
     if ((T > 1 && ot == 0) || (Hq > 1 && oh == 0)) return paged_fail(KVQ_ERR_INVALID, fn, "q_out: rows must not overlap");
+    if (q == q_out && ((T > 1 && qt != ot) || (Hq > 1 && qh != oh)))
+      return paged_fail(KVQ_ERR_INVALID, fn, "q_out = q needs the same strides");
     if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
     if (kvq_status s = check_buffer(q_out, dev, 16, fn, "q_out")) return s;
   }

@@ -545,6 +545,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         if (tok0 + t < t_all || tok0 + t >= t_end) {
           reinterpret_cast<__half*>(pg + L::VS)[at] = __ushort_as_half(0);
           reinterpret_cast<__half*>(pg + L::VO)[at] = __ushort_as_half(0);
+        } else if (__hisnan(reinterpret_cast<const __half*>(pg + L::VO)[at])) {
+          // a value that is NaN: into the token's score, which the rows that do not see it mask
+          // (a weight of 0 would not)
+          reinterpret_cast<__half*>(pg + L::VO)[at] = __ushort_as_half(0);
+          reinterpret_cast<unsigned short*>(pg + L::KO)[t * G] = 0x7fff;
         }
       }
       // ordered before the bulk copy that will overwrite the stage
@@ -937,6 +942,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 const char* shape_error(int B, int Q, int Hq, int Hkv, int hd) {
   if (B < 0 || B > 2048) return "batch must be in 0..2048";
   if (Q < 1 || Q > 64) return "n_q_tokens must be in 1..64";
+  if (Hkv > MAX_KV_HEADS) return "n_kv_heads must be in 1..4096";
   if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 64) return "n_q_heads / n_kv_heads must be an integer in 1..64";
   if (hd != 64 && hd != 128) return "head_dim must be 64 or 128";
   return nullptr;
@@ -980,6 +986,7 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   if (window < 0) return paged_fail(KVQ_ERR_INVALID, fn, "window must be >= 0");
   if (!std::isfinite(scale)) return paged_fail(KVQ_ERR_INVALID, fn, "scale must be finite");
   if (B == 0) return KVQ_OK;
+  if (q == out) return paged_fail(KVQ_ERR_INVALID, fn, "out must not be q");
   if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
   int dev = 0, sms = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");
@@ -1005,6 +1012,8 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   a.RT = (a.rows + R - 1) / R;
   // one CTA per SM (the counters hold 1024), fewer when the table cannot hold that many units
   a.grid = (int)std::min<long long>(std::min(sms, 1024), (long long)B * max_pages * Hkv * a.RT);
+  if ((long long)B * (max_pages + PA_LEAD) * Hkv * a.RT / a.grid >= (1ll << 30))   // a CTA's positions are ints
+    return paged_fail(KVQ_ERR_INVALID, fn, "batch * max_pages * n_kv_heads is too large for one call");
   a.arrived = static_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + PA_COUNTERS);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -313,7 +313,8 @@ kvq_status kvq_dense_decode_noalloc(const void* q, const void* k, const void* v,
  * rint((x - o) / s), ties to even, clamped.  Values of odd slots count down from the
  * maximum instead (o = fp16 of the maximum, s negative), so that sums of codes over tokens
  * change sign from one token to the next and do not lose precision to a common offset.
- * Elements beyond the binary16 range are held as +-65504.  Slot p * 64 + i is token i of
+ * Elements beyond the binary16 range are held as +-65504; a NaN makes its group's offset NaN,
+ * so that the 32 channels read as NaN.  Slot p * 64 + i is token i of
  * page p.
  *
  * Element types of q, k, v and outputs: kvq_dtype.  Strided operands [tokens, heads, D]
@@ -392,8 +393,9 @@ kvq_status kvq_paged_page_bytes(int head_dim, size_t* bytes);
  *   positions  [n_tokens] int32, device
  *   pages      the pool; only the bytes of the given slots change
  *   q, q_out   optional (NULL): [n_tokens, n_q_heads, head_dim] strided, turned by the same
- *              positions in the same launch (as kvq_rope), for every token, skipped or not
- * head_dim 64 or 128.  One kernel.  n_tokens = 0 is a no-op.
+ *              positions in the same launch (as kvq_rope), for every token, skipped or not;
+ *              q_out may be q with the same strides, and must not overlap q, k or v otherwise
+ * head_dim 64 or 128, n_kv_heads 1..4096.  One kernel.  n_tokens = 0 is a no-op.
  * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
 kvq_status kvq_paged_append(const kvq_rope_plan* plan, int dtype, const void* k, int64_t k_token_stride,
                             int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
@@ -404,7 +406,8 @@ kvq_status kvq_paged_append(const kvq_rope_plan* plan, int dtype, const void* k,
 
 /* kvq_paged_gather -- read tokens back from pages: k, v [n_tokens, n_kv_heads, head_dim]
  * strided receive o + s * code of the slots (keys as turned by the append), computed in
- * fp32 and rounded to the element type; rows of slots outside the pool become 0.
+ * fp32 and rounded to the element type; rows of slots outside the pool become 0.  k and v
+ * must not overlap.
  * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
 kvq_status kvq_paged_gather(const void* pages, int n_pages, const int32_t* slots, int n_tokens, int n_kv_heads,
                             int head_dim, int dtype, void* k, int64_t k_token_stride, int64_t k_head_stride, void* v,
@@ -429,17 +432,19 @@ kvq_status kvq_paged_attention_workspace(int batch, int n_q_tokens, int n_q_head
  *   window      0: query i of a sequence of n tokens sees tokens 0..n - n_q_tokens + i;
  *               w > 0: only the last w of them
  *   scale       0: 1 / sqrt(head_dim)
- *   out         [batch, n_q_tokens, Hq, head_dim], contiguous, of q's type
+ *   out         [batch, n_q_tokens, Hq, head_dim], contiguous, of q's type; must not overlap q
  *   lse         optional (NULL): [batch, n_q_tokens, Hq] float, natural log of the sum of
  *               exp(scale q k), for merging with attention over other keys
  * A query that sees no token gets out = 0 and lse = -inf.  What pages hold behind a
- * sequence's length (NaN included) does not matter.
+ * sequence's length (NaN included) does not matter.  A key or value that is NaN reaches the
+ * outputs of the queries that see its token, and no others: those of the value's 32 channels,
+ * or all of the row.
  *   workspace   at least kvq_paged_attention_workspace(...) bytes, 16-byte aligned, its
  *               first 4096 bytes set to zero once, before the first call that uses it: every
  *               call leaves them zero (they count the arrivals of a row's pieces), whatever
  *               its shape.  Calls that share it must not overlap on the GPU.
- * One kernel.  Hq / Hkv an integer in 1..64, n_q_tokens 1..64, batch <= 2048, head_dim 64 or
- * 128, batch * max_pages < 2^30.  Scores and sums in fp32.  batch = 0 is a no-op.  Every
+ * One kernel.  Hq / Hkv an integer in 1..64, Hkv <= 4096, n_q_tokens 1..64, batch <= 2048,
+ * head_dim 64 or 128, batch * max_pages < 2^30.  Scores and sums in fp32.  batch = 0 is a no-op.  Every
  * device-side wait is bounded (2 s); one that runs out, which does not happen in correct
  * operation, makes the affected outputs NaN.
  * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */

@@ -603,6 +603,67 @@ def test_attention_refusals():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_is_held_as_nan(D, rotate, dt):
+    """A NaN makes its group of 32 channels NaN (a rotated one its partner's as well) and
+    nothing else."""
+    T, H = 70, 3
+    k, v, slots = _randn((T, H, D), dt, 1), _randn((T, H, D), dt, 2), torch.arange(T).int().cuda()
+    kw = dict(plan=kvq.RopePlan(D), positions=slots) if rotate else {}
+    got = []
+    for bad in (float("nan"), 0.0):
+        kx, vx = k.clone(), v.clone()
+        kx[5, 1, 7], kx[64, 2, D - 1], vx[6, 2, 33], vx[7, 0, 3], vx[7, 0, 60] = (bad,) * 5
+        pages = torch.zeros(2, H, kvq.paged_page_bytes(D), dtype=torch.uint8, device="cuda")
+        kvq.paged_append(pages, kx, vx, slots, **kw)
+        kb, vb = torch.empty_like(k), torch.empty_like(v)
+        kvq.paged_gather(pages, slots, kb, vb)
+        got.append((kb, vb))
+    kn, vn = torch.zeros(T, H, D, dtype=torch.bool), torch.zeros(T, H, D, dtype=torch.bool)
+    kn[5, 1, 0:32] = kn[64, 2, D - 32:] = vn[6, 2, 32:64] = vn[7, 0, 0:64] = True
+    if rotate:
+        kn[5, 1, D // 2:D // 2 + 32] = kn[64, 2, D // 2 - 32:D // 2] = True
+    for a, b, n in zip(got[0], got[1], (kn.cuda(), vn.cuda())):
+        assert torch.equal(a.isnan(), n) and torch.equal(a[~n], b[~n]) and not b.isnan().any()
+
+
+@pytest.mark.parametrize("D,Q,n_rep", [(128, 1, 4), (128, 2, 2), (128, 2, 4), (128, 4, 4), (64, 4, 1), (64, 4, 2), (64, 4, 4)])
+@pytest.mark.parametrize("token,window", [(69, 0), (68, 0), (10, 58), (10, 0)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_nan_reaches_the_queries_that_see_it(D, Q, n_rep, token, window, what):
+    N, H = 70, 2
+    k, v, slots = _randn((N, H, D), torch.float16, 1), _randn((N, H, D), torch.float16, 2), torch.arange(N).int().cuda()
+    q = _randn((1, Q, H * n_rep, D), torch.float16, 3)
+    got = []
+    for bad in (float("nan"), 0.0):
+        kx, vx = k.clone(), v.clone()
+        (kx if what == "k" else vx)[token, 1, 40] = bad
+        pages = torch.zeros(2, H, kvq.paged_page_bytes(D), dtype=torch.uint8, device="cuda")
+        kvq.paged_append(pages, kx, vx, slots)
+        got.append(_attend(q, pages, _ints([[0, 1]]), _ints([N]), window=window))
+    (a, la, _), (b, lb, _) = got
+    assert not b.isnan().any()
+    for i in range(Q):
+        end = N - Q + 1 + i
+        sees = token < end and (not window or token >= end - window)
+        r = slice(n_rep, 2 * n_rep)      # the rows of KV head 1
+        assert torch.equal(a[0, i, :n_rep], b[0, i, :n_rep]) and torch.equal(la[0, i, :n_rep], lb[0, i, :n_rep])
+        if sees:
+            assert (a[0, i, r] if what == "k" else a[0, i, r, 32:64]).isnan().all()
+        else:
+            assert torch.equal(a[0, i, r], b[0, i, r]) and torch.equal(la[0, i, r], lb[0, i, r])
+
+
+def test_attention_refuses_what_its_positions_cannot_count():
+    x = torch.zeros(1 << 16, dtype=torch.int32, device="cuda")
+    at = x.data_ptr()
+    status = kvq.load_library().kvq_paged_attention(0, at, 128, 128, at, 1, at, 1 << 24, 1 << 24, at, 63, 1, 4096, 4096, 128, 0, 0.0,
+                                                    at + 4096, None, at, 1 << 30, None)
+    assert status == kvq.KVQ_ERR_INVALID and b"too large for one call" in kvq.load_library().kvq_last_error()
+
+
 # --------------------------------------------------------------------------------------
 # streams, graphs, and the operators together
 # --------------------------------------------------------------------------------------

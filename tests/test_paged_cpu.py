@@ -201,3 +201,16 @@ def test_python_refuses_cpu_tensors_and_odd_operands():
         kvq.rope(x[0], pos, plan)
     with pytest.raises(ValueError):
         kvq.paged_attention(x[0], pages, pos.reshape(3, 1), pos, x)
+
+
+@pytest.mark.parametrize("bad", [dict(xt=256), dict(xh=256), dict(ot=256), dict(oh=256)])
+def test_rope_in_place_needs_the_same_strides(bad):
+    assert _rope(**bad) == kvq.KVQ_ERR_INVALID
+    assert b"same strides" in kvq.load_library().kvq_last_error()
+
+
+def test_more_refusals_before_any_cuda_call():
+    lib = kvq.load_library()
+    assert _attend() == kvq.KVQ_ERR_INVALID and b"out must not be q" in lib.kvq_last_error()
+    for status in (_append(Hkv=4097), _attend(Hkv=4097, Hq=4097)):
+        assert status == kvq.KVQ_ERR_INVALID and b"n_kv_heads" in lib.kvq_last_error()
