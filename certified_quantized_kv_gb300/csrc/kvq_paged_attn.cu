@@ -879,30 +879,22 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 
   // ---- groups that were cut ----
   float* cpart = a.part + (size_t)a.grid * PA_WARPS * PART;
-  // runs of pieces of one group within this CTA: that of a group begun in an earlier CTA (w =
-  // -1), then those of the groups that each warp starts and leaves open
+  // Runs of pieces of one group within this CTA: that of a group begun in an earlier CTA (w =
+  // -1), then those of the groups that a warp starts and leaves open.  Warps hold consecutive
+  // ranges, so an open piece that its warp did not start, and an ended one, belong to the group
+  // that the warp before left open: bit masks over the warps tell where each run ends.
   int2 away[2] = {make_int2(-1, 0), make_int2(-1, 0)};   // groups with pieces in other CTAs
-  for (int w = -1; w < PA_WARPS; ++w) {
-    int2 grp;
-    bool closed = false;
-    int first = w, n = 0, last = w;   // pieces: the open ones of warps first..last - 1 or last, then an ending one
-    if (w < 0) {
-      first = 0;
-      grp = ended[0].x >= 0 ? ended[0] : (open_at[0].x >= 0 && !open_new[0]) ? open_at[0] : make_int2(-1, 0);
-      if (grp.x < 0) continue;
-      closed = ended[0].x >= 0;
-      n = 1, last = 0;
-    } else {
-      grp = open_at[w];
-      if (grp.x < 0 || !open_new[w]) continue;
-      n = 1;
-    }
-    while (!closed && last + 1 < PA_WARPS) {
-      const int2 en = ended[last + 1], op = open_at[last + 1];
-      if (en.x == grp.x && en.y == grp.y) closed = true;
-      else if (!(op.x == grp.x && op.y == grp.y)) break;
-      ++n, ++last;
-    }
+  const bool is_end = lane < PA_WARPS && ended[lane].x >= 0, is_open = lane < PA_WARPS && open_at[lane].x >= 0;
+  const bool is_new = is_open && open_new[lane];
+  const uint32_t ends = __ballot_sync(0xffffffffu, is_end), news = __ballot_sync(0xffffffffu, is_new);
+  const uint32_t goes_on = __ballot_sync(0xffffffffu, is_open && !is_new);
+  // bit w + 1: a run starts in warp w
+  for (uint32_t left = (news << 1) | ((ends | goes_on) & 1u); left; left &= left - 1) {
+    const int w = __ffs(left) - 2;
+    const int f = w + __ffs(~(goes_on >> (w + 1))) - 1;   // the last warp with an open piece of it
+    const bool closed = (ends >> (f + 1)) & 1u;
+    const int first = max(w, 0), n = f + closed - first + 1;
+    const int2 grp = w < 0 && !(goes_on & 1u) ? ended[0] : open_at[first];
     const int slot = w >= 0;
     const bool all = closed && w >= 0;
     if (!all) away[slot] = grp;
@@ -922,11 +914,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     first_cta[k] = k ? (int)blockIdx.x : sp.cta_of(at + lead);
     if (threadIdx.x == 32 * k) {
       const int n = sp.cta_of(at + size - 1) - first_cta[k] + 1;
-      __threadfence();
-      const int before = atomicAdd(&a.arrived[first_cta[k]], 1);
+      // releases this CTA's pieces (written before the barrier) and acquires the others'
+      int before;
+      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + first_cta[k]) : "memory");
       final_n[k] = before == n - 1 ? n : 0;
       if (before == n - 1) a.arrived[first_cta[k]] = 0;
-      __threadfence();
     }
   }
   __syncthreads();
