@@ -393,62 +393,74 @@ class RopePlan:
 
 # The calls below are made once per layer and token, where their host time counts (a decoding
 # step of a few microseconds on the device): operands are checked with as few attribute reads
-# as that takes.
+# as that takes, and what they need of torch is looked up once.
+
+_torch = None
+
+
+def _lookup():
+    global _torch, _F16, _BF16, _I32, _raw_stream, _current_device
+    import torch
+    _F16, _BF16, _I32 = torch.float16, torch.bfloat16, torch.int32
+    # the address alone: building a Stream object costs 2.7 us
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
+    return torch
+
 
 def _rows(t, name, dtype, shape):
     """Address and (token, head) strides of a [tokens, heads, head_dim] operand whose rows
     are contiguous."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     a, b, c = t.stride()
-    if c != 1 and shape[2] != 1:
+    T, H, D = shape
+    if c != 1 and D != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # a dimension of one row has no stride to speak of
-    return t.data_ptr(), a if shape[0] > 1 else 8, b if shape[1] > 1 else 8
+    return t.data_ptr(), a if T > 1 else 8, b if H > 1 else 8
 
 
 def _ints(t, name, n):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not _I32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous torch.int32 tensor of {n} elements")
     return t.data_ptr()
 
 
 def _float_code(t, name) -> int:
-    import torch
     dt = t.dtype
-    if dt == torch.float16:
+    if dt is _F16:
         return 0
-    if dt == torch.bfloat16:
+    if dt is _BF16:
         return 1
     raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {dt}")
 
 
 def _device_of(names, first, *others) -> int:
     """Index of the CUDA device that all given tensors (None: absent) are on."""
+    if _torch is None:
+        _lookup()
     dev = first.get_device()
     if dev < 0:
         raise ValueError(f"{names.split()[0]} must be a CUDA tensor")
-    for k, t in enumerate(others):
+    for t in others:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"{names.split()[k + 1]} must be on {first.device}, like {names.split()[0]}")
+            name = next(n for n, o in zip(names.split()[1:], others) if o is t)
+            raise ValueError(f"{name} must be on {first.device}, like {names.split()[0]}")
     return dev
 
 
 def _call(dev, stream, fn, *args):
     """Run a library call on device `dev` and `stream` (the device's current one when None)."""
-    import torch
-    if stream is None:   # the address alone: building a Stream object costs 2.7 us
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        stream = raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
-    else:
-        stream = getattr(stream, "cuda_stream", stream)
-    if dev == torch.cuda.current_device():
+    stream = _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+    if dev == _current_device():
         status = fn(*args, stream or None)
     else:
-        with torch.cuda.device(dev):
+        with _torch.cuda.device(dev):
             status = fn(*args, stream or None)
     if status != KVQ_OK:
         _check(status)
@@ -458,15 +470,15 @@ def rope(x, positions, plan, out=None, stream=None):
     """Rotary positions (kvq_rope): x [T, H, head_dim] fp16 or bf16 with contiguous rows (any
     token and head strides, e.g. a slice of a fused projection), positions [T] int32.
     out=None allocates the result; out=x works in place.  Returns out."""
-    if x.dim() != 3:
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("x must be [n_tokens, n_heads, head_dim]")
     if out is None:
-        import torch
         if stream is not None:
             raise ValueError("out must be given with a stream")
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = (_torch or _lookup()).empty(shape, dtype=x.dtype, device=x.device)
     dev = _device_of("x positions out", x, positions, out)
-    code, shape, dt = _float_code(x, "x"), x.shape, x.dtype
+    code, dt = _float_code(x, "x"), x.dtype
     T, H, hd = shape
     if hd != plan.head_dim:
         raise ValueError(f"x must have head_dim {plan.head_dim}, got {hd}")
@@ -489,14 +501,14 @@ _PAGE_BYTES = {64: 5120, 128: 10240}
 
 def _pool(pages, n_kv_heads, head_dim):
     """Address and page count of a pool of pages."""
-    import torch
     nbytes = _PAGE_BYTES.get(head_dim)
     if nbytes is None:
         raise ValueError("head_dim must be 64 or 128")
-    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.shape[1:] != (n_kv_heads, nbytes) \
+    shape = pages.shape
+    if pages.dtype is not _torch.uint8 or len(shape) != 3 or shape[1] != n_kv_heads or shape[2] != nbytes \
             or not pages.is_contiguous():
         raise ValueError(f"pages must be a contiguous uint8 tensor [n_pages, {n_kv_heads}, {nbytes}]")
-    return pages.data_ptr(), pages.shape[0]
+    return pages.data_ptr(), shape[0]
 
 
 def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=None, stream=None):
@@ -506,10 +518,11 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
     64 + offset; outside the pool, e.g. -1: skipped; all distinct).  With a RopePlan and
     positions (int32 [T]) keys are rotated on the way, and q [T, n_q_heads, head_dim], when
     given, into q_out (which may be q)."""
-    if k.dim() != 3:
+    shape = k.shape
+    if len(shape) != 3:
         raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
     dev = _device_of("k v slots pages positions q q_out", k, v, slots, pages, positions, q, q_out)
-    code, shape, dt = _float_code(k, "k"), k.shape, k.dtype
+    code, dt = _float_code(k, "k"), k.dtype
     T, hkv, hd = shape
     if (plan is None) != (positions is None):
         raise ValueError("plan and positions go together")
@@ -517,9 +530,10 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
         raise ValueError("q and q_out go together")
     hq, qa, oa = 0, (None, 0, 0), (None, 0, 0)
     if q is not None:
-        if q.dim() != 3:
+        qs = q.shape
+        if len(qs) != 3:
             raise ValueError("q must be [n_tokens, n_q_heads, head_dim]")
-        hq = q.shape[1]
+        hq = qs[1]
         qa = _rows(q, "q", dt, (T, hq, hd))
         oa = qa if q_out is q else _rows(q_out, "q_out", dt, (T, hq, hd))
     _call(dev, stream, load_library().kvq_paged_append, None if plan is None else plan.address, code,
@@ -531,10 +545,11 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
 def paged_gather(pages, slots, k, v, stream=None):
     """Read tokens back from a pool of pages (kvq_paged_gather): k, v [T, n_kv_heads, head_dim]
     fp16 or bf16 receive what the slots hold (rows of slots outside the pool become 0)."""
-    if k.dim() != 3:
+    shape = k.shape
+    if len(shape) != 3:
         raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
     dev = _device_of("pages slots k v", pages, slots, k, v)
-    code, shape, dt = _float_code(k, "k"), k.shape, k.dtype
+    code, dt = _float_code(k, "k"), k.dtype
     T, hkv, hd = shape
     _call(dev, stream, load_library().kvq_paged_gather, *_pool(pages, hkv, hd), _ints(slots, "slots", T), T, hkv, hd,
           code, *_rows(k, "k", dt, shape), *_rows(v, "v", dt, shape))
@@ -558,12 +573,12 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     its last dimension, or None.  `workspace` is a device uint8 tensor of at least
     paged_attention_workspace(...) bytes, zeroed once before its first use (allocated here
     when omitted).  Returns `workspace` so a caller can reuse it."""
-    import torch
-    if q.dim() not in (3, 4):
+    shape = q.shape
+    if len(shape) not in (3, 4):
         raise ValueError("q must be [batch, n_q_heads, head_dim] or [batch, n_q_tokens, n_q_heads, head_dim]")
     dev = _device_of("q pages page_table seq_lens out lse workspace", q, pages, page_table, seq_lens, out, lse,
                      workspace)
-    code, shape, st, dt = _float_code(q, "q"), q.shape, q.stride(), q.dtype
+    code, st, dt = _float_code(q, "q"), q.stride(), q.dtype
     B, hq, hd = shape[0], shape[-2], shape[-1]
     Q = shape[1] if len(shape) == 4 else 1
     if st[-1] != 1:
@@ -571,23 +586,24 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     qt = st[1] if Q > 1 else st[0] if B > 1 else 8
     if Q > 1 and B > 1 and st[0] != Q * st[1]:
         raise ValueError("q: the query tokens must be evenly spaced in memory")
-    if pages.dim() != 3:
+    pool = pages.shape
+    if len(pool) != 3:
         raise ValueError("pages must be [n_pages, n_kv_heads, page bytes]")
-    hkv = pages.shape[1]
+    hkv = pool[1]
     pool = _pool(pages, hkv, hd)
-    if out.dtype != dt or out.shape != shape or not out.is_contiguous():
+    if out.dtype is not dt or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and type")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1] or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not _torch.float32 or lse.shape != shape[:-1] or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32, of q's shape without the last dimension")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+    ts = page_table.stride()
+    if page_table.dtype is not _I32 or len(ts) != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table must be int32 [{B}, max_pages]")
-    (rows, max_pages), ts = page_table.shape, page_table.stride()
-    if rows != B:
-        raise ValueError(f"page_table must be int32 [{B}, max_pages]")
+    max_pages = page_table.shape[1]
     if ts[1] != 1 and max_pages > 1:
         raise ValueError("page_table: the last dimension must be contiguous")
     lens = _ints(seq_lens, "seq_lens", B)
     if workspace is None:
+        torch = _torch
         with torch.cuda.device(dev):
             workspace = torch.zeros(paged_attention_workspace(B, Q, hq, hkv, hd), dtype=torch.uint8, device=q.device)
             if stream is not None:
@@ -595,7 +611,7 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
                 other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
                 other.wait_stream(torch.cuda.current_stream())
                 workspace.record_stream(other)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    elif workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _call(dev, stream, load_library().kvq_paged_attention, code, q.data_ptr(), qt, st[-2] if hq > 1 else 8, *pool,
           page_table.data_ptr(), ts[0] if B > 1 else max_pages, max_pages, lens, B, Q, hq, hkv, hd, window,
