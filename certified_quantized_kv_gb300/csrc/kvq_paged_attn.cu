@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   // one it leaves open (started in this warp or before)
   __shared__ int2 ended[PA_WARPS], open_at[PA_WARPS];
   __shared__ bool open_new[PA_WARPS];
-  __shared__ int wsum[PA_WARPS], wcnt[PA_WARPS];
+  __shared__ int wsum[PA_WARPS];
   __shared__ int final_n[2];
   __shared__ const float* piece_at[PA_WARPS][2];   // where a warp's ended and open pieces lie
   int* pre = reinterpret_cast<int*>(sm + PA_WARPS * (PA_STAGES * L::BYTES + PaStage<HD>::FLOATS * 4));   // [B + 1] positions before each sequence
@@ -296,22 +296,22 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 
   // pages of every sequence and their sum, then the positions before each sequence
   auto pages_of = [&](int len) { return len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0; };
-  int pages = 0, full = 0;
+  int pages = 0;
   for (int b = threadIdx.x; b < a.B; b += PA_THREADS) {
     const int len = pa_len(a, b);
     slen[b] = len;
     pages += pages_of(len);
-    full += len > 0;
   }
   pages = __reduce_add_sync(0xffffffffu, pages);
-  full = __reduce_add_sync(0xffffffffu, full);
-  if (lane == 0) wsum[warp] = pages, wcnt[warp] = full;
+  if (lane == 0) wsum[warp] = pages;
   __syncthreads();
-  pages = full = 0;
+  pages = 0;
 #pragma unroll
-  for (int w = 0; w < PA_WARPS; ++w) pages += wsum[w], full += wcnt[w];
+  for (int w = 0; w < PA_WARPS; ++w) pages += wsum[w];
   const int U = a.Hkv * a.RT;
-  const int lead = ((long long)pages + (long long)full * PA_LEAD) * U >= (long long)a.grid * PA_WARPS * (PA_LEAD + 2) ? PA_LEAD : 0;
+  // (8 sequences of 1..4096 tokens, 1.6 pages per warp: 16.2 us, 18.2 without lead positions; 48 of
+  // 512, less than a page per warp: 12.4 us, 11.5 without)
+  const int lead = (long long)pages * U >= (long long)a.grid * PA_WARPS ? PA_LEAD : 0;
   if (threadIdx.x == 0) pre[0] = 0;
   for (int base = 0, run = 0; base < a.B; base += PA_THREADS) {
     const int b = base + threadIdx.x;
@@ -940,8 +940,18 @@ const char* shape_error(int B, int Q, int Hq, int Hkv, int hd) {
   return nullptr;
 }
 
-// Query rows per tile: the smallest that holds a KV head's rows, 16 at most.
-int tile_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+// Query rows per tile: 4 or 8 if those hold a KV head's rows, else 16 or, of 8, twice as many tiles,
+// each of which reads the pages again (from L2).  Tiles of 16 take less time per page and row (16 rows, 8
+// sequences of 16384 tokens: 64 us, 72 with tiles of 8; of 8192: 41 and 45), tiles of 8 start and
+// finish faster (of 4096: 29 us, 31 with tiles of 16; of 1024: 17 and 19), and 17 to 24 rows fill
+// three of them (20 rows, 8 sequences of 8192: 58 us, 64 with two tiles of 16).  The lengths are
+// not known on the host, the most pages are.
+constexpr int PA_FEW = 4;   // pages per warp, if all were in use
+int tile_rows(int rows, long long most_pages, int sms) {
+  if (rows <= 8) return rows <= 4 ? 4 : 8;
+  if (rows > 16 && rows <= 24) return 8;
+  return most_pages * ((rows + 15) / 16) < (long long)sms * PA_WARPS * PA_FEW ? 8 : 16;
+}
 
 cudaError_t sm_count(int* sms) {
   int dev = 0;
@@ -952,7 +962,8 @@ cudaError_t sm_count(int* sms) {
 // arrival counters, then pieces: one per warp and two per CTA
 constexpr size_t PA_COUNTERS = 4096;
 size_t ws_bytes(int sms, int Q, int Hq, int Hkv, int hd) {
-  return PA_COUNTERS + (size_t)sms * (PA_WARPS + 2) * tile_rows(Q * (Hq / Hkv)) * (hd + 2) * sizeof(float);
+  const int rows = Q * (Hq / Hkv);
+  return PA_COUNTERS + (size_t)sms * (PA_WARPS + 2) * (rows <= 4 ? 4 : rows <= 8 ? 8 : 16) * (hd + 2) * sizeof(float);
 }
 
 template <int HD, int R>
@@ -1000,7 +1011,7 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   a.window = std::min(window, 1 << 30);   // lengths stay below 2^30
   a.scale_log2 = (scale != 0.f ? scale : 1.f / std::sqrt((float)hd)) * LOG2E_F;
   a.bf16 = dtype == KVQ_BF16;
-  const int R = tile_rows(a.rows);
+  const int R = tile_rows(a.rows, (long long)B * max_pages * Hkv, sms);
   a.RT = (a.rows + R - 1) / R;
   // one CTA per SM (the counters hold 1024), fewer when the table cannot hold that many units
   a.grid = (int)std::min<long long>(std::min(sms, 1024), (long long)B * max_pages * Hkv * a.RT);

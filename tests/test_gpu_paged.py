@@ -460,6 +460,41 @@ def test_attention(lens, Q, Hq, Hkv, D, window, dt):
     assert torch.equal(out, out3)
 
 
+def _widened(table, columns=9000):
+    """The table with room for more pages: as many as make the call use its tiles of 16 rows."""
+    return np.concatenate([table, np.full((len(table), columns - table.shape[1]), -1, np.int32)], 1)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("lens,Q,Hq,Hkv,D,window", [
+    ([300, 5], 1, 16, 1, 128, 0),
+    ([450], 1, 96, 2, 64, 0),                            # 48 rows
+    ([129], 1, 64, 1, 128, 0),
+    ([300, 2, 0, 65], 3, 8, 2, 128, 0),                  # twelve rows
+    ([1, 700], 5, 10, 5, 128, 0),                        # ten
+    ([400, 66], 5, 6, 2, 64, 70),
+    ([200, 63], 16, 4, 1, 128, 0),
+    ([640, 64], 1, 27, 3, 128, 64),                      # nine
+    ([100], 64, 2, 2, 64, 33),
+    ([3000, 64 * 20], 4, 32, 8, 128, 0),                 # split over the GPU
+    ([9000], 3, 32, 2, 64, 0),
+    ([129] * 40 + [0] * 7, 7, 8, 4, 128, 0),
+])
+def test_attention_in_tiles_of_16_rows(lens, Q, Hq, Hkv, D, window, dt):
+    pages, table, kv = _cache(lens, Hkv, D, seed=sum(lens) + Q)
+    q = _randn((len(lens), Q, Hq, D), dt, 5, 2.0)
+    wide = torch.from_numpy(_widened(table)).cuda()
+    out, lse, ws = _attend(q, torch.from_numpy(pages).cuda(), wide, _ints(lens), window)
+    _check_attention(out, lse, q, kv, table, lens, window, None)
+    out2, lse2, _ = _attend(q, torch.from_numpy(pages).cuda(), wide, _ints(lens), window, workspace=ws)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    # tiles of 8 rows in the same workspace, then tiles of 16 again
+    out3, lse3, _ = _attend(q, torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda(), _ints(lens), window, workspace=ws)
+    _check_attention(out3, lse3, q, kv, table, lens, window, None)
+    out4, lse4, _ = _attend(q, torch.from_numpy(pages).cuda(), wide, _ints(lens), window, workspace=ws)
+    assert torch.equal(out, out4) and torch.equal(lse, lse4)
+
+
 @pytest.mark.parametrize("lens,Hq,Hkv,D,Q", [
     ([4096 + 37], 32, 8, 128, 1),          # one sequence split over the GPU
     ([40000], 4, 1, 128, 1),               # one group split over every warp
@@ -632,7 +667,8 @@ def test_nan_is_held_as_nan(D, rotate, dt):
 @pytest.mark.parametrize("D,Q,n_rep", [(128, 1, 4), (128, 2, 2), (128, 2, 4), (128, 4, 4), (64, 4, 1), (64, 4, 2), (64, 4, 4)])
 @pytest.mark.parametrize("token,window", [(69, 0), (68, 0), (10, 58), (10, 0)])
 @pytest.mark.parametrize("what", ["k", "v"])
-def test_nan_reaches_the_queries_that_see_it(D, Q, n_rep, token, window, what):
+@pytest.mark.parametrize("columns", [2, 9000])     # (9000: tiles of 16 rows for more than eight)
+def test_nan_reaches_the_queries_that_see_it(D, Q, n_rep, token, window, what, columns):
     N, H = 70, 2
     k, v, slots = _randn((N, H, D), torch.float16, 1), _randn((N, H, D), torch.float16, 2), torch.arange(N).int().cuda()
     q = _randn((1, Q, H * n_rep, D), torch.float16, 3)
@@ -642,7 +678,7 @@ def test_nan_reaches_the_queries_that_see_it(D, Q, n_rep, token, window, what):
         (kx if what == "k" else vx)[token, 1, 40] = bad
         pages = torch.zeros(2, H, kvq.paged_page_bytes(D), dtype=torch.uint8, device="cuda")
         kvq.paged_append(pages, kx, vx, slots)
-        got.append(_attend(q, pages, _ints([[0, 1]]), _ints([N]), window=window))
+        got.append(_attend(q, pages, _ints(_widened(np.array([[0, 1]], np.int32), columns).tolist()), _ints([N]), window=window))
     (a, la, _), (b, lb, _) = got
     assert not b.isnan().any()
     for i in range(Q):
