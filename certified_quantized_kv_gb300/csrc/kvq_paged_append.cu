@@ -28,64 +28,85 @@ struct AppendPagedArgs {
   RopeArgs q;
 };
 
-constexpr int E = 4;   // neighbouring elements of a row that a lane holds
-struct Quad {
-  uint32_t w[2];
+constexpr int E = 8;   // neighbouring elements of a row that a lane holds
+struct Octet {
+  uint32_t w[4];
   __device__ __forceinline__ void load(const unsigned short* p) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x, w[1] = v.y;
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  __device__ __forceinline__ void unpack(float (&x)[E], bool bf16) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 p = pair_to_f2(w[k], bf16);
+      x[2 * k] = p.x, x[2 * k + 1] = p.y;
+    }
   }
 };
 
-// Rotation of rows spread over HD / 4 lanes at one token's position.  The other element of a
+// Rotation of rows spread over HD / 8 lanes at one token's position.  The other element of a
 // pair is in the same lane (INTERLEAVED), or a whole number of lanes away (LANES), or, when half of
-// rotary_dim is no multiple of 4, anywhere (ELEMENTS).
+// rotary_dim is no multiple of 8, anywhere (ELEMENTS: through shared memory).
 enum class Turn { NONE, INTERLEAVED, LANES, ELEMENTS };
 template <int HD, Turn TURN, bool BF16>
 struct Rotation {
-  int from[E], el[E];
   float c[E], s[E];  // y = x c + other s (s carries the sign; elements not rotated: 1, 0)
-  __device__ __forceinline__ void set(const kvq_rope_plan& P, const uint64_t* steps, const int32_t* pos, int lane) {
+  int half, ch, from;   // this lane's first channel, the lane with the others (LANES)
+  __device__ __forceinline__ bool in(int e) const { return ch + e < 2 * half; }
+  __device__ __forceinline__ void set(const kvq_rope_plan& P, const uint64_t* steps, int at, int lane) {
     if (TURN == Turn::NONE) return;
-    const int half = P.rotary_dim / 2, at = *pos, sub = lane % (HD / E);
+    half = P.rotary_dim / 2;
+    ch = E * (lane % (HD / E));
+    auto turn = [&](int i) { return rope_cos_sin(at, steps[i], P.magnitude); };
+    if (TURN == Turn::INTERLEAVED) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int ch = E * sub + e;
-      const bool in = ch < P.rotary_dim, second = TURN == Turn::INTERLEAVED ? (e & 1) : ch >= half;
-      const int i = TURN == Turn::INTERLEAVED ? ch >> 1 : second ? ch - half : ch;
-      const int other = !in ? ch : second ? ch - half : ch + half;
-      from[e] = lane - sub + other / E, el[e] = other % E;
-      float2 cs = make_float2(1.f, 0.f);
-      if (TURN == Turn::INTERLEAVED && (e & 1)) cs = make_float2(c[e ^ 1], -s[e ^ 1]);
-      else if (in) cs = rope_cos_sin(at, steps[i], P.magnitude);
-      c[e] = cs.x;
-      s[e] = second ? cs.y : -cs.y;
-    }
-  }
-  __device__ __forceinline__ void apply(const Quad& r, float (&y)[E]) const {
-    float x[E], o[E];
+      for (int e = 0; e < E; e += 2) {
+        const float2 cs = in(e) ? turn((ch + e) / 2) : make_float2(1.f, 0.f);
+        c[e] = c[e + 1] = cs.x, s[e] = -cs.y, s[e + 1] = cs.y;
+      }
+    } else if (TURN == Turn::LANES) {
+      // both lanes of a pair of lanes need the same eight turns: each forms four of them
+      const bool second = ch >= half;
+      from = in(0) ? lane + (second ? -half : half) / E : lane;
+      const int i0 = second ? ch - half + 4 : ch;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float2 p = pair_to_f2(r.w[k], BF16);
-      x[2 * k] = p.x, x[2 * k + 1] = p.y;
-    }
+      for (int e = 0; e < 4; ++e) {
+        const float2 cs = in(0) ? turn(i0 + e) : make_float2(1.f, 0.f);
+        const float x = __shfl_sync(0xffffffffu, cs.x, from), y = __shfl_sync(0xffffffffu, cs.y, from);
+        c[e] = second ? x : cs.x, s[e] = second ? y : -cs.y;
+        c[4 + e] = second ? cs.x : x, s[4 + e] = second ? cs.y : -y;
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = TURN == Turn::INTERLEAVED ? x[e ^ 1] : 0.f;
-    if (TURN == Turn::LANES) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float2 p = pair_to_f2(__shfl_sync(0xffffffffu, r.w[k], from[0]), BF16);
-        o[2 * k] = p.x, o[2 * k + 1] = p.y;
+      for (int e = 0; e < E; ++e) {
+        const bool second = ch + e >= half;
+        const float2 cs = in(e) ? turn(second ? ch + e - half : ch + e) : make_float2(1.f, 0.f);
+        c[e] = cs.x, s[e] = second ? cs.y : -cs.y;
       }
     }
-    if (TURN == Turn::ELEMENTS) {
+  }
+  // room: 16 bytes per lane (ELEMENTS)
+  __device__ __forceinline__ void apply(const Octet& r, float (&y)[E], uint4* room, int lane) const {
+    float x[E], o[E];
+    r.unpack(x, BF16);
+    if (TURN == Turn::INTERLEAVED) {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
+      for (int e = 0; e < E; ++e) o[e] = in(e) ? x[e ^ 1] : 0.f;
+    } else if (TURN == Turn::LANES) {
+      Octet p;
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const float v = __shfl_sync(0xffffffffu, x[k], from[e]);
-          if (el[e] == k) o[e] = v;
-        }
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = __shfl_sync(0xffffffffu, r.w[k], from);
+        p.w[k] = in(0) ? w : 0u;
+      }
+      p.unpack(o, BF16);
+    } else if (TURN == Turn::ELEMENTS) {
+      room[lane] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+      __syncwarp();
+      const int row = (lane - lane % (HD / E)) * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = in(e) ? elem_to_f(room, row + (ch + e >= half ? ch + e - half : ch + e + half), BF16) : 0.f;
+      __syncwarp();
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = TURN == Turn::NONE ? x[e] : fmaf(x[e], c[e], o[e] * s[e]);
@@ -104,11 +125,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Extremes of a group (eight lanes) of fp32 elements, both NaN when an element is.
+// Extremes of a group (four lanes) of fp32 elements, both NaN when an element is.
 __device__ __forceinline__ float2 extremes(const float (&x)[E]) {
-  float lo = min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), hi = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
+  float lo = min_nan(min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), min_nan(min_nan(x[4], x[5]), min_nan(x[6], x[7])));
+  float hi = max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
+  for (int o = 1; o < 4; o <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
@@ -124,17 +146,18 @@ __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
   return h2_as_u32(__hmax2_nan(u32_as_h2(a), u32_as_h2(b)));
 }
 template <bool BF16>
-__device__ __forceinline__ float2 extremes(const Quad& r) {
-  const uint32_t n0 = r.w[0] ^ 0x80008000u, n1 = r.w[1] ^ 0x80008000u;
-  const uint32_t hi = max_pair<BF16>(r.w[0], r.w[1]), lo = max_pair<BF16>(n0, n1);
+__device__ __forceinline__ float2 extremes(const Octet& r) {
+  constexpr uint32_t NEG = 0x80008000u;
+  const uint32_t hi = max_pair<BF16>(max_pair<BF16>(r.w[0], r.w[1]), max_pair<BF16>(r.w[2], r.w[3]));
+  const uint32_t lo = max_pair<BF16>(max_pair<BF16>(r.w[0] ^ NEG, r.w[1] ^ NEG), max_pair<BF16>(r.w[2] ^ NEG, r.w[3] ^ NEG));
   uint32_t m = max_pair<BF16>(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) m = max_pair<BF16>(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 1; o < 4; o <<= 1) m = max_pair<BF16>(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float2 p = pair_to_f2(m, BF16);
   return make_float2(-p.y, p.x);
 }
 
-// Scale, offset and packed codes (4 bits each, from bit 0) of this lane's four elements of a
+// Scale, offset and packed codes (4 bits each, from bit 0) of this lane's elements of a
 // group with extremes lo and hi.  The scale is the smallest binary16 h with 15 h >= the span (15 h
 // is exact in fp32), which is the span / 15 rounded up.  Codes are rint(d / |s|) for the exact
 // quotient: they come from a product with the reciprocal, and the remainder d - code s, exact
@@ -156,129 +179,135 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], float2 ext, bo
   const float sa = __half2float(sh), s = down ? -sa : sa, half = 0.5f * sa;
   const float inv = sa > 0.f ? __fdividef(1.f, s) : 0.f;   // |s| lies in [2^-24, 2^14]
   const float2 rnd = make_float2(RND, RND);
-  float2 t[2], r[2];
+  float2 t[E / 2], r[E / 2];
+  float worst = fmaxf(before, behind);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < E / 2; ++k) {
     const float2 d = sub2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(of, of));
     t[k] = fma2(d, make_float2(inv, inv), rnd);   // bits: RND's plus the code
     r[k] = fma2(sub2(rnd, t[k]), make_float2(s, s), d);
+    worst = fmaxf(worst, fmaxf(fabsf(r[k].x), fabsf(r[k].y)));
   }
-  const float worst = fmaxf(fmaxf(fabsf(r[0].x), fabsf(r[0].y)), fmaxf(fabsf(r[1].x), fabsf(r[1].y)));
-  if (fmaxf(fmaxf(worst, before), behind) >= half) {
+  if (worst >= half) {
     auto fix = [&](float xe, float& te, float re) {
       const bool off = fabsf(re) > half || (fabsf(re) == half && (__float_as_uint(te) & 1u));
       const float to = off ? te + ((re < 0.f) == down ? 1.f : -1.f) : te;
       // beyond what the sum with RND holds as an integer, te is far from every code
       te = sa > 0.f ? fminf(fmaxf(to, RND), RND + 15.f) : RND;
     };
-    fix(x[0], t[0].x, r[0].x), fix(x[1], t[0].y, r[0].y), fix(x[2], t[1].x, r[1].x), fix(x[3], t[1].y, r[1].y);
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) fix(x[2 * k], t[k].x, r[k].x), fix(x[2 * k + 1], t[k].y, r[k].y);
   }
   if (down) sh = __hneg(sh);
-  // RND's bits lie above the codes' 16
-  return __float_as_uint(t[0].x) + (__float_as_uint(t[0].y) << 4) + (__float_as_uint(t[1].x) << 8) + (__float_as_uint(t[1].y) << 12);
+  // codes side by side, less the bits of RND (modulo 2^32)
+  constexpr uint32_t BITS = 0x4B400000u;
+  uint32_t code = 0u - (BITS + (BITS << 4) + (BITS << 8));   // (22 zeros at the end: nothing is left from << 12 on)
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) code += (__float_as_uint(t[k].x) << (8 * k)) + (__float_as_uint(t[k].y) << (8 * k + 4));
+  return code;
 }
 
-// One warp per item: a token's KV heads [h, h + a.per), one at a time at head_dim 128 and two at 64,
-// with cos and sin formed once per item and the rows of two steps on their way at once.  The
-// other blocks turn q, a thread per V pairs; the two kinds are spread over the grid in turn, since
-// the first are bound by their arithmetic and the second by HBM.
+// One warp per item: two tokens at head_dim 128, four at 64 (eight elements per lane: what is done once
+// per group and lane, the extremes and the scale, costs half of what it does with four: 32768
+// tokens without q 60 us, 79 with four), and of each the KV heads [h, h + a.per), one after the other
+// with cos and sin formed once.  The other blocks turn q, a thread per V pairs.
+//
+// The KV blocks are bound by the issue of their instructions (unpacking, rotation, the shuffles of
+// the extremes, the verified scale and codes), the q blocks by HBM; so the two kinds are spread
+// over the grid in turn.  32768 tokens of 32 + 8 heads of 128: 713 MB in 132 us (5.4 TB/s); 168
+// with the read-back behind it, where registers for 7 blocks per SM give 173, for 6 180.
 constexpr int APPEND_THREADS = 128;
 template <int HD, Turn TURN, int V, bool BF16>
 __global__ void __launch_bounds__(APPEND_THREADS, 8) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
   using L = Page<HD>;
-  constexpr int LANES = HD / E, HEADS = 32 / LANES, KU = 2;   // lanes of a row, heads of a step, steps at once
+  constexpr int LANES = HD / E, TOKENS = 32 / LANES;   // lanes of a row, tokens of an item
   constexpr int WARPS = APPEND_THREADS / 32;
   __shared__ __align__(16) uint64_t steps[128];
+  __shared__ uint4 rooms[TURN == Turn::ELEMENTS ? APPEND_THREADS : 1];
   pdl_trigger();
   if (TURN != Turn::NONE) load_steps(P, steps);
   pdl_wait();
   // block b is KV block number floor(b kv / all) when that number changes behind it
-  const int k0 = (int)((long long)blockIdx.x * a.kv_blocks / gridDim.x), k1 = (int)((blockIdx.x + 1ll) * a.kv_blocks / gridDim.x);
+  const unsigned k0 = blockIdx.x * a.kv_blocks / gridDim.x, k1 = (blockIdx.x + 1) * a.kv_blocks / gridDim.x;   // (products below 2^26)
   if (V > 0 && k0 == k1) {
     rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16, APPEND_THREADS, false>(P, steps, nullptr, a.q, (long long)(blockIdx.x - k0) * APPEND_THREADS,
                                                                           (long long)(gridDim.x - a.kv_blocks) * APPEND_THREADS);
     return;
   }
-  const int lane = threadIdx.x & 31, sub = lane % LANES, hh = lane / LANES, g = sub / 8, j = sub % 8;
+  const int lane = threadIdx.x & 31, sub = lane % LANES, hh = lane / LANES, g = sub / 4, j = sub % 4;
+  uint4* room = rooms + (TURN == Turn::ELEMENTS ? threadIdx.x - lane : 0);
   const int items = (a.Hkv + a.per - 1) / a.per;
-  const long long n = (long long)a.T * items;
-  for (long long base = (long long)k0 * WARPS; base < n; base += (long long)a.kv_blocks * WARPS) {
-    const long long u = base + (threadIdx.x >> 5), t = u / items;
-    const int slot = u < n ? a.slots[t] : -1;
-    if (slot < 0 || slot / PG >= a.n_pages) continue;
-    const int at = slot % PG, h0 = (int)(u - t * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
+  const long long n = ((long long)a.T + TOKENS - 1) / TOKENS * items;
+  for (long long u = (long long)k0 * WARPS + (threadIdx.x >> 5); u < n; u += (long long)a.kv_blocks * WARPS) {
+    const long long tp = quotient(u, items), t = tp * TOKENS + hh;
+    const int slot = t < a.T ? a.slots[t] : -1;
+    const bool live = slot >= 0 && slot / PG < a.n_pages;
+    if (!__any_sync(0xffffffffu, live)) continue;
+    const int at = live ? slot % PG : 0, h0 = (int)(u - tp * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
     const bool down = at & 1;
-    const unsigned short* kp = static_cast<const unsigned short*>(a.k) + t * a.kt + (h0 + hh) * a.kh + E * sub;
-    const unsigned short* vp = static_cast<const unsigned short*>(a.v) + t * a.vt + (h0 + hh) * a.vh + E * sub;
+    const unsigned short* kp = static_cast<const unsigned short*>(a.k) + t * a.kt + h0 * a.kh + E * sub;
+    const unsigned short* vp = static_cast<const unsigned short*>(a.v) + t * a.vt + h0 * a.vh + E * sub;
     // this lane's bytes of the codes, and its group's scale and offset (lane j = 0 writes)
-    unsigned char* pg = a.pages + ((size_t)(slot / PG) * a.Hkv + h0 + hh) * L::BYTES;
-    unsigned char* kc = pg + at * L::ROW + (j >> 1) * 4 * L::G + 4 * g + 2 * (j & 1);
-    unsigned char* vc = pg + L::VC + vcode_at<HD>(at, j * 2 * L::G + 2 * g);
+    unsigned char* pg = a.pages + ((size_t)(live ? slot / PG : 0) * a.Hkv + h0) * L::BYTES;
+    unsigned char* kc = pg + at * L::ROW + j * 4 * L::G + 4 * g;
+    unsigned char* vc = pg + L::VC + vcode_at<HD>(at, 2 * j * 2 * L::G + 2 * g);   // and 2G bytes on
     __half* ks = reinterpret_cast<__half*>(pg + L::KS) + at * L::G + g;
     __half* vs = reinterpret_cast<__half*>(pg + L::VS) + g * PG + vscale_at(at);
     Rotation<HD, TURN, BF16> rot;
-    for (int h = h0; h < h1; h += KU * HEADS) {   // (the same for the whole warp)
-      Quad rk[KU], rv[KU];
+    for (int h = h0; h < h1; ++h) {
+      Octet rk = {}, rv = {};
+      if (live) rk.load(kp), rv.load(vp);
+      if (TURN != Turn::NONE && h == h0) rot.set(P, steps, live ? a.pos[t] : 0, lane);
 #pragma unroll
-      for (int k = 0; k < KU; ++k) {
-        rk[k].w[0] = rk[k].w[1] = rv[k].w[0] = rv[k].w[1] = 0u;
-        if (h + k * HEADS + hh < h1) {
-          rk[k].load(kp);
-          rv[k].load(vp);
-          kp += HEADS * a.kh, vp += HEADS * a.vh;
+      for (int kv = 0; kv < 2; ++kv) {
+        float x[E];
+        float2 ext;
+        if (kv || TURN == Turn::NONE) {
+          const Octet& r = kv ? rv : rk;
+          ext = extremes<BF16>(r);
+          r.unpack(x, BF16);
+        } else {
+          rot.apply(rk, x, room, lane);
+          ext = extremes(x);
         }
-      }
-      if (h == h0) rot.set(P, steps, a.pos + t, lane);
-#pragma unroll
-      for (int k = 0; k < KU; ++k) {
-        if (h + k * HEADS >= h1) continue;
-        const bool live = HEADS == 1 || h + k * HEADS + hh < h1;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          float x[E];
-          float2 ext;
-          if (kv || TURN == Turn::NONE) {
-            const Quad& r = kv ? rv[k] : rk[k];
-            ext = extremes<BF16>(r);
-            const float2 p = pair_to_f2(r.w[0], BF16), q = pair_to_f2(r.w[1], BF16);
-            x[0] = p.x, x[1] = p.y, x[2] = q.x, x[3] = q.y;
+        __half s, o;
+        const uint32_t code = quantize(x, ext, kv && down, s, o);
+        if (live) {
+          if (kv) {
+            *reinterpret_cast<unsigned short*>(vc) = (unsigned short)code;
+            *reinterpret_cast<unsigned short*>(vc + 2 * L::G) = (unsigned short)(code >> 16);
           } else {
-            rot.apply(rk[k], x);
-            ext = extremes(x);
+            *reinterpret_cast<uint32_t*>(kc) = code;
           }
-          __half s, o;
-          const uint32_t code = quantize(x, ext, kv && down, s, o);
-          if (live) {
-            *reinterpret_cast<unsigned short*>((kv ? vc : kc) + k * HEADS * L::BYTES) = (unsigned short)code;
-            if (j == 0) {
-              __half* so = (kv ? vs : ks) + k * HEADS * (L::BYTES / 2);
-              so[0] = s;
-              so[L::SCALES / 2] = o;
-            }
+          if (j == 0) {
+            __half* so = kv ? vs : ks;
+            so[0] = s;
+            so[L::SCALES / 2] = o;
           }
         }
       }
-      kc += KU * HEADS * L::BYTES, vc += KU * HEADS * L::BYTES, ks += KU * HEADS * L::BYTES / 2, vs += KU * HEADS * L::BYTES / 2;
+      kp += a.kh, vp += a.vh;
+      kc += L::BYTES, vc += L::BYTES, ks += L::BYTES / 2, vs += L::BYTES / 2;
     }
   }
 }
 
-template <int HD, bool BF16>
-auto append_kernel_of(const kvq_rope_plan* plan, bool q) {
-  using K = void (*)(kvq_rope_plan, AppendPagedArgs);
-  if (!plan) return (K)paged_append_kernel<HD, Turn::NONE, 0, BF16>;
-  const bool wide = q && rope_pairs(*plan) == 8;
-  if (plan->interleaved)
-    return wide ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 1, BF16>;
-  if (plan->rotary_dim / 2 % E == 0)
-    return wide ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16> : (K)paged_append_kernel<HD, Turn::LANES, 4, BF16>;
-  return (K)paged_append_kernel<HD, Turn::ELEMENTS, 1, BF16>;
-}
-
-// Pairs per thread with which that kernel turns q.
+// Pairs per thread with which the kernel turns q.
 int append_pairs(const kvq_rope_plan& plan) {
   const int V = rope_pairs(plan);
   return V == 8 || (V == 4 && !plan.interleaved) ? V : 1;
+}
+
+template <int HD, bool BF16>
+auto append_kernel_of(const kvq_rope_plan* plan) {
+  using K = void (*)(kvq_rope_plan, AppendPagedArgs);
+  if (!plan) return (K)paged_append_kernel<HD, Turn::NONE, 0, BF16>;
+  const int V = append_pairs(*plan);
+  if (plan->interleaved)
+    return V == 8 ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 1, BF16>;
+  return V == 8   ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16>
+         : V == 4 ? (K)paged_append_kernel<HD, Turn::ELEMENTS, 4, BF16>
+                  : (K)paged_append_kernel<HD, Turn::ELEMENTS, 1, BF16>;
 }
 
 struct GatherArgs {
@@ -290,7 +319,9 @@ struct GatherArgs {
 };
 
 // One warp per item of a token's heads [h, h + a.per): half of the lanes read keys, half values, eight
-// channels each (one 16-byte store); at head_dim 64 a warp takes two heads at once.  HBM bound.
+// channels each (one 16-byte store); at head_dim 64 a warp takes two heads at once.  HBM bound at
+// large sizes (4-bit codes and scales in, two bytes per element out), by latency at small ones: four
+// steps' loads are on their way at once.
 constexpr int GATHER_THREADS = 128;
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs a) {
@@ -303,7 +334,7 @@ __global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs
   pdl_trigger();
   pdl_wait();
   for (long long u = blockIdx.x * (GATHER_THREADS / 32ll) + (threadIdx.x >> 5); u < n; u += gridDim.x * (GATHER_THREADS / 32ll)) {
-    const long long t = u / items;
+    const long long t = quotient(u, items);
     const int h0 = (int)(u - t * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
     const int slot = a.slots[t];
     const bool held = slot >= 0 && slot / PG < a.n_pages;
@@ -349,7 +380,9 @@ __global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs
   }
 }
 
-// Heads per item: few while the call does not fill the GPU, eight when it does.
+// Heads per item: few while the call does not fill the GPU with 32 warps per SM, eight when it
+// does (5003 tokens of 5 heads of 64 with the read-back 12 us, 17 with fewer
+// and longer items, for 64 warps per SM; the 32K-token prompt 172 us, 188 with at most four heads).
 int heads_per_item(long long T, int H) {
   return (int)std::min<long long>(8, std::max<long long>(1, T * H / (152 * 32)));   // 32 warps per SM
 }
@@ -399,8 +432,11 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
     if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
     if (kvq_status s = check_buffer(q_out, dev, 16, fn, "q_out")) return s;
   }
-  AppendPagedArgs a{k, v, slots, positions, static_cast<unsigned char*>(pages), kt, kh, vt, vh, T, Hkv, n_pages, heads_per_item(T, Hkv), 0, {}};
-  const long long items = (long long)T * ((Hkv + a.per - 1) / a.per);
+  AppendPagedArgs a{k, v, slots, positions, static_cast<unsigned char*>(pages), kt, kh, vt, vh, T, Hkv, n_pages, 0, 0, {}};
+  const int tokens = 32 * E / hd;   // of one item
+  const long long rows = ((long long)T + tokens - 1) / tokens;
+  a.per = heads_per_item(rows, Hkv);
+  const long long items = rows * ((Hkv + a.per - 1) / a.per);
   long long blocks = std::min<long long>((items + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32), 152 * 32);
   a.kv_blocks = (int)blocks;
   if (q) {
@@ -410,8 +446,8 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
     blocks += std::min<long long>(((long long)T * a.q.lanes * units + APPEND_THREADS - 1) / APPEND_THREADS, 152 * 32);
   }
   const bool bf16 = dtype == KVQ_BF16;
-  auto* kern = hd == 128 ? (bf16 ? append_kernel_of<128, true>(plan, q) : append_kernel_of<128, false>(plan, q))
-                         : (bf16 ? append_kernel_of<64, true>(plan, q) : append_kernel_of<64, false>(plan, q));
+  auto* kern = hd == 128 ? (bf16 ? append_kernel_of<128, true>(plan) : append_kernel_of<128, false>(plan))
+                         : (bf16 ? append_kernel_of<64, true>(plan) : append_kernel_of<64, false>(plan));
   kvq_rope_plan none = {};
   cudaError_t e = launch_dependent(kern, dim3((unsigned)blocks), dim3(APPEND_THREADS), 0, static_cast<cudaStream_t>(stream),
                                    plan ? *plan : none, a);

@@ -70,15 +70,11 @@ __device__ __forceinline__ int pa_first(const PaArgs& a, int len) {
 // Equal contiguous ranges of T unit positions for `ge` CTAs, none empty.  A group takes PA_LEAD
 // positions besides one per page when the ranges are long enough, for what starting and
 // finishing it costs.
-// a / b for 64-bit a and positive b: the 32-bit division (a quarter of the time) where it serves
-__device__ __forceinline__ long long pa_div(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
 struct PaSplit {
   long long T;
   int ge;
-  __device__ __forceinline__ long long cta0(int c) const { return pa_div(c * T, ge); }
-  __device__ __forceinline__ int cta_of(long long x) const { return (int)pa_div((x + 1) * ge - 1, T); }
+  __device__ __forceinline__ long long cta0(int c) const { return quotient(c * T, ge); }
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)quotient((x + 1) * ge - 1, T); }
 };
 
 __device__ __forceinline__ unsigned long long pa_ns() {
@@ -355,9 +351,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     const long long c0 = sp.cta0(blockIdx.x);
     const int n = (int)(sp.cta0(blockIdx.x + 1) - c0), na = min(PA_WARPS, n);
     if (warp < na) {
-      const int w0 = (int)pa_div((long long)warp * n, na);
+      const int w0 = (int)quotient((long long)warp * n, na);
       x0 = c0 + w0;
-      n_pos = (int)pa_div((long long)(warp + 1) * n, na) - w0;
+      n_pos = (int)quotient((long long)(warp + 1) * n, na) - w0;
     }
   }
 
@@ -384,7 +380,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   };
   Walk cw = {0, 0, 0, 0, 0, 0};
   if (n_pos) {
-    const int at = (int)pa_div(x0, U);
+    const int at = (int)quotient(x0, U);
     int lo = 0, hi = a.B - 1;   // the last sequence with pre[b] <= at
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -394,7 +390,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     cw.b = lo;
     enter(cw);
     const long long rem = x0 - (long long)pre[cw.b] * U;
-    cw.gr = (int)pa_div(rem, cw.np + lead);
+    cw.gr = (int)quotient(rem, cw.np + lead);
     cw.p = (int)(rem - (long long)cw.gr * (cw.np + lead)) - lead;
     if (cw.p < 0) cw.x = -cw.p, cw.p = 0;
   }

@@ -664,6 +664,22 @@ def test_nan_is_held_as_nan(D, rotate, dt):
         assert torch.equal(a.isnan(), n) and torch.equal(a[~n], b[~n]) and not b.isnan().any()
 
 
+@pytest.mark.parametrize("layout,rd", [("half", 64), ("half", 40), ("half", 26), ("interleaved", 64), ("interleaved", 36)])
+def test_infinities_behind_the_rotated_elements(layout, rd):
+    """Elements that no rotation touches are held as without one, infinite ones as 65504."""
+    k, slots = _randn((5, 2, 128), torch.float16, 1), _ints([0, 1, 2, 3, 4])
+    k[1, 0, 70], k[2, 1, 127] = float("inf"), float("-inf")
+    got = []
+    for kw in (dict(plan=kvq.RopePlan(128, rotary_dim=rd, layout=layout), positions=slots), {}):
+        pages = torch.zeros(1, 2, 10240, dtype=torch.uint8, device="cuda")
+        kvq.paged_append(pages, k, k, slots, **kw)
+        kb, vb = torch.empty_like(k), torch.empty_like(k)
+        kvq.paged_gather(pages, slots, kb, vb)
+        got.append((kb, vb))
+    assert torch.equal(got[0][0][..., 64:], got[1][0][..., 64:]) and torch.equal(got[0][1], got[1][1])
+    assert not got[0][0].isnan().any() and got[0][0][1, 0, 70] > 60000 and got[0][0][2, 1, 127] < -60000
+
+
 @pytest.mark.parametrize("D,Q,n_rep", [(128, 1, 4), (128, 2, 2), (128, 2, 4), (128, 4, 4), (64, 4, 1), (64, 4, 2), (64, 4, 4)])
 @pytest.mark.parametrize("token,window", [(69, 0), (68, 0), (10, 58), (10, 0)])
 @pytest.mark.parametrize("what", ["k", "v"])
