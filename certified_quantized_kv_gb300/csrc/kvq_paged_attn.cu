@@ -9,22 +9,33 @@
 //  - Nibbles are never converted: masked out of their words they are binary16 subnormals
 //    n 2^-24 (low nibble of a byte) or 16 n 2^-24 (high nibble), exact MMA operands.
 //    Scales and offsets enter outside the code products: the key scales multiply the group's
-//    fp32 sums, the value scales the softmax weights, the offsets are MMAs of their own
-//    (4 of the 72 per page each).  Channels that sit in high nibbles carry 1/16 in q.
-//  - Scores: tokens are MMA rows, the (up to 8 per tile) query rows are columns: one
-//    m16n8k16 covers 16 tokens x 16 channels.  A score fragment turned by movmatrix is the B
-//    fragment (k = tokens) of the value product, whose rows are channels.
+//    fp32 sums, the value scales the softmax weights, the offsets are MMAs of their own (8 of
+//    the 72 per page at head_dim 128 and four rows).  Channels in high nibbles carry 1/16 in q.
+//  - Scores: tokens are MMA rows, up to 8 query rows are columns: one m16n8k16 covers 16
+//    tokens x 16 channels.  A score fragment turned by movmatrix is the B fragment (k = tokens)
+//    of the value product, whose rows are channels.  With tiles of 16 rows the queries are MMA
+//    rows instead, and nothing is turned.
 //  - Weights go into the value product as binary16 halves hi + lo of p s (together 2^-21),
 //    formed by exact products.  With at most four query rows they fill one tile's eight
-//    columns (four hi, four lo); with more, hi and lo are two MMAs into the same sums.
-//  - Weights are p 2^k with k = 14 unless a value scale of 2 or more appears (then smaller,
-//    so that p s stays finite in binary16): small weights of long caches stay normal numbers.
+//    columns (four hi, four lo); with more, hi and lo are two MMAs into the same sums.  One half
+//    alone (2^-12) would cost 2.5 times the output's own rounding error: codes 0..15 are not
+//    centred, so the errors of all weights add up in them.
+//  - The softmax reference of a row moves only when a weight would pass 2^top, and is then set so
+//    that the largest is 2^(top - 4): most pages rescale nothing.  top is 14 unless a value
+//    scale of 2 or more appears (then smaller, so that p s stays finite in binary16): small
+//    weights of long caches stay normal numbers.
 //  - The (sequence, KV head, row tile, page) units are numbered in that order and cut into
 //    equal contiguous ranges, one per warp, whatever the lengths; every warp works alone on
 //    whole pages, fed by bulk copies into its own shared-memory ring.  A group (sequence, KV
 //    head, row tile) that lies within one warp's range is written out directly.  The pieces
 //    of one that is cut are merged within the CTA, and across CTAs by the last of them to
 //    arrive, each time in a fixed order, so the result does not depend on timing.
+//
+// Measured (GB300, 32 query heads on 8 KV heads of 128, device time): 8 sequences of 65536 tokens,
+// 671 MB: 111 us = 6.0 TB/s, 0.89 of a copy's 6.8; one of 131072: 37.5 us = 4.5 TB/s; one of 4096: 11.7 us.
+// What long calls take beside their bytes is about 13 us: launch, lengths, page numbers and first pages
+// (three dependent reads, 4 us with the launch), one page's arithmetic (1.5), writing pieces and merging them
+// within a CTA and across CTAs (5), and the ramp of the copies.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -37,9 +48,15 @@ namespace kvq {
 
 namespace {
 
+// Eight warps with two pages each: 160 KB at head_dim 128, two warps per scheduler.  At head_dim 64 more
+// would fit: 48 sequences of 4096 tokens took 23.3 us, with 12 warps 25.2, with 16 27.6 (8 sequences of
+// 32768: 27.5, 27.7 and 30.7), since each warp's first and last page cost more than waiting does.
 constexpr int PA_WARPS = 8;
 constexpr int PA_STAGES = 2;
 constexpr int PA_THREADS = 32 * PA_WARPS;
+// Positions that a group takes besides its pages, for what starting and finishing it costs (64 ragged
+// sequences up to 16384 tokens: 84 us; 95 with one, 107 with none, 84 with three; 8 with four query
+// tokens: 34 us; 38, 45, 44).
 constexpr int PA_LEAD = 2;
 constexpr float PA_TOP = 14.f;                              // weights are 2^14 at most,
 constexpr float PA_SLACK = 4.f;                             // 2^10 when their reference is set
@@ -68,8 +85,7 @@ __device__ __forceinline__ int pa_first(const PaArgs& a, int len) {
 }
 
 // Equal contiguous ranges of T unit positions for `ge` CTAs, none empty.  A group takes PA_LEAD
-// positions besides one per page when the ranges are long enough, for what starting and
-// finishing it costs.
+// positions besides one per page when the ranges are long enough.
 struct PaSplit {
   long long T;
   int ge;
@@ -246,7 +262,8 @@ __device__ __noinline__ void pa_merge(PaOut po, const float* const* at, int n, b
   }
 }
 
-// R query rows per tile: 4 (hi and lo weights share the eight columns), 8 (a row each), or 16, where
+// R query rows per tile: 4 (hi and lo weights share the eight columns: 37.5 us for 131072 tokens, 41.1
+// in a tile of 8), 8 (a row each), or 16, where
 // queries are MMA rows instead of columns (WIDE): a score fragment then is an A fragment of
 // the value product as it stands, and hi and lo weights multiply the same code fragments.
 template <int HD, int R>
@@ -254,7 +271,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   using L = Page<HD>;
   constexpr bool PACK = R == 4, WIDE = R == 16;
   constexpr int G = L::G, MT = WIDE ? HD / 8 : HD / 16, PART = R * (HD + 2);   // MT: accumulator tiles
-  constexpr int STEP = WIDE ? 2 : 4;   // tiles of 16 tokens at once
+  // tiles of 16 tokens at once: a whole page, if registers allow (131072 tokens 37.5 us, 39.5 with two;
+  // tiles of 16 rows: two 34.3 us, one 34.8)
+  constexpr int STEP = WIDE ? 2 : 4;
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTE = 0x00FF00FFu;
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ __align__(8) unsigned long long bars[PA_WARPS][PA_STAGES];

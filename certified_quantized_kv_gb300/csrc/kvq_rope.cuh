@@ -24,7 +24,7 @@ struct RopeArgs {
 // A cosine and sine cost about 60 instructions.  With TABLE a block forms those of its tokens once, in
 // shared memory (64 tokens of 40 heads: 2.44 us, 2.65 without; 4099 tokens of 13: 9.1 and 9.7);
 // without, each thread those of its pairs (in the append, whose blocks live on many warps in
-// different phases, the table's barriers cost more than they save: 179 us against 167).
+// different phases, the table's barriers cost more than they saved: 179 us against 167 when measured).
 
 template <int N>
 struct Words {   // N elements in one or two loads of at most 16 bytes
