@@ -297,10 +297,13 @@ def reference_arm(args, wl):
 
 
 def _source_hash() -> str:
+    """Of the kernels that the summary covers (the paged cache and rotary positions are none of them)."""
     import hashlib
     d = os.path.join(ROOT, "certified_quantized_kv_gb300", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(d)):
+        if f.startswith(("kvq_paged", "kvq_rope")):
+            continue
         with open(os.path.join(d, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]

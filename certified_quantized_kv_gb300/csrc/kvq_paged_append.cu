@@ -210,15 +210,16 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], float2 ext, bo
 // One warp per item: two tokens at head_dim 128, four at 64 (eight elements per lane: what is done once
 // per group and lane, the extremes and the scale, costs half of what it does with four: 32768
 // tokens without q 60 us, 79 with four), and of each the KV heads [h, h + a.per), one after the other
-// with cos and sin formed once.  The other blocks turn q, a thread per V pairs.
+// with cos and sin formed once; the next head's rows are on their way while one is coded (55 us,
+// 60 without).  The other blocks turn q, a thread per V pairs.
 //
 // The KV blocks are bound by the issue of their instructions (unpacking, rotation, the shuffles of
 // the extremes, the verified scale and codes), the q blocks by HBM; so the two kinds are spread
-// over the grid in turn.  32768 tokens of 32 + 8 heads of 128: 713 MB in 132 us (5.4 TB/s); 168
-// with the read-back behind it, where registers for 7 blocks per SM give 173, for 6 180.
+// over the grid in turn.  32768 tokens of 32 + 8 heads of 128: 713 MB in 123 us (5.8 TB/s, a copy's
+// 6.8); 159 with the read-back behind it, where registers for 8 blocks per SM give 160, for 6 162.
 constexpr int APPEND_THREADS = 128;
 template <int HD, Turn TURN, int V, bool BF16>
-__global__ void __launch_bounds__(APPEND_THREADS, 8) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
+__global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
   using L = Page<HD>;
   constexpr int LANES = HD / E, TOKENS = 32 / LANES;   // lanes of a row, tokens of an item
   constexpr int WARPS = APPEND_THREADS / 32;
@@ -254,9 +255,12 @@ __global__ void __launch_bounds__(APPEND_THREADS, 8) paged_append_kernel(const _
     __half* ks = reinterpret_cast<__half*>(pg + L::KS) + at * L::G + g;
     __half* vs = reinterpret_cast<__half*>(pg + L::VS) + g * PG + vscale_at(at);
     Rotation<HD, TURN, BF16> rot;
+    Octet next_k = {}, next_v = {};
+    if (live) next_k.load(kp), next_v.load(vp);
     for (int h = h0; h < h1; ++h) {
-      Octet rk = {}, rv = {};
-      if (live) rk.load(kp), rv.load(vp);
+      const Octet rk = next_k, rv = next_v;
+      kp += a.kh, vp += a.vh;
+      if (live && h + 1 < h1) next_k.load(kp), next_v.load(vp);   // on their way while this head is coded
       if (TURN != Turn::NONE && h == h0) rot.set(P, steps, live ? a.pos[t] : 0, lane);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
@@ -286,7 +290,6 @@ __global__ void __launch_bounds__(APPEND_THREADS, 8) paged_append_kernel(const _
           }
         }
       }
-      kp += a.kh, vp += a.vh;
       kc += L::BYTES, vc += L::BYTES, ks += L::BYTES / 2, vs += L::BYTES / 2;
     }
   }
@@ -320,8 +323,9 @@ struct GatherArgs {
 
 // One warp per item of a token's heads [h, h + a.per): half of the lanes read keys, half values, eight
 // channels each (one 16-byte store); at head_dim 64 a warp takes two heads at once.  HBM bound at
-// large sizes (4-bit codes and scales in, two bytes per element out), by latency at small ones: four
-// steps' loads are on their way at once.
+// large sizes (4-bit codes and scales in, two bytes per element out: 32768 tokens of 8 heads of 128,
+// 176 MB, 35 us), by latency at small ones: four steps' loads are on their way at once (two:
+// 38 us, eight: 39).
 constexpr int GATHER_THREADS = 128;
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs a) {
@@ -381,8 +385,8 @@ __global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs
 }
 
 // Heads per item: few while the call does not fill the GPU with 32 warps per SM, eight when it
-// does (5003 tokens of 5 heads of 64 with the read-back 12 us, 17 with fewer
-// and longer items, for 64 warps per SM; the 32K-token prompt 172 us, 188 with at most four heads).
+// does (5003 tokens of 5 heads of 64 with the read-back took 12 us, 17 with shorter items, for 64
+// warps per SM; the 32K-token prompt 172 us, 188 with at most four heads).
 int heads_per_item(long long T, int H) {
   return (int)std::min<long long>(8, std::max<long long>(1, T * H / (152 * 32)));   // 32 warps per SM
 }

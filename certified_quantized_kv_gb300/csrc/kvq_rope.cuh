@@ -91,7 +91,7 @@ __device__ __forceinline__ void fill_turns(const kvq_rope_plan& P, const uint64_
 template <int V, bool INTERLEAVED, bool BF16, int THREADS, bool TABLE>
 __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t* step, float2* turns, const RopeArgs& a, long long base,
                                           long long stride) {
-  constexpr int ROPE_UNROLL = TABLE ? 4 : 2;    // (two heads fit the append's 64 registers)
+  constexpr int ROPE_UNROLL = 4;
   constexpr int N0 = INTERLEAVED ? 2 * V : V;   // elements of one load (and of the other, half a head on)
   const int half = P.rotary_dim / 2, chunks = half / V;
   const int copies = a.copy ? P.head_dim / 8 - (P.rotary_dim + 7) / 8 : 0;   // vectors behind the rotated elements
