@@ -106,6 +106,25 @@ def test_rope_extreme_positions():
     assert np.abs(_f64(out) - ref).max() <= 8 * (2.0 ** -11 + 2.0 ** -16)
 
 
+def test_rope_phases_where_the_products_cancel():
+    """a cos - b sin with a / b close to tan: what is left shows the cosine's and the sine's own
+    errors.  Both lie within 2^-23.5 (series, roundings and the angle's), the two products and
+    their sum round by 3 2^-24 of 32768: 32768 (sqrt 2 2^-23.5 + 3 2^-24), beside the one
+    rounding to the element type and, for the frequencies in double, |p| 2^-50 turns."""
+    T, plan = 6000, kvq.RopePlan(128, base=500000.0)
+    pos = torch.randint(-2 ** 27, 2 ** 27, (T,), generator=_gen(3)).int()
+    pos[:9] = torch.tensor([0, 1, -1, 2, 3, -2 ** 31, 2 ** 31 - 1, 5, 7]).int()
+    ang = pos.numpy().astype(np.float64)[:, None] * P.frequencies(128, base=500000.0)
+    x = np.concatenate([32768 * np.sin(ang), 32768 * np.cos(ang)], 1)[:, None]
+    x = torch.from_numpy(x).half().cuda()
+    out = _f64(kvq.rope(x, pos.cuda(), plan))
+    ref = P.rope(_f64(x), pos.numpy(), 128, False, P.frequencies(128, base=500000.0))
+    far = np.abs(pos.numpy().astype(np.float64))[:, None, None] * 2.0 ** -50 * 2 * np.pi * 65536
+    tol = np.abs(ref) * 2.0 ** -11 + 2.0 ** -24 + 32768 * (2 ** 0.5 * 2.0 ** -23.5 + 3 * 2.0 ** -24) + far
+    assert np.all(np.abs(out - ref) <= tol), float((np.abs(out - ref) - tol).max())
+    assert np.abs(ref[..., :64]).max() < 40      # it does cancel
+
+
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("rd", [128, 36])
 def test_rope_strided_views(layout, rd):
