@@ -21,7 +21,7 @@ struct RopeArgs {
 // their way at once.  HBM bound (4 bytes per element, 32K tokens of 40 heads of 128: 671 MB);
 // at V = 8, which every layout with rotary_dim a multiple of 16 takes, all accesses are 16
 // bytes.  Smaller V serve the other rotary_dims (pairs that start or end between vectors).
-// A cosine and sine cost about 60 instructions.  With TABLE a block forms those of its tokens once, in
+// A cosine and sine cost about 30 instructions.  With TABLE a block forms those of its tokens once, in
 // shared memory (64 tokens of 40 heads: 2.44 us, 2.65 without; 4099 tokens of 13: 9.1 and 9.7);
 // without, each thread those of its pairs (in the append, whose blocks live on many warps in
 // different phases, the table's barriers cost more than they saved: 179 us against 167 when measured).
