@@ -32,7 +32,7 @@
 //    arrive, each time in a fixed order, so the result does not depend on timing.
 //
 // Measured (GB300, 32 query heads on 8 KV heads of 128, device time): 8 sequences of 65536 tokens,
-// 671 MB: 111 us = 6.0 TB/s, 0.89 of a copy's 6.8; one of 131072: 37.5 us = 4.5 TB/s; one of 4096: 11.7 us.
+// 671 MB: 111 us = 6.0 TB/s, 0.89 of a copy's 6.8; one of 131072: 37.2 us = 4.5 TB/s; one of 4096: 11.3 us.
 // What long calls take beside their bytes is about 13 us: launch, lengths, page numbers and first pages
 // (three dependent reads, 4 us with the launch), one page's arithmetic (1.5), writing pieces and merging them
 // within a CTA and across CTAs (5), and the ramp of the copies.
@@ -309,46 +309,63 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   pdl_trigger();
   pdl_wait();   // the launch and what lies above overlap the end of the previous kernel
 
-  // pages of every sequence and their sum, then the positions before each sequence
-  auto pages_of = [&](int len) { return len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0; };
-  int pages = 0;
-  for (int b = threadIdx.x; b < a.B; b += PA_THREADS) {
-    const int len = pa_len(a, b);
-    slen[b] = len;
-    pages += pages_of(len);
-  }
-  pages = __reduce_add_sync(0xffffffffu, pages);
-  if (lane == 0) wsum[warp] = pages;
-  __syncthreads();
-  pages = 0;
-#pragma unroll
-  for (int w = 0; w < PA_WARPS; ++w) pages += wsum[w];
+  // Pages of every sequence and their sum, then the positions before each sequence.  A group takes
+  // lead positions from one page per warp on (8 sequences of 1..4096 tokens, 1.6 pages per warp:
+  // 16.2 us, 18.2 without; 48 of 512, less than a page per warp: 12.4 us, 11.5 without).
   const int U = a.Hkv * a.RT;
-  // (8 sequences of 1..4096 tokens, 1.6 pages per warp: 16.2 us, 18.2 without lead positions; 48 of
-  // 512, less than a page per warp: 12.4 us, 11.5 without)
-  const int lead = (long long)pages * U >= (long long)a.grid * PA_WARPS ? PA_LEAD : 0;
-  if (threadIdx.x == 0) pre[0] = 0;
-  for (int base = 0, run = 0; base < a.B; base += PA_THREADS) {
-    const int b = base + threadIdx.x;
-    const int np = b < a.B ? pages_of(slen[b]) : 0;
-    int inc = np ? np + lead : 0;
+  auto pages_of = [&](int len) { return len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0; };
+  auto lead_of = [&](int pages) { return (long long)pages * U >= (long long)a.grid * PA_WARPS ? PA_LEAD : 0; };
+  auto sum_before = [&](int& inc) {   // inclusive sums over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    __syncthreads();
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int before = run;
-#pragma unroll
-    for (int w = 0; w < PA_WARPS; ++w) {
-      before += w < warp ? wsum[w] : 0;
-      run += wsum[w];
+  };
+  int lead;
+  // (up to 32 sequences every warp by itself, all writing the same: one of 4096 tokens 11.3 us, 11.7
+  // through the other way's barriers)
+  if (a.B <= 32) {
+    const int len = lane < a.B ? pa_len(a, lane) : 0, np = pages_of(len);
+    lead = lead_of(__reduce_add_sync(0xffffffffu, np));
+    int inc = np ? np + lead : 0;
+    sum_before(inc);
+    if (lane < a.B) slen[lane] = len, pre[lane + 1] = inc;
+    if (lane == 0) pre[0] = 0;
+    __syncwarp();
+  } else {
+    int pages = 0;
+    for (int b = threadIdx.x; b < a.B; b += PA_THREADS) {
+      const int len = pa_len(a, b);
+      slen[b] = len;
+      pages += pages_of(len);
     }
-    if (b < a.B) pre[b + 1] = before + inc;
+    pages = __reduce_add_sync(0xffffffffu, pages);
+    if (lane == 0) wsum[warp] = pages;
+    __syncthreads();
+    pages = 0;
+#pragma unroll
+    for (int w = 0; w < PA_WARPS; ++w) pages += wsum[w];
+    lead = lead_of(pages);
+    if (threadIdx.x == 0) pre[0] = 0;
+    for (int base = 0, run = 0; base < a.B; base += PA_THREADS) {
+      const int b = base + threadIdx.x;
+      const int np = b < a.B ? pages_of(slen[b]) : 0;
+      int inc = np ? np + lead : 0;
+      sum_before(inc);
+      __syncthreads();
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      int before = run;
+#pragma unroll
+      for (int w = 0; w < PA_WARPS; ++w) {
+        before += w < warp ? wsum[w] : 0;
+        run += wsum[w];
+      }
+      if (b < a.B) pre[b + 1] = before + inc;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {   // rows of empty sequences
     if (slen[b] > 0) continue;
     const size_t row0 = (size_t)b * a.Q * a.Hq;
