@@ -384,13 +384,6 @@ __global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(GatherArgs
   }
 }
 
-// Heads per item: few while the call does not fill the GPU with 32 warps per SM, eight when it
-// does (5003 tokens of 5 heads of 64 with the read-back took 12 us, 17 with shorter items, for 64
-// warps per SM; the 32K-token prompt 172 us, 188 with at most four heads).
-int heads_per_item(long long T, int H) {
-  return (int)std::min<long long>(8, std::max<long long>(1, T * H / (152 * 32)));   // 32 warps per SM
-}
-
 // checks shared by append and gather
 kvq_status check_common(const char* fn, int dtype, int T, int Hkv, int hd, int n_pages) {
   if (dtype != KVQ_F16 && dtype != KVQ_BF16) return paged_fail(KVQ_ERR_INVALID, fn, "dtype must be KVQ_F16 or KVQ_BF16");
@@ -439,14 +432,16 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   AppendPagedArgs a{k, v, slots, positions, static_cast<unsigned char*>(pages), kt, kh, vt, vh, T, Hkv, n_pages, 0, 0, {}};
   const int tokens = 32 * E / hd;   // of one item
   const long long rows = ((long long)T + tokens - 1) / tokens;
-  a.per = heads_per_item(rows, Hkv);
+  // 7 blocks of 4 warps per SM, half of them for q (heads_each)
+  constexpr long long ROOM = 152 * 7 * (APPEND_THREADS / 32);
+  a.per = heads_each(rows, Hkv, 1, q ? ROOM / 2 : ROOM);
   const long long items = rows * ((Hkv + a.per - 1) / a.per);
   long long blocks = std::min<long long>((items + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32), 152 * 32);
   a.kv_blocks = (int)blocks;
   if (q) {
     const bool copy = q != q_out && plan->rotary_dim < hd;
     const int units = rope_units(*plan, append_pairs(*plan), copy);
-    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, rope_lanes(T, Hq, units), copy};
+    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, rope_lanes(T, Hq, units, ROOM / 2 * 32), copy};
     blocks += std::min<long long>(((long long)T * a.q.lanes * units + APPEND_THREADS - 1) / APPEND_THREADS, 152 * 32);
   }
   const bool bf16 = dtype == KVQ_BF16;
@@ -474,7 +469,8 @@ kvq_status gather_impl(const void* pages, int n_pages, const int32_t* slots, int
   if (kvq_status s = check_buffer(slots, dev, 4, fn, "slots")) return s;
   if (kvq_status s = check_buffer(k, dev, 16, fn, "k")) return s;
   if (kvq_status s = check_buffer(v, dev, 16, fn, "v")) return s;
-  GatherArgs a{static_cast<const unsigned char*>(pages), slots, k, v, kt, kh, vt, vh, T, Hkv, n_pages, heads_per_item(T, Hkv)};
+  GatherArgs a{static_cast<const unsigned char*>(pages), slots, k, v, kt, kh, vt, vh, T, Hkv, n_pages, 0};
+  a.per = heads_each(T, Hkv, 1, 152 * 48);   // warps that run at once
   const long long items = (long long)T * ((Hkv + a.per - 1) / a.per);
   const dim3 grid((unsigned)std::min<long long>((items + 3) / 4, 1 << 30));
   auto* kern = hd == 128 ? (dtype == KVQ_BF16 ? paged_gather_kernel<128, true> : paged_gather_kernel<128, false>)

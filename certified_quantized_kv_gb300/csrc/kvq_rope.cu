@@ -101,7 +101,8 @@ kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_
   const int V = rope_pairs(*plan);
   const bool copy = x != out && plan->rotary_dim < plan->head_dim;
   const int units = rope_units(*plan, V, copy);
-  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, rope_lanes(T, H, units), copy};
+  const int resident = V == 8 ? 3 : V == 4 ? 5 : 6;   // blocks per SM, by their registers
+  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, rope_lanes(T, H, units, 152ll * ROPE_THREADS * resident), copy};
   const long long blocks = ((long long)T * a.lanes * units + ROPE_THREADS - 1) / ROPE_THREADS;
   const bool bf16 = dtype == KVQ_BF16;
   auto* k = plan->interleaved ? (bf16 ? rope_kernel_of<true, true>(V) : rope_kernel_of<true, false>(V))

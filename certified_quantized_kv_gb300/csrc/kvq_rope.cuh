@@ -190,12 +190,22 @@ inline int rope_units(const kvq_rope_plan& plan, int V, bool copy) {
   return plan.rotary_dim / 2 / V + (copy ? plan.head_dim / 8 - (plan.rotary_dim + 7) / 8 : 0);
 }
 
-// Heads in step (RopeArgs::lanes): a thread takes one head while the call does not fill the GPU (64
-// tokens of 40 heads), and up to eight when it does, so that the angles, which cost as much as
-// the rotation of four heads, are shared.
-inline int rope_lanes(long long T, int H, int chunks) {
-  const long long per = std::min<long long>(8, std::max<long long>(1, T * H * chunks / (152 * 1024)));
-  return (int)((H + per - 1) / per);
+// Heads per thread or warp: the fewest, 16 at most, with which all of a call's threads (or warps), `each`
+// per token and share of the heads, have room on the GPU at once.  A second wave of blocks costs as
+// much as more heads in one (1024 tokens of 32 heads of 128: 3.8 us with three heads per thread, 4.7 with
+// two, 6.7 with one; 2048 tokens: 5.3 with five, 5.9 with three; the append of 4096 with 8 KV heads: 15.3
+// us with 16 query heads per thread, 18.2 with eight).  Else eight: enough to share the angles, which
+// cost as much as the rotation of two heads (32768 tokens: 122 us, 126 with 16).
+inline int heads_each(long long T, int H, int each, long long room) {
+  for (int per = 1; per <= 16; ++per)
+    if (T * ((H + per - 1) / per) * each <= room) return per;
+  return 8;
+}
+
+// Heads in step (RopeArgs::lanes) when `room` threads run at once.
+inline int rope_lanes(long long T, int H, int units, long long room) {
+  const int per = heads_each(T, H, units, room);
+  return (H + per - 1) / per;
 }
 
 }  // namespace kvq
