@@ -295,21 +295,16 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
   }
 }
 
-// Pairs per thread with which the kernel turns q.
-int append_pairs(const kvq_rope_plan& plan) {
-  const int V = rope_pairs(plan);
-  return V == 8 || (V == 4 && !plan.interleaved) ? V : 1;
-}
-
 template <int HD, bool BF16>
 auto append_kernel_of(const kvq_rope_plan* plan) {
   using K = void (*)(kvq_rope_plan, AppendPagedArgs);
   if (!plan) return (K)paged_append_kernel<HD, Turn::NONE, 0, BF16>;
-  const int V = append_pairs(*plan);
+  const int V = rope_pairs(*plan);   // per thread that turns q
   if (plan->interleaved)
-    return V == 8 ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 1, BF16>;
+    return V == 8 ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 4, BF16>;
   return V == 8   ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16>
          : V == 4 ? (K)paged_append_kernel<HD, Turn::ELEMENTS, 4, BF16>
+         : V == 2 ? (K)paged_append_kernel<HD, Turn::ELEMENTS, 2, BF16>
                   : (K)paged_append_kernel<HD, Turn::ELEMENTS, 1, BF16>;
 }
 
@@ -440,7 +435,7 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   a.kv_blocks = (int)blocks;
   if (q) {
     const bool copy = q != q_out && plan->rotary_dim < hd;
-    const int units = rope_units(*plan, append_pairs(*plan), copy);
+    const int units = rope_units(*plan, rope_pairs(*plan), copy);
     a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, rope_lanes(T, Hq, units, ROOM / 2 * 32), copy};
     blocks += std::min<long long>(((long long)T * a.q.lanes * units + APPEND_THREADS - 1) / APPEND_THREADS, 152 * 32);
   }

@@ -75,8 +75,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
 
 template <bool INTERLEAVED, bool BF16>
 auto rope_kernel_of(int V) {
-  return V == 8 ? rope_kernel<8, INTERLEAVED, BF16> : V == 4 ? rope_kernel<4, INTERLEAVED, BF16>
-         : V == 2 ? rope_kernel<2, INTERLEAVED, BF16> : rope_kernel<1, INTERLEAVED, BF16>;
+  if constexpr (INTERLEAVED) return V == 8 ? rope_kernel<8, true, BF16> : rope_kernel<4, true, BF16>;
+  else return V == 8 ? rope_kernel<8, false, BF16> : V == 4 ? rope_kernel<4, false, BF16>
+              : V == 2 ? rope_kernel<2, false, BF16> : rope_kernel<1, false, BF16>;
 }
 
 kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_t xt, int64_t xh,

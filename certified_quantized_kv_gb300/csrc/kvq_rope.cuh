@@ -20,7 +20,8 @@ struct RopeArgs {
 // One thread per V pairs of a token, for every `lanes`-th head; the loads of several heads are on
 // their way at once.  HBM bound (4 bytes per element, 32K tokens of 40 heads of 128: 671 MB);
 // at V = 8, which every layout with rotary_dim a multiple of 16 takes, all accesses are 16
-// bytes.  Smaller V serve the other rotary_dims (pairs that start or end between vectors).
+// bytes.  Smaller V serve the other rotary_dims (pairs that start or end between vectors); interleaved
+// pairs need no fewer than four.
 // A cosine and sine cost about 30 instructions.  With TABLE a block forms those of its tokens once, in
 // shared memory (64 tokens of 40 heads: 2.44 us, 2.65 without; 4099 tokens of 13: 9.1 and 9.7);
 // without, each thread those of its pairs (in the append, whose blocks live on many warps in
@@ -93,7 +94,7 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
                                           long long stride) {
   constexpr int ROPE_UNROLL = 4;
   constexpr int N0 = INTERLEAVED ? 2 * V : V;   // elements of one load (and of the other, half a head on)
-  const int half = P.rotary_dim / 2, chunks = half / V;
+  const int half = P.rotary_dim / 2, chunks = (half + V - 1) / V;
   const int copies = a.copy ? P.head_dim / 8 - (P.rotary_dim + 7) / 8 : 0;   // vectors behind the rotated elements
   const int units = chunks + copies;
   const long long n = (long long)a.T * a.lanes * units;
@@ -130,12 +131,14 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
         *reinterpret_cast<uint4*>(out + h * a.oh + e) = *reinterpret_cast<const uint4*>(x + h * a.xh + e);
       continue;
     }
+    constexpr bool whole = !INTERLEAVED || V == 8;   // all pairs of every chunk are rotated
+    auto pair = [&](int i) { return whole ? i0 + i : min(i0 + i, half - 1); };
     float2 cs[V];
     const float2* mine = turns + (t - t0) * half;
     if constexpr (!TABLE) {
       const int pos = a.pos[t];
 #pragma unroll
-      for (int i = 0; i < V; ++i) cs[i] = rope_cos_sin(pos, step[i0 + i], P.magnitude);
+      for (int i = 0; i < V; ++i) cs[i] = rope_cos_sin(pos, step[pair(i)], P.magnitude);
     } else if constexpr (V == 8) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -144,7 +147,7 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) cs[i] = mine[i0 + i];
+      for (int i = 0; i < V; ++i) cs[i] = mine[pair(i)];
     }
     for (int h = h0; h < a.H; h += ROPE_UNROLL * a.lanes) {
       if (h != h0) fetch(h);
@@ -155,7 +158,8 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const float2 p = pair_to_f2(A[k].w[i], BF16);
-            A[k].w[i] = f2_to_pair(fmaf(p.x, cs[i].x, -p.y * cs[i].y), fmaf(p.y, cs[i].x, p.x * cs[i].y), BF16);
+            const uint32_t y = f2_to_pair(fmaf(p.x, cs[i].x, -p.y * cs[i].y), fmaf(p.y, cs[i].x, p.x * cs[i].y), BF16);
+            A[k].w[i] = whole || i0 + i < half ? y : A[k].w[i];
           }
         } else {
 #pragma unroll
@@ -171,7 +175,7 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
         if (!INTERLEAVED) B[k].store(o + e1);
       }
     }
-    if (a.copy && c == 0) {   // what lies between the rotated elements and the next whole vector
+    if (!INTERLEAVED && a.copy && c == 0) {   // what lies between the rotated elements and the next whole vector
       const int e1 = min(P.head_dim, (P.rotary_dim + 7) / 8 * 8);
       for (int h = h0; h < a.H; h += a.lanes)
         for (int e = P.rotary_dim; e < e1; ++e) out[h * a.oh + e] = x[h * a.xh + e];
@@ -179,15 +183,16 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
   }
 }
 
-// Pairs per thread: the widest vectors that divide the rotated half.
+// Pairs per thread: the widest vectors that divide the rotated half, and interleaved whole vectors of
+// four pairs at least, of which the last may lie partly behind the rotated elements.
 inline int rope_pairs(const kvq_rope_plan& plan) {
   const int half = plan.rotary_dim / 2;
-  return half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
+  return half % 8 == 0 ? 8 : half % 4 == 0 || plan.interleaved ? 4 : half % 2 == 0 ? 2 : 1;
 }
 
 // Pieces of a row: chunks of V pairs, and the vectors that are only copied.
 inline int rope_units(const kvq_rope_plan& plan, int V, bool copy) {
-  return plan.rotary_dim / 2 / V + (copy ? plan.head_dim / 8 - (plan.rotary_dim + 7) / 8 : 0);
+  return (plan.rotary_dim / 2 + V - 1) / V + (copy ? plan.head_dim / 8 - (plan.rotary_dim + 7) / 8 : 0);
 }
 
 // Heads per thread or warp: the fewest, 16 at most, with which all of a call's threads (or warps), `each`
