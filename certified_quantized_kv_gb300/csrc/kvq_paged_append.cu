@@ -398,7 +398,7 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   if (kvq_status s = check_common(fn, dtype, T, Hkv, hd, n_pages)) return s;
   if (plan) {
     if (kvq_status s = check_plan(plan, hd, fn)) return s;
-    if (!positions) return paged_fail(KVQ_ERR_INVALID, fn, "positions is NULL with a plan");
+    if (!positions && T > 0) return paged_fail(KVQ_ERR_INVALID, fn, "positions is NULL with a plan");
   } else if (positions || q || q_out) {
     return paged_fail(KVQ_ERR_INVALID, fn, "positions, q and q_out need a plan");
   }

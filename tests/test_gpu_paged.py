@@ -727,6 +727,45 @@ def test_nan_reaches_the_queries_that_see_it(D, Q, n_rep, token, window, what, c
             assert torch.equal(a[0, i, r], b[0, i, r]) and torch.equal(la[0, i, r], lb[0, i, r])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Q,n_rep", [(1, 4), (2, 4), (3, 5)])      # tiles of 4, 8 and 16 rows
+def test_attention_of_2048_sequences(D, Q, n_rep):
+    """The largest batch, over shared pages; the arrival counters are zero again behind it."""
+    B, g = 2048, np.random.default_rng(D + Q)
+    pages = P.make_pages(g.normal(size=(40, 64, D)), g.normal(size=(40, 64, D))).reshape(40, 1, -1)
+    kv = P.values(P.unpack(pages, D), D)
+    table = g.integers(0, 40, (B, 3)).astype(np.int32)
+    lens = g.integers(0, 193, B)
+    lens[::97], lens[5] = 0, 192
+    q = _randn((B, Q, n_rep, D), torch.float16, 4)
+    out, lse, ws = _attend(q, torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda(), _ints(lens.tolist()))
+    _check_attention(out, lse, q, kv, table, lens, 0, None)
+    assert not ws[:4096].any()
+
+
+@pytest.mark.parametrize("columns", [4, 9000])
+def test_attention_of_4096_rows(columns):
+    """64 query tokens of 64 heads on one KV head."""
+    pages, table, kv = _cache([200], 1, 128, seed=3)
+    q = _randn((1, 64, 64, 128), torch.bfloat16, 4)
+    wide = torch.from_numpy(_widened(table, max(columns, table.shape[1]))).cuda()
+    out, lse, ws = _attend(q, torch.from_numpy(pages).cuda(), wide, _ints([200]))
+    _check_attention(out, lse, q, kv, table, [200], 0, None)
+    assert not ws[:4096].any()
+
+
+def test_empty_calls():
+    plan = kvq.RopePlan(128)
+    x, n = torch.empty(0, 8, 128, dtype=torch.float16, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    pages = torch.zeros(1, 8, 10240, dtype=torch.uint8, device="cuda")
+    assert kvq.rope(x, n, plan).shape == x.shape
+    kvq.paged_append(pages, x, x, n, positions=n, plan=plan, q=x, q_out=x)
+    kvq.paged_gather(pages, n, x, x)
+    kvq.paged_attention(x, pages, torch.empty(0, 3, dtype=torch.int32, device="cuda"), n, torch.empty_like(x))
+    torch.cuda.synchronize()
+    assert not pages.any()
+
+
 def test_attention_refuses_what_its_positions_cannot_count():
     x = torch.zeros(1 << 16, dtype=torch.int32, device="cuda")
     at = x.data_ptr()
