@@ -385,12 +385,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   int n_pos = 0;   // positions of this warp
   {
     const long long c0 = sp.cta0(blockIdx.x);
-    const int n = (int)(sp.cta0(blockIdx.x + 1) - c0), na = min(PA_WARPS, n);
-    if (warp < na) {
-      const int w0 = (int)quotient((long long)warp * n, na);
-      x0 = c0 + w0;
-      n_pos = (int)quotient((long long)(warp + 1) * n, na) - w0;
-    }
+    // as equal as they get; the first n warps, if there are fewer positions than warps
+    const int n = (int)(sp.cta0(blockIdx.x + 1) - c0);
+    auto warp0 = [&](int w) { return n < PA_WARPS ? min(w, n) : (int)((long long)w * n / PA_WARPS); };
+    const int w0 = warp0(warp);
+    x0 = c0 + w0;
+    n_pos = warp0(warp + 1) - w0;
   }
 
   // a walk through the units: sequence b, group gr = KV head * RT + row tile, page p of np, at
@@ -416,11 +416,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   };
   Walk cw = {0, 0, 0, 0, 0, 0};
   if (n_pos) {
-    const int at = (int)quotient(x0, U);
-    int lo = 0, hi = a.B - 1;   // the last sequence with pre[b] <= at
+    int lo = 0, hi = a.B - 1;   // the last sequence that starts at x0 or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= at) lo = mid;
+      if ((long long)pre[mid] * U <= x0) lo = mid;
       else hi = mid - 1;
     }
     cw.b = lo;
