@@ -456,10 +456,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     if (pw.gr != gr) head = a.pages + (pw.gr / a.RT) * L::BYTES;
     if (pw.x < n_pos) next_id = a.table[pw.b * a.table_stride + pw.first + pw.p];
   };
-#pragma unroll 1
-  for (int s = 0; s < PA_STAGES; ++s)
-    if (pw.x < n_pos) issue(s);
-
   // ---- state of the group at hand ----
   // q as MMA operands: group, low and high nibbles, columns (B) or rows gid and gid + 8 (A)
   uint32_t qf[G][2][WIDE ? 4 : 2];
@@ -478,7 +474,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   float top = PA_TOP;         // weights stay below 2^top
   bool started = false, failed = false;
 
-  auto load_group = [&](const Walk& w) {
+  // a group's rows of q, as they lie in memory: of row gid (and gid + 8) channels 32k + 8tig, +7
+  struct Rows {
+    uint4 v[WIDE ? 2 : 1][G];
+  };
+  auto fetch_q = [&](const Walk& w, Rows& rows) {
+    const int g = w.gr / a.RT, r0 = (w.gr - g * a.RT) * R, rn = min(R, a.rows - r0);
+#pragma unroll
+    for (int rj = 0; rj < (WIDE ? 2 : 1); ++rj) {
+      const int r = WIDE ? gid + 8 * rj : PACK ? gid & 3 : gid;   // this lane's row of q
+      const int rr = r0 + (r < rn ? r : 0), i = rr / a.n_rep, h = g * a.n_rep + rr - i * a.n_rep;
+      const unsigned short* src = static_cast<const unsigned short*>(a.q) +
+                                  (size_t)(((long long)w.b * a.Q + i) * a.qt + h * a.qh) + 8 * tig;
+#pragma unroll
+      for (int k = 0; k < G; ++k) rows.v[rj][k] = r < rn ? *reinterpret_cast<const uint4*>(src + 32 * k) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto load_group = [&](const Walk& w, const Rows& rows) {
     const int len = slen[w.b], g = w.gr / a.RT, r0 = (w.gr - g * a.RT) * R;
     const int rn = min(R, a.rows - r0);
     const int i0 = r0 / a.n_rep, i1 = (r0 + rn - 1) / a.n_rep;   // first and last query token of the tile
@@ -488,14 +500,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 #pragma unroll
     for (int rj = 0; rj < (WIDE ? 2 : 1); ++rj) {
       const int r = WIDE ? gid + 8 * rj : PACK ? gid & 3 : gid;   // this lane's row of q
-      const bool live = r < rn;
-      const int rr = r0 + (live ? r : 0), i = rr / a.n_rep, h = g * a.n_rep + rr - i * a.n_rep;
-      const unsigned short* src = static_cast<const unsigned short*>(a.q) +
-                                  (size_t)(((long long)w.b * a.Q + i) * a.qt + h * a.qh) + 8 * tig;
       float f[G][8], mx = 0.f;
 #pragma unroll
       for (int k = 0; k < G; ++k) {
-        const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 32 * k) : make_uint4(0, 0, 0, 0);
+        const uint4 v = rows.v[rj][k];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 p = pair_to_f2(word_of(v, j), a.bf16);
@@ -870,11 +878,22 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     }
   };
 
-  bool open = false;
+  bool open = n_pos > 0;
   int it = 0;
+  if (open) {   // the first group's rows are on their way while the first pages are asked for
+    Rows rows;
+    fetch_q(cw, rows);
+#pragma unroll 1
+    for (int s = 0; s < PA_STAGES; ++s)
+      if (pw.x < n_pos) issue(s);
+    load_group(cw, rows);
+    started = cw.p == 0;
+  }
   while (cw.x < n_pos) {
     if (!open) {
-      load_group(cw);
+      Rows rows;
+      fetch_q(cw, rows);
+      load_group(cw, rows);
       open = true;
       started = cw.p == 0;
     }
