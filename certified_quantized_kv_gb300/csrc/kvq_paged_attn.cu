@@ -848,12 +848,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       const int mine = lane % TR, rt0 = 8 * ct;
       float lt = stage_l[mine];
       if (PACK) lt += stage_l[mine + 4];   // columns 4..7 hold the lo halves' sums
-      const float rf = stage_r[mine], inv = lt == 0.f ? 0.f : 1.f / lt;
-      const bool live = rt0 + mine < rn;
-      const size_t row = live && !dst ? po.row(w.b, g, r0 + rt0 + mine) : 0;
-      if (lane < TR) {
-        if (dst) reinterpret_cast<float2*>(dst + R * HD)[rt0 + lane] = make_float2(lt == 0.f ? -INFINITY : rf, lt);
-        else if (live && a.lse) a.lse[row] = lt == 0.f ? -INFINITY : (rf + log2f(lt)) * 0.69314718055994531f;
+      const float rf = stage_r[mine];
+      float inv = 0.f;
+      size_t row = 0;
+      if (dst) {
+        if (lane < TR) reinterpret_cast<float2*>(dst + R * HD)[rt0 + lane] = make_float2(lt == 0.f ? -INFINITY : rf, lt);
+      } else {
+        const bool live = rt0 + mine < rn;
+        if (lt != 0.f) inv = 1.f / lt;
+        if (live) row = po.row(w.b, g, r0 + rt0 + mine);
+        if (lane < TR && live && a.lse) a.lse[row] = lt == 0.f ? -INFINITY : (rf + log2f(lt)) * 0.69314718055994531f;
       }
 #pragma unroll
       for (int k = 0; k < TR * F4 / 32; ++k) {
