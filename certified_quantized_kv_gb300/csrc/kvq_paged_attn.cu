@@ -211,7 +211,7 @@ struct PaSum {
 template <int HD, int R, bool ACROSS>
 __device__ __noinline__ void pa_merge(PaOut po, const float* const* at, int n, bool closed, int b, int g, int r0, int rn, float* dst) {
   constexpr int PART = R * (HD + 2), VEC = R * HD / 4, KS = PA_THREADS / VEC > 1 ? PA_THREADS / VEC : 1;
-  constexpr int BATCH = KS > 1 ? 5 : 10;
+  constexpr int BATCH = KS > 1 ? 5 : ACROSS ? 10 : PA_WARPS;
   __shared__ float4 red[KS > 1 ? PA_THREADS : 1];
   __shared__ float2 redm[KS > 1 ? PA_THREADS : 1];
   const float* const base = ACROSS ? *at : nullptr;
