@@ -32,10 +32,10 @@
 //    arrive, each time in a fixed order, so the result does not depend on timing.
 //
 // Measured (GB300, 32 query heads on 8 KV heads of 128, device time): 8 sequences of 65536 tokens,
-// 671 MB: 111 us = 6.0 TB/s, 0.89 of a copy's 6.8; one of 131072: 37.2 us = 4.5 TB/s; one of 4096: 11.3 us.
-// What long calls take beside their bytes is about 13 us: launch, lengths, page numbers and first pages
-// (three dependent reads, 4 us with the launch), one page's arithmetic (1.5), writing pieces and merging them
-// within a CTA and across CTAs (5), and the ramp of the copies.
+// 671 MB: 109 us = 6.2 TB/s, 0.91 of a copy's 6.8; one of 131072: 35.4 us = 4.7 TB/s; one of 4096: 10.6 us.
+// What long calls take beside their bytes is about 10 us; a short one: launch 1.2 us, lengths 0.6, ranges 0.5,
+// page numbers and first pages (with the queries meanwhile) 1.5, one page's arithmetic 1.5, writing its piece
+// 0.6, merging within the CTA 0.9, arrival 1.1, merging across CTAs 1.9, and 0.5 between the first and last warp.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -54,10 +54,13 @@ namespace {
 constexpr int PA_WARPS = 8;
 constexpr int PA_STAGES = 2;
 constexpr int PA_THREADS = 32 * PA_WARPS;
-// Positions that a group takes besides its pages, for what starting and finishing it costs (64 ragged
-// sequences up to 16384 tokens: 84 us; 95 with one, 107 with none, 84 with three; 8 with four query
-// tokens: 34 us; 38, 45, 44).
-constexpr int PA_LEAD = 2;
+// Positions that a group takes besides its pages, for what starting and finishing it costs in pages' time:
+// two at head_dim 128 (64 ragged sequences up to 16384 tokens: 82 us; 89 with one, 101 with none, 82 with
+// three; 8 with four query tokens: 32 us; 34, 41, 31), three at 64, whose pages take less (48 ragged with a
+// window of 4096: 19.4 us; 20.0 with two, 27.3 with none).
+constexpr int PA_MAX_LEAD = 3;
+template <int HD>
+constexpr int PA_LEAD = HD == 64 ? PA_MAX_LEAD : 2;
 constexpr float PA_TOP = 14.f;                              // weights are 2^14 at most,
 constexpr float PA_SLACK = 4.f;                             // 2^10 when their reference is set
 constexpr unsigned long long PA_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
@@ -262,7 +265,7 @@ __device__ __noinline__ void pa_merge(PaOut po, const float* const* at, int n, b
   }
 }
 
-// R query rows per tile: 4 (hi and lo weights share the eight columns: 37.5 us for 131072 tokens, 41.1
+// R query rows per tile: 4 (hi and lo weights share the eight columns: 35.4 us for 131072 tokens, 39.1
 // in a tile of 8), 8 (a row each), or 16, where
 // queries are MMA rows instead of columns (WIDE): a score fragment then is an A fragment of
 // the value product as it stands, and hi and lo weights multiply the same code fragments.
@@ -271,8 +274,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
   using L = Page<HD>;
   constexpr bool PACK = R == 4, WIDE = R == 16;
   constexpr int G = L::G, MT = WIDE ? HD / 8 : HD / 16, PART = R * (HD + 2);   // MT: accumulator tiles
-  // tiles of 16 tokens at once: a whole page, if registers allow (131072 tokens 37.5 us, 39.5 with two;
-  // tiles of 16 rows: two 34.3 us, one 34.8)
+  // tiles of 16 tokens at once: a whole page, if registers allow (131072 tokens 35.4 us, 37.3 with two;
+  // tiles of 16 rows: two 31.6 us, one 32.1)
   constexpr int STEP = WIDE ? 2 : 4;
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTE = 0x00FF00FFu;
   extern __shared__ __align__(128) unsigned char sm[];
@@ -311,10 +314,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 
   // Pages of every sequence and their sum, then the positions before each sequence.  A group takes
   // lead positions from one page per warp on (8 sequences of 1..4096 tokens, 1.6 pages per warp:
-  // 16.2 us, 18.2 without; 48 of 512, less than a page per warp: 12.4 us, 11.5 without).
+  // 14.6 us, 16.3 without; 48 of 512, less than a page per warp, took 12.4 us, 11.5 without).
   const int U = a.Hkv * a.RT;
   auto pages_of = [&](int len) { return len > 0 ? (len + PG - 1) / PG - pa_first(a, len) : 0; };
-  auto lead_of = [&](int pages) { return (long long)pages * U >= (long long)a.grid * PA_WARPS ? PA_LEAD : 0; };
+  auto lead_of = [&](int pages) { return (long long)pages * U >= (long long)a.grid * PA_WARPS ? PA_LEAD<HD> : 0; };
   auto sum_before = [&](int& inc) {   // inclusive sums over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     }
   };
   int lead;
-  // (up to 32 sequences every warp by itself, all writing the same: one of 4096 tokens 11.3 us, 11.7
+  // (up to 32 sequences every warp by itself, all writing the same: one of 4096 tokens took 11.3 us, 11.7
   // through the other way's barriers)
   if (a.B <= 32) {
     const int len = lane < a.B ? pa_len(a, lane) : 0, np = pages_of(len);
@@ -996,9 +999,9 @@ const char* shape_error(int B, int Q, int Hq, int Hkv, int hd) {
 
 // Query rows per tile: 4 or 8 if those hold a KV head's rows, else 16 or, of 8, twice as many tiles,
 // each of which reads the pages again (from L2).  Tiles of 16 take less time per page and row (16 rows, 8
-// sequences of 16384 tokens: 64 us, 72 with tiles of 8; of 8192: 41 and 45), tiles of 8 start and
-// finish faster (of 4096: 29 us, 31 with tiles of 16; of 1024: 17 and 19), and 17 to 24 rows fill
-// three of them (20 rows, 8 sequences of 8192: 58 us, 64 with two tiles of 16).  The lengths are
+// sequences of 16384 tokens: 61 us, 69 with tiles of 8; of 8192: 38 and 41), tiles of 8 start and
+// finish faster (of 4096: 27 us, 28 with tiles of 16; of 1024: 15 and 18), and 17 to 24 rows fill
+// three of them (20 rows, 8 sequences of 8192: 56 us, 61 with two tiles of 16).  The lengths are
 // not known on the host, the most pages are.
 constexpr int PA_FEW = 4;   // pages per warp, if all were in use
 int tile_rows(int rows, long long most_pages, int sms) {
@@ -1069,7 +1072,7 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   a.RT = (a.rows + R - 1) / R;
   // one CTA per SM (the counters hold 1024), fewer when the table cannot hold that many units
   a.grid = (int)std::min<long long>(std::min(sms, 1024), (long long)B * max_pages * Hkv * a.RT);
-  if ((long long)B * (max_pages + PA_LEAD) * Hkv * a.RT / a.grid >= (1ll << 30))   // a CTA's positions are ints
+  if ((long long)B * (max_pages + PA_MAX_LEAD) * Hkv * a.RT / a.grid >= (1ll << 30))   // a CTA's positions are ints
     return paged_fail(KVQ_ERR_INVALID, fn, "batch * max_pages * n_kv_heads is too large for one call");
   a.arrived = static_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + PA_COUNTERS);
