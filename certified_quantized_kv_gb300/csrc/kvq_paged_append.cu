@@ -418,7 +418,7 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   if (q) {
     if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
     if (kvq_status s = check_strides(ot, oh, fn, "q_out")) return s;
-    if ((T > 1 && ot == 0) || (Hq > 1 && oh == 0)) return paged_fail(KVQ_ERR_INVALID, fn, "q_out: rows must not overlap");
+    if ((T > 1 && ot < hd) || (Hq > 1 && oh < hd)) return paged_fail(KVQ_ERR_INVALID, fn, "q_out: rows must not overlap");
     if (q == q_out && ((T > 1 && qt != ot) || (Hq > 1 && qh != oh)))
       return paged_fail(KVQ_ERR_INVALID, fn, "q_out = q needs the same strides");
     if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
@@ -456,7 +456,7 @@ kvq_status gather_impl(const void* pages, int n_pages, const int32_t* slots, int
   if (T == 0) return KVQ_OK;
   if (kvq_status s = check_strides(kt, kh, fn, "k")) return s;
   if (kvq_status s = check_strides(vt, vh, fn, "v")) return s;
-  if ((T > 1 && (kt == 0 || vt == 0)) || (Hkv > 1 && (kh == 0 || vh == 0)))
+  if ((T > 1 && std::min(kt, vt) < hd) || (Hkv > 1 && std::min(kh, vh) < hd))
     return paged_fail(KVQ_ERR_INVALID, fn, "k and v: rows must not overlap");
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");

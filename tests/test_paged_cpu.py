@@ -214,3 +214,11 @@ def test_more_refusals_before_any_cuda_call():
     assert _attend() == kvq.KVQ_ERR_INVALID and b"out must not be q" in lib.kvq_last_error()
     for status in (_append(Hkv=4097), _attend(Hkv=4097, Hq=4097)):
         assert status == kvq.KVQ_ERR_INVALID and b"n_kv_heads" in lib.kvq_last_error()
+
+
+def test_rows_of_outputs_must_not_overlap():
+    lib = kvq.load_library()
+    for kw in (dict(ot=120), dict(oh=64)):
+        assert _rope(x=ADDR + 4096, **kw) == kvq.KVQ_ERR_INVALID and b"must not overlap" in lib.kvq_last_error()
+    a = dict(pages=ADDR, n_pages=3, slots=ADDR, T=4, Hkv=2, hd=128, dtype=0, k=ADDR, kt=256, kh=128, v=ADDR, vt=256, vh=120)
+    assert lib.kvq_paged_gather(*a.values(), None) == kvq.KVQ_ERR_INVALID and b"must not overlap" in lib.kvq_last_error()
