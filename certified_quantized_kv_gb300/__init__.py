@@ -425,9 +425,9 @@ def _rows(t, name, dtype, shape):
     return t.data_ptr(), a if T > 1 else 8, b if H > 1 else 8
 
 
-def _ints(t, name, n):
-    if t.dtype is not _I32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous torch.int32 tensor of {n} elements")
+def _ints(t, name, n, dev):
+    if t.dtype is not _I32 or t.shape != (n,) or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous torch.int32 tensor of {n} elements on CUDA device {dev}")
     return t.data_ptr()
 
 
@@ -440,17 +440,14 @@ def _float_code(t, name) -> int:
     raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {dt}")
 
 
-def _device_of(names, first, *others) -> int:
-    """Index of the CUDA device that all given tensors (None: absent) are on."""
+def _device_of(t, name) -> int:
+    """Index of the CUDA device that a call runs on: the one of its first tensor.  The library
+    refuses buffers that are not on it."""
     if _torch is None:
         _lookup()
-    dev = first.get_device()
+    dev = t.get_device()
     if dev < 0:
-        raise ValueError(f"{names.split()[0]} must be a CUDA tensor")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            name = next(n for n, o in zip(names.split()[1:], others) if o is t)
-            raise ValueError(f"{name} must be on {first.device}, like {names.split()[0]}")
+        raise ValueError(f"{name} must be a CUDA tensor")
     return dev
 
 
@@ -477,14 +474,14 @@ def rope(x, positions, plan, out=None, stream=None):
         if stream is not None:
             raise ValueError("out must be given with a stream")
         out = (_torch or _lookup()).empty(shape, dtype=x.dtype, device=x.device)
-    dev = _device_of("x positions out", x, positions, out)
+    dev = _device_of(x, "x")
     code, dt = _float_code(x, "x"), x.dtype
     T, H, hd = shape
     if hd != plan.head_dim:
         raise ValueError(f"x must have head_dim {plan.head_dim}, got {hd}")
     a = _rows(x, "x", dt, shape)
     b = a if out is x else _rows(out, "out", dt, shape)
-    _call(dev, stream, load_library().kvq_rope, plan.address, code, *a, _ints(positions, "positions", T), T, H, *b)
+    _call(dev, stream, load_library().kvq_rope, plan.address, code, *a, _ints(positions, "positions", T, dev), T, H, *b)
     return out
 
 
@@ -521,7 +518,7 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
     shape = k.shape
     if len(shape) != 3:
         raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
-    dev = _device_of("k v slots pages positions q q_out", k, v, slots, pages, positions, q, q_out)
+    dev = _device_of(k, "k")
     code, dt = _float_code(k, "k"), k.dtype
     T, hkv, hd = shape
     if (plan is None) != (positions is None):
@@ -537,8 +534,8 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
         qa = _rows(q, "q", dt, (T, hq, hd))
         oa = qa if q_out is q else _rows(q_out, "q_out", dt, (T, hq, hd))
     _call(dev, stream, load_library().kvq_paged_append, None if plan is None else plan.address, code,
-          *_rows(k, "k", dt, shape), *_rows(v, "v", dt, shape), _ints(slots, "slots", T),
-          None if positions is None else _ints(positions, "positions", T), T, hkv, hd, *_pool(pages, hkv, hd),
+          *_rows(k, "k", dt, shape), *_rows(v, "v", dt, shape), _ints(slots, "slots", T, dev),
+          None if positions is None else _ints(positions, "positions", T, dev), T, hkv, hd, *_pool(pages, hkv, hd),
           *qa, hq, *oa)
 
 
@@ -548,10 +545,10 @@ def paged_gather(pages, slots, k, v, stream=None):
     shape = k.shape
     if len(shape) != 3:
         raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
-    dev = _device_of("pages slots k v", pages, slots, k, v)
+    dev = _device_of(pages, "pages")
     code, dt = _float_code(k, "k"), k.dtype
     T, hkv, hd = shape
-    _call(dev, stream, load_library().kvq_paged_gather, *_pool(pages, hkv, hd), _ints(slots, "slots", T), T, hkv, hd,
+    _call(dev, stream, load_library().kvq_paged_gather, *_pool(pages, hkv, hd), _ints(slots, "slots", T, dev), T, hkv, hd,
           code, *_rows(k, "k", dt, shape), *_rows(v, "v", dt, shape))
 
 
@@ -576,8 +573,7 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     shape = q.shape
     if len(shape) not in (3, 4):
         raise ValueError("q must be [batch, n_q_heads, head_dim] or [batch, n_q_tokens, n_q_heads, head_dim]")
-    dev = _device_of("q pages page_table seq_lens out lse workspace", q, pages, page_table, seq_lens, out, lse,
-                     workspace)
+    dev = _device_of(q, "q")
     code, st, dt = _float_code(q, "q"), q.stride(), q.dtype
     B, hq, hd = shape[0], shape[-2], shape[-1]
     Q = shape[1] if len(shape) == 4 else 1
@@ -601,7 +597,7 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     max_pages = page_table.shape[1]
     if ts[1] != 1 and max_pages > 1:
         raise ValueError("page_table: the last dimension must be contiguous")
-    lens = _ints(seq_lens, "seq_lens", B)
+    lens = _ints(seq_lens, "seq_lens", B, dev)
     if workspace is None:
         torch = _torch
         with torch.cuda.device(dev):
