@@ -241,13 +241,18 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
   const long long n = ((long long)a.T + TOKENS - 1) / TOKENS * items;
   for (long long u = (long long)k0 * WARPS + (threadIdx.x >> 5); u < n; u += (long long)a.kv_blocks * WARPS) {
     const long long tp = quotient(u, items), t = tp * TOKENS + hh;
-    const int slot = t < a.T ? a.slots[t] : -1;
-    const bool live = slot >= 0 && slot / PG < a.n_pages;
-    if (!__any_sync(0xffffffffu, live)) continue;
-    const int at = live ? slot % PG : 0, h0 = (int)(u - tp * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
-    const bool down = at & 1;
+    const int h0 = (int)(u - tp * items) * a.per, h1 = min(a.Hkv, h0 + a.per);
+    const bool in = t < a.T;
     const unsigned short* kp = static_cast<const unsigned short*>(a.k) + t * a.kt + h0 * a.kh + E * sub;
     const unsigned short* vp = static_cast<const unsigned short*>(a.v) + t * a.vt + h0 * a.vh + E * sub;
+    // the token's slot and position and its first rows in one go, whether it turns out to be skipped or not
+    const int slot = in ? a.slots[t] : -1, pos = TURN != Turn::NONE && in ? a.pos[t] : 0;
+    Octet next_k = {}, next_v = {};
+    if (in) next_k.load(kp), next_v.load(vp);
+    const bool live = slot >= 0 && slot / PG < a.n_pages;
+    if (!__any_sync(0xffffffffu, live)) continue;
+    const int at = live ? slot % PG : 0;
+    const bool down = at & 1;
     // this lane's bytes of the codes, and its group's scale and offset (lane j = 0 writes)
     unsigned char* pg = a.pages + ((size_t)(live ? slot / PG : 0) * a.Hkv + h0) * L::BYTES;
     unsigned char* kc = pg + at * L::ROW + j * 4 * L::G + 4 * g;
@@ -255,13 +260,11 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
     __half* ks = reinterpret_cast<__half*>(pg + L::KS) + at * L::G + g;
     __half* vs = reinterpret_cast<__half*>(pg + L::VS) + g * PG + vscale_at(at);
     Rotation<HD, TURN, BF16> rot;
-    Octet next_k = {}, next_v = {};
-    if (live) next_k.load(kp), next_v.load(vp);
     for (int h = h0; h < h1; ++h) {
       const Octet rk = next_k, rv = next_v;
       kp += a.kh, vp += a.vh;
       if (live && h + 1 < h1) next_k.load(kp), next_v.load(vp);   // on their way while this head is coded
-      if (TURN != Turn::NONE && h == h0) rot.set(P, steps, live ? a.pos[t] : 0, lane);
+      if (TURN != Turn::NONE && h == h0) rot.set(P, steps, pos, lane);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         float x[E];
