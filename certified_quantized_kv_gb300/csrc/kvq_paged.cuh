@@ -84,23 +84,30 @@ __device__ __forceinline__ void f_to_elem(void* p, size_t i, float x, bool bf16)
 // ---- rotary phases ----
 // The angle of position p and pair i is p * step_i in units of 2^-64 turn, an exact
 // integer product modulo one turn whatever the position's size and sign.  Its top 32 bits,
-// rounded, less the nearest quarter turn are an angle pi x with |x| <= 1/4, where the Taylor
-// series of sine and cosine to x^9 and x^10 end below 2^-29 and 2^-33; the fp32 result is
-// within 2^-23.7 (sincospif of an angle rounded to fp32: 2^-22.5, and no faster: the 32K-token
-// append with its read-back 159 us, 158 with the series).
+// rounded, less the nearest quarter turn are an angle pi (x + l) with |x| <= 1/4, l what
+// fp32 loses of it, where the Taylor series of sine and cosine to x^9 and x^10 end below 2^-29
+// and 2^-33.  The leading terms are carried with their rounding errors, so that both results
+// lie within 2^-24.2 (sincospif of an angle rounded to fp32: 2^-22.5, and no faster: the
+// 32K-token append with its read-back 159 us, 158 with the series): keys are coded from them, and
+// each error moves some quotient across a half.
 __device__ __forceinline__ float2 rope_cos_sin(int pos, uint64_t step, float magnitude) {
   constexpr double PI = 3.14159265358979323846, P2 = PI * PI;
   constexpr float S1 = (float)PI, S1L = (float)(PI - (double)S1);
   constexpr float S3 = (float)(-PI * P2 / 6), S5 = (float)(PI * P2 * P2 / 120);
   constexpr float S7 = (float)(-PI * P2 * P2 * P2 / 5040), S9 = (float)(PI * P2 * P2 * P2 * P2 / 362880);
-  constexpr float C2 = (float)(-P2 / 2), C4 = (float)(P2 * P2 / 24), C6 = (float)(-P2 * P2 * P2 / 720);
-  constexpr float C8 = (float)(P2 * P2 * P2 * P2 / 40320), C10 = (float)(-P2 * P2 * P2 * P2 * P2 / 3628800);
+  constexpr float C2 = (float)(-P2 / 2), C2L = (float)(-P2 / 2 - (double)C2), C4 = (float)(P2 * P2 / 24);
+  constexpr float C6 = (float)(-P2 * P2 * P2 / 720), C8 = (float)(P2 * P2 * P2 * P2 / 40320);
+  constexpr float C10 = (float)(-P2 * P2 * P2 * P2 * P2 / 3628800), UNIT = 4.656612873077393e-10f /* 2^-31 */;
   const uint32_t a = (uint32_t)(((uint64_t)(int64_t)pos * step + 0x80000000ull) >> 32);   // 2^-32 turns
   const uint32_t quarter = (a + 0x20000000u) >> 30;
-  const float x = (float)(int32_t)(a - (quarter << 30)) * 4.656612873077393e-10f /* 2^-31 */, z = x * x;
+  const int32_t f = (int32_t)(a - (quarter << 30));
+  const float xf = (float)f, x = xf * UNIT, l = (float)(f - (int32_t)xf) * UNIT;
+  const float z = x * x, zl = fmaf(x + x, l, fmaf(x, x, -z));   // z + zl = (x + l)^2
   const float p = fmaf(fmaf(fmaf(fmaf(S9, z, S7), z, S5), z, S3), z, S1L);
-  const float sn = fmaf(x, S1, x * p);
-  const float cn = fmaf(fmaf(fmaf(fmaf(fmaf(C10, z, C8), z, C6), z, C4), z, C2), z, 1.f);
+  const float sn = fmaf(x, S1, fmaf(x, p, S1 * l));
+  const float q = fmaf(fmaf(fmaf(fmaf(C10, z, C8), z, C6), z, C4), z, C2L);
+  const float m = C2 * z, t = 1.f + m;   // their errors: fma(C2, z, -m), (1 - t) + m
+  const float cn = t + (fmaf(q, z, fmaf(C2, zl, fmaf(C2, z, -m))) + ((1.f - t) + m));
   // cos and sin of the angle and quarter turns more: (c, s), (-s, c), (-c, -s), (s, -c)
   const float c = (quarter & 1u) ? sn : cn, s = (quarter & 1u) ? cn : sn;
   return make_float2(__uint_as_float(__float_as_uint(c * magnitude) ^ ((quarter + 1u) >> 1 << 31)),

@@ -215,8 +215,8 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], float2 ext, bo
 //
 // The KV blocks are bound by the issue of their instructions (unpacking, rotation, the shuffles of
 // the extremes, the verified scale and codes), the q blocks by HBM; so the two kinds are spread
-// over the grid in turn.  32768 tokens of 32 + 8 heads of 128: 713 MB in 120 us (5.9 TB/s, a copy's
-// 6.8); 156 with the read-back behind it (registers for 8 blocks per SM gave 160 where these gave 159,
+// over the grid in turn.  32768 tokens of 32 + 8 heads of 128: 713 MB in 122 us (5.8 TB/s, a copy's
+// 6.8); 158 with the read-back behind it (registers for 8 blocks per SM gave 160 where these gave 159,
 // for 6 162).
 constexpr int APPEND_THREADS = 128;
 template <int HD, Turn TURN, int V, bool BF16>

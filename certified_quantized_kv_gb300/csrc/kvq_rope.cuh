@@ -22,7 +22,7 @@ struct RopeArgs {
 // at V = 8, which every layout with rotary_dim a multiple of 16 takes, all accesses are 16
 // bytes.  Smaller V serve the other rotary_dims (pairs that start or end between vectors); interleaved
 // pairs need no fewer than four.
-// A cosine and sine cost about 30 instructions.  With TABLE a block forms those of its tokens once, in
+// A cosine and sine cost about 40 instructions.  With TABLE a block forms those of its tokens once, in
 // shared memory (64 tokens of 40 heads: 2.44 us, 2.65 without; 4099 tokens of 13: 9.1 and 9.7);
 // without, each thread those of its pairs (in the append, whose blocks live on many warps in
 // different phases, the table's barriers cost more than they saved: 179 us against 167 when measured).
