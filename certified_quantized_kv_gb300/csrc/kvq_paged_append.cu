@@ -231,6 +231,13 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
   pdl_wait();
   // block b is KV block number floor(b kv / all) when that number changes behind it
   const unsigned k0 = blockIdx.x * a.kv_blocks / gridDim.x, k1 = (blockIdx.x + 1) * a.kv_blocks / gridDim.x;   // (products below 2^26)
+  if (TURN != Turn::NONE && V == 0 && k0 == k1) {
+    __shared__ float2 turns[TURN != Turn::NONE && V == 0 ? WARPS : 1][128];
+    const int warp = threadIdx.x >> 5;
+    rope_rows<BF16>(P, steps, rooms + 32 * warp, turns[warp], a.q, (long long)(blockIdx.x - k0) * WARPS + warp,
+                    (long long)(gridDim.x - a.kv_blocks) * WARPS);
+    return;
+  }
   if (V > 0 && k0 == k1) {
     rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16, APPEND_THREADS, false>(P, steps, nullptr, a.q, (long long)(blockIdx.x - k0) * APPEND_THREADS,
                                                                           (long long)(gridDim.x - a.kv_blocks) * APPEND_THREADS);
@@ -303,13 +310,12 @@ template <int HD, bool BF16>
 auto append_kernel_of(const kvq_rope_plan* plan) {
   using K = void (*)(kvq_rope_plan, AppendPagedArgs);
   if (!plan) return (K)paged_append_kernel<HD, Turn::NONE, 0, BF16>;
-  const int V = rope_pairs(*plan);   // per thread that turns q
+  const int V = rope_pairs(*plan);   // per thread that turns q (0: rope_rows)
   if (plan->interleaved)
     return V == 8 ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 4, BF16>;
   return V == 8   ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16>
          : V == 4 ? (K)paged_append_kernel<HD, Turn::ELEMENTS, 4, BF16>
-         : V == 2 ? (K)paged_append_kernel<HD, Turn::ELEMENTS, 2, BF16>
-                  : (K)paged_append_kernel<HD, Turn::ELEMENTS, 1, BF16>;
+                  : (K)paged_append_kernel<HD, Turn::ELEMENTS, 0, BF16>;
 }
 
 struct GatherArgs {
@@ -439,9 +445,18 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   a.kv_blocks = (int)blocks;
   if (q) {
     const bool copy = q != q_out && plan->rotary_dim < hd;
-    const int units = rope_units(*plan, rope_pairs(*plan), copy);
-    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, rope_lanes(T, Hq, units, ROOM / 2 * 32), copy};
-    blocks += std::min<long long>(((long long)T * a.q.lanes * units + APPEND_THREADS - 1) / APPEND_THREADS, 152 * 32);
+    const int V = rope_pairs(*plan);
+    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, 0, copy, 0};
+    long long q_blocks;
+    if (V) {
+      const int units = rope_units(*plan, V, copy);
+      a.q.lanes = rope_lanes(T, Hq, units, ROOM / 2 * 32);
+      q_blocks = ((long long)T * a.q.lanes * units + APPEND_THREADS - 1) / APPEND_THREADS;
+    } else {
+      a.q.per = rope_rows_heads(*plan, T, Hq, ROOM / 2);
+      q_blocks = ((long long)T * ((Hq + a.q.per - 1) / a.q.per) + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32);
+    }
+    blocks += std::min<long long>(q_blocks, 152 * 32);
   }
   const bool bf16 = dtype == KVQ_BF16;
   auto* kern = hd == 128 ? (bf16 ? append_kernel_of<128, true>(plan) : append_kernel_of<128, false>(plan))

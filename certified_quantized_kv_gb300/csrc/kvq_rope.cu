@@ -73,11 +73,23 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
   rope_part<V, INTERLEAVED, BF16, ROPE_THREADS, true>(P, step, turns, a, blockIdx.x * (long long)ROPE_THREADS, (long long)gridDim.x * ROPE_THREADS);
 }
 
+template <bool BF16>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_rows_kernel(const __grid_constant__ kvq_rope_plan P, RopeArgs a) {
+  constexpr int WARPS = ROPE_THREADS / 32;
+  __shared__ __align__(16) uint64_t step[128];
+  __shared__ uint4 rooms[ROPE_THREADS];
+  __shared__ float2 turns[WARPS][128];
+  pdl_trigger();
+  load_steps(P, step);
+  pdl_wait();
+  const int warp = threadIdx.x >> 5;
+  rope_rows<BF16>(P, step, rooms + 32 * warp, turns[warp], a, (long long)blockIdx.x * WARPS + warp, (long long)gridDim.x * WARPS);
+}
+
 template <bool INTERLEAVED, bool BF16>
 auto rope_kernel_of(int V) {
   if constexpr (INTERLEAVED) return V == 8 ? rope_kernel<8, true, BF16> : rope_kernel<4, true, BF16>;
-  else return V == 8 ? rope_kernel<8, false, BF16> : V == 4 ? rope_kernel<4, false, BF16>
-              : V == 2 ? rope_kernel<2, false, BF16> : rope_kernel<1, false, BF16>;
+  else return V == 8 ? rope_kernel<8, false, BF16> : V == 4 ? rope_kernel<4, false, BF16> : rope_rows_kernel<BF16>;
 }
 
 kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_t xt, int64_t xh,
@@ -102,10 +114,17 @@ kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_
   if (kvq_status s = check_buffer(positions, dev, 4, fn, "positions")) return s;
   const int V = rope_pairs(*plan);
   const bool copy = x != out && plan->rotary_dim < plan->head_dim;
-  const int units = rope_units(*plan, V, copy);
-  const int resident = V == 8 ? 3 : V == 4 ? 5 : 6;   // blocks per SM, by their registers
-  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, rope_lanes(T, H, units, 152ll * ROPE_THREADS * resident), copy};
-  const long long blocks = ((long long)T * a.lanes * units + ROPE_THREADS - 1) / ROPE_THREADS;
+  RopeArgs a{x, out, positions, xt, xh, ot, oh, T, H, 0, copy, 0};
+  long long blocks;
+  if (V) {
+    const int units = rope_units(*plan, V, copy), resident = V == 8 ? 3 : 5;   // blocks per SM, by their registers
+    a.lanes = rope_lanes(T, H, units, 152ll * ROPE_THREADS * resident);
+    blocks = ((long long)T * a.lanes * units + ROPE_THREADS - 1) / ROPE_THREADS;
+  } else {
+    constexpr int WARPS = ROPE_THREADS / 32;
+    a.per = rope_rows_heads(*plan, T, H, 152 * WARPS * 3);
+    blocks = ((long long)T * ((H + a.per - 1) / a.per) + WARPS - 1) / WARPS;
+  }
   const bool bf16 = dtype == KVQ_BF16;
   auto* k = plan->interleaved ? (bf16 ? rope_kernel_of<true, true>(V) : rope_kernel_of<true, false>(V))
                               : (bf16 ? rope_kernel_of<false, true>(V) : rope_kernel_of<false, false>(V));

@@ -15,6 +15,7 @@ struct RopeArgs {
   long long xt, xh, ot, oh;   // strides in elements
   int T, H, lanes;   // lanes: heads in step, each with a thread of its own per chunk of pairs
   bool copy;         // the elements behind the rotated ones as well
+  int per;           // heads of one item (rope_rows)
 };
 
 // One thread per V pairs of a token, for every `lanes`-th head; the loads of several heads are on
@@ -183,11 +184,79 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
   }
 }
 
+// The same for halves that are no multiple of 4, whose pairs start anywhere in their vectors: a warp
+// takes whole rows of one token, as many at once as its lanes hold vectors of, and a lane reads the
+// other elements of its vector's pairs out of shared memory (room: 32 vectors; turns: 128 (cos, sin)).
+// Item: a token's heads [h, h + a.per); warp w0 takes every `warps`-th one.
+template <bool BF16>
+__device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t* step, uint4* room, float2* turns, const RopeArgs& a,
+                                          long long w0, long long warps) {
+  constexpr int U = 4;   // rows of a lane on their way at once
+  const int lane = threadIdx.x & 31, half = P.rotary_dim / 2;
+  const int vecs = (P.rotary_dim + 7) / 8, rows = 32 / vecs;   // vectors of a row, rows at once
+  const int r = lane / vecs, c0 = 8 * (lane - r * vecs);       // this lane's row and first channel
+  const int items = (a.H + a.per - 1) / a.per;
+  const long long n = (long long)a.T * items;
+  for (long long u = w0; u < n; u += warps) {
+    const long long t = quotient(u, items);
+    const int h0 = (int)(u - t * items) * a.per, h1 = min(a.H, h0 + a.per);
+    const unsigned short* x = static_cast<const unsigned short*>(a.x) + t * a.xt;
+    unsigned short* out = static_cast<unsigned short*>(a.out) + t * a.ot;
+    uint4 v[U];
+    auto fetch = [&](int h) {
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (r < rows && h + k * rows + r < h1) v[k] = *reinterpret_cast<const uint4*>(x + (h + k * rows + r) * a.xh + c0);
+    };
+    fetch(h0);   // on their way while cos and sin are formed
+    const int pos = a.pos[t];
+    __syncwarp();   // the last item's readers are done
+    for (int i = lane; i < half; i += 32) turns[i] = rope_cos_sin(pos, step[i], P.magnitude);
+    __syncwarp();
+    float c[8], s[8];
+    int from[8];   // the other element of the pair
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int ch = c0 + e;
+      const bool in = ch < 2 * half, second = ch >= half;
+      const float2 cs = in ? turns[second ? ch - half : ch] : make_float2(1.f, 0.f);
+      c[e] = cs.x, s[e] = second ? cs.y : -cs.y;
+      from[e] = (lane * 8 - c0) + (!in ? ch : second ? ch - half : ch + half);
+    }
+    for (int h = h0; h < h1; h += U * rows) {
+      if (h != h0) fetch(h);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (h + k * rows >= h1) continue;
+        room[lane] = v[k];
+        __syncwarp();
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 p = pair_to_f2(word_of(v[k], i), BF16);
+          const uint32_t w = f2_to_pair(fmaf(p.x, c[2 * i], elem_to_f(room, from[2 * i], BF16) * s[2 * i]),
+                                        fmaf(p.y, c[2 * i + 1], elem_to_f(room, from[2 * i + 1], BF16) * s[2 * i + 1]), BF16);
+          y[i] = c0 + 2 * i < 2 * half ? w : word_of(v[k], i);   // (rotary_dim is even)
+        }
+        if (r < rows && h + k * rows + r < h1) *reinterpret_cast<uint4*>(out + (h + k * rows + r) * a.oh + c0) = make_uint4(y[0], y[1], y[2], y[3]);
+        __syncwarp();
+      }
+    }
+    if (a.copy) {   // the vectors behind
+      const int rest = P.head_dim / 8 - vecs;
+      for (int i = lane; i < (h1 - h0) * rest; i += 32) {
+        const int h = h0 + i / rest, e = 8 * (vecs + i % rest);
+        *reinterpret_cast<uint4*>(out + h * a.oh + e) = *reinterpret_cast<const uint4*>(x + h * a.xh + e);
+      }
+    }
+  }
+}
+
 // Pairs per thread: the widest vectors that divide the rotated half, and interleaved whole vectors of
-// four pairs at least, of which the last may lie partly behind the rotated elements.
+// four pairs at least, of which the last may lie partly behind the rotated elements.  0: rope_rows.
 inline int rope_pairs(const kvq_rope_plan& plan) {
   const int half = plan.rotary_dim / 2;
-  return half % 8 == 0 ? 8 : half % 4 == 0 || plan.interleaved ? 4 : half % 2 == 0 ? 2 : 1;
+  return half % 8 == 0 ? 8 : half % 4 == 0 || plan.interleaved ? 4 : 0;
 }
 
 // Pieces of a row: chunks of V pairs, and the vectors that are only copied.
@@ -205,6 +274,12 @@ inline int heads_each(long long T, int H, int each, long long room) {
   for (int per = 1; per <= 16; ++per)
     if (T * ((H + per - 1) / per) * each <= room) return per;
   return 8;
+}
+
+// Heads per item of rope_rows when `room` warps run at once.
+inline int rope_rows_heads(const kvq_rope_plan& plan, long long T, int H, long long room) {
+  const int rows = 32 / ((plan.rotary_dim + 7) / 8);
+  return heads_each(T, (H + rows - 1) / rows, 1, room) * rows;
 }
 
 // Heads in step (RopeArgs::lanes) when `room` threads run at once.
