@@ -231,17 +231,19 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
   pdl_wait();
   // block b is KV block number floor(b kv / all) when that number changes behind it
   const unsigned k0 = blockIdx.x * a.kv_blocks / gridDim.x, k1 = (blockIdx.x + 1) * a.kv_blocks / gridDim.x;   // (products below 2^26)
-  if (TURN != Turn::NONE && V == 0 && k0 == k1) {
-    __shared__ float2 turns[TURN != Turn::NONE && V == 0 ? WARPS : 1][128];
-    const int warp = threadIdx.x >> 5;
-    rope_rows<BF16>(P, steps, rooms + 32 * warp, turns[warp], a.q, (long long)(blockIdx.x - k0) * WARPS + warp,
-                    (long long)(gridDim.x - a.kv_blocks) * WARPS);
-    return;
-  }
-  if (V > 0 && k0 == k1) {
-    rope_part<V ? V : 1, TURN == Turn::INTERLEAVED, BF16, APPEND_THREADS, false>(P, steps, nullptr, a.q, (long long)(blockIdx.x - k0) * APPEND_THREADS,
-                                                                          (long long)(gridDim.x - a.kv_blocks) * APPEND_THREADS);
-    return;
+  if constexpr (TURN != Turn::NONE) {
+    if (k0 == k1) {
+      const long long mine = blockIdx.x - k0, all = gridDim.x - a.kv_blocks;
+      if constexpr (V == 0) {
+        __shared__ float2 turns[WARPS][128];
+        const int warp = threadIdx.x >> 5;
+        rope_rows<BF16>(P, steps, rooms + 32 * warp, turns[warp], a.q, mine * WARPS + warp, all * WARPS);
+      } else {
+        rope_part<V, TURN == Turn::INTERLEAVED, BF16, APPEND_THREADS, false>(P, steps, nullptr, a.q, mine * APPEND_THREADS,
+                                                                             all * APPEND_THREADS);
+      }
+      return;
+    }
   }
   const int lane = threadIdx.x & 31, sub = lane % LANES, hh = lane / LANES, g = sub / 4, j = sub % 4;
   uint4* room = rooms + (TURN == Turn::ELEMENTS ? threadIdx.x - lane : 0);
@@ -453,7 +455,7 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
       a.q.lanes = rope_lanes(T, Hq, units, ROOM / 2 * 32);
       q_blocks = ((long long)T * a.q.lanes * units + APPEND_THREADS - 1) / APPEND_THREADS;
     } else {
-      a.q.per = rope_rows_heads(*plan, T, Hq, ROOM / 2);
+      a.q.per = rope_rows_heads(*plan, copy, T, Hq, ROOM / 2);
       q_blocks = ((long long)T * ((Hq + a.q.per - 1) / a.q.per) + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32);
     }
     blocks += std::min<long long>(q_blocks, 152 * 32);

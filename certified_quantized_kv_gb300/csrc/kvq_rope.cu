@@ -122,7 +122,7 @@ kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_
     blocks = ((long long)T * a.lanes * units + ROPE_THREADS - 1) / ROPE_THREADS;
   } else {
     constexpr int WARPS = ROPE_THREADS / 32;
-    a.per = rope_rows_heads(*plan, T, H, 152 * WARPS * 3);
+    a.per = rope_rows_heads(*plan, copy, T, H, 152 * WARPS * 3);
     blocks = ((long long)T * ((H + a.per - 1) / a.per) + WARPS - 1) / WARPS;
   }
   const bool bf16 = dtype == KVQ_BF16;

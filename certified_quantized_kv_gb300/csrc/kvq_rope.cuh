@@ -21,16 +21,16 @@ struct RopeArgs {
 // One thread per V pairs of a token, for every `lanes`-th head; the loads of several heads are on
 // their way at once.  HBM bound (4 bytes per element, 32K tokens of 40 heads of 128: 671 MB);
 // at V = 8, which every layout with rotary_dim a multiple of 16 takes, all accesses are 16
-// bytes.  Smaller V serve the other rotary_dims (pairs that start or end between vectors); interleaved
-// pairs need no fewer than four.
+// bytes.  V = 4 serves halves that are odd multiples of 4, and interleaved pairs of every other
+// rotary_dim; rope_rows (below) what is left.
 // A cosine and sine cost about 40 instructions.  With TABLE a block forms those of its tokens once, in
 // shared memory (64 tokens of 40 heads: 2.44 us, 2.65 without; 4099 tokens of 13: 9.1 and 9.7);
 // without, each thread those of its pairs (in the append, whose blocks live on many warps in
 // different phases, the table's barriers cost more than they saved: 179 us against 167 when measured).
 
 template <int N>
-struct Words {   // N elements in one or two loads of at most 16 bytes
-  static constexpr int W = N > 2 ? N / 2 : 1;
+struct Words {   // N = 4, 8 or 16 elements in one or two loads of at most 16 bytes
+  static constexpr int W = N / 2;
   uint32_t w[W];
   __device__ __forceinline__ void load(const unsigned short* p) {
     if constexpr (N == 16) {
@@ -39,13 +39,9 @@ struct Words {   // N elements in one or two loads of at most 16 bytes
     } else if constexpr (N == 8) {
       const uint4 a = *reinterpret_cast<const uint4*>(p);
       w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-    } else if constexpr (N == 4) {
+    } else {
       const uint2 a = *reinterpret_cast<const uint2*>(p);
       w[0] = a.x, w[1] = a.y;
-    } else if constexpr (N == 2) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-      w[0] = *p;
     }
   }
   __device__ __forceinline__ void store(unsigned short* p) const {
@@ -54,12 +50,8 @@ struct Words {   // N elements in one or two loads of at most 16 bytes
       reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     } else if constexpr (N == 8) {
       *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if constexpr (N == 4) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    } else if constexpr (N == 2) {
-      *reinterpret_cast<uint32_t*>(p) = w[0];
     } else {
-      *p = (unsigned short)w[0];
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
   }
 };
@@ -166,7 +158,7 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
 #pragma unroll
           for (int i = 0; i < Words<N0>::W; ++i) {
             const float2 p = pair_to_f2(A[k].w[i], BF16), q = pair_to_f2(B[k].w[i], BF16);
-            const float2 c0 = cs[2 * i], c1 = cs[V > 1 ? 2 * i + 1 : 0];
+            const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
             A[k].w[i] = f2_to_pair(fmaf(p.x, c0.x, -q.x * c0.y), fmaf(p.y, c1.x, -q.y * c1.y), BF16);
             B[k].w[i] = f2_to_pair(fmaf(q.x, c0.x, p.x * c0.y), fmaf(q.y, c1.x, p.y * c1.y), BF16);
           }
@@ -176,25 +168,28 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
         if (!INTERLEAVED) B[k].store(o + e1);
       }
     }
-    if (!INTERLEAVED && a.copy && c == 0) {   // what lies between the rotated elements and the next whole vector
-      const int e1 = min(P.head_dim, (P.rotary_dim + 7) / 8 * 8);
-      for (int h = h0; h < a.H; h += a.lanes)
-        for (int e = P.rotary_dim; e < e1; ++e) out[h * a.oh + e] = x[h * a.xh + e];
-    }
   }
+}
+
+// Vectors of a row that are rotated, or all of them with the copied ones.
+__host__ __device__ __forceinline__ int row_vectors(const kvq_rope_plan& P, bool copy) {
+  return (copy ? P.head_dim : P.rotary_dim + 7) / 8;
 }
 
 // The same for halves that are no multiple of 4, whose pairs start anywhere in their vectors: a warp
 // takes whole rows of one token, as many at once as its lanes hold vectors of, and a lane reads the
 // other elements of its vector's pairs out of shared memory (room: 32 vectors; turns: 128 (cos, sin)).
+// 4000 tokens of 32 heads of 128 from buffer to buffer, 52 elements rotated: 13.6 us; pairs by threads of
+// their own, as above with V = 2: 23.2.  With half = 52, V = 4: 14.3 us, rows 17.3.
 // Item: a token's heads [h, h + a.per); warp w0 takes every `warps`-th one.
 template <bool BF16>
 __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t* step, uint4* room, float2* turns, const RopeArgs& a,
                                           long long w0, long long warps) {
   constexpr int U = 4;   // rows of a lane on their way at once
   const int lane = threadIdx.x & 31, half = P.rotary_dim / 2;
-  const int vecs = (P.rotary_dim + 7) / 8, rows = 32 / vecs;   // vectors of a row, rows at once
+  const int vecs = row_vectors(P, a.copy), rows = 32 / vecs;   // vectors of a row, rows at once
   const int r = lane / vecs, c0 = 8 * (lane - r * vecs);       // this lane's row and first channel
+  const bool even = half % 2 == 0;
   const int items = (a.H + a.per - 1) / a.per;
   const long long n = (long long)a.T * items;
   for (long long u = w0; u < n; u += warps) {
@@ -233,20 +228,16 @@ __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t
         uint32_t y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 p = pair_to_f2(word_of(v[k], i), BF16);
-          const uint32_t w = f2_to_pair(fmaf(p.x, c[2 * i], elem_to_f(room, from[2 * i], BF16) * s[2 * i]),
-                                        fmaf(p.y, c[2 * i + 1], elem_to_f(room, from[2 * i + 1], BF16) * s[2 * i + 1]), BF16);
+          // (pairs of an even half lie in whole words)
+          const uint32_t other = even ? reinterpret_cast<const uint32_t*>(room)[from[2 * i] / 2]
+                                      : (uint32_t) reinterpret_cast<const unsigned short*>(room)[from[2 * i]] |
+                                            ((uint32_t) reinterpret_cast<const unsigned short*>(room)[from[2 * i + 1]] << 16);
+          const float2 p = pair_to_f2(word_of(v[k], i), BF16), o = pair_to_f2(other, BF16);
+          const uint32_t w = f2_to_pair(fmaf(p.x, c[2 * i], o.x * s[2 * i]), fmaf(p.y, c[2 * i + 1], o.y * s[2 * i + 1]), BF16);
           y[i] = c0 + 2 * i < 2 * half ? w : word_of(v[k], i);   // (rotary_dim is even)
         }
         if (r < rows && h + k * rows + r < h1) *reinterpret_cast<uint4*>(out + (h + k * rows + r) * a.oh + c0) = make_uint4(y[0], y[1], y[2], y[3]);
         __syncwarp();
-      }
-    }
-    if (a.copy) {   // the vectors behind
-      const int rest = P.head_dim / 8 - vecs;
-      for (int i = lane; i < (h1 - h0) * rest; i += 32) {
-        const int h = h0 + i / rest, e = 8 * (vecs + i % rest);
-        *reinterpret_cast<uint4*>(out + h * a.oh + e) = *reinterpret_cast<const uint4*>(x + h * a.xh + e);
       }
     }
   }
@@ -256,7 +247,7 @@ __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t
 // four pairs at least, of which the last may lie partly behind the rotated elements.  0: rope_rows.
 inline int rope_pairs(const kvq_rope_plan& plan) {
   const int half = plan.rotary_dim / 2;
-  return half % 8 == 0 ? 8 : half % 4 == 0 || plan.interleaved ? 4 : 0;
+    return half % 8 == 0 ? 8 : half % 4 == 0 || plan.interleaved ? 4 : 0;
 }
 
 // Pieces of a row: chunks of V pairs, and the vectors that are only copied.
@@ -277,8 +268,8 @@ inline int heads_each(long long T, int H, int each, long long room) {
 }
 
 // Heads per item of rope_rows when `room` warps run at once.
-inline int rope_rows_heads(const kvq_rope_plan& plan, long long T, int H, long long room) {
-  const int rows = 32 / ((plan.rotary_dim + 7) / 8);
+inline int rope_rows_heads(const kvq_rope_plan& plan, bool copy, long long T, int H, long long room) {
+  const int rows = 32 / row_vectors(plan, copy);
   return heads_each(T, (H + rows - 1) / rows, 1, room) * rows;
 }
 
