@@ -106,6 +106,29 @@ def test_rope_extreme_positions():
     assert np.abs(_f64(out) - ref).max() <= 8 * (2.0 ** -11 + 2.0 ** -16)
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,H,D,rd", [(7, 40, 128, 42), (3, 13, 256, 250), (500, 33, 64, 18), (40, 9, 80, 74), (2, 70, 128, 4),
+                                      (5000, 3, 128, 52), (1, 1, 16, 10)])
+def test_rope_of_halves_across_vectors(T, H, D, rd, dt):
+    """Halves that are no multiple of 4: out of place into a wider buffer, and in place."""
+    kw = ROPES[3]
+    plan = kvq.RopePlan(D, rotary_dim=rd, **kw)
+    x = _randn((T, H, D), dt, T + H)
+    pos = torch.randint(-100000, 100000, (T,), generator=_gen(rd)).int().cuda()
+    wide = torch.full((T, H + 1, D), 3.0, dtype=dt, device="cuda")
+    out = kvq.rope(x, pos, plan, out=wide[:, :H])
+    _check_rope(out, x, pos, kw, D, rd, False)
+    assert (wide[:, H] == 3).all()
+    same = x.clone()
+    kvq.rope(same, pos, plan, out=same)
+    assert torch.equal(same, out)
+    if D in (64, 128):      # the same rotation beside the append
+        pages = torch.zeros(-(-T // 64), H, kvq.paged_page_bytes(D), dtype=torch.uint8, device="cuda")
+        q = x.clone()
+        kvq.paged_append(pages, x, x, torch.arange(T).int().cuda(), positions=pos, plan=plan, q=x, q_out=q)
+        assert torch.equal(q, out)
+
+
 def test_rope_phases_where_the_products_cancel():
     """a cos - b sin with a / b close to tan: what is left shows the cosine's and the sine's own
     errors.  Both lie within 2^-23.5 (series, roundings and the angle's), the two products and
