@@ -2,9 +2,9 @@
 // keys and queries on the way), and back out of them.
 //
 // Per token, KV head and group of 32 channels (x the rotated key or the value, in fp32):
-//   s = fp16 rounded up of (max - min) / 15, o = fp16(min), code = clamp(rint((x - o) / s), 0, 15)
+//   o = fp16(min), s = fp16 rounded up of (max - o) / 15, code = clamp(rint((x - o) / s), 0, 15)
 // and for the values of odd slots, counted down from the maximum,
-//   s = -(fp16 rounded up of (max - min) / 15), o = fp16(max), code = clamp(rint((o - x) / |s|), 0, 15)
+//   o = fp16(max), s = -(fp16 rounded up of (o - min) / 15), code = clamp(rint((o - x) / |s|), 0, 15)
 // so x^ = o + s code in both.  The scale is rounded up so that 15 steps span the group.
 #include <algorithm>
 #include <string>
@@ -158,9 +158,10 @@ __device__ __forceinline__ float2 extremes(const Octet& r) {
 }
 
 // Scale, offset and packed codes (4 bits each, from bit 0) of this lane's elements of a
-// group with extremes lo and hi.  The scale is the smallest binary16 h with 15 h >= the span (15 h
-// is exact in fp32), which is the span / 15 rounded up.  Codes are rint(d / |s|) for the exact
-// quotient: they come from a product with the reciprocal, and the remainder d - code s, exact
+// group with extremes lo and hi.  The scale is the smallest binary16 h with 15 h >= the span,
+// which is the span / 15 rounded up; 15 h is exact in fp32, so that it is at least the exact span
+// where it is at least the span rounded up to fp32.  Codes are rint(d / |s|) for d = x - o in fp32 and
+// the exact quotient: they come from a product with the reciprocal, and the remainder d - code s, exact
 // near a half, tells where a neighbour is nearer, or as near and even (values on the binary16
 // grid meet exact halves in about one element of a hundred).  The slow path also clamps the codes,
 // which only elements beyond the rounded offset or the binary16 range need.  Extremes that are NaN
@@ -169,7 +170,7 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], float2 ext, bo
   constexpr float RND = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, ties to even
   const float lo = min_nan(max_nan(ext.x, -65504.f), 65504.f), hi = min_nan(max_nan(ext.y, -65504.f), 65504.f);
   oh = __float2half_rn(down ? hi : lo);
-  const float of = __half2float(oh), span = fmaxf(down ? of - lo : hi - of, 0.f);
+  const float of = __half2float(oh), span = fmaxf(__fsub_ru(down ? of : hi, down ? lo : of), 0.f);
   const float before = down ? ext.y - of : of - ext.x;   // how far the extreme lies before the offset,
   const float behind = (down ? of - ext.x : ext.y - of) - span;   // and the other one behind the span
   const unsigned short h = __half_as_ushort(__float2half_ru(span * 0.06666667f));

@@ -309,10 +309,11 @@ kvq_status kvq_dense_decode_noalloc(const void* q, const void* k, const void* v,
  * device buffer [n_pages][Hkv][kvq_paged_page_bytes(D)], 16-byte aligned, whose initial
  * contents do not matter.  Keys and values are held in 4 bits per element with a binary16
  * scale s and offset o per (token, 32-channel group), x^ = o + s * code, code in 0..15:
- * s = fp16 rounded up of (max - min) / 15, o = fp16 of the group's minimum and code =
- * rint((x - o) / s), ties to even, clamped.  Values of odd slots count down from the
- * maximum instead (o = fp16 of the maximum, s negative), so that sums of codes over tokens
- * change sign from one token to the next and do not lose precision to a common offset.
+ * o = fp16 of the group's minimum, s = fp16 rounded up of (max - o) / 15 and code =
+ * rint((x - o) / s), ties to even, clamped, for the x - o that fp32 holds.  Values of odd
+ * slots count down from the maximum instead (o = fp16 of the maximum, s the negative of
+ * (o - min) / 15 rounded up), so that sums of codes over tokens change sign from one token to
+ * the next and do not lose precision to a common offset.
  * Elements beyond the binary16 range are held as +-65504; a NaN makes its group's offset NaN,
  * so that the 32 channels read as NaN.  Slot p * 64 + i is token i of
  * page p.

@@ -1,0 +1,35 @@
+"""The paged 4-bit cache on the GPU at the edges of its number ranges and of its calls.  Definitions and
+tolerances are those of tests/test_gpu_paged.py where nothing else is said."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import certified_quantized_kv_gb300 as kvq  # noqa: E402
+import _paged as P  # noqa: E402
+from test_gpu_paged import TYPES, _check_append, _f64, _gen, _ints  # noqa: E402
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_of_spans_that_fp32_does_not_hold(D, dt):
+    """A large extreme of 15 h (h binary16) beside a tiny one of the other sign: the span passes 15 h by
+    less than fp32 shows, and 15 steps of h do not reach over it.  Scales and offsets are exact."""
+    T, H, G = 64, 2, D // 32
+    tiny = 2.0 ** -24        # in both types and in binary16
+    g = _gen(D)
+    x = torch.rand(T, H, G, 32, generator=g) * 7 + 1
+    h = 2.0 ** torch.randint(0, 5, (T, H, G), generator=g)
+    sign = torch.where(torch.rand(T, H, G, generator=g) < 0.5, -1.0, 1.0)
+    x[..., 3], x[..., 17] = 15 * h, -tiny
+    x = (x * sign[..., None]).reshape(T, H, D).to(dt).cuda()
+    pages = torch.zeros(2, H, P.page_bytes(D), dtype=torch.uint8, device="cuda")
+    slots = _ints(list(range(20, 20 + T)))
+    before = pages.clone()
+    kvq.paged_append(pages, x, x, slots)
+    _check_append(before, pages, _f64(x), _f64(x), slots, D)
