@@ -176,6 +176,18 @@ __host__ __device__ __forceinline__ int row_vectors(const kvq_rope_plan& P, bool
   return (copy ? P.head_dim : P.rotary_dim + 7) / 8;
 }
 
+// rope_rows (below): the first channel of a lane's vector.  Lanes left over behind the warp's last whole row
+// count on from there, behind every rotated channel, so that their elements are their own partners.
+__host__ __device__ __forceinline__ int row_channel(int lane, int vecs) {
+  const int r = lane / vecs;
+  return 8 * (r < 32 / vecs ? lane - r * vecs : lane);
+}
+// Where in a warp's room, eight elements per lane, the other element of the pair of channel ch lies, for a
+// lane whose vector starts with channel c0; the channel's own place when it is not rotated.
+__host__ __device__ __forceinline__ int row_partner(int lane, int c0, int ch, int half) {
+  return (lane * 8 - c0) + (ch >= 2 * half ? ch : ch >= half ? ch - half : ch + half);
+}
+
 // The same for halves that are no multiple of 4, whose pairs start anywhere in their vectors: a warp
 // takes whole rows of one token, as many at once as its lanes hold vectors of, and a lane reads the
 // other elements of its vector's pairs out of shared memory (room: 32 vectors; turns: 128 (cos, sin)).
@@ -188,7 +200,7 @@ __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t
   constexpr int U = 4;   // rows of a lane on their way at once
   const int lane = threadIdx.x & 31, half = P.rotary_dim / 2;
   const int vecs = row_vectors(P, a.copy), rows = 32 / vecs;   // vectors of a row, rows at once
-  const int r = lane / vecs, c0 = 8 * (lane - r * vecs);       // this lane's row and first channel
+  const int r = lane / vecs, c0 = row_channel(lane, vecs);     // this lane's row and first channel
   const bool even = half % 2 == 0;
   const int items = (a.H + a.per - 1) / a.per;
   const long long n = (long long)a.T * items;
@@ -197,7 +209,7 @@ __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t
     const int h0 = (int)(u - t * items) * a.per, h1 = min(a.H, h0 + a.per);
     const unsigned short* x = static_cast<const unsigned short*>(a.x) + t * a.xt;
     unsigned short* out = static_cast<unsigned short*>(a.out) + t * a.ot;
-    uint4 v[U];
+    uint4 v[U] = {};   // (lanes without a row take part in the exchange)
     auto fetch = [&](int h) {
 #pragma unroll
       for (int k = 0; k < U; ++k)
@@ -216,7 +228,7 @@ __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t
       const bool in = ch < 2 * half, second = ch >= half;
       const float2 cs = in ? turns[second ? ch - half : ch] : make_float2(1.f, 0.f);
       c[e] = cs.x, s[e] = second ? cs.y : -cs.y;
-      from[e] = (lane * 8 - c0) + (!in ? ch : second ? ch - half : ch + half);
+      from[e] = row_partner(lane, c0, ch, half);
     }
     for (int h = h0; h < h1; h += U * rows) {
       if (h != h0) fetch(h);
