@@ -60,6 +60,18 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
+// ---- a ring of stages filled by bulk copies ----
+// Copy number i goes to stage i % STAGES and completes phase i / STAGES of that stage's barrier.
+template <int STAGES>
+__host__ __device__ __forceinline__ constexpr int ring_stage(int i) { return i % STAGES; }
+template <int STAGES>
+__host__ __device__ __forceinline__ constexpr uint32_t ring_parity(int i) { return (uint32_t)(i / STAGES) & 1u; }
+// Waits for what may be in flight once `issued` copies were issued: the last one of each stage.
+template <int STAGES, typename Wait>
+__host__ __device__ __forceinline__ void ring_drain(int issued, const Wait& wait) {   // wait(stage, parity)
+  for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i) wait(ring_stage<STAGES>(i), ring_parity<STAGES>(i));
+}
+
 // ---- element types of q, k, v and outputs (kvq_dtype) ----
 __device__ __forceinline__ float2 pair_to_f2(uint32_t u, bool bf16) {
   if (bf16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));

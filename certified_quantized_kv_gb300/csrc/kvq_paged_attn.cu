@@ -119,6 +119,12 @@ __device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity) {
   return pa_try(bar, parity) || pa_wait_slow(bar, parity);
 }
 
+// Behind a wait that ran out, when nothing more is issued: for the copies still in flight (not inlined, to stay
+// out of the page loop: 8 sequences of 65536 tokens 108.7 us, inlined 109.6)
+__device__ __noinline__ void pa_drain(uint32_t bar0, int issued) {
+  ring_drain<PA_STAGES>(issued, [&](int k, uint32_t parity) { pa_wait_slow(bar0 + 8 * k, parity); });
+}
+
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -436,6 +442,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
                             // page numbers one further
   int next_id = pw.x < n_pos ? a.table[pw.b * a.table_stride + pw.first + pw.p] : 0;
   uint32_t valid = 0;       // bit s: stage s holds a page
+  int issued = 0;           // copies so far
   const unsigned char* head = a.pages + (pw.gr / a.RT) * L::BYTES;   // the KV head's part of page 0
   // pages are read once, unless several row tiles take them
   unsigned long long pol = evict_first_policy();
@@ -454,6 +461,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
       }
     }
+    ++issued;
     const int gr = pw.gr;
     advance(pw);
     if (pw.gr != gr) head = a.pages + (pw.gr / a.RT) * L::BYTES;
@@ -918,8 +926,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       open = true;
       started = cw.p == 0;
     }
-    const int s = it % PA_STAGES;
-    if (!failed && !pa_wait(bar_s + 8 * s, (uint32_t)(it / PA_STAGES) & 1u)) failed = true;
+    const int s = ring_stage<PA_STAGES>(it);
+    if (!failed && !pa_wait(bar_s + 8 * s, ring_parity<PA_STAGES>(it))) failed = true;
     failed = __any_sync(0xffffffffu, failed);
     if (!failed && ((valid >> s) & 1u)) page(ring + s * L::BYTES, (cw.first + cw.p) * PG);
     __syncwarp();
@@ -930,6 +938,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
     const bool end = at.p + 1 == at.np;
     if (end || cw.x >= n_pos) {
       // an open group's piece goes to the ring, which no copy uses any more
+      if (failed) pa_drain(bar_s, issued), issued = 0;
       float* dst = !end ? reinterpret_cast<float*>(ring) : started ? nullptr : a.part + (size_t)gw * PART;
       emit(at, dst);
       if (lane == 0) {
@@ -944,8 +953,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       open = false;
     }
   }
-  if (failed)   // the copies still in flight write into this CTA's memory: wait for them, within limits
-    for (int k = 0; k < PA_STAGES && it - 1 - k >= 0; ++k) pa_wait(bar_s + 8 * ((it - 1 - k) % PA_STAGES), (uint32_t)((it - 1 - k) / PA_STAGES) & 1u);
   __syncthreads();
 
   // ---- groups that were cut ----

@@ -45,11 +45,47 @@ void rows() {
   EXPECT(plans > 2000, "only %d plans", plans);
 }
 
+// A warp that fills a ring ahead of its work, with a copy that does not arrive in time: behind the drain
+// nothing is in flight any more, whatever the number of pages and the copy.
+template <int STAGES>
+void ring() {
+  for (int pages = 1; pages <= 20; ++pages)
+    for (int late = 0; late < pages; ++late) {
+      int done[STAGES] = {}, pending[STAGES] = {};   // phases completed, copies in flight
+      int issued = 0;
+      // a barrier's wait for a parity returns once the phase of that parity is behind it
+      auto ready = [&](int stage, uint32_t parity) { return (uint32_t)(done[stage] & 1) != parity; };
+      auto land = [&](int stage) { ++done[stage], --pending[stage]; };
+      auto issue = [&] { EXPECT(++pending[kvq::ring_stage<STAGES>(issued++)] == 1, "%d pages: a stage is filled twice", pages); };
+      while (issued < pages && issued < STAGES) issue();
+      bool failed = false;
+      for (int it = 0; it < pages; ++it) {
+        const int s = kvq::ring_stage<STAGES>(it);
+        if (!failed) {
+          EXPECT(!ready(s, kvq::ring_parity<STAGES>(it)), "%d pages: page %d seen before its copy", pages, it);
+          if (it != late) {
+            land(s);
+            EXPECT(ready(s, kvq::ring_parity<STAGES>(it)), "%d pages: page %d not seen", pages, it);
+          } else {
+            failed = true;
+            kvq::ring_drain<STAGES>(issued, [&](int stage, uint32_t parity) {
+              if (!ready(stage, parity)) land(stage);
+              EXPECT(ready(stage, parity), "%d pages, %d late: a wait for another phase", pages, late);
+            });
+            for (int k = 0; k < STAGES; ++k) EXPECT(pending[k] == 0, "%d pages, %d late: stage %d in flight", pages, late, k);
+          }
+        }
+        if (!failed && issued < pages) issue();
+      }
+    }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   const char* what = argc > 1 ? argv[1] : "";
   if (!std::strcmp(what, "rows")) rows();
+  else if (!std::strcmp(what, "ring")) ring<1>(), ring<2>(), ring<3>(), ring<4>();
   else EXPECT(false, "no check named '%s'", what);
   if (!wrong) std::puts("ok");
   return wrong != 0;

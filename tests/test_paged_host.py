@@ -31,3 +31,8 @@ def _run(program, check):
 def test_rows_exchange_within_the_room_of_their_warp(program):
     """Rotation of halves that are no multiple of 4: no lane reads outside its warp's shared memory."""
     _run(program, "rows")
+
+
+def test_a_late_copy_is_waited_for(program):
+    """The paged attention's ring after a wait that ran out: the copies in flight are the ones waited for."""
+    _run(program, "ring")
