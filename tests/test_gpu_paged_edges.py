@@ -1,7 +1,10 @@
 """The paged 4-bit cache on the GPU at the edges of its number ranges and of its calls.  Definitions and
 tolerances are those of tests/test_gpu_paged.py where nothing else is said."""
 
-import numpy as np
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -13,6 +16,8 @@ if not torch.cuda.is_available():  # pragma: no cover
 import certified_quantized_kv_gb300 as kvq  # noqa: E402
 import _paged as P  # noqa: E402
 from test_gpu_paged import TYPES, _check_append, _f64, _gen, _ints  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("dt", TYPES)
@@ -33,3 +38,16 @@ def test_scales_of_spans_that_fp32_does_not_hold(D, dt):
     before = pages.clone()
     kvq.paged_append(pages, x, x, slots)
     _check_append(before, pages, _f64(x), _f64(x), slots, D)
+
+
+def test_pieces_of_a_warp_whose_copy_never_arrived(tmp_path):
+    """The merge of an attention call's pieces by itself (tests/host/paged_merge.cu): sums as in 64 bits, and NaN
+    rows where a piece may hold anything."""
+    nvcc = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    exe = str(tmp_path / "paged_merge")
+    cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I",
+           os.path.join(ROOT, "certified_quantized_kv_gb300", "csrc"), os.path.join(ROOT, "tests", "host", "paged_merge.cu"), "-o", exe]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout[-3000:] + r.stderr[-1000:]
