@@ -60,6 +60,7 @@ constexpr int PA_LEAD = HD == 64 ? PA_MAX_LEAD : 2;
 constexpr float PA_TOP = 14.f;                              // weights are 2^14 at most,
 constexpr float PA_SLACK = 4.f;                             // 2^10 when their reference is set
 constexpr unsigned long long PA_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
+constexpr int PA_MAX_BATCH = 2048;                          // positions and lengths lie in shared memory
 
 struct PaArgs {
   const void* q;
@@ -904,7 +905,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
 }
 
 const char* shape_error(int B, int Q, int Hq, int Hkv, int hd) {
-  if (B < 0 || B > 2048) return "batch must be in 0..2048";
+  if (B < 0 || B > PA_MAX_BATCH) return "batch must be in 0..2048";
   if (Q < 1 || Q > 64) return "n_q_tokens must be in 1..64";
   if (Hkv > MAX_KV_HEADS) return "n_kv_heads must be in 1..4096";
   if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 64) return "n_q_heads / n_kv_heads must be an integer in 1..64";
@@ -940,11 +941,14 @@ size_t ws_bytes(int sms, int Q, int Hq, int Hkv, int hd) {
 
 template <int HD, int R>
 cudaError_t launch(const PaArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)PA_WARPS * (PA_STAGES * Page<HD>::BYTES + PaStage<HD>::FLOATS * sizeof(float)) +
-                      (2 * (size_t)a.B + 1) * sizeof(int);
+  auto bytes = [](int batch) {
+    return (size_t)PA_WARPS * (PA_STAGES * Page<HD>::BYTES + PaStage<HD>::FLOATS * sizeof(float)) + (2 * (size_t)batch + 1) * sizeof(int);
+  };
   auto* k = paged_attention_kernel<HD, R>;
-  if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-  return launch_dependent(k, dim3(a.grid), dim3(PA_THREADS), smem, st, a);
+  // the limit belongs to the function and is every host thread's: always the one of the largest batch, so that
+  // no call lowers another's
+  if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(PA_MAX_BATCH))) return e;
+  return launch_dependent(k, dim3(a.grid), dim3(PA_THREADS), bytes(a.B), st, a);
 }
 
 kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, const void* pages, int n_pages,

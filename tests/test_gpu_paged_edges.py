@@ -40,14 +40,30 @@ def test_scales_of_spans_that_fp32_does_not_hold(D, dt):
     _check_append(before, pages, _f64(x), _f64(x), slots, D)
 
 
+def _compiled(tmp_path, name, *flags):
+    """tests/host/<name>.cu, built against the kernels' headers."""
+    nvcc = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    exe = str(tmp_path / name)
+    cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I",
+           os.path.join(ROOT, "certified_quantized_kv_gb300", "csrc"), os.path.join(ROOT, "tests", "host", name + ".cu"), *flags, "-o", exe]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    return exe
+
+
+def _says_ok(exe):
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout[-3000:] + r.stderr[-1000:]
+
+
 def test_pieces_of_a_warp_whose_copy_never_arrived(tmp_path):
     """The merge of an attention call's pieces by itself (tests/host/paged_merge.cu): sums as in 64 bits, and NaN
     rows where a piece may hold anything."""
-    nvcc = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
-    exe = str(tmp_path / "paged_merge")
-    cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I",
-           os.path.join(ROOT, "certified_quantized_kv_gb300", "csrc"), os.path.join(ROOT, "tests", "host", "paged_merge.cu"), "-o", exe]
-    r = subprocess.run(cmd, capture_output=True, text=True, timeout=300)
-    assert r.returncode == 0, r.stderr[-3000:]
-    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
-    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout[-3000:] + r.stderr[-1000:]
+    _says_ok(_compiled(tmp_path, "paged_merge"))
+
+
+def test_attention_calls_of_several_host_threads(tmp_path):
+    """Threads with batches of their own size, streams and workspaces (tests/host/paged_threads.cu): no call
+    takes shared memory away from another one's launch."""
+    lib = os.path.dirname(kvq.LIB_PATH)
+    _says_ok(_compiled(tmp_path, "paged_threads", "-L", lib, "-l:libkvq.so", "-Xlinker", "-rpath", "-Xlinker", lib))
