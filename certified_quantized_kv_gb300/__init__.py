@@ -390,6 +390,15 @@ class RopePlan:
         self.address = ctypes.addressof(self.plan)
         self.head_dim = head_dim
 
+    # copies and pickled plans hold a struct of their own, at their own address
+    def __getstate__(self):
+        return {**self.__dict__, "plan": bytes(self.plan), "address": None}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self.plan = kvq_rope_plan.from_buffer_copy(state["plan"])
+        self.address = ctypes.addressof(self.plan)
+
 
 # The calls below are made once per layer and token, where their host time counts (a decoding
 # step of a few microseconds on the device): operands are checked with as few attribute reads
