@@ -419,22 +419,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the row times 2^e with a largest element in [2^9, 2^10): binary16 keeps all of a
-      // binary16 or bfloat16 element down to 2^-24 of 2^10 (elements below lose bits that
-      // are 2^-34 of the row's largest), and the sums of 32 stay finite
+      // the row times 2^e with a largest element in [2^9, 2^10), whatever its size down to 2^-117.  Binary16 then
+      // keeps all of a binary16 or bfloat16 element down to 2^-24 of 2^10, in odd channels, which carry another
+      // 1/16, down to 2^-20 (elements below lose bits that are 2^-34 of the row's largest, 2^-30 in odd
+      // channels), and the sums of 32 stay finite
       int e = 0;
       if (mx > 0.f) frexpf(mx, &e);
-      e = max(-100, min(100, 10 - e));
+      e = max(-126, min(126, 10 - e));
       const float up = a.scale_log2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e), upl = up * 0.0625f;
       float gs[G];
 #pragma unroll
       for (int k = 0; k < G; ++k) {
         float t = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t += f[k][j];
+        for (int j = 0; j < 8; ++j) t = fmaf(f[k][j], up, t);
         t += __shfl_xor_sync(0xffffffffu, t, 1);
         t += __shfl_xor_sync(0xffffffffu, t, 2);
-        gs[k] = t * up;
+        gs[k] = t;
         // A operands: rows gid, gid + 8 in registers 0 and 1, the upper half of k in 2 and 3
         constexpr int U = WIDE ? 2 : 1;
         qf[k][0][rj] = h2_as_u32(__floats2half2_rn(f[k][0] * up, f[k][4] * up));
@@ -448,8 +449,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) paged_attention_kernel(PaArgs a
       const __half2 h2 = __floats2half2_rn(u, v);
       const float2 hf = __half22float2(h2);
       qo[rj] = piece == 0 ? h2_as_u32(h2) : piece == 1 ? h2_as_u32(__floats2half2_rn(u - hf.x, v - hf.y)) : 0u;
-      // never 0, so that -inf stays -inf; the scale's sign is in q
-      const float mine = fmaxf(ldexpf(fabsf(a.scale_log2), -e), 1.17549435e-38f);
+      // never 0 or infinite, so that -inf stays -inf and 0 stays 0; the scale's sign is in q
+      const float mine = fminf(fmaxf(ldexpf(fabsf(a.scale_log2), -e), 1.17549435e-38f), 3.402823466e38f);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (WIDE && j != rj) continue;
