@@ -24,6 +24,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "kvq.h"
 #include "kvq_common.cuh"
 
@@ -124,6 +126,20 @@ __device__ __forceinline__ float2 rope_cos_sin(int pos, uint64_t step, float mag
   const float c = (quarter & 1u) ? sn : cn, s = (quarter & 1u) ? cn : sn;
   return make_float2(__uint_as_float(__float_as_uint(c * magnitude) ^ ((quarter + 1u) >> 1 << 31)),
                      __uint_as_float(__float_as_uint(s * magnitude) ^ (quarter >> 1 << 31)));
+}
+
+// Whether rows of n elements at t ts + h hs, t < T and h < H, share an element (strides >= 0).
+inline bool rows_overlap(int64_t T, int64_t H, int64_t ts, int64_t hs, int64_t n) {
+  if ((T > 1 && ts < n) || (H > 1 && hs < n)) return true;
+  if (T <= 1 || H <= 1) return false;
+  if ((ts - n) / (H - 1) >= hs || (hs - n) / (T - 1) >= ts) return false;   // a token's heads lie within its stride, or a head's tokens
+  if (H > T) std::swap(T, H), std::swap(ts, hs);
+  for (int64_t dh = 1; dh < H; ++dh) {   // rows (t, h + dh) and (t + dt, h): the tokens next to dh heads' distance
+    const __int128 x = (__int128)dh * hs, dt = x / ts;
+    if (dt < T && x - dt * ts < n) return true;
+    if (dt + 1 < T && (dt + 1) * ts - x < n) return true;
+  }
+  return false;
 }
 
 // ---- checks shared by the calls of this file's users (kvq_rope.cu) ----

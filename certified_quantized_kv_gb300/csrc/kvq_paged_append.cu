@@ -420,6 +420,14 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   if (T == 0) return KVQ_OK;
   if (kvq_status s = check_strides(kt, kh, fn, "k")) return s;
   if (kvq_status s = check_strides(vt, vh, fn, "v")) return s;
+  if (q) {
+    if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
+    if (kvq_status s = check_strides(ot, oh, fn, "q_out")) return s;
+    if (q == q_out && ((T > 1 && qt != ot) || (Hq > 1 && qh != oh)))
+      return paged_fail(KVQ_ERR_INVALID, fn, "q_out = q needs the same strides");
+    if (rows_overlap(T, Hq, ot, oh, hd)) return paged_fail(KVQ_ERR_INVALID, fn, "q_out: rows must not overlap");
+    if (q_out == k || q_out == v) return paged_fail(KVQ_ERR_INVALID, fn, "q_out must not be k or v");
+  }
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");
   if (kvq_status s = check_buffer(k, dev, 16, fn, "k")) return s;
@@ -429,11 +437,6 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   if (plan)
     if (kvq_status s = check_buffer(positions, dev, 4, fn, "positions")) return s;
   if (q) {
-    if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
-    if (kvq_status s = check_strides(ot, oh, fn, "q_out")) return s;
-    if ((T > 1 && ot < hd) || (Hq > 1 && oh < hd)) return paged_fail(KVQ_ERR_INVALID, fn, "q_out: rows must not overlap");
-    if (q == q_out && ((T > 1 && qt != ot) || (Hq > 1 && qh != oh)))
-      return paged_fail(KVQ_ERR_INVALID, fn, "q_out = q needs the same strides");
     if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
     if (kvq_status s = check_buffer(q_out, dev, 16, fn, "q_out")) return s;
   }
@@ -478,7 +481,7 @@ kvq_status gather_impl(const void* pages, int n_pages, const int32_t* slots, int
   if (T == 0) return KVQ_OK;
   if (kvq_status s = check_strides(kt, kh, fn, "k")) return s;
   if (kvq_status s = check_strides(vt, vh, fn, "v")) return s;
-  if ((T > 1 && std::min(kt, vt) < hd) || (Hkv > 1 && std::min(kh, vh) < hd))
+  if (k == v || rows_overlap(T, Hkv, kt, kh, hd) || rows_overlap(T, Hkv, vt, vh, hd))
     return paged_fail(KVQ_ERR_INVALID, fn, "k and v: rows must not overlap");
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");

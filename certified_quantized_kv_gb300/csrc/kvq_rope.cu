@@ -103,10 +103,9 @@ kvq_status rope_impl(const kvq_rope_plan* plan, int dtype, const void* x, int64_
   if (T == 0 || H == 0) return KVQ_OK;
   if (kvq_status s = check_strides(xt, xh, fn, "x")) return s;
   if (kvq_status s = check_strides(ot, oh, fn, "out")) return s;
-  if ((T > 1 && ot < plan->head_dim) || (H > 1 && oh < plan->head_dim))
-    return paged_fail(KVQ_ERR_INVALID, fn, "out: rows must not overlap");
   if (x == out && ((T > 1 && xt != ot) || (H > 1 && xh != oh)))
     return paged_fail(KVQ_ERR_INVALID, fn, "out = x needs the same strides");
+  if (rows_overlap(T, H, ot, oh, plan->head_dim)) return paged_fail(KVQ_ERR_INVALID, fn, "out: rows must not overlap");
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");
   if (kvq_status s = check_buffer(x, dev, 16, fn, "x")) return s;

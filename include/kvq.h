@@ -320,8 +320,9 @@ kvq_status kvq_dense_decode_noalloc(const void* q, const void* k, const void* v,
  *
  * Element types of q, k, v and outputs: kvq_dtype.  Strided operands [tokens, heads, D]
  * are given by a base pointer (16-byte aligned) and the strides of tokens and heads in
- * elements (multiples of 8); the D elements of a row are contiguous.  Every buffer is
- * device memory of the current device.  All calls are stream-ordered, allocate nothing
+ * elements (multiples of 8); the D elements of a row are contiguous.  Rows of an input may
+ * overlap (a stride of 0 repeats one), those of an output are refused when they do.  Every
+ * buffer is device memory of the current device.  All calls are stream-ordered, allocate nothing
  * and may be captured into a CUDA graph.
  * ---------------------------------------------------------------------------------- */
 typedef enum kvq_dtype { KVQ_F16 = 0, KVQ_BF16 = 1 } kvq_dtype;

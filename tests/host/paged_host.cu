@@ -45,6 +45,31 @@ void rows() {
   EXPECT(plans > 2000, "only %d plans", plans);
 }
 
+// Rows of an output share an element: against marking every element.
+void overlap() {
+  int yes = 0, no = 0;
+  for (int T = 1; T <= 6; ++T)
+    for (int H = 1; H <= 6; ++H)
+      for (int ts = 0; ts <= 40; ++ts)
+        for (int hs = 0; hs <= 40; ++hs) {
+          const int n = 4;
+          bool used[6 * 40 * 2 + 8] = {}, meet = false;
+          for (int t = 0; t < T; ++t)
+            for (int h = 0; h < H; ++h)
+              for (int c = 0; c < n; ++c) {
+                bool& u = used[t * ts + h * hs + c];
+                meet |= u, u = true;
+              }
+          ++(meet ? yes : no);
+          EXPECT(kvq::rows_overlap(T, H, ts, hs, n) == meet, "%d x %d rows, strides %d and %d: %d", T, H, ts, hs, meet);
+        }
+  EXPECT(yes > 1000 && no > 1000, "%d and %d layouts", yes, no);
+  const int64_t far = INT64_MAX - 7;
+  EXPECT(!kvq::rows_overlap(INT32_MAX, INT32_MAX, far, 128, 128), "far tokens");
+  EXPECT(!kvq::rows_overlap(2, 2, far, far - 128, 128), "far tokens and heads");
+  EXPECT(kvq::rows_overlap(3, 3, far, far, 128), "the same strides");
+}
+
 // A warp that fills a ring ahead of its work, with a copy that does not arrive in time: behind the drain
 // nothing is in flight any more, whatever the number of pages and the copy.
 template <int STAGES>
@@ -85,6 +110,7 @@ void ring() {
 int main(int argc, char** argv) {
   const char* what = argc > 1 ? argv[1] : "";
   if (!std::strcmp(what, "rows")) rows();
+  else if (!std::strcmp(what, "overlap")) overlap();
   else if (!std::strcmp(what, "ring")) ring<1>(), ring<2>(), ring<3>(), ring<4>();
   else EXPECT(false, "no check named '%s'", what);
   if (!wrong) std::puts("ok");

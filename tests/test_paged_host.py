@@ -36,3 +36,7 @@ def test_rows_exchange_within_the_room_of_their_warp(program):
 def test_a_late_copy_is_waited_for(program):
     """The paged attention's ring after a wait that ran out: the copies in flight are the ones waited for."""
     _run(program, "ring")
+
+
+def test_overlap_of_rows(program):
+    _run(program, "overlap")
