@@ -964,7 +964,8 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
     return paged_fail(KVQ_ERR_INVALID, fn, "max_pages must be in 1..16777216 and batch * max_pages below 2^30");
   if (table_stride < 0) return paged_fail(KVQ_ERR_INVALID, fn, "table_stride must be >= 0");
   if (window < 0) return paged_fail(KVQ_ERR_INVALID, fn, "window must be >= 0");
-  if (!std::isfinite(scale)) return paged_fail(KVQ_ERR_INVALID, fn, "scale must be finite");
+  const float scale_log2 = (scale != 0.f ? scale : 1.f / std::sqrt((float)hd)) * LOG2E_F;
+  if (!std::isfinite(scale_log2)) return paged_fail(KVQ_ERR_INVALID, fn, "scale * log2(e) must be finite");
   if (B == 0) return KVQ_OK;
   if (q == out) return paged_fail(KVQ_ERR_INVALID, fn, "out must not be q");
   if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
@@ -986,7 +987,7 @@ kvq_status attention_impl(int dtype, const void* q, int64_t qt, int64_t qh, cons
   a.qt = qt, a.qh = qh, a.table_stride = table_stride, a.n_pages = n_pages, a.max_pages = max_pages;
   a.B = B, a.Q = Q, a.Hq = Hq, a.Hkv = Hkv, a.n_rep = Hq / Hkv, a.rows = Q * a.n_rep;
   a.window = std::min(window, 1 << 30);   // lengths stay below 2^30
-  a.scale_log2 = (scale != 0.f ? scale : 1.f / std::sqrt((float)hd)) * LOG2E_F;
+  a.scale_log2 = scale_log2;
   a.bf16 = dtype == KVQ_BF16;
   const int R = tile_rows(a.rows, (long long)B * max_pages * Hkv, sms);
   a.RT = (a.rows + R - 1) / R;

@@ -433,7 +433,7 @@ kvq_status kvq_paged_attention_workspace(int batch, int n_q_tokens, int n_q_head
  *               sequence.
  *   window      0: query i of a sequence of n tokens sees tokens 0..n - n_q_tokens + i;
  *               w > 0: only the last w of them
- *   scale       0: 1 / sqrt(head_dim)
+ *   scale       0: 1 / sqrt(head_dim); else any number whose product with log2(e) is finite
  *   out         [batch, n_q_tokens, Hq, head_dim], contiguous, of q's type; must not overlap q
  *   lse         optional (NULL): [batch, n_q_tokens, Hq] float, natural log of the sum of
  *               exp(scale q k), for merging with attention over other keys

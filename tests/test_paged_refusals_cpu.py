@@ -3,7 +3,7 @@
 import pytest
 
 import certified_quantized_kv_gb300 as kvq
-from test_paged_cpu import ADDR, _append, _rope
+from test_paged_cpu import ADDR, _append, _attend, _rope
 
 FAR = ADDR + (1 << 16)
 
@@ -35,3 +35,8 @@ def test_the_same_buffer_for_two_outputs_or_for_an_output_and_another_input():
     for other in ("k", "v"):
         assert _append(**{other: FAR}, q=2 * FAR, q_out=FAR, qt=256, qh=128, ot=256, oh=128, Hq=2) == kvq.KVQ_ERR_INVALID
         assert b"q_out must not be k or v" in _error()
+
+
+@pytest.mark.parametrize("scale", [2.9e38, -3.4e38])
+def test_scales_whose_base_2_form_fp32_does_not_hold(scale):
+    assert _attend(scale=scale, out=FAR) == kvq.KVQ_ERR_INVALID and b"scale" in _error()
