@@ -6,6 +6,7 @@
 // accuracy, which an fp32 product of position and frequency would.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <string>
 
 #include "kvq.h"
@@ -148,7 +149,7 @@ kvq_status plan_impl(const kvq_rope_config* c, kvq_rope_plan* p) {
   if (scaled && (!(c->factor >= 1.0) || !std::isfinite(c->factor))) return bad("factor must be finite and >= 1");
   if (blend && c->original_ctx < 1) return bad("original_ctx must be >= 1");
   if (blend && !(c->low > 0.0 && c->low < c->high && std::isfinite(c->high))) return bad("0 < low < high is needed");
-  if (!(c->magnitude >= 0.0) || !std::isfinite(c->magnitude)) return bad("magnitude must be finite and >= 0");
+  if (!(c->magnitude >= 0.0 && c->magnitude <= std::numeric_limits<float>::max())) return bad("magnitude must be finite in fp32 and >= 0");
   const int rd = c->rotary_dim;
   double base = c->base;
   if (c->scaling == KVQ_ROPE_NTK) {

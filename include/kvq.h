@@ -351,7 +351,7 @@ typedef struct kvq_rope_config {
   double factor;     /* >= 1; used by every scaling but NONE */
   int original_ctx;  /* n >= 1; used by PARTS and YARN */
   double low, high;  /* 0 < low < high, turns; used by PARTS and YARN */
-  double magnitude;  /* factor on cos and sin; 0: 1, and 0.1 ln(f) + 1 with YARN */
+  double magnitude;  /* factor on cos and sin, finite in fp32; 0: 1, and 0.1 ln(f) + 1 with YARN */
 } kvq_rope_config;
 
 /* What the kernels take: plain data, initialised on the host by kvq_rope_plan_init and

@@ -3,7 +3,7 @@
 import pytest
 
 import certified_quantized_kv_gb300 as kvq
-from test_paged_cpu import ADDR, _append, _attend, _rope
+from test_paged_cpu import ADDR, _append, _attend, _plan, _rope
 
 FAR = ADDR + (1 << 16)
 
@@ -40,3 +40,9 @@ def test_the_same_buffer_for_two_outputs_or_for_an_output_and_another_input():
 @pytest.mark.parametrize("scale", [2.9e38, -3.4e38])
 def test_scales_whose_base_2_form_fp32_does_not_hold(scale):
     assert _attend(scale=scale, out=FAR) == kvq.KVQ_ERR_INVALID and b"scale" in _error()
+
+
+@pytest.mark.parametrize("magnitude", [3.5e38, 1e300])
+def test_magnitudes_that_fp32_does_not_hold(magnitude):
+    assert _plan(magnitude=magnitude)[0] == kvq.KVQ_ERR_INVALID and b"magnitude" in _error()
+    assert _plan(magnitude=3.4e38)[0] == kvq.KVQ_OK
