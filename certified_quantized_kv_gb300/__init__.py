@@ -576,9 +576,9 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
     q: [B, Hq, head_dim] or [B, n_q_tokens, Hq, head_dim] fp16 or bf16, the last tokens of each
     sequence; page_table: int32 [B, max_pages]; seq_lens: int32 [B], those tokens included (0:
     a padding sequence, whose out is 0); out: like q, contiguous; lse: float32 like q without
-    its last dimension, or None.  `workspace` is a device uint8 tensor of at least
-    paged_attention_workspace(...) bytes, zeroed once before its first use (allocated here
-    when omitted).  Returns `workspace` so a caller can reuse it."""
+    its last dimension, or None; scale: None (or 0) for 1 / sqrt(head_dim).  `workspace` is a
+    device uint8 tensor of at least paged_attention_workspace(...) bytes, zeroed once before its
+    first use (allocated here when omitted).  Returns `workspace` so a caller can reuse it."""
     shape = q.shape
     if len(shape) not in (3, 4):
         raise ValueError("q must be [batch, n_q_heads, head_dim] or [batch, n_q_tokens, n_q_heads, head_dim]")

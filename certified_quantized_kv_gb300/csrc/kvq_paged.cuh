@@ -90,10 +90,6 @@ __device__ __forceinline__ float elem_to_f(const void* p, size_t i, bool bf16) {
   const unsigned short u = static_cast<const unsigned short*>(p)[i];
   return bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
 }
-__device__ __forceinline__ void f_to_elem(void* p, size_t i, float x, bool bf16) {
-  static_cast<unsigned short*>(p)[i] =
-      bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
-}
 
 // ---- rotary phases ----
 // The angle of position p and pair i is p * step_i in units of 2^-64 turn, an exact

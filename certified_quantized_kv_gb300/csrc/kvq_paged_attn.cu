@@ -23,7 +23,8 @@
 //  - The softmax reference of a row moves only when a weight would pass 2^top, and is then set so
 //    that the largest is 2^(top - 4): most pages rescale nothing.  top is 14 unless a value
 //    scale of 2 or more appears (then smaller, so that p s stays finite in binary16): small
-//    weights of long caches stay normal numbers.
+//    weights of long caches stay normal numbers.  Weights below 2^-25 count as 0: 2^-35 of the row's
+//    largest one or less, 2^-(35 - j) where value scales reach 2^j (values that span 15 2^j).
 //  - The (sequence, KV head, row tile, page) units are numbered in that order and cut into
 //    equal contiguous ranges, one per warp, whatever the lengths; every warp works alone on
 //    whole pages, fed by bulk copies into its own shared-memory ring.  A group (sequence, KV

@@ -259,7 +259,7 @@ __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t
 // four pairs at least, of which the last may lie partly behind the rotated elements.  0: rope_rows.
 inline int rope_pairs(const kvq_rope_plan& plan) {
   const int half = plan.rotary_dim / 2;
-    return half % 8 == 0 ? 8 : half % 4 == 0 || plan.interleaved ? 4 : 0;
+  return half % 8 == 0 ? 8 : half % 4 == 0 || plan.interleaved ? 4 : 0;
 }
 
 // Pieces of a row: chunks of V pairs, and the vectors that are only copied.
@@ -271,8 +271,9 @@ inline int rope_units(const kvq_rope_plan& plan, int V, bool copy) {
 // per token and share of the heads, have room on the GPU at once.  A second wave of blocks costs as
 // much as more heads in one (1024 tokens of 32 heads of 128: 3.8 us with three heads per thread, 4.7 with
 // two, 6.7 with one; 2048 tokens: 5.3 with five, 5.9 with three; the append of 4096 with 8 KV heads: 15.3
-// us with 16 query heads per thread, 18.2 with eight).  Else eight: enough to share the angles, which
-// cost as much as the rotation of two heads (32768 tokens: 122 us, 126 with 16).
+// us with 16 query heads per thread, 18.2 with eight, both with phases of lower accuracy; 16.4 as it
+// is).  Else eight: enough to share the angles, which cost as much as the rotation of two heads
+// (32768 tokens: 122 us, 126 with 16).
 inline int heads_each(long long T, int H, int each, long long room) {
   for (int per = 1; per <= 16; ++per)
     if (T * ((H + per - 1) / per) * each <= room) return per;

@@ -373,9 +373,10 @@ kvq_status kvq_rope_plan_init(const kvq_rope_config* cfg, kvq_rope_plan* plan);
  *   positions  [n_tokens] int32, device; any value.  A negative position turns back: with
  *              -p the call is the transpose of the call with p (its gradient), and undoes
  *              it where the magnitude is 1.
- * head_dim must be a multiple of 8.  Angles are exact to 2^-33 turn plus the rounding of
- * the frequencies to double, for positions of any size.  Arithmetic in fp32, one rounding
- * to the element type.  n_tokens or n_heads = 0 is a no-op.
+ * head_dim must be a multiple of 8.  Angles are right to 2^-33 turn, for positions of any
+ * size, beside what the position makes of the frequency's own error (2^-63 turn, and its
+ * rounding to double).  Arithmetic in fp32, one rounding to the element type.  n_tokens or
+ * n_heads = 0 is a no-op.
  * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
 kvq_status kvq_rope(const kvq_rope_plan* plan, int dtype, const void* x, int64_t x_token_stride,
                     int64_t x_head_stride, const int32_t* positions, int n_tokens, int n_heads, void* out,
@@ -446,9 +447,11 @@ kvq_status kvq_paged_attention_workspace(int batch, int n_q_tokens, int n_q_head
  *               call leaves them zero (they count the arrivals of a row's pieces), whatever
  *               its shape.  Calls that share it must not overlap on the GPU.
  * One kernel.  Hq / Hkv an integer in 1..64, Hkv <= 4096, n_q_tokens 1..64, batch <= 2048,
- * head_dim 64 or 128, batch * max_pages < 2^30.  Scores and sums in fp32.  batch = 0 is a no-op.  Every
- * device-side wait is bounded (2 s); one that runs out, which does not happen in correct
- * operation, makes the affected outputs NaN.
+ * head_dim 64 or 128, batch * max_pages < 2^30.  Scores and sums in fp32; weights below
+ * 2^-35 of a row's largest count as 0 (2^-(35 - j) where value scales reach 2^j).  batch = 0
+ * is a no-op.  Every device-side wait is bounded (2 s); one that runs out, which does not
+ * happen in correct operation, makes the affected outputs NaN.  Host threads may call at once,
+ * each with its own workspace.
  * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
 kvq_status kvq_paged_attention(int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                const void* pages, int n_pages, const int32_t* page_table, int64_t table_stride,
