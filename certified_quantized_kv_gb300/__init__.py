@@ -70,6 +70,10 @@ class kvq_rope_plan(ctypes.Structure):
                 ("magnitude", ctypes.c_float), ("step", ctypes.c_uint64 * 128)]
 
 
+class kvq_rope_axes_plan(ctypes.Structure):
+    _fields_ = [("plan", kvq_rope_plan), ("n_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128)]
+
+
 CERT_DTYPE = np.dtype([("e_key", "<f4"), ("e_val", "<f4"), ("rank_ok", "<i4"), ("level", "<i4"),
                        ("k_star", "<i4"), ("n_val_promoted", "<i4"), ("promoted_bytes", "<i8")])
 assert CERT_DTYPE.itemsize == 32
@@ -105,6 +109,11 @@ def load_library() -> ctypes.CDLL:
                                 ctypes.POINTER(i32), i32],
         "kvq_rope_plan_init": [ctypes.POINTER(kvq_rope_config), ctypes.POINTER(kvq_rope_plan)],
         "kvq_rope": [vp, i32, vp, i64, i64, vp, i32, i32, vp, i64, i64, vp],
+        "kvq_rope_axes_plan_init": [ctypes.POINTER(kvq_rope_config), i32, ctypes.POINTER(ctypes.c_int32), i32, i32,
+                                    ctypes.POINTER(kvq_rope_axes_plan)],
+        "kvq_rope_axes": [vp, i32, vp, i64, i64, vp, i64, i32, i32, vp, i64, i64, vp],
+        "kvq_paged_append_axes": [vp, i32, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, i32, i32, vp, i32,
+                                  vp, i64, i64, i32, vp, i64, i64, vp],
         "kvq_paged_page_bytes": [i32, ctypes.POINTER(ctypes.c_size_t)],
         "kvq_paged_append": [vp, i32, vp, i64, i64, vp, i64, i64, vp, vp, i32, i32, i32, vp, i32,
                              vp, i64, i64, i32, vp, i64, i64, vp],
@@ -368,6 +377,9 @@ PAGE = 64   # tokens per page
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
 
 
+AXIS_ORDERS = {"blocks": 0, "cycled": 1}
+
+
 class RopePlan:
     """Rotary frequencies of a model, for `rope` and `paged_append` (kvq_rope_plan_init).
 
@@ -375,29 +387,54 @@ class RopePlan:
     scaling: "none", "linear", "ntk", "parts" (frequencies blended by their turns within
     original_ctx, between low and high) or "yarn" (blended over the pair index, cos and sin
     times 0.1 ln(factor) + 1 unless `magnitude` is given); see include/kvq.h.
+
+    axes: pairs of each of 1 to 4 axes, e.g. (16, 24, 24) for time, height and width, rotary_dim / 2 in
+    all (kvq_rope_axes_plan_init).  Positions are then int32 [len(axes), T], and each pair is turned
+    by its own axis' one.  axis_order: "blocks" (the first axis' pairs first) or "cycled" (dealt to the
+    axes in turn while they have pairs left); axis_frequencies: "shared" (pair i's frequency is that of
+    one axis) or "own" (each axis' pairs have the frequencies of a plan of their own).
     """
 
+    n_axes = 0   # positions [T]; else [n_axes, T]
+
     def __init__(self, head_dim, rotary_dim=None, layout="half", base=10000.0, scaling="none", factor=1.0,
-                 original_ctx=0, low=1.0, high=32.0, magnitude=0.0):
+                 original_ctx=0, low=1.0, high=32.0, magnitude=0.0, axes=None, axis_order="blocks",
+                 axis_frequencies="shared"):
         if layout not in ("half", "interleaved"):
             raise ValueError('layout must be "half" or "interleaved"')
         if scaling not in ROPE_SCALINGS:
             raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        if axis_order not in AXIS_ORDERS:
+            raise ValueError(f"axis_order must be one of {sorted(AXIS_ORDERS)}")
+        if axis_frequencies not in ("shared", "own"):
+            raise ValueError('axis_frequencies must be "shared" or "own"')
         cfg = kvq_rope_config(head_dim, head_dim if rotary_dim is None else rotary_dim, int(layout == "interleaved"),
                               ROPE_SCALINGS[scaling], base, factor, original_ctx, low, high, magnitude)
-        self.plan = kvq_rope_plan()
-        _check(load_library().kvq_rope_plan_init(ctypes.byref(cfg), ctypes.byref(self.plan)))
-        self.address = ctypes.addressof(self.plan)
+        if axes is None:
+            whole = kvq_rope_plan()
+            _check(load_library().kvq_rope_plan_init(ctypes.byref(cfg), ctypes.byref(whole)))
+        else:
+            whole, pairs = kvq_rope_axes_plan(), (ctypes.c_int32 * len(axes))(*axes)
+            _check(load_library().kvq_rope_axes_plan_init(ctypes.byref(cfg), len(axes), pairs, AXIS_ORDERS[axis_order],
+                                                          int(axis_frequencies == "own"), ctypes.byref(whole)))
+            self.n_axes = len(axes)
+        self._hold(whole)
         self.head_dim = head_dim
+
+    def _hold(self, whole):
+        self.whole = whole
+        self.plan = whole.plan if self.n_axes else whole
+        self.address = ctypes.addressof(whole)
 
     # copies and pickled plans hold a struct of their own, at their own address
     def __getstate__(self):
-        return {**self.__dict__, "plan": bytes(self.plan), "address": None}
+        state = {**self.__dict__, "plan": bytes(self.whole), "address": None}
+        del state["whole"]
+        return state
 
     def __setstate__(self, state):
         self.__dict__.update(state)
-        self.plan = kvq_rope_plan.from_buffer_copy(state["plan"])
-        self.address = ctypes.addressof(self.plan)
+        self._hold((kvq_rope_axes_plan if self.n_axes else kvq_rope_plan).from_buffer_copy(state["plan"]))
 
 
 # The calls below are made once per layer and token, where their host time counts (a decoding
@@ -440,6 +477,15 @@ def _ints(t, name, n, dev):
     return t.data_ptr()
 
 
+def _positions(t, plan, n, dev):
+    """Address of a plan's positions, and with several axes (as a tuple's second element) their stride."""
+    if not plan.n_axes:
+        return (_ints(t, "positions", n, dev),)
+    if t.dtype is not _I32 or t.shape != (plan.n_axes, n) or t.get_device() != dev or (n > 1 and t.stride(1) != 1):
+        raise ValueError(f"positions must be a torch.int32 tensor [{plan.n_axes}, {n}] with contiguous rows on CUDA device {dev}")
+    return t.data_ptr(), t.stride(0)
+
+
 def _float_code(t, name) -> int:
     dt = t.dtype
     if dt is _F16:
@@ -474,7 +520,8 @@ def _call(dev, stream, fn, *args):
 
 def rope(x, positions, plan, out=None, stream=None):
     """Rotary positions (kvq_rope): x [T, H, head_dim] fp16 or bf16 with contiguous rows (any
-    token and head strides, e.g. a slice of a fused projection), positions [T] int32.
+    token and head strides, e.g. a slice of a fused projection), positions [T] int32 ([n_axes, T] with a
+    plan of several axes: kvq_rope_axes).
     out=None allocates the result; out=x works in place.  Returns out."""
     shape = x.shape
     if len(shape) != 3:
@@ -490,7 +537,9 @@ def rope(x, positions, plan, out=None, stream=None):
         raise ValueError(f"x must have head_dim {plan.head_dim}, got {hd}")
     a = _rows(x, "x", dt, shape)
     b = a if out is x else _rows(out, "out", dt, shape)
-    _call(dev, stream, load_library().kvq_rope, plan.address, code, *a, _ints(positions, "positions", T, dev), T, H, *b)
+    lib = load_library()
+    _call(dev, stream, lib.kvq_rope_axes if plan.n_axes else lib.kvq_rope, plan.address, code, *a,
+          *_positions(positions, plan, T, dev), T, H, *b)
     return out
 
 
@@ -522,8 +571,8 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
 
     k, v: [T, n_kv_heads, head_dim] fp16 or bf16 with contiguous rows; slots: int32 [T] (page *
     64 + offset; outside the pool, e.g. -1: skipped; all distinct).  With a RopePlan and
-    positions (int32 [T]) keys are rotated on the way, and q [T, n_q_heads, head_dim], when
-    given, into q_out (which may be q)."""
+    positions (int32 [T], or [n_axes, T] with a plan of several axes: kvq_paged_append_axes) keys are
+    rotated on the way, and q [T, n_q_heads, head_dim], when given, into q_out (which may be q)."""
     shape = k.shape
     if len(shape) != 3:
         raise ValueError("k must be [n_tokens, n_kv_heads, head_dim]")
@@ -542,9 +591,11 @@ def paged_append(pages, k, v, slots, positions=None, plan=None, q=None, q_out=No
         hq = qs[1]
         qa = _rows(q, "q", dt, (T, hq, hd))
         oa = qa if q_out is q else _rows(q_out, "q_out", dt, (T, hq, hd))
-    _call(dev, stream, load_library().kvq_paged_append, None if plan is None else plan.address, code,
+    lib = load_library()
+    _call(dev, stream, lib.kvq_paged_append_axes if plan is not None and plan.n_axes else lib.kvq_paged_append,
+          None if plan is None else plan.address, code,
           *_rows(k, "k", dt, shape), *_rows(v, "v", dt, shape), _ints(slots, "slots", T, dev),
-          None if positions is None else _ints(positions, "positions", T, dev), T, hkv, hd, *_pool(pages, hkv, hd),
+          *((None,) if plan is None else _positions(positions, plan, T, dev)), T, hkv, hd, *_pool(pages, hkv, hd),
           *qa, hq, *oa)
 
 

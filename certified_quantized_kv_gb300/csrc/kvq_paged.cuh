@@ -147,5 +147,6 @@ kvq_status check_buffer(const void* p, int dev, size_t align, const char* fn, co
 // rows of a strided [tokens, heads, head_dim] operand: non-negative strides, multiples of 8
 kvq_status check_strides(int64_t token, int64_t head, const char* fn, const char* name);
 kvq_status check_plan(const kvq_rope_plan* plan, int head_dim, const char* fn);
+kvq_status check_axes(const kvq_rope_axes_plan& plan, int64_t axis_stride, const char* fn);
 
 }  // namespace kvq

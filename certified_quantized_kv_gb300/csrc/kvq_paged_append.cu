@@ -48,16 +48,16 @@ struct Octet {
 // pair is in the same lane (INTERLEAVED), or a whole number of lanes away (LANES), or, when half of
 // rotary_dim is no multiple of 8, anywhere (ELEMENTS: through shared memory).
 enum class Turn { NONE, INTERLEAVED, LANES, ELEMENTS };
-template <int HD, Turn TURN, bool BF16>
+template <int HD, Turn TURN, bool BF16, bool AXES>
 struct Rotation {
   float c[E], s[E];  // y = x c + other s (s carries the sign; elements not rotated: 1, 0)
   int half, ch, from;   // this lane's first channel, the lane with the others (LANES)
   __device__ __forceinline__ bool in(int e) const { return ch + e < 2 * half; }
-  __device__ __forceinline__ void set(const kvq_rope_plan& P, const uint64_t* steps, int at, int lane) {
+  __device__ __forceinline__ void set(const kvq_rope_plan& P, const uint64_t* steps, const Place<AXES>& at, int lane) {
     if (TURN == Turn::NONE) return;
     half = P.rotary_dim / 2;
     ch = E * (lane % (HD / E));
-    auto turn = [&](int i) { return rope_cos_sin(at, steps[i], P.magnitude); };
+    auto turn = [&](int i) { return at.turn(steps[i], P.magnitude); };
     if (TURN == Turn::INTERLEAVED) {
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
@@ -220,7 +220,7 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], float2 ext, bo
 // 6.8); 158 with the read-back behind it (registers for 8 blocks per SM gave 160 where these gave 159,
 // for 6 162).
 constexpr int APPEND_THREADS = 128;
-template <int HD, Turn TURN, int V, bool BF16>
+template <int HD, Turn TURN, int V, bool BF16, bool AXES>
 __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const __grid_constant__ kvq_rope_plan P, AppendPagedArgs a) {
   using L = Page<HD>;
   constexpr int LANES = HD / E, TOKENS = 32 / LANES;   // lanes of a row, tokens of an item
@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
       if constexpr (V == 0) {
         __shared__ float2 turns[WARPS][128];
         const int warp = threadIdx.x >> 5;
-        rope_rows<BF16>(P, steps, rooms + 32 * warp, turns[warp], a.q, mine * WARPS + warp, all * WARPS);
+        rope_rows<BF16, AXES>(P, steps, rooms + 32 * warp, turns[warp], a.q, mine * WARPS + warp, all * WARPS);
       } else {
-        rope_part<V, TURN == Turn::INTERLEAVED, BF16, APPEND_THREADS, false>(P, steps, nullptr, a.q, mine * APPEND_THREADS,
+        rope_part<V, TURN == Turn::INTERLEAVED, BF16, APPEND_THREADS, false, AXES>(P, steps, nullptr, a.q, mine * APPEND_THREADS,
                                                                              all * APPEND_THREADS);
       }
       return;
@@ -257,7 +257,10 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
     const unsigned short* kp = static_cast<const unsigned short*>(a.k) + t * a.kt + h0 * a.kh + E * sub;
     const unsigned short* vp = static_cast<const unsigned short*>(a.v) + t * a.vt + h0 * a.vh + E * sub;
     // the token's slot and position and its first rows in one go, whether it turns out to be skipped or not
-    const int slot = in ? a.slots[t] : -1, pos = TURN != Turn::NONE && in ? a.pos[t] : 0;
+    const int slot = in ? a.slots[t] : -1;
+    Place<AXES> pos;
+    if (TURN != Turn::NONE && in) pos.load(a.pos, a.q.ps, a.q.n_axes, t);
+    else pos.none();
     Octet next_k = {}, next_v = {};
     if (in) next_k.load(kp), next_v.load(vp);
     const bool live = slot >= 0 && slot / PG < a.n_pages;
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
     unsigned char* vc = pg + L::VC + vcode_at<HD>(at, 2 * j * 2 * L::G + 2 * g);   // and 2G bytes on
     __half* ks = reinterpret_cast<__half*>(pg + L::KS) + at * L::G + g;
     __half* vs = reinterpret_cast<__half*>(pg + L::VS) + g * PG + vscale_at(at);
-    Rotation<HD, TURN, BF16> rot;
+    Rotation<HD, TURN, BF16, AXES> rot;
     for (int h = h0; h < h1; ++h) {
       const Octet rk = next_k, rv = next_v;
       kp += a.kh, vp += a.vh;
@@ -309,16 +312,20 @@ __global__ void __launch_bounds__(APPEND_THREADS, 7) paged_append_kernel(const _
   }
 }
 
+using AppendKernel = void (*)(kvq_rope_plan, AppendPagedArgs);
+template <int HD, bool BF16, bool AXES>
+AppendKernel append_kernel_of(const kvq_rope_plan& plan) {
+  const int V = rope_pairs(plan);   // per thread that turns q (0: rope_rows)
+  if (plan.interleaved)
+    return V == 8 ? paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16, AXES> : paged_append_kernel<HD, Turn::INTERLEAVED, 4, BF16, AXES>;
+  return V == 8   ? paged_append_kernel<HD, Turn::LANES, 8, BF16, AXES>
+         : V == 4 ? paged_append_kernel<HD, Turn::ELEMENTS, 4, BF16, AXES>
+                  : paged_append_kernel<HD, Turn::ELEMENTS, 0, BF16, AXES>;
+}
 template <int HD, bool BF16>
-auto append_kernel_of(const kvq_rope_plan* plan) {
-  using K = void (*)(kvq_rope_plan, AppendPagedArgs);
-  if (!plan) return (K)paged_append_kernel<HD, Turn::NONE, 0, BF16>;
-  const int V = rope_pairs(*plan);   // per thread that turns q (0: rope_rows)
-  if (plan->interleaved)
-    return V == 8 ? (K)paged_append_kernel<HD, Turn::INTERLEAVED, 8, BF16> : (K)paged_append_kernel<HD, Turn::INTERLEAVED, 4, BF16>;
-  return V == 8   ? (K)paged_append_kernel<HD, Turn::LANES, 8, BF16>
-         : V == 4 ? (K)paged_append_kernel<HD, Turn::ELEMENTS, 4, BF16>
-                  : (K)paged_append_kernel<HD, Turn::ELEMENTS, 0, BF16>;
+AppendKernel append_kernel_of(const kvq_rope_plan* plan, bool axes) {
+  if (!plan) return paged_append_kernel<HD, Turn::NONE, 0, BF16, false>;
+  return axes ? append_kernel_of<HD, BF16, true>(*plan) : append_kernel_of<HD, BF16, false>(*plan);
 }
 
 struct GatherArgs {
@@ -403,14 +410,16 @@ kvq_status check_common(const char* fn, int dtype, int T, int Hkv, int hd, int n
   return KVQ_OK;
 }
 
-kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int64_t kt, int64_t kh, const void* v,
-                       int64_t vt, int64_t vh, const int32_t* slots, const int32_t* positions, int T, int Hkv, int hd,
-                       void* pages, int n_pages, const void* q, int64_t qt, int64_t qh, int Hq, void* q_out,
-                       int64_t ot, int64_t oh, void* stream) {
-  const char* fn = "kvq_paged_append";
+// axes: NULL for plans of one axis
+kvq_status append_impl(const char* fn, const kvq_rope_plan* plan, const kvq_rope_axes_plan* axes, int dtype, const void* k, int64_t kt,
+                       int64_t kh, const void* v, int64_t vt, int64_t vh, const int32_t* slots, const int32_t* positions,
+                       int64_t axis_stride, int T, int Hkv, int hd, void* pages, int n_pages, const void* q, int64_t qt, int64_t qh,
+                       int Hq, void* q_out, int64_t ot, int64_t oh, void* stream) {
   if (kvq_status s = check_common(fn, dtype, T, Hkv, hd, n_pages)) return s;
   if (plan) {
     if (kvq_status s = check_plan(plan, hd, fn)) return s;
+    if (axes)
+      if (kvq_status s = check_axes(*axes, axis_stride, fn)) return s;
     if (!positions && T > 0) return paged_fail(KVQ_ERR_INVALID, fn, "positions is NULL with a plan");
   } else if (positions || q || q_out) {
     return paged_fail(KVQ_ERR_INVALID, fn, "positions, q and q_out need a plan");
@@ -441,6 +450,7 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
     if (kvq_status s = check_buffer(q_out, dev, 16, fn, "q_out")) return s;
   }
   AppendPagedArgs a{k, v, slots, positions, static_cast<unsigned char*>(pages), kt, kh, vt, vh, T, Hkv, n_pages, 0, 0, {}};
+  a.q.ps = axis_stride, a.q.n_axes = axes ? axes->n_axes : 1;
   const int tokens = 32 * E / hd;   // of one item
   const long long rows = ((long long)T + tokens - 1) / tokens;
   // 7 blocks of 4 warps per SM, half of them for q (heads_each)
@@ -452,7 +462,7 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
   if (q) {
     const bool copy = q != q_out && plan->rotary_dim < hd;
     const int V = rope_pairs(*plan);
-    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, 0, copy, 0};
+    a.q = RopeArgs{q, q_out, positions, qt, qh, ot, oh, T, Hq, 0, copy, 0, a.q.ps, a.q.n_axes};
     long long q_blocks;
     if (V) {
       const int units = rope_units(*plan, V, copy);
@@ -465,11 +475,11 @@ kvq_status append_impl(const kvq_rope_plan* plan, int dtype, const void* k, int6
     blocks += std::min<long long>(q_blocks, 152 * 32);
   }
   const bool bf16 = dtype == KVQ_BF16;
-  auto* kern = hd == 128 ? (bf16 ? append_kernel_of<128, true>(plan) : append_kernel_of<128, false>(plan))
-                         : (bf16 ? append_kernel_of<64, true>(plan) : append_kernel_of<64, false>(plan));
+  const AppendKernel kern = hd == 128 ? (bf16 ? append_kernel_of<128, true>(plan, axes) : append_kernel_of<128, false>(plan, axes))
+                                      : (bf16 ? append_kernel_of<64, true>(plan, axes) : append_kernel_of<64, false>(plan, axes));
   kvq_rope_plan none = {};
   cudaError_t e = launch_dependent(kern, dim3((unsigned)blocks), dim3(APPEND_THREADS), 0, static_cast<cudaStream_t>(stream),
-                                   plan ? *plan : none, a);
+                                   axes ? with_axes(*axes) : plan ? *plan : none, a);
   if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
@@ -520,9 +530,25 @@ extern "C" kvq_status kvq_paged_append(const kvq_rope_plan* plan, int dtype, con
                                        const void* q, int64_t q_token_stride, int64_t q_head_stride, int n_q_heads,
                                        void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
                                        void* stream) try {
-  return kvq::append_impl(plan, dtype, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slots,
-                          positions, n_tokens, n_kv_heads, head_dim, pages, n_pages, q, q_token_stride, q_head_stride,
-                          n_q_heads, q_out, q_out_token_stride, q_out_head_stride, stream);
+  return kvq::append_impl("kvq_paged_append", plan, nullptr, dtype, k, k_token_stride, k_head_stride, v, v_token_stride,
+                          v_head_stride, slots, positions, 0, n_tokens, n_kv_heads, head_dim, pages, n_pages, q,
+                          q_token_stride, q_head_stride, n_q_heads, q_out, q_out_token_stride, q_out_head_stride, stream);
+} catch (...) {
+  return KVQ_ERR_HOST_OOM;
+}
+
+extern "C" kvq_status kvq_paged_append_axes(const kvq_rope_axes_plan* plan, int dtype, const void* k, int64_t k_token_stride,
+                                            int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                                            int64_t v_head_stride, const int32_t* slots, const int32_t* positions,
+                                            int64_t axis_stride, int n_tokens, int n_kv_heads, int head_dim, void* pages,
+                                            int n_pages, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                            int n_q_heads, void* q_out, int64_t q_out_token_stride,
+                                            int64_t q_out_head_stride, void* stream) try {
+  const char* fn = "kvq_paged_append_axes";
+  if (!plan) return kvq::paged_fail(KVQ_ERR_INVALID, fn, "plan is NULL");
+  return kvq::append_impl(fn, &plan->plan, plan, dtype, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
+                          slots, positions, axis_stride, n_tokens, n_kv_heads, head_dim, pages, n_pages, q, q_token_stride,
+                          q_head_stride, n_q_heads, q_out, q_out_token_stride, q_out_head_stride, stream);
 } catch (...) {
   return KVQ_ERR_HOST_OOM;
 }

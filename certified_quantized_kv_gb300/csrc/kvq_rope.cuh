@@ -16,7 +16,40 @@ struct RopeArgs {
   int T, H, lanes;   // lanes: heads in step, each with a thread of its own per chunk of pairs
   bool copy;         // the elements behind the rotated ones as well
   int per;           // heads of one item (rope_rows)
+  long long ps;      // stride of the positions' axes (AXES)
+  int n_axes;
 };
+
+// Positions of one token.  With AXES each pair is turned by the position on its own axis, whose number the
+// launch puts into the two lowest bits of the pair's step (0 in a plan: 2^-62 turns).  All of a token's positions
+// are loaded at once: at most four, the last one again for axes that are not there.
+template <bool AXES>
+struct Place {
+  int at[AXES ? 4 : 1];
+  __device__ __forceinline__ void load(const int32_t* pos, long long stride, int n_axes, long long t) {
+#pragma unroll
+    for (int a = 0; a < (AXES ? 4 : 1); ++a) at[a] = pos[(AXES ? min(a, n_axes - 1) * stride : 0) + t];
+  }
+  __device__ __forceinline__ void none() {
+#pragma unroll
+    for (int a = 0; a < (AXES ? 4 : 1); ++a) at[a] = 0;
+  }
+  __device__ __forceinline__ float2 turn(uint64_t step, float magnitude) const {
+    if constexpr (AXES) {
+      const int low = step & 1 ? at[1] : at[0], high = step & 1 ? at[3] : at[2];
+      return rope_cos_sin(step & 2 ? high : low, step & ~3ull, magnitude);
+    } else {
+      return rope_cos_sin(at[0], step, magnitude);
+    }
+  }
+};
+
+// A plan as the kernels with AXES take it.
+inline kvq_rope_plan with_axes(const kvq_rope_axes_plan& p) {
+  kvq_rope_plan out = p.plan;
+  for (int i = 0; i < out.rotary_dim / 2; ++i) out.step[i] = (out.step[i] & ~3ull) | p.axis[i];
+  return out;
+}
 
 // One thread per V pairs of a token, for every `lanes`-th head; the loads of several heads are on
 // their way at once.  HBM bound (4 bytes per element, 32K tokens of 40 heads of 128: 671 MB);
@@ -70,19 +103,21 @@ template <int V>
 __device__ __forceinline__ int turn_at(int i, int half) {
   return V == 8 ? ((i % 8) / 2 * (half / 8) + i / 8) * 2 + i % 2 : i;
 }
-template <int V>
-__device__ __forceinline__ void fill_turns(const kvq_rope_plan& P, const uint64_t* step, const int32_t* pos, long long t0, int n,
+template <int V, bool AXES>
+__device__ __forceinline__ void fill_turns(const kvq_rope_plan& P, const uint64_t* step, const RopeArgs& a, long long t0, int n,
                                            float2* turns) {
   const int half = P.rotary_dim / 2;
   for (int e = threadIdx.x; e < n * half; e += blockDim.x) {
     const int t = e / half, i = e - t * half;
-    turns[t * half + turn_at<V>(i, half)] = rope_cos_sin(pos[t0 + t], step[i], P.magnitude);
+    const uint64_t st = step[i];
+    const int32_t* pos = a.pos + (AXES ? (st & 3) * a.ps : 0);
+    turns[t * half + turn_at<V>(i, half)] = rope_cos_sin(pos[t0 + t], AXES ? st & ~3ull : st, P.magnitude);
   }
 }
 
 // The units of a block that starts with unit `base` and takes every `stride`-th run of THREADS units;
 // turns (TABLE): room for THREADS * V + 2 * 128 elements.
-template <int V, bool INTERLEAVED, bool BF16, int THREADS, bool TABLE>
+template <int V, bool INTERLEAVED, bool BF16, int THREADS, bool TABLE, bool AXES>
 __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t* step, float2* turns, const RopeArgs& a, long long base,
                                           long long stride) {
   constexpr int ROPE_UNROLL = 4;
@@ -113,7 +148,7 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
     if (turned) fetch(h0);   // on their way while cos and sin are formed
     if (TABLE) {
       __syncthreads();   // its previous readers are done
-      fill_turns<V>(P, step, a.pos, t0, (int)(t1 - t0) + 1, turns);
+      fill_turns<V, AXES>(P, step, a, t0, (int)(t1 - t0) + 1, turns);
       __syncthreads();
     }
     if (!live) continue;
@@ -129,9 +164,10 @@ __device__ __forceinline__ void rope_part(const kvq_rope_plan& P, const uint64_t
     float2 cs[V];
     const float2* mine = turns + (t - t0) * half;
     if constexpr (!TABLE) {
-      const int pos = a.pos[t];
+      Place<AXES> place;
+      place.load(a.pos, a.ps, a.n_axes, t);
 #pragma unroll
-      for (int i = 0; i < V; ++i) cs[i] = rope_cos_sin(pos, step[pair(i)], P.magnitude);
+      for (int i = 0; i < V; ++i) cs[i] = place.turn(step[pair(i)], P.magnitude);
     } else if constexpr (V == 8) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -194,7 +230,7 @@ __host__ __device__ __forceinline__ int row_partner(int lane, int c0, int ch, in
 // 4000 tokens of 32 heads of 128 from buffer to buffer, 52 elements rotated: 13.6 us; pairs by threads of
 // their own, as above with V = 2: 23.2.  With half = 52, V = 4: 14.3 us, rows 17.3.
 // Item: a token's heads [h, h + a.per); warp w0 takes every `warps`-th one.
-template <bool BF16>
+template <bool BF16, bool AXES>
 __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t* step, uint4* room, float2* turns, const RopeArgs& a,
                                           long long w0, long long warps) {
   constexpr int U = 4;   // rows of a lane on their way at once
@@ -216,9 +252,10 @@ __device__ __forceinline__ void rope_rows(const kvq_rope_plan& P, const uint64_t
         if (r < rows && h + k * rows + r < h1) v[k] = *reinterpret_cast<const uint4*>(x + (h + k * rows + r) * a.xh + c0);
     };
     fetch(h0);   // on their way while cos and sin are formed
-    const int pos = a.pos[t];
+    Place<AXES> place;
+    place.load(a.pos, a.ps, a.n_axes, t);
     __syncwarp();   // the last item's readers are done
-    for (int i = lane; i < half; i += 32) turns[i] = rope_cos_sin(pos, step[i], P.magnitude);
+    for (int i = lane; i < half; i += 32) turns[i] = place.turn(step[i], P.magnitude);
     __syncwarp();
     float c[8], s[8];
     int from[8];   // the other element of the pair

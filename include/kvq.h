@@ -382,6 +382,42 @@ kvq_status kvq_rope(const kvq_rope_plan* plan, int dtype, const void* x, int64_t
                     int64_t x_head_stride, const int32_t* positions, int n_tokens, int n_heads, void* out,
                     int64_t out_token_stride, int64_t out_head_stride, void* stream);
 
+/* Rotary positions with several axes, for images and video: a token has a position on each axis
+ * (time, height, width, ...) and each pair is turned by the one on its own axis.  Which pairs belong
+ * to which axis: */
+typedef enum kvq_axis_order {
+  KVQ_AXES_BLOCKS = 0, /* axis 0's pairs first, then axis 1's, ... */
+  KVQ_AXES_CYCLED = 1  /* pairs dealt to the axes in turn, to those that have pairs left */
+} kvq_axis_order;
+
+/* As kvq_rope_plan: plain data, initialised on the host and copied into every launch. */
+typedef struct kvq_rope_axes_plan {
+  kvq_rope_plan plan;
+  int32_t n_axes;
+  uint8_t axis[128];   /* of each pair */
+} kvq_rope_axes_plan;
+
+/* kvq_rope_axes_plan_init -- fill `plan` from `cfg` (host only; no CUDA call).
+ *   n_axes           1..4
+ *   axis_pairs       [n_axes] pairs of each axis, each >= 1, rotary_dim / 2 in all
+ *   order            kvq_axis_order
+ *   own_frequencies  0: pair i's frequency is that of a plan of one axis, w_i of rotary_dim
+ *                    elements; 1: the pairs of an axis have the frequencies of a plan of their own, w_j
+ *                    of 2 axis_pairs[a] elements for pair j of axis a (`scaling` too goes by that number)
+ * Errors: KVQ_ERR_INVALID (NULL, or a field outside its range); `plan` is then left as it was. */
+kvq_status kvq_rope_axes_plan_init(const kvq_rope_config* cfg, int n_axes, const int32_t* axis_pairs, int order,
+                                   int own_frequencies, kvq_rope_axes_plan* plan);
+
+/* kvq_rope_axes -- kvq_rope with several axes: pair i of token t is turned by
+ * positions[axis[i] * axis_stride + t] w_i.  With every axis at the same positions and shared
+ * frequencies it is kvq_rope.
+ *   positions    [n_axes][n_tokens] int32, device, axes axis_stride elements apart (>= 0; 0: all axes
+ *                at the same positions)
+ * Everything else as kvq_rope.  Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_rope_axes(const kvq_rope_axes_plan* plan, int dtype, const void* x, int64_t x_token_stride,
+                         int64_t x_head_stride, const int32_t* positions, int64_t axis_stride, int n_tokens,
+                         int n_heads, void* out, int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
 /* kvq_paged_page_bytes -- bytes of one page of one KV head (head_dim 64 or 128).
  * Errors: KVQ_ERR_INVALID. */
 kvq_status kvq_paged_page_bytes(int head_dim, size_t* bytes);
@@ -406,6 +442,15 @@ kvq_status kvq_paged_append(const kvq_rope_plan* plan, int dtype, const void* k,
                             int head_dim, void* pages, int n_pages, const void* q, int64_t q_token_stride,
                             int64_t q_head_stride, int n_q_heads, void* q_out, int64_t q_out_token_stride,
                             int64_t q_out_head_stride, void* stream);
+
+/* kvq_paged_append_axes -- kvq_paged_append with keys and queries turned as by kvq_rope_axes; plan
+ * must not be NULL, positions and axis_stride as there. */
+kvq_status kvq_paged_append_axes(const kvq_rope_axes_plan* plan, int dtype, const void* k, int64_t k_token_stride,
+                                 int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                                 const int32_t* slots, const int32_t* positions, int64_t axis_stride, int n_tokens,
+                                 int n_kv_heads, int head_dim, void* pages, int n_pages, const void* q,
+                                 int64_t q_token_stride, int64_t q_head_stride, int n_q_heads, void* q_out,
+                                 int64_t q_out_token_stride, int64_t q_out_head_stride, void* stream);
 
 /* kvq_paged_gather -- read tokens back from pages: k, v [n_tokens, n_kv_heads, head_dim]
  * strided receive o + s * code of the slots (keys as turned by the append), computed in
