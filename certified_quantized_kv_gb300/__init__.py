@@ -121,6 +121,8 @@ def load_library() -> ctypes.CDLL:
         "kvq_paged_attention_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
         "kvq_paged_attention": [i32, vp, i64, i64, vp, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, f32,
                                 vp, vp, vp, ctypes.c_size_t, vp],
+        "kvq_paged_evict": [vp, i32, vp, i64, i32, vp, i32, i32, i32, vp, i64, i64, i32, i32, i32, i32, vp, i32, vp, i64, i32,
+                            vp, vp, vp, i64, i64, vp],
     }
     for name, argt in sigs.items():
         fn = getattr(lib, name)
@@ -674,6 +676,64 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
           0.0 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return workspace
+
+
+def _table(t, name, B):
+    """Address, row stride and columns of a page table."""
+    st = t.stride()
+    if t.dtype is not _I32 or len(st) != 2 or t.shape[0] != B:
+        raise ValueError(f"{name} must be int32 [{B}, max_pages]")
+    n = t.shape[1]
+    if st[1] != 1 and n > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), st[0] if B > 1 else n, n
+
+
+def _weight_rows(t, name, B, hkv):
+    """Address, (sequence, head) strides and columns of a float32 [batch, n_kv_heads, columns] operand."""
+    if t.dtype is not _torch.float32 or len(t.shape) != 3 or t.shape[0] != B or t.shape[1] != hkv:
+        raise ValueError(f"{name} must be float32 [{B}, {hkv}, columns]")
+    a, b, c = t.stride()
+    n = t.shape[2]
+    if c != 1 and n > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # a dimension of one row has no stride to speak of
+    return t.data_ptr(), a if B > 1 else hkv * n, b if hkv > 1 else n, n
+
+
+def paged_evict(pages, page_table, seq_lens, weights, new_table, new_lens, keep, first=0, recent=0, origin=None, new_weights=None,
+                new_pages=None, stream=None):
+    """Cut sequences back to `keep` tokens per KV head (kvq_paged_evict): the first `first`, the last
+    `recent` and the heaviest of the others move, in their order, to the pages of new_table.
+
+    weights: float32 [B, n_kv_heads, columns]; new_table: int32 [B, pages] of
+    distinct pages that page_table does not name, in `pages` or, when given, in the pool new_pages;
+    new_lens: int32 [B], receives the new lengths; origin: int32 [B, n_kv_heads, keep], receives the kept
+    tokens' indices and -1 behind them (allocated when omitted); new_weights: float32 [B, n_kv_heads,
+    >= keep], receives their weights and 0 behind them in its first `keep` columns.  Returns origin."""
+    pool = pages.shape
+    if len(pool) != 3:
+        raise ValueError("pages must be [n_pages, n_kv_heads, page bytes]")
+    dev = _device_of(pages, "pages")
+    hkv, hd = pool[1], {5120: 64, 10240: 128}.get(pool[2], 0)
+    B = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    to = pages if new_pages is None else new_pages
+    if origin is None:
+        if stream is not None:
+            raise ValueError("origin must be given with a stream")
+        origin = _torch.empty((B, hkv, keep), dtype=_I32, device=pages.device)
+    elif origin.dtype is not _I32 or origin.shape != (B, hkv, keep) or not origin.is_contiguous():
+        raise ValueError(f"origin must be a contiguous int32 tensor [{B}, {hkv}, {keep}]")
+    nw = (None, 0, 0)
+    if new_weights is not None:
+        nw = _weight_rows(new_weights, "new_weights", B, hkv)
+        if nw[3] < keep:
+            raise ValueError(f"new_weights must have {keep} columns at least")
+    w = _weight_rows(weights, "weights", B, hkv)
+    _call(dev, stream, load_library().kvq_paged_evict, *_pool(pages, hkv, hd), *_table(page_table, "page_table", B),
+          _ints(seq_lens, "seq_lens", B, dev), B, hkv, hd, *w, keep, first, recent, *_pool(to, hkv, hd),
+          *_table(new_table, "new_table", B), _ints(new_lens, "new_lens", B, dev), origin.data_ptr(), *nw[:3])
+    return origin
 
 
 def header_functions(header_path: str | None = None) -> list[str]:

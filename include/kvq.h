@@ -504,6 +504,37 @@ kvq_status kvq_paged_attention(int dtype, const void* q, int64_t q_token_stride,
                                int n_kv_heads, int head_dim, int window, float scale, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* kvq_paged_evict -- cut sequences back to `keep` tokens per KV head, each head to its own.  Of a sequence of n
+ * tokens a head keeps the first `first`, the last `recent` and, of the others, those with the largest
+ * weights (the lowest index first among equal ones; a NaN counts as the largest), min(n, keep) in all.
+ * They move, in their order and as they are held (nothing is rounded again), to the pages of new_table.
+ *   pages, page_table, seq_lens   as kvq_paged_attention; a length beyond n_columns counts as n_columns
+ *   weights     [batch, Hkv, n_columns] float, device, columns contiguous, strides in elements (>= 0):
+ *               Columns from a sequence's length on are not read
+ *   keep        1..64 new_max_pages; first >= 0 and recent >= 0 are `keep` at most together
+ *   new_pages   the pool that the tokens move to, of new_n_pages pages (it may be `pages`)
+ *   new_table   [batch, new_max_pages] int32, device, row stride new_table_stride: page j of a sequence
+ *               receives its kept tokens 64j..64j+63; entries behind those are not read.  The pages must
+ *               be distinct, and none may be a page that page_table names; one outside the pool is
+ *               skipped, and tokens of a page_table entry outside its pool become 0
+ *   new_lens    [batch] int32, device: receives min(n, keep); must not be seq_lens
+ *   origin      [batch, Hkv, keep] int32, device, contiguous: receives each kept token's index in its
+ *               sequence, ascending, and -1 behind them
+ *   new_weights optional (NULL): [batch, Hkv, keep] float, device, strided like weights, rows that do not
+ *               overlap: receives the kept tokens' weights, and 0 behind them; must not be weights
+ * Afterwards new_pages, new_table and new_lens are a cache for every call above; tokens that are
+ * appended to it go behind new_lens.  A window counts cached tokens, not positions.  Bytes of the pages behind
+ * a sequence's last kept token stay as they were.  batch <= 2048, Hkv <= 4096, head_dim 64 or 128, batch *
+ * max_pages < 2^30.  Two kernels.  batch = 0 is a no-op.
+ * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_paged_evict(const void* pages, int n_pages, const int32_t* page_table, int64_t table_stride, int max_pages,
+                           const int32_t* seq_lens, int batch, int n_kv_heads, int head_dim, const float* weights,
+                           int64_t weights_seq_stride, int64_t weights_head_stride, int n_columns, int keep, int first,
+                           int recent, void* new_pages, int new_n_pages, const int32_t* new_table,
+                           int64_t new_table_stride, int new_max_pages, int32_t* new_lens, int32_t* origin,
+                           float* new_weights, int64_t new_weights_seq_stride, int64_t new_weights_head_stride,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif
