@@ -121,6 +121,8 @@ def load_library() -> ctypes.CDLL:
         "kvq_paged_attention_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
         "kvq_paged_attention": [i32, vp, i64, i64, vp, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, f32,
                                 vp, vp, vp, ctypes.c_size_t, vp],
+        "kvq_paged_weights": [i32, vp, i64, i64, vp, vp, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, f32, f32,
+                              vp, i64, i64, i32, vp],
         "kvq_paged_evict": [vp, i32, vp, i64, i32, vp, i32, i32, i32, vp, i64, i64, i32, i32, i32, i32, vp, i32, vp, i64, i32,
                             vp, vp, vp, i64, i64, vp],
     }
@@ -701,12 +703,47 @@ def _weight_rows(t, name, B, hkv):
     return t.data_ptr(), a if B > 1 else hkv * n, b if hkv > 1 else n, n
 
 
+def _queries(q):
+    """(batch, query tokens, heads, head_dim) and token and head strides of [B, H, D] or [B, n, H, D] queries."""
+    shape, st = q.shape, q.stride()
+    if len(shape) not in (3, 4):
+        raise ValueError("q must be [batch, n_q_heads, head_dim] or [batch, n_q_tokens, n_q_heads, head_dim]")
+    B, H, D = shape[0], shape[-2], shape[-1]
+    Q = shape[1] if len(shape) == 4 else 1
+    if st[-1] != 1:
+        raise ValueError("q: the last dimension must be contiguous")
+    if Q > 1 and B > 1 and st[0] != Q * st[1]:
+        raise ValueError("q: the query tokens must be evenly spaced in memory")
+    return B, Q, H, D, st[1] if Q > 1 else st[0] if B > 1 else 8, st[-2] if H > 1 else 8
+
+
+def paged_weights(q, lse, pages, page_table, seq_lens, weights, decay=1.0, scale=None, window=0, stream=None):
+    """Attention weights of the last query tokens, accumulated per cached token (kvq_paged_weights):
+    weights = decay * weights + the sum over query tokens and a KV head's query heads.
+
+    q, pages, page_table, seq_lens, scale and window as paged_attention took them, lse: the float32
+    log-sum-exp that it wrote; weights: float32 [B, n_kv_heads, columns], updated in place for the tokens
+    below each sequence's length (zero it before the first call, or begin with decay=0)."""
+    dev = _device_of(q, "q")
+    code = _float_code(q, "q")
+    B, Q, hq, hd, qt, qh = _queries(q)
+    pool = pages.shape
+    if len(pool) != 3:
+        raise ValueError("pages must be [n_pages, n_kv_heads, page bytes]")
+    hkv = pool[1]
+    if lse.dtype is not _torch.float32 or lse.shape != q.shape[:-1] or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32, of q's shape without the last dimension")
+    _call(dev, stream, load_library().kvq_paged_weights, code, q.data_ptr(), qt, qh, lse.data_ptr(), *_pool(pages, hkv, hd),
+          *_table(page_table, "page_table", B), _ints(seq_lens, "seq_lens", B, dev), B, Q, hq, hkv, hd, window,
+          0.0 if scale is None else float(scale), decay, *_weight_rows(weights, "weights", B, hkv))
+
+
 def paged_evict(pages, page_table, seq_lens, weights, new_table, new_lens, keep, first=0, recent=0, origin=None, new_weights=None,
                 new_pages=None, stream=None):
     """Cut sequences back to `keep` tokens per KV head (kvq_paged_evict): the first `first`, the last
     `recent` and the heaviest of the others move, in their order, to the pages of new_table.
 
-    weights: float32 [B, n_kv_heads, columns]; new_table: int32 [B, pages] of
+    weights: float32 [B, n_kv_heads, columns] (e.g. from paged_weights); new_table: int32 [B, pages] of
     distinct pages that page_table does not name, in `pages` or, when given, in the pool new_pages;
     new_lens: int32 [B], receives the new lengths; origin: int32 [B, n_kv_heads, keep], receives the kept
     tokens' indices and -1 behind them (allocated when omitted); new_weights: float32 [B, n_kv_heads,

@@ -1,0 +1,340 @@
+// kvq_paged_weights.cu -- attention weights summed per cached token of the paged 4-bit cache:
+//   w[b, g, t] = decay w[b, g, t] + sum over query tokens i and heads r of group g of exp(scale q_ir k^_t - lse_ir)
+// over the rows that see token t.  Only the keys' halves of the pages are read (80 bytes of a token's 160 at
+// head_dim 128).
+//
+// As in the attention over these pages, nibbles are never converted: masked out of their words they are binary16
+// subnormals n 2^-24 (low nibble of a byte) or 16 n 2^-24 (high nibble, whose channels carry 1/16 in q), exact MMA
+// operands; the key scales multiply each group's fp32 sums and the offsets are a product of their own,
+//   score = sum_g s_tg (q_g . code_tg) + sum_g o_tg sum(q_g),
+// so that scores are fp32 sums of exact products.  Tokens are MMA rows and query rows its columns: a lane holds two
+// tokens of each 16, and their sums over all query rows stay in its registers.
+//
+// The (sequence, KV head, page) units are numbered in that order and cut into equal contiguous ranges, one per CTA,
+// whatever the lengths.  For each (sequence, KV head) of its range a CTA brings up to 128 query rows to binary16 in
+// shared memory, in the order in which lanes take them (times a power of two per row, as in the attention); each warp
+// then takes whole pages: their keys go into registers once and the rows' tiles pass by.  Further rows are added to
+// what the first ones left.  Every sum has one owner and a fixed order.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "kvq.h"
+#include "kvq_launch.h"
+#include "kvq_paged.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int PW_ROWS = 8;            // query rows of a tile (MMA columns)
+constexpr int PW_TILES = 16;          // tiles in shared memory at once
+constexpr int PW_THREADS = 256, PW_WARPS = PW_THREADS / 32, PW_MAX_BATCH = 2048;
+
+// One tile of query rows as the main kernel takes it.
+template <int HD>
+struct alignas(16) PwTile {
+  uint4 q[HD / 32][32];       // per group and lane: B fragments of the low nibbles' and of the high nibbles' product
+  uint32_t o[32];             // per lane: B fragment of the offsets' product (sums of two groups, hi and lo halves)
+  float scale[PW_ROWS];       // of a score in base 2; 0 and
+  float lse[PW_ROWS];         // +inf for rows that count nothing: 2^(0 - inf) = 0
+  int lo[PW_ROWS], hi[PW_ROWS];   // tokens that a row sees
+};
+
+struct PwArgs {
+  const void* q;
+  const float* lse;
+  const unsigned char* pages;
+  const int32_t *table, *lens;
+  float* weights;
+  long long qt, qh, table_stride, ws, wh;
+  int n_pages, max_pages, columns, B, Q, Hq, Hkv, n_rep, rows, RT, window;
+  float scale_log2, decay;
+  bool bf16;
+};
+
+__device__ __forceinline__ int pw_len(const PwArgs& a, int b) {
+  return min(max(a.lens[b], 0), (int)min((long long)a.max_pages * PG, (long long)a.columns));
+}
+
+__device__ __forceinline__ void pw_mma(float (&c)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void pw_mma_z(float (&c)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void pw_mma_k8_z(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
+
+// Tile `rt` of a (sequence, KV head), by one warp: lane (gid, tig) holds the channels 32k + 8 tig .. + 7 of row gid.
+template <int HD>
+__device__ __forceinline__ void pw_rows(const PwArgs& a, int b, int g, int rt, int n, PwTile<HD>& out) {
+  constexpr int G = HD / 32;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int r = rt * PW_ROWS + gid;
+  const bool live = r < a.rows;
+  const int i = live ? r / a.n_rep : 0, h = g * a.n_rep + (live ? r - i * a.n_rep : 0);
+  const unsigned short* src = static_cast<const unsigned short*>(a.q) + ((long long)b * a.Q + i) * a.qt + h * a.qh + 8 * tig;
+  float f[G][8], mx = 0.f;
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 32 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = pair_to_f2(word_of(v, j), a.bf16);
+      f[k][2 * j] = p.x, f[k][2 * j + 1] = p.y;
+      mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
+    }
+  }
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  // the row times 2^e with a largest element in [2^9, 2^10) (as in the attention: what binary16 then loses lies
+  // 2^-30 below the row's largest element)
+  int e = 0;
+  if (mx > 0.f) frexpf(mx, &e);
+  e = max(-126, min(126, 10 - e));
+  const float up = a.scale_log2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e), upl = up * 0.0625f;
+  float gs[G];
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    float t = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaf(f[k][j], up, t);
+    t += __shfl_xor_sync(0xffffffffu, t, 1);
+    t += __shfl_xor_sync(0xffffffffu, t, 2);
+    gs[k] = t;
+    out.q[k][lane] = make_uint4(h2_as_u32(__floats2half2_rn(f[k][0] * up, f[k][4] * up)), h2_as_u32(__floats2half2_rn(f[k][2] * up, f[k][6] * up)),
+                                h2_as_u32(__floats2half2_rn(f[k][1] * upl, f[k][5] * upl)), h2_as_u32(__floats2half2_rn(f[k][3] * upl, f[k][7] * upl)));
+  }
+  const int pr = tig % (G / 2), piece = tig / (G / 2);
+  const float x = pr ? gs[G - 2] : gs[0], y = pr ? gs[G - 1] : gs[1];
+  const __half2 h2 = __floats2half2_rn(x, y);
+  const float2 hf = __half22float2(h2);
+  out.o[lane] = piece == 0 ? h2_as_u32(h2) : piece == 1 ? h2_as_u32(__floats2half2_rn(x - hf.x, y - hf.y)) : 0u;
+  if (tig == 0) {
+    const int hi = max(0, n - a.Q + 1 + i), lo = a.window ? max(0, hi - a.window) : 0;
+    const float lse = live ? a.lse[((long long)b * a.Q + i) * a.Hq + h] : 0.f;
+    // a row that sees nothing (lse -inf) counts nothing
+    const bool counts = live && lse > -INFINITY || lse != lse;
+    out.scale[gid] = counts ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), -e), 1.17549435e-38f), 3.402823466e38f) : 0.f;
+    out.lse[gid] = counts ? lse * LOG2E_F : INFINITY;
+    out.lo[gid] = counts ? lo : 0, out.hi[gid] = counts ? hi : 0;
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(PW_THREADS, 2) paged_weights_kernel(PwArgs a) {
+  using L = Page<HD>;
+  constexpr int G = L::G;
+  constexpr int STEP = 2;   // tiles of 16 tokens at once
+  constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
+  __shared__ PwTile<HD> tiles[PW_TILES];
+  __shared__ int pre[PW_MAX_BATCH + 1];   // pages before each sequence, of one KV head
+  __shared__ int wsum[PW_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  pdl_trigger();
+  pdl_wait();
+  if (threadIdx.x == 0) pre[0] = 0;
+  for (int base = 0, run = 0; base < a.B; base += PW_THREADS) {
+    const int b = base + threadIdx.x;
+    int inc = b < a.B ? (pw_len(a, b) + PG - 1) / PG : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int all = run;
+    for (int k = 0; k < PW_WARPS; ++k) {
+      if (k < warp) inc += wsum[k];
+      all += wsum[k];
+    }
+    if (b < a.B) pre[b + 1] = run + inc;
+    run = all;
+    __syncthreads();
+  }
+  const long long total = (long long)pre[a.B] * a.Hkv;
+  const long long x1 = quotient((blockIdx.x + 1) * total, gridDim.x);
+  long long x = quotient(blockIdx.x * total, gridDim.x);
+  int b = 0;
+  while (x < x1) {
+    // the sequence, KV head and page of unit x, and the end of this CTA's pages of that head
+    int b1 = a.B;
+    while (b1 - b > 1) {   // the last sequence that starts at x or before
+      const int m = (b + b1) / 2;
+      if ((long long)pre[m] * a.Hkv <= x) b = m; else b1 = m;
+    }
+    const int np = pre[b + 1] - pre[b];
+    const long long in = x - (long long)pre[b] * a.Hkv;
+    const int g = (int)quotient(in, np), page0 = (int)(in - (long long)g * np), page1 = (int)min((long long)np, page0 + (x1 - x));
+    x += page1 - page0;
+    const int n = pw_len(a, b), first = a.window ? max(0, n - a.Q + 1 - a.window) : 0;   // tokens before it no query sees
+    for (int rt0 = 0; rt0 < a.RT; rt0 += PW_TILES) {
+      const int nt = min(PW_TILES, a.RT - rt0);
+      __syncthreads();   // the tiles' last readers are done
+      for (int k = warp; k < nt; k += PW_WARPS) pw_rows<HD>(a, b, g, rt0 + k, n, tiles[k]);
+      __syncthreads();
+      for (int page = page0 + warp; page < page1; page += PW_WARPS) {
+        const int tok0 = page * PG;
+        float* w = a.weights + b * a.ws + g * a.wh + tok0;
+        const int at = a.table[b * a.table_stride + page];
+        const bool seen = at >= 0 && at < a.n_pages && tok0 + PG > first;
+        const unsigned char* pg = a.pages + ((size_t)(seen ? at : 0) * a.Hkv + g) * L::BYTES;
+        // (half a page at a time: a whole one's codes and scales leave too few registers)
+#pragma unroll 1
+        for (int i0 = 0; i0 < 64; i0 += 16 * STEP) {
+          float sum[STEP][2];
+#pragma unroll
+          for (int i = 0; i < STEP; ++i) sum[i][0] = sum[i][1] = 0.f;
+          if (seen) {
+            uint32_t code[STEP][2][G], sc[STEP][2][G / 2], off[STEP][2];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int t = i0 + 16 * i + 8 * k + gid;
+                const unsigned char* c = pg + t * L::ROW + tig * 4 * G;
+                if constexpr (G == 4) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(c);
+                  code[i][k][0] = v.x, code[i][k][1] = v.y, code[i][k][2] = v.z, code[i][k][3] = v.w;
+                  const uint2 s = *reinterpret_cast<const uint2*>(pg + L::KS + t * 2 * G);
+                  sc[i][k][0] = s.x, sc[i][k][1] = s.y;
+                } else {
+                  const uint2 v = *reinterpret_cast<const uint2*>(c);
+                  code[i][k][0] = v.x, code[i][k][1] = v.y;
+                  sc[i][k][0] = *reinterpret_cast<const uint32_t*>(pg + L::KS + t * 2 * G);
+                }
+                off[i][k] = *reinterpret_cast<const uint32_t*>(pg + L::KO + t * 2 * G + 4 * (tig % (G / 2)));
+              }
+#pragma unroll 1
+            for (int rt = 0; rt < nt; ++rt) {
+              const PwTile<HD>& T = tiles[rt];
+              uint4 q[G];
+#pragma unroll
+              for (int k = 0; k < G; ++k) q[k] = T.q[k][lane];
+              const uint32_t qo = T.o[lane];
+              const float2 scale = *reinterpret_cast<const float2*>(T.scale + 2 * tig), lse = *reinterpret_cast<const float2*>(T.lse + 2 * tig);
+              const int2 lo = *reinterpret_cast<const int2*>(T.lo + 2 * tig), hi = *reinterpret_cast<const int2*>(T.hi + 2 * tig);
+#pragma unroll
+              for (int i = 0; i < STEP; ++i) {
+                float r[4];
+#pragma unroll
+                for (int k = 0; k < G; ++k) {
+                  const uint32_t x = code[i][0][k], y = code[i][1][k];
+                  const uint32_t low[4] = {x & LO, y & LO, (x >> 8) & LO, (y >> 8) & LO};
+                  const uint32_t high[4] = {x & HI, y & HI, (x >> 8) & HI, (y >> 8) & HI};
+                  float X[4];
+                  pw_mma_z(X, low, q[k].x, q[k].y);
+                  pw_mma(X, high, q[k].z, q[k].w);
+                  const float2 sa = __half22float2(u32_as_h2(sc[i][0][k / 2])), sb = __half22float2(u32_as_h2(sc[i][1][k / 2]));
+                  const float fa = k & 1 ? sa.y : sa.x, fb = k & 1 ? sb.y : sb.x;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) r[j] = k == 0 ? X[j] * (j < 2 ? fa : fb) : fmaf(X[j], j < 2 ? fa : fb, r[j]);
+                }
+                float O[4];
+                pw_mma_k8_z(O, off[i][0], off[i][1], qo);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int t = tok0 + i0 + 16 * i + 8 * (j >> 1) + gid;
+                  const float s = fmaf(r[j], NIB_ROW_SCALE_LO, O[j]);
+                  const float p = exp2_approx(fmaf(s, j & 1 ? scale.y : scale.x, -(j & 1 ? lse.y : lse.x)));
+                  const bool in = t >= (j & 1 ? lo.y : lo.x) && t < (j & 1 ? hi.y : hi.x);
+                  sum[i][j >> 1] += in ? p : 0.f;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < STEP; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float s = sum[i][k];
+              s += __shfl_xor_sync(0xffffffffu, s, 1);
+              s += __shfl_xor_sync(0xffffffffu, s, 2);
+              const int t = i0 + 16 * i + 8 * k + gid;
+              // (decay 0 does not read what is there)
+              if (tig == 0 && tok0 + t < n) w[t] = rt0 ? w[t] + s : a.decay == 0.f ? s : fmaf(w[t], a.decay, s);
+            }
+        }
+      }
+    }
+  }
+}
+
+const char* pw_shape_error(int B, int Q, int Hq, int Hkv, int hd) {
+  if (B < 0 || B > 2048) return "batch must be in 0..2048";
+  if (Q < 1 || Q > 64) return "n_q_tokens must be in 1..64";
+  if (Hkv < 1 || Hkv > MAX_KV_HEADS) return "n_kv_heads must be in 1..4096";
+  if (Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 64) return "n_q_heads / n_kv_heads must be an integer in 1..64";
+  if (hd != 64 && hd != 128) return "head_dim must be 64 or 128";
+  return nullptr;
+}
+
+kvq_status weights_impl(int dtype, const void* q, int64_t qt, int64_t qh, const float* lse, const void* pages, int n_pages,
+                        const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens, int B, int Q, int Hq, int Hkv,
+                        int hd, int window, float scale, float decay, float* weights, int64_t ws, int64_t wh, int columns,
+                        void* stream) {
+  const char* fn = "kvq_paged_weights";
+  auto bad = [&](const char* what) { return paged_fail(KVQ_ERR_INVALID, fn, what); };
+  if (dtype != KVQ_F16 && dtype != KVQ_BF16) return bad("dtype must be KVQ_F16 or KVQ_BF16");
+  if (const char* msg = pw_shape_error(B, Q, Hq, Hkv, hd)) return bad(msg);
+  if (n_pages < 1 || n_pages > (1 << 25)) return bad("n_pages must be in 1..33554432");
+  if (max_pages < 1 || max_pages > (1 << 24) || (long long)B * max_pages >= (1ll << 30))
+    return bad("max_pages must be in 1..16777216 and batch * max_pages below 2^30");
+  if (table_stride < 0) return bad("table_stride must be >= 0");
+  if (window < 0) return bad("window must be >= 0");
+  if (columns < 1) return bad("weights need a column at least");
+  const float scale_log2 = (scale != 0.f ? scale : 1.f / std::sqrt((float)hd)) * LOG2E_F;
+  if (!std::isfinite(scale_log2)) return bad("scale * log2(e) must be finite");
+  if (!std::isfinite(decay)) return bad("decay must be finite");
+  if (B == 0) return KVQ_OK;
+  if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
+  if (ws < 0 || wh < 0 || rows_overlap(B, Hkv, ws, wh, columns)) return bad("weights: rows must not overlap");
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");
+  if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
+  if (kvq_status s = check_buffer(lse, dev, 4, fn, "lse")) return s;
+  if (kvq_status s = check_buffer(pages, dev, 16, fn, "pages")) return s;
+  if (kvq_status s = check_buffer(table, dev, 4, fn, "page_table")) return s;
+  if (kvq_status s = check_buffer(lens, dev, 4, fn, "seq_lens")) return s;
+  if (kvq_status s = check_buffer(weights, dev, 4, fn, "weights")) return s;
+  PwArgs a = {};
+  a.q = q, a.lse = lse, a.pages = static_cast<const unsigned char*>(pages), a.table = table, a.lens = lens, a.weights = weights;
+  a.qt = qt, a.qh = qh, a.table_stride = table_stride, a.ws = ws, a.wh = wh;
+  a.n_pages = n_pages, a.max_pages = (int)std::min<long long>(max_pages, ((long long)columns + PG - 1) / PG), a.columns = columns;
+  a.B = B, a.Q = Q, a.Hq = Hq, a.Hkv = Hkv, a.n_rep = Hq / Hkv, a.rows = Q * a.n_rep, a.RT = (a.rows + PW_ROWS - 1) / PW_ROWS;
+  a.window = std::min(window, 1 << 30);
+  a.scale_log2 = scale_log2, a.decay = decay, a.bf16 = dtype == KVQ_BF16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return paged_cuda_fail(e, fn, "device attributes");
+  // two CTAs per SM, fewer when the table cannot hold a page for each warp
+  const long long most = ((long long)B * a.max_pages * Hkv + PW_WARPS - 1) / PW_WARPS;
+  const dim3 grid((unsigned)std::min<long long>(2 * sms, most));
+  const cudaError_t e = launch_dependent(hd == 128 ? paged_weights_kernel<128> : paged_weights_kernel<64>, grid, dim3(PW_THREADS), 0, st, a);
+  if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
+  return KVQ_OK;
+}
+
+}  // namespace
+}  // namespace kvq
+
+extern "C" kvq_status kvq_paged_weights(int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride, const float* lse,
+                                        const void* pages, int n_pages, const int32_t* page_table, int64_t table_stride,
+                                        int max_pages, const int32_t* seq_lens, int batch, int n_q_tokens, int n_q_heads,
+                                        int n_kv_heads, int head_dim, int window, float scale, float decay, float* weights,
+                                        int64_t weights_seq_stride, int64_t weights_head_stride, int n_columns, void* stream) try {
+  return kvq::weights_impl(dtype, q, q_token_stride, q_head_stride, lse, pages, n_pages, page_table, table_stride, max_pages,
+                           seq_lens, batch, n_q_tokens, n_q_heads, n_kv_heads, head_dim, window, scale, decay, weights,
+                           weights_seq_stride, weights_head_stride, n_columns, stream);
+} catch (...) {
+  return KVQ_ERR_HOST_OOM;
+}

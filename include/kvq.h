@@ -504,13 +504,32 @@ kvq_status kvq_paged_attention(int dtype, const void* q, int64_t q_token_stride,
                                int n_kv_heads, int head_dim, int window, float scale, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* kvq_paged_weights -- the attention weights of the last n_q_tokens queries, summed per cached token and KV head and
+ * accumulated: weights[b, g, t] = decay weights[b, g, t] + the sum, over the query tokens i that see token t and the
+ * query heads r of KV head g, of exp(scale q_ir k_t - lse_ir), for t below the sequence's length; columns behind it
+ * are left as they were.
+ *   q, pages, page_table, seq_lens, window, scale   as kvq_paged_attention
+ *   lse         [batch, n_q_tokens, Hq] float, device, contiguous: the rows' log-sum-exp, as kvq_paged_attention writes
+ *               it.  A row with -inf adds nothing
+ *   decay       finite; 1: plain sums; 0: what is there is overwritten, whatever it is
+ *   weights     [batch, Hkv, n_columns] float, device, columns contiguous, strides in elements (>= 0), rows that
+ *               do not overlap.  Tokens from n_columns on have no weight
+ * A key that is NaN makes the weight of its token NaN; a lse that is NaN those of all tokens its row sees.  Scores
+ * and sums in fp32.  One kernel, no workspace.  Limits as kvq_paged_attention.  batch = 0 is a no-op.
+ * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_paged_weights(int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride, const float* lse,
+                             const void* pages, int n_pages, const int32_t* page_table, int64_t table_stride,
+                             int max_pages, const int32_t* seq_lens, int batch, int n_q_tokens, int n_q_heads,
+                             int n_kv_heads, int head_dim, int window, float scale, float decay, float* weights,
+                             int64_t weights_seq_stride, int64_t weights_head_stride, int n_columns, void* stream);
+
 /* kvq_paged_evict -- cut sequences back to `keep` tokens per KV head, each head to its own.  Of a sequence of n
  * tokens a head keeps the first `first`, the last `recent` and, of the others, those with the largest
  * weights (the lowest index first among equal ones; a NaN counts as the largest), min(n, keep) in all.
  * They move, in their order and as they are held (nothing is rounded again), to the pages of new_table.
  *   pages, page_table, seq_lens   as kvq_paged_attention; a length beyond n_columns counts as n_columns
  *   weights     [batch, Hkv, n_columns] float, device, columns contiguous, strides in elements (>= 0):
- *               Columns from a sequence's length on are not read
+ *               e.g. what kvq_paged_weights accumulates.  Columns from a sequence's length on are not read
  *   keep        1..64 new_max_pages; first >= 0 and recent >= 0 are `keep` at most together
  *   new_pages   the pool that the tokens move to, of new_n_pages pages (it may be `pages`)
  *   new_table   [batch, new_max_pages] int32, device, row stride new_table_stride: page j of a sequence
