@@ -121,6 +121,9 @@ def load_library() -> ctypes.CDLL:
         "kvq_paged_attention_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
         "kvq_paged_attention": [i32, vp, i64, i64, vp, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, f32,
                                 vp, vp, vp, ctypes.c_size_t, vp],
+        "kvq_paged_prefill_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "kvq_paged_prefill": [i32, vp, i64, i64, vp, i32, vp, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, f32,
+                              vp, vp, vp, ctypes.c_size_t, vp],
         "kvq_paged_weights": [i32, vp, i64, i64, vp, vp, i32, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, f32, f32,
                               vp, i64, i64, i32, vp],
         "kvq_paged_evict": [vp, i32, vp, i64, i32, vp, i32, i32, i32, vp, i64, i64, i32, i32, i32, i32, vp, i32, vp, i64, i32,
@@ -701,6 +704,64 @@ def _weight_rows(t, name, B, hkv):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # a dimension of one row has no stride to speak of
     return t.data_ptr(), a if B > 1 else hkv * n, b if hkv > 1 else n, n
+
+
+def _own_workspace(nbytes, dev, like, stream, zero):
+    """A workspace of a call that was given none."""
+    torch = _torch
+    with torch.cuda.device(dev):
+        workspace = (torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            # made (and zeroed) on the current stream and used on the other one
+            other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            other.wait_stream(torch.cuda.current_stream())
+            workspace.record_stream(other)
+    return workspace
+
+
+def paged_prefill_workspace(n_tokens: int, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int = HEAD_DIM) -> int:
+    """Workspace bytes kvq_paged_prefill needs for this shape on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().kvq_paged_prefill_workspace(n_tokens, batch, n_q_heads, n_kv_heads, head_dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_prefill(q, q_starts, pages, page_table, seq_lens, out, lse=None, causal=True, scale=None, window=0, workspace=None,
+                  stream=None):
+    """Attention of prompts or chunks over a pool of 4-bit pages that already holds them (kvq_paged_prefill).
+
+    q: [T, Hq, head_dim] fp16 or bf16 with contiguous rows, the sequences' new tokens packed one behind the
+    other; q_starts: int32 [B + 1], the first row of each sequence and the last one's end; page_table: int32
+    [B, max_pages]; seq_lens: int32 [B], the new tokens included; out: like q, contiguous; lse: float32 [T, Hq]
+    or None.  `workspace` is a device uint8 tensor of at least paged_prefill_workspace(...) bytes (allocated
+    here when omitted).  Returns `workspace` so a caller can reuse it."""
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [n_tokens, n_q_heads, head_dim]")
+    dev = _device_of(q, "q")
+    code, dt = _float_code(q, "q"), q.dtype
+    T, hq, hd = shape
+    pool = pages.shape
+    if len(pool) != 3:
+        raise ValueError("pages must be [n_pages, n_kv_heads, page bytes]")
+    hkv = pool[1]
+    if out.dtype is not dt or out.shape != shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse is not None and (lse.dtype is not _torch.float32 or lse.shape != shape[:-1] or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32, of q's shape without the last dimension")
+    B = seq_lens.shape[0] if len(seq_lens.shape) == 1 else -1
+    pool, rows, starts = _pool(pages, hkv, hd), _rows(q, "q", dt, shape), _ints(q_starts, "q_starts", B + 1, dev)
+    lens, table = _ints(seq_lens, "seq_lens", B, dev), _table(page_table, "page_table", B)
+    if workspace is None:
+        with _torch.cuda.device(dev):
+            need = paged_prefill_workspace(T, B, hq, hkv, hd)
+        workspace = _own_workspace(need, dev, q, stream, False)
+    elif workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _call(dev, stream, load_library().kvq_paged_prefill, code, *rows, starts, T, *pool, *table, lens, B, hq, hkv, hd, int(causal),
+          window, 0.0 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return workspace
 
 
 def _queries(q):

@@ -504,13 +504,46 @@ kvq_status kvq_paged_attention(int dtype, const void* q, int64_t q_token_stride,
                                int n_kv_heads, int head_dim, int window, float scale, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* kvq_paged_prefill_workspace -- device workspace bytes that kvq_paged_prefill needs for this shape on the current
+ * device, whatever the lengths.
+ * Errors: KVQ_ERR_INVALID (NULL bytes, bad shape), KVQ_ERR_CUDA. */
+kvq_status kvq_paged_prefill_workspace(int n_tokens, int batch, int n_q_heads, int n_kv_heads, int head_dim, size_t* bytes);
+
+/* kvq_paged_prefill -- attention of prompts, or of chunks of them, over the paged 4-bit cache that already holds them:
+ * out = softmax(scale q k^T) v over the tokens each query sees, for any number of new tokens per sequence
+ * (kvq_paged_attention is for 64 at most, and faster for a few).
+ *   q           [n_tokens, Hq, head_dim] strided: the sequences' new tokens, packed one behind the other
+ *   q_starts    [batch + 1] int32, device: sequence b's new tokens are rows q_starts[b]..q_starts[b + 1] - 1
+ *               (ascending, clamped to 0..n_tokens; none: an empty chunk), the last ones of its seq_lens[b]
+ *               cached tokens.  Rows in no chunk are left as they were
+ *   pages, page_table, seq_lens, scale   as kvq_paged_attention
+ *   causal      1: new token i of m, in a sequence of n, sees tokens 0..n - m + i; 0: all n tokens (an image's patches)
+ *   window      0; or w > 0, with causal: only the last w of those
+ *   out         [n_tokens, Hq, head_dim], contiguous, of q's type; must not overlap q
+ *   lse         optional (NULL): [n_tokens, Hq] float, natural log of the sum of exp(scale q k)
+ * A query that sees no token (of a chunk longer than its sequence, or of an empty one) gets out = 0 and lse = -inf.  What
+ * pages hold behind a sequence's length (NaN included) does not matter.  A key or value that is NaN reaches the
+ * outputs of the queries that see its token, and no others: those of the value's 32 channels, or all of the row.
+ *   workspace   at least kvq_paged_prefill_workspace(...) bytes, 16-byte aligned; its contents need no
+ *               initialisation.  Calls that share it must not overlap on the GPU.
+ * n_tokens <= 16777216, batch <= 2048, Hq / Hkv an integer in 1..64, Hkv <= 4096, head_dim 64 or 128, batch *
+ * max_pages < 2^30.  Keys, values and softmax weights enter the tensor cores rounded to binary16 (2^-11 each), queries
+ * of bfloat16 after a power of two per row; scores, sums and the softmax's statistics are fp32; weights below
+ * 2^-35 of a row's largest count as 0.  batch = 0 or n_tokens = 0 is a no-op.
+ * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
+kvq_status kvq_paged_prefill(int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const int32_t* q_starts, int n_tokens, const void* pages, int n_pages,
+                             const int32_t* page_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                             int batch, int n_q_heads, int n_kv_heads, int head_dim, int causal, int window, float scale,
+                             void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* kvq_paged_weights -- the attention weights of the last n_q_tokens queries, summed per cached token and KV head and
  * accumulated: weights[b, g, t] = decay weights[b, g, t] + the sum, over the query tokens i that see token t and the
  * query heads r of KV head g, of exp(scale q_ir k_t - lse_ir), for t below the sequence's length; columns behind it
  * are left as they were.
  *   q, pages, page_table, seq_lens, window, scale   as kvq_paged_attention
- *   lse         [batch, n_q_tokens, Hq] float, device, contiguous: the rows' log-sum-exp, as kvq_paged_attention writes
- *               it.  A row with -inf adds nothing
+ *   lse         [batch, n_q_tokens, Hq] float, device, contiguous: the rows' log-sum-exp, as kvq_paged_attention or
+ *               kvq_paged_prefill writes it.  A row with -inf adds nothing
  *   decay       finite; 1: plain sums; 0: what is there is overwritten, whatever it is
  *   weights     [batch, Hkv, n_columns] float, device, columns contiguous, strides in elements (>= 0), rows that
  *               do not overlap.  Tokens from n_columns on have no weight
