@@ -1,10 +1,33 @@
 // kvq_paged_prefill.cu -- attention of prompts and chunks over the paged 4-bit cache:
 //   out = softmax(scale q k^T) v over the tokens that each query sees,
-// for chunks of any length, packed one behind the other.  The rows of a (sequence, KV head) are its chunk's tokens times
-// the query heads of that KV head; a block takes 16 of them and goes over the pages once with a running maximum and sum.
+// for chunks of any length, packed one behind the other, on the 5th-generation tensor cores.
+//
+// The rows of a (sequence, KV head) are its chunk's tokens times the query heads of that KV head: the heads of a group share
+// every key and value that was unpacked.  A unit is 256 of these rows, two tiles of 128; it goes over its tokens 128 (two
+// pages) at a time.  One CTA per SM, whose warps have roles:
+//   warps 0-3, 4-7   softmax of tile 0 and of tile 1, a row per thread: scores out of TMEM, weights back into it
+//   warps 8-11       keys: a token per thread, 4-bit codes to binary16 in shared memory, ahead of their use
+//   warps 12-15      values, likewise
+//   warp 16          issues the MMAs: S = Q K^T (operands in shared memory), O += P V (P in TMEM, over S's columns)
+// The two tiles take turns: while one's scores are turned into weights, the tensor cores work on the other.
+//
+// Unpacking: x^ = o + s code.  Two nibbles at a time are masked into binary16 numbers 1024 + n, less 1024 (exact), then
+// one binary16 multiply-add, so each key and value is the held number rounded once (2^-11).  Nibbles four channels apart
+// come out of one word side by side; keys stay in that order, and so do the queries (a dot product does not mind); values
+// come out with channels of two groups in turn, so their scales and offsets enter in pairs, and the output is put in
+// order when it is written.  Weights are rounded once to binary16 (2^-11) before their product with the values.  The
+// decode attention keeps both exact, at four times the work per score; here the tensor cores would wait for it.
+//
+// The softmax reference of a row moves only when a weight would pass 2^15, and is then set so that the largest is
+// 2^10: accumulators in TMEM are rarely rescaled, and small weights stay normal binary16 numbers.
+//
+// The units' steps (128 tokens) are numbered, sequence by sequence, and cut into equal contiguous ranges, one per CTA,
+// whatever the lengths.  A unit within one range is written out directly; the pieces of one that is cut go to the
+// workspace, and a second kernel merges them in a fixed order, so that results do not depend on timing.
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "kvq.h"
 #include "kvq_launch.h"
@@ -20,132 +43,726 @@ struct PpArgs {
   const int32_t *starts, *table, *lens;
   void* out;
   float* lse;
+  int4* cut;      // [CTAs] the unit that a CTA begins and leaves: sequence, tile, KV head, pieces (0: none)
+  float* part;    // [CTAs][2] pieces of a unit begun in an earlier CTA, and of one that leaves the CTA: [HD + 2][256] floats
   long long qt, qh, table_stride;
   int n_pages, max_pages, T, B, Hq, Hkv, n_rep, window;
   float scale_log2;
   bool bf16, causal;
 };
 
-constexpr int PP_THREADS = 128, PP_ROWS = 16;
+constexpr int PP_ROWS = 256, PP_TOK = 128, PP_STAGES = 2, PP_MAX_BATCH = 2048;
+constexpr int PP_WARPS = 17, PP_THREADS = 32 * PP_WARPS;
+constexpr float PP_TOP = 15.f, PP_SET = 10.f;             // weights are 2^15 at most, 2^10 when their reference is set
+constexpr unsigned long long PP_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
+
+// A chunk and one of its units.
+struct PpUnit {
+  int b, qt, first, m, len;   // sequence, unit, first row of q, new tokens, cached tokens
+  int tiles;                  // units of the sequence (of one KV head)
+  int r0, rn, j0, np;         // rows, and first step and steps
+};
+
+__device__ __forceinline__ int pp_hi(const PpArgs& a, const PpUnit& u, int i) { return a.causal ? max(0, u.len - u.m + 1 + i) : u.len; }
+__device__ __forceinline__ int pp_lo(const PpArgs& a, int hi) { return a.window ? max(0, hi - a.window) : 0; }
+
+__device__ __forceinline__ void pp_sequence(const PpArgs& a, int b, PpUnit& u) {
+  u.b = b;
+  u.first = min(max(a.starts[b], 0), a.T);
+  u.m = max(min(a.starts[b + 1], a.T) - u.first, 0);
+  u.len = min(max(a.lens[b], 0), a.max_pages * PG);
+  u.tiles = (u.m * a.n_rep + PP_ROWS - 1) / PP_ROWS;
+}
+// (every unit has a step, also one whose rows see nothing: its outputs are written all the same)
+__device__ __forceinline__ void pp_unit(const PpArgs& a, int qt, PpUnit& u) {
+  u.qt = qt, u.r0 = qt * PP_ROWS, u.rn = min(PP_ROWS, u.m * a.n_rep - u.r0);
+  const int hi = pp_hi(a, u, (u.r0 + u.rn - 1) / a.n_rep), lo = pp_lo(a, pp_hi(a, u, u.r0 / a.n_rep));
+  u.j0 = lo / PP_TOK;
+  u.np = max(1, (hi + PP_TOK - 1) / PP_TOK - u.j0);
+}
+
+// ---- mbarriers, TMEM and MMAs ----
+__device__ __forceinline__ uint32_t pp_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ unsigned long long pp_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool pp_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// A wait that runs out, in any warp, lets all further ones pass: the CTA finishes with outputs that are NaN.
+__device__ __noinline__ void pp_wait_slow(uint32_t bar, uint32_t parity, volatile int* failed) {
+  const unsigned long long t0 = pp_ns();
+  while (!pp_try(bar, parity)) {
+    if (*failed) return;
+    if (pp_ns() - t0 > PP_WAIT_NS) *failed = 1;
+  }
+}
+__device__ __forceinline__ void pp_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+  if (!pp_try(bar, parity)) pp_wait_slow(bar, parity, failed);
+}
+__device__ __forceinline__ void pp_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pp_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pp_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void pp_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void pp_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand of 128-byte rows of 64 elements, 16-byte pieces XORed with the row's number modulo 8 (128-byte
+// swizzle), eight rows to 1024 bytes; `lead`: bytes between blocks of 64 elements along M or N where those are contiguous
+// (values: rows are tokens, the contraction's index).
+__device__ __forceinline__ uint64_t pp_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// fp32 accumulators, binary16 operands, M 128; B's contiguous index: the contraction's, or (turned) N
+__host__ __device__ constexpr uint32_t pp_idesc(int n, bool turned) {
+  return 1u << 4 | (turned ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
+}
+__device__ __forceinline__ void pp_mma_ss(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc, bool add) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+               :: "r"(d), "l"(x), "l"(y), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t x, uint64_t y, uint32_t idesc, bool add) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+               :: "r"(d), "r"(x), "l"(y), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+
+// 32 columns of this warp's 32 lanes, a lane's in one thread
+__device__ __forceinline__ void pp_ld32(uint32_t (&v)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void pp_st32(uint32_t at, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      :: "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+         "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+         "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void pp_st16(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      :: "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// (the loaded registers are tied to the wait, so that nothing reads them before it)
+__device__ __forceinline__ void pp_wait_ld(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]),
+        "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
+        "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
+        "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]) :: "memory");
+}
+__device__ __forceinline__ void pp_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- 4 bits to binary16 ----
+// Nibbles k and k + 4 of a word as a pair of binary16 numbers 0..15
+template <int K>
+__device__ __forceinline__ __half2 pp_nibbles(uint32_t w) {
+  const uint32_t m = ((w >> (4 * K)) & 0x000F000Fu) | 0x64006400u;   // 1024 + n
+  return __hsub2(u32_as_h2(m), u32_as_h2(0x64006400u));
+}
+// o + s n of a word's four pairs; CLAMP: no larger than binary16's largest (the held number may be, by a step's rounding)
+template <bool CLAMP>
+__device__ __forceinline__ uint4 pp_unpack(uint32_t w, __half2 s, __half2 o) {
+  __half2 h[4] = {__hfma2(pp_nibbles<0>(w), s, o), __hfma2(pp_nibbles<1>(w), s, o), __hfma2(pp_nibbles<2>(w), s, o),
+                  __hfma2(pp_nibbles<3>(w), s, o)};
+  if (CLAMP) {
+    const __half2 top = u32_as_h2(0x7BFF7BFFu), low = u32_as_h2(0xFBFFFBFFu);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = __hmin2_nan(__hmax2_nan(h[k], low), top);
+  }
+  return make_uint4(h2_as_u32(h[0]), h2_as_u32(h[1]), h2_as_u32(h[2]), h2_as_u32(h[3]));
+}
+// Whether |o| + 15 |s| rounds beyond binary16
+__device__ __forceinline__ bool pp_large(__half2 s, __half2 o) {
+  const uint32_t x = h2_as_u32(__hfma2(__habs2(s), u32_as_h2(0x4B804B80u), __habs2(o))) & 0x7FFF7FFFu;
+  return (x & 0xffffu) >= 0x7C00u || (x >> 16) >= 0x7C00u;
+}
+// piece `c` (16 bytes, eight elements) of row r of an operand of `rows` rows
+__device__ __forceinline__ uint32_t pp_place(int rows, int r, int c) {
+  return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
 
 template <int HD>
-__global__ void __launch_bounds__(PP_THREADS) paged_prefill_kernel(PpArgs a) {
+struct PpSmem {
+  static constexpr int Q = PP_ROWS * HD * 2, KV = PP_TOK * HD * 2;
+  static constexpr int K0 = Q, V0 = K0 + PP_STAGES * KV, PRE = V0 + PP_STAGES * KV;
+  static constexpr int bytes(int batch) { return PRE + 8 * (batch + 1) + 1024; }   // (1024: to the swizzle's boundary)
+};
+
+// CTAs among which the steps are cut, and the first step of one of them
+__device__ __forceinline__ int pp_ctas(long long total) { return (int)min((long long)gridDim.x, max(1ll, total)); }
+__device__ __forceinline__ long long pp_cta0(long long total, int c) {
+  const int ctas = pp_ctas(total);
+  return total * min(c, ctas) / ctas;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) {
   using L = Page<HD>;
-  constexpr int G = L::G, PER = PP_ROWS * HD / PP_THREADS, LANES = HD / PER;   // channels of a thread, threads of a row
-  __shared__ float q[PP_ROWS][HD];
-  __shared__ float x[PG][HD + 1];
-  __shared__ float s[PP_ROWS][PG];
-  __shared__ float alpha[PP_ROWS], total[PP_ROWS], top[PP_ROWS];
+  using S = PpSmem<HD>;
+  constexpr int G = L::G, CH = HD / 8;                        // 16-byte pieces of a row
+  constexpr uint32_t SCORES = 0, OUT = 256, TMEM = 512;       // columns: scores (and weights) of tiles 0 and 1, then outputs
+  extern __shared__ unsigned char raw_smem[];
+  unsigned char* sm = raw_smem + (1024 - (pp_smem(raw_smem) & 1023)) % 1024;
+  long long* pre = reinterpret_cast<long long*>(sm + S::PRE);   // [B + 1] steps before each sequence, of one KV head
+  __shared__ __align__(8) unsigned long long bars[17];
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed_at;
+  __shared__ int4 start_at;   // sequence, unit, KV head, step of this CTA's first position
+  volatile int* failed = &failed_at;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t bar0 = pp_smem(bars);
+  const uint32_t k_full = bar0, k_empty = bar0 + 16, v_full = bar0 + 32, v_empty = bar0 + 48;            // [stage]
+  const uint32_t q_full = bar0 + 64, s_full = bar0 + 80, p_full = bar0 + 96, o_full = bar0 + 112;        // [tile]
+  const uint32_t done = bar0 + 128;
+  if (threadIdx.x == 0) {
+    auto init = [&](uint32_t bar, int count) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory"); };
+    for (int k = 0; k < 2; ++k) {
+      init(k_full + 8 * k, 128), init(k_empty + 8 * k, 1), init(v_full + 8 * k, 128), init(v_empty + 8 * k, 1);
+      init(q_full + 8 * k, 128), init(s_full + 8 * k, 1), init(p_full + 8 * k, 128), init(o_full + 8 * k, 1);
+    }
+    init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    failed_at = 0;
+    pre[0] = 0;
+  }
+  if (warp == PP_WARPS - 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(pp_smem(&tmem_at)), "r"(TMEM) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   pdl_trigger();
   pdl_wait();
-  const int g = blockIdx.y;
-  // this block's sequence and tile
-  int b = 0, first = 0, rows = 0;
-  long long tile = blockIdx.x;
-  for (; b < a.B; ++b) {
-    first = min(max(a.starts[b], 0), a.T);
-    rows = (min(max(a.starts[b + 1], first), a.T) - first) * a.n_rep;
-    const int tiles = (rows + PP_ROWS - 1) / PP_ROWS;
-    if (tile < tiles) break;
-    tile -= tiles;
+
+  // ---- this CTA's range of steps ----
+  for (int b = warp; b < a.B; b += PP_WARPS) {
+    PpUnit u;
+    pp_sequence(a, b, u);
+    long long sum = 0;
+    for (int t = lane; t < u.tiles; t += 32) pp_unit(a, t, u), sum += u.np;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) pre[b + 1] = sum;
   }
-  if (b == a.B) return;
-  const int new_tokens = rows / a.n_rep, len = min(max(a.lens[b], 0), a.max_pages * PG);
-  const int r0 = (int)tile * PP_ROWS, rn = min(PP_ROWS, rows - r0);
-  auto hi_of = [&](int i) { return a.causal ? max(0, len - new_tokens + 1 + i) : len; };
-  auto lo_of = [&](int i) { return a.window ? max(0, hi_of(i) - a.window) : 0; };
-  auto row_at = [&](int r, long long ts, long long hs) {
-    const int i = (r0 + r) / a.n_rep, h = g * a.n_rep + (r0 + r) % a.n_rep;
-    return (first + i) * ts + h * hs;
-  };
-  for (int e = threadIdx.x; e < PP_ROWS * HD; e += PP_THREADS) {
-    const int r = e / HD, c = e % HD;
-    q[r][c] = r < rn ? elem_to_f(a.q, row_at(r, a.qt, a.qh) + c, a.bf16) : 0.f;
-  }
-  if (threadIdx.x < PP_ROWS) top[threadIdx.x] = -INFINITY, total[threadIdx.x] = 0.f;
-  const int row = threadIdx.x / LANES, c0 = threadIdx.x % LANES;   // this thread's row and channels c0 + LANES k
-  float acc[PER];
+  pp_before();
+  __syncthreads();
+  pp_after();
+  const uint32_t tmem = tmem_at;
+  long long n_pos;   // of this CTA
+  if (warp == 0) {
+    long long run = 0;
+    for (int base = 1; base <= a.B; base += 32) {
+      long long inc = base + lane <= a.B ? pre[base + lane] : 0;
 #pragma unroll
-  for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-  const int t_lo = lo_of(r0 / a.n_rep), t_hi = hi_of((r0 + rn - 1) / a.n_rep);
-  for (int tok0 = t_lo / PG * PG; tok0 < t_hi; tok0 += PG) {
-    const int page = a.table[b * a.table_stride + tok0 / PG];
-    if (page < 0 || page >= a.n_pages) continue;
-    const unsigned char* pg = a.pages + ((size_t)page * a.Hkv + g) * L::BYTES;
-    const int live = min(PG, t_hi - tok0);   // what lies behind is not read
-    __syncthreads();
-    for (int e = threadIdx.x; e < live * HD; e += PP_THREADS) {
-      const int t = e / HD, c = e % HD, gr = c / 32, j = c % 32;
-      const int code = pg[t * L::ROW + (j / 8) * 4 * G + 4 * gr + (j % 8) / 2] >> (4 * (j & 1)) & 15;
-      const __half* sc = reinterpret_cast<const __half*>(pg + L::KS) + t * G + gr;
-      x[t][c] = fmaf((float)code, __half2float(sc[0]), __half2float(sc[L::SCALES / 2]));
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < PP_ROWS * PG; e += PP_THREADS) {
-      const int r = e / PG, t = e % PG, i = (r0 + r) / a.n_rep;
-      float d = -INFINITY;
-      if (r < rn && tok0 + t >= lo_of(i) && tok0 + t < hi_of(i)) {
-        d = 0.f;
-        for (int c = 0; c < HD; ++c) d = fmaf(q[r][c], x[t][c], d);
-        d *= a.scale_log2;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
       }
-      s[r][t] = d;
+      if (base + lane <= a.B) pre[base + lane] = run + inc;
+      run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    __syncthreads();
-    if (threadIdx.x < PP_ROWS) {
-      float m = top[threadIdx.x];
-      for (int t = 0; t < PG; ++t) m = fmaxf(m, s[threadIdx.x][t]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      alpha[threadIdx.x] = exp2f(top[threadIdx.x] - ref);
-      float sum = 0.f;
-      for (int t = 0; t < PG; ++t) {
-        const float p = exp2f(s[threadIdx.x][t] - ref);
-        s[threadIdx.x][t] = p;
-        sum += p;
+    __syncwarp();
+    const long long total = run * a.Hkv, x0 = pp_cta0(total, blockIdx.x);
+    int b = 0, b1 = a.B;
+    while (b1 - b > 1) {   // the last sequence that starts at x0 or before
+      const int m = (b + b1) / 2;
+      if (pre[m] * a.Hkv <= x0) b = m; else b1 = m;
+    }
+    PpUnit u;
+    pp_sequence(a, b, u);
+    long long in = x0 - pre[b] * a.Hkv;   // position within the sequence: units, then KV heads, then steps
+    int t0 = 0;
+    for (; t0 < u.tiles; t0 += 32) {
+      if (t0 + lane < u.tiles) pp_unit(a, t0 + lane, u);
+      long long inc = t0 + lane < u.tiles ? (long long)u.np * a.Hkv : 0;
+      const long long mine = inc;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
       }
-      total[threadIdx.x] = fmaf(total[threadIdx.x], alpha[threadIdx.x], sum);
-      top[threadIdx.x] = m;
-    }
-    for (int e = threadIdx.x; e < live * HD; e += PP_THREADS) {
-      const int t = e / HD, c = e % HD, gr = c / 32, j = c % 32;
-      const int code = pg[L::VC + vcode_at<HD>(t, (j / 4) * 2 * G + 2 * gr + (j % 4) / 2)] >> (4 * (j & 1)) & 15;
-      const __half* sc = reinterpret_cast<const __half*>(pg + L::VS) + gr * PG + vscale_at(t);
-      x[t][c] = fmaf((float)code, __half2float(sc[0]), __half2float(sc[L::SCALES / 2]));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] *= alpha[row];
-    for (int t = 0; t < live; ++t) {
-      const int i = (r0 + row) / a.n_rep;
-      // (a token that the row does not see may hold anything)
-      if (tok0 + t < lo_of(i) || tok0 + t >= hi_of(i)) continue;
-      const float p = s[row][t];
-#pragma unroll
-      for (int k = 0; k < PER; ++k) acc[k] = fmaf(p, x[t][c0 + LANES * k], acc[k]);
+      const uint32_t here = __ballot_sync(0xffffffffu, mine > 0 && in >= inc - mine && in < inc);
+      if (here) {
+        const int src = __ffs(here) - 1;
+        if (lane == src) {
+          const long long at = in - (inc - mine);
+          start_at = make_int4(b, t0 + lane, (int)(at / u.np), (int)(at % u.np));
+        }
+        break;
+      }
+      in -= __shfl_sync(0xffffffffu, inc, 31);
     }
   }
   __syncthreads();
-  if (row >= rn) return;
-  const float l = total[row], inv = l == 0.f ? 0.f : 1.f / l;
-  const long long at = row_at(row, a.Hq, 1);
-  for (int k = 0; k < PER; ++k) {
-    const float y = acc[k] * inv;
-    unsigned short* o = static_cast<unsigned short*>(a.out) + at * HD + c0 + LANES * k;
-    *o = (unsigned short)(f2_to_pair(y, 0.f, a.bf16) & 0xffffu);
+  {
+    const long long total = pre[a.B] * a.Hkv;
+    n_pos = pp_cta0(total, blockIdx.x + 1) - pp_cta0(total, blockIdx.x);
   }
-  if (a.lse && c0 == 0) a.lse[at] = l == 0.f ? -INFINITY : (top[row] + log2f(l)) * 0.69314718055994531f;
+
+  // ---- the walk over this CTA's pieces of units, the same in every role ----
+  int g = start_at.z, p0 = start_at.w;   // KV head, first step within the unit
+  PpUnit u;
+  auto begin = [&]() {
+    if (n_pos == 0) return;
+    pp_sequence(a, start_at.x, u);
+    pp_unit(a, start_at.y, u);
+  };
+  auto piece = [&]() { return (int)min((long long)(u.np - p0), n_pos); };   // steps of the current piece
+  auto next = [&](int steps) {
+    n_pos -= steps;
+    p0 = 0;
+    if (n_pos == 0 || ++g < a.Hkv) return;
+    g = 0;
+    if (u.qt + 1 < u.tiles) return pp_unit(a, u.qt + 1, u);
+    int b = u.b + 1;
+    while (b < a.B && pre[b + 1] == pre[b]) ++b;
+    pp_sequence(a, b, u);
+    pp_unit(a, 0, u);
+  };
+
+  if (warp < 8) {
+    // ---- softmax ----
+    const int rt = warp >> 2, tid = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's lanes
+    const uint32_t sp = lanes + SCORES + 128 * rt, op = lanes + OUT + HD * rt;
+    unsigned char* qs = sm + rt * (S::Q / 2);
+    uint32_t s_par = 0, o_par = 0;
+    bool begun = false, cut = false;
+    for (begin(); n_pos > 0;) {
+      const int steps = piece();
+      if (128 * rt < u.rn) {
+        // this thread's row, out of memory once and into shared memory as binary16
+        const int r = u.r0 + 128 * rt + tid;
+        const bool live = 128 * rt + tid < u.rn;
+        const int i = live ? r / a.n_rep : 0, h = g * a.n_rep + (live ? r - i * a.n_rep : 0);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + (u.first + i) * a.qt + h * a.qh);
+        // bfloat16: the row times 2^e with a largest element in [2^9, 2^10), which binary16 holds down to 2^-34 of it
+        int e = 0;
+        float sc = fabsf(a.scale_log2);
+        uint32_t odd = 0;   // an infinity or a NaN: all of the row's outputs are NaN
+        float mx = 0.f;
+        if (live) {
+#pragma unroll 4
+          for (int c = 0; c < CH; ++c) {
+            const uint4 v = src[c];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 p = pair_to_f2(word_of(v, k), a.bf16);
+              mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
+              odd |= !(fabsf(p.x) < INFINITY) | !(fabsf(p.y) < INFINITY);
+            }
+          }
+        }
+        if (a.bf16) {
+          if (mx > 0.f && mx < INFINITY) frexpf(mx, &e);
+          e = max(-126, min(126, 10 - e));
+          // never 0 or infinite, so that -inf stays -inf and 0 stays 0
+          sc = fminf(fmaxf(ldexpf(sc, -e), 1.17549435e-38f), 3.402823466e38f);
+        }
+        if (odd) sc = __int_as_float(0x7fc00000);
+        const float up = a.scale_log2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e);
+#pragma unroll 4
+        for (int c = 0; c < CH; ++c) {
+          const uint4 v = live ? src[c] : make_uint4(0, 0, 0, 0);
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 p = pair_to_f2(word_of(v, k), a.bf16);
+            f[2 * k] = p.x * up, f[2 * k + 1] = p.y * up;
+          }
+          // channels 0, 4, 1, 5, ...: as the keys' nibbles come
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = h2_as_u32(__floats2half2_rn(f[k], f[k + 4]));
+          *reinterpret_cast<uint4*>(qs + pp_place(128, tid, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        pp_proxy();
+        pp_before();
+        pp_arrive(q_full + 8 * rt);
+
+        const int hi = live ? pp_hi(a, u, i) : 0, lo = live ? pp_lo(a, hi) : 0;
+        const int hi_all = pp_hi(a, u, (u.r0 + 128 * rt) / a.n_rep);                                       // what every row of the tile sees
+        const int lo_all = pp_lo(a, pp_hi(a, u, (u.r0 + min(u.rn, 128 * rt + 128) - 1) / a.n_rep));
+        const int32_t* table = a.table + u.b * a.table_stride;
+        float ref = -3.402823466e38f, lim = -INFINITY, l = 0.f;   // reference and limit of the scores, sum of weights
+        for (int j = 0; j < steps; ++j) {
+          const int t0 = (u.j0 + p0 + j) * PP_TOK;
+          // pages outside of the pool are not seen
+          uint32_t there = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int page = t0 + k * PG < u.len ? table[t0 / PG + k] : -1;
+            there |= (page >= 0 && page < a.n_pages) << k;
+          }
+          const bool edge = there != 3u || t0 < lo_all || t0 + PP_TOK > hi_all;
+          uint32_t mask[4];   // the tokens that this row sees
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int x = max(0, min(32, lo - t0 - 32 * c)), y = max(0, min(32, hi - t0 - 32 * c));
+              const uint32_t low = x >= 32 ? 0u : 0xffffffffu << x, high = y >= 32 ? 0xffffffffu : (1u << y) - 1u;
+              mask[c] = ((there >> (c >> 1)) & 1u) ? low & high : 0u;
+            }
+          }
+          pp_wait(s_full + 8 * rt, s_par, failed);
+          s_par ^= 1;
+          pp_after();
+          float m = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            pp_ld32(v, sp + 32 * c);
+            pp_wait_ld(v);
+            if (edge) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((mask[c] >> k) & 1u)) v[k] = 0xff800000u;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) m = fmaxf(m, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+          }
+          if (__any_sync(0xffffffffu, m > lim)) {
+            const float now = m > lim ? m * sc - PP_SET : ref, al = exp2_approx(ref - now);
+            if (m > lim) lim = (now + PP_TOP) / sc;
+            ref = now;
+            l *= al;
+            if (j > 0) {   // (the products with the weights before are complete: the scores came behind them)
+#pragma unroll 1
+              for (int c = 0; c < HD; c += 32) {
+                uint32_t v[32];
+                pp_ld32(v, op + c);
+                pp_wait_ld(v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                pp_st32(op + c, v);
+              }
+            }
+          }
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32], w[16];
+            pp_ld32(v, sp + 32 * c);
+            pp_wait_ld(v);
+            if (edge) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((mask[c] >> k) & 1u)) v[k] = 0xff800000u;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 x = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(sc, sc), make_float2(-ref, -ref));
+              const float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+              sum = add2(sum, p);
+              w[k] = h2_as_u32(__floats2half2_rn(p.x, p.y));
+            }
+            pp_st16(sp + 16 * c, w);
+          }
+          l += sum.x + sum.y;
+          pp_wait_st();
+          pp_before();
+          pp_arrive(p_full + 8 * rt);
+        }
+
+        // ---- the piece's end: to the output, or to the workspace ----
+        pp_wait(o_full + 8 * rt, o_par, failed);
+        o_par ^= 1;
+        pp_after();
+        const bool whole = steps == u.np, lost = *failed != 0;
+        if (lost) l = __int_as_float(0x7fc00000);
+        float* part = a.part + ((size_t)blockIdx.x * 2 + (p0 == 0)) * (HD + 2) * PP_ROWS + 128 * rt + tid;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t at = (size_t)(u.first + i) * a.Hq + h;
+        if (whole) {
+          if (live && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
+        } else {
+          part[HD * PP_ROWS] = l == 0.f ? -INFINITY : ref, part[(HD + 1) * PP_ROWS] = l;
+        }
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t v[32];
+          pp_ld32(v, op + 32 * c);
+          pp_wait_ld(v);
+          if (whole) {
+            // column 8w + 2k + (g & 1): channel 32g + 4a + k, w = a G / 2 + g / 2; 32 columns are 32 / G channels of each group
+            constexpr int RUN = 32 / G;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+              uint32_t y[RUN / 2];
+#pragma unroll
+              for (int k = 0; k < RUN; k += 2) {
+                const int col = 8 * ((k / 4) * (G / 2) + gr / 2) + 2 * (k % 4) + (gr & 1);
+                y[k / 2] = f2_to_pair(__uint_as_float(v[col]) * inv, __uint_as_float(v[col + 2]) * inv, a.bf16);
+              }
+              uint4* o = reinterpret_cast<uint4*>(static_cast<unsigned short*>(a.out) + at * HD + 32 * gr + RUN * c);
+              if (live) {
+#pragma unroll
+                for (int k = 0; k < RUN / 8; ++k) o[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) part[(32 * c + k) * PP_ROWS] = __uint_as_float(v[k]);
+          }
+        }
+        if (!whole && p0 == 0) begun = true;
+      }
+      if (steps < u.np && p0 == 0 && threadIdx.x == 0) {
+        // pieces: this CTA's and those of the CTAs that its other steps lie in
+        const long long total = pre[a.B] * a.Hkv, end = pp_cta0(total, blockIdx.x + 1) + (u.np - steps) - 1;
+        const int last = (int)(((end + 1) * pp_ctas(total) - 1) / total);
+        a.cut[blockIdx.x] = make_int4(u.b, u.qt, g, last - (int)blockIdx.x + 1);
+        cut = true;
+      }
+      next(steps);
+    }
+    if (threadIdx.x == 0 && !cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  } else if (warp < 16) {
+    // ---- keys and values: a token per thread ----
+    auto unpacker = [&](auto kind) {
+      constexpr bool values = decltype(kind)::value;
+      const int t = threadIdx.x & 127, pt = t & 63;
+      const uint32_t full = values ? v_full : k_full, empty = values ? v_empty : k_empty;
+      unsigned char* ring = sm + (values ? S::V0 : S::K0);
+      constexpr int W4 = HD / 32;   // 16-byte pieces of a token's codes
+      uint4 code[W4];
+      uint32_t s2[G / 2], o2[G / 2], vo[G / 2];   // scales and offsets of two groups each; keys: the value's offsets too
+      // the next step's codes are on their way while this one's are unpacked
+      auto fetch = [&](int step) {
+        const int tok = step * PP_TOK + t;
+        int page = -1;
+        if (tok < u.len) page = a.table[u.b * a.table_stride + tok / PG];
+        const bool in = page >= 0 && page < a.n_pages;
+        const unsigned char* pg = a.pages + ((size_t)(in ? page : 0) * a.Hkv + g) * L::BYTES;
+  #pragma unroll
+        for (int k = 0; k < W4; ++k) {
+          code[k] = make_uint4(0, 0, 0, 0);
+          if (in) code[k] = *reinterpret_cast<const uint4*>(values ? pg + L::VC + vcode_at<HD>(pt, 16 * k) : pg + pt * L::ROW + 16 * k);
+        }
+  #pragma unroll
+        for (int k = 0; k < G / 2; ++k) {
+          s2[k] = o2[k] = vo[k] = 0;
+          if (!in) continue;
+          const unsigned short* vs = reinterpret_cast<const unsigned short*>(pg + L::VS) + 2 * k * PG + vscale_at(pt);
+          vo[k] = vs[L::SCALES / 2] | (uint32_t)vs[L::SCALES / 2 + PG] << 16;
+          if (values) {
+            s2[k] = vs[0] | (uint32_t)vs[PG] << 16;
+            o2[k] = vo[k];
+          } else {
+            s2[k] = *reinterpret_cast<const uint32_t*>(pg + L::KS + pt * 2 * G + 4 * k);
+            o2[k] = *reinterpret_cast<const uint32_t*>(pg + L::KO + pt * 2 * G + 4 * k);
+          }
+        }
+      };
+      uint32_t stage = 0, par = 1;
+      begin();
+      if (n_pos > 0) fetch(u.j0 + p0);
+      while (n_pos > 0) {
+        const int steps = piece();
+        for (int j = 0; j < steps; ++j) {
+          // a value that is NaN: 0 in the product (weights of 0 would not hide it), and its token's key NaN instead, which
+          // the rows that do not see it mask
+          bool nan = false;
+  #pragma unroll
+          for (int k = 0; k < G / 2; ++k) {
+            const __half2 o = u32_as_h2(vo[k]);
+            const bool x = __hisnan(__low2half(o)), y = __hisnan(__high2half(o));
+            nan |= x | y;
+            if (values) {
+              if (x) o2[k] &= 0xffff0000u, s2[k] &= 0xffff0000u;
+              if (y) o2[k] &= 0x0000ffffu, s2[k] &= 0x0000ffffu;
+            }
+          }
+          if (nan && !values) o2[0] = 0x7fff7fffu;
+          __half2 sh[G], oh[G];   // keys: of each group, twice; values: of two groups, twice the same
+          bool large = false;
+  #pragma unroll
+          for (int k = 0; k < G; ++k) {
+            const __half2 s = u32_as_h2(s2[k / 2]), o = u32_as_h2(o2[k / 2]);
+            sh[k] = values ? s : k & 1 ? __high2half2(s) : __low2half2(s);
+            oh[k] = values ? o : k & 1 ? __high2half2(o) : __low2half2(o);
+            large |= pp_large(sh[k], oh[k]);
+          }
+          pp_wait(empty + 8 * stage, par, failed);
+          unsigned char* to = ring + stage * S::KV;
+          auto unpack = [&](auto clamp) {
+            constexpr bool CLAMP = decltype(clamp)::value;
+  #pragma unroll
+            for (int k = 0; k < W4; ++k)
+  #pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int w = 4 * k + x;   // word of the row
+                // keys: word G a + g is channels 32g + 8a .. + 7, piece 4g + a of the row; values: word G / 2 a + g / 2
+                const int gr = values ? 2 * (w % (G / 2)) : w % G, c = values ? w : 4 * (w % G) + w / G;
+                *reinterpret_cast<uint4*>(to + pp_place(PP_TOK, t, c)) = pp_unpack<CLAMP>(word_of(code[k], x), sh[gr], oh[gr]);
+              }
+          };
+          if (__any_sync(0xffffffffu, large)) unpack(std::true_type{}); else unpack(std::false_type{});
+          pp_proxy();
+          pp_arrive(full + 8 * stage);
+          if (++stage == PP_STAGES) stage = 0, par ^= 1;
+          if (j + 1 < steps) fetch(u.j0 + p0 + j + 1);
+        }
+        next(steps);
+        if (n_pos > 0) fetch(u.j0 + p0);
+      }
+    };
+    if (warp < 12) unpacker(std::false_type{}); else unpacker(std::true_type{});
+  } else if (lane == 0) {
+    // ---- MMAs ----
+    constexpr uint32_t IQK = pp_idesc(PP_TOK, false), IPV = pp_idesc(HD, true);
+    const uint32_t base = pp_smem(sm);
+    uint32_t q_par = 0, kn = 0, vn = 0, p_par = 0;   // steps of keys and values begun
+    auto scores = [&](int rt, uint32_t stage) {
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t at = (k / 4) * 128 * 128 + (k % 4) * 32;
+        pp_mma_ss(tmem + SCORES + 128 * rt, pp_desc(base + rt * (S::Q / 2) + at, 16), pp_desc(base + S::K0 + stage * S::KV + at, 16), IQK, k > 0);
+      }
+      pp_commit(s_full + 8 * rt);
+    };
+    for (begin(); n_pos > 0;) {
+      const int steps = piece(), nt = u.rn > 128 ? 2 : 1;
+      for (int rt = 0; rt < nt; ++rt) {
+        pp_wait(q_full + 8 * rt, (q_par >> rt) & 1u, failed);
+        q_par ^= 1u << rt;
+        if (rt == 0) pp_wait(k_full + 8 * (kn % PP_STAGES), (kn / PP_STAGES) & 1u, failed);
+        pp_after();
+        scores(rt, kn % PP_STAGES);
+      }
+      pp_commit(k_empty + 8 * (kn % PP_STAGES));
+      ++kn;
+      for (int j = 0; j < steps; ++j) {
+        const uint32_t vs = vn % PP_STAGES, ks = kn % PP_STAGES;
+        const bool more = j + 1 < steps;
+        pp_wait(v_full + 8 * vs, (vn / PP_STAGES) & 1u, failed);
+        for (int rt = 0; rt < nt; ++rt) {
+          pp_wait(p_full + 8 * rt, (p_par >> rt) & 1u, failed);
+          p_par ^= 1u << rt;
+          pp_after();
+#pragma unroll
+          for (int k = 0; k < PP_TOK / 16; ++k)
+            pp_mma_ts(tmem + OUT + HD * rt, tmem + SCORES + 128 * rt + 8 * k, pp_desc(base + S::V0 + vs * S::KV + k * 2048, PP_TOK * 128), IPV,
+                      j > 0 || k > 0);
+          if (more) {
+            if (rt == 0) pp_wait(k_full + 8 * ks, (kn / PP_STAGES) & 1u, failed), pp_after();
+            scores(rt, ks);
+          } else {
+            pp_commit(o_full + 8 * rt);
+          }
+        }
+        pp_commit(v_empty + 8 * vs);
+        ++vn;
+        if (more) pp_commit(k_empty + 8 * ks), ++kn;
+      }
+      next(steps);
+    }
+    // nothing of this CTA's is in flight any more when it gives its TMEM back, also behind a wait that ran out
+    pp_commit(done);
+    for (const unsigned long long t = pp_ns(); !pp_try(done, 0) && pp_ns() - t < PP_WAIT_NS;) {}
+  }
+  __syncwarp();
+  pp_before();
+  __syncthreads();
+  pp_after();
+  if (warp == PP_WARPS - 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM) : "memory");
+}
+
+// The pieces of the unit that CTA blockIdx.x begins and leaves, merged in their order: 32 rows per block, a row per
+// lane, eight output channels at a time per warp.
+constexpr int PP_MERGE_THREADS = 256;
+template <int HD>
+__global__ void __launch_bounds__(PP_MERGE_THREADS) prefill_merge_kernel(PpArgs a) {
+  constexpr int G = HD / 32, PART = (HD + 2) * PP_ROWS;
+  pdl_trigger();
+  pdl_wait();
+  const int4 cut = a.cut[blockIdx.x];
+  const int n = cut.w;
+  if (n == 0) return;
+  PpUnit u;
+  pp_sequence(a, cut.x, u);
+  pp_unit(a, cut.y, u);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + lane;
+  if ((int)blockIdx.y * 32 >= u.rn) return;
+  const float* part = a.part + (size_t)blockIdx.x * 2 * PART + row;
+  // piece 0 is the CTA's second one, the others their CTAs' first
+  auto at = [&](int k) { return part + (size_t)(k == 0 ? 1 : 2 * k) * PART; };
+  float top = -INFINITY;
+  for (int k = 0; k < n; ++k) top = fmaxf(top, at(k)[HD * PP_ROWS]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float l = 0.f;
+  for (int k = 0; k < n; ++k) l = fmaf(at(k)[(HD + 1) * PP_ROWS], exp2_approx(at(k)[HD * PP_ROWS] - ref), l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int r = u.r0 + row, i = r / a.n_rep, h = cut.z * a.n_rep + (r - i * a.n_rep);
+  const bool live = row < u.rn;
+  const size_t to = (size_t)(u.first + i) * a.Hq + h;
+  if (live && warp == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+#pragma unroll 1
+  for (int oct = warp; oct < HD / 8; oct += PP_MERGE_THREADS / 32) {
+    const int gr = oct / 4, x = oct % 4;   // channels 32 gr + 8 x .. + 7
+    const int col0 = 8 * (2 * x * (G / 2) + gr / 2) + (gr & 1);
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = 0.f;
+#pragma unroll 2
+    for (int p = 0; p < n; ++p) {
+      const float* from = at(p);
+      const float w = exp2_approx(from[HD * PP_ROWS] - ref);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = fmaf(from[(col0 + 4 * G * (k / 4) + 2 * (k % 4)) * PP_ROWS], w, y[k]);
+    }
+    if (live) {
+      uint32_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = f2_to_pair(y[2 * k] * inv, y[2 * k + 1] * inv, a.bf16);
+      *reinterpret_cast<uint4*>(static_cast<unsigned short*>(a.out) + to * HD + 8 * oct) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
 }
 
 const char* pp_shape_error(int T, int B, int Hq, int Hkv, int hd) {
   if (T < 0 || T > (1 << 24)) return "n_tokens must be in 0..16777216";
-  if (B < 0 || B > 2048) return "batch must be in 0..2048";
+  if (B < 0 || B > PP_MAX_BATCH) return "batch must be in 0..2048";
   if (Hkv < 1 || Hkv > MAX_KV_HEADS) return "n_kv_heads must be in 1..4096";
   if (Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 64) return "n_q_heads / n_kv_heads must be an integer in 1..64";
   if (hd != 64 && hd != 128) return "head_dim must be 64 or 128";
   return nullptr;
 }
 
-size_t pp_bytes(int T, int B, int Hq, int Hkv, int hd) { return 16; }
+size_t pp_cut_bytes(int sms) { return ((size_t)sms * sizeof(int4) + 255) / 256 * 256; }
+size_t pp_bytes(int sms, int hd) { return pp_cut_bytes(sms) + (size_t)sms * 2 * (hd + 2) * PP_ROWS * sizeof(float); }
+
+template <int HD>
+cudaError_t pp_launch(const PpArgs& a, int sms, cudaStream_t st) {
+  auto* k = paged_prefill_kernel<HD>;
+  // the limit belongs to the function and is every host thread's: always the one of the largest batch
+  if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PpSmem<HD>::bytes(PP_MAX_BATCH))) return e;
+  if (cudaError_t e = launch_dependent(k, dim3(sms), dim3(PP_THREADS), PpSmem<HD>::bytes(a.B), st, a)) return e;
+  return launch_dependent(prefill_merge_kernel<HD>, dim3(sms, PP_ROWS / 32), dim3(PP_MERGE_THREADS), 0, st, a);
+}
 
 kvq_status prefill_impl(int dtype, const void* q, int64_t qt, int64_t qh, const int32_t* starts, int T, const void* pages, int n_pages,
                         const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens, int B, int Hq, int Hkv,
@@ -166,8 +783,9 @@ kvq_status prefill_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   if (B == 0 || T == 0) return KVQ_OK;
   if (q == out) return bad("out must not be q");
   if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;
-  int dev = 0;
+  int dev = 0, sms = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return paged_cuda_fail(e, fn, "no current CUDA device");
+  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return paged_cuda_fail(e, fn, "device attributes");
   if (kvq_status s = check_buffer(q, dev, 16, fn, "q")) return s;
   if (kvq_status s = check_buffer(starts, dev, 4, fn, "q_starts")) return s;
   if (kvq_status s = check_buffer(pages, dev, 16, fn, "pages")) return s;
@@ -177,15 +795,16 @@ kvq_status prefill_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   if (lse)
     if (kvq_status s = check_buffer(lse, dev, 4, fn, "lse")) return s;
   if (kvq_status s = check_buffer(workspace, dev, 16, fn, "workspace")) return s;
-  if (workspace_bytes < pp_bytes(T, B, Hq, Hkv, hd)) return bad("workspace smaller than kvq_paged_prefill_workspace reports");
+  if (workspace_bytes < pp_bytes(sms, hd)) return bad("workspace smaller than kvq_paged_prefill_workspace reports");
   PpArgs a = {};
   a.q = q, a.pages = static_cast<const unsigned char*>(pages), a.starts = starts, a.table = table, a.lens = lens, a.out = out;
   a.lse = lse, a.qt = qt, a.qh = qh, a.table_stride = table_stride, a.n_pages = n_pages, a.max_pages = max_pages, a.T = T, a.B = B;
   a.Hq = Hq, a.Hkv = Hkv, a.n_rep = Hq / Hkv, a.window = std::min(window, 1 << 30), a.scale_log2 = scale_log2;
   a.bf16 = dtype == KVQ_BF16, a.causal = causal != 0;
-  const dim3 grid((unsigned)(((long long)T * a.n_rep + PP_ROWS - 1) / PP_ROWS + B), (unsigned)Hkv);
-  const cudaError_t e = launch_dependent(hd == 128 ? paged_prefill_kernel<128> : paged_prefill_kernel<64>, grid, dim3(PP_THREADS), 0,
-                                         static_cast<cudaStream_t>(stream), a);
+  a.cut = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp_cut_bytes(sms));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = hd == 128 ? pp_launch<128>(a, sms, st) : pp_launch<64>(a, sms, st);
   if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
@@ -199,7 +818,14 @@ extern "C" kvq_status kvq_paged_prefill_workspace(int n_tokens, int batch, int n
   if (!bytes) return kvq::paged_fail(KVQ_ERR_INVALID, fn, "NULL output");
   if (const char* msg = kvq::pp_shape_error(n_tokens, batch, n_q_heads, n_kv_heads, head_dim))
     return kvq::paged_fail(KVQ_ERR_INVALID, fn, msg);
-  *bytes = kvq::pp_bytes(n_tokens, batch, n_q_heads, n_kv_heads, head_dim);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return kvq::paged_cuda_fail(e, fn, "no current CUDA device");
+  }
+  *bytes = kvq::pp_bytes(sms, head_dim);
   return KVQ_OK;
 } catch (...) {
   return KVQ_ERR_HOST_OOM;

@@ -48,8 +48,8 @@ def _check(out, lse, q, starts, pages, table, lens, causal, window, scale, heads
                 gl = _f64(lse)[s0:s1, rows]
                 none = np.isneginf(rl)
                 assert np.array_equal(np.isneginf(gl), none)
-                lt = d[..., 0] + 2.0 ** -21 * (np.abs(rl, where=~none, out=np.zeros_like(rl)) + 1) + n * 2.0 ** -34
-                assert np.all(np.abs(gl - rl, where=~none, out=np.zeros_like(rl)) <= lt), (b, g)
+                lt = d[..., 0] + 2.0 ** -21 * (np.abs(np.where(none, 0, rl)) + 1) + n * 2.0 ** -34
+                assert np.all(np.abs(np.where(none, 0, gl) - np.where(none, 0, rl)) <= lt), (b, g)
 
 
 def _run(lens, chunks, Hq, Hkv, D, dt, causal=True, window=0, scale=None, seed=1, qscale=1.0, kscale=1.0, lead=0, per=None):
