@@ -6,13 +6,13 @@
 // every key and value that was unpacked.  A unit is 256 of these rows, two tiles of 128; it goes over its tokens 128 (two
 // pages) at a time.  One CTA per SM, whose warps have roles:
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1, a row per thread: scores out of TMEM, weights back into it
-//   warps 8-11       keys: a token per thread, 4-bit codes to binary16 in shared memory, ahead of their use
-//   warps 12-15      values, likewise
-//   warp 16          issues the MMAs: S = Q K^T (operands in shared memory), O += P V (P in TMEM, over S's columns)
+//   warps 8-11       keys and values: a token per thread, 4-bit codes to binary16 in shared memory, ahead of their use
+//   warp 12          issues the MMAs: S = Q K^T (operands in shared memory), O += P V (P in TMEM, over half of S's columns)
+//   warps 13-15      the next unit's queries to binary16 in shared memory, as soon as the last scores of this one are there
 // The two tiles take turns: while one's scores are turned into weights, the tensor cores work on the other.
 //
-// Unpacking: x^ = o + s code.  Two nibbles at a time are masked into binary16 numbers 1024 + n, less 1024 (exact), then
-// one binary16 multiply-add, so each key and value is the held number rounded once (2^-11).  Nibbles four channels apart
+// Unpacking: x^ = o + s code.  Two nibbles at a time are masked into binary16 numbers 1024 + n (or 64 + n), less 1024
+// (exact), then one binary16 multiply-add, so each key and value is the held number rounded once (2^-11).  Nibbles four channels apart
 // come out of one word side by side; keys stay in that order, and so do the queries (a dot product does not mind); values
 // come out with channels of two groups in turn, so their scales and offsets enter in pairs, and the output is put in
 // order when it is written.  Weights are rounded once to binary16 (2^-11) before their product with the values.  The
@@ -52,7 +52,10 @@ struct PpArgs {
 };
 
 constexpr int PP_ROWS = 256, PP_TOK = 128, PP_STAGES = 2, PP_MAX_BATCH = 2048;
-constexpr int PP_WARPS = 17, PP_THREADS = 32 * PP_WARPS;
+constexpr int PP_WARPS = 16, PP_THREADS = 32 * PP_WARPS, PP_MMA_WARP = 12, PP_Q_WARPS = 3;
+// Registers: 128 for each thread at launch, of which the softmax warps (a row's 128 scores each) get more: together as many
+constexpr int PP_REGS_SOFTMAX = 160, PP_REGS_UNPACK = 128, PP_REGS_OTHER = 64;
+static_assert(2 * PP_REGS_SOFTMAX + PP_REGS_UNPACK + PP_REGS_OTHER == 4 * 128, "");
 constexpr float PP_TOP = 15.f, PP_SET = 10.f;             // weights are 2^15 at most, 2^10 when their reference is set
 constexpr unsigned long long PP_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
 
@@ -96,12 +99,17 @@ __device__ __forceinline__ bool pp_try(uint32_t bar, uint32_t parity) {
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-// A wait that runs out, in any warp, lets all further ones pass: the CTA finishes with outputs that are NaN.
-__device__ __noinline__ void pp_wait_slow(uint32_t bar, uint32_t parity, volatile int* failed) {
-  const unsigned long long t0 = pp_ns();
-  while (!pp_try(bar, parity)) {
+// A wait that runs out, in any warp, lets all further ones pass: the CTA finishes with outputs that are NaN.  (The clock is
+// read once in 256 tries: it takes longer than they do.)
+__device__ __forceinline__ void pp_wait_slow(uint32_t bar, uint32_t parity, volatile int* failed) {
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 0; !pp_try(bar, parity); ++n) {
+    if ((n & 255) != 255) continue;
+    const unsigned long long t = pp_ns();
     if (*failed) return;
-    if (pp_ns() - t0 > PP_WAIT_NS) *failed = 1;
+    if (t0 == 0) t0 = t;
+    if (t - t0 > PP_WAIT_NS) *failed = 1;
   }
 }
 __device__ __forceinline__ void pp_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
@@ -110,32 +118,42 @@ __device__ __forceinline__ void pp_wait(uint32_t bar, uint32_t parity, volatile 
 __device__ __forceinline__ void pp_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-__device__ __forceinline__ void pp_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+// (the whole warp comes here, so that the compiler keeps addresses in uniform registers, which these instructions take: one
+// thread by itself needed 200 cycles per MMA)
+__device__ __forceinline__ void pp_commit(uint32_t bar, bool leader) {
+  if (leader) asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ void pp_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void pp_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void pp_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Shared-memory operand of 128-byte rows of 64 elements, 16-byte pieces XORed with the row's number modulo 8 (128-byte
-// swizzle), eight rows to 1024 bytes; `lead`: bytes between blocks of 64 elements along M or N where those are contiguous
-// (values: rows are tokens, the contraction's index).
-__device__ __forceinline__ uint64_t pp_desc(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
+// swizzle), eight rows to 1024 bytes: the descriptor's halves.  `lead`: bytes between blocks of 64 elements along M or N
+// where those are contiguous (values: rows are tokens, the contraction's index).
+constexpr uint32_t PP_DESC_HIGH = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t pp_desc(uint32_t addr, uint32_t lead) { return (addr >> 4) | (lead >> 4) << 16; }
 // fp32 accumulators, binary16 operands, M 128; B's contiguous index: the contraction's, or (turned) N
 __host__ __device__ constexpr uint32_t pp_idesc(int n, bool turned) {
   return 1u << 4 | (turned ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
 }
-__device__ __forceinline__ void pp_mma_ss(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-               " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-               :: "r"(d), "l"(x), "l"(y), "r"(idesc), "r"((uint32_t)add) : "memory");
+template <uint32_t IDESC>
+__device__ __forceinline__ void pp_mma_ss(uint32_t d, uint32_t x, uint32_t y, bool add, bool leader) {
+  if (leader)
+    asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n"
+                 :: "r"(d), "r"(x), "r"(y), "r"(IDESC), "r"((uint32_t)add), "r"(PP_DESC_HIGH) : "memory");
 }
-__device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t x, uint64_t y, uint32_t idesc, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-               :: "r"(d), "r"(x), "l"(y), "r"(idesc), "r"((uint32_t)add) : "memory");
+template <uint32_t IDESC>
+__device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t x, uint32_t y, bool add, bool leader) {
+  if (leader)
+    asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n"
+                 :: "r"(d), "r"(x), "r"(y), "r"(IDESC), "r"((uint32_t)add), "r"(PP_DESC_HIGH) : "memory");
+}
+__device__ __forceinline__ bool pp_elect() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 
 // 32 columns of this warp's 32 lanes, a lane's in one thread
@@ -149,22 +167,20 @@ __device__ __forceinline__ void pp_ld32(uint32_t (&v)[32], uint32_t at) {
         "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(at));
 }
-__device__ __forceinline__ void pp_st32(uint32_t at, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-      :: "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-         "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
-         "r"(v[30]), "r"(v[31])
-      : "memory");
-}
 __device__ __forceinline__ void pp_st16(uint32_t at, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
       :: "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+__device__ __forceinline__ void pp_ld16(uint32_t (&v)[16], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(at) : "memory");
 }
 // (the loaded registers are tied to the wait, so that nothing reads them before it)
 __device__ __forceinline__ void pp_wait_ld(uint32_t (&v)[32]) {
@@ -176,12 +192,24 @@ __device__ __forceinline__ void pp_wait_ld(uint32_t (&v)[32]) {
 }
 __device__ __forceinline__ void pp_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float pp_max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+template <int N>
+__device__ __forceinline__ void pp_more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void pp_fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+
 // ---- 4 bits to binary16 ----
-// Nibbles k and k + 4 of a word as a pair of binary16 numbers 0..15
+// Nibbles k and k + 4 of a word as a pair of binary16 numbers 0..15: 1024 + n from the lowest bits of the halves, 64 + n from
+// the next four (whose steps are 1 there), less 1024 or 64
 template <int K>
 __device__ __forceinline__ __half2 pp_nibbles(uint32_t w) {
-  const uint32_t m = ((w >> (4 * K)) & 0x000F000Fu) | 0x64006400u;   // 1024 + n
-  return __hsub2(u32_as_h2(m), u32_as_h2(0x64006400u));
+  const uint32_t x = K < 2 ? w : w >> 8;
+  if (K % 2 == 0) return __hsub2(u32_as_h2((x & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u));
+  return __hsub2(u32_as_h2((x & 0x00F000F0u) | 0x54005400u), u32_as_h2(0x54005400u));
 }
 // o + s n of a word's four pairs; CLAMP: no larger than binary16's largest (the held number may be, by a step's rounding)
 template <bool CLAMP>
@@ -228,28 +256,30 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   extern __shared__ unsigned char raw_smem[];
   unsigned char* sm = raw_smem + (1024 - (pp_smem(raw_smem) & 1023)) % 1024;
   long long* pre = reinterpret_cast<long long*>(sm + S::PRE);   // [B + 1] steps before each sequence, of one KV head
-  __shared__ __align__(8) unsigned long long bars[17];
+  __shared__ __align__(8) unsigned long long bars[21];
+  __shared__ float q_scale[2][PP_ROWS];   // of a row's scores in base 2, of two units in turn
   __shared__ uint32_t tmem_at;
   __shared__ int failed_at;
   __shared__ int4 start_at;   // sequence, unit, KV head, step of this CTA's first position
   volatile int* failed = &failed_at;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t bar0 = pp_smem(bars);
+  const uint32_t bar0 = __shfl_sync(0xffffffffu, pp_smem(bars), 0);
   const uint32_t k_full = bar0, k_empty = bar0 + 16, v_full = bar0 + 32, v_empty = bar0 + 48;            // [stage]
   const uint32_t q_full = bar0 + 64, s_full = bar0 + 80, p_full = bar0 + 96, o_full = bar0 + 112;        // [tile]
-  const uint32_t done = bar0 + 128;
+  const uint32_t o_empty = bar0 + 128, q_empty = bar0 + 144, done = bar0 + 160;
   if (threadIdx.x == 0) {
     auto init = [&](uint32_t bar, int count) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory"); };
     for (int k = 0; k < 2; ++k) {
       init(k_full + 8 * k, 128), init(k_empty + 8 * k, 1), init(v_full + 8 * k, 128), init(v_empty + 8 * k, 1);
-      init(q_full + 8 * k, 128), init(s_full + 8 * k, 1), init(p_full + 8 * k, 128), init(o_full + 8 * k, 1);
+      init(q_full + 8 * k, 32 * PP_Q_WARPS), init(o_empty + 8 * k, 128), init(s_full + 8 * k, 1), init(p_full + 8 * k, 128), init(o_full + 8 * k, 1);
+      init(q_empty + 8 * k, 129);
     }
     init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     failed_at = 0;
     pre[0] = 0;
   }
-  if (warp == PP_WARPS - 1) {
+  if (warp == PP_MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(pp_smem(&tmem_at)), "r"(TMEM) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -347,61 +377,17 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     const int rt = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's lanes
     const uint32_t sp = lanes + SCORES + 128 * rt, op = lanes + OUT + HD * rt;
-    unsigned char* qs = sm + rt * (S::Q / 2);
-    uint32_t s_par = 0, o_par = 0;
-    bool begun = false, cut = false;
+    uint32_t s_par = 0, o_par = 0, q_par = 0;
+    bool cut = false;
     for (begin(); n_pos > 0;) {
       const int steps = piece();
       if (128 * rt < u.rn) {
-        // this thread's row, out of memory once and into shared memory as binary16
-        const int r = u.r0 + 128 * rt + tid;
+        const int r = u.r0 + 128 * rt + tid;   // this thread's row
         const bool live = 128 * rt + tid < u.rn;
         const int i = live ? r / a.n_rep : 0, h = g * a.n_rep + (live ? r - i * a.n_rep : 0);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + (u.first + i) * a.qt + h * a.qh);
-        // bfloat16: the row times 2^e with a largest element in [2^9, 2^10), which binary16 holds down to 2^-34 of it
-        int e = 0;
-        float sc = fabsf(a.scale_log2);
-        uint32_t odd = 0;   // an infinity or a NaN: all of the row's outputs are NaN
-        float mx = 0.f;
-        if (live) {
-#pragma unroll 4
-          for (int c = 0; c < CH; ++c) {
-            const uint4 v = src[c];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 p = pair_to_f2(word_of(v, k), a.bf16);
-              mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
-              odd |= !(fabsf(p.x) < INFINITY) | !(fabsf(p.y) < INFINITY);
-            }
-          }
-        }
-        if (a.bf16) {
-          if (mx > 0.f && mx < INFINITY) frexpf(mx, &e);
-          e = max(-126, min(126, 10 - e));
-          // never 0 or infinite, so that -inf stays -inf and 0 stays 0
-          sc = fminf(fmaxf(ldexpf(sc, -e), 1.17549435e-38f), 3.402823466e38f);
-        }
-        if (odd) sc = __int_as_float(0x7fc00000);
-        const float up = a.scale_log2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e);
-#pragma unroll 4
-        for (int c = 0; c < CH; ++c) {
-          const uint4 v = live ? src[c] : make_uint4(0, 0, 0, 0);
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 p = pair_to_f2(word_of(v, k), a.bf16);
-            f[2 * k] = p.x * up, f[2 * k + 1] = p.y * up;
-          }
-          // channels 0, 4, 1, 5, ...: as the keys' nibbles come
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = h2_as_u32(__floats2half2_rn(f[k], f[k + 4]));
-          *reinterpret_cast<uint4*>(qs + pp_place(128, tid, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        pp_proxy();
-        pp_before();
-        pp_arrive(q_full + 8 * rt);
-
+        pp_wait(q_full + 8 * rt, q_par & 1, failed);
+        const float sc = q_scale[q_par][128 * rt + tid];
+        pp_arrive(q_empty + 8 * rt);   // (so that no warp falls two units behind the queries, whose barrier tells two phases apart)
         const int hi = live ? pp_hi(a, u, i) : 0, lo = live ? pp_lo(a, hi) : 0;
         const int hi_all = pp_hi(a, u, (u.r0 + 128 * rt) / a.n_rep);                                       // what every row of the tile sees
         const int lo_all = pp_lo(a, pp_hi(a, u, (u.r0 + min(u.rn, 128 * rt + 128) - 1) / a.n_rep));
@@ -417,7 +403,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
             there |= (page >= 0 && page < a.n_pages) << k;
           }
           const bool edge = there != 3u || t0 < lo_all || t0 + PP_TOK > hi_all;
-          uint32_t mask[4];   // the tokens that this row sees
+          uint32_t mask[4] = {};   // the tokens that this row sees
           if (edge) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -429,19 +415,29 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
           pp_wait(s_full + 8 * rt, s_par, failed);
           s_par ^= 1;
           pp_after();
-          float m = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            pp_ld32(v, sp + 32 * c);
-            pp_wait_ld(v);
+          // The scores 32 tokens at a time, twice (in registers they would be 128): for the row's maximum, then for the
+          // weights, which take the place of scores that were read.
+          auto hide = [&](uint32_t (&v)[32], uint32_t seen) {
             if (edge) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!((mask[c] >> k) & 1u)) v[k] = 0xff800000u;
+                if (!((seen >> k) & 1u)) v[k] = 0xff800000u;
             }
+          };
+          float m = -INFINITY;
+          auto most = [&](uint32_t (&v)[32], uint32_t seen) {
+            hide(v, seen);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) m = fmaxf(m, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+            for (int k = 0; k < 32; k += 2) m = pp_max3(m, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          };
+          uint32_t v0[32], v1[32];
+          pp_ld32(v0, sp);
+          // (rolled up, here and where the codes are unpacked: with each of the roles' loops straight, warps spent half of
+          // their time on instructions that were not there yet)
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            pp_wait_ld(v0), pp_ld32(v1, sp + 32 * c + 32), most(v0, c ? mask[2] : mask[0]);
+            pp_wait_ld(v1), pp_ld32(v0, sp + ((32 * c + 64) & 127)), most(v1, c ? mask[3] : mask[1]);
           }
           if (__any_sync(0xffffffffu, m > lim)) {
             const float now = m > lim ? m * sc - PP_SET : ref, al = exp2_approx(ref - now);
@@ -450,27 +446,19 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
             l *= al;
             if (j > 0) {   // (the products with the weights before are complete: the scores came behind them)
 #pragma unroll 1
-              for (int c = 0; c < HD; c += 32) {
-                uint32_t v[32];
-                pp_ld32(v, op + c);
-                pp_wait_ld(v);
+              for (int c = 0; c < HD; c += 16) {
+                uint32_t x[16];
+                pp_ld16(x, op + c);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
-                pp_st32(op + c, v);
+                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
+                pp_st16(op + c, x);
               }
             }
           }
           float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], w[16];
-            pp_ld32(v, sp + 32 * c);
-            pp_wait_ld(v);
-            if (edge) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((mask[c] >> k) & 1u)) v[k] = 0xff800000u;
-            }
+          auto weigh = [&](uint32_t (&v)[32], int c, uint32_t seen) {
+            hide(v, seen);
+            uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const float2 x = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(sc, sc), make_float2(-ref, -ref));
@@ -479,6 +467,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
               w[k] = h2_as_u32(__floats2half2_rn(p.x, p.y));
             }
             pp_st16(sp + 16 * c, w);
+          };
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            pp_wait_ld(v0), pp_ld32(v1, sp + 32 * c + 32), weigh(v0, c, c ? mask[2] : mask[0]);
+            pp_wait_ld(v1);
+            if (c == 0) pp_ld32(v0, sp + 64);
+            weigh(v1, c + 1, c ? mask[3] : mask[1]);
           }
           l += sum.x + sum.y;
           pp_wait_st();
@@ -527,7 +522,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
             for (int k = 0; k < 32; ++k) part[(32 * c + k) * PP_ROWS] = __uint_as_float(v[k]);
           }
         }
-        if (!whole && p0 == 0) begun = true;
+        pp_before();
+        pp_arrive(o_empty + 8 * rt);
+        q_par ^= 1;
       }
       if (steps < u.np && p0 == 0 && threadIdx.x == 0) {
         // pieces: this CTA's and those of the CTAs that its other steps lie in
@@ -539,155 +536,263 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
       next(steps);
     }
     if (threadIdx.x == 0 && !cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
-  } else if (warp < 16) {
+  } else if (warp < 12) {
     // ---- keys and values: a token per thread ----
-    auto unpacker = [&](auto kind) {
-      constexpr bool values = decltype(kind)::value;
-      const int t = threadIdx.x & 127, pt = t & 63;
-      const uint32_t full = values ? v_full : k_full, empty = values ? v_empty : k_empty;
-      unsigned char* ring = sm + (values ? S::V0 : S::K0);
-      constexpr int W4 = HD / 32;   // 16-byte pieces of a token's codes
-      uint4 code[W4];
-      uint32_t s2[G / 2], o2[G / 2], vo[G / 2];   // scales and offsets of two groups each; keys: the value's offsets too
-      // the next step's codes are on their way while this one's are unpacked
-      auto fetch = [&](int step) {
-        const int tok = step * PP_TOK + t;
-        int page = -1;
-        if (tok < u.len) page = a.table[u.b * a.table_stride + tok / PG];
-        const bool in = page >= 0 && page < a.n_pages;
-        const unsigned char* pg = a.pages + ((size_t)(in ? page : 0) * a.Hkv + g) * L::BYTES;
-  #pragma unroll
-        for (int k = 0; k < W4; ++k) {
-          code[k] = make_uint4(0, 0, 0, 0);
-          if (in) code[k] = *reinterpret_cast<const uint4*>(values ? pg + L::VC + vcode_at<HD>(pt, 16 * k) : pg + pt * L::ROW + 16 * k);
-        }
-  #pragma unroll
-        for (int k = 0; k < G / 2; ++k) {
-          s2[k] = o2[k] = vo[k] = 0;
-          if (!in) continue;
-          const unsigned short* vs = reinterpret_cast<const unsigned short*>(pg + L::VS) + 2 * k * PG + vscale_at(pt);
-          vo[k] = vs[L::SCALES / 2] | (uint32_t)vs[L::SCALES / 2 + PG] << 16;
-          if (values) {
-            s2[k] = vs[0] | (uint32_t)vs[PG] << 16;
-            o2[k] = vo[k];
-          } else {
-            s2[k] = *reinterpret_cast<const uint32_t*>(pg + L::KS + pt * 2 * G + 4 * k);
-            o2[k] = *reinterpret_cast<const uint32_t*>(pg + L::KO + pt * 2 * G + 4 * k);
-          }
-        }
-      };
-      uint32_t stage = 0, par = 1;
-      begin();
-      if (n_pos > 0) fetch(u.j0 + p0);
-      while (n_pos > 0) {
-        const int steps = piece();
-        for (int j = 0; j < steps; ++j) {
-          // a value that is NaN: 0 in the product (weights of 0 would not hide it), and its token's key NaN instead, which
-          // the rows that do not see it mask
-          bool nan = false;
-  #pragma unroll
-          for (int k = 0; k < G / 2; ++k) {
-            const __half2 o = u32_as_h2(vo[k]);
-            const bool x = __hisnan(__low2half(o)), y = __hisnan(__high2half(o));
-            nan |= x | y;
-            if (values) {
-              if (x) o2[k] &= 0xffff0000u, s2[k] &= 0xffff0000u;
-              if (y) o2[k] &= 0x0000ffffu, s2[k] &= 0x0000ffffu;
-            }
-          }
-          if (nan && !values) o2[0] = 0x7fff7fffu;
-          __half2 sh[G], oh[G];   // keys: of each group, twice; values: of two groups, twice the same
-          bool large = false;
-  #pragma unroll
-          for (int k = 0; k < G; ++k) {
-            const __half2 s = u32_as_h2(s2[k / 2]), o = u32_as_h2(o2[k / 2]);
-            sh[k] = values ? s : k & 1 ? __high2half2(s) : __low2half2(s);
-            oh[k] = values ? o : k & 1 ? __high2half2(o) : __low2half2(o);
-            large |= pp_large(sh[k], oh[k]);
-          }
-          pp_wait(empty + 8 * stage, par, failed);
-          unsigned char* to = ring + stage * S::KV;
-          auto unpack = [&](auto clamp) {
-            constexpr bool CLAMP = decltype(clamp)::value;
-  #pragma unroll
-            for (int k = 0; k < W4; ++k)
-  #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const int w = 4 * k + x;   // word of the row
-                // keys: word G a + g is channels 32g + 8a .. + 7, piece 4g + a of the row; values: word G / 2 a + g / 2
-                const int gr = values ? 2 * (w % (G / 2)) : w % G, c = values ? w : 4 * (w % G) + w / G;
-                *reinterpret_cast<uint4*>(to + pp_place(PP_TOK, t, c)) = pp_unpack<CLAMP>(word_of(code[k], x), sh[gr], oh[gr]);
-              }
-          };
-          if (__any_sync(0xffffffffu, large)) unpack(std::true_type{}); else unpack(std::false_type{});
-          pp_proxy();
-          pp_arrive(full + 8 * stage);
-          if (++stage == PP_STAGES) stage = 0, par ^= 1;
-          if (j + 1 < steps) fetch(u.j0 + p0 + j + 1);
-        }
-        next(steps);
-        if (n_pos > 0) fetch(u.j0 + p0);
+    const int t = threadIdx.x & 127, pt = t & 63;
+    constexpr int W4 = HD / 32;   // 16-byte pieces of a token's codes
+    struct Held {                 // a key and a value as they are held
+      uint4 code[2][W4];
+      uint32_t s[2][G / 2], o[2][G / 2];   // scales and offsets, of two groups each
+    };
+    // Three steps are on their way: the page number of the one after the next, the next one's codes, and this one's into
+    // shared memory.
+    int left = 0, page = -1, head = 0;
+    auto look = [&]() {   // the page of this thread's token in the walk's step, and on
+      page = -1;
+      if (n_pos == 0) return;
+      const int tok = (u.j0 + p0) * PP_TOK + t;
+      if (tok < u.len) page = a.table[u.b * a.table_stride + tok / PG];
+      head = g;
+      if (--left > 0) ++p0, --n_pos;
+      else {
+        next(1);
+        if (n_pos > 0) left = piece();
       }
     };
-    if (warp < 12) unpacker(std::false_type{}); else unpacker(std::true_type{});
-  } else if (lane == 0) {
-    // ---- MMAs ----
-    constexpr uint32_t IQK = pp_idesc(PP_TOK, false), IPV = pp_idesc(HD, true);
-    const uint32_t base = pp_smem(sm);
-    uint32_t q_par = 0, kn = 0, vn = 0, p_par = 0;   // steps of keys and values begun
-    auto scores = [&](int rt, uint32_t stage) {
+    auto fetch = [&](Held& x) {
+      const bool in = page >= 0 && page < a.n_pages;
+      const unsigned char* pg = a.pages + ((size_t)(in ? page : 0) * a.Hkv + head) * L::BYTES;
 #pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        const uint32_t at = (k / 4) * 128 * 128 + (k % 4) * 32;
-        pp_mma_ss(tmem + SCORES + 128 * rt, pp_desc(base + rt * (S::Q / 2) + at, 16), pp_desc(base + S::K0 + stage * S::KV + at, 16), IQK, k > 0);
+      for (int k = 0; k < W4; ++k) {
+        x.code[0][k] = x.code[1][k] = make_uint4(0, 0, 0, 0);
+        if (!in) continue;
+        x.code[0][k] = *reinterpret_cast<const uint4*>(pg + pt * L::ROW + 16 * k);
+        x.code[1][k] = *reinterpret_cast<const uint4*>(pg + L::VC + vcode_at<HD>(pt, 16 * k));
       }
-      pp_commit(s_full + 8 * rt);
+#pragma unroll
+      for (int k = 0; k < G / 2; ++k) {
+        x.s[0][k] = x.o[0][k] = x.s[1][k] = x.o[1][k] = 0;
+        if (!in) continue;
+        x.s[0][k] = *reinterpret_cast<const uint32_t*>(pg + L::KS + pt * 2 * G + 4 * k);
+        x.o[0][k] = *reinterpret_cast<const uint32_t*>(pg + L::KO + pt * 2 * G + 4 * k);
+        const unsigned short* vs = reinterpret_cast<const unsigned short*>(pg + L::VS) + 2 * k * PG + vscale_at(pt);
+        x.s[1][k] = vs[0] | (uint32_t)vs[PG] << 16;
+        x.o[1][k] = vs[L::SCALES / 2] | (uint32_t)vs[L::SCALES / 2 + PG] << 16;
+      }
+    };
+    // one operand's row of what is in hand
+    auto unpack = [&](auto kind, Held& x, unsigned char* to) {
+      constexpr bool values = decltype(kind)::value;
+      __half2 sh[G], oh[G];   // keys: of each group, twice; values: of two groups, twice the same
+      bool large = false;
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const __half2 s = u32_as_h2(x.s[values][k / 2]), o = u32_as_h2(x.o[values][k / 2]);
+        sh[k] = values ? s : k & 1 ? __high2half2(s) : __low2half2(s);
+        oh[k] = values ? o : k & 1 ? __high2half2(o) : __low2half2(o);
+        large |= pp_large(sh[k], oh[k]);
+      }
+      auto words = [&](auto clamp) {
+        constexpr bool CLAMP = decltype(clamp)::value;
+#pragma unroll 1
+        for (int k = 0; k < W4; ++k) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // word w = 4k + i of the row.  Keys: word G a + g is channels 32g + 8a .. + 7, piece 4g + a of the row; values:
+            // word G / 2 a + g / 2
+            const int gr = values ? 2 * (i % (G / 2)) : i % G, c = values ? 4 * k + i : 4 * (i % G) + 4 / G * k + i / G;
+            *reinterpret_cast<uint4*>(to + pp_place(PP_TOK, t, c)) = pp_unpack<CLAMP>(word_of(x.code[values][0], i), sh[gr], oh[gr]);
+          }
+#pragma unroll
+          for (int i = 0; i + 1 < W4; ++i) x.code[values][i] = x.code[values][i + 1];
+        }
+      };
+      if (__any_sync(0xffffffffu, large)) words(std::true_type{}); else words(std::false_type{});
+      pp_proxy();
+    };
+    uint32_t stage = 0, par = 1;
+    auto put = [&](Held& x) {
+      // a value that is NaN: 0 in the product (weights of 0 would not hide it), and its token's key NaN instead, which
+      // the rows that do not see it mask
+      bool nan = false;
+#pragma unroll
+      for (int k = 0; k < G / 2; ++k) {
+        const __half2 o = u32_as_h2(x.o[1][k]);
+        const bool lo = __hisnan(__low2half(o)), hi = __hisnan(__high2half(o));
+        nan |= lo | hi;
+        if (lo) x.o[1][k] &= 0xffff0000u, x.s[1][k] &= 0xffff0000u;
+        if (hi) x.o[1][k] &= 0x0000ffffu, x.s[1][k] &= 0x0000ffffu;
+      }
+      if (nan) x.o[0][0] = 0x7fff7fffu;
+      pp_wait(k_empty + 8 * stage, par, failed);
+      unpack(std::false_type{}, x, sm + S::K0 + stage * S::KV);
+      pp_arrive(k_full + 8 * stage);
+      pp_wait(v_empty + 8 * stage, par, failed);
+      unpack(std::true_type{}, x, sm + S::V0 + stage * S::KV);
+      pp_arrive(v_full + 8 * stage);
+      if (++stage == PP_STAGES) stage = 0, par ^= 1;
+    };
+    begin();
+    if (n_pos > 0) left = piece();
+    Held x, y;
+    long long todo = n_pos;
+    look();
+    if (todo > 0) fetch(y), look();
+#pragma unroll 1
+    for (; todo > 0; --todo) {
+      x = y;
+      if (todo > 1) fetch(y), look();
+      put(x);
+    }
+  } else if (warp > PP_MMA_WARP) {
+    // ---- queries ----
+    uint32_t par = 3, turn = 0;   // bit rt: parity of the wait for the tile's last scores, and of its units
+    // CH lanes hold a row, 16 bytes each; a warp takes RUN groups of rows at once, whose loads are on their way together
+    constexpr int PER = 32 / CH, RUN = 8;
+    const int c = lane % CH;
+    auto load = [&](int rt) {
+      unsigned char* qs = sm + rt * (S::Q / 2);
+      for (int row0 = (warp - PP_MMA_WARP - 1) * PER + lane / CH; row0 < 128; row0 += PP_Q_WARPS * PER * RUN) {
+        uint4 v[RUN];
+#pragma unroll
+        for (int x = 0; x < RUN; ++x) {
+          const int row = row0 + x * PP_Q_WARPS * PER, r = u.r0 + 128 * rt + row, i = r / a.n_rep, h = g * a.n_rep + r - i * a.n_rep;
+          v[x] = make_uint4(0, 0, 0, 0);
+          if (row < 128 && 128 * rt + row < u.rn)
+            v[x] = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + (u.first + i) * a.qt + h * a.qh + 8 * c);
+        }
+#pragma unroll
+        for (int x = 0; x < RUN; ++x) {
+          const int row = row0 + x * PP_Q_WARPS * PER;
+          // the largest bits of an element but its sign: from INF on an infinity or a NaN, with which all of the row's
+          // outputs are NaN
+          const uint32_t INF = a.bf16 ? 0x7F80u : 0x7C00u;
+          uint32_t mx = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, word_of(v[x], k) & 0x7FFF7FFFu);
+#pragma unroll
+          for (int o = 1; o < CH; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          mx = max(mx & 0xffffu, mx >> 16);
+          float sc = fabsf(a.scale_log2);
+          uint32_t w[4];
+          // channels 0, 4, 1, 5, ...: as the keys' nibbles come
+          if (a.bf16) {
+            // the row times 2^e with a largest element in [2^9, 2^10), which binary16 holds down to 2^-34 of it; both powers
+            // are normal fp32 numbers
+            const int e = max(-126, min(126, 136 - (int)(mx >> 7)));
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+            // never 0 or infinite, so that -inf stays -inf and 0 stays 0
+            sc = fminf(fmaxf(sc * down, 1.17549435e-38f), 3.402823466e38f);
+            const float f = a.scale_log2 < 0.f ? -up : up;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t p = word_of(v[x], k / 2), q = word_of(v[x], 2 + k / 2);
+              const float y = __uint_as_float(k & 1 ? p & 0xffff0000u : p << 16), z = __uint_as_float(k & 1 ? q & 0xffff0000u : q << 16);
+              w[k] = h2_as_u32(__floats2half2_rn(y * f, z * f));
+            }
+          } else {
+            const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __byte_perm(word_of(v[x], k / 2), word_of(v[x], 2 + k / 2), k & 1 ? 0x7632 : 0x5410) ^ sign;
+          }
+          if (row < 128) {
+            if (c == 0) q_scale[(turn >> rt) & 1u][128 * rt + row] = mx < INF ? sc : __int_as_float(0x7fc00000);
+            *reinterpret_cast<uint4*>(qs + pp_place(128, row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      pp_proxy();
+      pp_arrive(q_full + 8 * rt);
     };
     for (begin(); n_pos > 0;) {
       const int steps = piece(), nt = u.rn > 128 ? 2 : 1;
       for (int rt = 0; rt < nt; ++rt) {
-        pp_wait(q_full + 8 * rt, (q_par >> rt) & 1u, failed);
-        q_par ^= 1u << rt;
-        if (rt == 0) pp_wait(k_full + 8 * (kn % PP_STAGES), (kn / PP_STAGES) & 1u, failed);
-        pp_after();
-        scores(rt, kn % PP_STAGES);
-      }
-      pp_commit(k_empty + 8 * (kn % PP_STAGES));
-      ++kn;
-      for (int j = 0; j < steps; ++j) {
-        const uint32_t vs = vn % PP_STAGES, ks = kn % PP_STAGES;
-        const bool more = j + 1 < steps;
-        pp_wait(v_full + 8 * vs, (vn / PP_STAGES) & 1u, failed);
-        for (int rt = 0; rt < nt; ++rt) {
-          pp_wait(p_full + 8 * rt, (p_par >> rt) & 1u, failed);
-          p_par ^= 1u << rt;
-          pp_after();
-#pragma unroll
-          for (int k = 0; k < PP_TOK / 16; ++k)
-            pp_mma_ts(tmem + OUT + HD * rt, tmem + SCORES + 128 * rt + 8 * k, pp_desc(base + S::V0 + vs * S::KV + k * 2048, PP_TOK * 128), IPV,
-                      j > 0 || k > 0);
-          if (more) {
-            if (rt == 0) pp_wait(k_full + 8 * ks, (kn / PP_STAGES) & 1u, failed), pp_after();
-            scores(rt, ks);
-          } else {
-            pp_commit(o_full + 8 * rt);
-          }
-        }
-        pp_commit(v_empty + 8 * vs);
-        ++vn;
-        if (more) pp_commit(k_empty + 8 * ks), ++kn;
+        // the last unit's scores are there, so that its queries are not needed any more, and its softmax has begun
+        pp_wait(q_empty + 8 * rt, (par >> rt) & 1u, failed);
+        load(rt);
+        par ^= 1u << rt, turn ^= 1u << rt;
       }
       next(steps);
     }
+  } else {
+    // ---- MMAs ----
+    constexpr uint32_t IQK = pp_idesc(PP_TOK, false), IPV = pp_idesc(HD, true);
+    auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = uniform(tmem), base = uniform(pp_smem(sm));
+    const uint32_t q_at = pp_desc(base, 16), k_at = pp_desc(base + S::K0, 16), v_at = pp_desc(base + S::V0, PP_TOK * 128);
+    const bool leader = pp_elect();
+    uint32_t kn = 0, vn = 0;                     // steps of keys and values begun
+    uint32_t q_par = 0, p_par = 0, o_par = 3;    // bit rt: parities
+    auto scores = [&](int rt, uint32_t stage, bool last) {
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t at = ((k / 4) * 128 * 128 + (k % 4) * 32) >> 4;
+        pp_mma_ss<IQK>(tm + SCORES + 128 * rt, q_at + rt * (S::Q / 32) + at, k_at + stage * (S::KV / 16) + at, k > 0, leader);
+      }
+      pp_commit(s_full + 8 * rt, leader);
+      if (last) pp_commit(q_empty + 8 * rt, leader);   // the piece's queries have served
+    };
+    auto tiles = [&]() { return uniform(n_pos == 0 ? 0 : u.rn > 128 ? 2 : 1); };
+    auto first_scores = [&](int rt, bool only) {   // of a piece
+      pp_wait(q_full + 8 * rt, (q_par >> rt) & 1u, failed);
+      q_par ^= 1u << rt;
+      if (rt == 0) pp_wait(k_full + 8 * (kn % PP_STAGES), (kn / PP_STAGES) & 1u, failed);
+      pp_after();
+      scores(rt, kn % PP_STAGES, only);
+    };
+    begin();
+    uint32_t steps = n_pos > 0 ? uniform(piece()) : 0, nt = tiles();
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+      if (rt < nt) first_scores(rt, steps == 1);
+    if (nt) pp_commit(k_empty, leader), ++kn;
+    while (nt) {
+      uint32_t more_steps = 0, more = nt;
+      for (uint32_t j = 0; j < steps; ++j) {
+        const uint32_t vs = vn % PP_STAGES, ks = kn % PP_STAGES;
+        const bool last = j + 1 == steps;
+        if (last) {   // the next piece
+          next(steps);
+          more = tiles();
+          more_steps = more ? uniform(piece()) : 0;
+        }
+        pp_wait(v_full + 8 * vs, (vn / PP_STAGES) & 1u, failed);
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+          if (rt < nt) {
+            pp_wait(p_full + 8 * rt, (p_par >> rt) & 1u, failed);
+            p_par ^= 1u << rt;
+            if (j == 0) pp_wait(o_empty + 8 * rt, (o_par >> rt) & 1u, failed), o_par ^= 1u << rt;
+            pp_after();
+#pragma unroll
+            for (int k = 0; k < PP_TOK / 16; ++k)
+              pp_mma_ts<IPV>(tm + OUT + HD * rt, tm + SCORES + 128 * rt + 8 * k, v_at + vs * (S::KV / 16) + k * (2048 / 16), j > 0 || k > 0, leader);
+            if (last) pp_commit(o_full + 8 * rt, leader);
+          }
+          if (rt < more) {
+            if (last) {
+              first_scores(rt, more_steps == 1);
+            } else {
+              if (rt == 0) pp_wait(k_full + 8 * ks, (kn / PP_STAGES) & 1u, failed), pp_after();
+              scores(rt, ks, j + 2 == steps);
+            }
+          }
+        }
+        pp_commit(v_empty + 8 * vs, leader);
+        ++vn;
+        if (more) pp_commit(k_empty + 8 * ks, leader), ++kn;
+      }
+      steps = more_steps, nt = more;
+    }
     // nothing of this CTA's is in flight any more when it gives its TMEM back, also behind a wait that ran out
-    pp_commit(done);
+    pp_commit(done, leader);
     for (const unsigned long long t = pp_ns(); !pp_try(done, 0) && pp_ns() - t < PP_WAIT_NS;) {}
   }
   __syncwarp();
   pp_before();
   __syncthreads();
   pp_after();
-  if (warp == PP_WARPS - 1)
+  if (warp == PP_MMA_WARP)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM) : "memory");
 }
 
