@@ -430,14 +430,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
 #pragma unroll
             for (int k = 0; k < 32; k += 2) m = pp_max3(m, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
           };
-          uint32_t v0[32], v1[32];
-          pp_ld32(v0, sp);
           // (rolled up, here and where the codes are unpacked: with each of the roles' loops straight, warps spent half of
           // their time on instructions that were not there yet)
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            pp_wait_ld(v0), pp_ld32(v1, sp + 32 * c + 32), most(v0, c ? mask[2] : mask[0]);
-            pp_wait_ld(v1), pp_ld32(v0, sp + ((32 * c + 64) & 127)), most(v1, c ? mask[3] : mask[1]);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            pp_ld32(v, sp + 32 * c);
+            pp_wait_ld(v), most(v, c & 2 ? (c & 1 ? mask[3] : mask[2]) : (c & 1 ? mask[1] : mask[0]));
           }
           if (__any_sync(0xffffffffu, m > lim)) {
             const float now = m > lim ? m * sc - PP_SET : ref, al = exp2_approx(ref - now);
@@ -469,11 +468,10 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
             pp_st16(sp + 16 * c, w);
           };
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            pp_wait_ld(v0), pp_ld32(v1, sp + 32 * c + 32), weigh(v0, c, c ? mask[2] : mask[0]);
-            pp_wait_ld(v1);
-            if (c == 0) pp_ld32(v0, sp + 64);
-            weigh(v1, c + 1, c ? mask[3] : mask[1]);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            pp_ld32(v, sp + 32 * c);
+            pp_wait_ld(v), weigh(v, c, c & 2 ? (c & 1 ? mask[3] : mask[2]) : (c & 1 ? mask[1] : mask[0]));
           }
           l += sum.x + sum.y;
           pp_wait_st();
