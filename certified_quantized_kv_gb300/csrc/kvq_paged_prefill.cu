@@ -8,7 +8,7 @@
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1, a row per thread: scores out of TMEM, weights back into it
 //   warps 8-11       keys and values: a token per thread, 4-bit codes to binary16 in shared memory, ahead of their use
 //   warp 12          issues the MMAs: S = Q K^T (operands in shared memory), O += P V (P in TMEM, over half of S's columns)
-//   warps 13-15      the next unit's queries to binary16 in shared memory, as soon as the last scores of this one are there
+//   warp 13          the next unit's queries into shared memory, as soon as the last scores of this one are there
 // The two tiles take turns: while one's scores are turned into weights, the tensor cores work on the other.
 //
 // Unpacking: x^ = o + s code.  Two nibbles at a time are masked into binary16 numbers 1024 + n (or 64 + n), less 1024
@@ -18,11 +18,14 @@
 // order when it is written.  Weights are rounded once to binary16 (2^-11) before their product with the values.  The
 // decode attention keeps both exact, at four times the work per score; here the tensor cores would wait for it.
 //
+// Queries are brought to binary16, in the order that the MMAs take, by a kernel of their own before (a unit's 256 rows
+// would keep a CTA's warps for 10 us), so that one bulk copy per 64 channels moves a tile of them.
+//
 // The softmax reference of a row moves only when a weight would pass 2^15, and is then set so that the largest is
 // 2^10: accumulators in TMEM are rarely rescaled, and small weights stay normal binary16 numbers.
 //
 // The units' steps (128 tokens) are numbered, sequence by sequence, and cut into equal contiguous ranges, one per CTA,
-// whatever the lengths.  A unit within one range is written out directly; the pieces of one that is cut go to the
+// whatever the lengths; a unit counts PP_LEAD more than its steps, for what starting and finishing it takes.  A unit within one range is written out directly; the pieces of one that is cut go to the
 // workspace, and a second kernel merges them in a fixed order, so that results do not depend on timing.
 #include <algorithm>
 #include <cmath>
@@ -44,6 +47,8 @@ struct PpArgs {
   void* out;
   float* lse;
   int4* cut;      // [CTAs] the unit that a CTA begins and leaves: sequence, tile, KV head, pieces (0: none)
+  unsigned char* rows;   // [Hkv][HD / 64][T n_rep] rows of 64 elements in binary16, swizzled
+  float* scales;  // [Hkv][T n_rep] of a row's scores in base 2
   float* part;    // [CTAs][2] pieces of a unit begun in an earlier CTA, and of one that leaves the CTA: [HD + 2][256] floats
   long long qt, qh, table_stride;
   int n_pages, max_pages, T, B, Hq, Hkv, n_rep, window;
@@ -52,10 +57,8 @@ struct PpArgs {
 };
 
 constexpr int PP_ROWS = 256, PP_TOK = 128, PP_STAGES = 2, PP_MAX_BATCH = 2048;
-constexpr int PP_WARPS = 16, PP_THREADS = 32 * PP_WARPS, PP_MMA_WARP = 12, PP_Q_WARPS = 3;
-// Registers: 128 for each thread at launch, of which the softmax warps (a row's 128 scores each) get more: together as many
-constexpr int PP_REGS_SOFTMAX = 160, PP_REGS_UNPACK = 128, PP_REGS_OTHER = 64;
-static_assert(2 * PP_REGS_SOFTMAX + PP_REGS_UNPACK + PP_REGS_OTHER == 4 * 128, "");
+constexpr int PP_WARPS = 14, PP_THREADS = 32 * PP_WARPS, PP_MMA_WARP = 12;
+constexpr int PP_LEAD = 1;
 constexpr float PP_TOP = 15.f, PP_SET = 10.f;             // weights are 2^15 at most, 2^10 when their reference is set
 constexpr unsigned long long PP_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
 
@@ -197,11 +200,6 @@ __device__ __forceinline__ float pp_max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
   return m;
 }
-template <int N>
-__device__ __forceinline__ void pp_more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
-template <int N>
-__device__ __forceinline__ void pp_fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
-
 // ---- 4 bits to binary16 ----
 // Nibbles k and k + 4 of a word as a pair of binary16 numbers 0..15: 1024 + n from the lowest bits of the halves, 64 + n from
 // the next four (whose steps are 1 there), less 1024 or 64
@@ -240,6 +238,77 @@ struct PpSmem {
   static constexpr int bytes(int batch) { return PRE + 8 * (batch + 1) + 1024; }   // (1024: to the swizzle's boundary)
 };
 
+// A (token, query head)'s row: the lanes of HD / 8 hold 16 bytes each.  HBM bound: 67 MB read and written for 8192 tokens of 32
+// heads of 128.
+constexpr int PP_ROW_THREADS = 256;
+template <int HD>
+__global__ void __launch_bounds__(PP_ROW_THREADS) prefill_rows_kernel(PpArgs a) {
+  constexpr int CH = HD / 8, PER = PP_ROW_THREADS / CH, RUN = 4;   // 16-byte pieces of a row; rows at once, and on their way
+  const int c = threadIdx.x % CH;
+  const long long rows = (long long)a.T * a.n_rep, all = rows * a.Hkv;
+  pdl_trigger();
+  pdl_wait();
+  for (long long first = blockIdx.x * (long long)PER * RUN; first < all; first += (long long)gridDim.x * PER * RUN) {
+    const long long x0 = first + threadIdx.x / CH;
+    uint4 v[RUN];
+    int place[RUN];   // a row's number in its chunk, modulo 8 (that of its place in shared memory)
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) {
+      // in the order of memory: tokens, then query heads
+      const long long x = x0 + k * PER;
+      v[k] = make_uint4(0, 0, 0, 0), place[k] = 0;
+      if (x >= all) continue;
+      const int tok = (int)quotient(x, a.Hq), h = (int)(x - (long long)tok * a.Hq);
+      v[k] = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + tok * a.qt + h * a.qh + 8 * c);
+      int b = 0, b1 = a.B;
+      while (b1 - b > 1) {   // the last chunk that starts at tok or before
+        const int m = (b + b1) / 2;
+        if (a.starts[m] <= tok) b = m; else b1 = m;
+      }
+      place[k] = ((tok - min(max(a.starts[b], 0), a.T)) * a.n_rep + h % a.n_rep) & 7;
+    }
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) {
+      const long long x = x0 + k * PER;
+      // the largest bits of an element but its sign: from INF on an infinity or a NaN, with which all of the row's outputs are NaN
+      const uint32_t INF = a.bf16 ? 0x7F80u : 0x7C00u;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, word_of(v[k], i) & 0x7FFF7FFFu);
+#pragma unroll
+      for (int o = 1; o < CH; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = max(mx & 0xffffu, mx >> 16);
+      float sc = fabsf(a.scale_log2);
+      uint32_t w[4];
+      // channels 0, 4, 1, 5, ...: as the keys' nibbles come
+      if (a.bf16) {
+        // the row times 2^e with a largest element in [2^9, 2^10), which binary16 holds down to 2^-34 of it; both powers are
+        // normal fp32 numbers
+        const int e = max(-126, min(126, 136 - (int)(mx >> 7)));
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+        // never 0 or infinite, so that -inf stays -inf and 0 stays 0
+        sc = fminf(fmaxf(sc * down, 1.17549435e-38f), 3.402823466e38f);
+        const float f = a.scale_log2 < 0.f ? -up : up;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t p = word_of(v[k], i / 2), q = word_of(v[k], 2 + i / 2);
+          const float y = __uint_as_float(i & 1 ? p & 0xffff0000u : p << 16), z = __uint_as_float(i & 1 ? q & 0xffff0000u : q << 16);
+          w[i] = h2_as_u32(__floats2half2_rn(y * f, z * f));
+        }
+      } else {
+        const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(word_of(v[k], i / 2), word_of(v[k], 2 + i / 2), i & 1 ? 0x7632 : 0x5410) ^ sign;
+      }
+      if (x >= all) continue;
+      const int tok = (int)quotient(x, a.Hq), h = (int)(x - (long long)tok * a.Hq), g = h / a.n_rep;
+      const long long row = (long long)tok * a.n_rep + h - g * a.n_rep;
+      if (c == 0) a.scales[g * rows + row] = mx < INF ? sc : __int_as_float(0x7fc00000);
+      *reinterpret_cast<uint4*>(a.rows + ((g * (HD / 64) + c / 8) * rows + row) * 128 + (((c & 7) ^ place[k]) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // CTAs among which the steps are cut, and the first step of one of them
 __device__ __forceinline__ int pp_ctas(long long total) { return (int)min((long long)gridDim.x, max(1ll, total)); }
 __device__ __forceinline__ long long pp_cta0(long long total, int c) {
@@ -257,7 +326,6 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   unsigned char* sm = raw_smem + (1024 - (pp_smem(raw_smem) & 1023)) % 1024;
   long long* pre = reinterpret_cast<long long*>(sm + S::PRE);   // [B + 1] steps before each sequence, of one KV head
   __shared__ __align__(8) unsigned long long bars[21];
-  __shared__ float q_scale[2][PP_ROWS];   // of a row's scores in base 2, of two units in turn
   __shared__ uint32_t tmem_at;
   __shared__ int failed_at;
   __shared__ int4 start_at;   // sequence, unit, KV head, step of this CTA's first position
@@ -271,8 +339,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     auto init = [&](uint32_t bar, int count) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory"); };
     for (int k = 0; k < 2; ++k) {
       init(k_full + 8 * k, 128), init(k_empty + 8 * k, 1), init(v_full + 8 * k, 128), init(v_empty + 8 * k, 1);
-      init(q_full + 8 * k, 32 * PP_Q_WARPS), init(o_empty + 8 * k, 128), init(s_full + 8 * k, 1), init(p_full + 8 * k, 128), init(o_full + 8 * k, 1);
-      init(q_empty + 8 * k, 129);
+      init(q_full + 8 * k, 1), init(o_empty + 8 * k, 128), init(s_full + 8 * k, 1), init(p_full + 8 * k, 128), init(o_full + 8 * k, 1);
+      init(q_empty + 8 * k, 1);
     }
     init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -291,7 +359,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     PpUnit u;
     pp_sequence(a, b, u);
     long long sum = 0;
-    for (int t = lane; t < u.tiles; t += 32) pp_unit(a, t, u), sum += u.np;
+    for (int t = lane; t < u.tiles; t += 32) pp_unit(a, t, u), sum += u.np + PP_LEAD;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) pre[b + 1] = sum;
@@ -326,7 +394,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     int t0 = 0;
     for (; t0 < u.tiles; t0 += 32) {
       if (t0 + lane < u.tiles) pp_unit(a, t0 + lane, u);
-      long long inc = t0 + lane < u.tiles ? (long long)u.np * a.Hkv : 0;
+      long long inc = t0 + lane < u.tiles ? (long long)(u.np + PP_LEAD) * a.Hkv : 0;
       const long long mine = inc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -338,7 +406,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         const int src = __ffs(here) - 1;
         if (lane == src) {
           const long long at = in - (inc - mine);
-          start_at = make_int4(b, t0 + lane, (int)(at / u.np), (int)(at % u.np));
+          start_at = make_int4(b, t0 + lane, (int)(at / (u.np + PP_LEAD)), (int)(at % (u.np + PP_LEAD)));
         }
         break;
       }
@@ -352,24 +420,38 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   }
 
   // ---- the walk over this CTA's pieces of units, the same in every role ----
-  int g = start_at.z, p0 = start_at.w;   // KV head, first step within the unit
+  int g = start_at.z, p0 = start_at.w;   // KV head, position within the unit: PP_LEAD, then its steps
   PpUnit u;
+  int s0 = 0, steps = 0, taken = 0;      // first step and steps of the piece (0: no more), its positions
+  auto settle = [&]() {
+    for (steps = 0; n_pos > 0;) {
+      taken = (int)min((long long)(u.np + PP_LEAD - p0), n_pos);
+      s0 = max(0, p0 - PP_LEAD), steps = max(0, p0 + taken - PP_LEAD) - s0;
+      if (steps) return;
+      n_pos = 0;   // (a range that ends within a unit's lead)
+    }
+  };
   auto begin = [&]() {
     if (n_pos == 0) return;
     pp_sequence(a, start_at.x, u);
     pp_unit(a, start_at.y, u);
+    settle();
   };
-  auto piece = [&]() { return (int)min((long long)(u.np - p0), n_pos); };   // steps of the current piece
-  auto next = [&](int steps) {
-    n_pos -= steps;
+  auto next = [&]() {
+    n_pos -= taken;
     p0 = 0;
-    if (n_pos == 0 || ++g < a.Hkv) return;
-    g = 0;
-    if (u.qt + 1 < u.tiles) return pp_unit(a, u.qt + 1, u);
-    int b = u.b + 1;
-    while (b < a.B && pre[b + 1] == pre[b]) ++b;
-    pp_sequence(a, b, u);
-    pp_unit(a, 0, u);
+    if (n_pos > 0 && ++g == a.Hkv) {
+      g = 0;
+      if (u.qt + 1 < u.tiles) {
+        pp_unit(a, u.qt + 1, u);
+      } else {
+        int b = u.b + 1;
+        while (b + 1 < a.B && pre[b + 1] == pre[b]) ++b;
+        pp_sequence(a, b, u);
+        pp_unit(a, 0, u);
+      }
+    }
+    settle();
   };
 
   if (warp < 8) {
@@ -377,24 +459,21 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     const int rt = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's lanes
     const uint32_t sp = lanes + SCORES + 128 * rt, op = lanes + OUT + HD * rt;
-    uint32_t s_par = 0, o_par = 0, q_par = 0;
+    uint32_t s_par = 0, o_par = 0;
     bool cut = false;
-    for (begin(); n_pos > 0;) {
-      const int steps = piece();
+    for (begin(); steps > 0; next()) {
       if (128 * rt < u.rn) {
         const int r = u.r0 + 128 * rt + tid;   // this thread's row
         const bool live = 128 * rt + tid < u.rn;
         const int i = live ? r / a.n_rep : 0, h = g * a.n_rep + (live ? r - i * a.n_rep : 0);
-        pp_wait(q_full + 8 * rt, q_par & 1, failed);
-        const float sc = q_scale[q_par][128 * rt + tid];
-        pp_arrive(q_empty + 8 * rt);   // (so that no warp falls two units behind the queries, whose barrier tells two phases apart)
+        const float sc = live ? a.scales[(long long)g * a.T * a.n_rep + (long long)u.first * a.n_rep + r] : 0.f;
         const int hi = live ? pp_hi(a, u, i) : 0, lo = live ? pp_lo(a, hi) : 0;
         const int hi_all = pp_hi(a, u, (u.r0 + 128 * rt) / a.n_rep);                                       // what every row of the tile sees
         const int lo_all = pp_lo(a, pp_hi(a, u, (u.r0 + min(u.rn, 128 * rt + 128) - 1) / a.n_rep));
         const int32_t* table = a.table + u.b * a.table_stride;
         float ref = -3.402823466e38f, lim = -INFINITY, l = 0.f;   // reference and limit of the scores, sum of weights
         for (int j = 0; j < steps; ++j) {
-          const int t0 = (u.j0 + p0 + j) * PP_TOK;
+          const int t0 = (u.j0 + s0 + j) * PP_TOK;
           // pages outside of the pool are not seen
           uint32_t there = 0;
 #pragma unroll
@@ -485,7 +564,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         pp_after();
         const bool whole = steps == u.np, lost = *failed != 0;
         if (lost) l = __int_as_float(0x7fc00000);
-        float* part = a.part + ((size_t)blockIdx.x * 2 + (p0 == 0)) * (HD + 2) * PP_ROWS + 128 * rt + tid;
+        float* part = a.part + ((size_t)blockIdx.x * 2 + (s0 == 0)) * (HD + 2) * PP_ROWS + 128 * rt + tid;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(u.first + i) * a.Hq + h;
         if (whole) {
@@ -522,16 +601,14 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         }
         pp_before();
         pp_arrive(o_empty + 8 * rt);
-        q_par ^= 1;
       }
-      if (steps < u.np && p0 == 0 && threadIdx.x == 0) {
+      if (steps < u.np && s0 == 0 && threadIdx.x == 0) {
         // pieces: this CTA's and those of the CTAs that its other steps lie in
         const long long total = pre[a.B] * a.Hkv, end = pp_cta0(total, blockIdx.x + 1) + (u.np - steps) - 1;
         const int last = (int)(((end + 1) * pp_ctas(total) - 1) / total);
         a.cut[blockIdx.x] = make_int4(u.b, u.qt, g, last - (int)blockIdx.x + 1);
         cut = true;
       }
-      next(steps);
     }
     if (threadIdx.x == 0 && !cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp < 12) {
@@ -545,17 +622,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     // Three steps are on their way: the page number of the one after the next, the next one's codes, and this one's into
     // shared memory.
     int left = 0, page = -1, head = 0;
-    auto look = [&]() {   // the page of this thread's token in the walk's step, and on
-      page = -1;
-      if (n_pos == 0) return;
-      const int tok = (u.j0 + p0) * PP_TOK + t;
-      if (tok < u.len) page = a.table[u.b * a.table_stride + tok / PG];
+    auto look = [&]() {   // the page of this thread's token in the walk's step, and on; false: there is none
+      if (steps == 0) return false;
+      const int tok = (u.j0 + s0 + steps - left) * PP_TOK + t;
+      page = tok < u.len ? a.table[u.b * a.table_stride + tok / PG] : -1;
       head = g;
-      if (--left > 0) ++p0, --n_pos;
-      else {
-        next(1);
-        if (n_pos > 0) left = piece();
-      }
+      if (--left == 0) next(), left = steps;
+      return true;
     };
     auto fetch = [&](Held& x) {
       const bool in = page >= 0 && page < a.n_pages;
@@ -631,86 +704,40 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
       if (++stage == PP_STAGES) stage = 0, par ^= 1;
     };
     begin();
-    if (n_pos > 0) left = piece();
+    left = steps;
     Held x, y;
-    long long todo = n_pos;
-    look();
-    if (todo > 0) fetch(y), look();
+    bool has = look(), more = false;
+    if (has) fetch(y), more = look();
 #pragma unroll 1
-    for (; todo > 0; --todo) {
+    while (has) {
       x = y;
-      if (todo > 1) fetch(y), look();
+      has = more;
+      if (more) fetch(y), more = look();
       put(x);
     }
   } else if (warp > PP_MMA_WARP) {
     // ---- queries ----
-    uint32_t par = 3, turn = 0;   // bit rt: parity of the wait for the tile's last scores, and of its units
-    // CH lanes hold a row, 16 bytes each; a warp takes RUN groups of rows at once, whose loads are on their way together
-    constexpr int PER = 32 / CH, RUN = 8;
-    const int c = lane % CH;
-    auto load = [&](int rt) {
-      unsigned char* qs = sm + rt * (S::Q / 2);
-      for (int row0 = (warp - PP_MMA_WARP - 1) * PER + lane / CH; row0 < 128; row0 += PP_Q_WARPS * PER * RUN) {
-        uint4 v[RUN];
+    if (lane == 0) {
+      const long long rows = (long long)a.T * a.n_rep;
+      uint32_t par = 0, used = 0;   // bit rt: parity of the tile's copies, whether there was one
+      for (begin(); steps > 0; next())
+        for (int rt = 0; rt < (u.rn > 128 ? 2 : 1); ++rt) {
+          // the last unit's scores are there, so that its queries are not needed any more
+          pp_wait(q_empty + 8 * rt, ((par >> rt) & 1u) ^ 1u, failed);
+          const uint32_t bytes = 128u * min(128, u.rn - 128 * rt);
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(q_full + 8 * rt), "r"(bytes * (HD / 64)) : "memory");
 #pragma unroll
-        for (int x = 0; x < RUN; ++x) {
-          const int row = row0 + x * PP_Q_WARPS * PER, r = u.r0 + 128 * rt + row, i = r / a.n_rep, h = g * a.n_rep + r - i * a.n_rep;
-          v[x] = make_uint4(0, 0, 0, 0);
-          if (row < 128 && 128 * rt + row < u.rn)
-            v[x] = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + (u.first + i) * a.qt + h * a.qh + 8 * c);
+          for (int k = 0; k < HD / 64; ++k)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                         :: "r"(pp_smem(sm) + rt * (S::Q / 2) + k * 128 * 128),
+                            "l"(a.rows + ((g * (HD / 64) + k) * rows + (long long)u.first * a.n_rep + u.r0 + 128 * rt) * 128), "r"(bytes), "r"(q_full + 8 * rt)
+                         : "memory");
+          par ^= 1u << rt, used |= 1u << rt;
         }
-#pragma unroll
-        for (int x = 0; x < RUN; ++x) {
-          const int row = row0 + x * PP_Q_WARPS * PER;
-          // the largest bits of an element but its sign: from INF on an infinity or a NaN, with which all of the row's
-          // outputs are NaN
-          const uint32_t INF = a.bf16 ? 0x7F80u : 0x7C00u;
-          uint32_t mx = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, word_of(v[x], k) & 0x7FFF7FFFu);
-#pragma unroll
-          for (int o = 1; o < CH; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          mx = max(mx & 0xffffu, mx >> 16);
-          float sc = fabsf(a.scale_log2);
-          uint32_t w[4];
-          // channels 0, 4, 1, 5, ...: as the keys' nibbles come
-          if (a.bf16) {
-            // the row times 2^e with a largest element in [2^9, 2^10), which binary16 holds down to 2^-34 of it; both powers
-            // are normal fp32 numbers
-            const int e = max(-126, min(126, 136 - (int)(mx >> 7)));
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
-            // never 0 or infinite, so that -inf stays -inf and 0 stays 0
-            sc = fminf(fmaxf(sc * down, 1.17549435e-38f), 3.402823466e38f);
-            const float f = a.scale_log2 < 0.f ? -up : up;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t p = word_of(v[x], k / 2), q = word_of(v[x], 2 + k / 2);
-              const float y = __uint_as_float(k & 1 ? p & 0xffff0000u : p << 16), z = __uint_as_float(k & 1 ? q & 0xffff0000u : q << 16);
-              w[k] = h2_as_u32(__floats2half2_rn(y * f, z * f));
-            }
-          } else {
-            const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = __byte_perm(word_of(v[x], k / 2), word_of(v[x], 2 + k / 2), k & 1 ? 0x7632 : 0x5410) ^ sign;
-          }
-          if (row < 128) {
-            if (c == 0) q_scale[(turn >> rt) & 1u][128 * rt + row] = mx < INF ? sc : __int_as_float(0x7fc00000);
-            *reinterpret_cast<uint4*>(qs + pp_place(128, row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      pp_proxy();
-      pp_arrive(q_full + 8 * rt);
-    };
-    for (begin(); n_pos > 0;) {
-      const int steps = piece(), nt = u.rn > 128 ? 2 : 1;
-      for (int rt = 0; rt < nt; ++rt) {
-        // the last unit's scores are there, so that its queries are not needed any more, and its softmax has begun
-        pp_wait(q_empty + 8 * rt, (par >> rt) & 1u, failed);
-        load(rt);
-        par ^= 1u << rt, turn ^= 1u << rt;
-      }
-      next(steps);
+      // (nothing is on its way when the CTA ends, also behind a wait that ran out)
+      for (int rt = 0; rt < 2; ++rt)
+        if ((used >> rt) & 1u)
+          for (const unsigned long long t = pp_ns(); !pp_try(q_full + 8 * rt, ((par >> rt) & 1u) ^ 1u) && pp_ns() - t < PP_WAIT_NS;) {}
     }
   } else {
     // ---- MMAs ----
@@ -730,7 +757,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
       pp_commit(s_full + 8 * rt, leader);
       if (last) pp_commit(q_empty + 8 * rt, leader);   // the piece's queries have served
     };
-    auto tiles = [&]() { return uniform(n_pos == 0 ? 0 : u.rn > 128 ? 2 : 1); };
+    auto tiles = [&]() { return uniform(steps == 0 ? 0 : u.rn > 128 ? 2 : 1); };
     auto first_scores = [&](int rt, bool only) {   // of a piece
       pp_wait(q_full + 8 * rt, (q_par >> rt) & 1u, failed);
       q_par ^= 1u << rt;
@@ -739,20 +766,20 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
       scores(rt, kn % PP_STAGES, only);
     };
     begin();
-    uint32_t steps = n_pos > 0 ? uniform(piece()) : 0, nt = tiles();
+    uint32_t now = uniform(steps), nt = tiles();
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
-      if (rt < nt) first_scores(rt, steps == 1);
+      if (rt < nt) first_scores(rt, now == 1);
     if (nt) pp_commit(k_empty, leader), ++kn;
     while (nt) {
-      uint32_t more_steps = 0, more = nt;
-      for (uint32_t j = 0; j < steps; ++j) {
+      uint32_t then = 0, more = nt;
+      for (uint32_t j = 0; j < now; ++j) {
         const uint32_t vs = vn % PP_STAGES, ks = kn % PP_STAGES;
-        const bool last = j + 1 == steps;
+        const bool last = j + 1 == now;
         if (last) {   // the next piece
-          next(steps);
+          next();
           more = tiles();
-          more_steps = more ? uniform(piece()) : 0;
+          then = uniform(steps);
         }
         pp_wait(v_full + 8 * vs, (vn / PP_STAGES) & 1u, failed);
 #pragma unroll
@@ -769,10 +796,10 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
           }
           if (rt < more) {
             if (last) {
-              first_scores(rt, more_steps == 1);
+              first_scores(rt, then == 1);
             } else {
               if (rt == 0) pp_wait(k_full + 8 * ks, (kn / PP_STAGES) & 1u, failed), pp_after();
-              scores(rt, ks, j + 2 == steps);
+              scores(rt, ks, j + 2 == now);
             }
           }
         }
@@ -780,7 +807,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         ++vn;
         if (more) pp_commit(k_empty + 8 * ks, leader), ++kn;
       }
-      steps = more_steps, nt = more;
+      now = then, nt = more;
     }
     // nothing of this CTA's is in flight any more when it gives its TMEM back, also behind a wait that ran out
     pp_commit(done, leader);
@@ -856,13 +883,20 @@ const char* pp_shape_error(int T, int B, int Hq, int Hkv, int hd) {
 }
 
 size_t pp_cut_bytes(int sms) { return ((size_t)sms * sizeof(int4) + 255) / 256 * 256; }
-size_t pp_bytes(int sms, int hd) { return pp_cut_bytes(sms) + (size_t)sms * 2 * (hd + 2) * PP_ROWS * sizeof(float); }
+size_t pp_part_bytes(int sms, int hd) { return (size_t)sms * 2 * (hd + 2) * PP_ROWS * sizeof(float); }   // (a multiple of 1024)
+size_t pp_rows_bytes(int T, int Hq, int hd) { return (size_t)T * Hq * hd * 2; }
+size_t pp_bytes(int sms, int T, int Hq, int hd) {
+  return pp_cut_bytes(sms) + pp_part_bytes(sms, hd) + pp_rows_bytes(T, Hq, hd) + (size_t)T * Hq * sizeof(float);
+}
 
 template <int HD>
 cudaError_t pp_launch(const PpArgs& a, int sms, cudaStream_t st) {
   auto* k = paged_prefill_kernel<HD>;
   // the limit belongs to the function and is every host thread's: always the one of the largest batch
   if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PpSmem<HD>::bytes(PP_MAX_BATCH))) return e;
+  const long long all = ((long long)a.T * a.Hq + PP_ROW_THREADS * 8 / HD * 4 - 1) / (PP_ROW_THREADS * 8 / HD * 4);
+  if (cudaError_t e = launch_dependent(prefill_rows_kernel<HD>, dim3((unsigned)std::min<long long>(all, sms * 32)), dim3(PP_ROW_THREADS), 0, st, a))
+    return e;
   if (cudaError_t e = launch_dependent(k, dim3(sms), dim3(PP_THREADS), PpSmem<HD>::bytes(a.B), st, a)) return e;
   return launch_dependent(prefill_merge_kernel<HD>, dim3(sms, PP_ROWS / 32), dim3(PP_MERGE_THREADS), 0, st, a);
 }
@@ -898,14 +932,17 @@ kvq_status prefill_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   if (lse)
     if (kvq_status s = check_buffer(lse, dev, 4, fn, "lse")) return s;
   if (kvq_status s = check_buffer(workspace, dev, 16, fn, "workspace")) return s;
-  if (workspace_bytes < pp_bytes(sms, hd)) return bad("workspace smaller than kvq_paged_prefill_workspace reports");
+  if (workspace_bytes < pp_bytes(sms, T, Hq, hd)) return bad("workspace smaller than kvq_paged_prefill_workspace reports");
   PpArgs a = {};
   a.q = q, a.pages = static_cast<const unsigned char*>(pages), a.starts = starts, a.table = table, a.lens = lens, a.out = out;
   a.lse = lse, a.qt = qt, a.qh = qh, a.table_stride = table_stride, a.n_pages = n_pages, a.max_pages = max_pages, a.T = T, a.B = B;
   a.Hq = Hq, a.Hkv = Hkv, a.n_rep = Hq / Hkv, a.window = std::min(window, 1 << 30), a.scale_log2 = scale_log2;
   a.bf16 = dtype == KVQ_BF16, a.causal = causal != 0;
   a.cut = static_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp_cut_bytes(sms));
+  unsigned char* ws = static_cast<unsigned char*>(workspace) + pp_cut_bytes(sms);
+  a.part = reinterpret_cast<float*>(ws);
+  a.rows = ws + pp_part_bytes(sms, hd);
+  a.scales = reinterpret_cast<float*>(a.rows + pp_rows_bytes(T, Hq, hd));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = hd == 128 ? pp_launch<128>(a, sms, st) : pp_launch<64>(a, sms, st);
   if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
@@ -928,7 +965,7 @@ extern "C" kvq_status kvq_paged_prefill_workspace(int n_tokens, int batch, int n
     cudaGetLastError();
     return kvq::paged_cuda_fail(e, fn, "no current CUDA device");
   }
-  *bytes = kvq::pp_bytes(sms, head_dim);
+  *bytes = kvq::pp_bytes(sms, n_tokens, n_q_heads, head_dim);
   return KVQ_OK;
 } catch (...) {
   return KVQ_ERR_HOST_OOM;
