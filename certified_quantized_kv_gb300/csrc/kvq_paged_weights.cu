@@ -10,11 +10,12 @@
 // so that scores are fp32 sums of exact products.  Tokens are MMA rows and query rows its columns: a lane holds two
 // tokens of each 16, and their sums over all query rows stay in its registers.
 //
-// The (sequence, KV head, page) units are numbered in that order and cut into equal contiguous ranges, one per CTA,
-// whatever the lengths.  For each (sequence, KV head) of its range a CTA brings up to 128 query rows to binary16 in
+// The (sequence, KV head, page) units are numbered in that order and cut into equal contiguous ranges, one per CTA and
+// SM, whatever the lengths.  For each (sequence, KV head) of its range a CTA brings up to 128 query rows to binary16 in
 // shared memory, in the order in which lanes take them (times a power of two per row, as in the attention); each warp
-// then takes whole pages: their keys go into registers once and the rows' tiles pass by.  Further rows are added to
-// what the first ones left.  Every sum has one owner and a fixed order.
+// then takes whole pages, which bulk copies bring into a ring of its own two ahead, across the heads' borders too: half
+// a page's codes are masked into MMA operands once, and the rows' tiles pass by.  Further rows are added to what the
+// first ones left.  Every sum has one owner and a fixed order.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -29,7 +30,15 @@ namespace {
 
 constexpr int PW_ROWS = 8;            // query rows of a tile (MMA columns)
 constexpr int PW_TILES = 16;          // tiles in shared memory at once
-constexpr int PW_THREADS = 256, PW_WARPS = PW_THREADS / 32, PW_MAX_BATCH = 2048;
+constexpr int PW_THREADS = 384, PW_WARPS = PW_THREADS / 32, PW_MAX_BATCH = 2048;
+constexpr int PW_STAGES = 2;          // pages on their way per warp
+constexpr unsigned long long PW_WAIT_NS = 2000000000ull;   // bounded waits: 2 s
+
+// A page's keys in a stage: the codes, then scales and offsets
+template <int HD>
+struct PwStage {
+  static constexpr int KS = Page<HD>::CODES, KO = KS + Page<HD>::SCALES, BYTES = KO + Page<HD>::SCALES;
+};
 
 // One tile of query rows as the main kernel takes it.
 template <int HD>
@@ -129,16 +138,43 @@ __device__ __forceinline__ void pw_rows(const PwArgs& a, int b, int g, int rt, i
   }
 }
 
+__device__ __forceinline__ bool pw_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool pw_wait_slow(uint32_t bar, uint32_t parity) {
+  unsigned long long t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  while (!pw_try(bar, parity)) {
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > PW_WAIT_NS) return false;
+  }
+  return true;
+}
+
 template <int HD>
-__global__ void __launch_bounds__(PW_THREADS, 2) paged_weights_kernel(PwArgs a) {
+__global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) {
   using L = Page<HD>;
+  using St = PwStage<HD>;
   constexpr int G = L::G;
   constexpr int STEP = 2;   // tiles of 16 tokens at once
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-  __shared__ PwTile<HD> tiles[PW_TILES];
-  __shared__ int pre[PW_MAX_BATCH + 1];   // pages before each sequence, of one KV head
+  extern __shared__ __align__(128) unsigned char sm[];
+  PwTile<HD>* tiles = reinterpret_cast<PwTile<HD>*>(sm + PW_WARPS * PW_STAGES * St::BYTES);
+  int* pre = reinterpret_cast<int*>(tiles + PW_TILES);   // [B + 1] pages before each sequence, of one KV head
+  __shared__ __align__(8) unsigned long long bars[PW_WARPS][PW_STAGES];
   __shared__ int wsum[PW_WARPS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  unsigned char* ring = sm + warp * PW_STAGES * St::BYTES;
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring), bar_s = (uint32_t)__cvta_generic_to_shared(&bars[warp][0]);
+  if (lane == 0) {
+    for (int k = 0; k < PW_STAGES; ++k) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(bar_s + 8 * k) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   pdl_trigger();
   pdl_wait();
   if (threadIdx.x == 0) pre[0] = 0;
@@ -162,57 +198,130 @@ __global__ void __launch_bounds__(PW_THREADS, 2) paged_weights_kernel(PwArgs a) 
     __syncthreads();
   }
   const long long total = (long long)pre[a.B] * a.Hkv;
-  const long long x1 = quotient((blockIdx.x + 1) * total, gridDim.x);
-  long long x = quotient(blockIdx.x * total, gridDim.x);
-  int b = 0;
-  while (x < x1) {
-    // the sequence, KV head and page of unit x, and the end of this CTA's pages of that head
-    int b1 = a.B;
-    while (b1 - b > 1) {   // the last sequence that starts at x or before
-      const int m = (b + b1) / 2;
-      if ((long long)pre[m] * a.Hkv <= x) b = m; else b1 = m;
-    }
+  const long long x0 = quotient(blockIdx.x * total, gridDim.x), x1 = quotient((blockIdx.x + 1) * total, gridDim.x);
+  if (x0 == x1) return;
+
+  // The part of this CTA's range that lies in one (sequence, KV head): units [x, x + pages)
+  struct Part {
+    long long x;
+    int b, g, page0, pages;
+  };
+  auto part_at = [&](long long x, int b) {   // b: a sequence at or before x's
+    Part p;
+    while ((long long)pre[b + 1] * a.Hkv <= x) ++b;
     const int np = pre[b + 1] - pre[b];
     const long long in = x - (long long)pre[b] * a.Hkv;
-    const int g = (int)quotient(in, np), page0 = (int)(in - (long long)g * np), page1 = (int)min((long long)np, page0 + (x1 - x));
-    x += page1 - page0;
-    const int n = pw_len(a, b), first = a.window ? max(0, n - a.Q + 1 - a.window) : 0;   // tokens before it no query sees
+    p.x = x, p.b = b, p.g = (int)quotient(in, np), p.page0 = (int)(in - (long long)p.g * np);
+    p.pages = (int)min((long long)(np - p.page0), x1 - x);
+    return p;
+  };
+  auto first_of = [&](int n) { return a.window ? max(0, n - a.Q + 1 - a.window) : 0; };   // tokens before it no query sees
+  int b0 = 0;
+  for (int b1 = a.B; b1 - b0 > 1;) {   // the last sequence that starts at x0 or before
+    const int m = (b0 + b1) / 2;
+    if ((long long)pre[m] * a.Hkv <= x0) b0 = m; else b1 = m;
+  }
+  const int chunks = (a.RT + PW_TILES - 1) / PW_TILES;
+
+  // ---- copies, two pages ahead of their use: parts, then chunks of rows, then this warp's pages ----
+  Part ahead = part_at(x0, b0);
+  int at_chunk = 0, at_page = warp, issued = 0, found = -1;
+  bool failed = false, more = true;
+  uint32_t valid = 0;   // bit k: stage k holds a page that is seen
+  auto look = [&]() {   // the number of the walk's page (-1: none that is seen)
+    while (at_page >= ahead.pages) {
+      at_page = warp;
+      if (++at_chunk < chunks) continue;
+      at_chunk = 0;
+      if (ahead.x + ahead.pages >= x1) {
+        more = false;
+        return;
+      }
+      ahead = part_at(ahead.x + ahead.pages, ahead.b);
+    }
+    const int page = ahead.page0 + at_page;
+    found = a.table[ahead.b * a.table_stride + page];
+    if (found < 0 || found >= a.n_pages || (page + 1) * PG <= first_of(pw_len(a, ahead.b))) found = -1;
+  };
+  look();
+  auto issue = [&]() {   // into the next stage, and look up the page after
+    const int k = ring_stage<PW_STAGES>(issued);
+    ++issued;
+    valid = found >= 0 ? valid | 1u << k : valid & ~(1u << k);
+    if (lane == 0) {
+      const uint32_t bar = bar_s + 8 * k, to = ring_s + k * St::BYTES;
+      if (found >= 0) {
+        const unsigned char* pg = a.pages + ((size_t)found * a.Hkv + ahead.g) * L::BYTES;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(St::BYTES) : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     :: "r"(to), "l"(pg), "r"(L::CODES), "r"(bar) : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     :: "r"(to + St::KS), "l"(pg + L::KS), "r"(2 * L::SCALES), "r"(bar) : "memory");
+      } else {
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+      }
+    }
+    at_page += PW_WARPS;
+    look();
+  };
+  for (int k = 0; k < PW_STAGES; ++k)
+    if (more) issue();
+
+  int used = 0;
+  for (Part p = part_at(x0, b0);; p = part_at(p.x + p.pages, p.b)) {
+    const int n = pw_len(a, p.b);
     for (int rt0 = 0; rt0 < a.RT; rt0 += PW_TILES) {
       const int nt = min(PW_TILES, a.RT - rt0);
       __syncthreads();   // the tiles' last readers are done
-      for (int k = warp; k < nt; k += PW_WARPS) pw_rows<HD>(a, b, g, rt0 + k, n, tiles[k]);
+      for (int k = warp; k < nt; k += PW_WARPS) pw_rows<HD>(a, p.b, p.g, rt0 + k, n, tiles[k]);
       __syncthreads();
-      for (int page = page0 + warp; page < page1; page += PW_WARPS) {
-        const int tok0 = page * PG;
-        float* w = a.weights + b * a.ws + g * a.wh + tok0;
-        const int at = a.table[b * a.table_stride + page];
-        const bool seen = at >= 0 && at < a.n_pages && tok0 + PG > first;
-        const unsigned char* pg = a.pages + ((size_t)(seen ? at : 0) * a.Hkv + g) * L::BYTES;
-        // (half a page at a time: a whole one's codes and scales leave too few registers)
-#pragma unroll 1
-        for (int i0 = 0; i0 < 64; i0 += 16 * STEP) {
-          float sum[STEP][2];
+      for (int page = warp; page < p.pages; page += PW_WARPS) {
+        const int tok0 = (p.page0 + page) * PG;
+        float* w = a.weights + p.b * a.ws + p.g * a.wh + tok0;
+        float old[8];   // what is there, for the lanes that write (decay 0 does not read it)
 #pragma unroll
-          for (int i = 0; i < STEP; ++i) sum[i][0] = sum[i][1] = 0.f;
+        for (int k = 0; k < 8; ++k) old[k] = (rt0 || a.decay != 0.f) && tig == 0 && tok0 + 8 * k + gid < n ? w[8 * k + gid] : 0.f;
+        const int stage = ring_stage<PW_STAGES>(used);
+        const unsigned char* pg = ring + stage * St::BYTES;
+        const uint32_t parity = ring_parity<PW_STAGES>(used);
+        ++used;
+        if (!failed && !pw_try(bar_s + 8 * stage, parity)) failed = !pw_wait_slow(bar_s + 8 * stage, parity);
+        failed = __any_sync(0xffffffffu, failed);
+        const bool seen = (valid >> stage) & 1u;
+        // whether some row does not see all of the page
+        const bool edge = tok0 + PG > n - a.Q + 1 || (a.window && tok0 < n - a.window);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 4; i0 += STEP) {
+          float2 sum[STEP][2];   // tokens gid and gid + 8 of a tile; the even and the odd columns
+#pragma unroll
+          for (int i = 0; i < STEP; ++i) sum[i][0] = sum[i][1] = make_float2(0.f, 0.f);
           if (seen) {
-            uint32_t code[STEP][2][G], sc[STEP][2][G / 2], off[STEP][2];
+            uint32_t low[STEP][G][4], high[STEP][G][4], off[STEP][2];
+            float sc[STEP][2][G];
 #pragma unroll
             for (int i = 0; i < STEP; ++i)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const int t = i0 + 16 * i + 8 * k + gid;
-                const unsigned char* c = pg + t * L::ROW + tig * 4 * G;
+                const int t = 16 * (i0 + i) + 8 * k + gid;
+                uint32_t c[G], h[G / 2];
                 if constexpr (G == 4) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(c);
-                  code[i][k][0] = v.x, code[i][k][1] = v.y, code[i][k][2] = v.z, code[i][k][3] = v.w;
-                  const uint2 s = *reinterpret_cast<const uint2*>(pg + L::KS + t * 2 * G);
-                  sc[i][k][0] = s.x, sc[i][k][1] = s.y;
+                  const uint4 v = *reinterpret_cast<const uint4*>(pg + t * L::ROW + tig * 4 * G);
+                  c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+                  const uint2 y = *reinterpret_cast<const uint2*>(pg + St::KS + t * 2 * G);
+                  h[0] = y.x, h[1] = y.y;
                 } else {
-                  const uint2 v = *reinterpret_cast<const uint2*>(c);
-                  code[i][k][0] = v.x, code[i][k][1] = v.y;
-                  sc[i][k][0] = *reinterpret_cast<const uint32_t*>(pg + L::KS + t * 2 * G);
+                  const uint2 v = *reinterpret_cast<const uint2*>(pg + t * L::ROW + tig * 4 * G);
+                  c[0] = v.x, c[1] = v.y;
+                  h[0] = *reinterpret_cast<const uint32_t*>(pg + St::KS + t * 2 * G);
                 }
-                off[i][k] = *reinterpret_cast<const uint32_t*>(pg + L::KO + t * 2 * G + 4 * (tig % (G / 2)));
+                off[i][k] = *reinterpret_cast<const uint32_t*>(pg + St::KO + t * 2 * G + 4 * (tig % (G / 2)));
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                  low[i][g][k] = c[g] & LO, low[i][g][2 + k] = (c[g] >> 8) & LO;
+                  high[i][g][k] = c[g] & HI, high[i][g][2 + k] = (c[g] >> 8) & HI;
+                  const float2 f = __half22float2(u32_as_h2(h[g / 2]));
+                  sc[i][k][g] = g & 1 ? f.y : f.x;
+                }
               }
 #pragma unroll 1
             for (int rt = 0; rt < nt; ++rt) {
@@ -222,32 +331,34 @@ __global__ void __launch_bounds__(PW_THREADS, 2) paged_weights_kernel(PwArgs a) 
               for (int k = 0; k < G; ++k) q[k] = T.q[k][lane];
               const uint32_t qo = T.o[lane];
               const float2 scale = *reinterpret_cast<const float2*>(T.scale + 2 * tig), lse = *reinterpret_cast<const float2*>(T.lse + 2 * tig);
-              const int2 lo = *reinterpret_cast<const int2*>(T.lo + 2 * tig), hi = *reinterpret_cast<const int2*>(T.hi + 2 * tig);
+              const float2 minus = make_float2(-lse.x, -lse.y);
 #pragma unroll
               for (int i = 0; i < STEP; ++i) {
-                float r[4];
+                float2 r[2];   // of the tile's two tokens, two columns each
 #pragma unroll
-                for (int k = 0; k < G; ++k) {
-                  const uint32_t x = code[i][0][k], y = code[i][1][k];
-                  const uint32_t low[4] = {x & LO, y & LO, (x >> 8) & LO, (y >> 8) & LO};
-                  const uint32_t high[4] = {x & HI, y & HI, (x >> 8) & HI, (y >> 8) & HI};
+                for (int g = 0; g < G; ++g) {
                   float X[4];
-                  pw_mma_z(X, low, q[k].x, q[k].y);
-                  pw_mma(X, high, q[k].z, q[k].w);
-                  const float2 sa = __half22float2(u32_as_h2(sc[i][0][k / 2])), sb = __half22float2(u32_as_h2(sc[i][1][k / 2]));
-                  const float fa = k & 1 ? sa.y : sa.x, fb = k & 1 ? sb.y : sb.x;
+                  pw_mma_z(X, low[i][g], q[g].x, q[g].y);
+                  pw_mma(X, high[i][g], q[g].z, q[g].w);
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) r[j] = k == 0 ? X[j] * (j < 2 ? fa : fb) : fmaf(X[j], j < 2 ? fa : fb, r[j]);
+                  for (int k = 0; k < 2; ++k) {
+                    const float2 x = make_float2(X[2 * k], X[2 * k + 1]), f = make_float2(sc[i][k][g], sc[i][k][g]);
+                    r[k] = g == 0 ? mul2(x, f) : fma2(x, f, r[k]);
+                  }
                 }
                 float O[4];
                 pw_mma_k8_z(O, off[i][0], off[i][1], qo);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int t = tok0 + i0 + 16 * i + 8 * (j >> 1) + gid;
-                  const float s = fmaf(r[j], NIB_ROW_SCALE_LO, O[j]);
-                  const float p = exp2_approx(fmaf(s, j & 1 ? scale.y : scale.x, -(j & 1 ? lse.y : lse.x)));
-                  const bool in = t >= (j & 1 ? lo.y : lo.x) && t < (j & 1 ? hi.y : hi.x);
-                  sum[i][j >> 1] += in ? p : 0.f;
+                for (int k = 0; k < 2; ++k) {
+                  const float2 s = fma2(r[k], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[2 * k], O[2 * k + 1]));
+                  const float2 e = fma2(s, scale, minus);
+                  float2 pr = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                  if (edge) {
+                    const int t = tok0 + 16 * (i0 + i) + 8 * k + gid;
+                    const int2 lo = *reinterpret_cast<const int2*>(T.lo + 2 * tig), hi = *reinterpret_cast<const int2*>(T.hi + 2 * tig);
+                    pr = make_float2(t >= lo.x && t < hi.x ? pr.x : 0.f, t >= lo.y && t < hi.y ? pr.y : 0.f);
+                  }
+                  sum[i][k] = add2(sum[i][k], pr);
                 }
               }
             }
@@ -256,17 +367,34 @@ __global__ void __launch_bounds__(PW_THREADS, 2) paged_weights_kernel(PwArgs a) 
           for (int i = 0; i < STEP; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float s = sum[i][k];
+              float s = sum[i][k].x + sum[i][k].y;
               s += __shfl_xor_sync(0xffffffffu, s, 1);
               s += __shfl_xor_sync(0xffffffffu, s, 2);
-              const int t = i0 + 16 * i + 8 * k + gid;
-              // (decay 0 does not read what is there)
-              if (tig == 0 && tok0 + t < n) w[t] = rt0 ? w[t] + s : a.decay == 0.f ? s : fmaf(w[t], a.decay, s);
+              const int t = 16 * (i0 + i) + 8 * k + gid;
+              const float was = i0 ? old[4 + 2 * i + k] : old[2 * i + k];
+              if (failed) s = __int_as_float(0x7fc00000);
+              if (tig == 0 && tok0 + t < n) w[t] = rt0 ? was + s : a.decay == 0.f ? s : fmaf(was, a.decay, s);
             }
         }
+        __syncwarp();   // the stage's last readers are done
+        if (!failed && more) issue();
       }
     }
+    if (p.x + p.pages >= x1) break;
   }
+  if (failed) ring_drain<PW_STAGES>(issued, [&](int k, uint32_t parity) { pw_wait_slow(bar_s + 8 * k, parity); });
+}
+
+template <int HD>
+cudaError_t pw_launch(const PwArgs& a, int sms, cudaStream_t st) {
+  auto bytes = [](int batch) {
+    return PW_WARPS * PW_STAGES * PwStage<HD>::BYTES + PW_TILES * (int)sizeof(PwTile<HD>) + 4 * (batch + 1);
+  };
+  auto* k = paged_weights_kernel<HD>;
+  // the limit belongs to the function and is every host thread's: always the one of the largest batch
+  if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(PW_MAX_BATCH))) return e;
+  // one CTA per SM, fewer when the table cannot hold a page for each
+  return launch_dependent(k, dim3((unsigned)std::min<long long>(sms, (long long)a.B * a.max_pages * a.Hkv)), dim3(PW_THREADS), bytes(a.B), st, a);
 }
 
 const char* pw_shape_error(int B, int Q, int Hq, int Hkv, int hd) {
@@ -316,10 +444,7 @@ kvq_status weights_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int sms = 0;
   if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return paged_cuda_fail(e, fn, "device attributes");
-  // two CTAs per SM, fewer when the table cannot hold a page for each warp
-  const long long most = ((long long)B * a.max_pages * Hkv + PW_WARPS - 1) / PW_WARPS;
-  const dim3 grid((unsigned)std::min<long long>(2 * sms, most));
-  const cudaError_t e = launch_dependent(hd == 128 ? paged_weights_kernel<128> : paged_weights_kernel<64>, grid, dim3(PW_THREADS), 0, st, a);
+  const cudaError_t e = hd == 128 ? pw_launch<128>(a, sms, st) : pw_launch<64>(a, sms, st);
   if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
