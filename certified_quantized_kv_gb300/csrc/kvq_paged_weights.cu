@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   // The part of this CTA's range that lies in one (sequence, KV head): units [x, x + pages)
   struct Part {
     long long x;
-    int b, g, page0, pages;
+    int b, g, page0, pages, n;
+    int warp0;   // the first of its pages that this warp takes (every PW_WARPS-th unit of the CTA's range)
   };
   auto part_at = [&](long long x, int b) {   // b: a sequence at or before x's
     Part p;
@@ -213,6 +214,8 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
     const long long in = x - (long long)pre[b] * a.Hkv;
     p.x = x, p.b = b, p.g = (int)quotient(in, np), p.page0 = (int)(in - (long long)p.g * np);
     p.pages = (int)min((long long)(np - p.page0), x1 - x);
+    p.n = pw_len(a, b);
+    p.warp0 = (warp + PW_WARPS - (int)((x - x0) % PW_WARPS)) % PW_WARPS;
     return p;
   };
   auto first_of = [&](int n) { return a.window ? max(0, n - a.Q + 1 - a.window) : 0; };   // tokens before it no query sees
@@ -225,12 +228,12 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
 
   // ---- copies, two pages ahead of their use: parts, then chunks of rows, then this warp's pages ----
   Part ahead = part_at(x0, b0);
-  int at_chunk = 0, at_page = warp, issued = 0, found = -1;
+  int at_chunk = 0, at_page = ahead.warp0, issued = 0, found = -1;
   bool failed = false, more = true;
   uint32_t valid = 0;   // bit k: stage k holds a page that is seen
   auto look = [&]() {   // the number of the walk's page (-1: none that is seen)
     while (at_page >= ahead.pages) {
-      at_page = warp;
+      at_page = ahead.warp0;
       if (++at_chunk < chunks) continue;
       at_chunk = 0;
       if (ahead.x + ahead.pages >= x1) {
@@ -238,10 +241,11 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
         return;
       }
       ahead = part_at(ahead.x + ahead.pages, ahead.b);
+      at_page = ahead.warp0;
     }
     const int page = ahead.page0 + at_page;
     found = a.table[ahead.b * a.table_stride + page];
-    if (found < 0 || found >= a.n_pages || (page + 1) * PG <= first_of(pw_len(a, ahead.b))) found = -1;
+    if (found < 0 || found >= a.n_pages || (page + 1) * PG <= first_of(ahead.n)) found = -1;
   };
   look();
   auto issue = [&]() {   // into the next stage, and look up the page after
@@ -267,120 +271,150 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   for (int k = 0; k < PW_STAGES; ++k)
     if (more) issue();
 
+  // Rows of several parts at once where there is room for their tiles, so that warps meet once for all of them.
+  const int batch = max(1, PW_TILES / a.RT);
   int used = 0;
-  for (Part p = part_at(x0, b0);; p = part_at(p.x + p.pages, p.b)) {
-    const int n = pw_len(a, p.b);
+  for (Part first = part_at(x0, b0);;) {
+    Part behind = first;   // the part behind the batch
+    int parts = 0;
+    bool end = false;
     for (int rt0 = 0; rt0 < a.RT; rt0 += PW_TILES) {
       const int nt = min(PW_TILES, a.RT - rt0);
       __syncthreads();   // the tiles' last readers are done
-      for (int k = warp; k < nt; k += PW_WARPS) pw_rows<HD>(a, p.b, p.g, rt0 + k, n, tiles[k]);
+      behind = first;
+      for (parts = 0; parts < batch; ++parts) {
+        for (int k = warp; k < nt; k += PW_WARPS) pw_rows<HD>(a, behind.b, behind.g, rt0 + k, behind.n, tiles[parts * nt + k]);
+        if (behind.x + behind.pages >= x1) {
+          ++parts, end = true;
+          break;
+        }
+        behind = part_at(behind.x + behind.pages, behind.b);
+      }
       __syncthreads();
-      for (int page = warp; page < p.pages; page += PW_WARPS) {
-        const int tok0 = (p.page0 + page) * PG;
-        float* w = a.weights + p.b * a.ws + p.g * a.wh + tok0;
-        float old[8];   // what is there, for the lanes that write (decay 0 does not read it)
+      Part p = first;
+      for (int y = 0; y < parts; ++y) {
+        if (y) p = part_at(p.x + p.pages, p.b);
+        const int n = p.n;
+        for (int page = p.warp0; page < p.pages; page += PW_WARPS) {
+          const int tok0 = (p.page0 + page) * PG;
+          float* w = a.weights + p.b * a.ws + p.g * a.wh + tok0;
+          // what is there of this lane's tokens (decay 0 does not read it)
+          float old[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) old[k] = (rt0 || a.decay != 0.f) && tig == 0 && tok0 + 8 * k + gid < n ? w[8 * k + gid] : 0.f;
-        const int stage = ring_stage<PW_STAGES>(used);
-        const unsigned char* pg = ring + stage * St::BYTES;
-        const uint32_t parity = ring_parity<PW_STAGES>(used);
-        ++used;
-        if (!failed && !pw_try(bar_s + 8 * stage, parity)) failed = !pw_wait_slow(bar_s + 8 * stage, parity);
-        failed = __any_sync(0xffffffffu, failed);
-        const bool seen = (valid >> stage) & 1u;
-        // whether some row does not see all of the page
-        const bool edge = tok0 + PG > n - a.Q + 1 || (a.window && tok0 < n - a.window);
+          for (int k = 0; k < 2; ++k) old[k] = (rt0 || a.decay != 0.f) && tok0 + 32 * k + 8 * tig + gid < n ? w[32 * k + 8 * tig + gid] : 0.f;
+          const int stage = ring_stage<PW_STAGES>(used);
+          const unsigned char* pg = ring + stage * St::BYTES;
+          const uint32_t parity = ring_parity<PW_STAGES>(used);
+          ++used;
+          if (!failed && !pw_try(bar_s + 8 * stage, parity)) failed = !pw_wait_slow(bar_s + 8 * stage, parity);
+          failed = __any_sync(0xffffffffu, failed);
+          const bool seen = (valid >> stage) & 1u;
+          // whether some row does not see all of the page
+          const bool edge = tok0 + PG > n - a.Q + 1 || (a.window && tok0 < n - a.window);
+          float mine[8];   // sums of tokens 8k + gid
+#pragma unroll
+          for (int i0 = 0; i0 < 4; i0 += STEP) {
+            float2 sum[STEP][2];   // tokens gid and gid + 8 of a tile; the even and the odd columns
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) sum[i][0] = sum[i][1] = make_float2(0.f, 0.f);
+            if (seen) {
+              uint32_t low[STEP][G][4], high[STEP][G][4], off[STEP][2];
+              float sc[STEP][2][G];
+#pragma unroll
+              for (int i = 0; i < STEP; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int t = 16 * (i0 + i) + 8 * k + gid;
+                  uint32_t c[G], h[G / 2];
+                  if constexpr (G == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(pg + t * L::ROW + tig * 4 * G);
+                    c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+                    const uint2 y = *reinterpret_cast<const uint2*>(pg + St::KS + t * 2 * G);
+                    h[0] = y.x, h[1] = y.y;
+                  } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(pg + t * L::ROW + tig * 4 * G);
+                    c[0] = v.x, c[1] = v.y;
+                    h[0] = *reinterpret_cast<const uint32_t*>(pg + St::KS + t * 2 * G);
+                  }
+                  off[i][k] = *reinterpret_cast<const uint32_t*>(pg + St::KO + t * 2 * G + 4 * (tig % (G / 2)));
+#pragma unroll
+                  for (int g = 0; g < G; ++g) {
+                    low[i][g][k] = c[g] & LO, low[i][g][2 + k] = (c[g] >> 8) & LO;
+                    high[i][g][k] = c[g] & HI, high[i][g][2 + k] = (c[g] >> 8) & HI;
+                    const float2 f = __half22float2(u32_as_h2(h[g / 2]));
+                    sc[i][k][g] = g & 1 ? f.y : f.x;
+                  }
+                }
 #pragma unroll 1
-        for (int i0 = 0; i0 < 4; i0 += STEP) {
-          float2 sum[STEP][2];   // tokens gid and gid + 8 of a tile; the even and the odd columns
+              for (int rt = 0; rt < nt; ++rt) {
+                const PwTile<HD>& T = tiles[y * nt + rt];
+                uint4 q[G];
 #pragma unroll
-          for (int i = 0; i < STEP; ++i) sum[i][0] = sum[i][1] = make_float2(0.f, 0.f);
-          if (seen) {
-            uint32_t low[STEP][G][4], high[STEP][G][4], off[STEP][2];
-            float sc[STEP][2][G];
+                for (int k = 0; k < G; ++k) q[k] = T.q[k][lane];
+                const uint32_t qo = T.o[lane];
+                const float2 scale = *reinterpret_cast<const float2*>(T.scale + 2 * tig), lse = *reinterpret_cast<const float2*>(T.lse + 2 * tig);
+                const float2 minus = make_float2(-lse.x, -lse.y);
+#pragma unroll
+                for (int i = 0; i < STEP; ++i) {
+                  float2 r[2];   // of the tile's two tokens, two columns each
+#pragma unroll
+                  for (int g = 0; g < G; ++g) {
+                    float X[4];
+                    pw_mma_z(X, low[i][g], q[g].x, q[g].y);
+                    pw_mma(X, high[i][g], q[g].z, q[g].w);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                      const float2 x = make_float2(X[2 * k], X[2 * k + 1]), f = make_float2(sc[i][k][g], sc[i][k][g]);
+                      r[k] = g == 0 ? mul2(x, f) : fma2(x, f, r[k]);
+                    }
+                  }
+                  float O[4];
+                  pw_mma_k8_z(O, off[i][0], off[i][1], qo);
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const float2 s = fma2(r[k], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[2 * k], O[2 * k + 1]));
+                    const float2 e = fma2(s, scale, minus);
+                    float2 pr = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                    if (edge) {
+                      const int t = tok0 + 16 * (i0 + i) + 8 * k + gid;
+                      const int2 lo = *reinterpret_cast<const int2*>(T.lo + 2 * tig), hi = *reinterpret_cast<const int2*>(T.hi + 2 * tig);
+                      pr = make_float2(t >= lo.x && t < hi.x ? pr.x : 0.f, t >= lo.y && t < hi.y ? pr.y : 0.f);
+                    }
+                    sum[i][k] = add2(sum[i][k], pr);
+                  }
+                }
+              }
+            }
 #pragma unroll
             for (int i = 0; i < STEP; ++i)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int t = 16 * (i0 + i) + 8 * k + gid;
-                uint32_t c[G], h[G / 2];
-                if constexpr (G == 4) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(pg + t * L::ROW + tig * 4 * G);
-                  c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
-                  const uint2 y = *reinterpret_cast<const uint2*>(pg + St::KS + t * 2 * G);
-                  h[0] = y.x, h[1] = y.y;
-                } else {
-                  const uint2 v = *reinterpret_cast<const uint2*>(pg + t * L::ROW + tig * 4 * G);
-                  c[0] = v.x, c[1] = v.y;
-                  h[0] = *reinterpret_cast<const uint32_t*>(pg + St::KS + t * 2 * G);
-                }
-                off[i][k] = *reinterpret_cast<const uint32_t*>(pg + St::KO + t * 2 * G + 4 * (tig % (G / 2)));
+              for (int k = 0; k < 2; ++k) mine[2 * (i0 + i) + k] = sum[i][k].x + sum[i][k].y;
+          }
+          // over the four lanes with the other columns, each of which ends up with two tokens: 32k + 8 tig + gid
+          float half[4], own[2];
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                  low[i][g][k] = c[g] & LO, low[i][g][2 + k] = (c[g] >> 8) & LO;
-                  high[i][g][k] = c[g] & HI, high[i][g][2 + k] = (c[g] >> 8) & HI;
-                  const float2 f = __half22float2(u32_as_h2(h[g / 2]));
-                  sc[i][k][g] = g & 1 ? f.y : f.x;
-                }
-              }
-#pragma unroll 1
-            for (int rt = 0; rt < nt; ++rt) {
-              const PwTile<HD>& T = tiles[rt];
-              uint4 q[G];
-#pragma unroll
-              for (int k = 0; k < G; ++k) q[k] = T.q[k][lane];
-              const uint32_t qo = T.o[lane];
-              const float2 scale = *reinterpret_cast<const float2*>(T.scale + 2 * tig), lse = *reinterpret_cast<const float2*>(T.lse + 2 * tig);
-              const float2 minus = make_float2(-lse.x, -lse.y);
-#pragma unroll
-              for (int i = 0; i < STEP; ++i) {
-                float2 r[2];   // of the tile's two tokens, two columns each
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                  float X[4];
-                  pw_mma_z(X, low[i][g], q[g].x, q[g].y);
-                  pw_mma(X, high[i][g], q[g].z, q[g].w);
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    const float2 x = make_float2(X[2 * k], X[2 * k + 1]), f = make_float2(sc[i][k][g], sc[i][k][g]);
-                    r[k] = g == 0 ? mul2(x, f) : fma2(x, f, r[k]);
-                  }
-                }
-                float O[4];
-                pw_mma_k8_z(O, off[i][0], off[i][1], qo);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float2 s = fma2(r[k], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[2 * k], O[2 * k + 1]));
-                  const float2 e = fma2(s, scale, minus);
-                  float2 pr = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-                  if (edge) {
-                    const int t = tok0 + 16 * (i0 + i) + 8 * k + gid;
-                    const int2 lo = *reinterpret_cast<const int2*>(T.lo + 2 * tig), hi = *reinterpret_cast<const int2*>(T.hi + 2 * tig);
-                    pr = make_float2(t >= lo.x && t < hi.x ? pr.x : 0.f, t >= lo.y && t < hi.y ? pr.y : 0.f);
-                  }
-                  sum[i][k] = add2(sum[i][k], pr);
-                }
-              }
-            }
+          for (int k = 0; k < 4; ++k) {
+            const float keep = tig & 1 ? mine[2 * k + 1] : mine[2 * k], give = tig & 1 ? mine[2 * k] : mine[2 * k + 1];
+            half[k] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
           }
 #pragma unroll
-          for (int i = 0; i < STEP; ++i)
+          for (int k = 0; k < 2; ++k) {
+            const float keep = tig & 2 ? half[2 * k + 1] : half[2 * k], give = tig & 2 ? half[2 * k] : half[2 * k + 1];
+            own[k] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+          }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float s = sum[i][k].x + sum[i][k].y;
-              s += __shfl_xor_sync(0xffffffffu, s, 1);
-              s += __shfl_xor_sync(0xffffffffu, s, 2);
-              const int t = 16 * (i0 + i) + 8 * k + gid;
-              const float was = i0 ? old[4 + 2 * i + k] : old[2 * i + k];
-              if (failed) s = __int_as_float(0x7fc00000);
-              if (tig == 0 && tok0 + t < n) w[t] = rt0 ? was + s : a.decay == 0.f ? s : fmaf(was, a.decay, s);
-            }
+          for (int k = 0; k < 2; ++k) {
+            const int t = 32 * k + 8 * tig + gid;
+            const float x = failed ? __int_as_float(0x7fc00000) : own[k];
+            if (tok0 + t < n) w[t] = rt0 ? old[k] + x : a.decay == 0.f ? x : fmaf(old[k], a.decay, x);
+          }
+          __syncwarp();   // the stage's last readers are done
+          if (!failed && more) issue();
         }
-        __syncwarp();   // the stage's last readers are done
-        if (!failed && more) issue();
       }
     }
-    if (p.x + p.pages >= x1) break;
+    if (end) break;
+    first = behind;
   }
   if (failed) ring_drain<PW_STAGES>(issued, [&](int k, uint32_t parity) { pw_wait_slow(bar_s + 8 * k, parity); });
 }
