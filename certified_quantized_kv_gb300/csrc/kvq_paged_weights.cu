@@ -11,7 +11,7 @@
 // tokens of each 16, and their sums over all query rows stay in its registers.
 //
 // The (sequence, KV head, page) units are numbered in that order and cut into equal contiguous ranges, one per CTA and
-// SM, whatever the lengths.  For each (sequence, KV head) of its range a CTA brings up to 128 query rows to binary16 in
+// SM, whatever the lengths (each head counts PW_LEAD pages more, for its start).  For each (sequence, KV head) of its range a CTA brings up to 128 query rows to binary16 in
 // shared memory, in the order in which lanes take them (times a power of two per row, as in the attention); each warp
 // then takes whole pages, which bulk copies bring into a ring of its own two ahead, across the heads' borders too: half
 // a page's codes are masked into MMA operands once, and the rows' tiles pass by.  Further rows are added to what the
@@ -30,7 +30,9 @@ namespace {
 
 constexpr int PW_ROWS = 8;            // query rows of a tile (MMA columns)
 constexpr int PW_TILES = 16;          // tiles in shared memory at once
-constexpr int PW_THREADS = 384, PW_WARPS = PW_THREADS / 32, PW_MAX_BATCH = 2048;
+constexpr int PW_THREADS = 512, PW_WARPS = PW_THREADS / 32, PW_MAX_BATCH = 2048;
+// Positions that a (sequence, KV head) takes in the ranges besides its pages, for what starting it costs in pages' time
+constexpr int PW_LEAD = 2;
 constexpr int PW_STAGES = 2;          // pages on their way per warp
 constexpr unsigned long long PW_WAIT_NS = 2000000000ull;   // bounded waits: 2 s
 
@@ -161,11 +163,12 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   using L = Page<HD>;
   using St = PwStage<HD>;
   constexpr int G = L::G;
-  constexpr int STEP = 2;   // tiles of 16 tokens at once
+  constexpr int STEP = 1;   // tiles of 16 tokens at once
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
   extern __shared__ __align__(128) unsigned char sm[];
   PwTile<HD>* tiles = reinterpret_cast<PwTile<HD>*>(sm + PW_WARPS * PW_STAGES * St::BYTES);
-  int* pre = reinterpret_cast<int*>(tiles + PW_TILES);   // [B + 1] pages before each sequence, of one KV head
+  int* pre = reinterpret_cast<int*>(tiles + PW_TILES);   // [B + 1] positions before each sequence, of one KV head
+  int* lens = pre + a.B + 1;                             // [B]
   __shared__ __align__(8) unsigned long long bars[PW_WARPS][PW_STAGES];
   __shared__ int wsum[PW_WARPS];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -180,7 +183,9 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   if (threadIdx.x == 0) pre[0] = 0;
   for (int base = 0, run = 0; base < a.B; base += PW_THREADS) {
     const int b = base + threadIdx.x;
-    int inc = b < a.B ? (pw_len(a, b) + PG - 1) / PG : 0;
+    const int len = b < a.B ? pw_len(a, b) : 0, np = (len + PG - 1) / PG;
+    if (b < a.B) lens[b] = len;
+    int inc = np ? np + PW_LEAD : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -201,9 +206,9 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   const long long x0 = quotient(blockIdx.x * total, gridDim.x), x1 = quotient((blockIdx.x + 1) * total, gridDim.x);
   if (x0 == x1) return;
 
-  // The part of this CTA's range that lies in one (sequence, KV head): units [x, x + pages)
+  // The part of this CTA's range that lies in one (sequence, KV head)
   struct Part {
-    long long x;
+    long long x, end;        // positions
     int b, g, page0, pages, n;
     int warp0;   // the first of its pages that this warp takes (every PW_WARPS-th unit of the CTA's range)
   };
@@ -212,9 +217,11 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
     while ((long long)pre[b + 1] * a.Hkv <= x) ++b;
     const int np = pre[b + 1] - pre[b];
     const long long in = x - (long long)pre[b] * a.Hkv;
-    p.x = x, p.b = b, p.g = (int)quotient(in, np), p.page0 = (int)(in - (long long)p.g * np);
-    p.pages = (int)min((long long)(np - p.page0), x1 - x);
-    p.n = pw_len(a, b);
+    p.x = x, p.b = b, p.g = (int)quotient(in, np);
+    const int at = (int)(in - (long long)p.g * np), taken = (int)min((long long)(np - at), x1 - x);
+    p.end = x + taken;
+    p.page0 = max(0, at - PW_LEAD), p.pages = max(0, at + taken - PW_LEAD) - p.page0;
+    p.n = lens[b];
     p.warp0 = (warp + PW_WARPS - (int)((x - x0) % PW_WARPS)) % PW_WARPS;
     return p;
   };
@@ -236,11 +243,11 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
       at_page = ahead.warp0;
       if (++at_chunk < chunks) continue;
       at_chunk = 0;
-      if (ahead.x + ahead.pages >= x1) {
+      if (ahead.end >= x1) {
         more = false;
         return;
       }
-      ahead = part_at(ahead.x + ahead.pages, ahead.b);
+      ahead = part_at(ahead.end, ahead.b);
       at_page = ahead.warp0;
     }
     const int page = ahead.page0 + at_page;
@@ -283,17 +290,19 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
       __syncthreads();   // the tiles' last readers are done
       behind = first;
       for (parts = 0; parts < batch; ++parts) {
-        for (int k = warp; k < nt; k += PW_WARPS) pw_rows<HD>(a, behind.b, behind.g, rt0 + k, behind.n, tiles[parts * nt + k]);
-        if (behind.x + behind.pages >= x1) {
+        // tile k of part y is number y nt + k, one warp's each
+        for (int k = (warp + PW_WARPS - parts * nt % PW_WARPS) % PW_WARPS; k < nt; k += PW_WARPS)
+          pw_rows<HD>(a, behind.b, behind.g, rt0 + k, behind.n, tiles[parts * nt + k]);
+        if (behind.end >= x1) {
           ++parts, end = true;
           break;
         }
-        behind = part_at(behind.x + behind.pages, behind.b);
+        behind = part_at(behind.end, behind.b);
       }
       __syncthreads();
       Part p = first;
       for (int y = 0; y < parts; ++y) {
-        if (y) p = part_at(p.x + p.pages, p.b);
+        if (y) p = part_at(p.end, p.b);
         const int n = p.n;
         for (int page = p.warp0; page < p.pages; page += PW_WARPS) {
           const int tok0 = (p.page0 + page) * PG;
@@ -422,7 +431,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
 template <int HD>
 cudaError_t pw_launch(const PwArgs& a, int sms, cudaStream_t st) {
   auto bytes = [](int batch) {
-    return PW_WARPS * PW_STAGES * PwStage<HD>::BYTES + PW_TILES * (int)sizeof(PwTile<HD>) + 4 * (batch + 1);
+    return PW_WARPS * PW_STAGES * PwStage<HD>::BYTES + PW_TILES * (int)sizeof(PwTile<HD>) + 4 * (2 * batch + 1);
   };
   auto* k = paged_weights_kernel<HD>;
   // the limit belongs to the function and is every host thread's: always the one of the largest batch
