@@ -45,13 +45,14 @@ __device__ __forceinline__ uint32_t ev_key(float w) {
   return w != w ? 0xffffffffu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32, EV_BINS = 2048;
+constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32, EV_BINS = 2048, EV_CLUSTER = 8;
 constexpr int EV_SLICE = 32768;   // keys of a slice that are kept in shared memory (128 KB); longer ones are read again
 
 struct EvShared {
   uint32_t hist[2][EV_BINS];
   uint32_t warp_sum[EV_WARPS];
   uint32_t prefix, need;     // the selected key's leading bits, how many of the keys with them are still wanted
+  uint32_t settled;          // as many as there are of them
   uint32_t above[EV_WARPS], equal[EV_WARPS];   // kept for sure and undecided, of each warp's part
   uint32_t all_above, all_equal;
 };
@@ -84,7 +85,8 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictArgs a
   if (held)
     for (int i = threadIdx.x; i < sn; i += EV_THREADS) keys[i] = ev_key(w[s0 + i]);
   auto key_at = [&](int i) { return held ? keys[i] : ev_key(w[s0 + i]); };
-  if (threadIdx.x == 0) sh.prefix = 0, sh.need = want;
+  if (threadIdx.x == 0) sh.prefix = 0, sh.need = want, sh.settled = 0;
+  int shift = 32;   // bits of a key that are not looked at yet
   constexpr int SHIFT[4] = {32, 21, 10, 0};
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
@@ -100,14 +102,18 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictArgs a
     cluster.sync();
     // every CTA sums the cluster's histograms, from the largest keys down: this thread's two bins
     uint32_t c[2] = {0, 0};
-    for (int r = 0; r < C; ++r) {
-      const uint32_t* other = cluster.map_shared_rank(hist, r);
+    uint32_t got[EV_CLUSTER][2];   // (on their way together: one after the other they took 5 us)
+#pragma unroll
+    for (int r = 0; r < EV_CLUSTER; ++r) {
+      const uint32_t* other = cluster.map_shared_rank(hist, min(r, C - 1));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int bin = bins - 1 - (2 * (int)threadIdx.x + k);
-        if (bin >= 0) c[k] += other[bin];
+        got[r][k] = bin >= 0 && r < C ? other[bin] : 0u;
       }
     }
+#pragma unroll
+    for (int r = 0; r < EV_CLUSTER; ++r) c[0] += got[r][0], c[1] += got[r][1];
     uint32_t inc = c[0] + c[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -118,46 +124,47 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictArgs a
     __syncthreads();
     const uint32_t need = sh.need;
     uint32_t before = inc - c[0] - c[1];
-    for (int k = 0; k < warp; ++k) before += sh.warp_sum[k];
+    before += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0u);
     __syncthreads();   // (need and warp_sum have been read)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (before < need && need <= before + c[k]) {
         sh.prefix = (prefix << bits) | (uint32_t)(bins - 1 - (2 * (int)threadIdx.x + k));
         sh.need = need - before;
+        sh.settled = need == before + c[k];
       }
       before += c[k];
     }
     __syncthreads();
+    shift = SHIFT[pass + 1];
+    if (sh.settled) break;   // (all of the keys with these bits are kept: the same for the whole cluster)
   }
-  // keys above the selected one are kept, and the first `need` of those equal to it
+  // keys whose leading bits lie above the selected ones are kept, and the first `need` of those with the same
   const uint32_t sel = sh.prefix, need = sh.need;
   const int part = ((sn + EV_WARPS - 1) / EV_WARPS + 31) / 32 * 32, p0 = min(sn, warp * part), p1 = min(sn, p0 + part);
   uint32_t above = 0, equal = 0;
   for (int i = p0; i < p1; i += 32) {
     const bool in = i + lane < p1;
-    const uint32_t k = in ? key_at(i + lane) : 0u;
+    const uint32_t k = in ? key_at(i + lane) >> shift : 0u;
     above += __popc(__ballot_sync(0xffffffffu, in && k > sel));
     equal += __popc(__ballot_sync(0xffffffffu, in && k == sel));
   }
   if (lane == 0) sh.above[warp] = above, sh.equal[warp] = equal;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t x = 0, y = 0;
-    for (int k = 0; k < EV_WARPS; ++k) x += sh.above[k], y += sh.equal[k];
-    sh.all_above = x, sh.all_equal = y;
+  if (warp == 0) {
+    const uint32_t x = __reduce_add_sync(0xffffffffu, sh.above[lane]), y = __reduce_add_sync(0xffffffffu, sh.equal[lane]);
+    if (lane == 0) sh.all_above = x, sh.all_equal = y;
   }
   cluster.sync();
-  uint32_t x = 0, y = 0;   // above and equal before this warp's part
-  for (int r = 0; r < rank; ++r) {
-    const EvShared* other = cluster.map_shared_rank(&sh, r);
-    x += other->all_above, y += other->all_equal;
-  }
-  for (int k = 0; k < warp; ++k) x += sh.above[k], y += sh.equal[k];
+  // above and equal before this warp's part: in the CTAs before (a lane each) and in the warps before
+  const EvShared* other = cluster.map_shared_rank(&sh, min(lane, C - 1));
+  uint32_t x = lane < rank ? other->all_above : 0u, y = lane < rank ? other->all_equal : 0u;
+  if (lane < warp) x += sh.above[lane], y += sh.equal[lane];
+  x = __reduce_add_sync(0xffffffffu, x), y = __reduce_add_sync(0xffffffffu, y);
   const uint32_t below = (1u << lane) - 1u;
   for (int i = p0; i < p1; i += 32) {
     const bool in = i + lane < p1;
-    const uint32_t k = in ? key_at(i + lane) : 0u;
+    const uint32_t k = in ? key_at(i + lane) >> shift : 0u;
     const uint32_t gt = __ballot_sync(0xffffffffu, in && k > sel), eq = __ballot_sync(0xffffffffu, in && k == sel);
     const uint32_t eq_before = y + __popc(eq & below);
     if (in && (k > sel || (k == sel && eq_before < need)))
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(EvictArgs a, lon
 }
 
 // CTAs per row: more for rows that can be longer, eight (the portable most) at most.
-int ev_cluster(int columns) { return columns <= 4096 ? 1 : columns <= 16384 ? 4 : 8; }
+int ev_cluster(int columns) { return columns <= 4096 ? 1 : columns <= 16384 ? 4 : EV_CLUSTER; }
 
 kvq_status evict_impl(const void* pages, int n_pages, const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens,
                       int B, int Hkv, int hd, const float* weights, int64_t ws, int64_t wh, int columns, int keep, int first,

@@ -821,12 +821,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM) : "memory");
 }
 
-// The pieces of the unit that CTA blockIdx.x begins and leaves, merged in their order: 32 rows per block, a row per
-// lane, eight output channels at a time per warp.
-constexpr int PP_MERGE_THREADS = 256;
+// The pieces of the unit that CTA blockIdx.x begins and leaves, merged in their order: 32 rows and 32 channels per block, a
+// row per lane and eight output channels per warp.  Bound by the latency of its loads: pieces are read four at a time (64
+// tokens over 4096, 19 pieces to a unit: 35 us with 128 channels per block one piece after the other).
+constexpr int PP_MERGE_THREADS = 128;
 template <int HD>
 __global__ void __launch_bounds__(PP_MERGE_THREADS) prefill_merge_kernel(PpArgs a) {
-  constexpr int G = HD / 32, PART = (HD + 2) * PP_ROWS;
+  constexpr int G = HD / 32, PART = (HD + 2) * PP_ROWS, RUN = 4;
   pdl_trigger();
   pdl_wait();
   const int4 cut = a.cut[blockIdx.x];
@@ -835,42 +836,46 @@ __global__ void __launch_bounds__(PP_MERGE_THREADS) prefill_merge_kernel(PpArgs 
   PpUnit u;
   pp_sequence(a, cut.x, u);
   pp_unit(a, cut.y, u);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + lane;
+  const int lane = threadIdx.x & 31, x = threadIdx.x >> 5, gr = blockIdx.z, row = blockIdx.y * 32 + lane;
   if ((int)blockIdx.y * 32 >= u.rn) return;
   const float* part = a.part + (size_t)blockIdx.x * 2 * PART + row;
   // piece 0 is the CTA's second one, the others their CTAs' first
   auto at = [&](int k) { return part + (size_t)(k == 0 ? 1 : 2 * k) * PART; };
   float top = -INFINITY;
+#pragma unroll 8
   for (int k = 0; k < n; ++k) top = fmaxf(top, at(k)[HD * PP_ROWS]);
   const float ref = top == -INFINITY ? 0.f : top;
-  float l = 0.f;
-  for (int k = 0; k < n; ++k) l = fmaf(at(k)[(HD + 1) * PP_ROWS], exp2_approx(at(k)[HD * PP_ROWS] - ref), l);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int r = u.r0 + row, i = r / a.n_rep, h = cut.z * a.n_rep + (r - i * a.n_rep);
-  const bool live = row < u.rn;
-  const size_t to = (size_t)(u.first + i) * a.Hq + h;
-  if (live && warp == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
-#pragma unroll 1
-  for (int oct = warp; oct < HD / 8; oct += PP_MERGE_THREADS / 32) {
-    const int gr = oct / 4, x = oct % 4;   // channels 32 gr + 8 x .. + 7
-    const int col0 = 8 * (2 * x * (G / 2) + gr / 2) + (gr & 1);
-    float y[8];
+  float l = 0.f, y[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = 0.f;
-#pragma unroll 2
-    for (int p = 0; p < n; ++p) {
-      const float* from = at(p);
-      const float w = exp2_approx(from[HD * PP_ROWS] - ref);
+  for (int k = 0; k < 8; ++k) y[k] = 0.f;
+  const int col0 = 8 * (2 * x * (G / 2) + gr / 2) + (gr & 1);   // of channel 32 gr + 8 x
+  for (int p0 = 0; p0 < n; p0 += RUN) {
+    float v[RUN][8], w[RUN], sum[RUN];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = fmaf(from[(col0 + 4 * G * (k / 4) + 2 * (k % 4)) * PP_ROWS], w, y[k]);
+    for (int p = 0; p < RUN; ++p) {
+      const float* from = at(min(p0 + p, n - 1));
+      w[p] = from[HD * PP_ROWS], sum[p] = from[(HD + 1) * PP_ROWS];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[p][k] = from[(col0 + 4 * G * (k / 4) + 2 * (k % 4)) * PP_ROWS];
     }
-    if (live) {
-      uint32_t v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = f2_to_pair(y[2 * k] * inv, y[2 * k + 1] * inv, a.bf16);
-      *reinterpret_cast<uint4*>(static_cast<unsigned short*>(a.out) + to * HD + 8 * oct) = make_uint4(v[0], v[1], v[2], v[3]);
+    for (int p = 0; p < RUN; ++p) {
+      if (p0 + p >= n) break;
+      const float f = exp2_approx(w[p] - ref);
+      l = fmaf(sum[p], f, l);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = fmaf(v[p][k], f, y[k]);
     }
   }
+  if (row >= u.rn) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int r = u.r0 + row, i = r / a.n_rep, h = cut.z * a.n_rep + (r - i * a.n_rep);
+  const size_t to = (size_t)(u.first + i) * a.Hq + h;
+  if (x == 0 && gr == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+  uint32_t v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = f2_to_pair(y[2 * k] * inv, y[2 * k + 1] * inv, a.bf16);
+  *reinterpret_cast<uint4*>(static_cast<unsigned short*>(a.out) + to * HD + 32 * gr + 8 * x) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 const char* pp_shape_error(int T, int B, int Hq, int Hkv, int hd) {
@@ -898,7 +903,7 @@ cudaError_t pp_launch(const PpArgs& a, int sms, cudaStream_t st) {
   if (cudaError_t e = launch_dependent(prefill_rows_kernel<HD>, dim3((unsigned)std::min<long long>(all, sms * 32)), dim3(PP_ROW_THREADS), 0, st, a))
     return e;
   if (cudaError_t e = launch_dependent(k, dim3(sms), dim3(PP_THREADS), PpSmem<HD>::bytes(a.B), st, a)) return e;
-  return launch_dependent(prefill_merge_kernel<HD>, dim3(sms, PP_ROWS / 32), dim3(PP_MERGE_THREADS), 0, st, a);
+  return launch_dependent(prefill_merge_kernel<HD>, dim3(sms, PP_ROWS / 32, HD / 32), dim3(PP_MERGE_THREADS), 0, st, a);
 }
 
 kvq_status prefill_impl(int dtype, const void* q, int64_t qt, int64_t qh, const int32_t* starts, int T, const void* pages, int n_pages,
