@@ -5,13 +5,13 @@
 // into the pages of another table; codes, scales and offsets move as they are, so that nothing is rounded again (a
 // token from an odd slot keeps its values' negative scales in an even one, which stand for the same values).
 //
-// Two kernels.  The first finds the keep-th largest weight of a row by radix selection (three passes of 11, 11
-// and 10 bits over keys whose unsigned order is the weights') and writes the kept indices in order: a cluster of CTAs
-// per row, each with a contiguous slice of it, whose histograms and counts are added up over distributed shared
-// memory.  The second moves tokens, a block per destination page.
+// Two kernels.  The first finds the keep-th largest weight of a row by radix selection (three passes of 9, 12
+// and 11 bits over keys whose unsigned order is the weights') and writes the kept indices in order: a cluster of CTAs
+// per row, each with a contiguous slice of it, whose histograms are added up in the first CTA's shared memory.  The second moves tokens, a block per destination page.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <string>
 
 #include "kvq.h"
@@ -45,11 +45,13 @@ __device__ __forceinline__ uint32_t ev_key(float w) {
   return w != w ? 0xffffffffu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32, EV_BINS = 2048, EV_CLUSTER = 8;
+constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32, EV_CLUSTER = 8;
+constexpr int EV_COPIES = 8;   // of the first pass' 512 bins, of which a row's weights share a few: lanes meet less often
 constexpr int EV_SLICE = 32768;   // keys of a slice that are kept in shared memory (128 KB); longer ones are read again
 
 struct EvShared {
-  uint32_t hist[2][EV_BINS];
+  alignas(16) uint32_t copies[512 * EV_COPIES];
+  alignas(16) uint32_t bins[512 + 4096 + 2048];   // of the three passes
   uint32_t warp_sum[EV_WARPS];
   uint32_t prefix, need;     // the selected key's leading bits, how many of the keys with them are still wanted
   uint32_t settled;          // as many as there are of them
@@ -78,71 +80,88 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictArgs a
   const int per = ((hi - lo + C - 1) / C + 31) / 32 * 32;
   const int s0 = min(hi, lo + rank * per), s1 = min(hi, s0 + per), sn = s1 - s0;   // this CTA's slice
   const bool held = per <= EV_SLICE;
+  const int want = a.keep - a.first - a.recent;
+  if (held) {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < sn; i += EV_THREADS) keys[i] = ev_key(w[s0 + i]);
+  }
   for (int j = rank * EV_THREADS + threadIdx.x; j < a.first; j += C * EV_THREADS) origin[j] = j;
   for (int j = rank * EV_THREADS + threadIdx.x; j < a.recent; j += C * EV_THREADS) origin[a.keep - a.recent + j] = hi + j;
-  const int want = a.keep - a.first - a.recent;
   if (want == 0) return;
-  if (held)
-    for (int i = threadIdx.x; i < sn; i += EV_THREADS) keys[i] = ev_key(w[s0 + i]);
   auto key_at = [&](int i) { return held ? keys[i] : ev_key(w[s0 + i]); };
+  {
+    uint4* zero = reinterpret_cast<uint4*>(sh.copies);   // and the bins behind them
+    static_assert(offsetof(EvShared, bins) == sizeof(sh.copies), "");
+    for (int i = threadIdx.x; i < (int)((sizeof(sh.copies) + sizeof(sh.bins)) / 16); i += EV_THREADS) zero[i] = make_uint4(0, 0, 0, 0);
+  }
   if (threadIdx.x == 0) sh.prefix = 0, sh.need = want, sh.settled = 0;
   int shift = 32;   // bits of a key that are not looked at yet
-  constexpr int SHIFT[4] = {32, 21, 10, 0};
+  cluster.sync();
+  constexpr int SHIFT[4] = {32, 23, 11, 0}, FIRST[3] = {0, 512, 512 + 4096};
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = SHIFT[pass] - SHIFT[pass + 1], bins = 1 << bits;
-    uint32_t* hist = sh.hist[pass & 1];   // (the last pass' one may still be read by the rest of the cluster)
-    for (int i = threadIdx.x; i < EV_BINS; i += EV_THREADS) hist[i] = 0;
-    __syncthreads();
+    uint32_t* hist = sh.bins + FIRST[pass];
+    uint32_t* sums = cluster.map_shared_rank(hist, 0);   // the first CTA's
     const uint32_t prefix = sh.prefix;
+#pragma unroll 4
     for (int i = threadIdx.x; i < sn; i += EV_THREADS) {
       const uint32_t k = key_at(i);
-      if (pass == 0 || (k >> (SHIFT[pass] & 31)) == prefix) atomicAdd(&hist[(k >> SHIFT[pass + 1]) & (bins - 1)], 1u);
+      if (pass == 0) atomicAdd(&sh.copies[EV_COPIES * (k >> SHIFT[1]) + lane % EV_COPIES], 1u);
+      else if ((k >> (SHIFT[pass] & 31)) == prefix) atomicAdd(&hist[(k >> SHIFT[pass + 1]) & (bins - 1)], 1u);
+    }
+    // what is not 0 to the first CTA (that every CTA read the others' took 5 us a pass)
+    if (pass == 0) {
+      __syncthreads();
+      if (threadIdx.x < bins) {
+        const uint4 x = reinterpret_cast<const uint4*>(sh.copies)[2 * threadIdx.x], y = reinterpret_cast<const uint4*>(sh.copies)[2 * threadIdx.x + 1];
+        const uint32_t sum = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+        if (sum) atomicAdd(sums + threadIdx.x, sum);
+      }
+    } else if (rank != 0) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < bins; i += EV_THREADS)
+        if (hist[i]) atomicAdd(sums + i, hist[i]);
     }
     cluster.sync();
-    // every CTA sums the cluster's histograms, from the largest keys down: this thread's two bins
-    uint32_t c[2] = {0, 0};
-    uint32_t got[EV_CLUSTER][2];   // (on their way together: one after the other they took 5 us)
+    if (rank == 0) {   // the bin with the wanted key, from the largest keys down: four bins per thread
+      uint32_t c[4] = {0, 0, 0, 0};
+      if (4 * threadIdx.x < bins) {
+        const uint4 x = reinterpret_cast<const uint4*>(hist)[bins / 4 - 1 - threadIdx.x];
+        c[0] = x.w, c[1] = x.z, c[2] = x.y, c[3] = x.x;
+      }
+      uint32_t inc = c[0] + c[1] + c[2] + c[3];
 #pragma unroll
-    for (int r = 0; r < EV_CLUSTER; ++r) {
-      const uint32_t* other = cluster.map_shared_rank(hist, min(r, C - 1));
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) sh.warp_sum[warp] = inc;
+      const uint32_t need = sh.need;
+      __syncthreads();   // (need has been read)
+      uint32_t before = inc - c[0] - c[1] - c[2] - c[3] + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0u);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int bin = bins - 1 - (2 * (int)threadIdx.x + k);
-        got[r][k] = bin >= 0 && r < C ? other[bin] : 0u;
+      for (int k = 0; k < 4; ++k) {
+        if (before < need && need <= before + c[k]) {
+          for (int r = 0; r < C; ++r) {
+            EvShared* to = cluster.map_shared_rank(&sh, r);
+            to->prefix = (prefix << bits) | (uint32_t)(bins - 1 - (4 * (int)threadIdx.x + k));
+            to->need = need - before;
+            to->settled = need == before + c[k];
+          }
+        }
+        before += c[k];
       }
     }
-#pragma unroll
-    for (int r = 0; r < EV_CLUSTER; ++r) c[0] += got[r][0], c[1] += got[r][1];
-    uint32_t inc = c[0] + c[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) sh.warp_sum[warp] = inc;
-    __syncthreads();
-    const uint32_t need = sh.need;
-    uint32_t before = inc - c[0] - c[1];
-    before += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0u);
-    __syncthreads();   // (need and warp_sum have been read)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (before < need && need <= before + c[k]) {
-        sh.prefix = (prefix << bits) | (uint32_t)(bins - 1 - (2 * (int)threadIdx.x + k));
-        sh.need = need - before;
-        sh.settled = need == before + c[k];
-      }
-      before += c[k];
-    }
-    __syncthreads();
+    cluster.sync();
     shift = SHIFT[pass + 1];
-    if (sh.settled) break;   // (all of the keys with these bits are kept: the same for the whole cluster)
+    if (sh.settled) break;   // (all of the keys with these bits are kept)
   }
   // keys whose leading bits lie above the selected ones are kept, and the first `need` of those with the same
   const uint32_t sel = sh.prefix, need = sh.need;
   const int part = ((sn + EV_WARPS - 1) / EV_WARPS + 31) / 32 * 32, p0 = min(sn, warp * part), p1 = min(sn, p0 + part);
   uint32_t above = 0, equal = 0;
+#pragma unroll 4
   for (int i = p0; i < p1; i += 32) {
     const bool in = i + lane < p1;
     const uint32_t k = in ? key_at(i + lane) >> shift : 0u;
@@ -162,6 +181,7 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvictArgs a
   if (lane < warp) x += sh.above[lane], y += sh.equal[lane];
   x = __reduce_add_sync(0xffffffffu, x), y = __reduce_add_sync(0xffffffffu, y);
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int i = p0; i < p1; i += 32) {
     const bool in = i + lane < p1;
     const uint32_t k = in ? key_at(i + lane) >> shift : 0u;
