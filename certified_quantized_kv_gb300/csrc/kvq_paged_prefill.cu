@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   extern __shared__ unsigned char raw_smem[];
   unsigned char* sm = raw_smem + (1024 - (pp_smem(raw_smem) & 1023)) % 1024;
   long long* pre = reinterpret_cast<long long*>(sm + S::PRE);   // [B + 1] steps before each sequence, of one KV head
-  __shared__ __align__(8) unsigned long long bars[21];
+  __shared__ __align__(8) unsigned long long bars[23];
   __shared__ uint32_t tmem_at;
   __shared__ int failed_at;
   __shared__ int4 start_at;   // sequence, unit, KV head, step of this CTA's first position
@@ -334,13 +334,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   const uint32_t bar0 = __shfl_sync(0xffffffffu, pp_smem(bars), 0);
   const uint32_t k_full = bar0, k_empty = bar0 + 16, v_full = bar0 + 32, v_empty = bar0 + 48;            // [stage]
   const uint32_t q_full = bar0 + 64, s_full = bar0 + 80, p_full = bar0 + 96, o_full = bar0 + 112;        // [tile]
-  const uint32_t o_empty = bar0 + 128, q_empty = bar0 + 144, done = bar0 + 160;
+  const uint32_t o_empty = bar0 + 128, q_empty = bar0 + 144, done = bar0 + 160, p_half = bar0 + 168;
   if (threadIdx.x == 0) {
     auto init = [&](uint32_t bar, int count) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory"); };
     for (int k = 0; k < 2; ++k) {
       init(k_full + 8 * k, 128), init(k_empty + 8 * k, 1), init(v_full + 8 * k, 128), init(v_empty + 8 * k, 1);
       init(q_full + 8 * k, 1), init(o_empty + 8 * k, 128), init(s_full + 8 * k, 1), init(p_full + 8 * k, 128), init(o_full + 8 * k, 1);
-      init(q_empty + 8 * k, 1);
+      init(q_empty + 8 * k, 1), init(p_half + 8 * k, 128);
     }
     init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -551,6 +551,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
             uint32_t v[32];
             pp_ld32(v, sp + 32 * c);
             pp_wait_ld(v), weigh(v, c, c & 2 ? (c & 1 ? mask[3] : mask[2]) : (c & 1 ? mask[1] : mask[0]));
+            if (c == 1) {   // the product with the first half of the values can begin
+              pp_wait_st();
+              pp_before();
+              pp_arrive(p_half + 8 * rt);
+            }
           }
           l += sum.x + sum.y;
           pp_wait_st();
@@ -785,13 +790,17 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
           if (rt < nt) {
-            pp_wait(p_full + 8 * rt, (p_par >> rt) & 1u, failed);
+            const uint32_t par = (p_par >> rt) & 1u;
             p_par ^= 1u << rt;
             if (j == 0) pp_wait(o_empty + 8 * rt, (o_par >> rt) & 1u, failed), o_par ^= 1u << rt;
-            pp_after();
 #pragma unroll
-            for (int k = 0; k < PP_TOK / 16; ++k)
-              pp_mma_ts<IPV>(tm + OUT + HD * rt, tm + SCORES + 128 * rt + 8 * k, v_at + vs * (S::KV / 16) + k * (2048 / 16), j > 0 || k > 0, leader);
+            for (int half = 0; half < 2; ++half) {
+              pp_wait((half ? p_full : p_half) + 8 * rt, par, failed);
+              pp_after();
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                pp_mma_ts<IPV>(tm + OUT + HD * rt, tm + SCORES + 128 * rt + 8 * k, v_at + vs * (S::KV / 16) + k * (2048 / 16), j > 0 || k > 0, leader);
+            }
             if (last) pp_commit(o_full + 8 * rt, leader);
           }
           if (rt < more) {
