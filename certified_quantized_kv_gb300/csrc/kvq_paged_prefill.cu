@@ -58,7 +58,7 @@ struct PpArgs {
 
 constexpr int PP_ROWS = 256, PP_TOK = 128, PP_STAGES = 2, PP_MAX_BATCH = 2048;
 constexpr int PP_WARPS = 14, PP_THREADS = 32 * PP_WARPS, PP_MMA_WARP = 12;
-constexpr int PP_LEAD = 1;
+constexpr int PP_LEAD = 2;
 constexpr float PP_TOP = 15.f, PP_SET = 10.f;             // weights are 2^15 at most, 2^10 when their reference is set
 constexpr unsigned long long PP_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
 
