@@ -628,6 +628,19 @@ def paged_attention_workspace(batch: int, n_q_tokens: int, n_q_heads: int, n_kv_
     return int(n.value)
 
 
+def _own_workspace(nbytes, dev, like, stream, zero):
+    """A workspace of a call that was given none."""
+    torch = _torch
+    with torch.cuda.device(dev):
+        workspace = (torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            # made (and zeroed) on the current stream and used on the other one
+            other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            other.wait_stream(torch.cuda.current_stream())
+            workspace.record_stream(other)
+    return workspace
+
+
 def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, window=0, workspace=None, stream=None):
     """Decode attention over a pool of 4-bit pages (kvq_paged_attention).
 
@@ -666,14 +679,9 @@ def paged_attention(q, pages, page_table, seq_lens, out, lse=None, scale=None, w
         raise ValueError("page_table: the last dimension must be contiguous")
     lens = _ints(seq_lens, "seq_lens", B, dev)
     if workspace is None:
-        torch = _torch
-        with torch.cuda.device(dev):
-            workspace = torch.zeros(paged_attention_workspace(B, Q, hq, hkv, hd), dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                # zeroed on the current stream and used on the other one
-                other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-                other.wait_stream(torch.cuda.current_stream())
-                workspace.record_stream(other)
+        with _torch.cuda.device(dev):
+            need = paged_attention_workspace(B, Q, hq, hkv, hd)
+        workspace = _own_workspace(need, dev, q, stream, True)
     elif workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _call(dev, stream, load_library().kvq_paged_attention, code, q.data_ptr(), qt, st[-2] if hq > 1 else 8, *pool,
@@ -704,19 +712,6 @@ def _weight_rows(t, name, B, hkv):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # a dimension of one row has no stride to speak of
     return t.data_ptr(), a if B > 1 else hkv * n, b if hkv > 1 else n, n
-
-
-def _own_workspace(nbytes, dev, like, stream, zero):
-    """A workspace of a call that was given none."""
-    torch = _torch
-    with torch.cuda.device(dev):
-        workspace = (torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            # made (and zeroed) on the current stream and used on the other one
-            other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-            other.wait_stream(torch.cuda.current_stream())
-            workspace.record_stream(other)
-    return workspace
 
 
 def paged_prefill_workspace(n_tokens: int, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int = HEAD_DIM) -> int:

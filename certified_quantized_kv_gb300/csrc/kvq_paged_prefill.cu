@@ -931,6 +931,9 @@ kvq_status prefill_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   if (window < 0 || (window && !causal)) return bad("window must be >= 0, and 0 unless causal");
   const float scale_log2 = (scale != 0.f ? scale : 1.f / std::sqrt((float)hd)) * LOG2E_F;
   if (!std::isfinite(scale_log2)) return bad("scale * log2(e) must be finite");
+  // the steps of all units, times the CTAs, are counted in 64 bits
+  const double most = ((double)T * (Hq / Hkv) / PP_ROWS + B) * (max_pages / 2 + 1 + PP_LEAD) * Hkv * 1024;
+  if (most >= 9e18) return bad("n_tokens * max_pages * n_q_heads is too large for one call");
   if (B == 0 || T == 0) return KVQ_OK;
   if (q == out) return bad("out must not be q");
   if (kvq_status s = check_strides(qt, qh, fn, "q")) return s;

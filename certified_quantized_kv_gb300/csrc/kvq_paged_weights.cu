@@ -32,7 +32,7 @@ constexpr int PW_ROWS = 8;            // query rows of a tile (MMA columns)
 constexpr int PW_TILES = 16;          // tiles in shared memory at once
 constexpr int PW_THREADS = 512, PW_WARPS = PW_THREADS / 32, PW_MAX_BATCH = 2048;
 // Positions that a (sequence, KV head) takes in the ranges besides its pages, for what starting it costs in pages' time
-constexpr int PW_LEAD = 2;
+constexpr int PW_LEAD = 3;
 constexpr int PW_STAGES = 2;          // pages on their way per warp
 constexpr unsigned long long PW_WAIT_NS = 2000000000ull;   // bounded waits: 2 s
 
@@ -64,9 +64,7 @@ struct PwArgs {
   bool bf16;
 };
 
-__device__ __forceinline__ int pw_len(const PwArgs& a, int b) {
-  return min(max(a.lens[b], 0), (int)min((long long)a.max_pages * PG, (long long)a.columns));
-}
+__device__ __forceinline__ int pw_len(const PwArgs& a, int b) { return min(max(a.lens[b], 0), a.max_pages * PG); }
 
 __device__ __forceinline__ void pw_mma(float (&c)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -183,7 +181,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   if (threadIdx.x == 0) pre[0] = 0;
   for (int base = 0, run = 0; base < a.B; base += PW_THREADS) {
     const int b = base + threadIdx.x;
-    const int len = b < a.B ? pw_len(a, b) : 0, np = (len + PG - 1) / PG;
+    const int len = b < a.B ? pw_len(a, b) : 0, np = (min(len, a.columns) + PG - 1) / PG;   // (tokens without a column count nothing)
     if (b < a.B) lens[b] = len;
     int inc = np ? np + PW_LEAD : 0;
 #pragma unroll
@@ -303,14 +301,14 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
       Part p = first;
       for (int y = 0; y < parts; ++y) {
         if (y) p = part_at(p.end, p.b);
-        const int n = p.n;
+        const int n = p.n, cols = min(n, a.columns);
         for (int page = p.warp0; page < p.pages; page += PW_WARPS) {
           const int tok0 = (p.page0 + page) * PG;
           float* w = a.weights + p.b * a.ws + p.g * a.wh + tok0;
           // what is there of this lane's tokens (decay 0 does not read it)
           float old[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) old[k] = (rt0 || a.decay != 0.f) && tok0 + 32 * k + 8 * tig + gid < n ? w[32 * k + 8 * tig + gid] : 0.f;
+          for (int k = 0; k < 2; ++k) old[k] = (rt0 || a.decay != 0.f) && tok0 + 32 * k + 8 * tig + gid < cols ? w[32 * k + 8 * tig + gid] : 0.f;
           const int stage = ring_stage<PW_STAGES>(used);
           const unsigned char* pg = ring + stage * St::BYTES;
           const uint32_t parity = ring_parity<PW_STAGES>(used);
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
           for (int k = 0; k < 2; ++k) {
             const int t = 32 * k + 8 * tig + gid;
             const float x = failed ? __int_as_float(0x7fc00000) : own[k];
-            if (tok0 + t < n) w[t] = rt0 ? old[k] + x : a.decay == 0.f ? x : fmaf(old[k], a.decay, x);
+            if (tok0 + t < cols) w[t] = rt0 ? old[k] + x : a.decay == 0.f ? x : fmaf(old[k], a.decay, x);
           }
           __syncwarp();   // the stage's last readers are done
           if (!failed && more) issue();
@@ -480,7 +478,7 @@ kvq_status weights_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   PwArgs a = {};
   a.q = q, a.lse = lse, a.pages = static_cast<const unsigned char*>(pages), a.table = table, a.lens = lens, a.weights = weights;
   a.qt = qt, a.qh = qh, a.table_stride = table_stride, a.ws = ws, a.wh = wh;
-  a.n_pages = n_pages, a.max_pages = (int)std::min<long long>(max_pages, ((long long)columns + PG - 1) / PG), a.columns = columns;
+  a.n_pages = n_pages, a.max_pages = max_pages, a.columns = columns;
   a.B = B, a.Q = Q, a.Hq = Hq, a.Hkv = Hkv, a.n_rep = Hq / Hkv, a.rows = Q * a.n_rep, a.RT = (a.rows + PW_ROWS - 1) / PW_ROWS;
   a.window = std::min(window, 1 << 30);
   a.scale_log2 = scale_log2, a.decay = decay, a.bf16 = dtype == KVQ_BF16;

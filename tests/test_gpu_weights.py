@@ -46,13 +46,13 @@ def _reference(q, lse, pages, table, lens, w, decay, window, scale):
     rep, qf, lf, out = Hq // Hkv, _f64(q), _f64(lse), _f64(w).copy()
     tol = np.abs(out) * 2.0 ** -23
     for b, n in enumerate(lens):
-        n = min(n, w.shape[2])
+        cols = min(n, w.shape[2])
         if n == 0:
             continue
-        t = np.arange(n)
+        t = np.arange(cols)
         for g in range(Hkv):
-            k = _keys(pages, table, b, g, n, D)[0]
-            out[b, g, :n] = 0 if decay == 0 else out[b, g, :n] * decay
+            k = _keys(pages, table, b, g, n, D)[0][:cols]
+            out[b, g, :cols] = 0 if decay == 0 else out[b, g, :cols] * decay
             for i in range(Q):
                 hi = n - Q + 1 + i
                 lo = max(0, hi - window) if window else 0
@@ -62,9 +62,9 @@ def _reference(q, lse, pages, table, lens, w, decay, window, scale):
                     s = (k @ qf[b, i, r]) * scale
                     a = 3 * abs(scale) * np.abs(qf[b, i, r]).sum() * np.abs(k).max(-1)
                     p = np.where((t >= lo) & (t < hi), np.exp(s - lf[b, i, r]), 0.0)
-                    out[b, g, :n] += p
-                    tol[b, g, :n] += p * (2.0 ** -16 * a + 2.0 ** -22 * 1.5 * (np.abs(s) + abs(lf[b, i, r])) + 2.0 ** -21)
-            tol[b, g, :n] += Q * rep * 2.0 ** -23 * np.abs(out[b, g, :n]) + 2.0 ** -126
+                    out[b, g, :cols] += p
+                    tol[b, g, :cols] += p * (2.0 ** -16 * a + 2.0 ** -22 * 1.5 * (np.abs(s) + abs(lf[b, i, r])) + 2.0 ** -21)
+            tol[b, g, :cols] += Q * rep * 2.0 ** -23 * np.abs(out[b, g, :cols]) + 2.0 ** -126
     return out, tol
 
 
@@ -150,10 +150,10 @@ def test_operands():
     w, keep = wide.transpose(0, 1)[..., 3:3 + 290], wide.clone()
     lost = table[0, 2].item()
     table[0, 2] = 10 ** 6                 # tokens 128..191 are not seen: they only decay
-    # sequence 0 counts as 290 tokens: its queries are the last two of those
+    # sequence 0's last ten tokens have no column: its queries are the last two of 300 all the same
     kvq.paged_weights(q, lse, pages, table, _ints(lens), w, decay=0.5)
     table[0, 2] = lost
-    ref, tol = _reference(q, lse, pages, table, [290, 190], keep.transpose(0, 1)[..., 3:3 + 290], 0.5, 0, D ** -0.5)
+    ref, tol = _reference(q, lse, pages, table, lens, keep.transpose(0, 1)[..., 3:3 + 290], 0.5, 0, D ** -0.5)
     before = _f64(keep.transpose(0, 1)[..., 3:3 + 290])
     ref[0, :, 128:192] = before[0, :, 128:192] * 0.5
     assert np.all(np.abs(_f64(w) - ref) <= tol)
