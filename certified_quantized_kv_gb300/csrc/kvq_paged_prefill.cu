@@ -12,8 +12,8 @@
 // The two tiles take turns: while one's scores are turned into weights, the tensor cores work on the other.
 //
 // Unpacking: x^ = o + s code.  Two nibbles at a time are masked into binary16 numbers 1024 + n (or 64 + n), less 1024
-// (exact), then one binary16 multiply-add, so each key and value is the held number rounded once (2^-11).  Nibbles four channels apart
-// come out of one word side by side; keys stay in that order, and so do the queries (a dot product does not mind); values
+// (exact), then one binary16 multiply-add, so each key and value is the held number rounded once (2^-11).  Nibbles four
+// channels apart come out of one word side by side; keys stay in that order, and so do the queries (a dot product does not mind); values
 // come out with channels of two groups in turn, so their scales and offsets enter in pairs, and the output is put in
 // order when it is written.  Weights are rounded once to binary16 (2^-11) before their product with the values.  The
 // decode attention keeps both exact, at four times the work per score; here the tensor cores would wait for it.
@@ -25,8 +25,16 @@
 // 2^10: accumulators in TMEM are rarely rescaled, and small weights stay normal binary16 numbers.
 //
 // The units' steps (128 tokens) are numbered, sequence by sequence, and cut into equal contiguous ranges, one per CTA,
-// whatever the lengths; a unit counts PP_LEAD more than its steps, for what starting and finishing it takes.  A unit within one range is written out directly; the pieces of one that is cut go to the
-// workspace, and a second kernel merges them in a fixed order, so that results do not depend on timing.
+// whatever the lengths; a unit counts PP_LEAD more than its steps, for what starting and finishing it takes.
+// A unit within one range is written out directly; the pieces of one that is cut go to the workspace, and a second kernel
+// merges them in a fixed order, so that results do not depend on timing.
+//
+// Measured (32 query heads on 8 KV heads of 128, bf16; 1925 TFLOP/s measured for a product of 8192^3): 2048 tokens over 32768
+// 894 us = 1190 TFLOP/s (0.62), a prompt of 8192 tokens 527 us = 1043 (0.54); 64 tokens over 4096 29 us, of which the rows'
+// kernel takes 3, the merge 8.  A step of 256 rows and 128 tokens takes about 3700 cycles, 2048 of them the MMAs': each
+// tile's chain is its softmax (2700 cycles beside the other tile's and the unpacking, whose instructions fill 0.61 of the
+// issue slots) and its two products (1070).  Every role's loop is as short as it is because straight code was slower: the
+// same softmax with its four loads of scores unrolled took 968 us where this takes 879, unpacking unrolled 944 against 894.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -35,6 +43,7 @@
 #include "kvq.h"
 #include "kvq_launch.h"
 #include "kvq_paged.cuh"
+#include "kvq_tc.cuh"
 
 namespace kvq {
 
@@ -58,9 +67,9 @@ struct PpArgs {
 
 constexpr int PP_ROWS = 256, PP_TOK = 128, PP_STAGES = 2, PP_MAX_BATCH = 2048;
 constexpr int PP_WARPS = 14, PP_THREADS = 32 * PP_WARPS, PP_MMA_WARP = 12;
+// (a prompt of 8192 tokens: 598 us with one, 527 with two, 538 with four; without any the first CTA has 80 short units)
 constexpr int PP_LEAD = 2;
 constexpr float PP_TOP = 15.f, PP_SET = 10.f;             // weights are 2^15 at most, 2^10 when their reference is set
-constexpr unsigned long long PP_WAIT_NS = 2000000000ull;    // bounded waits: 2 s
 
 // A chunk and one of its units.
 struct PpUnit {
@@ -86,114 +95,6 @@ __device__ __forceinline__ void pp_unit(const PpArgs& a, int qt, PpUnit& u) {
   u.j0 = lo / PP_TOK;
   u.np = max(1, (hi + PP_TOK - 1) / PP_TOK - u.j0);
 }
-
-// ---- mbarriers, TMEM and MMAs ----
-__device__ __forceinline__ uint32_t pp_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ unsigned long long pp_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ bool pp_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-// A wait that runs out, in any warp, lets all further ones pass: the CTA finishes with outputs that are NaN.  (The clock is
-// read once in 256 tries: it takes longer than they do.)
-__device__ __forceinline__ void pp_wait_slow(uint32_t bar, uint32_t parity, volatile int* failed) {
-  unsigned long long t0 = 0;
-#pragma unroll 1
-  for (uint32_t n = 0; !pp_try(bar, parity); ++n) {
-    if ((n & 255) != 255) continue;
-    const unsigned long long t = pp_ns();
-    if (*failed) return;
-    if (t0 == 0) t0 = t;
-    if (t - t0 > PP_WAIT_NS) *failed = 1;
-  }
-}
-__device__ __forceinline__ void pp_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
-  if (!pp_try(bar, parity)) pp_wait_slow(bar, parity, failed);
-}
-__device__ __forceinline__ void pp_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-// (the whole warp comes here, so that the compiler keeps addresses in uniform registers, which these instructions take: one
-// thread by itself needed 200 cycles per MMA)
-__device__ __forceinline__ void pp_commit(uint32_t bar, bool leader) {
-  if (leader) asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void pp_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void pp_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void pp_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Shared-memory operand of 128-byte rows of 64 elements, 16-byte pieces XORed with the row's number modulo 8 (128-byte
-// swizzle), eight rows to 1024 bytes: the descriptor's halves.  `lead`: bytes between blocks of 64 elements along M or N
-// where those are contiguous (values: rows are tokens, the contraction's index).
-constexpr uint32_t PP_DESC_HIGH = (1024u >> 4) | 1u << 14 | 2u << 29;
-__device__ __forceinline__ uint32_t pp_desc(uint32_t addr, uint32_t lead) { return (addr >> 4) | (lead >> 4) << 16; }
-// fp32 accumulators, binary16 operands, M 128; B's contiguous index: the contraction's, or (turned) N
-__host__ __device__ constexpr uint32_t pp_idesc(int n, bool turned) {
-  return 1u << 4 | (turned ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
-}
-template <uint32_t IDESC>
-__device__ __forceinline__ void pp_mma_ss(uint32_t d, uint32_t x, uint32_t y, bool add, bool leader) {
-  if (leader)
-    asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n"
-                 :: "r"(d), "r"(x), "r"(y), "r"(IDESC), "r"((uint32_t)add), "r"(PP_DESC_HIGH) : "memory");
-}
-template <uint32_t IDESC>
-__device__ __forceinline__ void pp_mma_ts(uint32_t d, uint32_t x, uint32_t y, bool add, bool leader) {
-  if (leader)
-    asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n"
-                 :: "r"(d), "r"(x), "r"(y), "r"(IDESC), "r"((uint32_t)add), "r"(PP_DESC_HIGH) : "memory");
-}
-__device__ __forceinline__ bool pp_elect() {
-  uint32_t one;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
-  return one != 0;
-}
-
-// 32 columns of this warp's 32 lanes, a lane's in one thread
-__device__ __forceinline__ void pp_ld32(uint32_t (&v)[32], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(at));
-}
-__device__ __forceinline__ void pp_st16(uint32_t at, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-      :: "r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void pp_ld16(uint32_t (&v)[16], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(at) : "memory");
-}
-// (the loaded registers are tied to the wait, so that nothing reads them before it)
-__device__ __forceinline__ void pp_wait_ld(uint32_t (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-      : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]),
-        "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
-        "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
-        "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]) :: "memory");
-}
-__device__ __forceinline__ void pp_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float pp_max3(float x, float y, float z) {
   float m;
@@ -226,11 +127,6 @@ __device__ __forceinline__ bool pp_large(__half2 s, __half2 o) {
   const uint32_t x = h2_as_u32(__hfma2(__habs2(s), u32_as_h2(0x4B804B80u), __habs2(o))) & 0x7FFF7FFFu;
   return (x & 0xffffu) >= 0x7C00u || (x >> 16) >= 0x7C00u;
 }
-// piece `c` (16 bytes, eight elements) of row r of an operand of `rows` rows
-__device__ __forceinline__ uint32_t pp_place(int rows, int r, int c) {
-  return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 template <int HD>
 struct PpSmem {
   static constexpr int Q = PP_ROWS * HD * 2, KV = PP_TOK * HD * 2;
@@ -323,7 +219,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   constexpr int G = L::G, CH = HD / 8;                        // 16-byte pieces of a row
   constexpr uint32_t SCORES = 0, OUT = 256, TMEM = 512;       // columns: scores (and weights) of tiles 0 and 1, then outputs
   extern __shared__ unsigned char raw_smem[];
-  unsigned char* sm = raw_smem + (1024 - (pp_smem(raw_smem) & 1023)) % 1024;
+  unsigned char* sm = raw_smem + (1024 - (tc_smem(raw_smem) & 1023)) % 1024;
   long long* pre = reinterpret_cast<long long*>(sm + S::PRE);   // [B + 1] steps before each sequence, of one KV head
   __shared__ __align__(8) unsigned long long bars[23];
   __shared__ uint32_t tmem_at;
@@ -331,7 +227,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   __shared__ int4 start_at;   // sequence, unit, KV head, step of this CTA's first position
   volatile int* failed = &failed_at;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t bar0 = __shfl_sync(0xffffffffu, pp_smem(bars), 0);
+  const uint32_t bar0 = __shfl_sync(0xffffffffu, tc_smem(bars), 0);
   const uint32_t k_full = bar0, k_empty = bar0 + 16, v_full = bar0 + 32, v_empty = bar0 + 48;            // [stage]
   const uint32_t q_full = bar0 + 64, s_full = bar0 + 80, p_full = bar0 + 96, o_full = bar0 + 112;        // [tile]
   const uint32_t o_empty = bar0 + 128, q_empty = bar0 + 144, done = bar0 + 160, p_half = bar0 + 168;
@@ -348,7 +244,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     pre[0] = 0;
   }
   if (warp == PP_MMA_WARP) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(pp_smem(&tmem_at)), "r"(TMEM) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(tc_smem(&tmem_at)), "r"(TMEM) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_trigger();
@@ -364,9 +260,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) pre[b + 1] = sum;
   }
-  pp_before();
+  tc_before();
   __syncthreads();
-  pp_after();
+  tc_after();
   const uint32_t tmem = tmem_at;
   long long n_pos;   // of this CTA
   if (warp == 0) {
@@ -491,9 +387,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
               mask[c] = ((there >> (c >> 1)) & 1u) ? low & high : 0u;
             }
           }
-          pp_wait(s_full + 8 * rt, s_par, failed);
+          tc_wait(s_full + 8 * rt, s_par, failed);
           s_par ^= 1;
-          pp_after();
+          tc_after();
           // The scores 32 tokens at a time, twice (in registers they would be 128): for the row's maximum, then for the
           // weights, which take the place of scores that were read.
           auto hide = [&](uint32_t (&v)[32], uint32_t seen) {
@@ -514,8 +410,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
-            pp_ld32(v, sp + 32 * c);
-            pp_wait_ld(v), most(v, c & 2 ? (c & 1 ? mask[3] : mask[2]) : (c & 1 ? mask[1] : mask[0]));
+            tc_ld32(v, sp + 32 * c);
+            tc_wait_ld(v), most(v, c & 2 ? (c & 1 ? mask[3] : mask[2]) : (c & 1 ? mask[1] : mask[0]));
           }
           if (__any_sync(0xffffffffu, m > lim)) {
             const float now = m > lim ? m * sc - PP_SET : ref, al = exp2_approx(ref - now);
@@ -526,10 +422,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
 #pragma unroll 1
               for (int c = 0; c < HD; c += 16) {
                 uint32_t x[16];
-                pp_ld16(x, op + c);
+                tc_ld16(x, op + c);
+              tc_wait_ld(x);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
-                pp_st16(op + c, x);
+                tc_st16(op + c, x);
               }
             }
           }
@@ -544,29 +441,29 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
               sum = add2(sum, p);
               w[k] = h2_as_u32(__floats2half2_rn(p.x, p.y));
             }
-            pp_st16(sp + 16 * c, w);
+            tc_st16(sp + 16 * c, w);
           };
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
-            pp_ld32(v, sp + 32 * c);
-            pp_wait_ld(v), weigh(v, c, c & 2 ? (c & 1 ? mask[3] : mask[2]) : (c & 1 ? mask[1] : mask[0]));
+            tc_ld32(v, sp + 32 * c);
+            tc_wait_ld(v), weigh(v, c, c & 2 ? (c & 1 ? mask[3] : mask[2]) : (c & 1 ? mask[1] : mask[0]));
             if (c == 1) {   // the product with the first half of the values can begin
-              pp_wait_st();
-              pp_before();
-              pp_arrive(p_half + 8 * rt);
+              tc_wait_st();
+              tc_before();
+              tc_arrive(p_half + 8 * rt);
             }
           }
           l += sum.x + sum.y;
-          pp_wait_st();
-          pp_before();
-          pp_arrive(p_full + 8 * rt);
+          tc_wait_st();
+          tc_before();
+          tc_arrive(p_full + 8 * rt);
         }
 
         // ---- the piece's end: to the output, or to the workspace ----
-        pp_wait(o_full + 8 * rt, o_par, failed);
+        tc_wait(o_full + 8 * rt, o_par, failed);
         o_par ^= 1;
-        pp_after();
+        tc_after();
         const bool whole = steps == u.np, lost = *failed != 0;
         if (lost) l = __int_as_float(0x7fc00000);
         float* part = a.part + ((size_t)blockIdx.x * 2 + (s0 == 0)) * (HD + 2) * PP_ROWS + 128 * rt + tid;
@@ -580,8 +477,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
 #pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t v[32];
-          pp_ld32(v, op + 32 * c);
-          pp_wait_ld(v);
+          tc_ld32(v, op + 32 * c);
+          tc_wait_ld(v);
           if (whole) {
             // column 8w + 2k + (g & 1): channel 32g + 4a + k, w = a G / 2 + g / 2; 32 columns are 32 / G channels of each group
             constexpr int RUN = 32 / G;
@@ -604,8 +501,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
             for (int k = 0; k < 32; ++k) part[(32 * c + k) * PP_ROWS] = __uint_as_float(v[k]);
           }
         }
-        pp_before();
-        pp_arrive(o_empty + 8 * rt);
+        tc_before();
+        tc_arrive(o_empty + 8 * rt);
       }
       if (steps < u.np && s0 == 0 && threadIdx.x == 0) {
         // pieces: this CTA's and those of the CTAs that its other steps lie in
@@ -677,14 +574,14 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
             // word w = 4k + i of the row.  Keys: word G a + g is channels 32g + 8a .. + 7, piece 4g + a of the row; values:
             // word G / 2 a + g / 2
             const int gr = values ? 2 * (i % (G / 2)) : i % G, c = values ? 4 * k + i : 4 * (i % G) + 4 / G * k + i / G;
-            *reinterpret_cast<uint4*>(to + pp_place(PP_TOK, t, c)) = pp_unpack<CLAMP>(word_of(x.code[values][0], i), sh[gr], oh[gr]);
+            *reinterpret_cast<uint4*>(to + tc_place(PP_TOK, t, c)) = pp_unpack<CLAMP>(word_of(x.code[values][0], i), sh[gr], oh[gr]);
           }
 #pragma unroll
           for (int i = 0; i + 1 < W4; ++i) x.code[values][i] = x.code[values][i + 1];
         }
       };
       if (__any_sync(0xffffffffu, large)) words(std::true_type{}); else words(std::false_type{});
-      pp_proxy();
+      tc_proxy();
     };
     uint32_t stage = 0, par = 1;
     auto put = [&](Held& x) {
@@ -700,12 +597,12 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         if (hi) x.o[1][k] &= 0x0000ffffu, x.s[1][k] &= 0x0000ffffu;
       }
       if (nan) x.o[0][0] = 0x7fff7fffu;
-      pp_wait(k_empty + 8 * stage, par, failed);
+      tc_wait(k_empty + 8 * stage, par, failed);
       unpack(std::false_type{}, x, sm + S::K0 + stage * S::KV);
-      pp_arrive(k_full + 8 * stage);
-      pp_wait(v_empty + 8 * stage, par, failed);
+      tc_arrive(k_full + 8 * stage);
+      tc_wait(v_empty + 8 * stage, par, failed);
       unpack(std::true_type{}, x, sm + S::V0 + stage * S::KV);
-      pp_arrive(v_full + 8 * stage);
+      tc_arrive(v_full + 8 * stage);
       if (++stage == PP_STAGES) stage = 0, par ^= 1;
     };
     begin();
@@ -728,13 +625,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
       for (begin(); steps > 0; next())
         for (int rt = 0; rt < (u.rn > 128 ? 2 : 1); ++rt) {
           // the last unit's scores are there, so that its queries are not needed any more
-          pp_wait(q_empty + 8 * rt, ((par >> rt) & 1u) ^ 1u, failed);
+          tc_wait(q_empty + 8 * rt, ((par >> rt) & 1u) ^ 1u, failed);
           const uint32_t bytes = 128u * min(128, u.rn - 128 * rt);
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(q_full + 8 * rt), "r"(bytes * (HD / 64)) : "memory");
 #pragma unroll
           for (int k = 0; k < HD / 64; ++k)
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                         :: "r"(pp_smem(sm) + rt * (S::Q / 2) + k * 128 * 128),
+                         :: "r"(tc_smem(sm) + rt * (S::Q / 2) + k * 128 * 128),
                             "l"(a.rows + ((g * (HD / 64) + k) * rows + (long long)u.first * a.n_rep + u.r0 + 128 * rt) * 128), "r"(bytes), "r"(q_full + 8 * rt)
                          : "memory");
           par ^= 1u << rt, used |= 1u << rt;
@@ -742,32 +639,32 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
       // (nothing is on its way when the CTA ends, also behind a wait that ran out)
       for (int rt = 0; rt < 2; ++rt)
         if ((used >> rt) & 1u)
-          for (const unsigned long long t = pp_ns(); !pp_try(q_full + 8 * rt, ((par >> rt) & 1u) ^ 1u) && pp_ns() - t < PP_WAIT_NS;) {}
+          for (const unsigned long long t = tc_ns(); !tc_try(q_full + 8 * rt, ((par >> rt) & 1u) ^ 1u) && tc_ns() - t < TC_WAIT_NS;) {}
     }
   } else {
     // ---- MMAs ----
-    constexpr uint32_t IQK = pp_idesc(PP_TOK, false), IPV = pp_idesc(HD, true);
+    constexpr uint32_t IQK = tc_idesc(PP_TOK, false), IPV = tc_idesc(HD, true);
     auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-    const uint32_t tm = uniform(tmem), base = uniform(pp_smem(sm));
-    const uint32_t q_at = pp_desc(base, 16), k_at = pp_desc(base + S::K0, 16), v_at = pp_desc(base + S::V0, PP_TOK * 128);
-    const bool leader = pp_elect();
+    const uint32_t tm = uniform(tmem), base = uniform(tc_smem(sm));
+    const uint32_t q_at = tc_desc(base, 16), k_at = tc_desc(base + S::K0, 16), v_at = tc_desc(base + S::V0, PP_TOK * 128);
+    const bool leader = tc_elect();
     uint32_t kn = 0, vn = 0;                     // steps of keys and values begun
     uint32_t q_par = 0, p_par = 0, o_par = 3;    // bit rt: parities
     auto scores = [&](int rt, uint32_t stage, bool last) {
 #pragma unroll
       for (int k = 0; k < HD / 16; ++k) {
         const uint32_t at = ((k / 4) * 128 * 128 + (k % 4) * 32) >> 4;
-        pp_mma_ss<IQK>(tm + SCORES + 128 * rt, q_at + rt * (S::Q / 32) + at, k_at + stage * (S::KV / 16) + at, k > 0, leader);
+        tc_mma_ss<IQK>(tm + SCORES + 128 * rt, q_at + rt * (S::Q / 32) + at, k_at + stage * (S::KV / 16) + at, k > 0, leader);
       }
-      pp_commit(s_full + 8 * rt, leader);
-      if (last) pp_commit(q_empty + 8 * rt, leader);   // the piece's queries have served
+      tc_commit(s_full + 8 * rt, leader);
+      if (last) tc_commit(q_empty + 8 * rt, leader);   // the piece's queries have served
     };
     auto tiles = [&]() { return uniform(steps == 0 ? 0 : u.rn > 128 ? 2 : 1); };
     auto first_scores = [&](int rt, bool only) {   // of a piece
-      pp_wait(q_full + 8 * rt, (q_par >> rt) & 1u, failed);
+      tc_wait(q_full + 8 * rt, (q_par >> rt) & 1u, failed);
       q_par ^= 1u << rt;
-      if (rt == 0) pp_wait(k_full + 8 * (kn % PP_STAGES), (kn / PP_STAGES) & 1u, failed);
-      pp_after();
+      if (rt == 0) tc_wait(k_full + 8 * (kn % PP_STAGES), (kn / PP_STAGES) & 1u, failed);
+      tc_after();
       scores(rt, kn % PP_STAGES, only);
     };
     begin();
@@ -775,7 +672,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
       if (rt < nt) first_scores(rt, now == 1);
-    if (nt) pp_commit(k_empty, leader), ++kn;
+    if (nt) tc_commit(k_empty, leader), ++kn;
     while (nt) {
       uint32_t then = 0, more = nt;
       for (uint32_t j = 0; j < now; ++j) {
@@ -786,53 +683,53 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
           more = tiles();
           then = uniform(steps);
         }
-        pp_wait(v_full + 8 * vs, (vn / PP_STAGES) & 1u, failed);
+        tc_wait(v_full + 8 * vs, (vn / PP_STAGES) & 1u, failed);
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
           if (rt < nt) {
             const uint32_t par = (p_par >> rt) & 1u;
             p_par ^= 1u << rt;
-            if (j == 0) pp_wait(o_empty + 8 * rt, (o_par >> rt) & 1u, failed), o_par ^= 1u << rt;
+            if (j == 0) tc_wait(o_empty + 8 * rt, (o_par >> rt) & 1u, failed), o_par ^= 1u << rt;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              pp_wait((half ? p_full : p_half) + 8 * rt, par, failed);
-              pp_after();
+              tc_wait((half ? p_full : p_half) + 8 * rt, par, failed);
+              tc_after();
 #pragma unroll
               for (int k = 4 * half; k < 4 * half + 4; ++k)
-                pp_mma_ts<IPV>(tm + OUT + HD * rt, tm + SCORES + 128 * rt + 8 * k, v_at + vs * (S::KV / 16) + k * (2048 / 16), j > 0 || k > 0, leader);
+                tc_mma_ts<IPV>(tm + OUT + HD * rt, tm + SCORES + 128 * rt + 8 * k, v_at + vs * (S::KV / 16) + k * (2048 / 16), j > 0 || k > 0, leader);
             }
-            if (last) pp_commit(o_full + 8 * rt, leader);
+            if (last) tc_commit(o_full + 8 * rt, leader);
           }
           if (rt < more) {
             if (last) {
               first_scores(rt, then == 1);
             } else {
-              if (rt == 0) pp_wait(k_full + 8 * ks, (kn / PP_STAGES) & 1u, failed), pp_after();
+              if (rt == 0) tc_wait(k_full + 8 * ks, (kn / PP_STAGES) & 1u, failed), tc_after();
               scores(rt, ks, j + 2 == now);
             }
           }
         }
-        pp_commit(v_empty + 8 * vs, leader);
+        tc_commit(v_empty + 8 * vs, leader);
         ++vn;
-        if (more) pp_commit(k_empty + 8 * ks, leader), ++kn;
+        if (more) tc_commit(k_empty + 8 * ks, leader), ++kn;
       }
       now = then, nt = more;
     }
     // nothing of this CTA's is in flight any more when it gives its TMEM back, also behind a wait that ran out
-    pp_commit(done, leader);
-    for (const unsigned long long t = pp_ns(); !pp_try(done, 0) && pp_ns() - t < PP_WAIT_NS;) {}
+    tc_commit(done, leader);
+    for (const unsigned long long t = tc_ns(); !tc_try(done, 0) && tc_ns() - t < TC_WAIT_NS;) {}
   }
   __syncwarp();
-  pp_before();
+  tc_before();
   __syncthreads();
-  pp_after();
+  tc_after();
   if (warp == PP_MMA_WARP)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM) : "memory");
 }
 
 // The pieces of the unit that CTA blockIdx.x begins and leaves, merged in their order: 32 rows and 32 channels per block, a
 // row per lane and eight output channels per warp.  Bound by the latency of its loads: pieces are read four at a time (64
-// tokens over 4096, 19 pieces to a unit: 35 us with 128 channels per block one piece after the other).
+// tokens over 4096, 19 pieces to a unit: the call took 40 us with 128 channels per block, one piece after the other, 30 so).
 constexpr int PP_MERGE_THREADS = 128;
 template <int HD>
 __global__ void __launch_bounds__(PP_MERGE_THREADS) prefill_merge_kernel(PpArgs a) {

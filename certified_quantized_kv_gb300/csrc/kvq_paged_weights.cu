@@ -23,6 +23,7 @@
 #include "kvq.h"
 #include "kvq_launch.h"
 #include "kvq_paged.cuh"
+#include "kvq_tc.cuh"
 
 namespace kvq {
 
@@ -426,6 +427,330 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   if (failed) ring_drain<PW_STAGES>(issued, [&](int k, uint32_t parity) { pw_wait_slow(bar_s + 8 * k, parity); });
 }
 
+// ---- many query rows: on the 5th-generation tensor cores ----
+// The same sums with tokens as the rows of M = 128 tiles and up to 128 query rows as columns, 32 at a time: an accumulator
+// of its own for each group of 32 channels, since the groups' scales come behind them.  A thread owns a token (a lane of
+// TMEM), so its scales, offsets and sum stay in its registers and nothing is reduced across lanes; what a row brings (the
+// sums of its groups for the offsets, scale, log-sum-exp) is read from shared memory, the same for all lanes.
+// Bound by the reads of what rows bring: three 16-byte loads of shared memory per two rows and warp take two thirds of the
+// load unit's cycles, and the issue slots are 0.63 busy (128 rows, 131072 tokens, 8 KV heads of 128).
+//   warps 0-15    sums, four warps to a tile, each four with a quarter of TMEM (two tiles at once left them waiting for their
+//                 own instructions)
+//   warps 16-19   codes to MMA operands, a token per thread, ahead of their use
+//   warp 20       issues the MMAs
+constexpr int WT_TOK = 128, WT_ROWS = 32, WT_MOST = 128, WT_STAGES = 5, WT_SETS = 4;
+constexpr int WT_SUM_WARPS = 4 * WT_SETS, WT_MMA_WARP = WT_SUM_WARPS + 4, WT_THREADS = 32 * (WT_MMA_WARP + 1);
+constexpr int WT_MEET = 32 * (WT_SUM_WARPS + 1);   // threads that meet when the rows change
+constexpr int WT_LEAD = 2;            // tiles that a head counts more, for its start
+
+template <int HD>
+struct WtSmem {
+  static constexpr int TILE = WT_TOK * HD * 2, G = HD / 32;
+  static constexpr int Q0 = WT_STAGES * TILE, SUMS = Q0 + WT_MOST * HD * 2;   // (sums of pairs of rows: [row / 2][G] float2)
+  static constexpr int SCALE = SUMS + WT_MOST * G * 4, SPAN = SCALE + WT_MOST * 8, PRE = SPAN + WT_MOST * 8;
+  static constexpr int bytes(int batch) { return PRE + 4 * (2 * batch + 1) + 1024; }   // (1024: to the swizzle's boundary)
+};
+
+// Rows rt0.. of a (sequence, KV head) into shared memory, two (HD 64: four) per warp at a time: HD / 8 lanes hold a row
+template <int HD>
+__device__ __forceinline__ void wt_rows(const PwArgs& a, int b, int g, int r0, int rn, int n, unsigned char* sm) {
+  using S = WtSmem<HD>;
+  constexpr int CH = HD / 8, PER = 32 / CH;
+  const int lane = threadIdx.x & 31, c = lane % CH;
+  for (int x = (threadIdx.x >> 5) * PER + lane / CH; x < WT_MOST; x += WT_SUM_WARPS * PER) {
+    const int r = r0 + x, i = x < rn ? r / a.n_rep : 0, h = g * a.n_rep + (x < rn ? r - i * a.n_rep : 0);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (x < rn) v = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + ((long long)b * a.Q + i) * a.qt + h * a.qh + 8 * c);
+    float f[8], mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 p = pair_to_f2(word_of(v, k), a.bf16);
+      f[2 * k] = p.x, f[2 * k + 1] = p.y;
+      mx = fmaxf(mx, fmaxf(fabsf(p.x), fabsf(p.y)));
+    }
+#pragma unroll
+    for (int o = 1; o < CH; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    int e = 0;   // as in pw_rows
+    if (mx > 0.f) frexpf(mx, &e);
+    e = max(-126, min(126, 10 - e));
+    const float up = a.scale_log2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e), upl = up * 0.0625f;
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum = fmaf(f[k], up, sum);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    // channels 0, 4, 1, 5, ...: as the codes come; odd ones meet 16 times their codes
+    *reinterpret_cast<uint4*>(sm + S::Q0 + tc_place(WT_MOST, x, c)) =
+        make_uint4(h2_as_u32(__floats2half2_rn(f[0] * up, f[4] * up)), h2_as_u32(__floats2half2_rn(f[1] * upl, f[5] * upl)),
+                   h2_as_u32(__floats2half2_rn(f[2] * up, f[6] * up)), h2_as_u32(__floats2half2_rn(f[3] * upl, f[7] * upl)));
+    if (c % 4 == 0) reinterpret_cast<float*>(sm + S::SUMS)[((x / 2) * S::G + c / 4) * 2 + x % 2] = sum;
+    if (c == 0) {
+      const int hi = max(0, n - a.Q + 1 + i), lo = a.window ? max(0, hi - a.window) : 0;
+      const float lse = x < rn ? a.lse[((long long)b * a.Q + i) * a.Hq + h] : 0.f;
+      const bool counts = x < rn && (lse > -INFINITY || lse != lse);
+      // [row / 2]: scales of two rows, then their log-sum-exps in base 2, negated
+      float* sl = reinterpret_cast<float*>(sm + S::SCALE) + (x / 2) * 4 + x % 2;
+      sl[0] = counts ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), -e), 1.17549435e-38f), 3.402823466e38f) : 0.f;
+      sl[2] = counts ? -lse * LOG2E_F : -INFINITY;
+      int* span = reinterpret_cast<int*>(sm + S::SPAN) + (x / 2) * 4 + x % 2;
+      span[0] = counts ? lo : 0, span[2] = counts ? hi : 0;
+    }
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(WT_THREADS, 1) paged_weights_rows_kernel(PwArgs a) {
+  using L = Page<HD>;
+  using S = WtSmem<HD>;
+  constexpr int G = L::G;
+  constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, TMEM = WT_SETS * WT_ROWS * G;
+  extern __shared__ unsigned char raw_smem[];
+  unsigned char* sm = raw_smem + (1024 - (tc_smem(raw_smem) & 1023)) % 1024;
+  int* pre = reinterpret_cast<int*>(sm + S::PRE);   // [B + 1] positions before each sequence, of one KV head
+  int* lens = pre + a.B + 1;                        // [B]
+  __shared__ __align__(8) unsigned long long bars[2 * WT_STAGES + 2 * WT_SETS + 1];
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed_at;
+  volatile int* failed = &failed_at;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t bar0 = __shfl_sync(0xffffffffu, tc_smem(bars), 0);
+  const uint32_t full = bar0, empty = bar0 + 8 * WT_STAGES, d_full = empty + 8 * WT_STAGES, d_empty = d_full + 8 * WT_SETS, done = d_empty + 8 * WT_SETS;
+  if (threadIdx.x == 0) {
+    auto init = [&](uint32_t bar, int count) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory"); };
+    for (int k = 0; k < WT_STAGES; ++k) init(full + 8 * k, 128), init(empty + 8 * k, 1);
+    for (int k = 0; k < WT_SETS; ++k) init(d_full + 8 * k, 1), init(d_empty + 8 * k, 128);
+    init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    failed_at = 0;
+  }
+  if (warp == WT_MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(tc_smem(&tmem_at)), "r"(TMEM) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (warp == 0) {
+    int run = 0;
+    if (lane == 0) pre[0] = 0;
+    for (int base = 0; base < a.B; base += 32) {
+      const int b = base + lane, len = b < a.B ? pw_len(a, b) : 0, cols = min(len, a.columns);
+      int inc = cols ? (cols + WT_TOK - 1) / WT_TOK + WT_LEAD : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (b < a.B) lens[b] = len, pre[b + 1] = run + inc;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_at, 0);
+  const long long total = (long long)pre[a.B] * a.Hkv;
+  const long long x1 = quotient((blockIdx.x + 1) * total, gridDim.x);
+  // ---- the walk over this CTA's parts of (sequence, KV head)s and their chunks of rows, the same in every role ----
+  long long x = quotient(blockIdx.x * total, gridDim.x);
+  int b = 0, g = 0, tile0 = 0, tiles = 0, n = 0, r0 = 0, rn = 0;
+  for (int b1 = a.B; b1 - b > 1;) {   // the last sequence that starts at x or before
+    const int m = (b + b1) / 2;
+    if ((long long)pre[m] * a.Hkv <= x) b = m; else b1 = m;
+  }
+  r0 = a.rows;   // (as behind the last chunk)
+  auto next = [&]() {   // the next chunk of rows, or the first of the next part; false: there is none
+    r0 += WT_MOST;
+    while (r0 >= a.rows) {
+      if (x >= x1) return false;
+      while ((long long)pre[b + 1] * a.Hkv <= x) ++b;
+      const int np = pre[b + 1] - pre[b];
+      const long long in = x - (long long)pre[b] * a.Hkv;
+      g = (int)quotient(in, np);
+      const int at = (int)(in - (long long)g * np), taken = (int)min((long long)(np - at), x1 - x);
+      tile0 = max(0, at - WT_LEAD), tiles = max(0, at + taken - WT_LEAD) - tile0;
+      n = lens[b], x += taken;
+      if (tiles) r0 = 0;
+    }
+    rn = min(WT_MOST, a.rows - r0);
+    return true;
+  };
+  // the page of token `tok` (-1: not seen by any query, or in no page of the pool)
+  const int q_first = a.window ? a.Q - 1 + a.window : 0;   // tokens before n - q_first no query sees
+  auto page_of = [&](int tok) {
+    if (tok >= n || (a.window && (tok / PG + 1) * PG <= n - q_first)) return -1;
+    const int page = a.table[b * a.table_stride + tok / PG];
+    return page >= 0 && page < a.n_pages ? page : -1;
+  };
+
+  if (warp < WT_SUM_WARPS) {
+    // ---- sums ----
+    const int w = warp >> 2, t = threadIdx.x & 127;
+    const uint32_t dp = tmem + ((uint32_t)(warp & 3) << 21) + WT_ROWS * G * w;
+    uint32_t par = 0;
+    while (next()) {
+      asm volatile("bar.sync 1, %0;" :: "n"(WT_MEET) : "memory");   // everybody is done with the last rows
+      wt_rows<HD>(a, b, g, r0, rn, n, sm);
+      tc_proxy();
+      asm volatile("bar.sync 1, %0;" :: "n"(WT_MEET) : "memory");
+      const int blocks = (rn + WT_ROWS - 1) / WT_ROWS;
+      // what a tile's token brings, on its way while the tile before is summed up, its page's number one tile earlier
+      struct Held {
+        uint32_t s[G / 2], o[G / 2];
+        float old;
+      };
+      auto fetch = [&](int tok, int page) {
+        Held x;
+        x.old = (r0 || a.decay != 0.f) && tok < min(n, a.columns) ? a.weights[b * a.ws + g * a.wh + tok] : 0.f;   // (decay 0 does not read it)
+        const unsigned char* pg = a.pages + ((size_t)max(page, 0) * a.Hkv + g) * L::BYTES + (tok % PG) * 2 * G;
+#pragma unroll
+        for (int k = 0; k < G / 2; ++k) {
+          x.s[k] = page >= 0 ? *reinterpret_cast<const uint32_t*>(pg + L::KS + 4 * k) : 0u;
+          x.o[k] = page >= 0 ? *reinterpret_cast<const uint32_t*>(pg + L::KO + 4 * k) : 0u;
+        }
+        return x;
+      };
+      int tok = (tile0 + w) * WT_TOK + t, page = page_of(tok), page1 = page_of(tok + WT_SETS * WT_TOK);
+      Held held = fetch(tok, page);
+      for (int k = w; k < tiles; k += WT_SETS) {
+        const int tok0 = tok - t;
+        float s[G], o[G];
+#pragma unroll
+        for (int k = 0; k < G; k += 2) {
+          const float2 x = __half22float2(u32_as_h2(held.s[k / 2])), y = __half22float2(u32_as_h2(held.o[k / 2]));
+          s[k] = x.x * NIB_ROW_SCALE_LO, s[k + 1] = x.y * NIB_ROW_SCALE_LO, o[k] = y.x, o[k + 1] = y.y;
+        }
+        const float old = held.old;
+        held = fetch(tok + WT_SETS * WT_TOK, page1);
+        const int page2 = page_of(tok + 2 * WT_SETS * WT_TOK);
+        const bool edge = tok0 + WT_TOK > n - a.Q + 1 || (a.window && tok0 < n - a.window);   // some row does not see all of it
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int block = 0; block < blocks; ++block) {
+          tc_wait(d_full + 8 * w, par, failed);
+          par ^= 1;
+          tc_after();
+          // eight rows at a time
+#pragma unroll 1
+          for (int c = 0; c < WT_ROWS / 8; ++c) {
+            uint32_t v[G][8];
+#pragma unroll
+            for (int j = 0; j < G; ++j) tc_ld8(v[j], dp + WT_ROWS * j + 8 * c);
+#pragma unroll
+            for (int j = 0; j < G; ++j) tc_wait_ld(v[j]);
+            if (c + 1 == WT_ROWS / 8) {
+              tc_before();
+              tc_arrive(d_empty + 8 * w);
+            }
+            const int pair0 = (block * WT_ROWS + 8 * c) / 2;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float2 r = make_float2(0.f, 0.f), y = r;   // offsets' part, codes' part
+#pragma unroll
+              for (int j = 0; j < G; j += 2) {
+                const float4 q = *reinterpret_cast<const float4*>(sm + S::SUMS + ((pair0 + k) * G + j) * 8);
+                r = fma2(make_float2(q.x, q.y), make_float2(o[j], o[j]), r);
+                r = fma2(make_float2(q.z, q.w), make_float2(o[j + 1], o[j + 1]), r);
+              }
+#pragma unroll
+              for (int j = 0; j < G; ++j)
+                y = fma2(make_float2(__uint_as_float(v[j][2 * k]), __uint_as_float(v[j][2 * k + 1])), make_float2(s[j], s[j]), y);
+              const float4 sl = reinterpret_cast<const float4*>(sm + S::SCALE)[pair0 + k];
+              const float2 e = fma2(add2(r, y), make_float2(sl.x, sl.y), make_float2(sl.z, sl.w));
+              float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+              if (edge) {
+                const int4 span = reinterpret_cast<const int4*>(sm + S::SPAN)[pair0 + k];   // lo, lo, hi, hi
+                p = make_float2(tok >= span.x && tok < span.z ? p.x : 0.f, tok >= span.y && tok < span.w ? p.y : 0.f);
+              }
+              sum[k % 2] = add2(sum[k % 2], p);
+            }
+          }
+        }
+        const float all = *failed ? __int_as_float(0x7fc00000) : page >= 0 ? (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) : 0.f;
+        if (tok < min(n, a.columns)) a.weights[b * a.ws + g * a.wh + tok] = r0 ? old + all : a.decay == 0.f ? all : fmaf(old, a.decay, all);
+        tok += WT_SETS * WT_TOK, page = page1, page1 = page2;
+      }
+    }
+  } else if (warp < WT_MMA_WARP) {
+    // ---- codes ----
+    constexpr int W4 = HD / 32;   // 16-byte pieces of a token's codes
+    const int t = threadIdx.x & 127;
+    uint32_t stage = 0, par = 1;
+    struct Held {
+      uint4 code[W4];
+    };
+    auto fetch = [&](int tok, int page) {
+      Held x;
+      const unsigned char* pg = a.pages + ((size_t)max(page, 0) * a.Hkv + g) * L::BYTES + (tok % PG) * L::ROW;
+#pragma unroll
+      for (int i = 0; i < W4; ++i) x.code[i] = page >= 0 ? *reinterpret_cast<const uint4*>(pg + 16 * i) : make_uint4(0, 0, 0, 0);
+      return x;
+    };
+    while (next()) {
+      // the next tile's codes on their way while this one's are masked, its page's number one tile earlier
+      int tok = tile0 * WT_TOK + t, page = page_of(tok + WT_TOK);
+      Held held = fetch(tok, page_of(tok));
+      for (int k = 0; k < tiles; ++k, tok += WT_TOK) {
+        const Held x = held;
+        held = fetch(tok + WT_TOK, page);
+        page = page_of(tok + 2 * WT_TOK);
+        tc_wait(empty + 8 * stage, par, failed);
+        unsigned char* to = sm + stage * S::TILE;
+#pragma unroll
+        for (int i = 0; i < W4; ++i)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t c = word_of(x.code[i], y);   // word G a + g: channels 32g + 8a .. + 7, piece 4g + a
+            const int word = 4 * i + y;
+            *reinterpret_cast<uint4*>(to + tc_place(WT_TOK, t, 4 * (word % G) + word / G)) = make_uint4(c & LO, c & HI, (c >> 8) & LO, (c >> 8) & HI);
+          }
+        tc_proxy();
+        tc_arrive(full + 8 * stage);
+        if (++stage == WT_STAGES) stage = 0, par ^= 1;
+      }
+    }
+  } else {
+    // ---- MMAs ----
+    const uint32_t base = __shfl_sync(0xffffffffu, tc_smem(sm), 0);
+    const bool leader = tc_elect();
+    uint32_t used = 0, d_par = (1u << WT_SETS) - 1;   // tiles; bit w: parity of the wait for a set's accumulators
+    while (next()) {
+      asm volatile("bar.sync 1, %0;" :: "n"(WT_MEET) : "memory");
+      asm volatile("bar.sync 1, %0;" :: "n"(WT_MEET) : "memory");
+      tc_after();
+      const uint32_t blocks = __shfl_sync(0xffffffffu, (rn + WT_ROWS - 1) / WT_ROWS, 0), count = __shfl_sync(0xffffffffu, tiles, 0);
+      for (uint32_t k0 = 0; k0 < count; k0 += WT_SETS) {   // the sets' tiles in turn
+        const uint32_t sets = min((uint32_t)WT_SETS, count - k0);
+        for (uint32_t block = 0; block < blocks; ++block)
+#pragma unroll 1
+          for (uint32_t w = 0; w < sets; ++w) {
+            const uint32_t stage = (used + w) % WT_STAGES;
+            if (block == 0) tc_wait(full + 8 * stage, ((used + w) / WT_STAGES) & 1u, failed);
+            tc_wait(d_empty + 8 * w, (d_par >> w) & 1u, failed);
+            d_par ^= 1u << w;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < 2 * G; ++k) {   // 16 channels each
+              const uint32_t at = (k / 4) * WT_TOK * 128 + (k % 4) * 32, qt = (k / 4) * WT_MOST * 128 + (k % 4) * 32;
+              tc_mma_ss<tc_idesc(WT_ROWS, false)>(tmem + WT_ROWS * (G * w + k / 2), tc_desc(base + stage * S::TILE + at, 16),
+                                                  tc_desc(base + S::Q0 + block * WT_ROWS * 128 + qt, 16), k % 2 > 0, leader);
+            }
+            tc_commit(d_full + 8 * w, leader);
+            if (block + 1 == blocks) tc_commit(empty + 8 * stage, leader);
+          }
+        used += sets;
+      }
+    }
+    // nothing of this CTA's is in flight any more when it gives its TMEM back, also behind a wait that ran out
+    tc_commit(done, leader);
+    for (const unsigned long long t = tc_ns(); !tc_try(done, 0) && tc_ns() - t < TC_WAIT_NS;) {}
+  }
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == WT_MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM) : "memory");
+}
+
 template <int HD>
 cudaError_t pw_launch(const PwArgs& a, int sms, cudaStream_t st) {
   auto bytes = [](int batch) {
@@ -436,6 +761,17 @@ cudaError_t pw_launch(const PwArgs& a, int sms, cudaStream_t st) {
   if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(PW_MAX_BATCH))) return e;
   // one CTA per SM, fewer when the table cannot hold a page for each
   return launch_dependent(k, dim3((unsigned)std::min<long long>(sms, (long long)a.B * a.max_pages * a.Hkv)), dim3(PW_THREADS), bytes(a.B), st, a);
+}
+
+// Query rows of a KV head from which on tokens-as-lanes take less time (8 KV heads of 128 over 131072 tokens, rows of q: 48
+// 51.7 us with tiles of 8 and 61.7 with blocks of 32, 64 64.1 and 61.9, 128 114 and 103, 256 224 and 203; over 4096 tokens: 36
+// 9.2 and 9.1, 64 11.9 and 9.1, 128 18.6 and 12.5).
+constexpr int WT_FROM = 57;
+template <int HD>
+cudaError_t wt_launch(const PwArgs& a, int sms, cudaStream_t st) {
+  auto* k = paged_weights_rows_kernel<HD>;
+  if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, WtSmem<HD>::bytes(PW_MAX_BATCH))) return e;
+  return launch_dependent(k, dim3((unsigned)std::min<long long>(sms, (long long)a.B * a.max_pages * a.Hkv)), dim3(WT_THREADS), WtSmem<HD>::bytes(a.B), st, a);
 }
 
 const char* pw_shape_error(int B, int Q, int Hq, int Hkv, int hd) {
@@ -485,7 +821,8 @@ kvq_status weights_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int sms = 0;
   if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return paged_cuda_fail(e, fn, "device attributes");
-  const cudaError_t e = hd == 128 ? pw_launch<128>(a, sms, st) : pw_launch<64>(a, sms, st);
+  const cudaError_t e = a.rows >= WT_FROM ? (hd == 128 ? wt_launch<128>(a, sms, st) : wt_launch<64>(a, sms, st))
+                                          : (hd == 128 ? pw_launch<128>(a, sms, st) : pw_launch<64>(a, sms, st));
   if (e != cudaSuccess) return paged_cuda_fail(e, fn, "launch");
   return KVQ_OK;
 }
