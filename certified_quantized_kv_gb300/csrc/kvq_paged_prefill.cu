@@ -147,12 +147,14 @@ __global__ void __launch_bounds__(PP_ROW_THREADS) prefill_rows_kernel(PpArgs a) 
   for (long long first = blockIdx.x * (long long)PER * RUN; first < all; first += (long long)gridDim.x * PER * RUN) {
     const long long x0 = first + threadIdx.x / CH;
     uint4 v[RUN];
-    int place[RUN];   // a row's number in its chunk, modulo 8 (that of its place in shared memory)
+    int place[RUN];       // a row's number in its chunk, modulo 8 (that of its place in shared memory)
+    long long to[RUN];    // its number among all KV heads' rows (-1: none)
+    int head[RUN];
 #pragma unroll
     for (int k = 0; k < RUN; ++k) {
       // in the order of memory: tokens, then query heads
       const long long x = x0 + k * PER;
-      v[k] = make_uint4(0, 0, 0, 0), place[k] = 0;
+      v[k] = make_uint4(0, 0, 0, 0), place[k] = head[k] = 0, to[k] = -1;
       if (x >= all) continue;
       const int tok = (int)quotient(x, a.Hq), h = (int)(x - (long long)tok * a.Hq);
       v[k] = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + tok * a.qt + h * a.qh + 8 * c);
@@ -161,11 +163,12 @@ __global__ void __launch_bounds__(PP_ROW_THREADS) prefill_rows_kernel(PpArgs a) 
         const int m = (b + b1) / 2;
         if (a.starts[m] <= tok) b = m; else b1 = m;
       }
-      place[k] = ((tok - min(max(a.starts[b], 0), a.T)) * a.n_rep + h % a.n_rep) & 7;
+      const int g = head[k] = h / a.n_rep, r = h - g * a.n_rep;
+      place[k] = ((tok - min(max(a.starts[b], 0), a.T)) * a.n_rep + r) & 7;
+      to[k] = g * rows + (long long)tok * a.n_rep + r;
     }
 #pragma unroll
     for (int k = 0; k < RUN; ++k) {
-      const long long x = x0 + k * PER;
       // the largest bits of an element but its sign: from INF on an infinity or a NaN, with which all of the row's outputs are NaN
       const uint32_t INF = a.bf16 ? 0x7F80u : 0x7C00u;
       uint32_t mx = 0;
@@ -196,11 +199,11 @@ __global__ void __launch_bounds__(PP_ROW_THREADS) prefill_rows_kernel(PpArgs a) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __byte_perm(word_of(v[k], i / 2), word_of(v[k], 2 + i / 2), i & 1 ? 0x7632 : 0x5410) ^ sign;
       }
-      if (x >= all) continue;
-      const int tok = (int)quotient(x, a.Hq), h = (int)(x - (long long)tok * a.Hq), g = h / a.n_rep;
-      const long long row = (long long)tok * a.n_rep + h - g * a.n_rep;
-      if (c == 0) a.scales[g * rows + row] = mx < INF ? sc : __int_as_float(0x7fc00000);
-      *reinterpret_cast<uint4*>(a.rows + ((g * (HD / 64) + c / 8) * rows + row) * 128 + (((c & 7) ^ place[k]) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (to[k] < 0) continue;
+      if (c == 0) a.scales[to[k]] = mx < INF ? sc : __int_as_float(0x7fc00000);
+      // (KV head g's rows lie in HD / 64 blocks of `rows`)
+      const long long at = HD == 64 ? to[k] : to[k] + (head[k] + c / 8) * rows;
+      *reinterpret_cast<uint4*>(a.rows + at * 128 + (((c & 7) ^ place[k]) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
