@@ -814,7 +814,7 @@ def paged_evict(pages, page_table, seq_lens, weights, new_table, new_lens, keep,
     if origin is None:
         if stream is not None:
             raise ValueError("origin must be given with a stream")
-        origin = _torch.empty((B, hkv, keep), dtype=_I32, device=pages.device)
+        origin = _torch.empty((max(B, 0), hkv, max(keep, 0)), dtype=_I32, device=pages.device)
     elif origin.dtype is not _I32 or origin.shape != (B, hkv, keep) or not origin.is_contiguous():
         raise ValueError(f"origin must be a contiguous int32 tensor [{B}, {hkv}, {keep}]")
     nw = (None, 0, 0)

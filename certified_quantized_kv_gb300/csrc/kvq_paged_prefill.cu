@@ -30,7 +30,7 @@
 // merges them in a fixed order, so that results do not depend on timing.
 //
 // Measured (32 query heads on 8 KV heads of 128, bf16; 1925 TFLOP/s measured for a product of 8192^3): 2048 tokens over 32768
-// 894 us = 1190 TFLOP/s (0.62), a prompt of 8192 tokens 527 us = 1043 (0.54); 64 tokens over 4096 29 us, of which the rows'
+// 894 us = 1190 TFLOP/s (0.62), a prompt of 8192 tokens 517 us = 1063 (0.55); 64 tokens over 4096 29 us, of which the rows'
 // kernel takes 3, the merge 8.  A step of 256 rows and 128 tokens takes about 3700 cycles, 2048 of them the MMAs': each
 // tile's chain is its softmax (2700 cycles beside the other tile's and the unpacking, whose instructions fill 0.61 of the
 // issue slots) and its two products (1070).  Every role's loop is as short as it is because straight code was slower: the
@@ -134,8 +134,8 @@ struct PpSmem {
   static constexpr int bytes(int batch) { return PRE + 8 * (batch + 1) + 1024; }   // (1024: to the swizzle's boundary)
 };
 
-// A (token, query head)'s row: the lanes of HD / 8 hold 16 bytes each.  HBM bound: 67 MB read and written for 8192 tokens of 32
-// heads of 128.
+// A (token, query head)'s row: the lanes of HD / 8 hold 16 bytes each.  8192 tokens of 32 heads of 128, 134 MB: 29 us (issue:
+// the rows' places and powers of two; at a copy's rate 20).
 constexpr int PP_ROW_THREADS = 256;
 template <int HD>
 __global__ void __launch_bounds__(PP_ROW_THREADS) prefill_rows_kernel(PpArgs a) {
