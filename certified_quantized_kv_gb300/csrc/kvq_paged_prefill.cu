@@ -84,7 +84,7 @@ __device__ __forceinline__ int pp_lo(const PpArgs& a, int hi) { return a.window 
 __device__ __forceinline__ void pp_sequence(const PpArgs& a, int b, PpUnit& u) {
   u.b = b;
   u.first = min(max(a.starts[b], 0), a.T);
-  u.m = max(min(a.starts[b + 1], a.T) - u.first, 0);
+  u.m = max(min(max(a.starts[b + 1], 0), a.T) - u.first, 0);   // (both ends clamped: the difference of any two fits)
   u.len = min(max(a.lens[b], 0), a.max_pages * PG);
   u.tiles = (u.m * a.n_rep + PP_ROWS - 1) / PP_ROWS;
 }
@@ -831,8 +831,9 @@ kvq_status prefill_impl(int dtype, const void* q, int64_t qt, int64_t qh, const 
   if (window < 0 || (window && !causal)) return bad("window must be >= 0, and 0 unless causal");
   const float scale_log2 = (scale != 0.f ? scale : 1.f / std::sqrt((float)hd)) * LOG2E_F;
   if (!std::isfinite(scale_log2)) return bad("scale * log2(e) must be finite");
-  // the steps of all units, times the CTAs, are counted in 64 bits
-  const double most = ((double)T * (Hq / Hkv) / PP_ROWS + B) * (max_pages / 2 + 1 + PP_LEAD) * Hkv * 1024;
+  // the steps of all units, times the CTAs, are counted in 64 bits, also where starts that do not ascend make every chunk the whole
+  // of q (what fits a GPU's memory stays below 2^62 all the same)
+  const double most = ((double)T * (Hq / Hkv) / PP_ROWS + 1) * B * (max_pages / 2 + 1 + PP_LEAD) * Hkv * 1024;
   if (most >= 9e18) return bad("n_tokens * max_pages * n_q_heads is too large for one call");
   if (B == 0 || T == 0) return KVQ_OK;
   if (q == out) return bad("out must not be q");

@@ -178,6 +178,21 @@ def test_operands():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("end", [-2 ** 31, -2 ** 31 + 1, -2 ** 30, -1])
+def test_starts_at_the_ends_of_their_range(end):
+    """Starts far below 0 are clamped to 0 like any other: ascending ones are chunks as ever, and behind a start above them they
+    leave an empty chunk (the difference of unclamped ends would wrap to 2^31 - 100 rows at -2^31)."""
+    lens, Hq, Hkv, D = [300, 190, 77], 4, 2, 128
+    pages, table = _cache(lens, Hkv, D, 21)
+    q = _randn((150, Hq, D), torch.float16, 22)
+    out, lse = torch.full_like(q, 7.0), torch.full((150, Hq), 7.0, device="cuda")
+    kvq.paged_prefill(q, _ints([0, 100, end, end]), pages, table, _ints(lens), out, lse=lse)
+    assert (out[100:] == 7).all() and (lse[100:] == 7).all()
+    kvq.paged_prefill(q, _ints([end, end, end, 100]), pages, table, _ints(lens), out.fill_(7), lse=lse.fill_(7))
+    _check(out, lse, q, [0, 0, 0, 100], pages, table, lens, True, 0, D ** -0.5)
+    assert (out[100:] == 7).all() and (lse[100:] == 7).all()
+
+
 def test_offsets_beyond_32_bits():
     """A pool of 5 GB, the sequence's pages at its end."""
     n_pages, Hkv, D = 70000, 8, 128

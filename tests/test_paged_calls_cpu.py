@@ -77,6 +77,12 @@ def test_evict(bad, word):
     assert evict(**bad) == kvq.KVQ_ERR_INVALID and word in _error()
 
 
+def test_prefill_counts_chunks_that_overlap():
+    """Starts are only read on the device; if they do not ascend each of the chunks can be all of q."""
+    big = dict(T=1 << 24, Hq=64 * 512, Hkv=512, max_pages=1 << 18)
+    assert prefill(batch=2048, **big) == kvq.KVQ_ERR_INVALID and b"too large" in _error()
+
+
 def test_no_ops():
     for call in (prefill, weights, evict):
         assert call(batch=0) == kvq.KVQ_OK
