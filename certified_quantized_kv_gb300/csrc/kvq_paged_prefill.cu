@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(PP_ROW_THREADS) prefill_rows_kernel(PpArgs a) 
     }
 #pragma unroll
     for (int k = 0; k < RUN; ++k) {
-      // the largest bits of an element but its sign: from INF on an infinity or a NaN, with which all of the row's outputs are NaN
+      // the largest bits of an element but its sign: from INF on an infinity or a NaN, with which all of the row's outputs are NaN if it sees a token
       const uint32_t INF = a.bf16 ? 0x7F80u : 0x7C00u;
       uint32_t mx = 0;
 #pragma unroll
@@ -365,7 +365,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         const int r = u.r0 + 128 * rt + tid;   // this thread's row
         const bool live = 128 * rt + tid < u.rn;
         const int i = live ? r / a.n_rep : 0, h = g * a.n_rep + (live ? r - i * a.n_rep : 0);
-        const float sc = live ? a.scales[(long long)g * a.T * a.n_rep + (long long)u.first * a.n_rep + r] : 0.f;
+        const float held = live ? a.scales[(long long)g * a.T * a.n_rep + (long long)u.first * a.n_rep + r] : 0.f;
+        // a row with a NaN or an infinity is NaN if it sees a token; by a finite scale what it does not see has weight 0 here too
+        const bool bad = held != held;
+        const float sc = bad ? 1.f : held;
+        bool saw = false;
         const int hi = live ? pp_hi(a, u, i) : 0, lo = live ? pp_lo(a, hi) : 0;
         const int hi_all = pp_hi(a, u, (u.r0 + 128 * rt) / a.n_rep);                                       // what every row of the tile sees
         const int lo_all = pp_lo(a, pp_hi(a, u, (u.r0 + min(u.rn, 128 * rt + 128) - 1) / a.n_rep));
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
               mask[c] = ((there >> (c >> 1)) & 1u) ? low & high : 0u;
             }
           }
+          saw |= !edge || (mask[0] | mask[1] | mask[2] | mask[3]) != 0u;
           tc_wait(s_full + 8 * rt, s_par, failed);
           s_par ^= 1;
           tc_after();
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         o_par ^= 1;
         tc_after();
         const bool whole = steps == u.np, lost = *failed != 0;
-        if (lost) l = __int_as_float(0x7fc00000);
+        if (lost || (bad && saw)) l = __int_as_float(0x7fc00000);
         float* part = a.part + ((size_t)blockIdx.x * 2 + (s0 == 0)) * (HD + 2) * PP_ROWS + 128 * rt + tid;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(u.first + i) * a.Hq + h;

@@ -521,7 +521,8 @@ kvq_status kvq_paged_prefill_workspace(int n_tokens, int batch, int n_q_heads, i
  *   window      0; or w > 0, with causal: only the last w of those
  *   out         [n_tokens, Hq, head_dim], contiguous, of q's type; must not overlap q
  *   lse         optional (NULL): [n_tokens, Hq] float, natural log of the sum of exp(scale q k)
- * A query that sees no token (of a chunk longer than its sequence, or of an empty one) gets out = 0 and lse = -inf.  What
+ * A query that sees no token (of a chunk longer than its sequence, or of an empty one) gets out = 0 and lse = -inf, whatever
+ * its elements; one that holds a NaN or an infinity and sees a token gets NaN in all of out and lse.  What
  * pages hold behind a sequence's length (NaN included) does not matter.  A key or value that is NaN reaches the
  * outputs of the queries that see its token, and no others: those of the value's 32 channels, or all of the row.
  *   workspace   at least kvq_paged_prefill_workspace(...) bytes, 16-byte aligned; its contents need no

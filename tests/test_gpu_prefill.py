@@ -153,6 +153,42 @@ def test_chunks_that_are_longer_than_their_sequence():
         assert not out[50:].any() and lse[50:].isneginf().all()
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("lens,chunks,D,causal,window", [
+    ([20, 0], [50, 7], 128, True, 0), ([20, 0], [50, 7], 64, False, 0), ([300, 0, 5], [400, 3, 40], 128, True, 0), ([300, 1], [400, 300], 64, True, 9),
+    ([0] * 400, [1] * 400, 64, True, 0)])
+def test_rows_that_see_nothing_whatever_they_hold(lens, chunks, D, causal, window, dt):
+    """Padding that holds NaN or infinities: out 0, lse -inf, and the other rows' bits as ever; in units that one CTA writes
+    (128 tokens or fewer) and in ones that are merged from pieces."""
+    pages, table = _cache(lens, 2, D, 7)
+    starts = [sum(chunks[:b]) for b in range(len(lens) + 1)]
+    q = _randn((starts[-1], 4, D), dt, 8)
+    sees = torch.zeros(starts[-1], dtype=torch.bool)
+    for b, n in enumerate(lens):
+        sees[starts[b]:starts[b + 1]] = torch.tensor(_ends(n, chunks[b], causal)) > 0
+    want, wl = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    kvq.paged_prefill(q, _ints(starts), pages, table, _ints(lens), want, lse=wl, causal=causal, window=window)
+    none = (~sees).nonzero()[:, 0].tolist()
+    for k, t in enumerate(none):
+        q[t, k % 4] = (float("nan"), float("inf"), float("-inf"))[k % 3]
+        q[t, (k + 1) % 4, k % D] = (float("inf"), float("-inf"), float("nan"))[k % 3]
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    kvq.paged_prefill(q, _ints(starts), pages, table, _ints(lens), out, lse=lse, causal=causal, window=window)
+    assert not out[none].any() and lse[none].isneginf().all()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    if sees.any():          # and one that sees its sequence's first token alone, or all
+        t = int(sees.nonzero()[0])
+        q[t, 2, 5] = float("-inf")
+        kvq.paged_prefill(q, _ints(starts), pages, table, _ints(lens), out, lse=lse, causal=causal, window=window)
+        assert out[t, 2].isnan().all() and lse[t, 2].isnan()
+        out[t, 2], lse[t, 2] = want[t, 2], wl[t, 2]
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    table.fill_(2 ** 30)    # no page of the pool: no token is seen
+    q[:, 1] = float("nan")
+    kvq.paged_prefill(q, _ints(starts), pages, table, _ints(lens), out, lse=lse, causal=causal, window=window)
+    assert not out.any() and lse.isneginf().all()
+
+
 def test_operands():
     """A view of a fused projection, a padded table, entries outside the pool, starts that run backwards or out of the rows."""
     lens, Hq, Hkv, D = [300, 190], 4, 2, 128
