@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
   __shared__ uint32_t tmem_at;
   __shared__ int failed_at;
   __shared__ int4 start_at;   // sequence, unit, KV head, step of this CTA's first position
-  volatile int* failed = &failed_at;
+  __shared__ int nan_at;      // whether a value that is NaN came by
+  volatile int *failed = &failed_at, *nan_came = &nan_at;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t bar0 = __shfl_sync(0xffffffffu, tc_smem(bars), 0);
   const uint32_t k_full = bar0, k_empty = bar0 + 16, v_full = bar0 + 32, v_empty = bar0 + 48;            // [stage]
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     }
     init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    failed_at = 0;
+    failed_at = nan_at = 0;
     pre[0] = 0;
   }
   if (warp == PP_MMA_WARP) {
@@ -477,6 +478,37 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         float* part = a.part + ((size_t)blockIdx.x * 2 + (s0 == 0)) * (HD + 2) * PP_ROWS + 128 * rt + tid;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(u.first + i) * a.Hq + h;
+        // Values that are NaN were 0 in the product (weights of 0 would not hide them from rows that do not see them): the row's
+        // outputs of a group in which it sees one become NaN here.  32 tokens at a time, a token per lane.
+        if (__any_sync(0xffffffffu, *nan_came)) {
+          uint32_t nans = 0;   // bit gr: in group gr
+          const int end = min((u.j0 + s0 + steps) * PP_TOK, u.len);
+#pragma unroll 1
+          for (int t0 = (u.j0 + s0) * PP_TOK; t0 < end; t0 += 32) {
+            const int page = table[t0 / PG];
+            if (page < 0 || page >= a.n_pages) continue;
+            const unsigned short* vo = reinterpret_cast<const unsigned short*>(a.pages + ((size_t)page * a.Hkv + g) * L::BYTES + L::VO) +
+                                       vscale_at((t0 & (PG - 1)) + lane);
+            const int x = max(0, min(32, lo - t0)), y = max(0, min(32, hi - t0));
+            const uint32_t sees = (x >= 32 ? 0u : 0xffffffffu << x) & (y >= 32 ? 0xffffffffu : (1u << y) - 1u);
+#pragma unroll 1
+            for (int gr = 0; gr < G; ++gr)
+              nans |= (uint32_t)((__ballot_sync(0xffffffffu, t0 + lane < end && __hisnan(__ushort_as_half(vo[gr * PG]))) & sees) != 0u) << gr;
+          }
+          if (__any_sync(0xffffffffu, nans)) {
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              uint32_t x[16];
+              tc_ld16(x, op + c);
+              tc_wait_ld(x);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)   // (columns: as below)
+                if ((nans >> (2 * ((c / 8 + k / 8) % (G / 2)) + (k & 1))) & 1u) x[k] = 0x7fc00000u;
+              tc_st16(op + c, x);
+            }
+            tc_wait_st();
+          }
+        }
         if (whole) {
           if (live && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
         } else {
@@ -593,8 +625,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
     };
     uint32_t stage = 0, par = 1;
     auto put = [&](Held& x) {
-      // a value that is NaN: 0 in the product (weights of 0 would not hide it), and its token's key NaN instead, which
-      // the rows that do not see it mask
+      // a value that is NaN: 0 in the product, and known to the rows before their piece is complete
       bool nan = false;
 #pragma unroll
       for (int k = 0; k < G / 2; ++k) {
@@ -604,7 +635,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_prefill_kernel(PpArgs a) 
         if (lo) x.o[1][k] &= 0xffff0000u, x.s[1][k] &= 0xffff0000u;
         if (hi) x.o[1][k] &= 0x0000ffffu, x.s[1][k] &= 0x0000ffffu;
       }
-      if (nan) x.o[0][0] = 0x7fff7fffu;
+      if (nan) *nan_came = 1;
       tc_wait(k_empty + 8 * stage, par, failed);
       unpack(std::false_type{}, x, sm + S::K0 + stage * S::KV);
       tc_arrive(k_full + 8 * stage);

@@ -523,8 +523,9 @@ kvq_status kvq_paged_prefill_workspace(int n_tokens, int batch, int n_q_heads, i
  *   lse         optional (NULL): [n_tokens, Hq] float, natural log of the sum of exp(scale q k)
  * A query that sees no token (of a chunk longer than its sequence, or of an empty one) gets out = 0 and lse = -inf, whatever
  * its elements; one that holds a NaN or an infinity and sees a token gets NaN in all of out and lse.  What
- * pages hold behind a sequence's length (NaN included) does not matter.  A key or value that is NaN reaches the
- * outputs of the queries that see its token, and no others: those of the value's 32 channels, or all of the row.
+ * pages hold behind a sequence's length (NaN included) does not matter.  A key that is NaN makes all of out and lse NaN for
+ * the queries that see its token, a value that is NaN those queries' outputs in its 32 channels (lse does not depend on
+ * values); no other output is touched.
  *   workspace   at least kvq_paged_prefill_workspace(...) bytes, 16-byte aligned; its contents need no
  *               initialisation.  Calls that share it must not overlap on the GPU.
  * n_tokens <= 16777216, batch <= 2048, Hq / Hkv an integer in 1..64, Hkv <= 4096, head_dim 64 or 128, batch *

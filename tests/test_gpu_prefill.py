@@ -269,6 +269,46 @@ def test_nan_reaches_the_queries_that_see_it(D, token, window, what):
         assert out[sees].isnan().all() and lse[sees].isnan().all()
 
 
+@pytest.mark.parametrize("D,lens,chunks,causal,window", [
+    (128, [200, 90], [150, 90], True, 0), (64, [200, 90], [150, 90], True, 58), (128, [3000, 700], [300, 64], True, 0),
+    (64, [3000, 700], [300, 64], False, 0), (128, [5000], [3], True, 2000), (64, [130] * 40, [130] * 40, True, 100)])
+def test_nan_values_reach_their_channels_alone(D, lens, chunks, causal, window):
+    """Values that are NaN in one group: those channels of the queries that see the token, in whole units and in pieces; other
+    channels and lse have the same bits as without, and so have weights that go by that lse."""
+    Hq, Hkv = 4, 2
+    pages, table = _cache(lens, Hkv, D, 5)
+    raw, rng = pages.cpu().numpy(), np.random.default_rng(sum(lens))
+    hit = [sorted({0, n // 2, n - 1, int(rng.integers(0, n))}) for n in lens]
+    for b, ts in enumerate(hit):
+        for t in ts:
+            at = P.scale_places(t % 64, t % (D // 32), D)[3]
+            raw[int(table[b, t // 64]), 1, at:at + 2] = 255             # of KV head 1
+    starts = [sum(chunks[:b]) for b in range(len(lens) + 1)]
+    q = _randn((starts[-1], Hq, D), torch.float16, 6)
+    got = []
+    for pool in (pages, torch.from_numpy(raw).cuda()):
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+        kvq.paged_prefill(q, _ints(starts), pool, table, _ints(lens), out, lse=lse, causal=causal, window=window)
+        got.append((out, lse))
+    (want, wl), (out, lse) = got
+    assert torch.equal(lse, wl)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    for b, ts in enumerate(hit):
+        ends = np.array(_ends(lens[b], chunks[b], causal))
+        for t in ts:
+            sees = (t < ends) & ((t >= ends - window) if window else True)
+            gr = t % (D // 32)
+            bad[starts[b]:starts[b + 1], Hq // 2:, 32 * gr:32 * gr + 32] |= torch.from_numpy(sees).cuda()[:, None, None]
+    assert torch.equal(out.isnan(), bad) and torch.equal(out[~bad], want[~bad])
+    Q = min(chunks)
+    ends = _ints(starts)[1:].long()[:, None] - Q + torch.arange(Q, device="cuda")
+    if causal and Q <= 64:
+        w = torch.zeros(2, len(lens), Hkv, table.shape[1] * 64, device="cuda")
+        for k, x in enumerate((wl, lse)):
+            kvq.paged_weights(q[ends], x[ends].contiguous(), pages, table, _ints(lens), w[k], window=window)
+        assert torch.equal(w[0], w[1]) and not w.isnan().any()
+
+
 def test_queries_that_are_nan_or_infinite():
     """... make their own rows NaN, and no others."""
     pages, table = _cache([300], 1, 128, 5)
