@@ -83,9 +83,10 @@ __device__ __forceinline__ void pw_mma_k8_z(float (&c)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
-// Tile `rt` of a (sequence, KV head), by one warp: lane (gid, tig) holds the channels 32k + 8 tig .. + 7 of row gid.
+// Tile `rt` of a (sequence, KV head), by one warp: lane (gid, tig) holds the channels 32k + 8 tig .. + 7 of row gid.  True in
+// lanes whose row counts nothing: what it holds may be NaN, so that its tile is masked by lo and hi.
 template <int HD>
-__device__ __forceinline__ void pw_rows(const PwArgs& a, int b, int g, int rt, int n, PwTile<HD>& out) {
+__device__ __forceinline__ bool pw_rows(const PwArgs& a, int b, int g, int rt, int n, PwTile<HD>& out) {
   constexpr int G = HD / 32;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int r = rt * PW_ROWS + gid;
@@ -128,15 +129,16 @@ __device__ __forceinline__ void pw_rows(const PwArgs& a, int b, int g, int rt, i
   const __half2 h2 = __floats2half2_rn(x, y);
   const float2 hf = __half22float2(h2);
   out.o[lane] = piece == 0 ? h2_as_u32(h2) : piece == 1 ? h2_as_u32(__floats2half2_rn(x - hf.x, y - hf.y)) : 0u;
+  const float lse = live ? a.lse[((long long)b * a.Q + i) * a.Hq + h] : 0.f;
+  // a row that sees nothing (lse -inf) counts nothing
+  const bool counts = live && (lse > -INFINITY || lse != lse);
   if (tig == 0) {
     const int hi = max(0, n - a.Q + 1 + i), lo = a.window ? max(0, hi - a.window) : 0;
-    const float lse = live ? a.lse[((long long)b * a.Q + i) * a.Hq + h] : 0.f;
-    // a row that sees nothing (lse -inf) counts nothing
-    const bool counts = live && lse > -INFINITY || lse != lse;
     out.scale[gid] = counts ? fminf(fmaxf(ldexpf(fabsf(a.scale_log2), -e), 1.17549435e-38f), 3.402823466e38f) : 0.f;
     out.lse[gid] = counts ? lse * LOG2E_F : INFINITY;
     out.lo[gid] = counts ? lo : 0, out.hi[gid] = counts ? hi : 0;
   }
+  return live && !counts;
 }
 
 __device__ __forceinline__ bool pw_try(uint32_t bar, uint32_t parity) {
@@ -288,17 +290,18 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
       const int nt = min(PW_TILES, a.RT - rt0);
       __syncthreads();   // the tiles' last readers are done
       behind = first;
+      bool silent = false;
       for (parts = 0; parts < batch; ++parts) {
         // tile k of part y is number y nt + k, one warp's each
         for (int k = (warp + PW_WARPS - parts * nt % PW_WARPS) % PW_WARPS; k < nt; k += PW_WARPS)
-          pw_rows<HD>(a, behind.b, behind.g, rt0 + k, behind.n, tiles[parts * nt + k]);
+          silent |= pw_rows<HD>(a, behind.b, behind.g, rt0 + k, behind.n, tiles[parts * nt + k]);
         if (behind.end >= x1) {
           ++parts, end = true;
           break;
         }
         behind = part_at(behind.end, behind.b);
       }
-      __syncthreads();
+      silent = __syncthreads_or(silent);
       Part p = first;
       for (int y = 0; y < parts; ++y) {
         if (y) p = part_at(p.end, p.b);
@@ -317,8 +320,8 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
           if (!failed && !pw_try(bar_s + 8 * stage, parity)) failed = !pw_wait_slow(bar_s + 8 * stage, parity);
           failed = __any_sync(0xffffffffu, failed);
           const bool seen = (valid >> stage) & 1u;
-          // whether some row does not see all of the page
-          const bool edge = tok0 + PG > n - a.Q + 1 || (a.window && tok0 < n - a.window);
+          // whether some row does not see all of the page, or counts nothing
+          const bool edge = silent || tok0 + PG > n - a.Q + 1 || (a.window && tok0 < n - a.window);
           float mine[8];   // sums of tokens 8k + gid
 #pragma unroll
           for (int i0 = 0; i0 < 4; i0 += STEP) {
@@ -593,6 +596,10 @@ __global__ void __launch_bounds__(WT_THREADS, 1) paged_weights_rows_kernel(PwArg
       tc_proxy();
       asm volatile("bar.sync 1, %0;" :: "n"(WT_MEET) : "memory");
       const int blocks = (rn + WT_ROWS - 1) / WT_ROWS;
+      // whether some row counts nothing: what it holds may be NaN, so that all tiles are masked by the rows' spans
+      bool silent = false;
+      for (int x = lane; x < rn; x += 32) silent |= reinterpret_cast<const float*>(sm + S::SCALE)[(x / 2) * 4 + x % 2] == 0.f;
+      silent = __any_sync(0xffffffffu, silent);
       // what a tile's token brings, on its way while the tile before is summed up, its page's number one tile earlier
       struct Held {
         uint32_t s[G / 2], o[G / 2];
@@ -622,7 +629,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1) paged_weights_rows_kernel(PwArg
         const float old = held.old;
         held = fetch(tok + WT_SETS * WT_TOK, page1);
         const int page2 = page_of(tok + 2 * WT_SETS * WT_TOK);
-        const bool edge = tok0 + WT_TOK > n - a.Q + 1 || (a.window && tok0 < n - a.window);   // some row does not see all of it
+        const bool edge = silent || tok0 + WT_TOK > n - a.Q + 1 || (a.window && tok0 < n - a.window);   // some row does not see all of it
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         for (int block = 0; block < blocks; ++block) {
           tc_wait(d_full + 8 * w, par, failed);

@@ -545,12 +545,12 @@ kvq_status kvq_paged_prefill(int dtype, const void* q, int64_t q_token_stride, i
  * are left as they were.
  *   q, pages, page_table, seq_lens, window, scale   as kvq_paged_attention
  *   lse         [batch, n_q_tokens, Hq] float, device, contiguous: the rows' log-sum-exp, as kvq_paged_attention or
- *               kvq_paged_prefill writes it.  A row with -inf adds nothing
+ *               kvq_paged_prefill writes it.  A row with -inf adds nothing, whatever its queries and the keys are
  *   decay       finite; 1: plain sums; 0: what is there is overwritten, whatever it is
  *   weights     [batch, Hkv, n_columns] float, device, columns contiguous, strides in elements (>= 0), rows that
  *               do not overlap.  Tokens from n_columns on have no weight (and are seen by queries as
  *               any other)
- * A key that is NaN makes the weight of its token NaN; a lse that is NaN those of all tokens its row sees.  Scores
+ * A key that is NaN makes the weight of its token NaN where a row that adds something sees it; a lse that is NaN those of all tokens its row sees.  Scores
  * and sums in fp32.  One kernel, no workspace.  Limits as kvq_paged_attention.  batch = 0 is a no-op.
  * Errors: KVQ_ERR_INVALID, KVQ_ERR_CUDA. */
 kvq_status kvq_paged_weights(int dtype, const void* q, int64_t q_token_stride, int64_t q_head_stride, const float* lse,

@@ -186,6 +186,39 @@ def test_nan():
     assert w[0, 0].isnan().nonzero()[:, 0].tolist() == [40]
 
 
+@pytest.mark.parametrize("lens,Q,Hq,Hkv,D,window", [
+    ([1000, 70], 1, 8, 2, 128, 0), ([700], 6, 8, 2, 64, 300), ([900, 130], 10, 8, 2, 128, 0), ([1000], 16, 8, 2, 128, 0), ([900, 300], 33, 8, 2, 64, 500),
+    ([2000], 64, 6, 2, 128, 0)])
+def test_rows_that_add_nothing_whatever_they_hold(lens, Q, Hq, Hkv, D, window):
+    """Rows marked with a log-sum-exp of -inf (padding) whose queries are NaN or infinite, few rows and many, over full pages: the
+    same bits as with finite queries there, and the definition's weights.  A KV head of such rows alone is left as it was, also
+    where its keys are NaN."""
+    pages, table = _cache(lens, Hkv, D, 3)
+    q = _randn((len(lens), Q, Hq, D), torch.float16, 4)
+    lse = _lse(q, pages, table, lens, window, D ** -0.5)
+    rng = np.random.default_rng(Q)
+    none = torch.from_numpy(rng.random((len(lens), Q, Hq)) < 0.3).cuda()
+    none[0, 0, 0] = True
+    none[0, :, Hq // 2:] = True             # KV head 1 of the first sequence
+    none[-1, Q - 1, 0] = False
+    lse[none] = float("-inf")
+    before = torch.rand(len(lens), Hkv, table.shape[1] * 64, generator=_gen(5)).cuda()
+    w = before.clone()
+    kvq.paged_weights(q, lse, pages, table, _ints(lens), w, decay=1.0, window=window)
+    ref, tol = _reference(q, lse, pages, table, lens, before, 1.0, window, D ** -0.5)
+    assert np.all(np.abs(_f64(w) - ref) <= tol)
+    raw = pages.cpu().numpy()
+    for t in (0, 100, 333, 640):            # NaN keys of that KV head, which no row that adds something sees
+        at = P.scale_places(t % 64, 1, D)[1]
+        raw[int(table[0, t // 64]), 1, at:at + 2] = 255
+    bad = q.clone()
+    for k, (b, i, r) in enumerate(none.nonzero().tolist()):
+        bad[b, i, r, :: 1 + k % D] = (float("nan"), float("inf"), float("-inf"))[k % 3]
+    got = before.clone()
+    kvq.paged_weights(bad, lse, torch.from_numpy(raw).cuda(), table, _ints(lens), got, decay=1.0, window=window)
+    assert torch.equal(got, w) and torch.equal(got[0, 1], before[0, 1])
+
+
 def test_empty_and_refused_calls():
     pages, table = _cache([100], 2, 64, 1)
     q, lse, lens = _randn((1, 4, 64), torch.float16, 1), torch.zeros(1, 4, device="cuda"), _ints([100])
