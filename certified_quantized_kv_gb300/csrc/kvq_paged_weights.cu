@@ -11,11 +11,11 @@
 // tokens of each 16, and their sums over all query rows stay in its registers.
 //
 // The (sequence, KV head, page) units are numbered in that order and cut into equal contiguous ranges, one per CTA and
-// SM, whatever the lengths (each head counts PW_LEAD pages more, for its start).  For each (sequence, KV head) of its range a CTA brings up to 128 query rows to binary16 in
-// shared memory, in the order in which lanes take them (times a power of two per row, as in the attention); each warp
-// then takes whole pages, which bulk copies bring into a ring of its own two ahead, across the heads' borders too: half
-// a page's codes are masked into MMA operands once, and the rows' tiles pass by.  Further rows are added to what the
-// first ones left.  Every sum has one owner and a fixed order.
+// SM, whatever the lengths (each head counts PW_LEAD pages more, for its start).  For each (sequence, KV head) of its range,
+// several at once, a CTA brings the query rows (WT_FROM - 1 at most) to binary16 in shared memory, in the order in which lanes
+// take them (times a power of two per row, as in the attention); each warp then takes whole pages, which bulk copies bring into
+// a ring of its own two ahead, across the heads' borders too: a quarter of a page's codes is masked into MMA operands once,
+// and the rows' tiles pass by.  More rows go to the kernel further below.  Every sum has one owner and a fixed order.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -36,6 +36,20 @@ constexpr int PW_THREADS = 512, PW_WARPS = PW_THREADS / 32, PW_MAX_BATCH = 2048;
 constexpr int PW_LEAD = 3;
 constexpr int PW_STAGES = 2;          // pages on their way per warp
 constexpr unsigned long long PW_WAIT_NS = 2000000000ull;   // bounded waits: 2 s
+
+// Query rows of a KV head from which on the second kernel takes them, tokens as lanes.  us with tiles of 8 / with blocks of 32:
+//   sequences x tokens, KV heads, head_dim    32 rows        56             64             80              128
+//   1 x 131072, 8, 128                        38.5 / 41.4    57.3 / 61.9    63.6 / 61.9    76.3 / 82.2     114 / 103
+//   1 x 4096, 8, 128                          7.2 / 7.5      9.4 / 9.1      10.1 / 9.1     11.6 / 10.7     15.9 / 12.4
+//   64 x 2048, 8, 128                         46.4 / 56.3    70.2 / 82.8    77.5 / 83.0    96.1 / 107      142 / 132
+//   256 x 256, 8, 128                         48.4 / 77.6    72.5 / 106     78.5 / 108     145 / 135       210 / 174
+//   1 x 131072, 8, 64                         28.4 / 28.6    41.2 / 44.7    45.5 / 44.7    54.0 / 59.9     79.7 / 74.5
+//   64 x 2048, 8, 64                          35.6 / 38.5    52.6 / 56.5    57.7 / 56.4    71.4 / 74.2     104 / 90.8
+//   8 x 1000, 1, 64                           6.9 / 5.8      8.8 / 6.9      9.4 / 6.9      10.7 / 8.4      14.4 / 9.5
+// The crossing moves with the number of sequences, which blocks of 32 pay for at each start, and with what a block leaves
+// empty (65 to 96 rows); lengths are on the device, so the rule goes by rows alone.
+constexpr int WT_FROM = 57;
+static_assert(WT_FROM - 1 <= PW_ROWS * PW_TILES, "the first kernel holds all of its rows at once");
 
 // A page's keys in a stage: the codes, then scales and offsets
 template <int HD>
@@ -164,7 +178,6 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
   using L = Page<HD>;
   using St = PwStage<HD>;
   constexpr int G = L::G;
-  constexpr int STEP = 1;   // tiles of 16 tokens at once
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
   extern __shared__ __align__(128) unsigned char sm[];
   PwTile<HD>* tiles = reinterpret_cast<PwTile<HD>*>(sm + PW_WARPS * PW_STAGES * St::BYTES);
@@ -232,18 +245,14 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
     const int m = (b0 + b1) / 2;
     if ((long long)pre[m] * a.Hkv <= x0) b0 = m; else b1 = m;
   }
-  const int chunks = (a.RT + PW_TILES - 1) / PW_TILES;
 
-  // ---- copies, two pages ahead of their use: parts, then chunks of rows, then this warp's pages ----
+  // ---- copies, two pages ahead of their use: parts, then this warp's pages ----
   Part ahead = part_at(x0, b0);
-  int at_chunk = 0, at_page = ahead.warp0, issued = 0, found = -1;
+  int at_page = ahead.warp0, issued = 0, found = -1;
   bool failed = false, more = true;
   uint32_t valid = 0;   // bit k: stage k holds a page that is seen
   auto look = [&]() {   // the number of the walk's page (-1: none that is seen)
     while (at_page >= ahead.pages) {
-      at_page = ahead.warp0;
-      if (++at_chunk < chunks) continue;
-      at_chunk = 0;
       if (ahead.end >= x1) {
         more = false;
         return;
@@ -280,152 +289,131 @@ __global__ void __launch_bounds__(PW_THREADS, 1) paged_weights_kernel(PwArgs a) 
     if (more) issue();
 
   // Rows of several parts at once where there is room for their tiles, so that warps meet once for all of them.
-  const int batch = max(1, PW_TILES / a.RT);
+  const int nt = a.RT, batch = PW_TILES / nt;
   int used = 0;
-  for (Part first = part_at(x0, b0);;) {
-    Part behind = first;   // the part behind the batch
+  for (Part p = part_at(x0, b0);; p = part_at(p.end, p.b)) {
     int parts = 0;
-    bool end = false;
-    for (int rt0 = 0; rt0 < a.RT; rt0 += PW_TILES) {
-      const int nt = min(PW_TILES, a.RT - rt0);
-      __syncthreads();   // the tiles' last readers are done
-      behind = first;
-      bool silent = false;
-      for (parts = 0; parts < batch; ++parts) {
-        // tile k of part y is number y nt + k, one warp's each
-        for (int k = (warp + PW_WARPS - parts * nt % PW_WARPS) % PW_WARPS; k < nt; k += PW_WARPS)
-          silent |= pw_rows<HD>(a, behind.b, behind.g, rt0 + k, behind.n, tiles[parts * nt + k]);
-        if (behind.end >= x1) {
-          ++parts, end = true;
-          break;
-        }
-        behind = part_at(behind.end, behind.b);
-      }
-      silent = __syncthreads_or(silent);
-      Part p = first;
-      for (int y = 0; y < parts; ++y) {
-        if (y) p = part_at(p.end, p.b);
-        const int n = p.n, cols = min(n, a.columns);
-        for (int page = p.warp0; page < p.pages; page += PW_WARPS) {
-          const int tok0 = (p.page0 + page) * PG;
-          float* w = a.weights + p.b * a.ws + p.g * a.wh + tok0;
-          // what is there of this lane's tokens (decay 0 does not read it)
-          float old[2];
+    bool silent = false;
+    __syncthreads();   // the tiles' last readers are done
+    for (Part r = p;; r = part_at(r.end, r.b)) {
+      // tile k of part y is number y nt + k, one warp's each
+      for (int k = (warp + PW_WARPS - parts * nt % PW_WARPS) % PW_WARPS; k < nt; k += PW_WARPS)
+        silent |= pw_rows<HD>(a, r.b, r.g, k, r.n, tiles[parts * nt + k]);
+      if (++parts == batch || r.end >= x1) break;
+    }
+    silent = __syncthreads_or(silent);
+    for (int y = 0; y < parts; ++y) {
+      if (y) p = part_at(p.end, p.b);
+      const int n = p.n, cols = min(n, a.columns);
+      for (int page = p.warp0; page < p.pages; page += PW_WARPS) {
+        const int tok0 = (p.page0 + page) * PG;
+        float* w = a.weights + p.b * a.ws + p.g * a.wh + tok0;
+        // what is there of this lane's tokens (decay 0 does not read it)
+        float old[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) old[k] = (rt0 || a.decay != 0.f) && tok0 + 32 * k + 8 * tig + gid < cols ? w[32 * k + 8 * tig + gid] : 0.f;
-          const int stage = ring_stage<PW_STAGES>(used);
-          const unsigned char* pg = ring + stage * St::BYTES;
-          const uint32_t parity = ring_parity<PW_STAGES>(used);
-          ++used;
-          if (!failed && !pw_try(bar_s + 8 * stage, parity)) failed = !pw_wait_slow(bar_s + 8 * stage, parity);
-          failed = __any_sync(0xffffffffu, failed);
-          const bool seen = (valid >> stage) & 1u;
-          // whether some row does not see all of the page, or counts nothing
-          const bool edge = silent || tok0 + PG > n - a.Q + 1 || (a.window && tok0 < n - a.window);
-          float mine[8];   // sums of tokens 8k + gid
+        for (int k = 0; k < 2; ++k) old[k] = a.decay != 0.f && tok0 + 32 * k + 8 * tig + gid < cols ? w[32 * k + 8 * tig + gid] : 0.f;
+        const int stage = ring_stage<PW_STAGES>(used);
+        const unsigned char* pg = ring + stage * St::BYTES;
+        const uint32_t parity = ring_parity<PW_STAGES>(used);
+        ++used;
+        if (!failed && !pw_try(bar_s + 8 * stage, parity)) failed = !pw_wait_slow(bar_s + 8 * stage, parity);
+        failed = __any_sync(0xffffffffu, failed);
+        const bool seen = (valid >> stage) & 1u;
+        // whether some row does not see all of the page, or counts nothing
+        const bool edge = silent || tok0 + PG > n - a.Q + 1 || (a.window && tok0 < n - a.window);
+        float mine[8];   // sums of tokens 8k + gid
 #pragma unroll
-          for (int i0 = 0; i0 < 4; i0 += STEP) {
-            float2 sum[STEP][2];   // tokens gid and gid + 8 of a tile; the even and the odd columns
+        for (int i = 0; i < 4; ++i) {
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // tokens gid and gid + 8 of a tile; the even and the odd columns
+          if (seen) {
+            uint32_t low[G][4], high[G][4], off[2];
+            float sc[2][G];
 #pragma unroll
-            for (int i = 0; i < STEP; ++i) sum[i][0] = sum[i][1] = make_float2(0.f, 0.f);
-            if (seen) {
-              uint32_t low[STEP][G][4], high[STEP][G][4], off[STEP][2];
-              float sc[STEP][2][G];
+            for (int k = 0; k < 2; ++k) {
+              const int t = 16 * i + 8 * k + gid;
+              uint32_t c[G], h[G / 2];
+              if constexpr (G == 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(pg + t * L::ROW + tig * 4 * G);
+                c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+                const uint2 y = *reinterpret_cast<const uint2*>(pg + St::KS + t * 2 * G);
+                h[0] = y.x, h[1] = y.y;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(pg + t * L::ROW + tig * 4 * G);
+                c[0] = v.x, c[1] = v.y;
+                h[0] = *reinterpret_cast<const uint32_t*>(pg + St::KS + t * 2 * G);
+              }
+              off[k] = *reinterpret_cast<const uint32_t*>(pg + St::KO + t * 2 * G + 4 * (tig % (G / 2)));
 #pragma unroll
-              for (int i = 0; i < STEP; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int t = 16 * (i0 + i) + 8 * k + gid;
-                  uint32_t c[G], h[G / 2];
-                  if constexpr (G == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(pg + t * L::ROW + tig * 4 * G);
-                    c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
-                    const uint2 y = *reinterpret_cast<const uint2*>(pg + St::KS + t * 2 * G);
-                    h[0] = y.x, h[1] = y.y;
-                  } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(pg + t * L::ROW + tig * 4 * G);
-                    c[0] = v.x, c[1] = v.y;
-                    h[0] = *reinterpret_cast<const uint32_t*>(pg + St::KS + t * 2 * G);
-                  }
-                  off[i][k] = *reinterpret_cast<const uint32_t*>(pg + St::KO + t * 2 * G + 4 * (tig % (G / 2)));
-#pragma unroll
-                  for (int g = 0; g < G; ++g) {
-                    low[i][g][k] = c[g] & LO, low[i][g][2 + k] = (c[g] >> 8) & LO;
-                    high[i][g][k] = c[g] & HI, high[i][g][2 + k] = (c[g] >> 8) & HI;
-                    const float2 f = __half22float2(u32_as_h2(h[g / 2]));
-                    sc[i][k][g] = g & 1 ? f.y : f.x;
-                  }
-                }
-#pragma unroll 1
-              for (int rt = 0; rt < nt; ++rt) {
-                const PwTile<HD>& T = tiles[y * nt + rt];
-                uint4 q[G];
-#pragma unroll
-                for (int k = 0; k < G; ++k) q[k] = T.q[k][lane];
-                const uint32_t qo = T.o[lane];
-                const float2 scale = *reinterpret_cast<const float2*>(T.scale + 2 * tig), lse = *reinterpret_cast<const float2*>(T.lse + 2 * tig);
-                const float2 minus = make_float2(-lse.x, -lse.y);
-#pragma unroll
-                for (int i = 0; i < STEP; ++i) {
-                  float2 r[2];   // of the tile's two tokens, two columns each
-#pragma unroll
-                  for (int g = 0; g < G; ++g) {
-                    float X[4];
-                    pw_mma_z(X, low[i][g], q[g].x, q[g].y);
-                    pw_mma(X, high[i][g], q[g].z, q[g].w);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                      const float2 x = make_float2(X[2 * k], X[2 * k + 1]), f = make_float2(sc[i][k][g], sc[i][k][g]);
-                      r[k] = g == 0 ? mul2(x, f) : fma2(x, f, r[k]);
-                    }
-                  }
-                  float O[4];
-                  pw_mma_k8_z(O, off[i][0], off[i][1], qo);
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    const float2 s = fma2(r[k], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[2 * k], O[2 * k + 1]));
-                    const float2 e = fma2(s, scale, minus);
-                    float2 pr = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-                    if (edge) {
-                      const int t = tok0 + 16 * (i0 + i) + 8 * k + gid;
-                      const int2 lo = *reinterpret_cast<const int2*>(T.lo + 2 * tig), hi = *reinterpret_cast<const int2*>(T.hi + 2 * tig);
-                      pr = make_float2(t >= lo.x && t < hi.x ? pr.x : 0.f, t >= lo.y && t < hi.y ? pr.y : 0.f);
-                    }
-                    sum[i][k] = add2(sum[i][k], pr);
-                  }
-                }
+              for (int g = 0; g < G; ++g) {
+                low[g][k] = c[g] & LO, low[g][2 + k] = (c[g] >> 8) & LO;
+                high[g][k] = c[g] & HI, high[g][2 + k] = (c[g] >> 8) & HI;
+                const float2 f = __half22float2(u32_as_h2(h[g / 2]));
+                sc[k][g] = g & 1 ? f.y : f.x;
               }
             }
+#pragma unroll 1
+            for (int rt = 0; rt < nt; ++rt) {
+              const PwTile<HD>& T = tiles[y * nt + rt];
+              uint4 q[G];
 #pragma unroll
-            for (int i = 0; i < STEP; ++i)
+              for (int k = 0; k < G; ++k) q[k] = T.q[k][lane];
+              const uint32_t qo = T.o[lane];
+              const float2 scale = *reinterpret_cast<const float2*>(T.scale + 2 * tig), lse = *reinterpret_cast<const float2*>(T.lse + 2 * tig);
+              const float2 minus = make_float2(-lse.x, -lse.y);
+              float2 r[2];   // of the tile's two tokens, two columns each
 #pragma unroll
-              for (int k = 0; k < 2; ++k) mine[2 * (i0 + i) + k] = sum[i][k].x + sum[i][k].y;
+              for (int g = 0; g < G; ++g) {
+                float X[4];
+                pw_mma_z(X, low[g], q[g].x, q[g].y);
+                pw_mma(X, high[g], q[g].z, q[g].w);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float2 x = make_float2(X[2 * k], X[2 * k + 1]), f = make_float2(sc[k][g], sc[k][g]);
+                  r[k] = g == 0 ? mul2(x, f) : fma2(x, f, r[k]);
+                }
+              }
+              float O[4];
+              pw_mma_k8_z(O, off[0], off[1], qo);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 s = fma2(r[k], make_float2(NIB_ROW_SCALE_LO, NIB_ROW_SCALE_LO), make_float2(O[2 * k], O[2 * k + 1]));
+                const float2 e = fma2(s, scale, minus);
+                float2 pr = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                if (edge) {
+                  const int t = tok0 + 16 * i + 8 * k + gid;
+                  const int2 lo = *reinterpret_cast<const int2*>(T.lo + 2 * tig), hi = *reinterpret_cast<const int2*>(T.hi + 2 * tig);
+                  pr = make_float2(t >= lo.x && t < hi.x ? pr.x : 0.f, t >= lo.y && t < hi.y ? pr.y : 0.f);
+                }
+                sum[k] = add2(sum[k], pr);
+              }
+            }
           }
-          // over the four lanes with the other columns, each of which ends up with two tokens: 32k + 8 tig + gid
-          float half[4], own[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float keep = tig & 1 ? mine[2 * k + 1] : mine[2 * k], give = tig & 1 ? mine[2 * k] : mine[2 * k + 1];
-            half[k] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float keep = tig & 2 ? half[2 * k + 1] : half[2 * k], give = tig & 2 ? half[2 * k] : half[2 * k + 1];
-            own[k] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int t = 32 * k + 8 * tig + gid;
-            const float x = failed ? __int_as_float(0x7fc00000) : own[k];
-            if (tok0 + t < cols) w[t] = rt0 ? old[k] + x : a.decay == 0.f ? x : fmaf(old[k], a.decay, x);
-          }
-          __syncwarp();   // the stage's last readers are done
-          if (!failed && more) issue();
+          for (int k = 0; k < 2; ++k) mine[2 * i + k] = sum[k].x + sum[k].y;
         }
+        // over the four lanes with the other columns, each of which ends up with two tokens: 32k + 8 tig + gid
+        float half[4], own[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float keep = tig & 1 ? mine[2 * k + 1] : mine[2 * k], give = tig & 1 ? mine[2 * k] : mine[2 * k + 1];
+          half[k] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float keep = tig & 2 ? half[2 * k + 1] : half[2 * k], give = tig & 2 ? half[2 * k] : half[2 * k + 1];
+          own[k] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = 32 * k + 8 * tig + gid;
+          const float x = failed ? __int_as_float(0x7fc00000) : own[k];
+          if (tok0 + t < cols) w[t] = a.decay == 0.f ? x : fmaf(old[k], a.decay, x);
+        }
+        __syncwarp();   // the stage's last readers are done
+        if (!failed && more) issue();
       }
     }
-    if (end) break;
-    first = behind;
+    if (p.end >= x1) break;
   }
   if (failed) ring_drain<PW_STAGES>(issued, [&](int k, uint32_t parity) { pw_wait_slow(bar_s + 8 * k, parity); });
 }
@@ -454,7 +442,8 @@ struct WtSmem {
   static constexpr int bytes(int batch) { return PRE + 4 * (2 * batch + 1) + 1024; }   // (1024: to the swizzle's boundary)
 };
 
-// Rows rt0.. of a (sequence, KV head) into shared memory, two (HD 64: four) per warp at a time: HD / 8 lanes hold a row
+// Rows r0.. (rn of them, WT_MOST at most; further ones are added to what the first ones left) of a (sequence, KV head) into shared
+// memory, two (HD 64: four) per warp at a time: HD / 8 lanes hold a row
 template <int HD>
 __device__ __forceinline__ void wt_rows(const PwArgs& a, int b, int g, int r0, int rn, int n, unsigned char* sm) {
   using S = WtSmem<HD>;
@@ -770,10 +759,6 @@ cudaError_t pw_launch(const PwArgs& a, int sms, cudaStream_t st) {
   return launch_dependent(k, dim3((unsigned)std::min<long long>(sms, (long long)a.B * a.max_pages * a.Hkv)), dim3(PW_THREADS), bytes(a.B), st, a);
 }
 
-// Query rows of a KV head from which on tokens-as-lanes take less time (8 KV heads of 128 over 131072 tokens, rows of q: 48
-// 51.7 us with tiles of 8 and 61.7 with blocks of 32, 64 64.1 and 61.9, 128 114 and 103, 256 224 and 203; over 4096 tokens: 36
-// 9.2 and 9.1, 64 11.9 and 9.1, 128 18.6 and 12.5).
-constexpr int WT_FROM = 57;
 template <int HD>
 cudaError_t wt_launch(const PwArgs& a, int sms, cudaStream_t st) {
   auto* k = paged_weights_rows_kernel<HD>;
