@@ -144,6 +144,19 @@ def test_elements_at_the_end_of_binary16(D):
     _check(out, None, q, [0, 100], pages, _ints([0, 1])[None], [128], True, 0, D ** -0.5)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("top", [65504.0, 64992.0, 40000.0])
+def test_elements_at_the_end_of_binary16_and_fp16_rows(D, top):
+    """The same for rows of fp16, with their log-sum-exp, up to the end and short of it."""
+    rng = np.random.default_rng(D)
+    k = rng.choice([-top, top, 30000.0], (2, 64, D))
+    pages = torch.from_numpy(P.make_pages(k, k[::-1].copy())[:, None]).cuda()
+    q, scale = _randn((100, 2, D), torch.float16, 1, 2.0 ** -8), 2.0 ** -8 * D ** -0.5
+    out, lse = torch.zeros_like(q), torch.zeros(100, 2, device="cuda")
+    kvq.paged_prefill(q, _ints([0, 100]), pages, _ints([0, 1])[None], _ints([128]), out, lse=lse, scale=scale)
+    _check(out, lse, q, [0, 100], pages, _ints([0, 1])[None], [128], True, 0, scale)
+
+
 def test_chunks_that_are_longer_than_their_sequence():
     """The first queries then see nothing: out 0, lse -inf.  Causal, without, and with a window."""
     for causal, window in ((True, 0), (False, 0), (True, 9)):
