@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(EvictArgs a, lon
   }
 }
 
-// CTAs per row: more for rows that can be longer, eight (the portable most) at most.
+// CTAs per row: more for rows that can be longer, eight (the portable most) at most.  By the room for columns, as lengths are on the
+// device: four sequences of 1100 tokens 10.9 us with 1152 columns and 25.4 with 131072; one of 16384 15.8 and 16.2.
 int ev_cluster(int columns) { return columns <= 4096 ? 1 : columns <= 16384 ? 4 : EV_CLUSTER; }
 
 kvq_status evict_impl(const void* pages, int n_pages, const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens,

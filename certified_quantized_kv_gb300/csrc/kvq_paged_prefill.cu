@@ -15,8 +15,12 @@
 // (exact), then one binary16 multiply-add, so each key and value is the held number rounded once (2^-11).  Nibbles four
 // channels apart come out of one word side by side; keys stay in that order, and so do the queries (a dot product does not mind); values
 // come out with channels of two groups in turn, so their scales and offsets enter in pairs, and the output is put in
-// order when it is written.  Weights are rounded once to binary16 (2^-11) before their product with the values.  The
-// decode attention keeps both exact, at four times the work per score; here the tensor cores would wait for it.
+// order when it is written.  Weights are rounded once to binary16 (2^-11) before their product with the values.  The three
+// roundings weigh the same: on fp16 rows outputs are 4.3e-4 of their norm off, 2.1e-4 of it their own rounding (bf16: 1.7e-3, all
+// but their own).  The decode attention keeps all exact, at four times the work per score.  Here, keys and values in two
+// binary16 parts each (high parts exact, weights still rounded) brought that to 2.7e-4 for twice the MMAs and a shared memory that
+// then holds one step instead of two: 2048 fp16 rows over 32768 tokens 874 -> 1493 us, at head_dim 64 over 16384 262 -> 344.
+// What 4 bits lose is a hundred times as much, so the rows are not made to wait for it.
 //
 // Queries are brought to binary16, in the order that the MMAs take, by a kernel of their own before (a unit's 256 rows
 // would keep a CTA's warps for 10 us), so that one bulk copy per 64 channels moves a tile of them.
@@ -30,8 +34,8 @@
 // merges them in a fixed order, so that results do not depend on timing.
 //
 // Measured (32 query heads on 8 KV heads of 128, bf16; 1925 TFLOP/s measured for a product of 8192^3): 2048 tokens over 32768
-// 894 us = 1190 TFLOP/s (0.62), a prompt of 8192 tokens 517 us = 1063 (0.55); 64 tokens over 4096 29 us, of which the rows'
-// kernel takes 3, the merge 8.  A step of 256 rows and 128 tokens takes about 3700 cycles, 2048 of them the MMAs': each
+// 905 us = 1176 TFLOP/s (0.61; 899 to 937 on different GPUs), a prompt of 8192 tokens 524 us = 1049 (0.54); 64 tokens over 4096
+// 29 us, of which the rows' kernel takes 3, the merge 8.  A step of 256 rows and 128 tokens takes about 3700 cycles, 2048 of them the MMAs': each
 // tile's chain is its softmax (2700 cycles beside the other tile's and the unpacking, whose instructions fill 0.61 of the
 // issue slots) and its two products (1070).  Every role's loop is as short as it is because straight code was slower: the
 // same softmax with its four loads of scores unrolled took 968 us where this takes 879, unpacking unrolled 944 against 894.
